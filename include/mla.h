@@ -260,6 +260,78 @@ MLA_API int mla_quantize_latent_fp8(const void *c, long long ld_c, void *c8, lon
                                     float cache_scale, void *stream);
 
 /*
+ * The 4-bit latent cache.
+ *
+ * The cache-size argument of the page "Gated MLA（矩阵吸收版）" (sections "标准 MHA 的 KV cache 问题" and
+ * "形状与参数对比": only r values per token are cached) carried one step past the e4m3 cache; the page itself
+ * caches bf16/fp32 c.  A row of r latent values (r a multiple of 32) is stored in the OCP MX fp4 format:
+ *   r / 2 bytes    e2m1 codes, element 2j in the low half of byte j: a sign bit, then the index of the magnitude
+ *                  in {0, 0.5, 1, 1.5, 2, 3, 4, 6}
+ *   r / 32 bytes   one scale byte X per 32 consecutive elements: 2^(X - 127), X taken into [87, 167]; 255 is NaN
+ *                  (every element of the group is then NaN)
+ *   padding        to a multiple of 16 bytes; never read or written
+ * mla_latent_fp4_row_bytes(r) is that row's size: 272 at r = 512 (1024 in bf16).  Returns 0 for an r that is not a
+ * positive multiple of 32 up to 65536.
+ */
+MLA_API size_t mla_latent_fp4_row_bytes(int r);
+
+/*
+ * mla_quantize_latent_fp4 - fill rows of an fp4 latent cache from latent rows.
+ * Per group of 32: X - 127 = the smallest exponent e in [-40, 40] with max|c| <= 7 * 2^e, and each code is
+ * c * 2^-e (exact) rounded to the nearest e2m1 value (ties to the even index, clamped to +-6; a negative value
+ * that rounds to zero keeps its sign bit).  A group that holds a NaN or an infinity becomes NaN (X = 255, codes 0).
+ *   c      [rows, r] of `dtype` (BF16 or F32), row stride ld_c elements (>= r, rows 16-byte aligned)
+ *   c4     [rows] cache rows, row stride ld_c4 bytes (>= mla_latent_fp4_row_bytes(r), a multiple of 16)
+ * rows == 0 is a no-op.  Returns MLA_OK or a negative mla_status_t; nothing is launched on error.
+ */
+MLA_API int mla_quantize_latent_fp4(const void *c, long long ld_c, void *c4, long long ld_c4, long long rows, int r,
+                                    int dtype, void *stream);
+
+/*
+ * mla_append_latent_fp4 - quantise new latent rows into a cache where each sequence ends: row t of sequence b goes
+ * to cache row lens[b] + t, for t < counts[b] (all T when counts is NULL).  T = 1 is a decode step's append, a larger
+ * T a chunk of a prompt.  No other cache row is touched.
+ *   c         [B, T, r] of `dtype`, dense but for the row stride ld_c (batch stride T * ld_c)
+ *   c4_cache  row u of sequence b at byte (b * max_len + u) * ld_cache
+ *   lens      int32 [B] on the device, read only: the caller advances it
+ *   counts    int32 [B] on the device or NULL; a count below 0 or above T is taken as 0 or T and reported as
+ *             MLA_ERR_DEVICE_BOUNDS (mla_get_device_error)
+ * A row whose place is outside [0, max_len) is not written and reported as MLA_ERR_DEVICE_BOUNDS.
+ * Returns MLA_OK or a negative mla_status_t; nothing is launched on error.
+ */
+MLA_API int mla_append_latent_fp4(const void *c, long long ld_c, void *c4_cache, long long ld_cache, const int *lens,
+                                  const int *counts, int max_len, int B, int T, int r, int dtype, void *stream);
+
+/*
+ * mla_dequantize_latent_fp4 - read cache rows back as latent rows of `dtype`; every value the format holds is exact
+ * in BF16 and F32.
+ *   c4        row u of sequence b at byte b * batch_c4 + u * ld_c4 (both multiples of 16, batch_c4 >= 0)
+ *   c         [B, rows, r], dense but for the row stride ld_c (elements, >= r, rows 16-byte aligned)
+ *   lens      int32 [B] on the device or NULL: only rows u < lens[b] are read and written, the others of c are left
+ *             as they were.  A negative length is taken as 0 and reported as MLA_ERR_DEVICE_BOUNDS.
+ * Returns MLA_OK or a negative mla_status_t; nothing is launched on error.
+ */
+MLA_API int mla_dequantize_latent_fp4(const void *c4, long long ld_c4, long long batch_c4, const int *lens, void *c,
+                                      long long ld_c, int B, int rows, int r, int dtype, void *stream);
+
+/*
+ * mla_latent_decode_fp4 - mla_latent_decode over an fp4 latent cache: exactly mla_latent_decode over the rows'
+ * values.
+ * Arguments as for mla_latent_decode, except:
+ *   c4_cache   row u of sequence b at byte (b * max_len + u) * ld_cache
+ *   ld_cache   row stride in bytes (>= 272, a multiple of 16)
+ *   q_abs, w_uv, gate, out  bf16 (there is no dtype argument)
+ *   workspace  >= mla_latent_decode_fp4_workspace_size(...) bytes, 16-byte aligned, not used by any other call in
+ *              flight
+ * Supported: r = 512, d_v = 128, 1 <= H <= 96.
+ * Returns MLA_OK or a negative mla_status_t; nothing is launched on error.
+ */
+MLA_API size_t mla_latent_decode_fp4_workspace_size(int B, int H, int r, int max_len);
+MLA_API int mla_latent_decode_fp4(const void *q_abs, const void *c4_cache, long long ld_cache, const int *lens,
+                                  int max_len, const void *w_uv, const void *gate, float scale, void *out, int B,
+                                  int H, int d_v, int r, void *workspace, size_t workspace_bytes, void *stream);
+
+/*
  * mla_latent_decode_noalloc - mla_latent_decode for callers that cannot
  * allocate device memory.
  *

@@ -13,6 +13,11 @@ Entry points (same names as the C functions):
     mla_latent_decode_workspace_size(B, H, r, max_len)
     mla_latent_decode_fp8(q_abs, c8_cache, lens, w_uv, cache_scale, gate=None, scale=1.0, out=None, workspace=None)
     mla_quantize_latent_fp8(c, cache_scale, out=None)
+    mla_latent_fp4_row_bytes(r)
+    mla_quantize_latent_fp4(c, out=None)
+    mla_append_latent_fp4(c, c4_cache, lens, counts=None)
+    mla_dequantize_latent_fp4(c4, r, lens=None, dtype=torch.bfloat16, out=None)
+    mla_latent_decode_fp4(q_abs, c4_cache, lens, w_uv, gate=None, scale=1.0, out=None, workspace=None)
     mla_get_device_error(stream=None)
 """
 from __future__ import annotations
@@ -26,7 +31,9 @@ from ._build import LIB_PATH, build
 __all__ = ["MLAError", "build", "library", "library_path", "mla_absorbed_attn_fwd",
            "mla_absorbed_attn_fwd_workspace_size", "mla_latent_decode",
            "mla_latent_decode_workspace_size", "mla_latent_decode_noalloc", "mla_latent_decode_fp8",
-           "mla_quantize_latent_fp8", "mla_get_device_error",
+           "mla_quantize_latent_fp8", "mla_latent_fp4_row_bytes", "mla_quantize_latent_fp4",
+           "mla_append_latent_fp4", "mla_dequantize_latent_fp4", "mla_latent_decode_fp4",
+           "mla_latent_decode_fp4_workspace_size", "mla_get_device_error",
            "mla_status_string", "mla_version", "mla_kernel_launches", "mla_debug_wait_timeout",
            "mla_absorbed_attn_bwd", "mla_gated_layer_fwd", "mla_gated_layer_workspace_size",
            "mla_gated_layer_decode", "layer_workspace_views", "DTYPE_BF16", "DTYPE_F32"]
@@ -74,6 +81,18 @@ def library():
             lib.mla_latent_decode_fp8.restype = i
             lib.mla_quantize_latent_fp8.argtypes = [vp, ll, vp, ll, ll, i, f, vp]
             lib.mla_quantize_latent_fp8.restype = i
+            lib.mla_latent_fp4_row_bytes.argtypes = [i]
+            lib.mla_latent_fp4_row_bytes.restype = sz
+            lib.mla_quantize_latent_fp4.argtypes = [vp, ll, vp, ll, ll, i, i, vp]
+            lib.mla_quantize_latent_fp4.restype = i
+            lib.mla_append_latent_fp4.argtypes = [vp, ll, vp, ll, vp, vp, i, i, i, i, i, vp]
+            lib.mla_append_latent_fp4.restype = i
+            lib.mla_dequantize_latent_fp4.argtypes = [vp, ll, ll, vp, vp, ll, i, i, i, i, vp]
+            lib.mla_dequantize_latent_fp4.restype = i
+            lib.mla_latent_decode_fp4_workspace_size.argtypes = [i, i, i, i]
+            lib.mla_latent_decode_fp4_workspace_size.restype = sz
+            lib.mla_latent_decode_fp4.argtypes = [vp, vp, ll, vp, i, vp, vp, f, vp, i, i, i, i, vp, sz, vp]
+            lib.mla_latent_decode_fp4.restype = i
             lib.mla_latent_decode_noalloc.argtypes = [vp, vp, ll, vp, i, vp, vp, f, vp, i, i, i, i, i, vp]
             lib.mla_latent_decode_noalloc.restype = i
             lib.mla_gated_layer_workspace_size.argtypes = [i, i, i, i, i, i, i, i, i]
@@ -471,6 +490,155 @@ def mla_quantize_latent_fp8(c, cache_scale: float, out=None, stream=None):
                                            _stream_ptr(stream, c.device))
     if rc != 0:
         raise MLAError(rc, "mla_quantize_latent_fp8")
+    return out
+
+
+def _on(stream, device):
+    """The device, and the stream where one is given, that a call's allocations and launches go to."""
+    torch = _torch()
+    return torch.cuda.device(device) if stream is None else torch.cuda.stream(stream)
+
+
+def mla_latent_fp4_row_bytes(r: int) -> int:
+    """Bytes of one row of the fp4 latent cache: r / 2 code bytes and r / 32 scale bytes, rounded up to 16."""
+    n = int(library().mla_latent_fp4_row_bytes(int(r)))
+    if n == 0:
+        raise ValueError(f"r = {r}: the fp4 latent cache holds rows of a positive multiple of 32 values, up to 65536")
+    return n
+
+
+def _fp4_cache(c4, B, r):
+    """Checks a [B, rows, row_bytes] uint8 cache (rows at one stride); returns (rows, row stride, batch stride)."""
+    torch = _torch()
+    if c4.dtype != torch.uint8 or not c4.is_cuda:
+        raise TypeError("the fp4 cache must be a uint8 CUDA tensor")
+    if c4.dim() != 3 or (B is not None and c4.shape[0] != B) or c4.shape[2] != mla_latent_fp4_row_bytes(r) \
+            or c4.stride(2) != 1:
+        raise ValueError(f"the fp4 cache must be [B,max_len,{mla_latent_fp4_row_bytes(r)}] with unit inner stride")
+    # a dimension of one row or one sequence has no stride of its own to go by
+    ld = c4.stride(1) if c4.shape[1] > 1 else max(c4.stride(1), c4.shape[2])
+    return c4.shape[1], ld, c4.stride(0) if c4.shape[0] > 1 else c4.shape[1] * ld
+
+
+def mla_quantize_latent_fp4(c, out=None, stream=None):
+    """Cache rows of latent rows: c bf16 or fp32 [..., r] (contiguous) -> uint8 [..., mla_latent_fp4_row_bytes(r)]."""
+    torch = _torch()
+    if not c.is_cuda or not c.is_contiguous():
+        raise ValueError("c must be a contiguous CUDA tensor")
+    code, r = _dtype_code(c), c.shape[-1]
+    shape = (*c.shape[:-1], mla_latent_fp4_row_bytes(r))
+    with _on(stream, c.device):
+        if out is None:
+            out = torch.empty(shape, dtype=torch.uint8, device=c.device)
+        _check(out, "out", torch.uint8, c.device, shape)
+        rc = library().mla_quantize_latent_fp4(c.data_ptr(), r, out.data_ptr(), shape[-1], c.numel() // r, r, code,
+                                               _stream_ptr(stream, c.device))
+    if rc != 0:
+        raise MLAError(rc, "mla_quantize_latent_fp4")
+    return out
+
+
+def mla_append_latent_fp4(c, c4_cache, lens, counts=None, stream=None):
+    """Quantise c [B,T,r] (bf16 or fp32) into cache rows lens[b] .. lens[b] + counts[b] - 1 (T rows each without
+    counts) of c4_cache [B,max_len,row_bytes] (uint8, or a row-strided view); returns c4_cache.
+
+    lens and counts: int32 [B] on the device; lens is read only, advance it after the call.  Rows that would land
+    outside the cache are not written and set the device error word (mla_get_device_error).
+    """
+    torch = _torch()
+    dev = c.device
+    if c.dim() != 3:
+        raise ValueError("c must be [B,T,r]")
+    B, T, r = c.shape
+    _check(c, "c", c.dtype, dev)
+    if c4_cache.device != dev:
+        raise ValueError(f"c4_cache is on {c4_cache.device}, expected {dev}")
+    max_len, ld, batch = _fp4_cache(c4_cache, B, r)
+    if batch != max_len * ld:
+        raise ValueError("c4_cache must have batch stride max_len*row_stride")
+    _check(lens, "lens", torch.int32, dev, (B,))
+    if counts is not None:
+        _check(counts, "counts", torch.int32, dev, (B,))
+    with _on(stream, dev):
+        rc = library().mla_append_latent_fp4(c.data_ptr(), r, c4_cache.data_ptr(), ld, lens.data_ptr(),
+                                             None if counts is None else counts.data_ptr(), max_len, B, T, r,
+                                             _dtype_code(c), _stream_ptr(stream, dev))
+    if rc != 0:
+        raise MLAError(rc, "mla_append_latent_fp4")
+    return c4_cache
+
+
+def mla_dequantize_latent_fp4(c4, r: int, lens=None, dtype=None, out=None, stream=None):
+    """The latent rows [..., r] (bf16, or fp32 with dtype=torch.float32) that cache rows c4 stand for.
+
+    c4: uint8 [B,rows,row_bytes], or any slice of a cache with one row stride (c4_cache[:, :n]), or [rows,row_bytes].
+    With lens (int32 [B] on the device) only rows u < lens[b] are read and written; the others of out are left as
+    they were (out, when not given, is then zeroed first).
+    """
+    torch = _torch()
+    if dtype is None:
+        dtype = torch.bfloat16 if out is None else out.dtype
+    if c4.dim() == 2 and lens is None:
+        got = mla_dequantize_latent_fp4(c4.unsqueeze(0), r, None, dtype, None if out is None else out.unsqueeze(0),
+                                        stream)
+        return got.squeeze(0)
+    rows, ld, batch = _fp4_cache(c4, None, r)
+    B, dev = c4.shape[0], c4.device
+    if lens is not None:
+        _check(lens, "lens", torch.int32, dev, (B,))
+    with _on(stream, dev):
+        if out is None:
+            out = (torch.empty if lens is None else torch.zeros)((B, rows, r), dtype=dtype, device=dev)
+        _check(out, "out", dtype, dev, (B, rows, r))
+        rc = library().mla_dequantize_latent_fp4(c4.data_ptr(), ld, batch, None if lens is None else lens.data_ptr(),
+                                                 out.data_ptr(), r, B, rows, r, _dtype_code(out),
+                                                 _stream_ptr(stream, dev))
+    if rc != 0:
+        raise MLAError(rc, "mla_dequantize_latent_fp4")
+    return out
+
+
+def mla_latent_decode_fp4_workspace_size(B: int, H: int, r: int, max_len: int) -> int:
+    return int(library().mla_latent_decode_fp4_workspace_size(B, H, r, max_len))
+
+
+def mla_latent_decode_fp4(q_abs, c4_cache, lens, w_uv, gate=None, scale: float = 1.0, out=None, workspace=None,
+                          stream=None):
+    """Decode over an fp4 latent cache; returns out [B,H*d_v] (bf16).
+
+    c4_cache: uint8 [B,max_len,272] (or a row-strided view, row stride a multiple of 16 bytes), e.g. from
+    mla_quantize_latent_fp4 and mla_append_latent_fp4; q_abs [B,H,512], w_uv [H,128,512] and gate [B,H*128] (or None)
+    bf16; lens int32 [B].  A workspace is allocated when not given.
+    """
+    torch = _torch()
+    B, H, r = q_abs.shape
+    d_v = w_uv.shape[1]
+    dev = q_abs.device
+    _check(q_abs, "q_abs", torch.bfloat16, dev)
+    if c4_cache.device != dev:
+        raise ValueError(f"c4_cache is on {c4_cache.device}, expected {dev}")
+    max_len, ld, batch = _fp4_cache(c4_cache, B, r)
+    if batch != max_len * ld:
+        raise ValueError("c4_cache must have batch stride max_len*row_stride")
+    _check(lens, "lens", torch.int32, dev, (B,))
+    _check(w_uv, "w_uv", torch.bfloat16, dev, (H, d_v, r))
+    if gate is not None:
+        _check(gate, "gate", torch.bfloat16, dev, (B, H * d_v))
+    lib = library()
+    with _on(stream, dev):
+        if out is None:
+            out = torch.empty((B, H * d_v), dtype=torch.bfloat16, device=dev)
+        _check(out, "out", torch.bfloat16, dev, (B, H * d_v))
+        need = int(lib.mla_latent_decode_fp4_workspace_size(B, H, r, max_len))
+        if workspace is None and need > 0:
+            workspace = torch.empty(need, dtype=torch.uint8, device=dev)
+        ws_ptr = None if workspace is None else workspace.data_ptr()
+        ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
+        rc = lib.mla_latent_decode_fp4(q_abs.data_ptr(), c4_cache.data_ptr(), ld, lens.data_ptr(), max_len,
+                                       w_uv.data_ptr(), None if gate is None else gate.data_ptr(), float(scale),
+                                       out.data_ptr(), B, H, d_v, r, ws_ptr, ws_bytes, _stream_ptr(stream, dev))
+    if rc != 0:
+        raise MLAError(rc, "mla_latent_decode_fp4")
     return out
 
 

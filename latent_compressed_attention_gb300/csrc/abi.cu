@@ -334,6 +334,99 @@ MLA_API int mla_quantize_latent_fp8(const void *c, long long ld_c, void *c8, lon
     return e == cudaSuccess ? MLA_OK : MLA_ERR_CUDA;
 }
 
+namespace {
+bool fp4_rank(int r) { return r > 0 && r % 32 == 0 && r <= 65536; }
+// Checks shared by the writers and the reader: sizes, then pointers, then alignment.
+int fp4_rows_check(const void *c, long long ld_c, const void *c4, long long ld_c4, long long rows, int r, int dtype) {
+    if (dtype != MLA_DTYPE_BF16 && dtype != MLA_DTYPE_F32) return MLA_ERR_DTYPE;
+    if (rows < 0 || r <= 0 || ld_c < r) return MLA_ERR_SHAPE;
+    if (!fp4_rank(r)) return MLA_ERR_UNSUPPORTED;
+    if (ld_c4 < latent_fp4_row_bytes(r) || !mul_fits(rows, ld_c, LLONG_MAX / 8) || !mul_fits(rows, ld_c4, LLONG_MAX / 8))
+        return MLA_ERR_SHAPE;
+    if (rows == 0) return MLA_OK;
+    if (!c || !c4) return MLA_ERR_NULL;
+    if (!aligned16(c) || !aligned16(c4) || ld_c % (dtype == MLA_DTYPE_BF16 ? 8 : 4) != 0 || ld_c4 % 16 != 0)
+        return MLA_ERR_ALIGN;
+    return MLA_OK;
+}
+}  // namespace
+
+MLA_API size_t mla_latent_fp4_row_bytes(int r) {
+    return fp4_rank(r) ? static_cast<size_t>(latent_fp4_row_bytes(r)) : 0;
+}
+
+MLA_API int mla_quantize_latent_fp4(const void *c, long long ld_c, void *c4, long long ld_c4, long long rows, int r,
+                                    int dtype, void *stream) {
+    const int bad = fp4_rows_check(c, ld_c, c4, ld_c4, rows, r, dtype);
+    if (bad != MLA_OK || rows == 0) return bad;
+    const LatentFp4Args a{c, c4, ld_c, ld_c4, nullptr, 1, rows, r, dtype == MLA_DTYPE_F32, nullptr};
+    return launch_write_latent_fp4(a, static_cast<cudaStream_t>(stream)) == cudaSuccess ? MLA_OK : MLA_ERR_CUDA;
+}
+
+MLA_API int mla_append_latent_fp4(const void *c, long long ld_c, void *c4_cache, long long ld_cache, const int *lens,
+                                  const int *counts, int max_len, int B, int T, int r, int dtype, void *stream) {
+    if (B < 0 || T < 0 || max_len < 0) return MLA_ERR_SHAPE;
+    const long long rows = static_cast<long long>(B) * T;
+    const int bad = fp4_rows_check(c, ld_c, c4_cache, ld_cache, rows, r, dtype);
+    if (bad != MLA_OK) return bad;
+    if (!mul_fits(static_cast<long long>(B) * max_len, ld_cache, LLONG_MAX / 8)) return MLA_ERR_SHAPE;
+    if (rows == 0) return MLA_OK;
+    if (!lens) return MLA_ERR_NULL;
+    if (!aligned16(lens) || (counts && !aligned16(counts))) return MLA_ERR_ALIGN;
+    DeviceInfo *dev = nullptr;
+    if (device_info(dev) != cudaSuccess) return MLA_ERR_CUDA;
+    const LatentFp4Args a{c, c4_cache, ld_c, ld_cache, lens, B, T, r, dtype == MLA_DTYPE_F32, dev->err_word, counts,
+                          max_len};
+    return launch_write_latent_fp4(a, static_cast<cudaStream_t>(stream)) == cudaSuccess ? MLA_OK : MLA_ERR_CUDA;
+}
+
+MLA_API int mla_dequantize_latent_fp4(const void *c4, long long ld_c4, long long batch_c4, const int *lens, void *c,
+                                      long long ld_c, int B, int rows, int r, int dtype, void *stream) {
+    if (B < 0 || rows < 0 || batch_c4 < 0) return MLA_ERR_SHAPE;
+    const long long all = static_cast<long long>(B) * rows;
+    const int bad = fp4_rows_check(c, ld_c, c4, ld_c4, all, r, dtype);
+    if (bad != MLA_OK) return bad;
+    if (!mul_fits(B, batch_c4, LLONG_MAX / 8)) return MLA_ERR_SHAPE;
+    if (all == 0) return MLA_OK;
+    if (batch_c4 % 16 != 0 || (lens && !aligned16(lens))) return MLA_ERR_ALIGN;
+    DeviceInfo *dev = nullptr;
+    if (device_info(dev) != cudaSuccess) return MLA_ERR_CUDA;
+    const LatentFp4Args a{c, const_cast<void *>(c4), ld_c, ld_c4, lens, B, rows, r, dtype == MLA_DTYPE_F32,
+                          dev->err_word, nullptr, 0, batch_c4};
+    return launch_read_latent_fp4(a, static_cast<cudaStream_t>(stream)) == cudaSuccess ? MLA_OK : MLA_ERR_CUDA;
+}
+
+MLA_API size_t mla_latent_decode_fp4_workspace_size(int B, int H, int r, int max_len) {
+    if (B <= 0 || H <= 0 || r <= 0 || max_len < 0) return 0;
+    if (!decode_bf16_supports(H, 128, r)) return 0;
+    DeviceInfo *dev = nullptr;
+    if (device_info(dev) != cudaSuccess) return 0;
+    return decode_fp4_workspace_bytes(B, H, max_len, dev->num_sms);
+}
+
+MLA_API int mla_latent_decode_fp4(const void *q_abs, const void *c4_cache, long long ld_cache, const int *lens,
+                                  int max_len, const void *w_uv, const void *gate, float scale, void *out, int B,
+                                  int H, int d_v, int r, void *workspace, size_t workspace_bytes, void *stream) {
+    if (B < 0 || H <= 0 || d_v <= 0 || r <= 0 || max_len < 0) return MLA_ERR_SHAPE;
+    if (!decode_bf16_supports(H, d_v, r)) return MLA_ERR_UNSUPPORTED;
+    if (ld_cache < latent_fp4_row_bytes(r) || !mul_fits(static_cast<long long>(B) * max_len, ld_cache, LLONG_MAX / 8))
+        return MLA_ERR_SHAPE;
+    if (!q_abs || !c4_cache || !lens || !w_uv || !out) return MLA_ERR_NULL;
+    if (!aligned16(q_abs) || !aligned16(c4_cache) || !aligned16(w_uv) || !aligned16(out) || !aligned16(lens) ||
+        (gate && !aligned16(gate)) || (ld_cache % 16) != 0)
+        return MLA_ERR_ALIGN;
+    if (B == 0) return MLA_OK;
+    DeviceInfo *dev = nullptr;
+    if (device_info(dev) != cudaSuccess) return MLA_ERR_CUDA;
+    const size_t need = decode_fp4_workspace_bytes(B, H, max_len, dev->num_sms);
+    if (!workspace || workspace_bytes < need) return MLA_ERR_WORKSPACE;
+    if (!aligned16(workspace)) return MLA_ERR_ALIGN;
+    DecodeArgs a{q_abs, c4_cache, w_uv, gate, lens, out, ld_cache, max_len, scale, B, H, d_v, r,
+                 workspace, workspace_bytes, dev->err_word, dev->num_sms};
+    const cudaError_t e = launch_decode_fp4(a, static_cast<cudaStream_t>(stream));
+    return e == cudaSuccess ? MLA_OK : MLA_ERR_CUDA;
+}
+
 MLA_API int mla_latent_decode_noalloc(const void *q_abs, const void *c_cache, long long ld_cache, const int *lens,
                                       int max_len, const void *w_uv, const void *gate, float scale, void *out,
                                       int B, int H, int d_v, int r, int dtype, void *stream) {

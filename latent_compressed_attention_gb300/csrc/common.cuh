@@ -10,6 +10,7 @@
 #include <cstdint>
 #include <cstdio>
 #include <cuda_bf16.h>
+#include <cuda_fp16.h>
 #include <cuda_runtime.h>
 
 namespace mla {
@@ -597,6 +598,46 @@ __device__ __forceinline__ uint32_t split_e4m3x2(float a, float b) {
     const uint32_t hi = cvt_e4m3x2(a, b);
     const uint32_t lo = f16x2_to_e4m3x2(sub_f16x2(pack_f16x2(a, b), e4m3x2_to_f16x2(hi)));
     return hi | (lo << 16);
+}
+
+// e2m1 (OCP MX fp4: sign, then the index of 0, 0.5, 1, 1.5, 2, 3, 4, 6).  Eight elements per 32-bit word, element k in
+// bits 4k .. 4k + 3.  Codes of x * mul, rounded to nearest (ties to the even code) and clamped to +-6.
+__device__ __forceinline__ uint32_t pack_e2m1x8(const float (&x)[8], float mul) {
+    uint32_t r;
+    asm("{\n\t.reg .b8 a, b, c, d;\n\t"
+        "cvt.rn.satfinite.e2m1x2.f32 a, %2, %1;\n\t"
+        "cvt.rn.satfinite.e2m1x2.f32 b, %4, %3;\n\t"
+        "cvt.rn.satfinite.e2m1x2.f32 c, %6, %5;\n\t"
+        "cvt.rn.satfinite.e2m1x2.f32 d, %8, %7;\n\t"
+        "mov.b32 %0, {a, b, c, d};\n\t}"
+        : "=r"(r)
+        : "f"(x[0] * mul), "f"(x[1] * mul), "f"(x[2] * mul), "f"(x[3] * mul), "f"(x[4] * mul), "f"(x[5] * mul),
+          "f"(x[6] * mul), "f"(x[7] * mul));
+    return r;
+}
+// The eight values of a word of codes.
+__device__ __forceinline__ void unpack_e2m1x8(uint32_t codes, float (&x)[8]) {
+    uint32_t h[4];
+    asm("{\n\t.reg .b8 a, b, c, d;\n\t"
+        "mov.b32 {a, b, c, d}, %4;\n\t"
+        "cvt.rn.f16x2.e2m1x2 %0, a;\n\t"
+        "cvt.rn.f16x2.e2m1x2 %1, b;\n\t"
+        "cvt.rn.f16x2.e2m1x2 %2, c;\n\t"
+        "cvt.rn.f16x2.e2m1x2 %3, d;\n\t}"
+        : "=r"(h[0]), "=r"(h[1]), "=r"(h[2]), "=r"(h[3])
+        : "r"(codes));
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+        const float2 v = __half22float2(*reinterpret_cast<const __half2 *>(&h[k]));
+        x[2 * k] = v.x;
+        x[2 * k + 1] = v.y;
+    }
+}
+// Scale bytes of the fp4 latent cache: 2^(X - 127) with X taken into [87, 167] (2^-40 .. 2^40); 255 is NaN.
+constexpr int kFp4ScaleMin = 87, kFp4ScaleMax = 167, kFp4ScaleNan = 255;
+__device__ __forceinline__ float fp4_scale(int X) {
+    return __uint_as_float(X == kFp4ScaleNan ? 0x7FFFFFFFu
+                                             : static_cast<uint32_t>(min(max(X, kFp4ScaleMin), kFp4ScaleMax)) << 23);
 }
 
 // 2^k for an integer k in [-126, 127], exactly.

@@ -101,6 +101,27 @@ cudaError_t launch_quantize_latent_e4m3(const void *c, long long ld_c, void *c8,
                                         float inv_scale, cudaStream_t s);
 bool decode_bf16_supports(int H, int d_v, int r);
 
+// The fp4 latent cache: rows of r / 2 code bytes and r / 32 scale bytes (latent_fp4.cu).
+inline long long latent_fp4_row_bytes(int r) { return (r / 2 + r / 32 + 15) / 16 * 16; }
+struct LatentFp4Args {
+    const void *c;           // B x rows latent rows, batch stride rows * ld_c (the read-back writes them)
+    void *c4;
+    long long ld_c, ld_c4;   // elements, bytes
+    const int *lens;         // append: first row of each sequence's new ones; read: rows to read; or NULL
+    long long B, rows;
+    int r;
+    bool f32;
+    int *dev_err;
+    const int *counts = nullptr;   // append: new rows of each sequence (NULL: all)
+    long long max_len = 0;         // append: rows allocated per sequence
+    long long batch_c4 = 0;        // read: bytes between sequences
+};
+cudaError_t launch_write_latent_fp4(const LatentFp4Args &a, cudaStream_t s);
+cudaError_t launch_read_latent_fp4(const LatentFp4Args &a, cudaStream_t s);
+// One query per sequence over the fp4 cache (decode_fp4.cu; c_cache holds bytes, ld_cache in bytes).
+size_t decode_fp4_workspace_bytes(int B, int H, int max_len, int num_sms);
+cudaError_t launch_decode_fp4(const DecodeArgs &a, cudaStream_t s);
+
 // Scratch of the no-alloc decode entry point: capacity in bytes, and its
 // device address on the current device (set up once per device).
 size_t decode_noalloc_scratch_capacity();

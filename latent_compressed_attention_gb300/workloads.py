@@ -140,6 +140,46 @@ def quantize_e4m3(a, inv_scale: float) -> np.ndarray:
     return encode_e4m3(prod.astype(np.float64))
 
 
+# The fp4 latent cache (OCP MX fp4): e2m1 codes, two per byte, low half first, then one scale byte per 32 elements.
+E2M1 = np.array([0.0, 0.5, 1.0, 1.5, 2.0, 3.0, 4.0, 6.0])
+FP4_GROUP = 32
+FP4_EXP = (-40, 40)      # exponents the format's scale bytes (exponent + 127) may hold; 255 is NaN
+
+
+def fp4_row_bytes(r: int) -> int:
+    return -(-(r // 2 + r // FP4_GROUP) // 16) * 16
+
+
+def encode_fp4(c) -> np.ndarray:
+    """Cache rows uint8 [..., fp4_row_bytes(r)] (padding zero) of latent rows c [..., r]."""
+    c = np.asarray(c, dtype=np.float64)
+    r = c.shape[-1]
+    g = c.reshape(*c.shape[:-1], r // FP4_GROUP, FP4_GROUP)
+    bad = ~np.isfinite(g).all(-1)
+    g = np.where(bad[..., None], 0.0, g)
+    top = np.abs(g).max(-1)
+    units = np.exp2(np.arange(FP4_EXP[0], FP4_EXP[1] + 1, dtype=np.float64))
+    e = FP4_EXP[0] + (top[..., None] > 7.0 * units[:-1]).sum(-1)   # smallest e with top <= 7 * 2^e
+    m = np.abs(g) * np.exp2(-e.astype(np.float64))[..., None]
+    mid = (E2M1[1:] + E2M1[:-1]) / 2                               # ties go to the even index
+    code = sum((m >= t if k % 2 else m > t) for k, t in enumerate(mid)).astype(np.uint8)
+    code = np.where(bad[..., None], 0, code | np.signbit(g).astype(np.uint8) << 3).reshape(*c.shape)
+    out = np.zeros((*c.shape[:-1], fp4_row_bytes(r)), np.uint8)
+    out[..., : r // 2] = code[..., 0::2] | code[..., 1::2] << 4
+    out[..., r // 2 : r // 2 + r // FP4_GROUP] = np.where(bad, 255, e + 127)
+    return out
+
+
+def decode_fp4(rows, r: int) -> np.ndarray:
+    """fp64 values [..., r] of cache rows."""
+    rows = np.asarray(rows, np.uint8)
+    code = np.stack([rows[..., : r // 2] & 15, rows[..., : r // 2] >> 4], -1).reshape(*rows.shape[:-1], r)
+    X = rows[..., r // 2 : r // 2 + r // FP4_GROUP].astype(np.int64)
+    scale = np.where(X == 255, np.nan, np.exp2(np.clip(X - 127, *FP4_EXP).astype(np.float64)))
+    v = np.where(code >> 3, -1.0, 1.0) * E2M1[code & 7]
+    return v * np.repeat(scale, FP4_GROUP, axis=-1)
+
+
 def round_f32(a) -> np.ndarray:
     return np.asarray(a, dtype=np.float64).astype(np.float32).astype(np.float64)
 
