@@ -1,13 +1,39 @@
-// Cached-latent decode over the fp4 latent cache (latent_fp4.cu): r = 512, d_v = 128, 1 <= H <= 96.
+// Cached-latent decode over the fp4 latent cache (latent_fp4.cu) on the sm_103a tensor cores: r = 512, d_v = 128,
+// 1 <= H <= 96.
 //
 // Sequence b's absorbed query q_abs[b] (all H heads) attends to its cache rows [0, lens[b]); steps 2-4 of section
 // "完整计算流（四步）" of the page "Gated MLA（矩阵吸收版）" follow: scores against c itself, softmax, the latent
 // weighting by c itself, W_UV^T, gate.
 //
-// Split kernel: a warp takes one head and one of the `nsplit` runs of a sequence's rows; lane j holds latent elements
-// 16j .. 16j + 15 and the warp keeps a running maximum, sum and weighted row, all fp32.
-// Merge kernel: a block per (head, sequence) joins the runs with the log-sum-exp rule, multiplies by W_UV^T and applies
-// the gate.
+// Attention kernel (persistent, one CTA per SM).  A CTA takes up to 48 heads (two groups above that) and a contiguous
+// share of all sequences' rows, in units of 128 rows, and computes both products with the rows' side as M:
+//   S^T [128 rows x heads]       = c . q_abs^T     A = c as stored, K-major       (K = r)
+//   O^T [128 latent x heads] x 4 += c^T . P^T      A = the same tile, MN-major    (K = rows)
+// so a unit is expanded once, to e4m3 in shared memory, for both, heads are never padded to 128, and O^T (fp32) leaves
+// room in tensor memory for S^T.  An e2m1 value times its group's power of two is exact in e4m3 relative to its row's
+// largest scale (14 binades down; smaller groups are rounded at 2^-18 of the row's largest value), so the tile is the
+// row divided by a power of two, `ref`, that goes into the softmax's exponent.  q_abs and P are split into e4m3 hi and
+// lo parts (lo = the rest times 16: 8 bits), side by side as 2 x heads columns of the N side: one pass over the tile
+// serves both parts, which the fp32 epilogues join.
+//
+// Softmax of one unit: thread = row, so every head's statistics lie across lanes.  With a = score * log2 e + ref,
+//   P = 2^(a - M + 8), l += P * 2^-ref,   M[head] >= running max of a - 0.75
+// M moves only when some row exceeds it by more than 0.75 (P <= 2^8.75 = 430, inside e4m3's 448): a barrier with an
+// OR tells whether any does, and only then are maxima taken across lanes and O^T rescaled.  A weight below 2^-22 of
+// the largest is lost; sequences are cut into chunks of 32768 rows with maxima of their own, so at most 2^-8 of a
+// chunk's weight can go that way.
+//
+// Warps: 0 TMA, 1 issues S, 2 issues O, 4-7 softmax (and q_abs, rescale, drain), 8-15 expand.  The expansion is a byte
+// permute per four codes: the group's exponent selects an 8-byte table of e4m3 magnitudes, the codes' three magnitude
+// bits are the selector.
+//
+// Merge kernel: a CTA per (head, 32 sequences) joins the segments of a sequence with the log-sum-exp rule, splits
+// o_lat into bf16 hi + lo and multiplies by W_UV^T on the tensor cores (W_UV as the M side), then the gate.
+#include <cuda.h>
+#include <cudaTypedefs.h>
+
+#include <climits>
+
 #include "common.cuh"
 #include "internal.h"
 
@@ -16,147 +42,935 @@ namespace {
 
 constexpr int kR = 512;
 constexpr int kDV = 128;
+constexpr int kRows = 128;                 // cache rows per unit
+constexpr int kChunkUnits = 256;           // units of a sequence that share one running maximum per segment
+constexpr int kChunkRows = kChunkUnits * kRows;
+constexpr int kOverUnits = 2;              // what starting a segment costs, in units (query, first fill, drain)
+constexpr int kThreads = 512;
 constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kBias = 8.f;               // P = 2^(a - M + kBias)
+constexpr float kSlack = 0.75f;
+// Register split of the 4 warpgroups x 128 launched: control, softmax, 2 x expansion.
+constexpr uint32_t kRegsCtl = 88, kRegsSoft = 208, kRegsExp = 104, kRegsLaunch = 128;
+static_assert(kRegsCtl + kRegsSoft + 2 * kRegsExp <= 4 * kRegsLaunch, "register split exceeds the launch");
+
+constexpr uint32_t kSlab = 16384;          // [128 rows x 128 latent] e4m3, 128-byte swizzle
+constexpr uint32_t kStage = 8192;          // codes of one slab: [128 rows x 64 bytes]
+constexpr uint32_t kScaleTile = 2048;      // [128 rows x 16 scale bytes]
+constexpr int kStages = 4, kScaleSlots = 3, kPBufs = 2;
+constexpr int kTables = 22;                // exponents -14 (all zero) .. 6 below the row's largest, then NaN
+
+template <int HP>
+struct Fp4Layout {
+    static constexpr int N = 2 * HP;                                   // hi and lo columns
+    static constexpr int kSlabs = HP == 48 ? 6 : (HP == 32 ? 7 : 8);   // expanded tiles in flight, four per unit
+    static constexpr uint32_t kQSlab = N * 128;                        // [N x 128 latent] e4m3
+    static constexpr uint32_t Q = 0, C = Q + 4 * kQSlab, P = C + kSlabs * kSlab, STAGE = P + kPBufs * kSlab,
+                              SCALE = STAGE + kStages * kStage, END = SCALE + kScaleSlots * kScaleTile;
+    static constexpr uint32_t kSmem = END + 4096 + 1024;               // + Fp4Shared + alignment slack
+    static constexpr uint32_t S_COL = 0, O_COL = 128;                  // TMEM columns
+    static_assert(kQSlab % 1024 == 0 && O_COL + 4 * N <= 512 && N <= 128, "layout");
+    static_assert(kSlabs <= 8, "a row's ref slot is reused two units later");
+    static_assert(kSmem <= 232448, "attention kernel exceeds shared memory");
+};
+
+struct Fp4Shared {
+    uint64_t stage_full[kStages], stage_empty[kStages];
+    uint64_t scale_full[kScaleSlots], scale_empty[kScaleSlots];
+    uint64_t slab_full[8], slab_free[8];
+    uint64_t s_full, s_free, q_ready;
+    uint64_t p_full[kPBufs], p_free[kPBufs];
+    uint32_t tmem_base;
+    int abort;
+    uint32_t flagged;                      // 16-head groups whose maximum moved
+    uint32_t pad_;
+    uint2 table[kTables];
+    alignas(16) float ref[2][kRows];
+    // per head: score factor, M + slack, kBias - M, 2^(M_old - M_new)
+    alignas(16) float mul[48], thr[48], bias[48], fac[48];
+    float red[4][48];
+};
+static_assert(sizeof(Fp4Shared) <= 4096, "shared block too large");
 
 struct Fp4Params {
-    const __nv_bfloat16 *q_abs, *w_uv, *gate;
-    const uint8_t *c4;
-    long long ld;
+    const __nv_bfloat16 *q_abs;
     const int *lens;
-    __nv_bfloat16 *out;
-    float *ws_o, *ws_m, *ws_l;   // [nsplit][B][H] (x kR)
+    float *ws_o, *ws_m, *ws_l;   // [slots][H] (x r): sum of P c, M - kBias, l
     int *err;
-    int B, H, max_len, nsplit;
+    int B, H, max_len, G, groups, heads_per_group;
     float scale_log2;
 };
 
-__device__ __forceinline__ float warp_sum(float v) {
+// ------------------------------------------------------------------ the work axis
+// Virtual units: a sequence is a run of chunks of up to kChunkUnits units, each preceded by kOverUnits.  Share c of G
+// owns [share_lo(c), share_lo(c + 1)); its part of chunk number v (over all sequences) is segment slot c + v: both
+// only grow along the axis and one of them does between two segments.
+constexpr int kChunkSpan = kOverUnits + kChunkUnits;
+__host__ __device__ __forceinline__ int chunks_of(int len) {
+    return static_cast<int>((static_cast<unsigned>(len) + kChunkRows - 1u) / kChunkRows);
+}
+__device__ __forceinline__ long long units_of(int len) {   // virtual units of a sequence
+    const int full = len / kChunkRows, rest = len - full * kChunkRows;
+    return static_cast<long long>(full) * kChunkSpan + (rest > 0 ? kOverUnits + (rest + kRows - 1) / kRows : 0);
+}
+__device__ __forceinline__ long long share_lo(long long total, int c, int G) { return total * c / G; }
+__device__ __forceinline__ int read_len(const int *lens, int b, int max_len, int *err) {
+    const int x = __ldg(lens + b);
+    if (err && (x < 0 || x > max_len)) record_error(err, kDevErrBounds);
+    return min(max(x, 0), max_len);
+}
+template <typename T>
+__device__ __forceinline__ T warp_scan(T v, int lane) {
 #pragma unroll
-    for (int o = 16; o >= 1; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+    for (int o = 1; o < 32; o <<= 1) {
+        const T n = __shfl_up_sync(0xffffffffu, v, o);
+        if (lane >= o) v += n;
+    }
     return v;
 }
 
-__global__ void __launch_bounds__(128) fp4_split_kernel(const Fp4Params p) {
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int h = static_cast<int>(blockIdx.x) * 4 + warp, split = blockIdx.y, b = blockIdx.z;
-    if (h >= p.H) return;
-    const int raw = __ldg(p.lens + b);
-    if (raw < 0 || raw > p.max_len) record_error(p.err, kDevErrBounds);
-    const int len = min(max(raw, 0), p.max_len);
-    const int per = (len + p.nsplit - 1) / p.nsplit;
-    const int k0 = static_cast<int>(min(static_cast<long long>(per) * split, static_cast<long long>(len)));
-    const int k1 = min(len - k0, per) + k0;
-    float q[16], o[16], m = -INFINITY, l = 0.f;
-    const uint4 *qs = reinterpret_cast<const uint4 *>(p.q_abs + (static_cast<size_t>(b) * p.H + h) * kR) + lane * 2;
+struct Segment {
+    int seq, row0, units, len;   // rows row0 .. row0 + 128 * units - 1, those below len
+    long long slot;
+};
+
+struct Walk {
+    const int *lens;
+    int B, max_len, c, b, j;     // chunk j of sequence b is next
+    long long lo, hi, pre, v;    // its first virtual unit and its number
+    // Every lane of a warp calls this; all get the same walk.
+    __device__ void start(const Fp4Params &p, int share, int lane, int *err) {
+        lens = p.lens, B = p.B, max_len = p.max_len, c = share;
+        long long total = 0;
+        for (int i = lane; i < B; i += 32) total += units_of(read_len(lens, i, max_len, err));
 #pragma unroll
-    for (int half = 0; half < 2; ++half) {
-        const uint4 v = __ldg(qs + half);
-        const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-            q[8 * half + 2 * k] = __uint_as_float(w[k] << 16) * p.scale_log2;
-            q[8 * half + 2 * k + 1] = __uint_as_float(w[k] & 0xFFFF0000u) * p.scale_log2;
+        for (int o = 16; o >= 1; o >>= 1) total += __shfl_xor_sync(0xffffffffu, total, o);
+        lo = share_lo(total, share, p.G), hi = share_lo(total, share + 1, p.G);
+        b = B, j = 0, pre = total, v = 0;
+        long long run = 0, chunks = 0;
+        for (int i0 = 0; i0 < B && lo < hi; i0 += 32) {
+            const int len = i0 + lane < B ? read_len(lens, i0 + lane, max_len, nullptr) : 0;
+            const long long u = units_of(len), incl = warp_scan(u, lane);
+            const int n = len > 0 ? chunks_of(len) : 0, nincl = warp_scan(n, lane);
+            const unsigned past = __ballot_sync(0xffffffffu, run + incl > lo);
+            if (past) {
+                const int first = __ffs(past) - 1;
+                b = i0 + first;
+                pre = run + __shfl_sync(0xffffffffu, incl - u, first);
+                v = chunks + __shfl_sync(0xffffffffu, nincl - n, first);
+                j = static_cast<int>((lo - pre) / kChunkSpan);
+                pre += static_cast<long long>(j) * kChunkSpan;
+                v += j;
+                break;
+            }
+            run += __shfl_sync(0xffffffffu, incl, 31);
+            chunks += __shfl_sync(0xffffffffu, nincl, 31);
         }
     }
-#pragma unroll
-    for (int k = 0; k < 16; ++k) o[k] = 0.f;
-    for (int u = k0; u < k1; ++u) {
-        const uint8_t *row = p.c4 + (static_cast<long long>(b) * p.max_len + u) * p.ld;
-        const uint2 codes = __ldg(reinterpret_cast<const uint2 *>(row) + lane);
-        const float scale = fp4_scale(__ldg(row + kR / 2 + (lane >> 1)));
-        float c[16], (&lo)[8] = *reinterpret_cast<float (*)[8]>(c), (&hi)[8] = *reinterpret_cast<float (*)[8]>(c + 8);
-        unpack_e2m1x8(codes.x, lo);
-        unpack_e2m1x8(codes.y, hi);
-        float s = 0.f;
-#pragma unroll
-        for (int k = 0; k < 16; ++k) s += q[k] * (c[k] *= scale);
-        s = warp_sum(s);
-        const float mn = fmaxf(m, s), base = mn == -INFINITY ? 0.f : mn;
-        const float f = exp2f(m - base), w = exp2f(s - base);
-        l = l * f + w;
-#pragma unroll
-        for (int k = 0; k < 16; ++k) o[k] = o[k] * f + w * c[k];
-        m = mn;
+    __device__ bool next(Segment &s) {
+        while (b < B && pre < hi) {
+            const int len = read_len(lens, b, max_len, nullptr);
+            if (len <= 0) {
+                ++b;
+                continue;
+            }
+            const int left = len - j * kChunkRows;   // > 0: the walk leaves a sequence with its last chunk
+            const int units = left >= kChunkRows ? kChunkUnits : (left + kRows - 1) / kRows;
+            const long long base = pre + kOverUnits, s0 = max(base, lo), s1 = min(base + units, hi);
+            s.seq = b, s.len = len, s.slot = c + v;
+            s.row0 = j * kChunkRows + static_cast<int>(s0 - base) * kRows;
+            s.units = static_cast<int>(s1 - s0);
+            pre = base + units, ++v;
+            if (left > kChunkRows) ++j; else ++b, j = 0;
+            if (s1 > s0) return true;
+        }
+        return false;
     }
-    const size_t slot = (static_cast<size_t>(split) * p.B + b) * p.H + h;
-    float4 *dst = reinterpret_cast<float4 *>(p.ws_o + slot * kR) + lane * 4;
+};
+
+// ------------------------------------------------------------------ small pieces
+__device__ __forceinline__ uint32_t mul_f16x2(uint32_t a, uint32_t b) {
+    uint32_t r;
+    asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+    return r;
+}
+// (a, b) as e4m3 hi (bits 0-15) and lo (bits 16-31): hi = e4m3(x), lo = e4m3(16 (x - hi)), the difference exact in f16.
+__device__ __forceinline__ uint32_t split16_e4m3x2(float a, float b) {
+    const uint32_t hi = cvt_e4m3x2(a, b);
+    const uint32_t rest = sub_f16x2(pack_f16x2(a, b), e4m3x2_to_f16x2(hi));
+    return hi | (f16x2_to_e4m3x2(mul_f16x2(rest, 0x4C004C00u)) << 16);   // f16 16.0
+}
+constexpr float kLoPart = 0.0625f;
+__device__ __forceinline__ uint32_t byte_perm(uint32_t a, uint32_t b, uint32_t sel) {
+    uint32_t r;
+    asm("prmt.b32 %0, %1, %2, %3;" : "=r"(r) : "r"(a), "r"(b), "r"(sel));
+    return r;
+}
+// Four codes (the low 16 bits of w) as e4m3 bytes by the group's table of magnitudes.
+__device__ __forceinline__ uint32_t expand4(uint32_t w, uint2 table) {
+    return byte_perm(table.x, table.y, w & 0x7777u) | byte_perm(0u, 0x80808080u, (w >> 1) & 0x4444u);
+}
+// Floats as integers of the same order (NaN aside).
+__device__ __forceinline__ int ordered(float x) {
+    const int i = __float_as_int(x);
+    return i >= 0 ? i : i ^ 0x7FFFFFFF;
+}
+__device__ __forceinline__ float from_ordered(int i) { return __int_as_float(i >= 0 ? i : i ^ 0x7FFFFFFF); }
+__device__ __forceinline__ float4 lds4(const float *p) { return *reinterpret_cast<const float4 *>(p); }
+
+// One head's query into the N side of S: row h (hi) and row HP + h (lo), lane j the latent elements 16j .. 16j + 15.
+// Scaled by a power of two that brings its largest magnitude into [128, 256); returns the factor that undoes it (NaN
+// for a query that holds a NaN or an infinity).
+template <int HP>
+__device__ __forceinline__ float store_query(uint32_t q_base, int h, int lane, const uint4 (&v)[2]) {
+    const uint32_t w[8] = {v[0].x, v[0].y, v[0].z, v[0].w, v[1].x, v[1].y, v[1].z, v[1].w};
+    uint32_t top = 0;
 #pragma unroll
-    for (int k = 0; k < 4; ++k) dst[k] = make_float4(o[4 * k], o[4 * k + 1], o[4 * k + 2], o[4 * k + 3]);
-    if (lane == 0) {
-        p.ws_m[slot] = m;
-        p.ws_l[slot] = l;
+    for (int i = 0; i < 8; ++i) top = max(top, max(w[i] << 16 & 0x7FFFFFFFu, w[i] & 0x7FFF0000u));
+    top = __reduce_max_sync(0xffffffffu, top);
+    const int e = f16_range_exponent(__uint_as_float(top)) - 6;
+    const float up = exp2_int(e);
+    uint32_t hw[4], lw[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+        const uint32_t a = split16_e4m3x2(__uint_as_float(w[2 * k] << 16) * up, __uint_as_float(w[2 * k] & 0xFFFF0000u) * up);
+        const uint32_t b =
+            split16_e4m3x2(__uint_as_float(w[2 * k + 1] << 16) * up, __uint_as_float(w[2 * k + 1] & 0xFFFF0000u) * up);
+        hw[k] = byte_perm(a, b, 0x5410);
+        lw[k] = byte_perm(a, b, 0x7632);
     }
+    const uint32_t slab = q_base + (lane >> 3) * Fp4Layout<HP>::kQSlab;
+    st_shared_v4(slab + sw128_offset(h, lane & 7), hw[0], hw[1], hw[2], hw[3]);
+    st_shared_v4(slab + sw128_offset(HP + h, lane & 7), lw[0], lw[1], lw[2], lw[3]);
+    return top >= 0x7F800000u ? __uint_as_float(0x7FFFFFFFu) : exp2_int(-e);
 }
 
-__global__ void __launch_bounds__(128) fp4_merge_kernel(const Fp4Params p) {
-    __shared__ float o_lat[kR];
-    const int h = blockIdx.x, b = blockIdx.y, t = threadIdx.x;
-    const int len = min(max(__ldg(p.lens + b), 0), p.max_len);
-    float m = -INFINITY, l = 0.f, o[4] = {0.f, 0.f, 0.f, 0.f};
-    auto slot = [&](int i) { return (static_cast<size_t>(i) * p.B + b) * p.H + h; };
-    for (int i = 0; i < p.nsplit; ++i) m = fmaxf(m, p.ws_m[slot(i)]);
-    const float base = m == -INFINITY ? 0.f : m;
-    for (int i = 0; i < p.nsplit; ++i) {
-        const float w = exp2f(p.ws_m[slot(i)] - base), li = p.ws_l[slot(i)];
-        l += w * li;
-        if (w == 0.f && li == li) continue;
-        const float4 v = *(reinterpret_cast<const float4 *>(p.ws_o + slot(i) * kR) + t);
-        o[0] += w * v.x, o[1] += w * v.y, o[2] += w * v.z, o[3] += w * v.w;
+// ------------------------------------------------------------------ attention
+template <int HP>
+__global__ void __launch_bounds__(kThreads, 1)
+    fp4_attention_kernel(const __grid_constant__ CUtensorMap tm_codes, const __grid_constant__ CUtensorMap tm_scales,
+                         const Fp4Params p) {
+    using L = Fp4Layout<HP>;
+    constexpr int N = L::N, kSlabs = L::kSlabs;
+    extern __shared__ uint8_t smem_raw[];
+    const uint32_t raw = smem_u32(smem_raw), base = (raw + 1023u) & ~1023u;
+    Fp4Shared &sh = *reinterpret_cast<Fp4Shared *>(smem_raw + (base - raw) + L::END);
+    volatile int *abort_flag = &sh.abort;
+    auto bar = [](uint64_t &b) { return smem_u32(&b); };
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int group = static_cast<int>(blockIdx.x) % p.groups, share = static_cast<int>(blockIdx.x) / p.groups;
+    const int h0 = group * p.heads_per_group, heads = min(p.heads_per_group, p.H - h0);
+
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < kStages; ++i) mbar_init(bar(sh.stage_full[i]), 1), mbar_init(bar(sh.stage_empty[i]), 8);
+        for (int i = 0; i < kScaleSlots; ++i) mbar_init(bar(sh.scale_full[i]), 1), mbar_init(bar(sh.scale_empty[i]), 8);
+        for (int i = 0; i < kSlabs; ++i) mbar_init(bar(sh.slab_full[i]), 8), mbar_init(bar(sh.slab_free[i]), 1);
+        mbar_init(bar(sh.s_full), 1);
+        mbar_init(bar(sh.s_free), 4);
+        mbar_init(bar(sh.q_ready), 4);
+        for (int i = 0; i < kPBufs; ++i) mbar_init(bar(sh.p_full[i]), 4), mbar_init(bar(sh.p_free[i]), 1);
+        sh.abort = 0;
+        fence_mbar_init();
     }
+    if (threadIdx.x >= 64 && threadIdx.x < 64 + kTables) {   // magnitudes times 2^k as e4m3 bytes
+        const int i = threadIdx.x - 64;
+        const float f = i == kTables - 1 ? __uint_as_float(0x7FFFFFFFu) : (i == 0 ? 0.f : exp2_int(i - 14));
+        uint32_t b[4];
+        const float m[8] = {0.f, 0.5f, 1.f, 1.5f, 2.f, 3.f, 4.f, 6.f};
 #pragma unroll
-    for (int k = 0; k < 4; ++k) o_lat[4 * t + k] = len > 0 ? o[k] / l : 0.f;
+        for (int k = 0; k < 4; ++k) b[k] = cvt_e4m3x2(m[2 * k] * f, m[2 * k + 1] * f);
+        sh.table[i] = make_uint2(b[0] | b[1] << 16, b[2] | b[3] << 16);
+    }
+    if (warp == 1) {
+        tmem_alloc(smem_u32(&sh.tmem_base), 512);
+        tmem_relinquish();
+    }
+    tc_fence_before();
     __syncthreads();
-    float y = 0.f;
-    const uint32_t *w = reinterpret_cast<const uint32_t *>(p.w_uv + (static_cast<size_t>(h) * kDV + t) * kR);
-    for (int j = 0; j < kR / 2; ++j) {
-        const uint32_t v = __ldg(w + j);
-        y += __uint_as_float(v << 16) * o_lat[2 * j] + __uint_as_float(v & 0xFFFF0000u) * o_lat[2 * j + 1];
+    tc_fence_after();
+    const uint32_t tmem = sh.tmem_base;
+    grid_launch_dependents();   // the merge takes SMs as CTAs finish; it waits for the whole grid
+
+    Walk walk;
+    walk.start(p, share, lane, blockIdx.x == 0 && warp == 3 ? p.err : nullptr);
+    Segment seg;
+
+    if (warp < 4) {
+        regs_release<kRegsCtl>();
+        if (warp == 0 && lane == 0) {
+            // ---- TMA: per unit the scale bytes and four boxes of codes [128 rows x 128 latent]
+            tma_prefetch_desc(&tm_codes);
+            tma_prefetch_desc(&tm_scales);
+            uint32_t it = 0, un = 0;
+            bool ok = true;
+            while (ok && walk.next(seg)) {
+                for (int u = 0; ok && u < seg.units; ++u, ++un) {
+                    const int row = seg.row0 + u * kRows;
+                    const uint32_t sl = un % kScaleSlots;
+                    if (un >= kScaleSlots &&
+                        !(ok = mbar_wait(bar(sh.scale_empty[sl]), (un / kScaleSlots - 1) & 1, p.err, abort_flag)))
+                        break;
+                    mbar_arrive_expect_tx(bar(sh.scale_full[sl]), kScaleTile);
+                    tma_load_3d(base + L::SCALE + sl * kScaleTile, &tm_scales, bar(sh.scale_full[sl]), kR / 2, row, seg.seq);
+                    for (int k = 0; k < 4; ++k, ++it) {
+                        const uint32_t st = it % kStages;
+                        if (it >= kStages &&
+                            !(ok = mbar_wait(bar(sh.stage_empty[st]), (it / kStages - 1) & 1, p.err, abort_flag)))
+                            break;
+                        mbar_arrive_expect_tx(bar(sh.stage_full[st]), kStage);
+                        tma_load_3d(base + L::STAGE + st * kStage, &tm_codes, bar(sh.stage_full[st]), k * 64, row, seg.seq);
+                    }
+                }
+            }
+            if (!ok) *abort_flag = 1;
+            // no load may still be landing when the CTA exits
+            for (uint32_t k = it > kStages ? it - kStages : 0; k < it; ++k)
+                mbar_wait(bar(sh.stage_full[k % kStages]), (k / kStages) & 1, p.err);
+            // (an abort between the two kinds leaves `un` one behind the scale tiles asked for)
+            for (uint32_t k = un >= kScaleSlots ? un - kScaleSlots + (ok ? 0 : 1) : 0; k < un + (ok ? 0 : 1); ++k)
+                mbar_wait(bar(sh.scale_full[k % kScaleSlots]), (k / kScaleSlots) & 1, p.err, ok ? nullptr : abort_flag);
+        } else if (warp == 1 && lane == 0) {
+            // ---- S^T = c . q^T: four slabs of K = 128
+            constexpr uint32_t idesc = make_idesc_e4m3(128, N, 0, 0);
+            const uint64_t q0 = make_smem_desc(base + L::Q, 16, 1024), c0 = make_smem_desc(base + L::C, 16, 1024);
+            uint32_t it = 0, un = 0, ns = 0;
+            bool ok = true;
+            while (ok && walk.next(seg)) {
+                if (!(ok = mbar_wait(bar(sh.q_ready), ns++ & 1, p.err, abort_flag))) break;
+                for (int u = 0; ok && u < seg.units; ++u, ++un) {
+                    if (un >= 1 && !(ok = mbar_wait(bar(sh.s_free), (un - 1) & 1, p.err, abort_flag))) break;
+                    for (int k = 0; k < 4; ++k, ++it) {
+                        const uint32_t sl = it % kSlabs;
+                        if (!(ok = mbar_wait(bar(sh.slab_full[sl]), (it / kSlabs) & 1, p.err, abort_flag))) break;
+                        tc_fence_after();
+#pragma unroll
+                        for (int kk = 0; kk < 4; ++kk)
+                            umma_f8(tmem + L::S_COL, desc_add(c0, sl * kSlab + kk * 32), desc_add(q0, k * L::kQSlab + kk * 32),
+                                    idesc, (k | kk) != 0);
+                    }
+                    if (ok) umma_commit(bar(sh.s_full));
+                }
+            }
+            if (!ok) *abort_flag = 1;
+        } else if (warp == 2 && lane == 0) {
+            // ---- O^T += c^T . P^T: slab t holds latent columns [128 t, 128 t + 128)
+            constexpr uint32_t idesc = make_idesc_e4m3(128, N, 1, 1);
+            const uint64_t p0 = make_smem_desc(base + L::P, kSlab, 1024), c0 = make_smem_desc(base + L::C, kSlab, 1024);
+            uint32_t it = 0, un = 0;
+            bool ok = true;
+            while (ok && walk.next(seg)) {
+                for (int u = 0; ok && u < seg.units; ++u, ++un) {
+                    const uint32_t pb = un % kPBufs;
+                    if (!(ok = mbar_wait(bar(sh.p_full[pb]), (un / kPBufs) & 1, p.err, abort_flag))) break;
+                    tc_fence_after();
+                    for (int t = 0; t < 4; ++t, ++it) {
+                        const uint32_t sl = it % kSlabs;
+                        if (!(ok = mbar_wait(bar(sh.slab_full[sl]), (it / kSlabs) & 1, p.err, abort_flag))) break;
+#pragma unroll
+                        for (int kk = 0; kk < 4; ++kk)
+                            umma_f8(tmem + L::O_COL + t * N, desc_add(c0, sl * kSlab + kk * 4096),
+                                    desc_add(p0, pb * kSlab + kk * 4096), idesc, (u | kk) != 0);
+                        umma_commit(bar(sh.slab_free[sl]));
+                    }
+                    if (ok) umma_commit(bar(sh.p_free[pb]));
+                }
+            }
+            if (!ok) *abort_flag = 1;
+        }
+    } else if (warp < 8) {
+        regs_acquire<kRegsSoft>();
+        // ---- softmax: thread = row `t` of the unit (TMEM lane t); a failed wait is agreed on at the barriers
+        const int t = threadIdx.x - 128, quad = warp - 4;
+        const uint32_t lanes = tmem + (static_cast<uint32_t>(quad * 32) << 16);
+        uint32_t un = 0;
+        bool fail = false, more = walk.next(seg);
+        float l[HP];
+        while (more) {
+            // the segment's queries (S of the last unit before this has been read, so the buffer is free)
+            for (int i0 = quad; i0 < HP; i0 += 16) {
+                uint4 v[4][2];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const int h = i0 + 4 * i;
+                    const uint4 *src = reinterpret_cast<const uint4 *>(
+                                           p.q_abs + (static_cast<size_t>(seg.seq) * p.H + h0 + min(h, heads - 1)) * kR) +
+                                       lane * 2;
+                    v[i][0] = h < heads ? __ldg(src) : make_uint4(0, 0, 0, 0);
+                    v[i][1] = h < heads ? __ldg(src + 1) : make_uint4(0, 0, 0, 0);
+                }
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const int h = i0 + 4 * i;
+                    const float undo = store_query<HP>(base + L::Q, h, lane, v[i]);
+                    if (lane == 0) {   // padding heads: P = 0, never a new maximum
+                        sh.mul[h] = h < heads ? undo * p.scale_log2 : 0.f;
+                        sh.thr[h] = h < heads ? -INFINITY : INFINITY;
+                        sh.bias[h] = h < heads ? kBias : -INFINITY;
+                    }
+                }
+            }
+            fence_proxy_async_smem();
+            named_bar_sync(1, 128);
+            if (lane == 0) mbar_arrive(bar(sh.q_ready));
+#pragma unroll
+            for (int h = 0; h < HP; ++h) l[h] = 0.f;
+
+            for (int u = 0; u < seg.units; ++u, ++un) {
+                float a[HP];
+                fail |= !mbar_wait(bar(sh.s_full), un & 1, p.err, abort_flag);
+                __syncwarp();
+                const float ref = sh.ref[un & 1][t], row_scale = exp2_int(static_cast<int>(ref));
+                tc_fence_after();
+#pragma unroll
+                for (int g = 0; g < HP / 16; ++g) {
+                    float hi[16], lo[16];
+                    tmem_ld16(lanes + L::S_COL + g * 16, hi);
+                    tmem_ld16(lanes + L::S_COL + HP + g * 16, lo);
+                    tmem_wait_ld();
+#pragma unroll
+                    for (int k = 0; k < 16; ++k) a[g * 16 + k] = fmaf(lo[k], kLoPart, hi[k]) * row_scale;
+                }
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(bar(sh.s_free));
+                const bool valid = t < seg.len - seg.row0 - u * kRows;
+                bool past = fail;
+#pragma unroll
+                for (int h = 0; h < HP; h += 4) {
+                    const float4 m = lds4(sh.mul + h), th = lds4(sh.thr + h);
+                    const float mm[4] = {m.x, m.y, m.z, m.w}, tt[4] = {th.x, th.y, th.z, th.w};
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) {
+                        a[h + k] = valid ? fmaf(a[h + k], mm[k], ref) : -INFINITY;
+                        past |= a[h + k] > tt[k];
+                    }
+                }
+                if (named_bar_or(1, 128, past)) {
+                    if (named_bar_or(1, 128, fail)) break;
+                    // maxima over the 128 rows
+                    int top0 = INT_MIN, top1 = INT_MIN;   // lane j: heads j and 32 + j
+#pragma unroll
+                    for (int h = 0; h < HP; ++h) {
+                        const int x = __reduce_max_sync(0xffffffffu, a[h] == a[h] ? ordered(a[h]) : INT_MIN);
+                        if (lane == (h & 31)) (h < 32 ? top0 : top1) = x;
+                    }
+                    if (lane < HP) sh.red[quad][lane] = __int_as_float(top0);
+                    if (HP > 32 && lane < HP - 32) sh.red[quad][32 + lane] = __int_as_float(top1);
+                    if (t == 0) sh.flagged = 0;
+                    named_bar_sync(1, 128);
+                    if (t < HP) {
+                        int x = INT_MIN;
+#pragma unroll
+                        for (int q = 0; q < 4; ++q) x = max(x, __float_as_int(sh.red[q][t]));
+                        const float top = x == INT_MIN ? -INFINITY : from_ordered(x);
+                        float f = 1.f;
+                        if (top > sh.thr[t]) {
+                            f = fast_exp2((kBias - sh.bias[t]) - top);   // 2^(M_old - M_new); the first time l is 0
+                            sh.thr[t] = top + kSlack;
+                            sh.bias[t] = kBias - top;
+                            atomicOr(&sh.flagged, 1u << (t >> 4));
+                        }
+                        sh.fac[t] = f;
+                    }
+                    named_bar_sync(1, 128);
+                    if (u > 0) {
+                        const uint32_t flagged = sh.flagged;
+#pragma unroll
+                        for (int h = 0; h < HP; h += 4) {
+                            const float4 f = lds4(sh.fac + h);
+                            l[h] *= f.x, l[h + 1] *= f.y, l[h + 2] *= f.z, l[h + 3] *= f.w;
+                        }
+                        // the products of the unit before are complete before O^T is scaled
+                        fail |= !mbar_wait(bar(sh.p_free[(un - 1) % kPBufs]), ((un - 1) / kPBufs) & 1, p.err, abort_flag);
+                        __syncwarp();
+                        tc_fence_after();
+#pragma unroll 1
+                        for (int g = 0; g < HP / 16; ++g) {
+                            if (!(flagged >> g & 1)) continue;
+#pragma unroll 1
+                            for (int c = 0; c < 8; ++c) {   // latent tile c >> 1, hi or lo columns
+                                float o[16];
+                                const uint32_t at = lanes + L::O_COL + (c >> 1) * N + (c & 1) * HP + g * 16;
+                                tmem_ld16(at, o);
+                                tmem_wait_ld();
+#pragma unroll
+                                for (int k = 0; k < 16; k += 4) {
+                                    const float4 f = lds4(sh.fac + g * 16 + k);
+                                    o[k] *= f.x, o[k + 1] *= f.y, o[k + 2] *= f.z, o[k + 3] *= f.w;
+                                }
+                                tmem_st16(at, o);
+                            }
+                        }
+                        tmem_wait_st();
+                        tc_fence_before();
+                    }
+                }
+                // weights, their sums, and P^T as the MN-major N side: row t, hi bytes then lo bytes of all heads
+                const uint32_t pb = un % kPBufs;
+                if (un >= kPBufs) fail |= !mbar_wait(bar(sh.p_free[pb]), (un / kPBufs - 1) & 1, p.err, abort_flag);
+                const float unref = exp2_int(-static_cast<int>(ref));
+                const uint32_t prow = base + L::P + pb * kSlab;
+#pragma unroll
+                for (int g = 0; g < HP / 16; ++g) {
+                    uint32_t hw[4], lw[4];
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) {
+                        const int h = g * 16 + 4 * k;
+                        const float4 bi = lds4(sh.bias + h);
+                        const float x0 = fast_exp2(a[h] + bi.x), x1 = fast_exp2(a[h + 1] + bi.y);
+                        const float x2 = fast_exp2(a[h + 2] + bi.z), x3 = fast_exp2(a[h + 3] + bi.w);
+                        l[h] = fmaf(x0, unref, l[h]), l[h + 1] = fmaf(x1, unref, l[h + 1]);
+                        l[h + 2] = fmaf(x2, unref, l[h + 2]), l[h + 3] = fmaf(x3, unref, l[h + 3]);
+                        const uint32_t x = split16_e4m3x2(x0, x1), y = split16_e4m3x2(x2, x3);
+                        hw[k] = byte_perm(x, y, 0x5410);
+                        lw[k] = byte_perm(x, y, 0x7632);
+                    }
+                    st_shared_v4(prow + sw128_offset(t, g), hw[0], hw[1], hw[2], hw[3]);
+                    st_shared_v4(prow + sw128_offset(t, HP / 16 + g), lw[0], lw[1], lw[2], lw[3]);
+                }
+                fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(bar(sh.p_full[pb]));
+            }
+            // ---- drain: l over the 128 rows, then O^T (lane = latent column of its tile)
+#pragma unroll
+            for (int h = 0; h < HP; ++h) {
+                float s = l[h];
+#pragma unroll
+                for (int o = 16; o >= 1; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+                if (lane == (h & 31)) sh.red[quad][h] = s;
+            }
+            const uint32_t last = un - 1;
+            fail |= !mbar_wait(bar(sh.p_free[last % kPBufs]), (last / kPBufs) & 1, p.err, abort_flag);
+            if (named_bar_or(1, 128, fail)) break;
+            tc_fence_after();
+            const size_t slot = static_cast<size_t>(seg.slot) * p.H + h0;
+            if (t < heads) {
+                p.ws_m[slot + t] = -sh.bias[t];
+                p.ws_l[slot + t] = (sh.red[0][t] + sh.red[1][t]) + (sh.red[2][t] + sh.red[3][t]);
+            }
+#pragma unroll 1
+            for (int c = 0; c < 4 * (HP / 16); ++c) {
+                const int tile = c / (HP / 16), g = c % (HP / 16);
+                float hi[16], lo[16];
+                tmem_ld16(lanes + L::O_COL + tile * N + g * 16, hi);
+                tmem_ld16(lanes + L::O_COL + tile * N + HP + g * 16, lo);
+                tmem_wait_ld();
+                float *dst = p.ws_o + (slot + g * 16) * kR + tile * 128 + t;
+#pragma unroll
+                for (int k = 0; k < 16; ++k)
+                    if (g * 16 + k < heads) dst[static_cast<size_t>(k) * kR] = fmaf(lo[k], kLoPart, hi[k]);
+            }
+            tc_fence_before();
+            named_bar_sync(1, 128);   // red, thr and bias are read before the next segment sets them
+            more = walk.next(seg);
+        }
+        if (fail) *abort_flag = 1;
+    } else {
+        regs_release<kRegsExp>();
+        // ---- expansion: 32 codes (a group) per thread and step, two steps per slab
+        const int tid = threadIdx.x - 256;
+        uint32_t it = 0, un = 0;
+        bool fail = false, stop = false;
+        while (!stop && walk.next(seg)) {
+            for (int u = 0; u < seg.units; ++u, ++un) {
+                const int rows = min(kRows, seg.len - seg.row0 - u * kRows);
+                const uint32_t sc = un % kScaleSlots, tile = base + L::SCALE + sc * kScaleTile;
+                fail |= !mbar_wait(bar(sh.scale_full[sc]), (un / kScaleSlots) & 1, p.err, abort_flag);
+                // the unit's first slab is free once the products two units back are issued and done, so the softmax
+                // has read what the ref slot held
+                if (it >= kSlabs)
+                    fail |= !mbar_wait(bar(sh.slab_free[it % kSlabs]), (it / kSlabs - 1) & 1, p.err, abort_flag);
+                if (tid < kRows) {   // the row's largest scale exponent (NaN bytes aside) becomes e4m3's 2^6
+                    const uint4 v = ld_shared_v4(tile + tid * 16);
+                    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+                    uint32_t top = kFp4ScaleMin;
+#pragma unroll
+                    for (int k = 0; k < 16; ++k) {
+                        const uint32_t X = w[k >> 2] >> (8 * (k & 3)) & 0xFFu;
+                        if (X != kFp4ScaleNan) top = max(top, X);
+                    }
+                    top = min(top, static_cast<uint32_t>(kFp4ScaleMax));
+                    sh.ref[un & 1][tid] = static_cast<float>(static_cast<int>(top) - 127 - 6);
+                }
+                if (named_bar_or(2, 256, fail)) {
+                    stop = true;
+                    break;
+                }
+                for (int k = 0; k < 4; ++k, ++it) {
+                    const uint32_t st = it % kStages, sl = it % kSlabs;
+                    fail |= !mbar_wait(bar(sh.stage_full[st]), (it / kStages) & 1, p.err, abort_flag);
+                    if (k > 0 && it >= kSlabs)
+                        fail |= !mbar_wait(bar(sh.slab_free[sl]), (it / kSlabs - 1) & 1, p.err, abort_flag);
+#pragma unroll
+                    for (int half = 0; half < 2; ++half) {
+                        const int row = half * 64 + (tid >> 2), g = tid & 3;
+                        const uint4 v = ld_shared_v4(base + L::STAGE + st * kStage + row * 64 + g * 16);
+                        uint32_t X;
+                        asm volatile("ld.shared.u8 %0, [%1];" : "=r"(X) : "r"(tile + row * 16 + k * 4 + g) : "memory");
+                        const int top = static_cast<int>(sh.ref[un & 1][row]) + 127 + 6;
+                        const int Xc = min(max(static_cast<int>(X), kFp4ScaleMin), kFp4ScaleMax);
+                        uint2 tb = sh.table[X == kFp4ScaleNan ? kTables - 1 : max(Xc - top + 20, 0)];
+                        if (row >= rows) tb = make_uint2(0u, 0u);
+                        const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+                        uint32_t o[8];
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            o[2 * i] = expand4(w[i], tb);
+                            o[2 * i + 1] = expand4(w[i] >> 16, tb);
+                        }
+                        const uint32_t slab = base + L::C + sl * kSlab;
+                        st_shared_v4(slab + sw128_offset(row, 2 * g), o[0], o[1], o[2], o[3]);
+                        st_shared_v4(slab + sw128_offset(row, 2 * g + 1), o[4], o[5], o[6], o[7]);
+                    }
+                    fence_proxy_async_smem();
+                    __syncwarp();
+                    if (lane == 0) {
+                        mbar_arrive(bar(sh.slab_full[sl]));
+                        mbar_arrive(bar(sh.stage_empty[st]));
+                        if (k == 3) mbar_arrive(bar(sh.scale_empty[sc]));
+                    }
+                }
+            }
+        }
+        if (fail) *abort_flag = 1;
     }
-    const size_t at = (static_cast<size_t>(b) * p.H + h) * kDV + t;
-    if (p.gate) y /= 1.f + exp2f(-__bfloat162float(p.gate[at]) * kLog2e);
-    p.out[at] = __float2bfloat16(y);
+
+    __syncwarp();
+    tc_fence_before();
+    __syncthreads();
+    if (warp == 1) tmem_dealloc(tmem, 512);
 }
 
-int splits(int B, int H, int max_len, int num_sms) {
-    const long long warps = static_cast<long long>(num_sms) * 32, want = (warps + B * H - 1) / (static_cast<long long>(B) * H);
-    const long long most = (max_len + 63) / 64;
-    const long long n = want < most ? want : most;
-    return static_cast<int>(n < 1 ? 1 : (n > 4096 ? 4096 : n));
+// ------------------------------------------------------------------ merge
+constexpr int kMRows = 32;                          // sequences per CTA
+constexpr int kMergeThreads = 512;
+constexpr uint32_t kOSlab = 2 * kMRows * 128;       // o_lat [hi rows | lo rows] x 64 latent columns, bf16
+constexpr uint32_t kWSlab = kDV * 128;              // W_UV[h] [128 x 64 latent columns]
+constexpr int kWStages = 2;
+constexpr uint32_t MW_OFF = 8 * kOSlab, MBAR_OFF = MW_OFF + kWStages * kWSlab;
+constexpr uint32_t kSmemMerge = MBAR_OFF + 128 + 1024;
+static_assert(16 * kR * 4 <= 8 * kOSlab, "the warps' partial rows fit the o_lat tile");
+
+struct MergeParams {
+    const int *lens;
+    const float *ws_o, *ws_m, *ws_l;
+    const __nv_bfloat16 *gate;
+    __nv_bfloat16 *out;
+    int *err;
+    int B, H, max_len, G;
+};
+
+__global__ void __launch_bounds__(kMergeThreads, 2)
+    fp4_merge_kernel(const __grid_constant__ CUtensorMap tm_wuv, const MergeParams p) {
+    extern __shared__ uint8_t smem_raw[];
+    const uint32_t raw = smem_u32(smem_raw), base = (raw + 1023u) & ~1023u;
+    uint64_t *w_full = reinterpret_cast<uint64_t *>(smem_raw + (base - raw) + MBAR_OFF), *w_empty = w_full + kWStages,
+             *done = w_empty + kWStages;
+    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(done + 1);
+    __shared__ long long s_pre[kMRows], s_chunk[kMRows], s_total;   // per sequence: first virtual unit, first chunk number
+    __shared__ int s_len[kMRows];
+    __shared__ float s_m[16], s_l[16];
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int h = blockIdx.x, b0 = static_cast<int>(blockIdx.y) * kMRows, nb = min(kMRows, p.B - b0);
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < 2 * kWStages + 1; ++i) mbar_init(smem_u32(w_full + i), 1);
+        fence_mbar_init();
+    }
+    if (warp == 0) {
+        tmem_alloc(smem_u32(tmem_slot), 64);
+        tmem_relinquish();
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = *tmem_slot;
+    auto load_w = [&](int k) {   // latent columns [64 k, 64 k + 64) of W_UV[h]
+        const uint32_t b = smem_u32(w_full + k % kWStages);
+        mbar_arrive_expect_tx(b, kWSlab);
+        tma_load_2d(base + MW_OFF + (k % kWStages) * kWSlab, &tm_wuv, b, k * 64, h * kDV);
+    };
+    if (threadIdx.x == 0) {
+        tma_prefetch_desc(&tm_wuv);
+        for (int k = 0; k < kWStages; ++k) load_w(k);
+        for (int k = kWStages; k < 8; ++k) tma_prefetch_l2_2d(&tm_wuv, k * 64, h * kDV);
+    }
+    if (warp == 1) {
+        long long run = 0, chunks = 0;
+        for (int i0 = 0; i0 < p.B; i0 += 32) {
+            const int b = i0 + lane;
+            const int len = b < p.B ? read_len(p.lens, b, p.max_len, nullptr) : 0;
+            const long long u = units_of(len), incl = warp_scan(u, lane);
+            const int n = len > 0 ? chunks_of(len) : 0, nincl = warp_scan(n, lane);
+            if (b >= b0 && b < b0 + nb) {
+                s_pre[b - b0] = run + incl - u;
+                s_chunk[b - b0] = chunks + nincl - n;
+                s_len[b - b0] = len;
+            }
+            run += __shfl_sync(0xffffffffu, incl, 31);
+            chunks += __shfl_sync(0xffffffffu, nincl, 31);
+        }
+        if (lane == 0) s_total = run;
+    }
+    __syncthreads();
+    const long long total = s_total;
+    // launched as a programmatic dependent: what is above overlaps the attention's tail, its segments are complete
+    // and visible after this
+    grid_dependency_wait();
+
+    // `per` warps share a sequence (all 16 when it is alone): warp `sub` takes every per-th share of the work axis.
+    // A lane holds four latent columns of each 128: 4 lane + 128 q.
+    int per = 16;
+    while (per > 1 && 16 / per < nb) per >>= 1;
+    const int sub = warp % per;
+    float o[16], M = -INFINITY, Lsum = 0.f;
+    auto put = [&](int i, const float (&x)[16], float mul) {   // row i of the o_lat tile, hi and lo parts
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+            float y[4], z[4];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                y[k] = x[4 * q + k] * mul;
+                z[k] = y[k] - __bfloat162float(__float2bfloat16(y[k]));
+            }
+            const uint32_t at = base + (2 * q + (lane >> 4)) * kOSlab + 8 * (lane & 1);
+            const uint32_t ch = (lane & 15) >> 1;
+            asm volatile("st.shared.v2.b32 [%0], {%1, %2};" ::"r"(at + sw128_offset(i, ch)), "r"(pack_bf16x2(y[0], y[1])),
+                         "r"(pack_bf16x2(y[2], y[3])) : "memory");
+            asm volatile("st.shared.v2.b32 [%0], {%1, %2};" ::"r"(at + sw128_offset(kMRows + i, ch)),
+                         "r"(pack_bf16x2(z[0], z[1])), "r"(pack_bf16x2(z[2], z[3])) : "memory");
+        }
+    };
+    for (int i = warp / per; i < nb; i += 16 / per) {
+        const int len = s_len[i];
+        M = -INFINITY, Lsum = 0.f;
+#pragma unroll
+        for (int k = 0; k < 16; ++k) o[k] = 0.f;
+        const int chunks = len > 0 ? chunks_of(len) : 0;
+        for (int j = 0; j < chunks; ++j) {
+            const int rows = min(kChunkRows, len - j * kChunkRows);
+            const long long r0 = s_pre[i] + static_cast<long long>(j) * kChunkSpan + kOverUnits,
+                            r1 = r0 + (rows + kRows - 1) / kRows;
+            const int c_first = static_cast<int>(((r0 + 1) * p.G - 1) / total);
+            for (int c0 = c_first + sub; c0 < p.G && share_lo(total, c0, p.G) < r1; c0 += 32 * per) {
+                const int c = c0 + lane * per;
+                const bool has = c < p.G && min(share_lo(total, c + 1, p.G), r1) > max(share_lo(total, c, p.G), r0);
+                const size_t slot = static_cast<size_t>(c + s_chunk[i] + j) * p.H + h;
+                const float m = has ? __ldg(p.ws_m + slot) : -INFINITY;
+                float w = m;
+#pragma unroll
+                for (int q = 16; q >= 1; q >>= 1) w = fmaxf(w, __shfl_xor_sync(0xffffffffu, w, q));
+                const float top = fmaxf(M, w), f = M == -INFINITY ? 0.f : fast_exp2(M - top);
+                w = has ? fast_exp2(m - top) : 0.f;
+                float s = has ? w * __ldg(p.ws_l + slot) : 0.f;
+#pragma unroll
+                for (int q = 16; q >= 1; q >>= 1) s += __shfl_xor_sync(0xffffffffu, s, q);
+                Lsum = Lsum * f + s;
+                M = top;
+#pragma unroll
+                for (int k = 0; k < 16; ++k) o[k] *= f;
+                for (unsigned left = __ballot_sync(0xffffffffu, has); left;) {   // two segments' loads in flight
+                    const int a = __ffs(left) - 1;
+                    left &= left - 1;
+                    const int b = left ? __ffs(left) - 1 : a;
+                    const float wa = __shfl_sync(0xffffffffu, w, a), wb = left ? __shfl_sync(0xffffffffu, w, b) : 0.f;
+                    const float4 *sa = reinterpret_cast<const float4 *>(p.ws_o + __shfl_sync(0xffffffffu, slot, a) * kR) + lane;
+                    const float4 *sb = reinterpret_cast<const float4 *>(p.ws_o + __shfl_sync(0xffffffffu, slot, b) * kR) + lane;
+                    const bool two = left != 0;
+                    left &= left - 1;
+                    float4 va[4], vb[4];
+#pragma unroll
+                    for (int q = 0; q < 4; ++q) {
+                        va[q] = __ldg(sa + 32 * q);
+                        vb[q] = two ? __ldg(sb + 32 * q) : make_float4(0.f, 0.f, 0.f, 0.f);
+                    }
+#pragma unroll
+                    for (int q = 0; q < 4; ++q) {
+                        o[4 * q] += wa * va[q].x + wb * vb[q].x;
+                        o[4 * q + 1] += wa * va[q].y + wb * vb[q].y;
+                        o[4 * q + 2] += wa * va[q].z + wb * vb[q].z;
+                        o[4 * q + 3] += wa * va[q].w + wb * vb[q].w;
+                    }
+                }
+            }
+        }
+        if (per == 1) put(i, o, len > 0 ? 1.f / Lsum : 0.f);
+    }
+    if (per > 1) {   // join the warps of each sequence (here every warp has had at most one)
+        float *part = reinterpret_cast<float *>(smem_raw + (base - raw));
+        float4 *mine = reinterpret_cast<float4 *>(part + warp * kR) + lane;
+#pragma unroll
+        for (int q = 0; q < 4; ++q) mine[32 * q] = make_float4(o[4 * q], o[4 * q + 1], o[4 * q + 2], o[4 * q + 3]);
+        if (lane == 0) s_m[warp] = M, s_l[warp] = Lsum;
+        __syncthreads();
+        const int i = warp / per, first = i * per;
+        if (sub == 0 && i < nb) {
+            M = -INFINITY, Lsum = 0.f;
+            for (int k = 0; k < per; ++k) M = fmaxf(M, s_m[first + k]);
+#pragma unroll
+            for (int k = 0; k < 16; ++k) o[k] = 0.f;
+            for (int k = 0; k < per; ++k) {
+                if (s_m[first + k] == -INFINITY) continue;   // a warp without a segment
+                const float w = fast_exp2(s_m[first + k] - M);
+                Lsum += w * s_l[first + k];
+                const float4 *src = reinterpret_cast<const float4 *>(part + (first + k) * kR) + lane;
+#pragma unroll
+                for (int q = 0; q < 4; ++q) {
+                    const float4 v = src[32 * q];
+                    o[4 * q] += w * v.x, o[4 * q + 1] += w * v.y, o[4 * q + 2] += w * v.z, o[4 * q + 3] += w * v.w;
+                }
+            }
+        }
+        __syncthreads();   // the partial rows are read before the tile is written over them
+        if (sub == 0 && i < nb) put(i, o, s_len[i] > 0 ? 1.f / Lsum : 0.f);
+    }
+    fence_proxy_async_smem();
+    tc_fence_before();
+    __syncthreads();
+    if (threadIdx.x == 0) {
+        // [128 x hi | lo rows] = W_UV[h] . o_lat^T over eight 64-column slabs of the latent
+        constexpr uint32_t idesc = make_idesc_bf16(kDV, 2 * kMRows, 0, 0);
+        tc_fence_after();
+        bool ok = true;
+        int loaded = kWStages;
+        for (int k = 0; ok && k < 8; ++k) {
+            const int st = k % kWStages;
+            if (!(ok = mbar_wait(smem_u32(w_full + st), (k / kWStages) & 1, p.err))) break;
+            tc_fence_after();
+#pragma unroll
+            for (int kk = 0; kk < 4; ++kk)
+                umma_bf16(tmem, make_smem_desc(base + MW_OFF + st * kWSlab + kk * 32, 16, 1024),
+                          make_smem_desc(base + k * kOSlab + kk * 32, 16, 1024), idesc, (k | kk) != 0);
+            umma_commit(smem_u32(w_empty + st));
+            if (k + kWStages < 8) {
+                if (!(ok = mbar_wait(smem_u32(w_empty + st), (k / kWStages) & 1, p.err))) break;
+                load_w(k + kWStages);
+                ++loaded;
+            }
+        }
+        if (ok) umma_commit(smem_u32(done));
+        if (!ok)   // no load may still be landing when the CTA exits
+            for (int k = 0; k < loaded; ++k) mbar_wait(smem_u32(w_full + k % kWStages), (k / kWStages) & 1, p.err);
+    }
+    __syncwarp();
+    const bool ok = mbar_wait(smem_u32(done), 0, p.err);
+    tc_fence_after();
+    if (warp < 8 && __all_sync(0xffffffffu, ok)) {   // warp: output column 32 (warp & 3) + lane, rows 16 (warp >> 2) ..
+        const int v = (warp & 3) * 32 + lane, i0 = (warp >> 2) * 16;
+        const uint32_t at = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16) + i0;
+        float hi[16], lo[16];
+        tmem_ld16(at, hi);
+        tmem_ld16(at + kMRows, lo);
+        tmem_wait_ld();
+#pragma unroll
+        for (int k = 0; k < 16; ++k) {
+            if (i0 + k >= nb) break;
+            const size_t off = (static_cast<size_t>(b0 + i0 + k) * p.H + h) * kDV + v;
+            float y = hi[k] + lo[k];
+            if (p.gate) y *= __fdividef(1.f, 1.f + fast_exp2(-__bfloat162float(p.gate[off]) * kLog2e));
+            p.out[off] = __float2bfloat16(y);
+        }
+    }
+    tc_fence_before();
+    __syncthreads();
+    if (warp == 0) tmem_dealloc(tmem, 64);
+}
+
+// ------------------------------------------------------------------ host
+CUresult encode_map(CUtensorMap *m, CUtensorMapDataType type, CUtensorMapSwizzle swizzle, const void *ptr, int rank,
+                    const cuuint64_t *dims, const cuuint64_t *strides, const cuuint32_t *box) {
+    auto fn = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(tensor_map_encode_fn());
+    if (!fn) return CUDA_ERROR_NOT_SUPPORTED;
+    const cuuint32_t es[3] = {1, 1, 1};
+    return fn(m, type, rank, const_cast<void *>(ptr), dims, strides, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle,
+              CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+}
+
+// Heads per CTA: one group up to 48 heads, two above; the tile's columns are padded to 16, 32 or 48.
+int head_groups(int H) { return H > 48 ? 2 : 1; }
+int shares(int H, int num_sms) {
+    const int g = num_sms / head_groups(H);
+    return g < 1 ? 1 : g;
+}
+size_t slot_count(int B, int max_len, int G) {
+    return static_cast<size_t>(G) + static_cast<size_t>(B) * (max_len > 0 ? chunks_of(max_len) : 0);
+}
+
+template <int HP>
+cudaError_t launch_attention(const CUtensorMap &codes, const CUtensorMap &scales, const Fp4Params &p, cudaStream_t s) {
+    using L = Fp4Layout<HP>;
+    cudaError_t e = cudaFuncSetAttribute(fp4_attention_kernel<HP>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                         static_cast<int>(L::kSmem));
+    if (e != cudaSuccess) return e;
+    cudaFuncAttributes fa;   // the kernel's register split assumes this launch budget
+    if ((e = cudaFuncGetAttributes(&fa, fp4_attention_kernel<HP>)) != cudaSuccess) return e;
+    if (fa.numRegs != static_cast<int>(kRegsLaunch)) return cudaErrorInvalidConfiguration;
+    note_launch();
+    fp4_attention_kernel<HP><<<p.G * p.groups, kThreads, L::kSmem, s>>>(codes, scales, p);
+    return cudaGetLastError();
 }
 
 }  // namespace
 
 size_t decode_fp4_workspace_bytes(int B, int H, int max_len, int num_sms) {
-    return static_cast<size_t>(splits(B, H, max_len, num_sms)) * B * H * (kR + 2) * sizeof(float);
+    return slot_count(B, max_len, shares(H, num_sms)) * H * (kR + 2) * sizeof(float);
 }
 
 cudaError_t launch_decode_fp4(const DecodeArgs &a, cudaStream_t s) {
-    if (!decode_bf16_supports(a.H, a.d_v, a.r) || a.B > 65535) return cudaErrorInvalidValue;
+    if (!decode_bf16_supports(a.H, a.d_v, a.r)) return cudaErrorInvalidValue;
     Fp4Params p;
     p.q_abs = static_cast<const __nv_bfloat16 *>(a.q_abs);
-    p.w_uv = static_cast<const __nv_bfloat16 *>(a.w_uv);
-    p.gate = static_cast<const __nv_bfloat16 *>(a.gate);
-    p.c4 = static_cast<const uint8_t *>(a.c_cache);
-    p.ld = a.ld_cache;
     p.lens = a.lens;
-    p.out = static_cast<__nv_bfloat16 *>(a.out);
-    p.nsplit = splits(a.B, a.H, a.max_len, a.num_sms);
-    const size_t slots = static_cast<size_t>(p.nsplit) * a.B * a.H;
-    p.ws_o = static_cast<float *>(a.workspace);
-    p.ws_m = p.ws_o + slots * kR;
-    p.ws_l = p.ws_m + slots;
-    p.err = a.dev_err;
     p.B = a.B;
     p.H = a.H;
     p.max_len = a.max_len;
+    p.groups = head_groups(a.H);
+    p.heads_per_group = (a.H + p.groups - 1) / p.groups;
+    p.G = shares(a.H, a.num_sms);
+    const size_t slots = slot_count(a.B, a.max_len, p.G);
+    if (slots * a.H * (kR + 2) * sizeof(float) > a.workspace_bytes) return cudaErrorInvalidValue;
+    p.ws_o = static_cast<float *>(a.workspace);
+    p.ws_m = p.ws_o + slots * a.H * kR;
+    p.ws_l = p.ws_m + slots * a.H;
+    p.err = a.dev_err;
     p.scale_log2 = a.scale * kLog2e;
-    note_launch();
-    fp4_split_kernel<<<dim3((a.H + 3) / 4, p.nsplit, a.B), 128, 0, s>>>(p);
-    cudaError_t e = cudaGetLastError();
+    CUtensorMap tm_codes, tm_scales, tm_wuv;
+    {
+        const cuuint64_t rows = static_cast<cuuint64_t>(a.max_len > 0 ? a.max_len : 1);
+        const cuuint64_t dims[3] = {kR / 2 + kR / 32, rows, static_cast<cuuint64_t>(a.B)};
+        const cuuint64_t strides[2] = {static_cast<cuuint64_t>(a.ld_cache), rows * static_cast<cuuint64_t>(a.ld_cache)};
+        const cuuint32_t box[3] = {64, kRows, 1}, sbox[3] = {16, kRows, 1};
+        const cuuint64_t wd[2] = {kR, static_cast<cuuint64_t>(a.H) * kDV}, ws[1] = {kR * 2};
+        const cuuint32_t wb[2] = {64, kDV};
+        if (encode_map(&tm_codes, CU_TENSOR_MAP_DATA_TYPE_UINT8, CU_TENSOR_MAP_SWIZZLE_NONE, a.c_cache, 3, dims, strides,
+                       box) != CUDA_SUCCESS ||
+            encode_map(&tm_scales, CU_TENSOR_MAP_DATA_TYPE_UINT8, CU_TENSOR_MAP_SWIZZLE_NONE, a.c_cache, 3, dims, strides,
+                       sbox) != CUDA_SUCCESS ||
+            encode_map(&tm_wuv, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, CU_TENSOR_MAP_SWIZZLE_128B, a.w_uv, 2, wd, ws, wb) !=
+                CUDA_SUCCESS)
+            return cudaErrorInvalidValue;
+    }
+    const int hp = p.heads_per_group;
+    cudaError_t e = hp <= 16   ? launch_attention<16>(tm_codes, tm_scales, p, s)
+                    : hp <= 32 ? launch_attention<32>(tm_codes, tm_scales, p, s)
+                               : launch_attention<48>(tm_codes, tm_scales, p, s);
     if (e != cudaSuccess) return e;
+    e = cudaFuncSetAttribute(fp4_merge_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(kSmemMerge));
+    if (e != cudaSuccess) return e;
+    const MergeParams mp{a.lens, p.ws_o, p.ws_m, p.ws_l, static_cast<const __nv_bfloat16 *>(a.gate),
+                         static_cast<__nv_bfloat16 *>(a.out), a.dev_err, a.B, a.H, a.max_len, p.G};
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(a.H, (a.B + kMRows - 1) / kMRows);
+    cfg.blockDim = dim3(kMergeThreads);
+    cfg.dynamicSmemBytes = kSmemMerge;
+    cfg.stream = s;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
     note_launch();
-    fp4_merge_kernel<<<dim3(a.H, a.B), 128, 0, s>>>(p);
-    return cudaGetLastError();
+    return cudaLaunchKernelEx(&cfg, fp4_merge_kernel, tm_wuv, mp);
 }
 
 }  // namespace mla
