@@ -18,12 +18,13 @@
 //
 // Softmax of one unit: thread = row, so every head's statistics lie across lanes.  With a = score * log2 e + ref,
 //   P = 2^(a - M + 8), l += P * 2^-ref,   M[head] >= running max of a - 0.75
-// M moves only when some row exceeds it by more than 0.75 (P <= 2^8.75 = 430, inside e4m3's 448): a barrier with an
-// OR tells whether any does, and only then are maxima taken across lanes and O^T rescaled.  A weight below 2^-22 of
-// the largest is lost; sequences are cut into chunks of 32768 rows with maxima of their own, so at most 2^-8 of a
-// chunk's weight can go that way.
+// M moves only when some row exceeds it by more than 0.75 (P <= 2^8.75 = 430, inside e4m3's 448), then to one above
+// that row: a barrier with an OR tells whether any does, and only then are the maxima of those heads taken across
+// lanes and their columns of O^T rescaled.  A weight below 2^-22 of the largest is lost; sequences are cut into chunks
+// of 32768 rows with maxima of their own, so less than 2^-7 of a chunk's weight can go that way.
 //
-// Warps: 0 TMA, 1 issues S, 2 issues O, 4-7 softmax (and q_abs, rescale, drain), 8-15 expand.  The expansion is a byte
+// Warps: 0 TMA, 1 issues S, 2 issues O, 4-11 softmax (and q_abs, rescale, drain; half of the heads to each of two
+// warpgroups that never wait for one another), 12-19 expand.  The expansion is a byte
 // permute per four codes: the group's exponent selects an 8-byte table of e4m3 magnitudes, the codes' three magnitude
 // bits are the selector.
 //
@@ -46,49 +47,49 @@ constexpr int kRows = 128;                 // cache rows per unit
 constexpr int kChunkUnits = 256;           // units of a sequence that share one running maximum per segment
 constexpr int kChunkRows = kChunkUnits * kRows;
 constexpr int kOverUnits = 2;              // what starting a segment costs, in units (query, first fill, drain)
-constexpr int kThreads = 512;
+constexpr int kThreads = 640;               // warps 0-3 control, 4-11 softmax, 12-19 expansion
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kBias = 8.f;               // P = 2^(a - M + kBias)
-constexpr float kSlack = 0.75f;
-// Register split of the 4 warpgroups x 128 launched: control, softmax, 2 x expansion.
-constexpr uint32_t kRegsCtl = 88, kRegsSoft = 208, kRegsExp = 104, kRegsLaunch = 128;
-static_assert(kRegsCtl + kRegsSoft + 2 * kRegsExp <= 4 * kRegsLaunch, "register split exceeds the launch");
+constexpr float kHead = 1.f, kSlack = 0.75f;   // a new maximum is set kHead above the row that forced it
+// Register split of the 5 warpgroups x 96 launched: control, 2 x softmax, 2 x expansion.
+constexpr uint32_t kRegsCtl = 64, kRegsSoft = 128, kRegsExp = 80, kRegsLaunch = 96;
+static_assert(kRegsCtl + 2 * kRegsSoft + 2 * kRegsExp <= 5 * kRegsLaunch, "register split exceeds the launch");
 
 constexpr uint32_t kSlab = 16384;          // [128 rows x 128 latent] e4m3, 128-byte swizzle
 constexpr uint32_t kStage = 8192;          // codes of one slab: [128 rows x 64 bytes]
 constexpr uint32_t kScaleTile = 2048;      // [128 rows x 16 scale bytes]
-constexpr int kStages = 4, kScaleSlots = 3, kPBufs = 2;
+constexpr int kScaleSlots = 3, kSlabs = 8;   // expanded tiles in flight: two units
 constexpr int kTables = 22;                // exponents -14 (all zero) .. 6 below the row's largest, then NaN
 
+// Heads of a CTA are padded to HP and shared by two softmax warpgroups of HW each; a warpgroup's columns of the N side
+// are its heads' hi parts, then their lo parts.
 template <int HP>
 struct Fp4Layout {
-    static constexpr int N = 2 * HP;                                   // hi and lo columns
-    static constexpr int kSlabs = HP == 48 ? 6 : (HP == 32 ? 7 : 8);   // expanded tiles in flight, four per unit
+    static constexpr int HW = HP / 2, N = 2 * HP;
+    static constexpr int kStages = HP == 16 ? 4 : 3, kPBufs = HP == 48 ? 1 : 2, kSBufs = HP == 48 ? 1 : 2;
     static constexpr uint32_t kQSlab = N * 128;                        // [N x 128 latent] e4m3
     static constexpr uint32_t Q = 0, C = Q + 4 * kQSlab, P = C + kSlabs * kSlab, STAGE = P + kPBufs * kSlab,
                               SCALE = STAGE + kStages * kStage, END = SCALE + kScaleSlots * kScaleTile;
     static constexpr uint32_t kSmem = END + 4096 + 1024;               // + Fp4Shared + alignment slack
     static constexpr uint32_t S_COL = 0, O_COL = 128;                  // TMEM columns
-    static_assert(kQSlab % 1024 == 0 && O_COL + 4 * N <= 512 && N <= 128, "layout");
-    static_assert(kSlabs <= 8, "a row's ref slot is reused two units later");
+    static_assert(kQSlab % 1024 == 0 && O_COL + 4 * N <= 512 && kSBufs * N <= O_COL && HW % 8 == 0, "layout");
     static_assert(kSmem <= 232448, "attention kernel exceeds shared memory");
 };
 
 struct Fp4Shared {
-    uint64_t stage_full[kStages], stage_empty[kStages];
+    uint64_t stage_full[4], stage_empty[4];
     uint64_t scale_full[kScaleSlots], scale_empty[kScaleSlots];
-    uint64_t slab_full[8], slab_free[8];
-    uint64_t s_full, s_free, q_ready;
-    uint64_t p_full[kPBufs], p_free[kPBufs];
+    uint64_t slab_full[kSlabs], slab_free[kSlabs];
+    uint64_t s_full[2], s_free[2], q_ready;
+    uint64_t p_full[2], p_free[2];
     uint32_t tmem_base;
     int abort;
-    uint32_t flagged;                      // 16-head groups whose maximum moved
-    uint32_t pad_;
+    uint32_t moved[2];                     // per warpgroup: heads whose maximum moved
     uint2 table[kTables];
     alignas(16) float ref[2][kRows];
     // per head: score factor, M + slack, kBias - M, 2^(M_old - M_new)
     alignas(16) float mul[48], thr[48], bias[48], fac[48];
-    float red[4][48];
+    float red[4][48];                      // per warp of a warpgroup and head
 };
 static_assert(sizeof(Fp4Shared) <= 4096, "shared block too large");
 
@@ -218,7 +219,12 @@ __device__ __forceinline__ int ordered(float x) {
 __device__ __forceinline__ float from_ordered(int i) { return __int_as_float(i >= 0 ? i : i ^ 0x7FFFFFFF); }
 __device__ __forceinline__ float4 lds4(const float *p) { return *reinterpret_cast<const float4 *>(p); }
 
-// One head's query into the N side of S: row h (hi) and row HP + h (lo), lane j the latent elements 16j .. 16j + 15.
+// N-side row of head h's hi part (its lo part is HW rows further).
+template <int HP>
+__device__ __forceinline__ int hi_row(int h) {
+    return h < HP / 2 ? h : h + HP / 2;
+}
+// One head's query into the N side of S, lane j the latent elements 16j .. 16j + 15.
 // Scaled by a power of two that brings its largest magnitude into [128, 256); returns the factor that undoes it (NaN
 // for a query that holds a NaN or an infinity).
 template <int HP>
@@ -240,8 +246,8 @@ __device__ __forceinline__ float store_query(uint32_t q_base, int h, int lane, c
         lw[k] = byte_perm(a, b, 0x7632);
     }
     const uint32_t slab = q_base + (lane >> 3) * Fp4Layout<HP>::kQSlab;
-    st_shared_v4(slab + sw128_offset(h, lane & 7), hw[0], hw[1], hw[2], hw[3]);
-    st_shared_v4(slab + sw128_offset(HP + h, lane & 7), lw[0], lw[1], lw[2], lw[3]);
+    st_shared_v4(slab + sw128_offset(hi_row<HP>(h), lane & 7), hw[0], hw[1], hw[2], hw[3]);
+    st_shared_v4(slab + sw128_offset(hi_row<HP>(h) + HP / 2, lane & 7), lw[0], lw[1], lw[2], lw[3]);
     return top >= 0x7F800000u ? __uint_as_float(0x7FFFFFFFu) : exp2_int(-e);
 }
 
@@ -251,7 +257,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     fp4_attention_kernel(const __grid_constant__ CUtensorMap tm_codes, const __grid_constant__ CUtensorMap tm_scales,
                          const Fp4Params p) {
     using L = Fp4Layout<HP>;
-    constexpr int N = L::N, kSlabs = L::kSlabs;
+    constexpr int HW = L::HW, N = L::N, kStages = L::kStages, kPBufs = L::kPBufs, kSBufs = L::kSBufs;
     extern __shared__ uint8_t smem_raw[];
     const uint32_t raw = smem_u32(smem_raw), base = (raw + 1023u) & ~1023u;
     Fp4Shared &sh = *reinterpret_cast<Fp4Shared *>(smem_raw + (base - raw) + L::END);
@@ -265,10 +271,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int i = 0; i < kStages; ++i) mbar_init(bar(sh.stage_full[i]), 1), mbar_init(bar(sh.stage_empty[i]), 8);
         for (int i = 0; i < kScaleSlots; ++i) mbar_init(bar(sh.scale_full[i]), 1), mbar_init(bar(sh.scale_empty[i]), 8);
         for (int i = 0; i < kSlabs; ++i) mbar_init(bar(sh.slab_full[i]), 8), mbar_init(bar(sh.slab_free[i]), 1);
-        mbar_init(bar(sh.s_full), 1);
-        mbar_init(bar(sh.s_free), 4);
-        mbar_init(bar(sh.q_ready), 4);
-        for (int i = 0; i < kPBufs; ++i) mbar_init(bar(sh.p_full[i]), 4), mbar_init(bar(sh.p_free[i]), 1);
+        for (int i = 0; i < kSBufs; ++i) mbar_init(bar(sh.s_full[i]), 1), mbar_init(bar(sh.s_free[i]), 8);
+        for (int i = 0; i < kPBufs; ++i) mbar_init(bar(sh.p_full[i]), 8), mbar_init(bar(sh.p_free[i]), 1);
+        mbar_init(bar(sh.q_ready), 8);
         sh.abort = 0;
         fence_mbar_init();
     }
@@ -338,17 +343,19 @@ __global__ void __launch_bounds__(kThreads, 1)
             while (ok && walk.next(seg)) {
                 if (!(ok = mbar_wait(bar(sh.q_ready), ns++ & 1, p.err, abort_flag))) break;
                 for (int u = 0; ok && u < seg.units; ++u, ++un) {
-                    if (un >= 1 && !(ok = mbar_wait(bar(sh.s_free), (un - 1) & 1, p.err, abort_flag))) break;
+                    const uint32_t sb = un % kSBufs;
+                    if (un >= kSBufs && !(ok = mbar_wait(bar(sh.s_free[sb]), (un / kSBufs - 1) & 1, p.err, abort_flag)))
+                        break;
                     for (int k = 0; k < 4; ++k, ++it) {
                         const uint32_t sl = it % kSlabs;
                         if (!(ok = mbar_wait(bar(sh.slab_full[sl]), (it / kSlabs) & 1, p.err, abort_flag))) break;
                         tc_fence_after();
 #pragma unroll
                         for (int kk = 0; kk < 4; ++kk)
-                            umma_f8(tmem + L::S_COL, desc_add(c0, sl * kSlab + kk * 32), desc_add(q0, k * L::kQSlab + kk * 32),
+                            umma_f8(tmem + L::S_COL + sb * N, desc_add(c0, sl * kSlab + kk * 32), desc_add(q0, k * L::kQSlab + kk * 32),
                                     idesc, (k | kk) != 0);
                     }
-                    if (ok) umma_commit(bar(sh.s_full));
+                    if (ok) umma_commit(bar(sh.s_full[sb]));
                 }
             }
             if (!ok) *abort_flag = 1;
@@ -377,67 +384,72 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             if (!ok) *abort_flag = 1;
         }
-    } else if (warp < 8) {
+    } else if (warp < 12) {
         regs_acquire<kRegsSoft>();
-        // ---- softmax: thread = row `t` of the unit (TMEM lane t); a failed wait is agreed on at the barriers
-        const int t = threadIdx.x - 128, quad = warp - 4;
-        const uint32_t lanes = tmem + (static_cast<uint32_t>(quad * 32) << 16);
+        // ---- softmax: thread = row `t` of the unit (TMEM lane t), warpgroup `wg` the heads [HW wg, HW wg + HW); a
+        // failed wait is agreed on at the barriers
+        const int wg = (warp - 4) >> 2, quad = warp & 3, t = quad * 32 + lane, id = 1 + wg;
+        const uint32_t lanes = tmem + (static_cast<uint32_t>(quad * 32) << 16) + wg * 2 * HW;
+        float *const mul = sh.mul + wg * HW, *const thr = sh.thr + wg * HW, *const bias = sh.bias + wg * HW,
+                     *const fac = sh.fac + wg * HW;
+        const int mine = min(HW, heads - wg * HW);   // real heads of this warpgroup (may be <= 0)
         uint32_t un = 0;
         bool fail = false, more = walk.next(seg);
-        float l[HP];
+        float l[HW];
         while (more) {
             // the segment's queries (S of the last unit before this has been read, so the buffer is free)
-            for (int i0 = quad; i0 < HP; i0 += 16) {
-                uint4 v[4][2];
+            for (int i0 = quad; i0 < HW; i0 += 8) {
+                uint4 v[2][2];
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
+                for (int i = 0; i < 2; ++i) {
                     const int h = i0 + 4 * i;
                     const uint4 *src = reinterpret_cast<const uint4 *>(
-                                           p.q_abs + (static_cast<size_t>(seg.seq) * p.H + h0 + min(h, heads - 1)) * kR) +
+                                           p.q_abs + (static_cast<size_t>(seg.seq) * p.H + h0 + (h < mine ? wg * HW + h : 0)) * kR) +
                                        lane * 2;
-                    v[i][0] = h < heads ? __ldg(src) : make_uint4(0, 0, 0, 0);
-                    v[i][1] = h < heads ? __ldg(src + 1) : make_uint4(0, 0, 0, 0);
+                    v[i][0] = h < mine ? __ldg(src) : make_uint4(0, 0, 0, 0);
+                    v[i][1] = h < mine ? __ldg(src + 1) : make_uint4(0, 0, 0, 0);
                 }
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
+                for (int i = 0; i < 2; ++i) {
                     const int h = i0 + 4 * i;
-                    const float undo = store_query<HP>(base + L::Q, h, lane, v[i]);
+                    const float undo = store_query<HP>(base + L::Q, wg * HW + h, lane, v[i]);
                     if (lane == 0) {   // padding heads: P = 0, never a new maximum
-                        sh.mul[h] = h < heads ? undo * p.scale_log2 : 0.f;
-                        sh.thr[h] = h < heads ? -INFINITY : INFINITY;
-                        sh.bias[h] = h < heads ? kBias : -INFINITY;
+                        mul[h] = h < mine ? undo * p.scale_log2 : 0.f;
+                        thr[h] = h < mine ? -INFINITY : INFINITY;
+                        bias[h] = h < mine ? kBias : -INFINITY;
                     }
                 }
             }
             fence_proxy_async_smem();
-            named_bar_sync(1, 128);
+            named_bar_sync(id, 128);
             if (lane == 0) mbar_arrive(bar(sh.q_ready));
 #pragma unroll
-            for (int h = 0; h < HP; ++h) l[h] = 0.f;
+            for (int h = 0; h < HW; ++h) l[h] = 0.f;
 
             for (int u = 0; u < seg.units; ++u, ++un) {
-                float a[HP];
-                fail |= !mbar_wait(bar(sh.s_full), un & 1, p.err, abort_flag);
+                const uint32_t sb = un % kSBufs, pb = un % kPBufs;
+                float a[HW];
+                fail |= !mbar_wait(bar(sh.s_full[sb]), (un / kSBufs) & 1, p.err, abort_flag);
                 __syncwarp();
-                const float ref = sh.ref[un & 1][t], row_scale = exp2_int(static_cast<int>(ref));
                 tc_fence_after();
+                const float ref = sh.ref[un & 1][t], row_scale = exp2_int(static_cast<int>(ref));
 #pragma unroll
-                for (int g = 0; g < HP / 16; ++g) {
-                    float hi[16], lo[16];
-                    tmem_ld16(lanes + L::S_COL + g * 16, hi);
-                    tmem_ld16(lanes + L::S_COL + HP + g * 16, lo);
+                for (int g = 0; g < HW; g += 8) {
+                    float hi[8], lo[8];
+                    tmem_ld8(lanes + L::S_COL + sb * N + g, hi);
+                    tmem_ld8(lanes + L::S_COL + sb * N + HW + g, lo);
                     tmem_wait_ld();
 #pragma unroll
-                    for (int k = 0; k < 16; ++k) a[g * 16 + k] = fmaf(lo[k], kLoPart, hi[k]) * row_scale;
+                    for (int k = 0; k < 8; ++k) a[g + k] = fmaf(lo[k], kLoPart, hi[k]) * row_scale;
                 }
                 tc_fence_before();
                 __syncwarp();
-                if (lane == 0) mbar_arrive(bar(sh.s_free));
+                if (lane == 0) mbar_arrive(bar(sh.s_free[sb]));
                 const bool valid = t < seg.len - seg.row0 - u * kRows;
                 bool past = fail;
 #pragma unroll
-                for (int h = 0; h < HP; h += 4) {
-                    const float4 m = lds4(sh.mul + h), th = lds4(sh.thr + h);
+                for (int h = 0; h < HW; h += 4) {
+                    const float4 m = lds4(mul + h), th = lds4(thr + h);
                     const float mm[4] = {m.x, m.y, m.z, m.w}, tt[4] = {th.x, th.y, th.z, th.w};
 #pragma unroll
                     for (int k = 0; k < 4; ++k) {
@@ -445,131 +457,123 @@ __global__ void __launch_bounds__(kThreads, 1)
                         past |= a[h + k] > tt[k];
                     }
                 }
-                if (named_bar_or(1, 128, past)) {
-                    if (named_bar_or(1, 128, fail)) break;
-                    // maxima over the 128 rows
-                    int top0 = INT_MIN, top1 = INT_MIN;   // lane j: heads j and 32 + j
+                if (named_bar_or(id, 128, past)) {
+                    if (named_bar_or(id, 128, fail)) break;
+                    // maxima over the rows, of the heads that some row of this warp pushes past their threshold
+                    uint32_t heads_past = 0;
 #pragma unroll
-                    for (int h = 0; h < HP; ++h) {
-                        const int x = __reduce_max_sync(0xffffffffu, a[h] == a[h] ? ordered(a[h]) : INT_MIN);
-                        if (lane == (h & 31)) (h < 32 ? top0 : top1) = x;
-                    }
-                    if (lane < HP) sh.red[quad][lane] = __int_as_float(top0);
-                    if (HP > 32 && lane < HP - 32) sh.red[quad][32 + lane] = __int_as_float(top1);
-                    if (t == 0) sh.flagged = 0;
-                    named_bar_sync(1, 128);
-                    if (t < HP) {
-                        int x = INT_MIN;
+                    for (int h = 0; h < HW; ++h) heads_past |= a[h] > thr[h] ? 1u << h : 0u;
+                    heads_past = __reduce_or_sync(0xffffffffu, heads_past);
+                    int top = INT_MIN;   // lane h: head h
 #pragma unroll
-                        for (int q = 0; q < 4; ++q) x = max(x, __float_as_int(sh.red[q][t]));
-                        const float top = x == INT_MIN ? -INFINITY : from_ordered(x);
-                        float f = 1.f;
-                        if (top > sh.thr[t]) {
-                            f = fast_exp2((kBias - sh.bias[t]) - top);   // 2^(M_old - M_new); the first time l is 0
-                            sh.thr[t] = top + kSlack;
-                            sh.bias[t] = kBias - top;
-                            atomicOr(&sh.flagged, 1u << (t >> 4));
+                    for (int h = 0; h < HW; ++h)
+                        if (heads_past >> h & 1) {
+                            const int x = __reduce_max_sync(0xffffffffu, a[h] == a[h] ? ordered(a[h]) : INT_MIN);
+                            if (lane == h) top = x;
                         }
-                        sh.fac[t] = f;
+                    if (lane < HW) sh.red[quad][wg * HW + lane] = __int_as_float(top);
+                    named_bar_sync(id, 128);
+                    if (quad == 0) {
+                        if (lane < HW) {
+#pragma unroll
+                            for (int q = 1; q < 4; ++q) top = max(top, __float_as_int(sh.red[q][wg * HW + lane]));
+                        }
+                        if (top != INT_MIN) {
+                            const float m = from_ordered(top) + kHead;
+                            fac[lane] = fast_exp2((kBias - bias[lane]) - m);   // 2^(M_old - M_new); the first time l is 0
+                            thr[lane] = m + kSlack;
+                            bias[lane] = kBias - m;
+                        }
+                        const uint32_t moved = __ballot_sync(0xffffffffu, top != INT_MIN);
+                        if (lane == 0) sh.moved[wg] = moved;
                     }
-                    named_bar_sync(1, 128);
+                    named_bar_sync(id, 128);
                     if (u > 0) {
-                        const uint32_t flagged = sh.flagged;
+                        uint32_t moved = sh.moved[wg];
 #pragma unroll
-                        for (int h = 0; h < HP; h += 4) {
-                            const float4 f = lds4(sh.fac + h);
-                            l[h] *= f.x, l[h + 1] *= f.y, l[h + 2] *= f.z, l[h + 3] *= f.w;
-                        }
+                        for (int h = 0; h < HW; ++h)
+                            if (moved >> h & 1) l[h] *= fac[h];
                         // the products of the unit before are complete before O^T is scaled
                         fail |= !mbar_wait(bar(sh.p_free[(un - 1) % kPBufs]), ((un - 1) / kPBufs) & 1, p.err, abort_flag);
                         __syncwarp();
                         tc_fence_after();
-#pragma unroll 1
-                        for (int g = 0; g < HP / 16; ++g) {
-                            if (!(flagged >> g & 1)) continue;
-#pragma unroll 1
-                            for (int c = 0; c < 8; ++c) {   // latent tile c >> 1, hi or lo columns
-                                float o[16];
-                                const uint32_t at = lanes + L::O_COL + (c >> 1) * N + (c & 1) * HP + g * 16;
-                                tmem_ld16(at, o);
-                                tmem_wait_ld();
+                        for (; moved; moved &= moved - 1) {
+                            const int h = __ffs(moved) - 1;
+                            const float f = fac[h];
+                            float o[8];   // hi and lo columns of the four latent tiles
 #pragma unroll
-                                for (int k = 0; k < 16; k += 4) {
-                                    const float4 f = lds4(sh.fac + g * 16 + k);
-                                    o[k] *= f.x, o[k + 1] *= f.y, o[k + 2] *= f.z, o[k + 3] *= f.w;
-                                }
-                                tmem_st16(at, o);
-                            }
+                            for (int c = 0; c < 8; ++c) tmem_ld1(lanes + L::O_COL + (c >> 1) * N + (c & 1) * HW + h, o[c]);
+                            tmem_wait_ld();
+#pragma unroll
+                            for (int c = 0; c < 8; ++c)
+                                tmem_st1(lanes + L::O_COL + (c >> 1) * N + (c & 1) * HW + h, o[c] * f);
                         }
                         tmem_wait_st();
                         tc_fence_before();
                     }
                 }
-                // weights, their sums, and P^T as the MN-major N side: row t, hi bytes then lo bytes of all heads
-                const uint32_t pb = un % kPBufs;
-                if (un >= kPBufs) fail |= !mbar_wait(bar(sh.p_free[pb]), (un / kPBufs - 1) & 1, p.err, abort_flag);
+                // weights, their sums, and P^T as the MN-major N side: row t, 2 HW bytes of this warpgroup
                 const float unref = exp2_int(-static_cast<int>(ref));
+                uint32_t w[HW / 2];   // HW / 4 words of hi bytes, then of lo bytes
+#pragma unroll
+                for (int h = 0; h < HW; h += 4) {
+                    const float4 bi = lds4(bias + h);
+                    const float x0 = fast_exp2(a[h] + bi.x), x1 = fast_exp2(a[h + 1] + bi.y);
+                    const float x2 = fast_exp2(a[h + 2] + bi.z), x3 = fast_exp2(a[h + 3] + bi.w);
+                    l[h] = fmaf(x0, unref, l[h]), l[h + 1] = fmaf(x1, unref, l[h + 1]);
+                    l[h + 2] = fmaf(x2, unref, l[h + 2]), l[h + 3] = fmaf(x3, unref, l[h + 3]);
+                    const uint32_t x = split16_e4m3x2(x0, x1), y = split16_e4m3x2(x2, x3);
+                    w[h / 4] = byte_perm(x, y, 0x5410);
+                    w[HW / 4 + h / 4] = byte_perm(x, y, 0x7632);
+                }
+                if (un >= kPBufs) fail |= !mbar_wait(bar(sh.p_free[pb]), (un / kPBufs - 1) & 1, p.err, abort_flag);
                 const uint32_t prow = base + L::P + pb * kSlab;
 #pragma unroll
-                for (int g = 0; g < HP / 16; ++g) {
-                    uint32_t hw[4], lw[4];
-#pragma unroll
-                    for (int k = 0; k < 4; ++k) {
-                        const int h = g * 16 + 4 * k;
-                        const float4 bi = lds4(sh.bias + h);
-                        const float x0 = fast_exp2(a[h] + bi.x), x1 = fast_exp2(a[h + 1] + bi.y);
-                        const float x2 = fast_exp2(a[h + 2] + bi.z), x3 = fast_exp2(a[h + 3] + bi.w);
-                        l[h] = fmaf(x0, unref, l[h]), l[h + 1] = fmaf(x1, unref, l[h + 1]);
-                        l[h + 2] = fmaf(x2, unref, l[h + 2]), l[h + 3] = fmaf(x3, unref, l[h + 3]);
-                        const uint32_t x = split16_e4m3x2(x0, x1), y = split16_e4m3x2(x2, x3);
-                        hw[k] = byte_perm(x, y, 0x5410);
-                        lw[k] = byte_perm(x, y, 0x7632);
-                    }
-                    st_shared_v4(prow + sw128_offset(t, g), hw[0], hw[1], hw[2], hw[3]);
-                    st_shared_v4(prow + sw128_offset(t, HP / 16 + g), lw[0], lw[1], lw[2], lw[3]);
-                }
+                for (int i = 0; i < HW / 8; ++i)
+                    st_shared_v4(prow + sw128_offset(t, wg * (HW / 8) + i), w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
                 fence_proxy_async_smem();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(bar(sh.p_full[pb]));
             }
             // ---- drain: l over the 128 rows, then O^T (lane = latent column of its tile)
 #pragma unroll
-            for (int h = 0; h < HP; ++h) {
+            for (int h = 0; h < HW; ++h) {
                 float s = l[h];
 #pragma unroll
                 for (int o = 16; o >= 1; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
-                if (lane == (h & 31)) sh.red[quad][h] = s;
+                if (lane == h) sh.red[quad][wg * HW + h] = s;
             }
             const uint32_t last = un - 1;
             fail |= !mbar_wait(bar(sh.p_free[last % kPBufs]), (last / kPBufs) & 1, p.err, abort_flag);
-            if (named_bar_or(1, 128, fail)) break;
+            if (named_bar_or(id, 128, fail)) break;
             tc_fence_after();
-            const size_t slot = static_cast<size_t>(seg.slot) * p.H + h0;
-            if (t < heads) {
-                p.ws_m[slot + t] = -sh.bias[t];
-                p.ws_l[slot + t] = (sh.red[0][t] + sh.red[1][t]) + (sh.red[2][t] + sh.red[3][t]);
+            const size_t slot = static_cast<size_t>(seg.slot) * p.H + h0 + wg * HW;
+            if (t < mine) {
+                const int h = wg * HW + t;
+                p.ws_m[slot + t] = -bias[t];
+                p.ws_l[slot + t] = (sh.red[0][h] + sh.red[1][h]) + (sh.red[2][h] + sh.red[3][h]);
             }
 #pragma unroll 1
-            for (int c = 0; c < 4 * (HP / 16); ++c) {
-                const int tile = c / (HP / 16), g = c % (HP / 16);
-                float hi[16], lo[16];
-                tmem_ld16(lanes + L::O_COL + tile * N + g * 16, hi);
-                tmem_ld16(lanes + L::O_COL + tile * N + HP + g * 16, lo);
+            for (int c = 0; c < 4 * (HW / 8); ++c) {
+                const int tile = c / (HW / 8), g = c % (HW / 8) * 8;
+                float hi[8], lo[8];
+                tmem_ld8(lanes + L::O_COL + tile * N + g, hi);
+                tmem_ld8(lanes + L::O_COL + tile * N + HW + g, lo);
                 tmem_wait_ld();
-                float *dst = p.ws_o + (slot + g * 16) * kR + tile * 128 + t;
+                float *dst = p.ws_o + (slot + g) * kR + tile * 128 + t;
 #pragma unroll
-                for (int k = 0; k < 16; ++k)
-                    if (g * 16 + k < heads) dst[static_cast<size_t>(k) * kR] = fmaf(lo[k], kLoPart, hi[k]);
+                for (int k = 0; k < 8; ++k)
+                    if (g + k < mine) dst[static_cast<size_t>(k) * kR] = fmaf(lo[k], kLoPart, hi[k]);
             }
             tc_fence_before();
-            named_bar_sync(1, 128);   // red, thr and bias are read before the next segment sets them
+            named_bar_sync(id, 128);   // red, thr and bias are read before the next segment sets them
             more = walk.next(seg);
         }
         if (fail) *abort_flag = 1;
     } else {
         regs_release<kRegsExp>();
         // ---- expansion: 32 codes (a group) per thread and step, two steps per slab
-        const int tid = threadIdx.x - 256;
+        const int tid = threadIdx.x - 384;
         uint32_t it = 0, un = 0;
         bool fail = false, stop = false;
         while (!stop && walk.next(seg)) {
@@ -593,7 +597,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     top = min(top, static_cast<uint32_t>(kFp4ScaleMax));
                     sh.ref[un & 1][tid] = static_cast<float>(static_cast<int>(top) - 127 - 6);
                 }
-                if (named_bar_or(2, 256, fail)) {
+                if (named_bar_or(3, 256, fail)) {
                     stop = true;
                     break;
                 }
