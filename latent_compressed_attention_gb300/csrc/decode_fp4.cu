@@ -84,12 +84,14 @@ struct Fp4Shared {
     uint64_t p_full[2], p_free[2];
     uint32_t tmem_base;
     int abort;
-    uint32_t moved[2];                     // per warpgroup: heads whose maximum moved
+    uint32_t pad_[2];
     uint2 table[kTables];
-    alignas(16) float ref[2][kRows];
-    // per head: score factor, M + slack, kBias - M, 2^(M_old - M_new)
-    alignas(16) float mul[48], thr[48], bias[48], fac[48];
-    float red[4][48];                      // per warp of a warpgroup and head
+    int16_t ref[2][kRows];                 // per row of the last two units: the power of two its tile is divided by
+    alignas(16) float mul[48];             // per head: score factor
+    // per softmax warp and head: M + slack, kBias - M and the last 2^(M_old - M_new), the same in a warpgroup's four
+    // (and the warps' parts of l while a segment is drained)
+    alignas(16) float thr[8][24], bias[8][24], fac[8][24];
+    int top[2][48];                        // per head: the largest score past its threshold, by turns
 };
 static_assert(sizeof(Fp4Shared) <= 4096, "shared block too large");
 
@@ -207,9 +209,12 @@ __device__ __forceinline__ uint32_t byte_perm(uint32_t a, uint32_t b, uint32_t s
     asm("prmt.b32 %0, %1, %2, %3;" : "=r"(r) : "r"(a), "r"(b), "r"(sel));
     return r;
 }
-// Four codes (the low 16 bits of w) as e4m3 bytes by the group's table of magnitudes.
-__device__ __forceinline__ uint32_t expand4(uint32_t w, uint2 table) {
-    return byte_perm(table.x, table.y, w & 0x7777u) | byte_perm(0u, 0x80808080u, (w >> 1) & 0x4444u);
+// Eight codes as e4m3 bytes by the group's table of magnitudes: three bits of each code select one of its bytes, the
+// fourth the sign.
+__device__ __forceinline__ void expand8(uint32_t w, uint2 table, uint32_t &o0, uint32_t &o1) {
+    const uint32_t m = w & 0x77777777u, s = (w >> 1) & 0x44444444u;
+    o0 = byte_perm(table.x, table.y, m) | byte_perm(0u, 0x80808080u, s);
+    o1 = byte_perm(table.x, table.y, m >> 16) | byte_perm(0u, 0x80808080u, s >> 16);
 }
 // Floats as integers of the same order (NaN aside).
 __device__ __forceinline__ int ordered(float x) {
@@ -277,6 +282,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         sh.abort = 0;
         fence_mbar_init();
     }
+    if (threadIdx.x >= 128 && threadIdx.x < 128 + 96) sh.top[0][threadIdx.x - 128] = INT_MIN;
     if (threadIdx.x >= 64 && threadIdx.x < 64 + kTables) {   // magnitudes times 2^k as e4m3 bytes
         const int i = threadIdx.x - 64;
         const float f = i == kTables - 1 ? __uint_as_float(0x7FFFFFFFu) : (i == 0 ? 0.f : exp2_int(i - 14));
@@ -386,15 +392,15 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
     } else if (warp < 12) {
         regs_acquire<kRegsSoft>();
-        // ---- softmax: thread = row `t` of the unit (TMEM lane t), warpgroup `wg` the heads [HW wg, HW wg + HW); a
-        // failed wait is agreed on at the barriers
+        // ---- softmax: thread = row `t` of the unit (TMEM lane t), warpgroup `wg` the heads [HW wg, HW wg + HW).  After a
+        // failed wait every warp runs its loops to their end, without waiting
         const int wg = (warp - 4) >> 2, quad = warp & 3, t = quad * 32 + lane, id = 1 + wg;
         const uint32_t lanes = tmem + (static_cast<uint32_t>(quad * 32) << 16) + wg * 2 * HW;
-        float *const mul = sh.mul + wg * HW, *const thr = sh.thr + wg * HW, *const bias = sh.bias + wg * HW,
-                     *const fac = sh.fac + wg * HW;
+        float *const mul = sh.mul + wg * HW, *const thr = sh.thr[warp - 4], *const bias = sh.bias[warp - 4],
+                     *const fac = sh.fac[warp - 4];
         const int mine = min(HW, heads - wg * HW);   // real heads of this warpgroup (may be <= 0)
-        uint32_t un = 0;
-        bool fail = false, more = walk.next(seg);
+        uint32_t un = 0, turn = 0;
+        bool ok = true, more = walk.next(seg);
         float l[HW];
         while (more) {
             // the segment's queries (S of the last unit before this has been read, so the buffer is free)
@@ -413,12 +419,12 @@ __global__ void __launch_bounds__(kThreads, 1)
                 for (int i = 0; i < 2; ++i) {
                     const int h = i0 + 4 * i;
                     const float undo = store_query<HP>(base + L::Q, wg * HW + h, lane, v[i]);
-                    if (lane == 0) {   // padding heads: P = 0, never a new maximum
-                        mul[h] = h < mine ? undo * p.scale_log2 : 0.f;
-                        thr[h] = h < mine ? -INFINITY : INFINITY;
-                        bias[h] = h < mine ? kBias : -INFINITY;
-                    }
+                    if (lane == 0) mul[h] = h < mine ? undo * p.scale_log2 : 0.f;
                 }
+            }
+            if (lane < HW) {   // padding heads: P = 0, never a new maximum
+                thr[lane] = lane < mine ? -INFINITY : INFINITY;
+                bias[lane] = lane < mine ? kBias : -INFINITY;
             }
             fence_proxy_async_smem();
             named_bar_sync(id, 128);
@@ -428,92 +434,91 @@ __global__ void __launch_bounds__(kThreads, 1)
 
             for (int u = 0; u < seg.units; ++u, ++un) {
                 const uint32_t sb = un % kSBufs, pb = un % kPBufs;
-                float a[HW];
-                fail |= !mbar_wait(bar(sh.s_full[sb]), (un / kSBufs) & 1, p.err, abort_flag);
+                float a[HW], lo[HW];
+                ok &= mbar_wait(bar(sh.s_full[sb]), (un / kSBufs) & 1, p.err, abort_flag);
                 __syncwarp();
                 tc_fence_after();
-                const float ref = sh.ref[un & 1][t], row_scale = exp2_int(static_cast<int>(ref));
 #pragma unroll
                 for (int g = 0; g < HW; g += 8) {
-                    float hi[8], lo[8];
-                    tmem_ld8(lanes + L::S_COL + sb * N + g, hi);
-                    tmem_ld8(lanes + L::S_COL + sb * N + HW + g, lo);
-                    tmem_wait_ld();
-#pragma unroll
-                    for (int k = 0; k < 8; ++k) a[g + k] = fmaf(lo[k], kLoPart, hi[k]) * row_scale;
+                    tmem_ld8(lanes + L::S_COL + sb * N + g, *reinterpret_cast<float (*)[8]>(a + g));
+                    tmem_ld8(lanes + L::S_COL + sb * N + HW + g, *reinterpret_cast<float (*)[8]>(lo + g));
                 }
-                tc_fence_before();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(bar(sh.s_free[sb]));
+                const int ref = sh.ref[un & 1][t];
+                const float row_scale = exp2_int(ref), row_exp = static_cast<float>(ref);
+                tmem_wait_ld();
                 const bool valid = t < seg.len - seg.row0 - u * kRows;
-                bool past = fail;
+                uint32_t past = 0;
 #pragma unroll
                 for (int h = 0; h < HW; h += 4) {
                     const float4 m = lds4(mul + h), th = lds4(thr + h);
                     const float mm[4] = {m.x, m.y, m.z, m.w}, tt[4] = {th.x, th.y, th.z, th.w};
 #pragma unroll
                     for (int k = 0; k < 4; ++k) {
-                        a[h + k] = valid ? fmaf(a[h + k], mm[k], ref) : -INFINITY;
-                        past |= a[h + k] > tt[k];
+                        const float s = fmaf(lo[h + k], kLoPart, a[h + k]) * row_scale;
+                        a[h + k] = valid ? fmaf(s, mm[k], row_exp) : -INFINITY;
+                        if (a[h + k] > tt[k]) past |= 1u << (h + k);
                     }
                 }
-                if (named_bar_or(id, 128, past)) {
-                    if (named_bar_or(id, 128, fail)) break;
-                    // maxima over the rows, of the heads that some row of this warp pushes past their threshold
-                    uint32_t heads_past = 0;
-#pragma unroll
-                    for (int h = 0; h < HW; ++h) heads_past |= a[h] > thr[h] ? 1u << h : 0u;
-                    heads_past = __reduce_or_sync(0xffffffffu, heads_past);
-                    int top = INT_MIN;   // lane h: head h
-#pragma unroll
-                    for (int h = 0; h < HW; ++h)
-                        if (heads_past >> h & 1) {
-                            const int x = __reduce_max_sync(0xffffffffu, a[h] == a[h] ? ordered(a[h]) : INT_MIN);
-                            if (lane == h) top = x;
-                        }
-                    if (lane < HW) sh.red[quad][wg * HW + lane] = __int_as_float(top);
-                    named_bar_sync(id, 128);
-                    if (quad == 0) {
-                        if (lane < HW) {
-#pragma unroll
-                            for (int q = 1; q < 4; ++q) top = max(top, __float_as_int(sh.red[q][wg * HW + lane]));
-                        }
-                        if (top != INT_MIN) {
-                            const float m = from_ordered(top) + kHead;
-                            fac[lane] = fast_exp2((kBias - bias[lane]) - m);   // 2^(M_old - M_new); the first time l is 0
-                            thr[lane] = m + kSlack;
-                            bias[lane] = kBias - m;
-                        }
-                        const uint32_t moved = __ballot_sync(0xffffffffu, top != INT_MIN);
-                        if (lane == 0) sh.moved[wg] = moved;
+                if (named_bar_or(id, 128, past != 0)) {
+                    // maxima over the rows, of the heads that some row of this warp pushes past their threshold (read
+                    // again from S: a loop over these heads alone keeps the code small)
+                    past = __reduce_or_sync(0xffffffffu, past);
+                    int *const top = sh.top[turn & 1] + wg * HW, *const other = sh.top[~turn & 1] + wg * HW;
+                    ++turn;
+                    for (; past; past &= past - 1) {
+                        const int h = __ffs(past) - 1;
+                        float s_hi, s_lo;
+                        tmem_ld1(lanes + L::S_COL + sb * N + h, s_hi);
+                        tmem_ld1(lanes + L::S_COL + sb * N + HW + h, s_lo);
+                        tmem_wait_ld();
+                        const float v = fmaf(fmaf(s_lo, kLoPart, s_hi) * row_scale, mul[h], row_exp);
+                        const int x = __reduce_max_sync(0xffffffffu, valid && v == v ? ordered(v) : INT_MIN);
+                        if (lane == 0) atomicMax(top + h, x);
                     }
                     named_bar_sync(id, 128);
+                    const int x = lane < HW ? top[lane] : INT_MIN;
+                    // the other turn's maxima were read before this turn's barriers
+                    if (quad == 0 && lane < HW) other[lane] = INT_MIN;
+                    float f = 1.f;
+                    if (x != INT_MIN) {
+                        const float m = from_ordered(x) + kHead;
+                        f = fast_exp2((kBias - bias[lane]) - m);   // 2^(M_old - M_new); the first time l is 0
+                        thr[lane] = m + kSlack;
+                        bias[lane] = kBias - m;
+                    }
+                    if (lane < HW) fac[lane] = f;
+                    uint32_t moved = __ballot_sync(0xffffffffu, x != INT_MIN);
+                    __syncwarp();
                     if (u > 0) {
-                        uint32_t moved = sh.moved[wg];
 #pragma unroll
-                        for (int h = 0; h < HW; ++h)
-                            if (moved >> h & 1) l[h] *= fac[h];
+                        for (int h = 0; h < HW; h += 4) {
+                            const float4 g = lds4(fac + h);
+                            l[h] *= g.x, l[h + 1] *= g.y, l[h + 2] *= g.z, l[h + 3] *= g.w;
+                        }
                         // the products of the unit before are complete before O^T is scaled
-                        fail |= !mbar_wait(bar(sh.p_free[(un - 1) % kPBufs]), ((un - 1) / kPBufs) & 1, p.err, abort_flag);
+                        ok &= mbar_wait(bar(sh.p_free[(un - 1) % kPBufs]), ((un - 1) / kPBufs) & 1, p.err, abort_flag);
                         __syncwarp();
                         tc_fence_after();
                         for (; moved; moved &= moved - 1) {
                             const int h = __ffs(moved) - 1;
-                            const float f = fac[h];
+                            const float g = fac[h];
                             float o[8];   // hi and lo columns of the four latent tiles
 #pragma unroll
                             for (int c = 0; c < 8; ++c) tmem_ld1(lanes + L::O_COL + (c >> 1) * N + (c & 1) * HW + h, o[c]);
                             tmem_wait_ld();
 #pragma unroll
                             for (int c = 0; c < 8; ++c)
-                                tmem_st1(lanes + L::O_COL + (c >> 1) * N + (c & 1) * HW + h, o[c] * f);
+                                tmem_st1(lanes + L::O_COL + (c >> 1) * N + (c & 1) * HW + h, o[c] * g);
                         }
                         tmem_wait_st();
                         tc_fence_before();
                     }
                 }
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(bar(sh.s_free[sb]));
                 // weights, their sums, and P^T as the MN-major N side: row t, 2 HW bytes of this warpgroup
-                const float unref = exp2_int(-static_cast<int>(ref));
+                const float unref = exp2_int(-ref);
                 uint32_t w[HW / 2];   // HW / 4 words of hi bytes, then of lo bytes
 #pragma unroll
                 for (int h = 0; h < HW; h += 4) {
@@ -526,7 +531,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     w[h / 4] = byte_perm(x, y, 0x5410);
                     w[HW / 4 + h / 4] = byte_perm(x, y, 0x7632);
                 }
-                if (un >= kPBufs) fail |= !mbar_wait(bar(sh.p_free[pb]), (un / kPBufs - 1) & 1, p.err, abort_flag);
+                if (un >= kPBufs) ok &= mbar_wait(bar(sh.p_free[pb]), (un / kPBufs - 1) & 1, p.err, abort_flag);
                 const uint32_t prow = base + L::P + pb * kSlab;
 #pragma unroll
                 for (int i = 0; i < HW / 8; ++i)
@@ -541,103 +546,105 @@ __global__ void __launch_bounds__(kThreads, 1)
                 float s = l[h];
 #pragma unroll
                 for (int o = 16; o >= 1; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
-                if (lane == h) sh.red[quad][wg * HW + h] = s;
+                if (lane == h) fac[h] = s;
             }
             const uint32_t last = un - 1;
-            fail |= !mbar_wait(bar(sh.p_free[last % kPBufs]), (last / kPBufs) & 1, p.err, abort_flag);
-            if (named_bar_or(id, 128, fail)) break;
+            ok &= mbar_wait(bar(sh.p_free[last % kPBufs]), (last / kPBufs) & 1, p.err, abort_flag);
+            named_bar_sync(id, 128);
             tc_fence_after();
             const size_t slot = static_cast<size_t>(seg.slot) * p.H + h0 + wg * HW;
-            if (t < mine) {
-                const int h = wg * HW + t;
+            if (t < mine) {   // (mine <= 24: the warpgroup's first warp)
+                const float(*part)[24] = sh.fac + 4 * wg;
                 p.ws_m[slot + t] = -bias[t];
-                p.ws_l[slot + t] = (sh.red[0][h] + sh.red[1][h]) + (sh.red[2][h] + sh.red[3][h]);
+                p.ws_l[slot + t] = (part[0][t] + part[1][t]) + (part[2][t] + part[3][t]);
             }
 #pragma unroll 1
             for (int c = 0; c < 4 * (HW / 8); ++c) {
                 const int tile = c / (HW / 8), g = c % (HW / 8) * 8;
-                float hi[8], lo[8];
+                float hi[8], lw[8];
                 tmem_ld8(lanes + L::O_COL + tile * N + g, hi);
-                tmem_ld8(lanes + L::O_COL + tile * N + HW + g, lo);
+                tmem_ld8(lanes + L::O_COL + tile * N + HW + g, lw);
                 tmem_wait_ld();
                 float *dst = p.ws_o + (slot + g) * kR + tile * 128 + t;
 #pragma unroll
                 for (int k = 0; k < 8; ++k)
-                    if (g + k < mine) dst[static_cast<size_t>(k) * kR] = fmaf(lo[k], kLoPart, hi[k]);
+                    if (g + k < mine) dst[static_cast<size_t>(k) * kR] = fmaf(lw[k], kLoPart, hi[k]);
             }
             tc_fence_before();
-            named_bar_sync(id, 128);   // red, thr and bias are read before the next segment sets them
+            named_bar_sync(id, 128);   // fac and mul are read before the next segment sets them
             more = walk.next(seg);
         }
-        if (fail) *abort_flag = 1;
+        if (!ok) *abort_flag = 1;
     } else {
         regs_release<kRegsExp>();
-        // ---- expansion: 32 codes (a group) per thread and step, two steps per slab
-        const int tid = threadIdx.x - 384;
+        // ---- expansion: a warp takes 16 of a unit's rows, a lane group `g` (32 codes) of every slab in rows r and r + 8
+        const int r = (warp - 12) * 16 + (lane >> 2), g = lane & 3;
+        const uint8_t *const smem = smem_raw + (base - raw);
         uint32_t it = 0, un = 0;
-        bool fail = false, stop = false;
-        while (!stop && walk.next(seg)) {
+        bool ok = true;
+        while (walk.next(seg)) {
             for (int u = 0; u < seg.units; ++u, ++un) {
-                const int rows = min(kRows, seg.len - seg.row0 - u * kRows);
-                const uint32_t sc = un % kScaleSlots, tile = base + L::SCALE + sc * kScaleTile;
-                fail |= !mbar_wait(bar(sh.scale_full[sc]), (un / kScaleSlots) & 1, p.err, abort_flag);
-                // the unit's first slab is free once the products two units back are issued and done, so the softmax
-                // has read what the ref slot held
-                if (it >= kSlabs)
-                    fail |= !mbar_wait(bar(sh.slab_free[it % kSlabs]), (it / kSlabs - 1) & 1, p.err, abort_flag);
-                if (tid < kRows) {   // the row's largest scale exponent (NaN bytes aside) becomes e4m3's 2^6
-                    const uint4 v = ld_shared_v4(tile + tid * 16);
-                    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-                    uint32_t top = kFp4ScaleMin;
+                const int rows = seg.len - seg.row0 - u * kRows;
+                const uint32_t sc = un % kScaleSlots;
+                const uint8_t *const tile = smem + L::SCALE + sc * kScaleTile + r * 16 + g;
+                ok &= mbar_wait(bar(sh.scale_full[sc]), (un / kScaleSlots) & 1, p.err, abort_flag);
+                // the rows' largest scale exponent (NaN bytes aside) becomes e4m3's 2^6; `pick`: tables of the 4 slabs
+                int X[2][4], top[2];
+                uint32_t pick[2];
 #pragma unroll
-                    for (int k = 0; k < 16; ++k) {
-                        const uint32_t X = w[k >> 2] >> (8 * (k & 3)) & 0xFFu;
-                        if (X != kFp4ScaleNan) top = max(top, X);
+                for (int i = 0; i < 2; ++i) {
+                    top[i] = kFp4ScaleMin;
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) {
+                        X[i][k] = tile[i * 128 + k * 4];
+                        if (X[i][k] != kFp4ScaleNan) top[i] = max(top[i], X[i][k]);
                     }
-                    top = min(top, static_cast<uint32_t>(kFp4ScaleMax));
-                    sh.ref[un & 1][tid] = static_cast<float>(static_cast<int>(top) - 127 - 6);
+                    top[i] = max(top[i], __shfl_xor_sync(0xffffffffu, top[i], 1));
+                    top[i] = min(max(top[i], __shfl_xor_sync(0xffffffffu, top[i], 2)), kFp4ScaleMax);
+                    pick[i] = 0;
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) {
+                        const int in = min(max(X[i][k], kFp4ScaleMin), kFp4ScaleMax);
+                        pick[i] |= static_cast<uint32_t>(X[i][k] == kFp4ScaleNan ? kTables - 1 : max(in - top[i] + 20, 0)) << 8 * k;
+                    }
+                    if (r + 8 * i >= rows) pick[i] = 0;   // rows past the end: zeros
                 }
-                if (named_bar_or(3, 256, fail)) {
-                    stop = true;
-                    break;
-                }
+                __syncwarp();
+                if (lane == 0) mbar_arrive(bar(sh.scale_empty[sc]));
+#pragma unroll 1
                 for (int k = 0; k < 4; ++k, ++it) {
                     const uint32_t st = it % kStages, sl = it % kSlabs;
-                    fail |= !mbar_wait(bar(sh.stage_full[st]), (it / kStages) & 1, p.err, abort_flag);
-                    if (k > 0 && it >= kSlabs)
-                        fail |= !mbar_wait(bar(sh.slab_free[sl]), (it / kSlabs - 1) & 1, p.err, abort_flag);
+                    // (the unit's first slab is free once the products two units back are done, so the softmax has read
+                    // what the ref slot held)
+                    if (it >= kSlabs) ok &= mbar_wait(bar(sh.slab_free[sl]), (it / kSlabs - 1) & 1, p.err, abort_flag);
+                    if (k == 0 && g == 0) {
+                        sh.ref[un & 1][r] = static_cast<int16_t>(top[0] - 127 - 6);
+                        sh.ref[un & 1][r + 8] = static_cast<int16_t>(top[1] - 127 - 6);
+                    }
+                    ok &= mbar_wait(bar(sh.stage_full[st]), (it / kStages) & 1, p.err, abort_flag);
+                    const uint4 *const src = reinterpret_cast<const uint4 *>(smem + L::STAGE + st * kStage) + r * 4 + g;
+                    const uint4 v[2] = {src[0], src[32]};
+                    const uint2 tb[2] = {sh.table[pick[0] >> 8 * k & 0xFFu], sh.table[pick[1] >> 8 * k & 0xFFu]};
+                    const uint32_t slab = base + L::C + sl * kSlab;
 #pragma unroll
-                    for (int half = 0; half < 2; ++half) {
-                        const int row = half * 64 + (tid >> 2), g = tid & 3;
-                        const uint4 v = ld_shared_v4(base + L::STAGE + st * kStage + row * 64 + g * 16);
-                        uint32_t X;
-                        asm volatile("ld.shared.u8 %0, [%1];" : "=r"(X) : "r"(tile + row * 16 + k * 4 + g) : "memory");
-                        const int top = static_cast<int>(sh.ref[un & 1][row]) + 127 + 6;
-                        const int Xc = min(max(static_cast<int>(X), kFp4ScaleMin), kFp4ScaleMax);
-                        uint2 tb = sh.table[X == kFp4ScaleNan ? kTables - 1 : max(Xc - top + 20, 0)];
-                        if (row >= rows) tb = make_uint2(0u, 0u);
-                        const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+                    for (int i = 0; i < 2; ++i) {
+                        const uint32_t w[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
                         uint32_t o[8];
 #pragma unroll
-                        for (int i = 0; i < 4; ++i) {
-                            o[2 * i] = expand4(w[i], tb);
-                            o[2 * i + 1] = expand4(w[i] >> 16, tb);
-                        }
-                        const uint32_t slab = base + L::C + sl * kSlab;
-                        st_shared_v4(slab + sw128_offset(row, 2 * g), o[0], o[1], o[2], o[3]);
-                        st_shared_v4(slab + sw128_offset(row, 2 * g + 1), o[4], o[5], o[6], o[7]);
+                        for (int j = 0; j < 4; ++j) expand8(w[j], tb[i], o[2 * j], o[2 * j + 1]);
+                        st_shared_v4(slab + sw128_offset(r + 8 * i, 2 * g), o[0], o[1], o[2], o[3]);
+                        st_shared_v4(slab + sw128_offset(r + 8 * i, 2 * g + 1), o[4], o[5], o[6], o[7]);
                     }
                     fence_proxy_async_smem();
                     __syncwarp();
                     if (lane == 0) {
                         mbar_arrive(bar(sh.slab_full[sl]));
                         mbar_arrive(bar(sh.stage_empty[st]));
-                        if (k == 3) mbar_arrive(bar(sh.scale_empty[sc]));
                     }
                 }
             }
         }
-        if (fail) *abort_flag = 1;
+        if (!ok) *abort_flag = 1;
     }
 
     __syncwarp();
