@@ -33,8 +33,6 @@
 #include <cuda.h>
 #include <cudaTypedefs.h>
 
-#include <climits>
-
 #include "common.cuh"
 #include "internal.h"
 
@@ -52,13 +50,14 @@ constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kBias = 8.f;               // P = 2^(a - M + kBias)
 constexpr float kHead = 1.f, kSlack = 0.75f;   // a new maximum is set kHead above the row that forced it
 // Register split of the 5 warpgroups x 96 launched: control, 2 x softmax, 2 x expansion.
-constexpr uint32_t kRegsCtl = 64, kRegsSoft = 128, kRegsExp = 80, kRegsLaunch = 96;
+constexpr uint32_t kRegsCtl = 80, kRegsSoft = 120, kRegsExp = 80, kRegsLaunch = 96;
 static_assert(kRegsCtl + 2 * kRegsSoft + 2 * kRegsExp <= 5 * kRegsLaunch, "register split exceeds the launch");
 
 constexpr uint32_t kSlab = 16384;          // [128 rows x 128 latent] e4m3, 128-byte swizzle
 constexpr uint32_t kStage = 8192;          // codes of one slab: [128 rows x 64 bytes]
 constexpr uint32_t kScaleTile = 2048;      // [128 rows x 16 scale bytes]
-constexpr int kScaleSlots = 3, kSlabs = 8;   // expanded tiles in flight: two units
+constexpr int kScaleSlots = 2, kSlabs = 8;   // expanded tiles in flight: two units
+constexpr uint32_t kSharedBytes = 5120;    // Fp4Shared
 constexpr int kTables = 22;                // exponents -14 (all zero) .. 6 below the row's largest, then NaN
 
 // Heads of a CTA are padded to HP and shared by two softmax warpgroups of HW each; a warpgroup's columns of the N side
@@ -70,7 +69,7 @@ struct Fp4Layout {
     static constexpr uint32_t kQSlab = N * 128;                        // [N x 128 latent] e4m3
     static constexpr uint32_t Q = 0, C = Q + 4 * kQSlab, P = C + kSlabs * kSlab, STAGE = P + kPBufs * kSlab,
                               SCALE = STAGE + kStages * kStage, END = SCALE + kScaleSlots * kScaleTile;
-    static constexpr uint32_t kSmem = END + 4096 + 1024;               // + Fp4Shared + alignment slack
+    static constexpr uint32_t kSmem = END + kSharedBytes + 1024;               // + Fp4Shared + alignment slack
     static constexpr uint32_t S_COL = 0, O_COL = 128;                  // TMEM columns
     static_assert(kQSlab % 1024 == 0 && O_COL + 4 * N <= 512 && kSBufs * N <= O_COL && HW % 8 == 0, "layout");
     static_assert(kSmem <= 232448, "attention kernel exceeds shared memory");
@@ -88,12 +87,12 @@ struct Fp4Shared {
     uint2 table[kTables];
     int16_t ref[2][kRows];                 // per row of the last two units: the power of two its tile is divided by
     alignas(16) float mul[48];             // per head: score factor
-    // per softmax warp and head: M + slack, kBias - M and the last 2^(M_old - M_new), the same in a warpgroup's four
-    // (and the warps' parts of l while a segment is drained)
-    alignas(16) float thr[8][24], bias[8][24], fac[8][24];
-    int top[2][48];                        // per head: the largest score past its threshold, by turns
+    // per softmax warp and head, the same in a warpgroup's four: kBias - M, and the last change of it with its power of
+    // two (part: the warps' maxima, and their parts of l while a segment is drained)
+    alignas(16) float bias[8][24], step[8][24], fac[8][24];
+    float part[8][24];
 };
-static_assert(sizeof(Fp4Shared) <= 4096, "shared block too large");
+static_assert(sizeof(Fp4Shared) <= kSharedBytes, "shared block too large");
 
 struct Fp4Params {
     const __nv_bfloat16 *q_abs;
@@ -216,12 +215,38 @@ __device__ __forceinline__ void expand8(uint32_t w, uint2 table, uint32_t &o0, u
     o0 = byte_perm(table.x, table.y, m) | byte_perm(0u, 0x80808080u, s);
     o1 = byte_perm(table.x, table.y, m >> 16) | byte_perm(0u, 0x80808080u, s >> 16);
 }
-// Floats as integers of the same order (NaN aside).
-__device__ __forceinline__ int ordered(float x) {
-    const int i = __float_as_int(x);
-    return i >= 0 ? i : i ^ 0x7FFFFFFF;
+// Two fp32 operations in one instruction (sm_100 family).
+__device__ __forceinline__ unsigned long long bits2(float2 v) {
+    unsigned long long r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(v.x), "f"(v.y));
+    return r;
 }
-__device__ __forceinline__ float from_ordered(int i) { return __int_as_float(i >= 0 ? i : i ^ 0x7FFFFFFF); }
+__device__ __forceinline__ float2 floats2(unsigned long long v) {
+    float2 r;
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(v));
+    return r;
+}
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+    unsigned long long r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(bits2(a)), "l"(bits2(b)), "l"(bits2(c)));
+    return floats2(r);
+}
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
+    unsigned long long r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(bits2(a)), "l"(bits2(b)));
+    return floats2(r);
+}
+__device__ __forceinline__ float2 add2(float2 a, float2 b) {
+    unsigned long long r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(bits2(a)), "l"(bits2(b)));
+    return floats2(r);
+}
+// Maximum over the warp, NaN aside (-infinity when there is nothing else).
+__device__ __forceinline__ float warp_max(float v) {
+    float r;
+    asm volatile("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(r) : "f"(v));
+    return r;
+}
 __device__ __forceinline__ float4 lds4(const float *p) { return *reinterpret_cast<const float4 *>(p); }
 
 // N-side row of head h's hi part (its lo part is HW rows further).
@@ -282,7 +307,6 @@ __global__ void __launch_bounds__(kThreads, 1)
         sh.abort = 0;
         fence_mbar_init();
     }
-    if (threadIdx.x >= 128 && threadIdx.x < 128 + 96) sh.top[0][threadIdx.x - 128] = INT_MIN;
     if (threadIdx.x >= 64 && threadIdx.x < 64 + kTables) {   // magnitudes times 2^k as e4m3 bytes
         const int i = threadIdx.x - 64;
         const float f = i == kTables - 1 ? __uint_as_float(0x7FFFFFFFu) : (i == 0 ? 0.f : exp2_int(i - 14));
@@ -396,10 +420,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         // failed wait every warp runs its loops to their end, without waiting
         const int wg = (warp - 4) >> 2, quad = warp & 3, t = quad * 32 + lane, id = 1 + wg;
         const uint32_t lanes = tmem + (static_cast<uint32_t>(quad * 32) << 16) + wg * 2 * HW;
-        float *const mul = sh.mul + wg * HW, *const thr = sh.thr[warp - 4], *const bias = sh.bias[warp - 4],
-                     *const fac = sh.fac[warp - 4];
+        float *const mul = sh.mul + wg * HW, *const bias = sh.bias[warp - 4], *const step = sh.step[warp - 4],
+                     *const fac = sh.fac[warp - 4], *const part = sh.part[warp - 4];
         const int mine = min(HW, heads - wg * HW);   // real heads of this warpgroup (may be <= 0)
-        uint32_t un = 0, turn = 0;
+        uint32_t un = 0;
         bool ok = true, more = walk.next(seg);
         float l[HW];
         while (more) {
@@ -422,10 +446,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     if (lane == 0) mul[h] = h < mine ? undo * p.scale_log2 : 0.f;
                 }
             }
-            if (lane < HW) {   // padding heads: P = 0, never a new maximum
-                thr[lane] = lane < mine ? -INFINITY : INFINITY;
-                bias[lane] = lane < mine ? kBias : -INFINITY;
-            }
+            if (lane < HW) bias[lane] = lane < mine ? kBias : -INFINITY;   // padding heads: P = 0, never a new maximum
             fence_proxy_async_smem();
             named_bar_sync(id, 128);
             if (lane == 0) mbar_arrive(bar(sh.q_ready));
@@ -434,61 +455,67 @@ __global__ void __launch_bounds__(kThreads, 1)
 
             for (int u = 0; u < seg.units; ++u, ++un) {
                 const uint32_t sb = un % kSBufs, pb = un % kPBufs;
-                float a[HW], lo[HW];
+                float x[HW], lo[HW];
                 ok &= mbar_wait(bar(sh.s_full[sb]), (un / kSBufs) & 1, p.err, abort_flag);
                 __syncwarp();
                 tc_fence_after();
 #pragma unroll
                 for (int g = 0; g < HW; g += 8) {
-                    tmem_ld8(lanes + L::S_COL + sb * N + g, *reinterpret_cast<float (*)[8]>(a + g));
+                    tmem_ld8(lanes + L::S_COL + sb * N + g, *reinterpret_cast<float (*)[8]>(x + g));
                     tmem_ld8(lanes + L::S_COL + sb * N + HW + g, *reinterpret_cast<float (*)[8]>(lo + g));
                 }
                 const int ref = sh.ref[un & 1][t];
-                const float row_scale = exp2_int(ref), row_exp = static_cast<float>(ref);
+                // a row past the end has an all-zero tile row: its exponents are -infinity
+                const float row_scale = exp2_int(ref),
+                            row_exp = t < seg.len - seg.row0 - u * kRows ? static_cast<float>(ref) : -INFINITY;
                 tmem_wait_ld();
-                const bool valid = t < seg.len - seg.row0 - u * kRows;
-                uint32_t past = 0;
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(bar(sh.s_free[sb]));
+                // x = score * log2 e + ref + kBias - M
+                float top = -INFINITY;
 #pragma unroll
                 for (int h = 0; h < HW; h += 4) {
-                    const float4 m = lds4(mul + h), th = lds4(thr + h);
-                    const float mm[4] = {m.x, m.y, m.z, m.w}, tt[4] = {th.x, th.y, th.z, th.w};
+                    const float4 m = lds4(mul + h), bi = lds4(bias + h);
+                    const float2 rs = make_float2(row_scale, row_scale), re = make_float2(row_exp, row_exp),
+                                 part_lo = make_float2(kLoPart, kLoPart);
 #pragma unroll
-                    for (int k = 0; k < 4; ++k) {
-                        const float s = fmaf(lo[h + k], kLoPart, a[h + k]) * row_scale;
-                        a[h + k] = valid ? fmaf(s, mm[k], row_exp) : -INFINITY;
-                        if (a[h + k] > tt[k]) past |= 1u << (h + k);
+                    for (int k = 0; k < 4; k += 2) {
+                        const float2 mk = k ? make_float2(m.z, m.w) : make_float2(m.x, m.y);
+                        const float2 bk = k ? make_float2(bi.z, bi.w) : make_float2(bi.x, bi.y);
+                        const float2 s2 = fma2(make_float2(lo[h + k], lo[h + k + 1]), part_lo, make_float2(x[h + k], x[h + k + 1]));
+                        const float2 v = fma2(s2, mul2(mk, rs), add2(bk, re));
+                        x[h + k] = v.x, x[h + k + 1] = v.y;
+                        top = fmaxf(fmaxf(top, v.x), v.y);
                     }
                 }
-                if (named_bar_or(id, 128, past != 0)) {
-                    // maxima over the rows, of the heads that some row of this warp pushes past their threshold (read
-                    // again from S: a loop over these heads alone keeps the code small)
-                    past = __reduce_or_sync(0xffffffffu, past);
-                    int *const top = sh.top[turn & 1] + wg * HW, *const other = sh.top[~turn & 1] + wg * HW;
-                    ++turn;
-                    for (; past; past &= past - 1) {
-                        const int h = __ffs(past) - 1;
-                        float s_hi, s_lo;
-                        tmem_ld1(lanes + L::S_COL + sb * N + h, s_hi);
-                        tmem_ld1(lanes + L::S_COL + sb * N + HW + h, s_lo);
-                        tmem_wait_ld();
-                        const float v = fmaf(fmaf(s_lo, kLoPart, s_hi) * row_scale, mul[h], row_exp);
-                        const int x = __reduce_max_sync(0xffffffffu, valid && v == v ? ordered(v) : INT_MIN);
-                        if (lane == 0) atomicMax(top + h, x);
+                if (u == 0 || named_bar_or(id, 128, top > kBias + kSlack)) {
+                    // every head's maximum over the rows: lane h gets head h's, first of its warp, then of all four
+                    float most = -INFINITY;
+#pragma unroll
+                    for (int h = 0; h < HW; ++h) {
+                        const float v = warp_max(x[h]);
+                        if (lane == h) most = v;
                     }
+                    if (lane < HW) part[lane] = most;
                     named_bar_sync(id, 128);
-                    const int x = lane < HW ? top[lane] : INT_MIN;
-                    // the other turn's maxima were read before this turn's barriers
-                    if (quad == 0 && lane < HW) other[lane] = INT_MIN;
-                    float f = 1.f;
-                    if (x != INT_MIN) {
-                        const float m = from_ordered(x) + kHead;
-                        f = fast_exp2((kBias - bias[lane]) - m);   // 2^(M_old - M_new); the first time l is 0
-                        thr[lane] = m + kSlack;
-                        bias[lane] = kBias - m;
+                    bool moves = false;
+                    if (lane < HW) {
+                        const float(*all)[24] = sh.part + 4 * wg;
+                        most = fmaxf(fmaxf(all[0][lane], all[1][lane]), fmaxf(all[2][lane], all[3][lane]));
+                        moves = (most > kBias + kSlack || u == 0) && most > -INFINITY;
+                        const float by = moves ? kBias - kHead - most : 0.f;   // M_old - M_new
+                        step[lane] = by;
+                        fac[lane] = fast_exp2(by);
+                        bias[lane] += by;
                     }
-                    if (lane < HW) fac[lane] = f;
-                    uint32_t moved = __ballot_sync(0xffffffffu, x != INT_MIN);
+                    uint32_t moved = __ballot_sync(0xffffffffu, moves);
                     __syncwarp();
+#pragma unroll
+                    for (int h = 0; h < HW; h += 4) {
+                        const float4 by = lds4(step + h);
+                        x[h] += by.x, x[h + 1] += by.y, x[h + 2] += by.z, x[h + 3] += by.w;
+                    }
                     if (u > 0) {
 #pragma unroll
                         for (int h = 0; h < HW; h += 4) {
@@ -514,22 +541,19 @@ __global__ void __launch_bounds__(kThreads, 1)
                         tc_fence_before();
                     }
                 }
-                tc_fence_before();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(bar(sh.s_free[sb]));
                 // weights, their sums, and P^T as the MN-major N side: row t, 2 HW bytes of this warpgroup
-                const float unref = exp2_int(-ref);
+                const float2 unref = make_float2(exp2_int(-ref), exp2_int(-ref));
                 uint32_t w[HW / 2];   // HW / 4 words of hi bytes, then of lo bytes
 #pragma unroll
                 for (int h = 0; h < HW; h += 4) {
-                    const float4 bi = lds4(bias + h);
-                    const float x0 = fast_exp2(a[h] + bi.x), x1 = fast_exp2(a[h + 1] + bi.y);
-                    const float x2 = fast_exp2(a[h + 2] + bi.z), x3 = fast_exp2(a[h + 3] + bi.w);
-                    l[h] = fmaf(x0, unref, l[h]), l[h + 1] = fmaf(x1, unref, l[h + 1]);
-                    l[h + 2] = fmaf(x2, unref, l[h + 2]), l[h + 3] = fmaf(x3, unref, l[h + 3]);
-                    const uint32_t x = split16_e4m3x2(x0, x1), y = split16_e4m3x2(x2, x3);
-                    w[h / 4] = byte_perm(x, y, 0x5410);
-                    w[HW / 4 + h / 4] = byte_perm(x, y, 0x7632);
+                    const float2 p01 = make_float2(fast_exp2(x[h]), fast_exp2(x[h + 1]));
+                    const float2 p23 = make_float2(fast_exp2(x[h + 2]), fast_exp2(x[h + 3]));
+                    const float2 l01 = fma2(p01, unref, make_float2(l[h], l[h + 1]));
+                    const float2 l23 = fma2(p23, unref, make_float2(l[h + 2], l[h + 3]));
+                    l[h] = l01.x, l[h + 1] = l01.y, l[h + 2] = l23.x, l[h + 3] = l23.y;
+                    const uint32_t y = split16_e4m3x2(p01.x, p01.y), z = split16_e4m3x2(p23.x, p23.y);
+                    w[h / 4] = byte_perm(y, z, 0x5410);
+                    w[HW / 4 + h / 4] = byte_perm(y, z, 0x7632);
                 }
                 if (un >= kPBufs) ok &= mbar_wait(bar(sh.p_free[pb]), (un / kPBufs - 1) & 1, p.err, abort_flag);
                 const uint32_t prow = base + L::P + pb * kSlab;
@@ -546,7 +570,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 float s = l[h];
 #pragma unroll
                 for (int o = 16; o >= 1; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
-                if (lane == h) fac[h] = s;
+                if (lane == h) part[h] = s;
             }
             const uint32_t last = un - 1;
             ok &= mbar_wait(bar(sh.p_free[last % kPBufs]), (last / kPBufs) & 1, p.err, abort_flag);
@@ -554,9 +578,9 @@ __global__ void __launch_bounds__(kThreads, 1)
             tc_fence_after();
             const size_t slot = static_cast<size_t>(seg.slot) * p.H + h0 + wg * HW;
             if (t < mine) {   // (mine <= 24: the warpgroup's first warp)
-                const float(*part)[24] = sh.fac + 4 * wg;
+                const float(*all)[24] = sh.part + 4 * wg;
                 p.ws_m[slot + t] = -bias[t];
-                p.ws_l[slot + t] = (part[0][t] + part[1][t]) + (part[2][t] + part[3][t]);
+                p.ws_l[slot + t] = (all[0][t] + all[1][t]) + (all[2][t] + all[3][t]);
             }
 #pragma unroll 1
             for (int c = 0; c < 4 * (HW / 8); ++c) {
@@ -571,7 +595,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     if (g + k < mine) dst[static_cast<size_t>(k) * kR] = fmaf(lw[k], kLoPart, hi[k]);
             }
             tc_fence_before();
-            named_bar_sync(id, 128);   // fac and mul are read before the next segment sets them
+            named_bar_sync(id, 128);   // part and mul are read before the next segment sets them
             more = walk.next(seg);
         }
         if (!ok) *abort_flag = 1;
