@@ -50,13 +50,12 @@ constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kBias = 8.f;               // P = 2^(a - M + kBias)
 constexpr float kHead = 1.f, kSlack = 0.75f;   // a new maximum is set kHead above the row that forced it
 // Register split of the 5 warpgroups x 96 launched: control, 2 x softmax, 2 x expansion.
-constexpr uint32_t kRegsCtl = 80, kRegsSoft = 120, kRegsExp = 80, kRegsLaunch = 96;
+constexpr uint32_t kRegsCtl = 64, kRegsSoft = 120, kRegsExp = 88, kRegsLaunch = 96;
 static_assert(kRegsCtl + 2 * kRegsSoft + 2 * kRegsExp <= 5 * kRegsLaunch, "register split exceeds the launch");
 
 constexpr uint32_t kSlab = 16384;          // [128 rows x 128 latent] e4m3, 128-byte swizzle
-constexpr uint32_t kStage = 8192;          // codes of one slab: [128 rows x 64 bytes]
 constexpr uint32_t kScaleTile = 2048;      // [128 rows x 16 scale bytes]
-constexpr int kScaleSlots = 2, kSlabs = 8;   // expanded tiles in flight: two units
+constexpr int kScaleSlots = 2, kPBufs = 2, kSlabs = 8;   // slabs: expanded tiles in flight, two units
 constexpr uint32_t kSharedBytes = 5120;    // Fp4Shared
 constexpr int kTables = 22;                // exponents -14 (all zero) .. 6 below the row's largest, then NaN
 
@@ -65,10 +64,10 @@ constexpr int kTables = 22;                // exponents -14 (all zero) .. 6 belo
 template <int HP>
 struct Fp4Layout {
     static constexpr int HW = HP / 2, N = 2 * HP;
-    static constexpr int kStages = HP == 16 ? 4 : 3, kPBufs = HP == 48 ? 1 : 2, kSBufs = HP == 48 ? 1 : 2;
+    static constexpr int kSBufs = HP == 48 ? 1 : 2;
     static constexpr uint32_t kQSlab = N * 128;                        // [N x 128 latent] e4m3
-    static constexpr uint32_t Q = 0, C = Q + 4 * kQSlab, P = C + kSlabs * kSlab, STAGE = P + kPBufs * kSlab,
-                              SCALE = STAGE + kStages * kStage, END = SCALE + kScaleSlots * kScaleTile;
+    static constexpr uint32_t Q = 0, C = Q + 4 * kQSlab, P = C + kSlabs * kSlab, SCALE = P + kPBufs * kSlab,
+                              END = SCALE + kScaleSlots * kScaleTile;
     static constexpr uint32_t kSmem = END + kSharedBytes + 1024;               // + Fp4Shared + alignment slack
     static constexpr uint32_t S_COL = 0, O_COL = 128;                  // TMEM columns
     static_assert(kQSlab % 1024 == 0 && O_COL + 4 * N <= 512 && kSBufs * N <= O_COL && HW % 8 == 0, "layout");
@@ -76,11 +75,10 @@ struct Fp4Layout {
 };
 
 struct Fp4Shared {
-    uint64_t stage_full[4], stage_empty[4];
     uint64_t scale_full[kScaleSlots], scale_empty[kScaleSlots];
     uint64_t slab_full[kSlabs], slab_free[kSlabs];
     uint64_t s_full[2], s_free[2], q_ready;
-    uint64_t p_full[2], p_free[2];
+    uint64_t p_full[kPBufs], p_free[kPBufs];
     uint32_t tmem_base;
     int abort;
     uint32_t pad_[2];
@@ -96,6 +94,8 @@ static_assert(sizeof(Fp4Shared) <= kSharedBytes, "shared block too large");
 
 struct Fp4Params {
     const __nv_bfloat16 *q_abs;
+    const uint8_t *c4;
+    long long ld;
     const int *lens;
     float *ws_o, *ws_m, *ws_l;   // [slots][H] (x r): sum of P c, M - kBias, l
     int *err;
@@ -133,13 +133,14 @@ __device__ __forceinline__ T warp_scan(T v, int lane) {
 
 struct Segment {
     int seq, row0, units, len;   // rows row0 .. row0 + 128 * units - 1, those below len
-    long long slot;
+    int slot;
 };
 
+// (Positions on the axis fit 32 bits: 2^31 units are 75 TB of cache.)
 struct Walk {
     const int *lens;
     int B, max_len, c, b, j;     // chunk j of sequence b is next
-    long long lo, hi, pre, v;    // its first virtual unit and its number
+    int lo, hi, pre, v;          // its first virtual unit and its number
     // Every lane of a warp calls this; all get the same walk.
     __device__ void start(const Fp4Params &p, int share, int lane, int *err) {
         lens = p.lens, B = p.B, max_len = p.max_len, c = share;
@@ -147,12 +148,12 @@ struct Walk {
         for (int i = lane; i < B; i += 32) total += units_of(read_len(lens, i, max_len, err));
 #pragma unroll
         for (int o = 16; o >= 1; o >>= 1) total += __shfl_xor_sync(0xffffffffu, total, o);
-        lo = share_lo(total, share, p.G), hi = share_lo(total, share + 1, p.G);
-        b = B, j = 0, pre = total, v = 0;
-        long long run = 0, chunks = 0;
+        lo = static_cast<int>(share_lo(total, share, p.G)), hi = static_cast<int>(share_lo(total, share + 1, p.G));
+        b = B, j = 0, pre = hi, v = 0;
+        int run = 0, chunks = 0;
         for (int i0 = 0; i0 < B && lo < hi; i0 += 32) {
             const int len = i0 + lane < B ? read_len(lens, i0 + lane, max_len, nullptr) : 0;
-            const long long u = units_of(len), incl = warp_scan(u, lane);
+            const int u = static_cast<int>(units_of(len)), incl = warp_scan(u, lane);
             const int n = len > 0 ? chunks_of(len) : 0, nincl = warp_scan(n, lane);
             const unsigned past = __ballot_sync(0xffffffffu, run + incl > lo);
             if (past) {
@@ -160,8 +161,8 @@ struct Walk {
                 b = i0 + first;
                 pre = run + __shfl_sync(0xffffffffu, incl - u, first);
                 v = chunks + __shfl_sync(0xffffffffu, nincl - n, first);
-                j = static_cast<int>((lo - pre) / kChunkSpan);
-                pre += static_cast<long long>(j) * kChunkSpan;
+                j = (lo - pre) / kChunkSpan;
+                pre += j * kChunkSpan;
                 v += j;
                 break;
             }
@@ -178,10 +179,10 @@ struct Walk {
             }
             const int left = len - j * kChunkRows;   // > 0: the walk leaves a sequence with its last chunk
             const int units = left >= kChunkRows ? kChunkUnits : (left + kRows - 1) / kRows;
-            const long long base = pre + kOverUnits, s0 = max(base, lo), s1 = min(base + units, hi);
+            const int base = pre + kOverUnits, s0 = max(base, lo), s1 = min(base + units, hi);
             s.seq = b, s.len = len, s.slot = c + v;
-            s.row0 = j * kChunkRows + static_cast<int>(s0 - base) * kRows;
-            s.units = static_cast<int>(s1 - s0);
+            s.row0 = j * kChunkRows + (s0 - base) * kRows;
+            s.units = s1 - s0;
             pre = base + units, ++v;
             if (left > kChunkRows) ++j; else ++b, j = 0;
             if (s1 > s0) return true;
@@ -208,12 +209,34 @@ __device__ __forceinline__ uint32_t byte_perm(uint32_t a, uint32_t b, uint32_t s
     asm("prmt.b32 %0, %1, %2, %3;" : "=r"(r) : "r"(a), "r"(b), "r"(sel));
     return r;
 }
-// Eight codes as e4m3 bytes by the group's table of magnitudes: three bits of each code select one of its bytes, the
-// fourth the sign.
+// Eight codes as e4m3 bytes by the group's table of magnitudes: three bits of each code select one of its bytes; the
+// codes' fourth bits are the top bits of the bytes of w (odd codes) and of w << 4 (even ones).
 __device__ __forceinline__ void expand8(uint32_t w, uint2 table, uint32_t &o0, uint32_t &o1) {
-    const uint32_t m = w & 0x77777777u, s = (w >> 1) & 0x44444444u;
-    o0 = byte_perm(table.x, table.y, m) | byte_perm(0u, 0x80808080u, s);
-    o1 = byte_perm(table.x, table.y, m >> 16) | byte_perm(0u, 0x80808080u, s >> 16);
+    const uint32_t m = w & 0x77777777u, w4 = w * 16u, m_hi = static_cast<uint32_t>(static_cast<uint64_t>(m) * 65536u >> 32);
+    o0 = byte_perm(table.x, table.y, m) | (byte_perm(w, w4, 0x1504) & 0x80808080u);
+    o1 = byte_perm(table.x, table.y, m_hi) | (byte_perm(w, w4, 0x3726) & 0x80808080u);
+}
+// 16 bytes that are read once by this SM.
+__device__ __forceinline__ uint4 ld_stream(const uint8_t *p) {
+    uint4 v;
+    asm("ld.global.nc.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "l"(p));
+    return v;
+}
+// The largest of a row's 16 scale bytes, NaN bytes aside, in the range that the format allows.
+__device__ __forceinline__ int row_top(const uint8_t *row) {
+    const uint4 v = *reinterpret_cast<const uint4 *>(row);
+    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+    uint32_t m = 0;   // two 16-bit maxima
+#pragma unroll
+    for (int i = 0; i < 4; ++i) m = __vmaxu2(m, __vmaxu2(w[i] & 0x00FF00FFu, w[i] >> 8 & 0x00FF00FFu));
+    int top = max(m & 0xFFFFu, m >> 16);
+    if (top == kFp4ScaleNan) {
+        top = 0;
+#pragma unroll 1
+        for (int i = 0; i < 16; ++i)
+            if (row[i] != kFp4ScaleNan) top = max(top, static_cast<int>(row[i]));
+    }
+    return min(max(top, kFp4ScaleMin), kFp4ScaleMax);
 }
 // Two fp32 operations in one instruction (sm_100 family).
 __device__ __forceinline__ unsigned long long bits2(float2 v) {
@@ -284,10 +307,9 @@ __device__ __forceinline__ float store_query(uint32_t q_base, int h, int lane, c
 // ------------------------------------------------------------------ attention
 template <int HP>
 __global__ void __launch_bounds__(kThreads, 1)
-    fp4_attention_kernel(const __grid_constant__ CUtensorMap tm_codes, const __grid_constant__ CUtensorMap tm_scales,
-                         const Fp4Params p) {
+    fp4_attention_kernel(const __grid_constant__ CUtensorMap tm_scales, const Fp4Params p) {
     using L = Fp4Layout<HP>;
-    constexpr int HW = L::HW, N = L::N, kStages = L::kStages, kPBufs = L::kPBufs, kSBufs = L::kSBufs;
+    constexpr int HW = L::HW, N = L::N, kSBufs = L::kSBufs;
     extern __shared__ uint8_t smem_raw[];
     const uint32_t raw = smem_u32(smem_raw), base = (raw + 1023u) & ~1023u;
     Fp4Shared &sh = *reinterpret_cast<Fp4Shared *>(smem_raw + (base - raw) + L::END);
@@ -298,9 +320,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int h0 = group * p.heads_per_group, heads = min(p.heads_per_group, p.H - h0);
 
     if (threadIdx.x == 0) {
-        for (int i = 0; i < kStages; ++i) mbar_init(bar(sh.stage_full[i]), 1), mbar_init(bar(sh.stage_empty[i]), 8);
         for (int i = 0; i < kScaleSlots; ++i) mbar_init(bar(sh.scale_full[i]), 1), mbar_init(bar(sh.scale_empty[i]), 8);
-        for (int i = 0; i < kSlabs; ++i) mbar_init(bar(sh.slab_full[i]), 8), mbar_init(bar(sh.slab_free[i]), 1);
+        for (int i = 0; i < kSlabs; ++i) mbar_init(bar(sh.slab_full[i]), 2), mbar_init(bar(sh.slab_free[i]), 1);
         for (int i = 0; i < kSBufs; ++i) mbar_init(bar(sh.s_full[i]), 1), mbar_init(bar(sh.s_free[i]), 8);
         for (int i = 0; i < kPBufs; ++i) mbar_init(bar(sh.p_full[i]), 8), mbar_init(bar(sh.p_free[i]), 1);
         mbar_init(bar(sh.q_ready), 8);
@@ -333,37 +354,25 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (warp < 4) {
         regs_release<kRegsCtl>();
         if (warp == 0 && lane == 0) {
-            // ---- TMA: per unit the scale bytes and four boxes of codes [128 rows x 128 latent]
-            tma_prefetch_desc(&tm_codes);
+            // ---- TMA: a unit's scale bytes
             tma_prefetch_desc(&tm_scales);
-            uint32_t it = 0, un = 0;
+            uint32_t un = 0;
             bool ok = true;
             while (ok && walk.next(seg)) {
-                for (int u = 0; ok && u < seg.units; ++u, ++un) {
-                    const int row = seg.row0 + u * kRows;
+                for (int u = 0; u < seg.units; ++u, ++un) {
                     const uint32_t sl = un % kScaleSlots;
                     if (un >= kScaleSlots &&
                         !(ok = mbar_wait(bar(sh.scale_empty[sl]), (un / kScaleSlots - 1) & 1, p.err, abort_flag)))
                         break;
                     mbar_arrive_expect_tx(bar(sh.scale_full[sl]), kScaleTile);
-                    tma_load_3d(base + L::SCALE + sl * kScaleTile, &tm_scales, bar(sh.scale_full[sl]), kR / 2, row, seg.seq);
-                    for (int k = 0; k < 4; ++k, ++it) {
-                        const uint32_t st = it % kStages;
-                        if (it >= kStages &&
-                            !(ok = mbar_wait(bar(sh.stage_empty[st]), (it / kStages - 1) & 1, p.err, abort_flag)))
-                            break;
-                        mbar_arrive_expect_tx(bar(sh.stage_full[st]), kStage);
-                        tma_load_3d(base + L::STAGE + st * kStage, &tm_codes, bar(sh.stage_full[st]), k * 64, row, seg.seq);
-                    }
+                    tma_load_3d(base + L::SCALE + sl * kScaleTile, &tm_scales, bar(sh.scale_full[sl]), kR / 2,
+                                seg.row0 + u * kRows, seg.seq);
                 }
             }
             if (!ok) *abort_flag = 1;
             // no load may still be landing when the CTA exits
-            for (uint32_t k = it > kStages ? it - kStages : 0; k < it; ++k)
-                mbar_wait(bar(sh.stage_full[k % kStages]), (k / kStages) & 1, p.err);
-            // (an abort between the two kinds leaves `un` one behind the scale tiles asked for)
-            for (uint32_t k = un >= kScaleSlots ? un - kScaleSlots + (ok ? 0 : 1) : 0; k < un + (ok ? 0 : 1); ++k)
-                mbar_wait(bar(sh.scale_full[k % kScaleSlots]), (k / kScaleSlots) & 1, p.err, ok ? nullptr : abort_flag);
+            for (uint32_t k = un > kScaleSlots ? un - kScaleSlots : 0; k < un; ++k)
+                mbar_wait(bar(sh.scale_full[k % kScaleSlots]), (k / kScaleSlots) & 1, p.err);
         } else if (warp == 1 && lane == 0) {
             // ---- S^T = c . q^T: four slabs of K = 128
             constexpr uint32_t idesc = make_idesc_e4m3(128, N, 0, 0);
@@ -601,72 +610,79 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (!ok) *abort_flag = 1;
     } else {
         regs_release<kRegsExp>();
-        // ---- expansion: a warp takes 16 of a unit's rows, a lane group `g` (32 codes) of every slab in rows r and r + 8
-        const int r = (warp - 12) * 16 + (lane >> 2), g = lane & 3;
-        const uint8_t *const smem = smem_raw + (base - raw);
-        uint32_t it = 0, un = 0;
-        bool ok = true;
-        while (walk.next(seg)) {
-            for (int u = 0; u < seg.units; ++u, ++un) {
-                const int rows = seg.len - seg.row0 - u * kRows;
-                const uint32_t sc = un % kScaleSlots;
-                const uint8_t *const tile = smem + L::SCALE + sc * kScaleTile + r * 16 + g;
-                ok &= mbar_wait(bar(sh.scale_full[sc]), (un / kScaleSlots) & 1, p.err, abort_flag);
-                // the rows' largest scale exponent (NaN bytes aside) becomes e4m3's 2^6; `pick`: tables of the 4 slabs
-                int X[2][4], top[2];
-                uint32_t pick[2];
-#pragma unroll
-                for (int i = 0; i < 2; ++i) {
-                    top[i] = kFp4ScaleMin;
-#pragma unroll
-                    for (int k = 0; k < 4; ++k) {
-                        X[i][k] = tile[i * 128 + k * 4];
-                        if (X[i][k] != kFp4ScaleNan) top[i] = max(top[i], X[i][k]);
-                    }
-                    top[i] = max(top[i], __shfl_xor_sync(0xffffffffu, top[i], 1));
-                    top[i] = min(max(top[i], __shfl_xor_sync(0xffffffffu, top[i], 2)), kFp4ScaleMax);
-                    pick[i] = 0;
-#pragma unroll
-                    for (int k = 0; k < 4; ++k) {
-                        const int in = min(max(X[i][k], kFp4ScaleMin), kFp4ScaleMax);
-                        pick[i] |= static_cast<uint32_t>(X[i][k] == kFp4ScaleNan ? kTables - 1 : max(in - top[i] + 20, 0)) << 8 * k;
-                    }
-                    if (r + 8 * i >= rows) pick[i] = 0;   // rows past the end: zeros
-                }
-                __syncwarp();
-                if (lane == 0) mbar_arrive(bar(sh.scale_empty[sc]));
-#pragma unroll 1
-                for (int k = 0; k < 4; ++k, ++it) {
-                    const uint32_t st = it % kStages, sl = it % kSlabs;
-                    // (the unit's first slab is free once the products two units back are done, so the softmax has read
-                    // what the ref slot held)
-                    if (it >= kSlabs) ok &= mbar_wait(bar(sh.slab_free[sl]), (it / kSlabs - 1) & 1, p.err, abort_flag);
-                    if (k == 0 && g == 0) {
-                        sh.ref[un & 1][r] = static_cast<int16_t>(top[0] - 127 - 6);
-                        sh.ref[un & 1][r + 8] = static_cast<int16_t>(top[1] - 127 - 6);
-                    }
-                    ok &= mbar_wait(bar(sh.stage_full[st]), (it / kStages) & 1, p.err, abort_flag);
-                    const uint4 *const src = reinterpret_cast<const uint4 *>(smem + L::STAGE + st * kStage) + r * 4 + g;
-                    const uint4 v[2] = {src[0], src[32]};
-                    const uint2 tb[2] = {sh.table[pick[0] >> 8 * k & 0xFFu], sh.table[pick[1] >> 8 * k & 0xFFu]};
-                    const uint32_t slab = base + L::C + sl * kSlab;
-#pragma unroll
-                    for (int i = 0; i < 2; ++i) {
-                        const uint32_t w[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
-                        uint32_t o[8];
-#pragma unroll
-                        for (int j = 0; j < 4; ++j) expand8(w[j], tb[i], o[2 * j], o[2 * j + 1]);
-                        st_shared_v4(slab + sw128_offset(r + 8 * i, 2 * g), o[0], o[1], o[2], o[3]);
-                        st_shared_v4(slab + sw128_offset(r + 8 * i, 2 * g + 1), o[4], o[5], o[6], o[7]);
-                    }
-                    fence_proxy_async_smem();
-                    __syncwarp();
-                    if (lane == 0) {
-                        mbar_arrive(bar(sh.slab_full[sl]));
-                        mbar_arrive(bar(sh.stage_empty[st]));
-                    }
-                }
+        // ---- expansion: a warp takes half of the rows of one of a unit's four slabs, a lane the groups (32 codes) `g` of
+        // rows r + 8 i.  A lane's codes of the next unit are loaded as those of this one are used: 32 KB in flight per SM
+        const int k = (warp - 12) & 3, half = (warp - 12) >> 2, g = lane & 3, r = half * 64 + (lane >> 2);
+        uint8_t *const smem = smem_raw + (base - raw);
+        const long long step8 = 8 * p.ld;
+        const uint8_t *next = nullptr;   // this lane's codes of row r of the next unit
+        int nu = 0, nrows = 0;           // the next unit's number in its segment, and its rows
+        auto find = [&] {
+            if (nrows > 0 && nu < seg.units) {
+                next += kRows * p.ld;
+            } else if (walk.next(seg)) {
+                nu = 0;
+                next = p.c4 + (static_cast<long long>(seg.seq) * p.max_len + seg.row0 + r) * p.ld + k * 64 + g * 16;
+            } else {
+                nrows = 0;
+                return;
             }
+            nrows = seg.len - seg.row0 - nu * kRows;
+            ++nu;
+        };
+        uint4 v[8];
+        find();
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[i] = r + 8 * i < nrows ? ld_stream(next + i * step8) : make_uint4(0, 0, 0, 0);
+        bool ok = true;
+        for (uint32_t it = k, un = 0; nrows > 0; it += 4, ++un) {
+            const int rows = nrows;
+            find();
+            const uint32_t sc = un % kScaleSlots, sl = it % kSlabs;
+            const uint8_t *const tile = smem + L::SCALE + sc * kScaleTile;
+            ok &= mbar_wait(bar(sh.scale_full[sc]), (un / kScaleSlots) & 1, p.err, abort_flag);
+            // the largest scale exponent of rows 64 half + lane and + 32 (NaN bytes aside) becomes e4m3's 2^6
+            int top[2];
+#pragma unroll
+            for (int i = 0; i < 2; ++i) top[i] = row_top(tile + (half * 64 + i * 32 + lane) * 16);
+            // (the unit's first slab is free once the products two units back are done, so the softmax has read what the
+            // ref slot held)
+            if (it >= kSlabs) ok &= mbar_wait(bar(sh.slab_free[sl]), (it / kSlabs - 1) & 1, p.err, abort_flag);
+            if (k == 0) {
+                sh.ref[un & 1][half * 64 + lane] = static_cast<int16_t>(top[0] - 127 - 6);
+                sh.ref[un & 1][half * 64 + 32 + lane] = static_cast<int16_t>(top[1] - 127 - 6);
+            }
+            uint8_t *const slab = smem + L::C + sl * kSlab + sw128_offset(r, 0) - (lane >> 2) * 16;
+            const int x = ((2 * g) ^ (lane >> 2)) * 16;   // row & 7 = lane >> 2: the swizzle of the group's first 16 bytes
+            uint2 tb[8];   // all read before the first store
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                const int X = tile[(r + 8 * i) * 16 + k * 4 + g];
+                const int t = __shfl_sync(0xffffffffu, top[i / 4], (lane >> 2) + 8 * (i & 3));
+                int at = X == kFp4ScaleNan ? kTables - 1 : max(min(max(X, kFp4ScaleMin), kFp4ScaleMax) - t + 20, 0);
+                if (r + 8 * i >= rows) at = 0;   // rows past the end: zeros
+                tb[i] = sh.table[at];
+            }
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                uint32_t o[8];
+                expand8(v[i].x, tb[i], o[0], o[1]);
+                expand8(v[i].y, tb[i], o[2], o[3]);
+                expand8(v[i].z, tb[i], o[4], o[5]);
+                expand8(v[i].w, tb[i], o[6], o[7]);
+                *reinterpret_cast<uint4 *>(slab + i * 1024 + x) = make_uint4(o[0], o[1], o[2], o[3]);
+                *reinterpret_cast<uint4 *>(slab + i * 1024 + (x ^ 16)) = make_uint4(o[4], o[5], o[6], o[7]);
+            }
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) {
+                mbar_arrive(bar(sh.slab_full[sl]));
+                mbar_arrive(bar(sh.scale_empty[sc]));
+            }
+            // (after the fence, which would wait for them)
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+                v[i] = r + 8 * i < nrows ? ld_stream(next + i * step8) : make_uint4(0, 0, 0, 0);
         }
         if (!ok) *abort_flag = 1;
     }
@@ -932,7 +948,7 @@ size_t slot_count(int B, int max_len, int G) {
 }
 
 template <int HP>
-cudaError_t launch_attention(const CUtensorMap &codes, const CUtensorMap &scales, const Fp4Params &p, cudaStream_t s) {
+cudaError_t launch_attention(const CUtensorMap &scales, const Fp4Params &p, cudaStream_t s) {
     using L = Fp4Layout<HP>;
     cudaError_t e = cudaFuncSetAttribute(fp4_attention_kernel<HP>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                          static_cast<int>(L::kSmem));
@@ -941,7 +957,7 @@ cudaError_t launch_attention(const CUtensorMap &codes, const CUtensorMap &scales
     if ((e = cudaFuncGetAttributes(&fa, fp4_attention_kernel<HP>)) != cudaSuccess) return e;
     if (fa.numRegs != static_cast<int>(kRegsLaunch)) return cudaErrorInvalidConfiguration;
     note_launch();
-    fp4_attention_kernel<HP><<<p.G * p.groups, kThreads, L::kSmem, s>>>(codes, scales, p);
+    fp4_attention_kernel<HP><<<p.G * p.groups, kThreads, L::kSmem, s>>>(scales, p);
     return cudaGetLastError();
 }
 
@@ -955,6 +971,8 @@ cudaError_t launch_decode_fp4(const DecodeArgs &a, cudaStream_t s) {
     if (!decode_bf16_supports(a.H, a.d_v, a.r)) return cudaErrorInvalidValue;
     Fp4Params p;
     p.q_abs = static_cast<const __nv_bfloat16 *>(a.q_abs);
+    p.c4 = static_cast<const uint8_t *>(a.c_cache);
+    p.ld = a.ld_cache;
     p.lens = a.lens;
     p.B = a.B;
     p.H = a.H;
@@ -969,26 +987,24 @@ cudaError_t launch_decode_fp4(const DecodeArgs &a, cudaStream_t s) {
     p.ws_l = p.ws_m + slots * a.H;
     p.err = a.dev_err;
     p.scale_log2 = a.scale * kLog2e;
-    CUtensorMap tm_codes, tm_scales, tm_wuv;
+    CUtensorMap tm_scales, tm_wuv;
     {
         const cuuint64_t rows = static_cast<cuuint64_t>(a.max_len > 0 ? a.max_len : 1);
         const cuuint64_t dims[3] = {kR / 2 + kR / 32, rows, static_cast<cuuint64_t>(a.B)};
         const cuuint64_t strides[2] = {static_cast<cuuint64_t>(a.ld_cache), rows * static_cast<cuuint64_t>(a.ld_cache)};
-        const cuuint32_t box[3] = {64, kRows, 1}, sbox[3] = {16, kRows, 1};
+        const cuuint32_t box[3] = {16, kRows, 1};
         const cuuint64_t wd[2] = {kR, static_cast<cuuint64_t>(a.H) * kDV}, ws[1] = {kR * 2};
         const cuuint32_t wb[2] = {64, kDV};
-        if (encode_map(&tm_codes, CU_TENSOR_MAP_DATA_TYPE_UINT8, CU_TENSOR_MAP_SWIZZLE_NONE, a.c_cache, 3, dims, strides,
+        if (encode_map(&tm_scales, CU_TENSOR_MAP_DATA_TYPE_UINT8, CU_TENSOR_MAP_SWIZZLE_NONE, a.c_cache, 3, dims, strides,
                        box) != CUDA_SUCCESS ||
-            encode_map(&tm_scales, CU_TENSOR_MAP_DATA_TYPE_UINT8, CU_TENSOR_MAP_SWIZZLE_NONE, a.c_cache, 3, dims, strides,
-                       sbox) != CUDA_SUCCESS ||
             encode_map(&tm_wuv, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, CU_TENSOR_MAP_SWIZZLE_128B, a.w_uv, 2, wd, ws, wb) !=
                 CUDA_SUCCESS)
             return cudaErrorInvalidValue;
     }
     const int hp = p.heads_per_group;
-    cudaError_t e = hp <= 16   ? launch_attention<16>(tm_codes, tm_scales, p, s)
-                    : hp <= 32 ? launch_attention<32>(tm_codes, tm_scales, p, s)
-                               : launch_attention<48>(tm_codes, tm_scales, p, s);
+    cudaError_t e = hp <= 16   ? launch_attention<16>(tm_scales, p, s)
+                    : hp <= 32 ? launch_attention<32>(tm_scales, p, s)
+                               : launch_attention<48>(tm_scales, p, s);
     if (e != cudaSuccess) return e;
     e = cudaFuncSetAttribute(fp4_merge_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(kSmemMerge));
     if (e != cudaSuccess) return e;
