@@ -23,7 +23,7 @@
 // lanes and their columns of O^T rescaled.  A weight below 2^-22 of the largest is lost; sequences are cut into chunks
 // of 32768 rows with maxima of their own, so less than 2^-7 of a chunk's weight can go that way.
 //
-// Warps: 0 TMA, 1 issues S, 2 issues O, 4-11 softmax (and q_abs, rescale, drain; half of the heads to each of two
+// Warps: 0 and 3 turn scale bytes into table numbers, 1 issues S, 2 issues O, 4-11 softmax (and q_abs, rescale, drain; half of the heads to each of two
 // warpgroups that never wait for one another), 12-19 expand.  The expansion is a byte
 // permute per four codes: the group's exponent selects an 8-byte table of e4m3 magnitudes, the codes' three magnitude
 // bits are the selector.
@@ -50,24 +50,24 @@ constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kBias = 8.f;               // P = 2^(a - M + kBias)
 constexpr float kHead = 1.f, kSlack = 0.75f;   // a new maximum is set kHead above the row that forced it
 // Register split of the 5 warpgroups x 96 launched: control, 2 x softmax, 2 x expansion.
-constexpr uint32_t kRegsCtl = 64, kRegsSoft = 120, kRegsExp = 88, kRegsLaunch = 96;
+constexpr uint32_t kRegsCtl = 80, kRegsSoft = 104, kRegsExp = 96, kRegsLaunch = 96;
 static_assert(kRegsCtl + 2 * kRegsSoft + 2 * kRegsExp <= 5 * kRegsLaunch, "register split exceeds the launch");
 
 constexpr uint32_t kSlab = 16384;          // [128 rows x 128 latent] e4m3, 128-byte swizzle
-constexpr uint32_t kScaleTile = 2048;      // [128 rows x 16 scale bytes]
-constexpr int kScaleSlots = 2, kPBufs = 2, kSlabs = 8;   // slabs: expanded tiles in flight, two units
+constexpr uint32_t kPicks = 2048;          // [128 rows x 16 groups] table numbers of a unit
+constexpr int kPickBufs = 2, kPBufs = 2, kSlabs = 8;   // slabs: expanded tiles in flight, two units
 constexpr uint32_t kSharedBytes = 5120;    // Fp4Shared
 constexpr int kTables = 22;                // exponents -14 (all zero) .. 6 below the row's largest, then NaN
 
-// Heads of a CTA are padded to HP and shared by two softmax warpgroups of HW each; a warpgroup's columns of the N side
-// are its heads' hi parts, then their lo parts.
+// Heads of a CTA are padded to HP and shared by two softmax warpgroups of HW each.  Columns of the N side: the two hi
+// parts of a pair of heads, then their lo parts.
 template <int HP>
 struct Fp4Layout {
     static constexpr int HW = HP / 2, N = 2 * HP;
     static constexpr int kSBufs = HP == 48 ? 1 : 2;
     static constexpr uint32_t kQSlab = N * 128;                        // [N x 128 latent] e4m3
-    static constexpr uint32_t Q = 0, C = Q + 4 * kQSlab, P = C + kSlabs * kSlab, SCALE = P + kPBufs * kSlab,
-                              END = SCALE + kScaleSlots * kScaleTile;
+    static constexpr uint32_t Q = 0, C = Q + 4 * kQSlab, P = C + kSlabs * kSlab, PICK = P + kPBufs * kSlab,
+                              END = PICK + kPickBufs * kPicks;
     static constexpr uint32_t kSmem = END + kSharedBytes + 1024;               // + Fp4Shared + alignment slack
     static constexpr uint32_t S_COL = 0, O_COL = 128;                  // TMEM columns
     static_assert(kQSlab % 1024 == 0 && O_COL + 4 * N <= 512 && kSBufs * N <= O_COL && HW % 8 == 0, "layout");
@@ -75,7 +75,7 @@ struct Fp4Layout {
 };
 
 struct Fp4Shared {
-    uint64_t scale_full[kScaleSlots], scale_empty[kScaleSlots];
+    uint64_t pick_full[kPickBufs], pick_empty[kPickBufs];
     uint64_t slab_full[kSlabs], slab_free[kSlabs];
     uint64_t s_full[2], s_free[2], q_ready;
     uint64_t p_full[kPBufs], p_free[kPBufs];
@@ -83,7 +83,7 @@ struct Fp4Shared {
     int abort;
     uint32_t pad_[2];
     uint2 table[kTables];
-    int16_t ref[2][kRows];                 // per row of the last two units: the power of two its tile is divided by
+    int16_t ref[4][kRows];                 // per row of the last four units: the power of two its tile is divided by
     alignas(16) float mul[48];             // per head: score factor
     // per softmax warp and head, the same in a warpgroup's four: kBias - M, and the last change of it with its power of
     // two (part: the warps' maxima, and their parts of l while a segment is drained)
@@ -191,6 +191,24 @@ struct Walk {
     }
 };
 
+// The units of a walk, one after the other; rows = 0 at the end.
+struct Units {
+    int u, rows;
+    __device__ void start(Walk &walk, Segment &seg) {
+        u = -1, rows = 0, seg.units = 0;
+        next(walk, seg);
+    }
+    __device__ void next(Walk &walk, Segment &seg) {
+        rows = 0;
+        if (++u >= seg.units) {
+            if (!walk.next(seg)) return;
+            u = 0;
+        }
+        rows = min(kRows, seg.len - seg.row0 - u * kRows);
+    }
+    __device__ int row(const Segment &seg) const { return seg.row0 + u * kRows; }
+};
+
 // ------------------------------------------------------------------ small pieces
 __device__ __forceinline__ uint32_t mul_f16x2(uint32_t a, uint32_t b) {
     uint32_t r;
@@ -222,21 +240,43 @@ __device__ __forceinline__ uint4 ld_stream(const uint8_t *p) {
     asm("ld.global.nc.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "l"(p));
     return v;
 }
-// The largest of a row's 16 scale bytes, NaN bytes aside, in the range that the format allows.
-__device__ __forceinline__ int row_top(const uint8_t *row) {
-    const uint4 v = *reinterpret_cast<const uint4 *>(row);
-    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-    uint32_t m = 0;   // two 16-bit maxima
+// A row's 16 scale bytes to the numbers of their tables; returns the largest of them, NaN bytes aside, in the range that
+// the format allows: what becomes e4m3's 2^6.
+__device__ __forceinline__ int row_picks(uint32_t (&w)[4]) {
+    uint32_t hi = 0, lo = 0x00FF00FFu;   // two 16-bit maxima and minima
 #pragma unroll
-    for (int i = 0; i < 4; ++i) m = __vmaxu2(m, __vmaxu2(w[i] & 0x00FF00FFu, w[i] >> 8 & 0x00FF00FFu));
-    int top = max(m & 0xFFFFu, m >> 16);
+    for (int i = 0; i < 4; ++i) {
+        const uint32_t even = w[i] & 0x00FF00FFu, odd = byte_perm(w[i], 0u, 0x4341);
+        hi = __vmaxu2(hi, __vmaxu2(even, odd));
+        lo = __vminu2(lo, __vminu2(even, odd));
+    }
+    int top = max(hi & 0xFFFFu, hi >> 16);
+    const int least = min(lo & 0xFFFFu, lo >> 16);
+    if (top <= kFp4ScaleMax && least >= max(kFp4ScaleMin, top - 20)) {   // every group within the tables
+#pragma unroll
+        for (int i = 0; i < 4; ++i) w[i] -= static_cast<uint32_t>(top - 20) * 0x01010101u;   // no byte borrows
+        return top;
+    }
     if (top == kFp4ScaleNan) {
         top = 0;
-#pragma unroll 1
-        for (int i = 0; i < 16; ++i)
-            if (row[i] != kFp4ScaleNan) top = max(top, static_cast<int>(row[i]));
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+            const int X = w[i >> 2] >> (8 * (i & 3)) & 0xFF;
+            if (X != kFp4ScaleNan) top = max(top, X);
+        }
     }
-    return min(max(top, kFp4ScaleMin), kFp4ScaleMax);
+    top = min(max(top, kFp4ScaleMin), kFp4ScaleMax);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        uint32_t at = 0;
+#pragma unroll 1
+        for (int k = 0; k < 32; k += 8) {
+            const int X = w[i] >> k & 0xFF, in = min(max(X, kFp4ScaleMin), kFp4ScaleMax);
+            at |= static_cast<uint32_t>(X == kFp4ScaleNan ? kTables - 1 : max(in - top + 20, 0)) << k;
+        }
+        w[i] = at;
+    }
+    return top;
 }
 // Two fp32 operations in one instruction (sm_100 family).
 __device__ __forceinline__ unsigned long long bits2(float2 v) {
@@ -272,11 +312,8 @@ __device__ __forceinline__ float warp_max(float v) {
 }
 __device__ __forceinline__ float4 lds4(const float *p) { return *reinterpret_cast<const float4 *>(p); }
 
-// N-side row of head h's hi part (its lo part is HW rows further).
-template <int HP>
-__device__ __forceinline__ int hi_row(int h) {
-    return h < HP / 2 ? h : h + HP / 2;
-}
+// N-side row of head h's hi part; its lo part is two further.
+__device__ __forceinline__ int hi_row(int h) { return 2 * (h & ~1) + (h & 1); }
 // One head's query into the N side of S, lane j the latent elements 16j .. 16j + 15.
 // Scaled by a power of two that brings its largest magnitude into [128, 256); returns the factor that undoes it (NaN
 // for a query that holds a NaN or an infinity).
@@ -299,15 +336,36 @@ __device__ __forceinline__ float store_query(uint32_t q_base, int h, int lane, c
         lw[k] = byte_perm(a, b, 0x7632);
     }
     const uint32_t slab = q_base + (lane >> 3) * Fp4Layout<HP>::kQSlab;
-    st_shared_v4(slab + sw128_offset(hi_row<HP>(h), lane & 7), hw[0], hw[1], hw[2], hw[3]);
-    st_shared_v4(slab + sw128_offset(hi_row<HP>(h) + HP / 2, lane & 7), lw[0], lw[1], lw[2], lw[3]);
+    st_shared_v4(slab + sw128_offset(hi_row(h), lane & 7), hw[0], hw[1], hw[2], hw[3]);
+    st_shared_v4(slab + sw128_offset(hi_row(h) + 2, lane & 7), lw[0], lw[1], lw[2], lw[3]);
     return top >= 0x7F800000u ? __uint_as_float(0x7FFFFFFFu) : exp2_int(-e);
+}
+
+// mbar_wait whose tries sleep (up to 2 us each) instead of polling: 20 warps share the schedulers here.
+__device__ __forceinline__ bool sleep_wait(uint32_t bar, uint32_t parity, int *err, const volatile int *abort = nullptr) {
+    const uint64_t t0 = globaltimer_ns();
+    for (;;) {
+        uint32_t ok;
+        asm volatile(
+            "{\n\t.reg .pred p;\n\t"
+            "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\t"
+            "selp.u32 %0, 1, 0, p;\n\t}"
+            : "=r"(ok)
+            : "r"(bar), "r"(parity), "r"(2000u)
+            : "memory");
+        if (ok) return true;
+        if (abort && *abort) return false;
+        if (globaltimer_ns() - t0 > MLA_WAIT_LIMIT_NS) {
+            record_error(err, kDevErrTimeout);
+            return false;
+        }
+    }
 }
 
 // ------------------------------------------------------------------ attention
 template <int HP>
 __global__ void __launch_bounds__(kThreads, 1)
-    fp4_attention_kernel(const __grid_constant__ CUtensorMap tm_scales, const Fp4Params p) {
+    fp4_attention_kernel(const Fp4Params p) {
     using L = Fp4Layout<HP>;
     constexpr int HW = L::HW, N = L::N, kSBufs = L::kSBufs;
     extern __shared__ uint8_t smem_raw[];
@@ -320,7 +378,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int h0 = group * p.heads_per_group, heads = min(p.heads_per_group, p.H - h0);
 
     if (threadIdx.x == 0) {
-        for (int i = 0; i < kScaleSlots; ++i) mbar_init(bar(sh.scale_full[i]), 1), mbar_init(bar(sh.scale_empty[i]), 8);
+        for (int i = 0; i < kPickBufs; ++i) mbar_init(bar(sh.pick_full[i]), 2), mbar_init(bar(sh.pick_empty[i]), 8);
         for (int i = 0; i < kSlabs; ++i) mbar_init(bar(sh.slab_full[i]), 2), mbar_init(bar(sh.slab_free[i]), 1);
         for (int i = 0; i < kSBufs; ++i) mbar_init(bar(sh.s_full[i]), 1), mbar_init(bar(sh.s_free[i]), 8);
         for (int i = 0; i < kPBufs; ++i) mbar_init(bar(sh.p_full[i]), 8), mbar_init(bar(sh.p_free[i]), 1);
@@ -348,31 +406,50 @@ __global__ void __launch_bounds__(kThreads, 1)
     grid_launch_dependents();   // the merge takes SMs as CTAs finish; it waits for the whole grid
 
     Walk walk;
-    walk.start(p, share, lane, blockIdx.x == 0 && warp == 3 ? p.err : nullptr);
+    walk.start(p, share, lane, blockIdx.x == 0 && warp == 0 ? p.err : nullptr);
     Segment seg;
 
     if (warp < 4) {
         regs_release<kRegsCtl>();
-        if (warp == 0 && lane == 0) {
-            // ---- TMA: a unit's scale bytes
-            tma_prefetch_desc(&tm_scales);
-            uint32_t un = 0;
+        if (warp == 0 || warp == 3) {
+            // ---- scale bytes to table numbers and refs, a unit or two ahead: a lane takes rows r0 and r0 + 32
+            const int r0 = (warp == 3 ? 64 : 0) + lane;
+            uint4 v[2];
+            Units unit;
+            unit.start(walk, seg);
+            auto load = [&] {
+                const uint8_t *src = p.c4 + (static_cast<long long>(seg.seq) * p.max_len + unit.row(seg) + r0) * p.ld + kR / 2;
+#pragma unroll
+                for (int i = 0; i < 2; ++i)
+                    v[i] = r0 + 32 * i < unit.rows ? ld_stream(src + 32 * i * p.ld) : make_uint4(0, 0, 0, 0);
+            };
+            if (unit.rows > 0) load();
             bool ok = true;
-            while (ok && walk.next(seg)) {
-                for (int u = 0; u < seg.units; ++u, ++un) {
-                    const uint32_t sl = un % kScaleSlots;
-                    if (un >= kScaleSlots &&
-                        !(ok = mbar_wait(bar(sh.scale_empty[sl]), (un / kScaleSlots - 1) & 1, p.err, abort_flag)))
-                        break;
-                    mbar_arrive_expect_tx(bar(sh.scale_full[sl]), kScaleTile);
-                    tma_load_3d(base + L::SCALE + sl * kScaleTile, &tm_scales, bar(sh.scale_full[sl]), kR / 2,
-                                seg.row0 + u * kRows, seg.seq);
+            for (uint32_t un = 0; unit.rows > 0; ++un) {
+                const uint32_t pb = un % kPickBufs;
+                uint32_t w[2][4];
+                int top[2];
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    w[i][0] = v[i].x, w[i][1] = v[i].y, w[i][2] = v[i].z, w[i][3] = v[i].w;
+                    top[i] = row_picks(w[i]);
+                    if (r0 + 32 * i >= unit.rows) w[i][0] = w[i][1] = w[i][2] = w[i][3] = 0;   // rows past the end: zeros
                 }
+                unit.next(walk, seg);
+                if (unit.rows > 0) load();
+                // this buffer was used two units back; its slabs were free after the products four units back, so the
+                // softmax has read what the ref slot held
+                if (un >= kPickBufs) ok &= sleep_wait(bar(sh.pick_empty[pb]), (un / kPickBufs - 1) & 1, p.err, abort_flag);
+                uint4 *const dst = reinterpret_cast<uint4 *>(smem_raw + (base - raw) + L::PICK + pb * kPicks) + r0;
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    dst[32 * i] = make_uint4(w[i][0], w[i][1], w[i][2], w[i][3]);
+                    sh.ref[un & 3][r0 + 32 * i] = static_cast<int16_t>(top[i] - 127 - 6);
+                }
+                __syncwarp();
+                if (lane == 0) mbar_arrive(bar(sh.pick_full[pb]));
             }
             if (!ok) *abort_flag = 1;
-            // no load may still be landing when the CTA exits
-            for (uint32_t k = un > kScaleSlots ? un - kScaleSlots : 0; k < un; ++k)
-                mbar_wait(bar(sh.scale_full[k % kScaleSlots]), (k / kScaleSlots) & 1, p.err);
         } else if (warp == 1 && lane == 0) {
             // ---- S^T = c . q^T: four slabs of K = 128
             constexpr uint32_t idesc = make_idesc_e4m3(128, N, 0, 0);
@@ -380,14 +457,14 @@ __global__ void __launch_bounds__(kThreads, 1)
             uint32_t it = 0, un = 0, ns = 0;
             bool ok = true;
             while (ok && walk.next(seg)) {
-                if (!(ok = mbar_wait(bar(sh.q_ready), ns++ & 1, p.err, abort_flag))) break;
+                if (!(ok = sleep_wait(bar(sh.q_ready), ns++ & 1, p.err, abort_flag))) break;
                 for (int u = 0; ok && u < seg.units; ++u, ++un) {
                     const uint32_t sb = un % kSBufs;
-                    if (un >= kSBufs && !(ok = mbar_wait(bar(sh.s_free[sb]), (un / kSBufs - 1) & 1, p.err, abort_flag)))
+                    if (un >= kSBufs && !(ok = sleep_wait(bar(sh.s_free[sb]), (un / kSBufs - 1) & 1, p.err, abort_flag)))
                         break;
                     for (int k = 0; k < 4; ++k, ++it) {
                         const uint32_t sl = it % kSlabs;
-                        if (!(ok = mbar_wait(bar(sh.slab_full[sl]), (it / kSlabs) & 1, p.err, abort_flag))) break;
+                        if (!(ok = sleep_wait(bar(sh.slab_full[sl]), (it / kSlabs) & 1, p.err, abort_flag))) break;
                         tc_fence_after();
 #pragma unroll
                         for (int kk = 0; kk < 4; ++kk)
@@ -407,11 +484,11 @@ __global__ void __launch_bounds__(kThreads, 1)
             while (ok && walk.next(seg)) {
                 for (int u = 0; ok && u < seg.units; ++u, ++un) {
                     const uint32_t pb = un % kPBufs;
-                    if (!(ok = mbar_wait(bar(sh.p_full[pb]), (un / kPBufs) & 1, p.err, abort_flag))) break;
+                    if (!(ok = sleep_wait(bar(sh.p_full[pb]), (un / kPBufs) & 1, p.err, abort_flag))) break;
                     tc_fence_after();
                     for (int t = 0; t < 4; ++t, ++it) {
                         const uint32_t sl = it % kSlabs;
-                        if (!(ok = mbar_wait(bar(sh.slab_full[sl]), (it / kSlabs) & 1, p.err, abort_flag))) break;
+                        if (!(ok = sleep_wait(bar(sh.slab_full[sl]), (it / kSlabs) & 1, p.err, abort_flag))) break;
 #pragma unroll
                         for (int kk = 0; kk < 4; ++kk)
                             umma_f8(tmem + L::O_COL + t * N, desc_add(c0, sl * kSlab + kk * 4096),
@@ -464,16 +541,14 @@ __global__ void __launch_bounds__(kThreads, 1)
 
             for (int u = 0; u < seg.units; ++u, ++un) {
                 const uint32_t sb = un % kSBufs, pb = un % kPBufs;
-                float x[HW], lo[HW];
-                ok &= mbar_wait(bar(sh.s_full[sb]), (un / kSBufs) & 1, p.err, abort_flag);
+                float x[HW], s[2 * HW];
+                ok &= sleep_wait(bar(sh.s_full[sb]), (un / kSBufs) & 1, p.err, abort_flag);
                 __syncwarp();
                 tc_fence_after();
 #pragma unroll
-                for (int g = 0; g < HW; g += 8) {
-                    tmem_ld8(lanes + L::S_COL + sb * N + g, *reinterpret_cast<float (*)[8]>(x + g));
-                    tmem_ld8(lanes + L::S_COL + sb * N + HW + g, *reinterpret_cast<float (*)[8]>(lo + g));
-                }
-                const int ref = sh.ref[un & 1][t];
+                for (int g = 0; g < 2 * HW; g += 16)
+                    tmem_ld16(lanes + L::S_COL + sb * N + g, *reinterpret_cast<float (*)[16]>(s + g));
+                const int ref = sh.ref[un & 3][t];
                 // a row past the end has an all-zero tile row: its exponents are -infinity
                 const float row_scale = exp2_int(ref),
                             row_exp = t < seg.len - seg.row0 - u * kRows ? static_cast<float>(ref) : -INFINITY;
@@ -492,7 +567,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                     for (int k = 0; k < 4; k += 2) {
                         const float2 mk = k ? make_float2(m.z, m.w) : make_float2(m.x, m.y);
                         const float2 bk = k ? make_float2(bi.z, bi.w) : make_float2(bi.x, bi.y);
-                        const float2 s2 = fma2(make_float2(lo[h + k], lo[h + k + 1]), part_lo, make_float2(x[h + k], x[h + k + 1]));
+                        const float2 s2 = fma2(make_float2(s[2 * (h + k) + 2], s[2 * (h + k) + 3]), part_lo,
+                                               make_float2(s[2 * (h + k)], s[2 * (h + k) + 1]));
                         const float2 v = fma2(s2, mul2(mk, rs), add2(bk, re));
                         x[h + k] = v.x, x[h + k + 1] = v.y;
                         top = fmaxf(fmaxf(top, v.x), v.y);
@@ -532,19 +608,22 @@ __global__ void __launch_bounds__(kThreads, 1)
                             l[h] *= g.x, l[h + 1] *= g.y, l[h + 2] *= g.z, l[h + 3] *= g.w;
                         }
                         // the products of the unit before are complete before O^T is scaled
-                        ok &= mbar_wait(bar(sh.p_free[(un - 1) % kPBufs]), ((un - 1) / kPBufs) & 1, p.err, abort_flag);
+                        ok &= sleep_wait(bar(sh.p_free[(un - 1) % kPBufs]), ((un - 1) / kPBufs) & 1, p.err, abort_flag);
                         __syncwarp();
                         tc_fence_after();
                         for (; moved; moved &= moved - 1) {
                             const int h = __ffs(moved) - 1;
                             const float g = fac[h];
-                            float o[8];   // hi and lo columns of the four latent tiles
+                            const float g0 = h & 1 ? 1.f : g, g1 = h & 1 ? g : 1.f;
+                            float o[4][4];   // the pair's columns of the four latent tiles
 #pragma unroll
-                            for (int c = 0; c < 8; ++c) tmem_ld1(lanes + L::O_COL + (c >> 1) * N + (c & 1) * HW + h, o[c]);
+                            for (int c = 0; c < 4; ++c) tmem_ld4(lanes + L::O_COL + c * N + 2 * (h & ~1), o[c]);
                             tmem_wait_ld();
 #pragma unroll
-                            for (int c = 0; c < 8; ++c)
-                                tmem_st1(lanes + L::O_COL + (c >> 1) * N + (c & 1) * HW + h, o[c] * g);
+                            for (int c = 0; c < 4; ++c) {
+                                o[c][0] *= g0, o[c][1] *= g1, o[c][2] *= g0, o[c][3] *= g1;
+                                tmem_st4(lanes + L::O_COL + c * N + 2 * (h & ~1), o[c]);
+                            }
                         }
                         tmem_wait_st();
                         tc_fence_before();
@@ -552,7 +631,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
                 // weights, their sums, and P^T as the MN-major N side: row t, 2 HW bytes of this warpgroup
                 const float2 unref = make_float2(exp2_int(-ref), exp2_int(-ref));
-                uint32_t w[HW / 2];   // HW / 4 words of hi bytes, then of lo bytes
+                uint32_t w[HW / 2];
 #pragma unroll
                 for (int h = 0; h < HW; h += 4) {
                     const float2 p01 = make_float2(fast_exp2(x[h]), fast_exp2(x[h + 1]));
@@ -560,11 +639,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                     const float2 l01 = fma2(p01, unref, make_float2(l[h], l[h + 1]));
                     const float2 l23 = fma2(p23, unref, make_float2(l[h + 2], l[h + 3]));
                     l[h] = l01.x, l[h + 1] = l01.y, l[h + 2] = l23.x, l[h + 3] = l23.y;
-                    const uint32_t y = split16_e4m3x2(p01.x, p01.y), z = split16_e4m3x2(p23.x, p23.y);
-                    w[h / 4] = byte_perm(y, z, 0x5410);
-                    w[HW / 4 + h / 4] = byte_perm(y, z, 0x7632);
+                    w[h / 2] = split16_e4m3x2(p01.x, p01.y);
+                    w[h / 2 + 1] = split16_e4m3x2(p23.x, p23.y);
                 }
-                if (un >= kPBufs) ok &= mbar_wait(bar(sh.p_free[pb]), (un / kPBufs - 1) & 1, p.err, abort_flag);
+                if (un >= kPBufs) ok &= sleep_wait(bar(sh.p_free[pb]), (un / kPBufs - 1) & 1, p.err, abort_flag);
                 const uint32_t prow = base + L::P + pb * kSlab;
 #pragma unroll
                 for (int i = 0; i < HW / 8; ++i)
@@ -582,7 +660,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (lane == h) part[h] = s;
             }
             const uint32_t last = un - 1;
-            ok &= mbar_wait(bar(sh.p_free[last % kPBufs]), (last / kPBufs) & 1, p.err, abort_flag);
+            ok &= sleep_wait(bar(sh.p_free[last % kPBufs]), (last / kPBufs) & 1, p.err, abort_flag);
             named_bar_sync(id, 128);
             tc_fence_after();
             const size_t slot = static_cast<size_t>(seg.slot) * p.H + h0 + wg * HW;
@@ -594,14 +672,15 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll 1
             for (int c = 0; c < 4 * (HW / 8); ++c) {
                 const int tile = c / (HW / 8), g = c % (HW / 8) * 8;
-                float hi[8], lw[8];
-                tmem_ld8(lanes + L::O_COL + tile * N + g, hi);
-                tmem_ld8(lanes + L::O_COL + tile * N + HW + g, lw);
+                float o[16];
+                tmem_ld16(lanes + L::O_COL + tile * N + 2 * g, o);
                 tmem_wait_ld();
                 float *dst = p.ws_o + (slot + g) * kR + tile * 128 + t;
 #pragma unroll
-                for (int k = 0; k < 8; ++k)
-                    if (g + k < mine) dst[static_cast<size_t>(k) * kR] = fmaf(lw[k], kLoPart, hi[k]);
+                for (int k = 0; k < 8; ++k) {
+                    const int at = 2 * (k & ~1) + (k & 1);
+                    if (g + k < mine) dst[static_cast<size_t>(k) * kR] = fmaf(o[at + 2], kLoPart, o[at]);
+                }
             }
             tc_fence_before();
             named_bar_sync(id, 128);   // part and mul are read before the next segment sets them
@@ -611,58 +690,39 @@ __global__ void __launch_bounds__(kThreads, 1)
     } else {
         regs_release<kRegsExp>();
         // ---- expansion: a warp takes half of the rows of one of a unit's four slabs, a lane the groups (32 codes) `g` of
-        // rows r + 8 i.  A lane's codes of the next unit are loaded as those of this one are used: 32 KB in flight per SM
+        // rows r + 8 i.  A lane loads its codes a unit ahead: 32 KB in flight per SM
         const int k = (warp - 12) & 3, half = (warp - 12) >> 2, g = lane & 3, r = half * 64 + (lane >> 2);
         uint8_t *const smem = smem_raw + (base - raw);
         const long long step8 = 8 * p.ld;
-        const uint8_t *next = nullptr;   // this lane's codes of row r of the next unit
-        int nu = 0, nrows = 0;           // the next unit's number in its segment, and its rows
-        auto find = [&] {
-            if (nrows > 0 && nu < seg.units) {
-                next += kRows * p.ld;
-            } else if (walk.next(seg)) {
-                nu = 0;
-                next = p.c4 + (static_cast<long long>(seg.seq) * p.max_len + seg.row0 + r) * p.ld + k * 64 + g * 16;
-            } else {
-                nrows = 0;
-                return;
-            }
-            nrows = seg.len - seg.row0 - nu * kRows;
-            ++nu;
-        };
+        const int x = ((2 * g) ^ (lane >> 2)) * 16;   // row & 7 = lane >> 2: the swizzle of the group's first 16 bytes
+        const uint32_t slab_at = L::C + sw128_offset(r, 0) - (lane >> 2) * 16, pick_at = L::PICK + r * 16 + k * 4 + g;
         uint4 v[8];
-        find();
+        Units unit;
+        unit.start(walk, seg);
+        auto load = [&] {
+            const uint8_t *src =
+                p.c4 + (static_cast<long long>(seg.seq) * p.max_len + unit.row(seg) + r) * p.ld + k * 64 + g * 16;
+            if (unit.rows == kRows) {
 #pragma unroll
-        for (int i = 0; i < 8; ++i) v[i] = r + 8 * i < nrows ? ld_stream(next + i * step8) : make_uint4(0, 0, 0, 0);
-        bool ok = true;
-        for (uint32_t it = k, un = 0; nrows > 0; it += 4, ++un) {
-            const int rows = nrows;
-            find();
-            const uint32_t sc = un % kScaleSlots, sl = it % kSlabs;
-            const uint8_t *const tile = smem + L::SCALE + sc * kScaleTile;
-            ok &= mbar_wait(bar(sh.scale_full[sc]), (un / kScaleSlots) & 1, p.err, abort_flag);
-            // the largest scale exponent of rows 64 half + lane and + 32 (NaN bytes aside) becomes e4m3's 2^6
-            int top[2];
+                for (int i = 0; i < 8; ++i) v[i] = ld_stream(src + i * step8);
+            } else {   // (what the lane holds for rows past the end goes with a table of zeros)
 #pragma unroll
-            for (int i = 0; i < 2; ++i) top[i] = row_top(tile + (half * 64 + i * 32 + lane) * 16);
-            // (the unit's first slab is free once the products two units back are done, so the softmax has read what the
-            // ref slot held)
-            if (it >= kSlabs) ok &= mbar_wait(bar(sh.slab_free[sl]), (it / kSlabs - 1) & 1, p.err, abort_flag);
-            if (k == 0) {
-                sh.ref[un & 1][half * 64 + lane] = static_cast<int16_t>(top[0] - 127 - 6);
-                sh.ref[un & 1][half * 64 + 32 + lane] = static_cast<int16_t>(top[1] - 127 - 6);
+                for (int i = 0; i < 8; ++i)
+                    if (r + 8 * i < unit.rows) v[i] = ld_stream(src + i * step8);
             }
-            uint8_t *const slab = smem + L::C + sl * kSlab + sw128_offset(r, 0) - (lane >> 2) * 16;
-            const int x = ((2 * g) ^ (lane >> 2)) * 16;   // row & 7 = lane >> 2: the swizzle of the group's first 16 bytes
+        };
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[i] = make_uint4(0, 0, 0, 0);
+        if (unit.rows > 0) load();
+        bool ok = true;
+        for (uint32_t it = k, un = 0; unit.rows > 0; it += 4, ++un) {
+            const uint32_t pb = un % kPickBufs, sl = it % kSlabs;
+            ok &= sleep_wait(bar(sh.pick_full[pb]), (un / kPickBufs) & 1, p.err, abort_flag);
             uint2 tb[8];   // all read before the first store
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                const int X = tile[(r + 8 * i) * 16 + k * 4 + g];
-                const int t = __shfl_sync(0xffffffffu, top[i / 4], (lane >> 2) + 8 * (i & 3));
-                int at = X == kFp4ScaleNan ? kTables - 1 : max(min(max(X, kFp4ScaleMin), kFp4ScaleMax) - t + 20, 0);
-                if (r + 8 * i >= rows) at = 0;   // rows past the end: zeros
-                tb[i] = sh.table[at];
-            }
+            for (int i = 0; i < 8; ++i) tb[i] = sh.table[smem[pick_at + pb * kPicks + i * 128]];
+            if (it >= kSlabs) ok &= sleep_wait(bar(sh.slab_free[sl]), (it / kSlabs - 1) & 1, p.err, abort_flag);
+            uint8_t *const slab = smem + slab_at + sl * kSlab;
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
                 uint32_t o[8];
@@ -677,12 +737,10 @@ __global__ void __launch_bounds__(kThreads, 1)
             __syncwarp();
             if (lane == 0) {
                 mbar_arrive(bar(sh.slab_full[sl]));
-                mbar_arrive(bar(sh.scale_empty[sc]));
+                mbar_arrive(bar(sh.pick_empty[pb]));
             }
-            // (after the fence, which would wait for them)
-#pragma unroll
-            for (int i = 0; i < 8; ++i)
-                v[i] = r + 8 * i < nrows ? ld_stream(next + i * step8) : make_uint4(0, 0, 0, 0);
+            unit.next(walk, seg);
+            if (unit.rows > 0) load();   // after the fence, which would wait for it
         }
         if (!ok) *abort_flag = 1;
     }
@@ -948,7 +1006,7 @@ size_t slot_count(int B, int max_len, int G) {
 }
 
 template <int HP>
-cudaError_t launch_attention(const CUtensorMap &scales, const Fp4Params &p, cudaStream_t s) {
+cudaError_t launch_attention(const Fp4Params &p, cudaStream_t s) {
     using L = Fp4Layout<HP>;
     cudaError_t e = cudaFuncSetAttribute(fp4_attention_kernel<HP>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                          static_cast<int>(L::kSmem));
@@ -957,7 +1015,7 @@ cudaError_t launch_attention(const CUtensorMap &scales, const Fp4Params &p, cuda
     if ((e = cudaFuncGetAttributes(&fa, fp4_attention_kernel<HP>)) != cudaSuccess) return e;
     if (fa.numRegs != static_cast<int>(kRegsLaunch)) return cudaErrorInvalidConfiguration;
     note_launch();
-    fp4_attention_kernel<HP><<<p.G * p.groups, kThreads, L::kSmem, s>>>(scales, p);
+    fp4_attention_kernel<HP><<<p.G * p.groups, kThreads, L::kSmem, s>>>(p);
     return cudaGetLastError();
 }
 
@@ -987,24 +1045,18 @@ cudaError_t launch_decode_fp4(const DecodeArgs &a, cudaStream_t s) {
     p.ws_l = p.ws_m + slots * a.H;
     p.err = a.dev_err;
     p.scale_log2 = a.scale * kLog2e;
-    CUtensorMap tm_scales, tm_wuv;
+    CUtensorMap tm_wuv;
     {
-        const cuuint64_t rows = static_cast<cuuint64_t>(a.max_len > 0 ? a.max_len : 1);
-        const cuuint64_t dims[3] = {kR / 2 + kR / 32, rows, static_cast<cuuint64_t>(a.B)};
-        const cuuint64_t strides[2] = {static_cast<cuuint64_t>(a.ld_cache), rows * static_cast<cuuint64_t>(a.ld_cache)};
-        const cuuint32_t box[3] = {16, kRows, 1};
-        const cuuint64_t wd[2] = {kR, static_cast<cuuint64_t>(a.H) * kDV}, ws[1] = {kR * 2};
-        const cuuint32_t wb[2] = {64, kDV};
-        if (encode_map(&tm_scales, CU_TENSOR_MAP_DATA_TYPE_UINT8, CU_TENSOR_MAP_SWIZZLE_NONE, a.c_cache, 3, dims, strides,
-                       box) != CUDA_SUCCESS ||
-            encode_map(&tm_wuv, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, CU_TENSOR_MAP_SWIZZLE_128B, a.w_uv, 2, wd, ws, wb) !=
-                CUDA_SUCCESS)
+        const cuuint64_t dims[2] = {kR, static_cast<cuuint64_t>(a.H) * kDV}, strides[1] = {kR * 2};
+        const cuuint32_t box[2] = {64, kDV};
+        if (encode_map(&tm_wuv, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, CU_TENSOR_MAP_SWIZZLE_128B, a.w_uv, 2, dims, strides, box) !=
+            CUDA_SUCCESS)
             return cudaErrorInvalidValue;
     }
     const int hp = p.heads_per_group;
-    cudaError_t e = hp <= 16   ? launch_attention<16>(tm_scales, p, s)
-                    : hp <= 32 ? launch_attention<32>(tm_scales, p, s)
-                               : launch_attention<48>(tm_scales, p, s);
+    cudaError_t e = hp <= 16   ? launch_attention<16>(p, s)
+                    : hp <= 32 ? launch_attention<32>(p, s)
+                               : launch_attention<48>(p, s);
     if (e != cudaSuccess) return e;
     e = cudaFuncSetAttribute(fp4_merge_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(kSmemMerge));
     if (e != cudaSuccess) return e;
