@@ -5,28 +5,30 @@
 // "完整计算流（四步）" of the page "Gated MLA（矩阵吸收版）" follow: scores against c itself, softmax, the latent
 // weighting by c itself, W_UV^T, gate.
 //
-// Attention kernel (persistent, one CTA per SM).  A CTA takes up to 48 heads (two groups above that) and a contiguous
-// share of all sequences' rows, in units of 128 rows, and computes both products with the rows' side as M:
+// Attention kernel (persistent, one CTA per SM).  A CTA takes all heads and a contiguous share of all sequences' rows, in
+// units of 128 rows, and computes both products with the rows' side as M:
 //   S^T [128 rows x heads]       = c . q_abs^T     A = c as stored, K-major       (K = r)
 //   O^T [128 latent x heads] x 4 += c^T . P^T      A = the same tile, MN-major    (K = rows)
-// so a unit is expanded once, to e4m3 in shared memory, for both, heads are never padded to 128, and O^T (fp32) leaves
-// room in tensor memory for S^T.  An e2m1 value times its group's power of two is exact in e4m3 relative to its row's
-// largest scale (14 binades down; smaller groups are rounded at 2^-18 of the row's largest value), so the tile is the
-// row divided by a power of two, `ref`, that goes into the softmax's exponent.  q_abs and P are split into e4m3 hi and
-// lo parts (lo = the rest times 16: 8 bits), side by side as 2 x heads columns of the N side: one pass over the tile
-// serves both parts, which the fp32 epilogues join.
+// so a unit is expanded once, to e4m3 in shared memory, for both, heads are not padded to 128, and O^T (fp32) leaves room
+// in tensor memory for S^T.  An e2m1 value times its group's power of two is exact in e4m3 relative to its row's largest
+// scale (14 binades down; smaller groups are rounded at 2^-18 of the row's largest value), so the tile is the row divided
+// by a power of two, `ref`, that goes into the softmax's exponent.  q_abs and P are split into two 8-bit parts:
+//   up to 48 heads   e4m3 hi and lo = e4m3(16 x rest), side by side as 2 x heads columns of the N side: one pass over the
+//                    tile serves both parts, which the fp32 epilogues join
+//   above            the two parts' products go into the same accumulators, as 2 x heads columns would not fit tensor
+//                    memory: unscaled, q_abs's lo in e4m3 (a bf16 query is exact), P's in e5m2 for its range
 //
 // Softmax of one unit: thread = row, so every head's statistics lie across lanes.  With a = score * log2 e + ref,
 //   P = 2^(a - M + 8), l += P * 2^-ref,   M[head] >= running max of a - 0.75
 // M moves only when some row exceeds it by more than 0.75 (P <= 2^8.75 = 430, inside e4m3's 448), then to one above
-// that row: a barrier with an OR tells whether any does, and only then are the maxima of those heads taken across
-// lanes and their columns of O^T rescaled.  A weight below 2^-22 of the largest is lost; sequences are cut into chunks
-// of 32768 rows with maxima of their own, so less than 2^-7 of a chunk's weight can go that way.
+// that row: a barrier with an OR tells whether any does, and only then are the maxima taken across lanes and the moved
+// heads' columns of O^T rescaled.  A weight below 2^-22 of the largest is lost; sequences are cut into chunks of 32768
+// rows with maxima of their own, so less than 2^-7 of a chunk's weight can go that way.
 //
-// Warps: 0 and 3 turn scale bytes into table numbers, 1 issues S, 2 issues O, 4-11 softmax (and q_abs, rescale, drain; half of the heads to each of two
-// warpgroups that never wait for one another), 12-19 expand.  The expansion is a byte
-// permute per four codes: the group's exponent selects an 8-byte table of e4m3 magnitudes, the codes' three magnitude
-// bits are the selector.
+// Warps: 0 turns scale bytes into table numbers, 1 issues S, 2 issues O, 3 loads codes (TMA); two (above 48 heads: four) softmax
+// warpgroups, each with its share of the heads, that never wait for one another (also q_abs, rescale and drain); two
+// (one) warpgroups expand.  The expansion is a byte permute per four codes: the group's exponent selects an 8-byte table
+// of e4m3 magnitudes, the codes' three magnitude bits are the selector.
 //
 // Merge kernel: a CTA per (head, 32 sequences) joins the segments of a sequence with the log-sum-exp rule, splits
 // o_lat into bf16 hi + lo and multiplies by W_UV^T on the tensor cores (W_UV as the M side), then the gate.
@@ -45,52 +47,60 @@ constexpr int kRows = 128;                 // cache rows per unit
 constexpr int kChunkUnits = 256;           // units of a sequence that share one running maximum per segment
 constexpr int kChunkRows = kChunkUnits * kRows;
 constexpr int kOverUnits = 2;              // what starting a segment costs, in units (query, first fill, drain)
-constexpr int kThreads = 640;               // warps 0-3 control, 4-11 softmax, 12-19 expansion
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kBias = 8.f;               // P = 2^(a - M + kBias)
 constexpr float kHead = 1.f, kSlack = 0.75f;   // a new maximum is set kHead above the row that forced it
-// Register split of the 5 warpgroups x 96 launched: control, 2 x softmax, 2 x expansion.
-constexpr uint32_t kRegsCtl = 80, kRegsSoft = 104, kRegsExp = 96, kRegsLaunch = 96;
-static_assert(kRegsCtl + 2 * kRegsSoft + 2 * kRegsExp <= 5 * kRegsLaunch, "register split exceeds the launch");
-
 constexpr uint32_t kSlab = 16384;          // [128 rows x 128 latent] e4m3, 128-byte swizzle
 constexpr uint32_t kPicks = 2048;          // [128 rows x 16 groups] table numbers of a unit
-constexpr int kPickBufs = 2, kPBufs = 2, kSlabs = 8;   // slabs: expanded tiles in flight, two units
-constexpr uint32_t kSharedBytes = 5120;    // Fp4Shared
+constexpr uint32_t kStage = 8192;          // codes of one slab: [128 rows x 64 bytes]
+constexpr int kPickBufs = 2;
 constexpr int kTables = 22;                // exponents -14 (all zero) .. 6 below the row's largest, then NaN
-
-// Heads of a CTA are padded to HP and shared by two softmax warpgroups of HW each.  Columns of the N side: the two hi
-// parts of a pair of heads, then their lo parts.
-template <int HP>
-struct Fp4Layout {
-    static constexpr int HW = HP / 2, N = 2 * HP;
-    static constexpr int kSBufs = HP == 48 ? 1 : 2;
-    static constexpr uint32_t kQSlab = N * 128;                        // [N x 128 latent] e4m3
-    static constexpr uint32_t Q = 0, C = Q + 4 * kQSlab, P = C + kSlabs * kSlab, PICK = P + kPBufs * kSlab,
-                              END = PICK + kPickBufs * kPicks;
-    static constexpr uint32_t kSmem = END + kSharedBytes + 1024;               // + Fp4Shared + alignment slack
-    static constexpr uint32_t S_COL = 0, O_COL = 128;                  // TMEM columns
-    static_assert(kQSlab % 1024 == 0 && O_COL + 4 * N <= 512 && kSBufs * N <= O_COL && HW % 8 == 0, "layout");
-    static_assert(kSmem <= 232448, "attention kernel exceeds shared memory");
-};
+constexpr int kMaxSoftWarps = 16, kMaxHW = 24;
 
 struct Fp4Shared {
+    uint64_t stage_full[4], stage_empty[4];
     uint64_t pick_full[kPickBufs], pick_empty[kPickBufs];
-    uint64_t slab_full[kSlabs], slab_free[kSlabs];
+    uint64_t slab_full[8], slab_free[8];
     uint64_t s_full[2], s_free[2], q_ready;
-    uint64_t p_full[kPBufs], p_free[kPBufs];
+    uint64_t p_full[2], p_free[2];
     uint32_t tmem_base;
     int abort;
-    uint32_t pad_[2];
     uint2 table[kTables];
-    int16_t ref[4][kRows];                 // per row of the last four units: the power of two its tile is divided by
-    alignas(16) float mul[48];             // per head: score factor
+    int16_t ref[8][kRows];                 // per row of the last eight units: the power of two its tile is divided by
+    alignas(16) float mul[96];             // per head: score factor
     // per softmax warp and head, the same in a warpgroup's four: kBias - M, and the last change of it with its power of
     // two (part: the warps' maxima, and their parts of l while a segment is drained)
-    alignas(16) float bias[8][24], step[8][24], fac[8][24];
-    float part[8][24];
+    alignas(16) float bias[kMaxSoftWarps][kMaxHW], step[kMaxSoftWarps][kMaxHW], fac[kMaxSoftWarps][kMaxHW];
+    float part[kMaxSoftWarps][kMaxHW];
 };
-static_assert(sizeof(Fp4Shared) <= kSharedBytes, "shared block too large");
+
+// Heads are padded to HP and shared by the softmax warpgroups, HW each.  kJoin: hi and lo parts have columns of their own,
+// per pair of heads the two hi parts, then the two lo parts; else head h is column h of both.
+template <int HP>
+struct Fp4Layout {
+    static constexpr bool kJoin = HP <= 48;
+    static constexpr int kSoftGroups = kJoin ? 2 : 4, kExpGroups = kJoin ? 2 : 1, kGroups = 1 + kSoftGroups + kExpGroups;
+    static constexpr int kThreads = 128 * kGroups, HW = HP / kSoftGroups, N = kJoin ? 2 * HP : HP;   // N: columns of an MMA
+    static constexpr int WC = N / kSoftGroups;                          // columns of a warpgroup
+    static constexpr int kExpRows = kJoin ? 16 : 32;                    // rows that an expanding warp takes
+    // expanded tiles in flight (four per unit), and what the rest of shared memory holds of codes
+    static constexpr int kSlabs = HP == 96 ? 4 : (HP == 64 ? 6 : (HP == 48 ? 7 : 8)), kStages = HP == 16 ? 4 : 2;
+    static constexpr int kPBufs = kJoin ? 2 : 1, kSBufs = 2 * N <= 128 ? 2 : 1;
+    static constexpr uint32_t kQPart = HP * 128, kQSlab = 2 * kQPart;   // [hi | lo rows x 128 latent]; kJoin: interleaved
+    static constexpr uint32_t kPPart = kRows * 128, kPBuf = kJoin ? kPPart : 2 * kPPart;
+    static constexpr uint32_t Q = 0, C = Q + 4 * kQSlab, P = C + kSlabs * kSlab, STAGE = P + kPBufs * kPBuf,
+                              PICK = STAGE + kStages * kStage, END = PICK + kPickBufs * kPicks;
+    static constexpr uint32_t kSmem = END + sizeof(Fp4Shared) + 1024;   // + alignment slack
+    static constexpr uint32_t S_COL = 0, O_COL = 128;                   // TMEM columns
+    // Register split of the warpgroups: control, softmax, expansion.
+    static constexpr uint32_t kRegsLaunch = kJoin ? 96 : 80, kRegsCtl = kJoin ? 80 : 72, kRegsSoft = kJoin ? 104 : 88,
+                              kRegsExp = kJoin ? 96 : 56;
+    static_assert(kRegsCtl + kSoftGroups * kRegsSoft + kExpGroups * kRegsExp <= kGroups * kRegsLaunch,
+                  "register split exceeds the launch");
+    static_assert(kQPart % 1024 == 0 && O_COL + 4 * N <= 512 && kSBufs * N <= O_COL && N <= 128, "layout");
+    static_assert(HW % 8 == 0 && HW <= kMaxHW && 4 * kSoftGroups <= kMaxSoftWarps, "layout");
+    static_assert(kSlabs <= 8 && kSlabs >= 4 && END % 16 == 0 && kSmem <= 232448, "shared memory");
+};
 
 struct Fp4Params {
     const __nv_bfloat16 *q_abs;
@@ -99,7 +109,7 @@ struct Fp4Params {
     const int *lens;
     float *ws_o, *ws_m, *ws_l;   // [slots][H] (x r): sum of P c, M - kBias, l
     int *err;
-    int B, H, max_len, G, groups, heads_per_group;
+    int B, H, max_len, G;
     float scale_log2;
 };
 
@@ -222,6 +232,13 @@ __device__ __forceinline__ uint32_t split16_e4m3x2(float a, float b) {
     return hi | (f16x2_to_e4m3x2(mul_f16x2(rest, 0x4C004C00u)) << 16);   // f16 16.0
 }
 constexpr float kLoPart = 0.0625f;
+// (a, b) as e4m3 hi (bits 0-15) and e5m2 lo (bits 16-31): lo = e5m2(x - hi).
+__device__ __forceinline__ uint32_t split_e4m3_e5m2x2(float a, float b) {
+    const uint32_t hi = cvt_e4m3x2(a, b);
+    uint16_t lo;
+    asm("cvt.rn.satfinite.e5m2x2.f16x2 %0, %1;" : "=h"(lo) : "r"(sub_f16x2(pack_f16x2(a, b), e4m3x2_to_f16x2(hi))));
+    return hi | static_cast<uint32_t>(lo) << 16;
+}
 __device__ __forceinline__ uint32_t byte_perm(uint32_t a, uint32_t b, uint32_t sel) {
     uint32_t r;
     asm("prmt.b32 %0, %1, %2, %3;" : "=r"(r) : "r"(a), "r"(b), "r"(sel));
@@ -312,13 +329,12 @@ __device__ __forceinline__ float warp_max(float v) {
 }
 __device__ __forceinline__ float4 lds4(const float *p) { return *reinterpret_cast<const float4 *>(p); }
 
-// N-side row of head h's hi part; its lo part is two further.
-__device__ __forceinline__ int hi_row(int h) { return 2 * (h & ~1) + (h & 1); }
 // One head's query into the N side of S, lane j the latent elements 16j .. 16j + 15.
 // Scaled by a power of two that brings its largest magnitude into [128, 256); returns the factor that undoes it (NaN
 // for a query that holds a NaN or an infinity).
 template <int HP>
 __device__ __forceinline__ float store_query(uint32_t q_base, int h, int lane, const uint4 (&v)[2]) {
+    using L = Fp4Layout<HP>;
     const uint32_t w[8] = {v[0].x, v[0].y, v[0].z, v[0].w, v[1].x, v[1].y, v[1].z, v[1].w};
     uint32_t top = 0;
 #pragma unroll
@@ -329,60 +345,59 @@ __device__ __forceinline__ float store_query(uint32_t q_base, int h, int lane, c
     uint32_t hw[4], lw[4];
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
-        const uint32_t a = split16_e4m3x2(__uint_as_float(w[2 * k] << 16) * up, __uint_as_float(w[2 * k] & 0xFFFF0000u) * up);
-        const uint32_t b =
-            split16_e4m3x2(__uint_as_float(w[2 * k + 1] << 16) * up, __uint_as_float(w[2 * k + 1] & 0xFFFF0000u) * up);
+        const float x0 = __uint_as_float(w[2 * k] << 16) * up, x1 = __uint_as_float(w[2 * k] & 0xFFFF0000u) * up;
+        const float x2 = __uint_as_float(w[2 * k + 1] << 16) * up, x3 = __uint_as_float(w[2 * k + 1] & 0xFFFF0000u) * up;
+        const uint32_t a = L::kJoin ? split16_e4m3x2(x0, x1) : split_e4m3x2(x0, x1);
+        const uint32_t b = L::kJoin ? split16_e4m3x2(x2, x3) : split_e4m3x2(x2, x3);
         hw[k] = byte_perm(a, b, 0x5410);
         lw[k] = byte_perm(a, b, 0x7632);
     }
-    const uint32_t slab = q_base + (lane >> 3) * Fp4Layout<HP>::kQSlab;
-    st_shared_v4(slab + sw128_offset(hi_row(h), lane & 7), hw[0], hw[1], hw[2], hw[3]);
-    st_shared_v4(slab + sw128_offset(hi_row(h) + 2, lane & 7), lw[0], lw[1], lw[2], lw[3]);
+    const uint32_t slab = q_base + (lane >> 3) * L::kQSlab;
+    const int row = L::kJoin ? 2 * (h & ~1) + (h & 1) : h;
+    st_shared_v4(slab + sw128_offset(row, lane & 7), hw[0], hw[1], hw[2], hw[3]);
+    st_shared_v4(slab + sw128_offset(row + (L::kJoin ? 2 : HP), lane & 7), lw[0], lw[1], lw[2], lw[3]);
     return top >= 0x7F800000u ? __uint_as_float(0x7FFFFFFFu) : exp2_int(-e);
 }
 
-// mbar_wait whose tries sleep (up to 2 us each) instead of polling: 20 warps share the schedulers here.
-__device__ __forceinline__ bool sleep_wait(uint32_t bar, uint32_t parity, int *err, const volatile int *abort = nullptr) {
-    const uint64_t t0 = globaltimer_ns();
-    for (;;) {
-        uint32_t ok;
-        asm volatile(
-            "{\n\t.reg .pred p;\n\t"
-            "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\t"
-            "selp.u32 %0, 1, 0, p;\n\t}"
-            : "=r"(ok)
-            : "r"(bar), "r"(parity), "r"(2000u)
-            : "memory");
-        if (ok) return true;
+// mbar_wait that looks at the clock only every 256 tries.
+__device__ __forceinline__ bool wait_bar(uint32_t bar, uint32_t parity, int *err, const volatile int *abort = nullptr) {
+    uint64_t t0 = 0;
+    for (uint32_t i = 1; !mbar_try_wait(bar, parity); ++i) {
+        if ((i & 255u) != 0) continue;
         if (abort && *abort) return false;
-        if (globaltimer_ns() - t0 > MLA_WAIT_LIMIT_NS) {
+        const uint64_t now = globaltimer_ns();
+        if (t0 == 0) t0 = now;
+        if (now - t0 > MLA_WAIT_LIMIT_NS) {
             record_error(err, kDevErrTimeout);
             return false;
         }
     }
+    return true;
 }
 
 // ------------------------------------------------------------------ attention
 template <int HP>
-__global__ void __launch_bounds__(kThreads, 1)
-    fp4_attention_kernel(const Fp4Params p) {
+__global__ void __launch_bounds__(Fp4Layout<HP>::kThreads, 1) 
+    fp4_attention_kernel(const __grid_constant__ CUtensorMap tm_codes, const Fp4Params p) {
     using L = Fp4Layout<HP>;
-    constexpr int HW = L::HW, N = L::N, kSBufs = L::kSBufs;
+    constexpr bool kJoin = L::kJoin;
+    constexpr int HW = L::HW, N = L::N, WC = L::WC, kSlabs = L::kSlabs, kPBufs = L::kPBufs, kSBufs = L::kSBufs, kStages = L::kStages;
+    constexpr int kSoftWarps = 4 * L::kSoftGroups, kExpWarps = 4 * L::kExpGroups;
     extern __shared__ uint8_t smem_raw[];
     const uint32_t raw = smem_u32(smem_raw), base = (raw + 1023u) & ~1023u;
-    Fp4Shared &sh = *reinterpret_cast<Fp4Shared *>(smem_raw + (base - raw) + L::END);
+    uint8_t *const smem = smem_raw + (base - raw);
+    Fp4Shared &sh = *reinterpret_cast<Fp4Shared *>(smem + L::END);
     volatile int *abort_flag = &sh.abort;
     auto bar = [](uint64_t &b) { return smem_u32(&b); };
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int group = static_cast<int>(blockIdx.x) % p.groups, share = static_cast<int>(blockIdx.x) / p.groups;
-    const int h0 = group * p.heads_per_group, heads = min(p.heads_per_group, p.H - h0);
 
     if (threadIdx.x == 0) {
-        for (int i = 0; i < kPickBufs; ++i) mbar_init(bar(sh.pick_full[i]), 2), mbar_init(bar(sh.pick_empty[i]), 8);
-        for (int i = 0; i < kSlabs; ++i) mbar_init(bar(sh.slab_full[i]), 2), mbar_init(bar(sh.slab_free[i]), 1);
-        for (int i = 0; i < kSBufs; ++i) mbar_init(bar(sh.s_full[i]), 1), mbar_init(bar(sh.s_free[i]), 8);
-        for (int i = 0; i < kPBufs; ++i) mbar_init(bar(sh.p_full[i]), 8), mbar_init(bar(sh.p_free[i]), 1);
-        mbar_init(bar(sh.q_ready), 8);
+        for (int i = 0; i < kStages; ++i) mbar_init(bar(sh.stage_full[i]), 1), mbar_init(bar(sh.stage_empty[i]), kExpWarps);
+        for (int i = 0; i < kPickBufs; ++i) mbar_init(bar(sh.pick_full[i]), 1), mbar_init(bar(sh.pick_empty[i]), kExpWarps);
+        for (int i = 0; i < kSlabs; ++i) mbar_init(bar(sh.slab_full[i]), kExpWarps), mbar_init(bar(sh.slab_free[i]), 1);
+        for (int i = 0; i < kSBufs; ++i) mbar_init(bar(sh.s_full[i]), 1), mbar_init(bar(sh.s_free[i]), kSoftWarps);
+        for (int i = 0; i < kPBufs; ++i) mbar_init(bar(sh.p_full[i]), kSoftWarps), mbar_init(bar(sh.p_free[i]), 1);
+        mbar_init(bar(sh.q_ready), kSoftWarps);
         sh.abort = 0;
         fence_mbar_init();
     }
@@ -406,50 +421,71 @@ __global__ void __launch_bounds__(kThreads, 1)
     grid_launch_dependents();   // the merge takes SMs as CTAs finish; it waits for the whole grid
 
     Walk walk;
-    walk.start(p, share, lane, blockIdx.x == 0 && warp == 0 ? p.err : nullptr);
+    walk.start(p, blockIdx.x, lane, blockIdx.x == 0 && warp == 0 ? p.err : nullptr);
     Segment seg;
 
     if (warp < 4) {
-        regs_release<kRegsCtl>();
-        if (warp == 0 || warp == 3) {
-            // ---- scale bytes to table numbers and refs, a unit or two ahead: a lane takes rows r0 and r0 + 32
-            const int r0 = (warp == 3 ? 64 : 0) + lane;
-            uint4 v[2];
+        regs_release<L::kRegsCtl>();
+        if (warp == 0) {
+            // ---- scale bytes to table numbers and refs, a unit or two ahead: a lane takes rows lane + 32 i
+            uint4 v[4];
             Units unit;
             unit.start(walk, seg);
             auto load = [&] {
-                const uint8_t *src = p.c4 + (static_cast<long long>(seg.seq) * p.max_len + unit.row(seg) + r0) * p.ld + kR / 2;
+                const uint8_t *src = p.c4 + (static_cast<long long>(seg.seq) * p.max_len + unit.row(seg) + lane) * p.ld + kR / 2;
 #pragma unroll
-                for (int i = 0; i < 2; ++i)
-                    v[i] = r0 + 32 * i < unit.rows ? ld_stream(src + 32 * i * p.ld) : make_uint4(0, 0, 0, 0);
+                for (int i = 0; i < 4; ++i)
+                    v[i] = lane + 32 * i < unit.rows ? ld_stream(src + 32 * i * p.ld) : make_uint4(0, 0, 0, 0);
             };
             if (unit.rows > 0) load();
             bool ok = true;
             for (uint32_t un = 0; unit.rows > 0; ++un) {
                 const uint32_t pb = un % kPickBufs;
-                uint32_t w[2][4];
-                int top[2];
+                uint32_t w[4][4];
+                int top[4];
 #pragma unroll
-                for (int i = 0; i < 2; ++i) {
+                for (int i = 0; i < 4; ++i) {
                     w[i][0] = v[i].x, w[i][1] = v[i].y, w[i][2] = v[i].z, w[i][3] = v[i].w;
                     top[i] = row_picks(w[i]);
-                    if (r0 + 32 * i >= unit.rows) w[i][0] = w[i][1] = w[i][2] = w[i][3] = 0;   // rows past the end: zeros
+                    if (lane + 32 * i >= unit.rows) w[i][0] = w[i][1] = w[i][2] = w[i][3] = 0;   // rows past the end: zeros
                 }
                 unit.next(walk, seg);
                 if (unit.rows > 0) load();
-                // this buffer was used two units back; its slabs were free after the products four units back, so the
-                // softmax has read what the ref slot held
-                if (un >= kPickBufs) ok &= sleep_wait(bar(sh.pick_empty[pb]), (un / kPickBufs - 1) & 1, p.err, abort_flag);
-                uint4 *const dst = reinterpret_cast<uint4 *>(smem_raw + (base - raw) + L::PICK + pb * kPicks) + r0;
+                // the expansion has begun with the unit two back, so it is done with the one before, for which products at
+                // most five back were done: the softmax has read what the ref slot held eight back
+                if (un >= kPickBufs) ok &= wait_bar(bar(sh.pick_empty[pb]), (un / kPickBufs - 1) & 1, p.err, abort_flag);
+                uint4 *const dst = reinterpret_cast<uint4 *>(smem + L::PICK + pb * kPicks) + lane;
 #pragma unroll
-                for (int i = 0; i < 2; ++i) {
+                for (int i = 0; i < 4; ++i) {
                     dst[32 * i] = make_uint4(w[i][0], w[i][1], w[i][2], w[i][3]);
-                    sh.ref[un & 3][r0 + 32 * i] = static_cast<int16_t>(top[i] - 127 - 6);
+                    sh.ref[un & 7][lane + 32 * i] = static_cast<int16_t>(top[i] - 127 - 6);
                 }
                 __syncwarp();
                 if (lane == 0) mbar_arrive(bar(sh.pick_full[pb]));
             }
             if (!ok) *abort_flag = 1;
+        } else if (warp == 3 && lane == 0) {
+            // ---- TMA: a unit's codes, slab by slab
+            tma_prefetch_desc(&tm_codes);
+            uint32_t it = 0;
+            bool ok = true;
+            while (ok && walk.next(seg)) {
+                for (int u = 0; ok && u < seg.units; ++u) {
+                    for (int k = 0; k < 4; ++k, ++it) {
+                        const uint32_t st = it % kStages;
+                        if (it >= kStages &&
+                            !(ok = wait_bar(bar(sh.stage_empty[st]), (it / kStages - 1) & 1, p.err, abort_flag)))
+                            break;
+                        mbar_arrive_expect_tx(bar(sh.stage_full[st]), kStage);
+                        tma_load_3d(base + L::STAGE + st * kStage, &tm_codes, bar(sh.stage_full[st]), k * 64,
+                                    seg.row0 + u * kRows, seg.seq);
+                    }
+                }
+            }
+            if (!ok) *abort_flag = 1;
+            // no load may still be landing when the CTA exits
+            for (uint32_t k = it > kStages ? it - kStages : 0; k < it; ++k)
+                wait_bar(bar(sh.stage_full[k % kStages]), (k / kStages) & 1, p.err);
         } else if (warp == 1 && lane == 0) {
             // ---- S^T = c . q^T: four slabs of K = 128
             constexpr uint32_t idesc = make_idesc_e4m3(128, N, 0, 0);
@@ -457,19 +493,21 @@ __global__ void __launch_bounds__(kThreads, 1)
             uint32_t it = 0, un = 0, ns = 0;
             bool ok = true;
             while (ok && walk.next(seg)) {
-                if (!(ok = sleep_wait(bar(sh.q_ready), ns++ & 1, p.err, abort_flag))) break;
+                if (!(ok = wait_bar(bar(sh.q_ready), ns++ & 1, p.err, abort_flag))) break;
                 for (int u = 0; ok && u < seg.units; ++u, ++un) {
-                    const uint32_t sb = un % kSBufs;
-                    if (un >= kSBufs && !(ok = sleep_wait(bar(sh.s_free[sb]), (un / kSBufs - 1) & 1, p.err, abort_flag)))
+                    const uint32_t sb = un % kSBufs, d = tmem + L::S_COL + sb * N;
+                    if (un >= kSBufs && !(ok = wait_bar(bar(sh.s_free[sb]), (un / kSBufs - 1) & 1, p.err, abort_flag)))
                         break;
                     for (int k = 0; k < 4; ++k, ++it) {
                         const uint32_t sl = it % kSlabs;
-                        if (!(ok = sleep_wait(bar(sh.slab_full[sl]), (it / kSlabs) & 1, p.err, abort_flag))) break;
+                        if (!(ok = wait_bar(bar(sh.slab_full[sl]), (it / kSlabs) & 1, p.err, abort_flag))) break;
                         tc_fence_after();
+                        const uint64_t a = desc_add(c0, sl * kSlab), b = desc_add(q0, k * L::kQSlab);
 #pragma unroll
-                        for (int kk = 0; kk < 4; ++kk)
-                            umma_f8(tmem + L::S_COL + sb * N, desc_add(c0, sl * kSlab + kk * 32), desc_add(q0, k * L::kQSlab + kk * 32),
-                                    idesc, (k | kk) != 0);
+                        for (int kk = 0; kk < 4; ++kk) {
+                            umma_f8(d, desc_add(a, kk * 32), desc_add(b, kk * 32), idesc, (k | kk) != 0);
+                            if (!kJoin) umma_f8(d, desc_add(a, kk * 32), desc_add(b, L::kQPart + kk * 32), idesc, 1);
+                        }
                     }
                     if (ok) umma_commit(bar(sh.s_full[sb]));
                 }
@@ -477,22 +515,24 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (!ok) *abort_flag = 1;
         } else if (warp == 2 && lane == 0) {
             // ---- O^T += c^T . P^T: slab t holds latent columns [128 t, 128 t + 128)
-            constexpr uint32_t idesc = make_idesc_e4m3(128, N, 1, 1);
+            constexpr uint32_t idesc = make_idesc_e4m3(128, N, 1, 1), idesc_lo = idesc | 1u << 10;   // B: e5m2
             const uint64_t p0 = make_smem_desc(base + L::P, kSlab, 1024), c0 = make_smem_desc(base + L::C, kSlab, 1024);
             uint32_t it = 0, un = 0;
             bool ok = true;
             while (ok && walk.next(seg)) {
                 for (int u = 0; ok && u < seg.units; ++u, ++un) {
                     const uint32_t pb = un % kPBufs;
-                    if (!(ok = sleep_wait(bar(sh.p_full[pb]), (un / kPBufs) & 1, p.err, abort_flag))) break;
+                    if (!(ok = wait_bar(bar(sh.p_full[pb]), (un / kPBufs) & 1, p.err, abort_flag))) break;
                     tc_fence_after();
                     for (int t = 0; t < 4; ++t, ++it) {
-                        const uint32_t sl = it % kSlabs;
-                        if (!(ok = sleep_wait(bar(sh.slab_full[sl]), (it / kSlabs) & 1, p.err, abort_flag))) break;
+                        const uint32_t sl = it % kSlabs, d = tmem + L::O_COL + t * N;
+                        if (!(ok = wait_bar(bar(sh.slab_full[sl]), (it / kSlabs) & 1, p.err, abort_flag))) break;
+                        const uint64_t a = desc_add(c0, sl * kSlab), b = desc_add(p0, pb * L::kPBuf);
 #pragma unroll
-                        for (int kk = 0; kk < 4; ++kk)
-                            umma_f8(tmem + L::O_COL + t * N, desc_add(c0, sl * kSlab + kk * 4096),
-                                    desc_add(p0, pb * kSlab + kk * 4096), idesc, (u | kk) != 0);
+                        for (int kk = 0; kk < 4; ++kk) {
+                            umma_f8(d, desc_add(a, kk * 4096), desc_add(b, kk * 4096), idesc, (u | kk) != 0);
+                            if (!kJoin) umma_f8(d, desc_add(a, kk * 4096), desc_add(b, L::kPPart + kk * 4096), idesc_lo, 1);
+                        }
                         umma_commit(bar(sh.slab_free[sl]));
                     }
                     if (ok) umma_commit(bar(sh.p_free[pb]));
@@ -500,15 +540,16 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             if (!ok) *abort_flag = 1;
         }
-    } else if (warp < 12) {
-        regs_acquire<kRegsSoft>();
+    } else if (warp < 4 + kSoftWarps) {
+        regs_acquire<L::kRegsSoft>();
         // ---- softmax: thread = row `t` of the unit (TMEM lane t), warpgroup `wg` the heads [HW wg, HW wg + HW).  After a
         // failed wait every warp runs its loops to their end, without waiting
-        const int wg = (warp - 4) >> 2, quad = warp & 3, t = quad * 32 + lane, id = 1 + wg;
-        const uint32_t lanes = tmem + (static_cast<uint32_t>(quad * 32) << 16) + wg * 2 * HW;
-        float *const mul = sh.mul + wg * HW, *const bias = sh.bias[warp - 4], *const step = sh.step[warp - 4],
-                     *const fac = sh.fac[warp - 4], *const part = sh.part[warp - 4];
-        const int mine = min(HW, heads - wg * HW);   // real heads of this warpgroup (may be <= 0)
+        const int sw = warp - 4, wg = sw >> 2, quad = warp & 3, t = quad * 32 + lane, id = 1 + wg;
+        const uint32_t lanes = tmem + (static_cast<uint32_t>(quad * 32) << 16) + wg * WC;
+        float *const mul = sh.mul + wg * HW, *const bias = sh.bias[sw], *const step = sh.step[sw], *const fac = sh.fac[sw],
+                     *const part = sh.part[sw];
+        const float(*const all)[kMaxHW] = sh.part + 4 * wg;
+        const int mine = min(HW, p.H - wg * HW);   // real heads of this warpgroup (may be <= 0)
         uint32_t un = 0;
         bool ok = true, more = walk.next(seg);
         float l[HW];
@@ -520,7 +561,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 for (int i = 0; i < 2; ++i) {
                     const int h = i0 + 4 * i;
                     const uint4 *src = reinterpret_cast<const uint4 *>(
-                                           p.q_abs + (static_cast<size_t>(seg.seq) * p.H + h0 + (h < mine ? wg * HW + h : 0)) * kR) +
+                                           p.q_abs + (static_cast<size_t>(seg.seq) * p.H + (h < mine ? wg * HW + h : 0)) * kR) +
                                        lane * 2;
                     v[i][0] = h < mine ? __ldg(src) : make_uint4(0, 0, 0, 0);
                     v[i][1] = h < mine ? __ldg(src + 1) : make_uint4(0, 0, 0, 0);
@@ -541,14 +582,13 @@ __global__ void __launch_bounds__(kThreads, 1)
 
             for (int u = 0; u < seg.units; ++u, ++un) {
                 const uint32_t sb = un % kSBufs, pb = un % kPBufs;
-                float x[HW], s[2 * HW];
-                ok &= sleep_wait(bar(sh.s_full[sb]), (un / kSBufs) & 1, p.err, abort_flag);
+                float x[HW], s[WC];
+                ok &= wait_bar(bar(sh.s_full[sb]), (un / kSBufs) & 1, p.err, abort_flag);
                 __syncwarp();
                 tc_fence_after();
 #pragma unroll
-                for (int g = 0; g < 2 * HW; g += 16)
-                    tmem_ld16(lanes + L::S_COL + sb * N + g, *reinterpret_cast<float (*)[16]>(s + g));
-                const int ref = sh.ref[un & 3][t];
+                for (int g = 0; g < WC; g += 8) tmem_ld8(lanes + L::S_COL + sb * N + g, *reinterpret_cast<float (*)[8]>(s + g));
+                const int ref = sh.ref[un & 7][t];
                 // a row past the end has an all-zero tile row: its exponents are -infinity
                 const float row_scale = exp2_int(ref),
                             row_exp = t < seg.len - seg.row0 - u * kRows ? static_cast<float>(ref) : -INFINITY;
@@ -558,35 +598,47 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (lane == 0) mbar_arrive(bar(sh.s_free[sb]));
                 // x = score * log2 e + ref + kBias - M
                 float top = -INFINITY;
+                const float2 rs = make_float2(row_scale, row_scale), re = make_float2(row_exp, row_exp);
 #pragma unroll
                 for (int h = 0; h < HW; h += 4) {
                     const float4 m = lds4(mul + h), bi = lds4(bias + h);
-                    const float2 rs = make_float2(row_scale, row_scale), re = make_float2(row_exp, row_exp),
-                                 part_lo = make_float2(kLoPart, kLoPart);
 #pragma unroll
                     for (int k = 0; k < 4; k += 2) {
                         const float2 mk = k ? make_float2(m.z, m.w) : make_float2(m.x, m.y);
                         const float2 bk = k ? make_float2(bi.z, bi.w) : make_float2(bi.x, bi.y);
-                        const float2 s2 = fma2(make_float2(s[2 * (h + k) + 2], s[2 * (h + k) + 3]), part_lo,
-                                               make_float2(s[2 * (h + k)], s[2 * (h + k) + 1]));
-                        const float2 v = fma2(s2, mul2(mk, rs), add2(bk, re));
+                        float2 sc;
+                        if constexpr (kJoin) {
+                            const int c = 2 * (h + k);
+                            sc = fma2(make_float2(s[c + 2], s[c + 3]), make_float2(kLoPart, kLoPart), make_float2(s[c], s[c + 1]));
+                        } else {
+                            sc = make_float2(s[h + k], s[h + k + 1]);
+                        }
+                        const float2 v = fma2(sc, mul2(mk, rs), add2(bk, re));
                         x[h + k] = v.x, x[h + k + 1] = v.y;
                         top = fmaxf(fmaxf(top, v.x), v.y);
                     }
                 }
+                uint32_t moved = 0;   // heads whose columns of O^T are to be rescaled
                 if (u == 0 || named_bar_or(id, 128, top > kBias + kSlack)) {
-                    // every head's maximum over the rows: lane h gets head h's, first of its warp, then of all four
+                    // the maxima over the rows of the heads that a row of this warp pushes past (of all, the first time):
+                    // lane h gets head h's, first of its warp, then of all four
+                    uint32_t past = u == 0 ? ~0u : 0u;
+                    if (u > 0) {
+#pragma unroll
+                        for (int h = 0; h < HW; ++h) past |= x[h] > kBias + kSlack ? 1u << h : 0u;
+                        past = __reduce_or_sync(0xffffffffu, past);
+                    }
                     float most = -INFINITY;
 #pragma unroll
-                    for (int h = 0; h < HW; ++h) {
-                        const float v = warp_max(x[h]);
-                        if (lane == h) most = v;
-                    }
+                    for (int h = 0; h < HW; ++h)
+                        if (past >> h & 1) {
+                            const float v = warp_max(x[h]);
+                            if (lane == h) most = v;
+                        }
                     if (lane < HW) part[lane] = most;
                     named_bar_sync(id, 128);
                     bool moves = false;
                     if (lane < HW) {
-                        const float(*all)[24] = sh.part + 4 * wg;
                         most = fmaxf(fmaxf(all[0][lane], all[1][lane]), fmaxf(all[2][lane], all[3][lane]));
                         moves = (most > kBias + kSlack || u == 0) && most > -INFINITY;
                         const float by = moves ? kBias - kHead - most : 0.f;   // M_old - M_new
@@ -594,44 +646,28 @@ __global__ void __launch_bounds__(kThreads, 1)
                         fac[lane] = fast_exp2(by);
                         bias[lane] += by;
                     }
-                    uint32_t moved = __ballot_sync(0xffffffffu, moves);
+                    moved = u > 0 ? __ballot_sync(0xffffffffu, moves) : 0u;
                     __syncwarp();
 #pragma unroll
                     for (int h = 0; h < HW; h += 4) {
                         const float4 by = lds4(step + h);
-                        x[h] += by.x, x[h + 1] += by.y, x[h + 2] += by.z, x[h + 3] += by.w;
+                        const float2 a = add2(make_float2(x[h], x[h + 1]), make_float2(by.x, by.y));
+                        const float2 b = add2(make_float2(x[h + 2], x[h + 3]), make_float2(by.z, by.w));
+                        x[h] = a.x, x[h + 1] = a.y, x[h + 2] = b.x, x[h + 3] = b.y;
                     }
                     if (u > 0) {
 #pragma unroll
                         for (int h = 0; h < HW; h += 4) {
-                            const float4 g = lds4(fac + h);
-                            l[h] *= g.x, l[h + 1] *= g.y, l[h + 2] *= g.z, l[h + 3] *= g.w;
+                            const float4 f = lds4(fac + h);
+                            const float2 a = mul2(make_float2(l[h], l[h + 1]), make_float2(f.x, f.y));
+                            const float2 b = mul2(make_float2(l[h + 2], l[h + 3]), make_float2(f.z, f.w));
+                            l[h] = a.x, l[h + 1] = a.y, l[h + 2] = b.x, l[h + 3] = b.y;
                         }
-                        // the products of the unit before are complete before O^T is scaled
-                        ok &= sleep_wait(bar(sh.p_free[(un - 1) % kPBufs]), ((un - 1) / kPBufs) & 1, p.err, abort_flag);
-                        __syncwarp();
-                        tc_fence_after();
-                        for (; moved; moved &= moved - 1) {
-                            const int h = __ffs(moved) - 1;
-                            const float g = fac[h];
-                            const float g0 = h & 1 ? 1.f : g, g1 = h & 1 ? g : 1.f;
-                            float o[4][4];   // the pair's columns of the four latent tiles
-#pragma unroll
-                            for (int c = 0; c < 4; ++c) tmem_ld4(lanes + L::O_COL + c * N + 2 * (h & ~1), o[c]);
-                            tmem_wait_ld();
-#pragma unroll
-                            for (int c = 0; c < 4; ++c) {
-                                o[c][0] *= g0, o[c][1] *= g1, o[c][2] *= g0, o[c][3] *= g1;
-                                tmem_st4(lanes + L::O_COL + c * N + 2 * (h & ~1), o[c]);
-                            }
-                        }
-                        tmem_wait_st();
-                        tc_fence_before();
                     }
                 }
-                // weights, their sums, and P^T as the MN-major N side: row t, 2 HW bytes of this warpgroup
+                // weights, their sums, and P^T as the MN-major N side: row t, the bytes of this warpgroup's columns
                 const float2 unref = make_float2(exp2_int(-ref), exp2_int(-ref));
-                uint32_t w[HW / 2];
+                uint32_t w[HW / 2];   // kJoin: two heads' hi and lo; else HW / 4 words of hi, then of lo
 #pragma unroll
                 for (int h = 0; h < HW; h += 4) {
                     const float2 p01 = make_float2(fast_exp2(x[h]), fast_exp2(x[h + 1]));
@@ -639,14 +675,52 @@ __global__ void __launch_bounds__(kThreads, 1)
                     const float2 l01 = fma2(p01, unref, make_float2(l[h], l[h + 1]));
                     const float2 l23 = fma2(p23, unref, make_float2(l[h + 2], l[h + 3]));
                     l[h] = l01.x, l[h + 1] = l01.y, l[h + 2] = l23.x, l[h + 3] = l23.y;
-                    w[h / 2] = split16_e4m3x2(p01.x, p01.y);
-                    w[h / 2 + 1] = split16_e4m3x2(p23.x, p23.y);
+                    if constexpr (kJoin) {
+                        w[h / 2] = split16_e4m3x2(p01.x, p01.y);
+                        w[h / 2 + 1] = split16_e4m3x2(p23.x, p23.y);
+                    } else {
+                        const uint32_t y = split_e4m3_e5m2x2(p01.x, p01.y), z = split_e4m3_e5m2x2(p23.x, p23.y);
+                        w[h / 4] = byte_perm(y, z, 0x5410);
+                        w[HW / 4 + h / 4] = byte_perm(y, z, 0x7632);
+                    }
                 }
-                if (un >= kPBufs) ok &= sleep_wait(bar(sh.p_free[pb]), (un / kPBufs - 1) & 1, p.err, abort_flag);
-                const uint32_t prow = base + L::P + pb * kSlab;
+                if (un >= kPBufs) ok &= wait_bar(bar(sh.p_free[pb]), (un / kPBufs - 1) & 1, p.err, abort_flag);
+                const uint32_t prow = base + L::P + pb * L::kPBuf;
+                if constexpr (kJoin) {
 #pragma unroll
-                for (int i = 0; i < HW / 8; ++i)
-                    st_shared_v4(prow + sw128_offset(t, wg * (HW / 8) + i), w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
+                    for (int i = 0; i < HW / 8; ++i)
+                        st_shared_v4(prow + sw128_offset(t, wg * (HW / 8) + i), w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
+                } else {
+#pragma unroll
+                    for (int i = 0; i < HW / 8; ++i) {   // HW = 24 leaves 8-byte pieces
+                        const int piece = wg * (HW / 8) + i;
+                        const uint32_t at = prow + sw128_offset(t, piece >> 1) + 8 * (piece & 1);
+                        st_shared_v2(at, w[2 * i], w[2 * i + 1]);
+                        st_shared_v2(at + L::kPPart, w[HW / 4 + 2 * i], w[HW / 4 + 2 * i + 1]);
+                    }
+                }
+                if (moved) {   // once the products of the unit before are complete
+                    ok &= wait_bar(bar(sh.p_free[(un - 1) % kPBufs]), ((un - 1) / kPBufs) & 1, p.err, abort_flag);
+                    __syncwarp();
+                    tc_fence_after();
+                    for (; moved; moved &= moved - 1) {
+                        const int h = __ffs(moved) - 1, j = kJoin ? h & 1 : h & 3, col = kJoin ? 2 * (h & ~1) : h & ~3;
+                        const float f = fac[h];
+                        float o[4][4];   // the four columns around the head's, of the four latent tiles
+#pragma unroll
+                        for (int c = 0; c < 4; ++c) tmem_ld4(lanes + L::O_COL + c * N + col, o[c]);
+                        tmem_wait_ld();
+#pragma unroll
+                        for (int c = 0; c < 4; ++c) {
+#pragma unroll
+                            for (int i = 0; i < 4; ++i)
+                                if ((kJoin ? i & 1 : i) == j) o[c][i] *= f;
+                            tmem_st4(lanes + L::O_COL + c * N + col, o[c]);
+                        }
+                    }
+                    tmem_wait_st();
+                    tc_fence_before();
+                }
                 fence_proxy_async_smem();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(bar(sh.p_full[pb]));
@@ -654,32 +728,33 @@ __global__ void __launch_bounds__(kThreads, 1)
             // ---- drain: l over the 128 rows, then O^T (lane = latent column of its tile)
 #pragma unroll
             for (int h = 0; h < HW; ++h) {
-                float s = l[h];
+                float v = l[h];
 #pragma unroll
-                for (int o = 16; o >= 1; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
-                if (lane == h) part[h] = s;
+                for (int o = 16; o >= 1; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+                if (lane == h) part[h] = v;
             }
             const uint32_t last = un - 1;
-            ok &= sleep_wait(bar(sh.p_free[last % kPBufs]), (last / kPBufs) & 1, p.err, abort_flag);
+            ok &= wait_bar(bar(sh.p_free[last % kPBufs]), (last / kPBufs) & 1, p.err, abort_flag);
             named_bar_sync(id, 128);
             tc_fence_after();
-            const size_t slot = static_cast<size_t>(seg.slot) * p.H + h0 + wg * HW;
+            const size_t slot = static_cast<size_t>(seg.slot) * p.H + wg * HW;
             if (t < mine) {   // (mine <= 24: the warpgroup's first warp)
-                const float(*all)[24] = sh.part + 4 * wg;
                 p.ws_m[slot + t] = -bias[t];
                 p.ws_l[slot + t] = (all[0][t] + all[1][t]) + (all[2][t] + all[3][t]);
             }
 #pragma unroll 1
             for (int c = 0; c < 4 * (HW / 8); ++c) {
                 const int tile = c / (HW / 8), g = c % (HW / 8) * 8;
-                float o[16];
-                tmem_ld16(lanes + L::O_COL + tile * N + 2 * g, o);
+                float *const dst = p.ws_o + (slot + g) * kR + tile * 128 + t;
+                float o[kJoin ? 16 : 8];
+#pragma unroll
+                for (int i = 0; i < (kJoin ? 16 : 8); i += 8)
+                    tmem_ld8(lanes + L::O_COL + tile * N + (kJoin ? 2 * g : g) + i, *reinterpret_cast<float (*)[8]>(o + i));
                 tmem_wait_ld();
-                float *dst = p.ws_o + (slot + g) * kR + tile * 128 + t;
 #pragma unroll
                 for (int k = 0; k < 8; ++k) {
-                    const int at = 2 * (k & ~1) + (k & 1);
-                    if (g + k < mine) dst[static_cast<size_t>(k) * kR] = fmaf(o[at + 2], kLoPart, o[at]);
+                    const int at = kJoin ? 2 * (k & ~1) + (k & 1) : k;
+                    if (g + k < mine) dst[static_cast<size_t>(k) * kR] = kJoin ? fmaf(o[(at + 2) % 16], kLoPart, o[at]) : o[at];
                 }
             }
             tc_fence_before();
@@ -688,59 +763,52 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         if (!ok) *abort_flag = 1;
     } else {
-        regs_release<kRegsExp>();
-        // ---- expansion: a warp takes half of the rows of one of a unit's four slabs, a lane the groups (32 codes) `g` of
-        // rows r + 8 i.  A lane loads its codes a unit ahead: 32 KB in flight per SM
-        const int k = (warp - 12) & 3, half = (warp - 12) >> 2, g = lane & 3, r = half * 64 + (lane >> 2);
-        uint8_t *const smem = smem_raw + (base - raw);
-        const long long step8 = 8 * p.ld;
+        regs_release<L::kRegsExp>();
+        // ---- expansion: a warp takes kExpRows rows of each of a unit's four slabs as it gets free, a lane the groups (32
+        // codes) `g` of rows r + 8 i
+        constexpr int kI = L::kExpRows / 8;
+        const int g = lane & 3, r = (warp - 4 - kSoftWarps) * L::kExpRows + (lane >> 2);
         const int x = ((2 * g) ^ (lane >> 2)) * 16;   // row & 7 = lane >> 2: the swizzle of the group's first 16 bytes
-        const uint32_t slab_at = L::C + sw128_offset(r, 0) - (lane >> 2) * 16, pick_at = L::PICK + r * 16 + k * 4 + g;
-        uint4 v[8];
-        Units unit;
-        unit.start(walk, seg);
-        auto load = [&] {
-            const uint8_t *src =
-                p.c4 + (static_cast<long long>(seg.seq) * p.max_len + unit.row(seg) + r) * p.ld + k * 64 + g * 16;
-            if (unit.rows == kRows) {
-#pragma unroll
-                for (int i = 0; i < 8; ++i) v[i] = ld_stream(src + i * step8);
-            } else {   // (what the lane holds for rows past the end goes with a table of zeros)
-#pragma unroll
-                for (int i = 0; i < 8; ++i)
-                    if (r + 8 * i < unit.rows) v[i] = ld_stream(src + i * step8);
-            }
-        };
-#pragma unroll
-        for (int i = 0; i < 8; ++i) v[i] = make_uint4(0, 0, 0, 0);
-        if (unit.rows > 0) load();
+        const uint32_t slab_at = L::C + sw128_offset(r, 0) - (lane >> 2) * 16, pick_at = L::PICK + r * 16 + g,
+                       stage_at = L::STAGE + r * 64 + g * 16;
         bool ok = true;
-        for (uint32_t it = k, un = 0; unit.rows > 0; it += 4, ++un) {
-            const uint32_t pb = un % kPickBufs, sl = it % kSlabs;
-            ok &= sleep_wait(bar(sh.pick_full[pb]), (un / kPickBufs) & 1, p.err, abort_flag);
-            uint2 tb[8];   // all read before the first store
+        uint32_t it = 0, un = 0;
+        while (walk.next(seg)) {
+            for (int u = 0; u < seg.units; ++u, ++un) {
+                const uint32_t pb = un % kPickBufs;
+                ok &= wait_bar(bar(sh.pick_full[pb]), (un / kPickBufs) & 1, p.err, abort_flag);
+#pragma unroll 1
+                for (int k = 0; k < 4; ++k, ++it) {
+                    const uint32_t sl = it % kSlabs, st = it % kStages;
+                    ok &= wait_bar(bar(sh.stage_full[st]), (it / kStages) & 1, p.err, abort_flag);
+                    uint4 c[kI];
+                    uint2 tb[kI];   // all read before the first store
 #pragma unroll
-            for (int i = 0; i < 8; ++i) tb[i] = sh.table[smem[pick_at + pb * kPicks + i * 128]];
-            if (it >= kSlabs) ok &= sleep_wait(bar(sh.slab_free[sl]), (it / kSlabs - 1) & 1, p.err, abort_flag);
-            uint8_t *const slab = smem + slab_at + sl * kSlab;
+                    for (int i = 0; i < kI; ++i) {
+                        c[i] = *reinterpret_cast<const uint4 *>(smem + stage_at + st * kStage + i * 512);
+                        tb[i] = sh.table[smem[pick_at + pb * kPicks + i * 128 + k * 4]];
+                    }
+                    if (it >= kSlabs) ok &= wait_bar(bar(sh.slab_free[sl]), (it / kSlabs - 1) & 1, p.err, abort_flag);
+                    uint8_t *const slab = smem + slab_at + sl * kSlab;
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                uint32_t o[8];
-                expand8(v[i].x, tb[i], o[0], o[1]);
-                expand8(v[i].y, tb[i], o[2], o[3]);
-                expand8(v[i].z, tb[i], o[4], o[5]);
-                expand8(v[i].w, tb[i], o[6], o[7]);
-                *reinterpret_cast<uint4 *>(slab + i * 1024 + x) = make_uint4(o[0], o[1], o[2], o[3]);
-                *reinterpret_cast<uint4 *>(slab + i * 1024 + (x ^ 16)) = make_uint4(o[4], o[5], o[6], o[7]);
+                    for (int i = 0; i < kI; ++i) {
+                        uint32_t o[8];
+                        expand8(c[i].x, tb[i], o[0], o[1]);
+                        expand8(c[i].y, tb[i], o[2], o[3]);
+                        expand8(c[i].z, tb[i], o[4], o[5]);
+                        expand8(c[i].w, tb[i], o[6], o[7]);
+                        *reinterpret_cast<uint4 *>(slab + i * 1024 + x) = make_uint4(o[0], o[1], o[2], o[3]);
+                        *reinterpret_cast<uint4 *>(slab + i * 1024 + (x ^ 16)) = make_uint4(o[4], o[5], o[6], o[7]);
+                    }
+                    fence_proxy_async_smem();
+                    __syncwarp();
+                    if (lane == 0) {
+                        mbar_arrive(bar(sh.slab_full[sl]));
+                        mbar_arrive(bar(sh.stage_empty[st]));
+                        if (k == 3) mbar_arrive(bar(sh.pick_empty[pb]));
+                    }
+                }
             }
-            fence_proxy_async_smem();
-            __syncwarp();
-            if (lane == 0) {
-                mbar_arrive(bar(sh.slab_full[sl]));
-                mbar_arrive(bar(sh.pick_empty[pb]));
-            }
-            unit.next(walk, seg);
-            if (unit.rows > 0) load();   // after the fence, which would wait for it
         }
         if (!ok) *abort_flag = 1;
     }
@@ -995,34 +1063,28 @@ CUresult encode_map(CUtensorMap *m, CUtensorMapDataType type, CUtensorMapSwizzle
               CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
 }
 
-// Heads per CTA: one group up to 48 heads, two above; the tile's columns are padded to 16, 32 or 48.
-int head_groups(int H) { return H > 48 ? 2 : 1; }
-int shares(int H, int num_sms) {
-    const int g = num_sms / head_groups(H);
-    return g < 1 ? 1 : g;
-}
 size_t slot_count(int B, int max_len, int G) {
     return static_cast<size_t>(G) + static_cast<size_t>(B) * (max_len > 0 ? chunks_of(max_len) : 0);
 }
 
 template <int HP>
-cudaError_t launch_attention(const Fp4Params &p, cudaStream_t s) {
+cudaError_t launch_attention(const CUtensorMap &codes, const Fp4Params &p, cudaStream_t s) {
     using L = Fp4Layout<HP>;
     cudaError_t e = cudaFuncSetAttribute(fp4_attention_kernel<HP>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                          static_cast<int>(L::kSmem));
     if (e != cudaSuccess) return e;
     cudaFuncAttributes fa;   // the kernel's register split assumes this launch budget
     if ((e = cudaFuncGetAttributes(&fa, fp4_attention_kernel<HP>)) != cudaSuccess) return e;
-    if (fa.numRegs != static_cast<int>(kRegsLaunch)) return cudaErrorInvalidConfiguration;
+    if (fa.numRegs != static_cast<int>(L::kRegsLaunch)) return cudaErrorInvalidConfiguration;
     note_launch();
-    fp4_attention_kernel<HP><<<p.G * p.groups, kThreads, L::kSmem, s>>>(p);
+    fp4_attention_kernel<HP><<<p.G, L::kThreads, L::kSmem, s>>>(codes, p);
     return cudaGetLastError();
 }
 
 }  // namespace
 
 size_t decode_fp4_workspace_bytes(int B, int H, int max_len, int num_sms) {
-    return slot_count(B, max_len, shares(H, num_sms)) * H * (kR + 2) * sizeof(float);
+    return slot_count(B, max_len, num_sms) * H * (kR + 2) * sizeof(float);
 }
 
 cudaError_t launch_decode_fp4(const DecodeArgs &a, cudaStream_t s) {
@@ -1035,9 +1097,7 @@ cudaError_t launch_decode_fp4(const DecodeArgs &a, cudaStream_t s) {
     p.B = a.B;
     p.H = a.H;
     p.max_len = a.max_len;
-    p.groups = head_groups(a.H);
-    p.heads_per_group = (a.H + p.groups - 1) / p.groups;
-    p.G = shares(a.H, a.num_sms);
+    p.G = a.num_sms;
     const size_t slots = slot_count(a.B, a.max_len, p.G);
     if (slots * a.H * (kR + 2) * sizeof(float) > a.workspace_bytes) return cudaErrorInvalidValue;
     p.ws_o = static_cast<float *>(a.workspace);
@@ -1045,18 +1105,25 @@ cudaError_t launch_decode_fp4(const DecodeArgs &a, cudaStream_t s) {
     p.ws_l = p.ws_m + slots * a.H;
     p.err = a.dev_err;
     p.scale_log2 = a.scale * kLog2e;
-    CUtensorMap tm_wuv;
+    CUtensorMap tm_codes, tm_wuv;
     {
-        const cuuint64_t dims[2] = {kR, static_cast<cuuint64_t>(a.H) * kDV}, strides[1] = {kR * 2};
-        const cuuint32_t box[2] = {64, kDV};
-        if (encode_map(&tm_wuv, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, CU_TENSOR_MAP_SWIZZLE_128B, a.w_uv, 2, dims, strides, box) !=
-            CUDA_SUCCESS)
+        const cuuint64_t rows = static_cast<cuuint64_t>(a.max_len > 0 ? a.max_len : 1);
+        const cuuint64_t dims[3] = {kR / 2, rows, static_cast<cuuint64_t>(a.B)};
+        const cuuint64_t strides[2] = {static_cast<cuuint64_t>(a.ld_cache), rows * static_cast<cuuint64_t>(a.ld_cache)};
+        const cuuint32_t box[3] = {64, kRows, 1};
+        const cuuint64_t wd[2] = {kR, static_cast<cuuint64_t>(a.H) * kDV}, ws[1] = {kR * 2};
+        const cuuint32_t wb[2] = {64, kDV};
+        if (encode_map(&tm_codes, CU_TENSOR_MAP_DATA_TYPE_UINT8, CU_TENSOR_MAP_SWIZZLE_NONE, a.c_cache, 3, dims, strides,
+                       box) != CUDA_SUCCESS ||
+            encode_map(&tm_wuv, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, CU_TENSOR_MAP_SWIZZLE_128B, a.w_uv, 2, wd, ws, wb) !=
+                CUDA_SUCCESS)
             return cudaErrorInvalidValue;
     }
-    const int hp = p.heads_per_group;
-    cudaError_t e = hp <= 16   ? launch_attention<16>(p, s)
-                    : hp <= 32 ? launch_attention<32>(p, s)
-                               : launch_attention<48>(p, s);
+    cudaError_t e = a.H <= 16   ? launch_attention<16>(tm_codes, p, s)
+                    : a.H <= 32 ? launch_attention<32>(tm_codes, p, s)
+                    : a.H <= 48 ? launch_attention<48>(tm_codes, p, s)
+                    : a.H <= 64 ? launch_attention<64>(tm_codes, p, s)
+                                : launch_attention<96>(tm_codes, p, s);
     if (e != cudaSuccess) return e;
     e = cudaFuncSetAttribute(fp4_merge_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(kSmemMerge));
     if (e != cudaSuccess) return e;
