@@ -79,10 +79,9 @@ struct Fp4Shared {
 template <int HP>
 struct Fp4Layout {
     static constexpr bool kJoin = HP <= 48;
-    static constexpr int kSoftGroups = kJoin ? 2 : 4, kExpGroups = kJoin ? 2 : 1, kGroups = 1 + kSoftGroups + kExpGroups;
+    static constexpr int kSoftGroups = kJoin ? 2 : 4, kExpGroups = 2, kGroups = 1 + kSoftGroups + kExpGroups;
     static constexpr int kThreads = 128 * kGroups, HW = HP / kSoftGroups, N = kJoin ? 2 * HP : HP;   // N: columns of an MMA
     static constexpr int WC = N / kSoftGroups;                          // columns of a warpgroup
-    static constexpr int kExpRows = kJoin ? 16 : 32;                    // rows that an expanding warp takes
     // expanded tiles in flight (four per unit), and what the rest of shared memory holds of codes
     static constexpr int kSlabs = HP == 96 ? 4 : (HP == 64 ? 6 : (HP == 48 ? 7 : 8)), kStages = HP == 16 ? 4 : 2;
     static constexpr int kPBufs = kJoin ? 2 : 1, kSBufs = 2 * N <= 128 ? 2 : 1;
@@ -93,8 +92,8 @@ struct Fp4Layout {
     static constexpr uint32_t kSmem = END + sizeof(Fp4Shared) + 1024;   // + alignment slack
     static constexpr uint32_t S_COL = 0, O_COL = 128;                   // TMEM columns
     // Register split of the warpgroups: control, softmax, expansion.
-    static constexpr uint32_t kRegsLaunch = kJoin ? 96 : 80, kRegsCtl = kJoin ? 80 : 72, kRegsSoft = kJoin ? 104 : 88,
-                              kRegsExp = kJoin ? 96 : 56;
+    static constexpr uint32_t kRegsLaunch = kJoin ? 96 : 72, kRegsCtl = kJoin ? 80 : 56, kRegsSoft = kJoin ? 104 : 88,
+                              kRegsExp = kJoin ? 96 : 48;
     static_assert(kRegsCtl + kSoftGroups * kRegsSoft + kExpGroups * kRegsExp <= kGroups * kRegsLaunch,
                   "register split exceeds the launch");
     static_assert(kQPart % 1024 == 0 && O_COL + 4 * N <= 512 && kSBufs * N <= O_COL && N <= 128, "layout");
@@ -392,9 +391,9 @@ __global__ void __launch_bounds__(Fp4Layout<HP>::kThreads, 1)
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
     if (threadIdx.x == 0) {
-        for (int i = 0; i < kStages; ++i) mbar_init(bar(sh.stage_full[i]), 1), mbar_init(bar(sh.stage_empty[i]), kExpWarps);
+        for (int i = 0; i < kStages; ++i) mbar_init(bar(sh.stage_full[i]), 1), mbar_init(bar(sh.stage_empty[i]), 4);
         for (int i = 0; i < kPickBufs; ++i) mbar_init(bar(sh.pick_full[i]), 1), mbar_init(bar(sh.pick_empty[i]), kExpWarps);
-        for (int i = 0; i < kSlabs; ++i) mbar_init(bar(sh.slab_full[i]), kExpWarps), mbar_init(bar(sh.slab_free[i]), 1);
+        for (int i = 0; i < kSlabs; ++i) mbar_init(bar(sh.slab_full[i]), 4), mbar_init(bar(sh.slab_free[i]), 1);
         for (int i = 0; i < kSBufs; ++i) mbar_init(bar(sh.s_full[i]), 1), mbar_init(bar(sh.s_free[i]), kSoftWarps);
         for (int i = 0; i < kPBufs; ++i) mbar_init(bar(sh.p_full[i]), kSoftWarps), mbar_init(bar(sh.p_free[i]), 1);
         mbar_init(bar(sh.q_ready), kSoftWarps);
@@ -441,25 +440,20 @@ __global__ void __launch_bounds__(Fp4Layout<HP>::kThreads, 1)
             bool ok = true;
             for (uint32_t un = 0; unit.rows > 0; ++un) {
                 const uint32_t pb = un % kPickBufs;
-                uint32_t w[4][4];
-                int top[4];
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    w[i][0] = v[i].x, w[i][1] = v[i].y, w[i][2] = v[i].z, w[i][3] = v[i].w;
-                    top[i] = row_picks(w[i]);
-                    if (lane + 32 * i >= unit.rows) w[i][0] = w[i][1] = w[i][2] = w[i][3] = 0;   // rows past the end: zeros
-                }
-                unit.next(walk, seg);
-                if (unit.rows > 0) load();
                 // the expansion has begun with the unit two back, so it is done with the one before, for which products at
                 // most five back were done: the softmax has read what the ref slot held eight back
                 if (un >= kPickBufs) ok &= wait_bar(bar(sh.pick_empty[pb]), (un / kPickBufs - 1) & 1, p.err, abort_flag);
                 uint4 *const dst = reinterpret_cast<uint4 *>(smem + L::PICK + pb * kPicks) + lane;
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
-                    dst[32 * i] = make_uint4(w[i][0], w[i][1], w[i][2], w[i][3]);
-                    sh.ref[un & 7][lane + 32 * i] = static_cast<int16_t>(top[i] - 127 - 6);
+                    uint32_t w[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
+                    const int top = row_picks(w);
+                    const bool real = lane + 32 * i < unit.rows;   // rows past the end: zeros
+                    dst[32 * i] = real ? make_uint4(w[0], w[1], w[2], w[3]) : make_uint4(0, 0, 0, 0);
+                    sh.ref[un & 7][lane + 32 * i] = static_cast<int16_t>(top - 127 - 6);
                 }
+                unit.next(walk, seg);
+                if (unit.rows > 0) load();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(bar(sh.pick_full[pb]));
             }
@@ -583,8 +577,9 @@ __global__ void __launch_bounds__(Fp4Layout<HP>::kThreads, 1)
             for (int u = 0; u < seg.units; ++u, ++un) {
                 const uint32_t sb = un % kSBufs, pb = un % kPBufs;
                 float x[HW], s[WC];
-                ok &= wait_bar(bar(sh.s_full[sb]), (un / kSBufs) & 1, p.err, abort_flag);
-                __syncwarp();
+                // one warp asks: tries cost the others their shared-memory accesses
+                if (quad == 0) ok &= wait_bar(bar(sh.s_full[sb]), (un / kSBufs) & 1, p.err, abort_flag);
+                named_bar_sync(id, 128);
                 tc_fence_after();
 #pragma unroll
                 for (int g = 0; g < WC; g += 8) tmem_ld8(lanes + L::S_COL + sb * N + g, *reinterpret_cast<float (*)[8]>(s + g));
@@ -593,9 +588,6 @@ __global__ void __launch_bounds__(Fp4Layout<HP>::kThreads, 1)
                 const float row_scale = exp2_int(ref),
                             row_exp = t < seg.len - seg.row0 - u * kRows ? static_cast<float>(ref) : -INFINITY;
                 tmem_wait_ld();
-                tc_fence_before();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(bar(sh.s_free[sb]));
                 // x = score * log2 e + ref + kBias - M
                 float top = -INFINITY;
                 const float2 rs = make_float2(row_scale, row_scale), re = make_float2(row_exp, row_exp);
@@ -622,19 +614,35 @@ __global__ void __launch_bounds__(Fp4Layout<HP>::kThreads, 1)
                 if (u == 0 || named_bar_or(id, 128, top > kBias + kSlack)) {
                     // the maxima over the rows of the heads that a row of this warp pushes past (of all, the first time):
                     // lane h gets head h's, first of its warp, then of all four
-                    uint32_t past = u == 0 ? ~0u : 0u;
-                    if (u > 0) {
-#pragma unroll
-                        for (int h = 0; h < HW; ++h) past |= x[h] > kBias + kSlack ? 1u << h : 0u;
-                        past = __reduce_or_sync(0xffffffffu, past);
-                    }
                     float most = -INFINITY;
+                    if (u == 0) {
 #pragma unroll
-                    for (int h = 0; h < HW; ++h)
-                        if (past >> h & 1) {
+                        for (int h = 0; h < HW; ++h) {
                             const float v = warp_max(x[h]);
                             if (lane == h) most = v;
                         }
+                    } else {   // a few: a short loop that reads S again, as this code is seldom in the instruction cache
+                        uint32_t past = 0;   // bit HW - 1 - h: head h (the sign of threshold - x)
+#pragma unroll
+                        for (int h = 0; h < HW; ++h)
+                            past = __funnelshift_l(__float_as_uint(kBias + kSlack - x[h]), past, 1);
+                        for (past = __reduce_or_sync(0xffffffffu, past); past; past &= past - 1) {
+                            const int h = HW - __ffs(past);
+                            float v;
+                            if constexpr (kJoin) {
+                                float lo;
+                                tmem_ld1(lanes + L::S_COL + sb * N + 2 * (h & ~1) + (h & 1), v);
+                                tmem_ld1(lanes + L::S_COL + sb * N + 2 * (h & ~1) + (h & 1) + 2, lo);
+                                tmem_wait_ld();
+                                v = fmaf(lo, kLoPart, v);
+                            } else {
+                                tmem_ld1(lanes + L::S_COL + sb * N + h, v);
+                                tmem_wait_ld();
+                            }
+                            v = warp_max(fmaf(v, mul[h] * row_scale, bias[h] + row_exp));
+                            if (lane == h) most = v;
+                        }
+                    }
                     if (lane < HW) part[lane] = most;
                     named_bar_sync(id, 128);
                     bool moves = false;
@@ -665,6 +673,9 @@ __global__ void __launch_bounds__(Fp4Layout<HP>::kThreads, 1)
                         }
                     }
                 }
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(bar(sh.s_free[sb]));
                 // weights, their sums, and P^T as the MN-major N side: row t, the bytes of this warpgroup's columns
                 const float2 unref = make_float2(exp2_int(-ref), exp2_int(-ref));
                 uint32_t w[HW / 2];   // kJoin: two heads' hi and lo; else HW / 4 words of hi, then of lo
@@ -764,48 +775,50 @@ __global__ void __launch_bounds__(Fp4Layout<HP>::kThreads, 1)
         if (!ok) *abort_flag = 1;
     } else {
         regs_release<L::kRegsExp>();
-        // ---- expansion: a warp takes kExpRows rows of each of a unit's four slabs as it gets free, a lane the groups (32
-        // codes) `g` of rows r + 8 i
-        constexpr int kI = L::kExpRows / 8;
-        const int g = lane & 3, r = (warp - 4 - kSoftWarps) * L::kExpRows + (lane >> 2);
+        // ---- expansion: a warpgroup takes every other slab, a warp 32 of its rows, a lane the groups (32 codes) `g` of rows
+        // r + 8 i
+        const int first = (warp - 4 - kSoftWarps) >> 2, g = lane & 3, r = (warp & 3) * 32 + (lane >> 2);
         const int x = ((2 * g) ^ (lane >> 2)) * 16;   // row & 7 = lane >> 2: the swizzle of the group's first 16 bytes
         const uint32_t slab_at = L::C + sw128_offset(r, 0) - (lane >> 2) * 16, pick_at = L::PICK + r * 16 + g,
                        stage_at = L::STAGE + r * 64 + g * 16;
         bool ok = true;
-        uint32_t it = 0, un = 0;
+        uint32_t un = 0;
         while (walk.next(seg)) {
             for (int u = 0; u < seg.units; ++u, ++un) {
                 const uint32_t pb = un % kPickBufs;
                 ok &= wait_bar(bar(sh.pick_full[pb]), (un / kPickBufs) & 1, p.err, abort_flag);
 #pragma unroll 1
-                for (int k = 0; k < 4; ++k, ++it) {
-                    const uint32_t sl = it % kSlabs, st = it % kStages;
+                for (int k = first; k < 4; k += L::kExpGroups) {
+                    const uint32_t it = 4 * un + k, sl = it % kSlabs, st = it % kStages;
                     ok &= wait_bar(bar(sh.stage_full[st]), (it / kStages) & 1, p.err, abort_flag);
-                    uint4 c[kI];
-                    uint2 tb[kI];   // all read before the first store
-#pragma unroll
-                    for (int i = 0; i < kI; ++i) {
-                        c[i] = *reinterpret_cast<const uint4 *>(smem + stage_at + st * kStage + i * 512);
-                        tb[i] = sh.table[smem[pick_at + pb * kPicks + i * 128 + k * 4]];
-                    }
                     if (it >= kSlabs) ok &= wait_bar(bar(sh.slab_free[sl]), (it / kSlabs - 1) & 1, p.err, abort_flag);
                     uint8_t *const slab = smem + slab_at + sl * kSlab;
 #pragma unroll
-                    for (int i = 0; i < kI; ++i) {
-                        uint32_t o[8];
-                        expand8(c[i].x, tb[i], o[0], o[1]);
-                        expand8(c[i].y, tb[i], o[2], o[3]);
-                        expand8(c[i].z, tb[i], o[4], o[5]);
-                        expand8(c[i].w, tb[i], o[6], o[7]);
-                        *reinterpret_cast<uint4 *>(slab + i * 1024 + x) = make_uint4(o[0], o[1], o[2], o[3]);
-                        *reinterpret_cast<uint4 *>(slab + i * 1024 + (x ^ 16)) = make_uint4(o[4], o[5], o[6], o[7]);
+                    for (int h = 0; h < 2; ++h) {
+                        uint4 c[2];
+                        uint2 tb[2];   // read before the stores
+#pragma unroll
+                        for (int i = 0; i < 2; ++i) {
+                            c[i] = *reinterpret_cast<const uint4 *>(smem + stage_at + st * kStage + (2 * h + i) * 512);
+                            tb[i] = sh.table[smem[pick_at + pb * kPicks + (2 * h + i) * 128 + k * 4]];
+                        }
+#pragma unroll
+                        for (int i = 0; i < 2; ++i) {
+                            uint32_t o[8];
+                            expand8(c[i].x, tb[i], o[0], o[1]);
+                            expand8(c[i].y, tb[i], o[2], o[3]);
+                            expand8(c[i].z, tb[i], o[4], o[5]);
+                            expand8(c[i].w, tb[i], o[6], o[7]);
+                            *reinterpret_cast<uint4 *>(slab + (2 * h + i) * 1024 + x) = make_uint4(o[0], o[1], o[2], o[3]);
+                            *reinterpret_cast<uint4 *>(slab + (2 * h + i) * 1024 + (x ^ 16)) = make_uint4(o[4], o[5], o[6], o[7]);
+                        }
                     }
                     fence_proxy_async_smem();
                     __syncwarp();
                     if (lane == 0) {
                         mbar_arrive(bar(sh.slab_full[sl]));
                         mbar_arrive(bar(sh.stage_empty[st]));
-                        if (k == 3) mbar_arrive(bar(sh.pick_empty[pb]));
+                        if (k >= 2) mbar_arrive(bar(sh.pick_empty[pb]));
                     }
                 }
             }
