@@ -107,6 +107,9 @@ struct Fp4Params {
     long long ld;
     const int *lens;
     float *ws_o, *ws_m, *ws_l;   // [slots][H] (x r): sum of P c, M - kBias, l
+    int2 *ws_seq;                // [B] per sequence: its first virtual unit and first chunk number
+    int *ws_share;               // [G + 1] the shares' first virtual units
+    const __nv_bfloat16 *w_uv;   // asked into L2 for the merge
     int *err;
     int B, H, max_len, G;
     float scale_log2;
@@ -199,6 +202,20 @@ struct Walk {
         return false;
     }
 };
+
+// Where each sequence and each share lies on the axis, for the merge.
+__device__ __forceinline__ void write_seq(const Fp4Params &p, int lane) {
+    int run = 0, chunks = 0;
+    for (int i0 = 0; i0 < p.B; i0 += 32) {
+        const int len = i0 + lane < p.B ? read_len(p.lens, i0 + lane, p.max_len, nullptr) : 0;
+        const int u = static_cast<int>(units_of(len)), n = len > 0 ? chunks_of(len) : 0;
+        const int incl = warp_scan(u, lane), nincl = warp_scan(n, lane);
+        if (i0 + lane < p.B) p.ws_seq[i0 + lane] = make_int2(run + incl - u, chunks + nincl - n);
+        run += __shfl_sync(0xffffffffu, incl, 31);
+        chunks += __shfl_sync(0xffffffffu, nincl, 31);
+    }
+    for (int c = lane; c <= p.G; c += 32) p.ws_share[c] = static_cast<int>(share_lo(run, c, p.G));
+}
 
 // The units of a walk, one after the other; rows = 0 at the end.
 struct Units {
@@ -477,6 +494,11 @@ __global__ void __launch_bounds__(Fp4Layout<HP>::kThreads, 1)
                 }
             }
             if (!ok) *abort_flag = 1;
+            {   // this CTA's part of W_UV into L2: the cache's rows have pushed it out
+                const long long bytes = static_cast<long long>(p.H) * kDV * kR * 2, from = bytes * blockIdx.x / gridDim.x & ~15ll,
+                                to = bytes * (blockIdx.x + 1) / gridDim.x & ~15ll;
+                if (to > from) bulk_prefetch_l2(reinterpret_cast<const uint8_t *>(p.w_uv) + from, static_cast<uint32_t>(to - from));
+            }
             // no load may still be landing when the CTA exits
             for (uint32_t k = it > kStages ? it - kStages : 0; k < it; ++k)
                 wait_bar(bar(sh.stage_full[k % kStages]), (k / kStages) & 1, p.err);
@@ -507,7 +529,9 @@ __global__ void __launch_bounds__(Fp4Layout<HP>::kThreads, 1)
                 }
             }
             if (!ok) *abort_flag = 1;
-        } else if (warp == 2 && lane == 0) {
+        } else if (warp == 2) {
+            if (blockIdx.x == 0) write_seq(p, lane);   // its first product is far off
+            if (lane == 0) {
             // ---- O^T += c^T . P^T: slab t holds latent columns [128 t, 128 t + 128)
             constexpr uint32_t idesc = make_idesc_e4m3(128, N, 1, 1), idesc_lo = idesc | 1u << 10;   // B: e5m2
             const uint64_t p0 = make_smem_desc(base + L::P, kSlab, 1024), c0 = make_smem_desc(base + L::C, kSlab, 1024);
@@ -533,6 +557,7 @@ __global__ void __launch_bounds__(Fp4Layout<HP>::kThreads, 1)
                 }
             }
             if (!ok) *abort_flag = 1;
+            }
         }
     } else if (warp < 4 + kSoftWarps) {
         regs_acquire<L::kRegsSoft>();
@@ -833,23 +858,177 @@ __global__ void __launch_bounds__(Fp4Layout<HP>::kThreads, 1)
 }
 
 // ------------------------------------------------------------------ merge
-constexpr int kMRows = 32;                          // sequences per CTA
+struct MergeParams {
+    const int *lens;
+    const int2 *ws_seq;
+    const int *ws_share;
+    const float *ws_o, *ws_m, *ws_l;
+    const __nv_bfloat16 *w_uv, *gate;
+    __nv_bfloat16 *out;
+    int *err;
+    int B, H, max_len, G;
+};
+
+constexpr int kMaxShares = 512;   // share boundaries that the merge keeps in shared memory
+
+// Log-sum-exp join of a sequence's segments for one head by one warp, which takes every `per`-th share of the axis from
+// the `sub`-th on: o = sum of 2^(m - M) ws_o in the lane's columns 4 lane + 128 q, L = sum of 2^(m - M) l.
+template <int kFly>   // segments whose rows are in flight at a time
+__device__ __forceinline__ void join_segments(const MergeParams &p, const int *shares, int2 at, int h, int len, int sub,
+                                              int per, int lane, float (&o)[16], float &M, float &L) {
+    M = -INFINITY, L = 0.f;
+#pragma unroll
+    for (int k = 0; k < 16; ++k) o[k] = 0.f;
+    if (len <= 0) return;
+    const int chunks = chunks_of(len);
+    int c_first = 0;
+    for (int j = 0; j < chunks; ++j) {
+        const int rows = min(kChunkRows, len - j * kChunkRows);
+        const int r0 = at.x + j * kChunkSpan + kOverUnits, r1 = r0 + (rows + kRows - 1) / kRows;
+        if (j == 0)   // the share that holds r0: from an estimate on, as shares are equal but for a unit
+            c_first = min(p.G - 1, static_cast<int>(static_cast<float>(r0) * p.G / shares[p.G]));
+        while (c_first > 0 && shares[c_first] > r0) --c_first;
+        while (c_first + 1 < p.G && shares[c_first + 1] <= r0) ++c_first;
+        for (int c0 = c_first + sub; c0 < p.G && shares[c0] < r1; c0 += 32 * per) {
+            const int c = c0 + lane * per;
+            const bool has = c < p.G && min(shares[c + 1], r1) > max(shares[c], r0);
+            const size_t slot = static_cast<size_t>(c + at.y + j) * p.H + h;
+            const float m = has ? p.ws_m[slot] : -INFINITY, l = has ? p.ws_l[slot] : 0.f;
+            float w = 0.f;
+            bool first = true;
+            for (unsigned left = __ballot_sync(0xffffffffu, has); left;) {
+                float4 v[kFly][4];
+                int from[kFly];
+#pragma unroll
+                for (int i = 0; i < kFly; ++i) {
+                    from[i] = left ? __ffs(left) - 1 : -1;
+                    left &= left - 1;
+                    const size_t row = __shfl_sync(0xffffffffu, slot, max(from[i], 0));
+                    const float4 *src = reinterpret_cast<const float4 *>(p.ws_o + row * kR) + lane;
+#pragma unroll
+                    for (int q = 0; q < 4; ++q) v[i][q] = from[i] >= 0 ? src[32 * q] : make_float4(0.f, 0.f, 0.f, 0.f);
+                }
+                if (first) {   // the weights, once the rows are on their way
+                    first = false;
+                    const float top = fmaxf(M, warp_max(m)), f = M == -INFINITY ? 0.f : fast_exp2(M - top);
+                    w = has ? fast_exp2(m - top) : 0.f;
+                    float s = has ? w * l : 0.f;
+#pragma unroll
+                    for (int q = 16; q >= 1; q >>= 1) s += __shfl_xor_sync(0xffffffffu, s, q);
+                    L = L * f + s;
+                    M = top;
+#pragma unroll
+                    for (int k = 0; k < 16; ++k) o[k] *= f;
+                }
+#pragma unroll
+                for (int i = 0; i < kFly; ++i) {
+                    const float wi = __shfl_sync(0xffffffffu, w, max(from[i], 0));
+                    if (from[i] < 0) continue;
+#pragma unroll
+                    for (int q = 0; q < 4; ++q) {
+                        o[4 * q] = fmaf(wi, v[i][q].x, o[4 * q]);
+                        o[4 * q + 1] = fmaf(wi, v[i][q].y, o[4 * q + 1]);
+                        o[4 * q + 2] = fmaf(wi, v[i][q].z, o[4 * q + 2]);
+                        o[4 * q + 3] = fmaf(wi, v[i][q].w, o[4 * q + 3]);
+                    }
+                }
+            }
+        }
+    }
+}
+__device__ __forceinline__ float gated(const __nv_bfloat16 *gate, size_t at, float y) {
+    return gate ? y * __fdividef(1.f, 1.f + fast_exp2(-__bfloat162float(gate[at]) * kLog2e)) : y;
+}
+
+// Few (head, sequence) pairs: a CTA per head and kSeqs sequences, fp32 products.  W_UV[h] is in registers before the
+// attention is done (a warp takes eight of its rows, a lane 16 columns of each); 16 / kSeqs warps join a sequence's
+// segments and one of them their parts.
+constexpr int kDotThreads = 512;
+template <int kSeqs>
+__global__ void __launch_bounds__(kDotThreads, 1) fp4_merge_dot_kernel(const MergeParams p) {
+    constexpr int kPer = 16 / kSeqs;
+    __shared__ __align__(16) float s_part[16][kR];
+    __shared__ __align__(16) float s_lat[kSeqs][kR];
+    __shared__ float s_m[16], s_l[16];
+    __shared__ int s_shares[kMaxShares + 1];
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int h = blockIdx.x, b0 = static_cast<int>(blockIdx.y) * kSeqs, nb = min(kSeqs, p.B - b0);
+    uint4 w[8][2];
+    const uint4 *src = reinterpret_cast<const uint4 *>(p.w_uv + (static_cast<size_t>(h) * kDV + warp * 8) * kR) + lane * 2;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) w[i][0] = __ldg(src + i * (kR / 8)), w[i][1] = __ldg(src + i * (kR / 8) + 1);
+    const int i = warp / kPer, b = b0 + min(i, nb - 1), len = i < nb ? read_len(p.lens, b, p.max_len, nullptr) : 0;
+    grid_dependency_wait();   // the segments are complete and visible after this
+    for (int c = threadIdx.x; c <= p.G; c += kDotThreads) s_shares[c] = p.ws_share[c];
+    const int2 at = p.ws_seq[b];
+    __syncthreads();
+    {
+        float o[16], M, L;
+        join_segments<2>(p, s_shares, at, h, len, warp % kPer, kPer, lane, o, M, L);
+        float4 *mine = reinterpret_cast<float4 *>(s_part[warp]) + lane;
+#pragma unroll
+        for (int q = 0; q < 4; ++q) mine[32 * q] = make_float4(o[4 * q], o[4 * q + 1], o[4 * q + 2], o[4 * q + 3]);
+        if (lane == 0) s_m[warp] = M, s_l[warp] = L;
+    }
+    __syncthreads();
+    for (int k = threadIdx.x; k < nb * kR; k += kDotThreads) {
+        const int s = k / kR, col = k % kR;
+        float M = -INFINITY, L = 0.f, x = 0.f;
+#pragma unroll
+        for (int q = 0; q < kPer; ++q) M = fmaxf(M, s_m[s * kPer + q]);
+        for (int q = 0; q < kPer; ++q) {
+            const float m = s_m[s * kPer + q];
+            if (m == -INFINITY) continue;   // a warp without a segment
+            const float f = fast_exp2(m - M);
+            L = fmaf(f, s_l[s * kPer + q], L);
+            x = fmaf(f, s_part[s * kPer + q][col], x);
+        }
+        s_lat[s][col] = M == -INFINITY ? 0.f : x / L;   // (an empty sequence has no segments)
+    }
+    __syncthreads();
+    for (int s = 0; s < nb; ++s) {
+        const float4 *lat = reinterpret_cast<const float4 *>(s_lat[s]) + lane * 4;
+        const float4 a[4] = {lat[0], lat[1], lat[2], lat[3]};
+        float y[8];
+#pragma unroll
+        for (int v = 0; v < 8; ++v) {
+            const uint32_t x[8] = {w[v][0].x, w[v][0].y, w[v][0].z, w[v][0].w, w[v][1].x, w[v][1].y, w[v][1].z, w[v][1].w};
+            const float c[16] = {a[0].x, a[0].y, a[0].z, a[0].w, a[1].x, a[1].y, a[1].z, a[1].w,
+                                 a[2].x, a[2].y, a[2].z, a[2].w, a[3].x, a[3].y, a[3].z, a[3].w};
+            y[v] = 0.f;
+#pragma unroll
+            for (int k = 0; k < 8; ++k) {
+                y[v] = fmaf(__uint_as_float(x[k] << 16), c[2 * k], y[v]);
+                y[v] = fmaf(__uint_as_float(x[k] & 0xFFFF0000u), c[2 * k + 1], y[v]);
+            }
+        }
+        // eight sums over the warp: halve the number of values held with each of the first three exchanges
+#pragma unroll
+        for (int k = 4; k >= 1; k >>= 1) {
+            const bool up = lane & k;
+#pragma unroll
+            for (int v = 0; v < k; ++v) {
+                const float keep = up ? y[v + k] : y[v], give = up ? y[v] : y[v + k];
+                y[v] = keep + __shfl_xor_sync(0xffffffffu, give, k);
+            }
+        }
+        y[0] += __shfl_xor_sync(0xffffffffu, y[0], 8);
+        y[0] += __shfl_xor_sync(0xffffffffu, y[0], 16);
+        if (lane < 8) {   // lane v: output column 8 warp + v
+            const size_t at = (static_cast<size_t>(b0 + s) * p.H + h) * kDV + warp * 8 + lane;
+            p.out[at] = __float2bfloat16(gated(p.gate, at, y[0]));
+        }
+    }
+}
+
+// Many: a CTA per head and 32 sequences; o_lat as bf16 hi + lo, the product on the tensor cores.
+constexpr int kMRows = 32;
 constexpr int kMergeThreads = 512;
 constexpr uint32_t kOSlab = 2 * kMRows * 128;       // o_lat [hi rows | lo rows] x 64 latent columns, bf16
 constexpr uint32_t kWSlab = kDV * 128;              // W_UV[h] [128 x 64 latent columns]
 constexpr int kWStages = 2;
 constexpr uint32_t MW_OFF = 8 * kOSlab, MBAR_OFF = MW_OFF + kWStages * kWSlab;
 constexpr uint32_t kSmemMerge = MBAR_OFF + 128 + 1024;
-static_assert(16 * kR * 4 <= 8 * kOSlab, "the warps' partial rows fit the o_lat tile");
-
-struct MergeParams {
-    const int *lens;
-    const float *ws_o, *ws_m, *ws_l;
-    const __nv_bfloat16 *gate;
-    __nv_bfloat16 *out;
-    int *err;
-    int B, H, max_len, G;
-};
 
 __global__ void __launch_bounds__(kMergeThreads, 2)
     fp4_merge_kernel(const __grid_constant__ CUtensorMap tm_wuv, const MergeParams p) {
@@ -858,9 +1037,7 @@ __global__ void __launch_bounds__(kMergeThreads, 2)
     uint64_t *w_full = reinterpret_cast<uint64_t *>(smem_raw + (base - raw) + MBAR_OFF), *w_empty = w_full + kWStages,
              *done = w_empty + kWStages;
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(done + 1);
-    __shared__ long long s_pre[kMRows], s_chunk[kMRows], s_total;   // per sequence: first virtual unit, first chunk number
-    __shared__ int s_len[kMRows];
-    __shared__ float s_m[16], s_l[16];
+    __shared__ int s_shares[kMaxShares + 1];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int h = blockIdx.x, b0 = static_cast<int>(blockIdx.y) * kMRows, nb = min(kMRows, p.B - b0);
     if (threadIdx.x == 0) {
@@ -885,134 +1062,29 @@ __global__ void __launch_bounds__(kMergeThreads, 2)
         for (int k = 0; k < kWStages; ++k) load_w(k);
         for (int k = kWStages; k < 8; ++k) tma_prefetch_l2_2d(&tm_wuv, k * 64, h * kDV);
     }
-    if (warp == 1) {
-        long long run = 0, chunks = 0;
-        for (int i0 = 0; i0 < p.B; i0 += 32) {
-            const int b = i0 + lane;
-            const int len = b < p.B ? read_len(p.lens, b, p.max_len, nullptr) : 0;
-            const long long u = units_of(len), incl = warp_scan(u, lane);
-            const int n = len > 0 ? chunks_of(len) : 0, nincl = warp_scan(n, lane);
-            if (b >= b0 && b < b0 + nb) {
-                s_pre[b - b0] = run + incl - u;
-                s_chunk[b - b0] = chunks + nincl - n;
-                s_len[b - b0] = len;
-            }
-            run += __shfl_sync(0xffffffffu, incl, 31);
-            chunks += __shfl_sync(0xffffffffu, nincl, 31);
-        }
-        if (lane == 0) s_total = run;
-    }
-    __syncthreads();
-    const long long total = s_total;
     // launched as a programmatic dependent: what is above overlaps the attention's tail, its segments are complete
     // and visible after this
     grid_dependency_wait();
 
-    // `per` warps share a sequence (all 16 when it is alone): warp `sub` takes every per-th share of the work axis.
-    // A lane holds four latent columns of each 128: 4 lane + 128 q.
-    int per = 16;
-    while (per > 1 && 16 / per < nb) per >>= 1;
-    const int sub = warp % per;
-    float o[16], M = -INFINITY, Lsum = 0.f;
-    auto put = [&](int i, const float (&x)[16], float mul) {   // row i of the o_lat tile, hi and lo parts
+    for (int c = threadIdx.x; c <= p.G; c += kMergeThreads) s_shares[c] = p.ws_share[c];
+    __syncthreads();
+    for (int i = warp; i < nb; i += kMergeThreads / 32) {
+        const int len = read_len(p.lens, b0 + i, p.max_len, nullptr);
+        float o[16], M, L;
+        join_segments<2>(p, s_shares, p.ws_seq[b0 + i], h, len, 0, 1, lane, o, M, L);
+        const float mul = len > 0 ? 1.f / L : 0.f;
 #pragma unroll
-        for (int q = 0; q < 4; ++q) {
+        for (int q = 0; q < 4; ++q) {   // row i of the o_lat tile, hi and lo parts
             float y[4], z[4];
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
-                y[k] = x[4 * q + k] * mul;
+                y[k] = o[4 * q + k] * mul;
                 z[k] = y[k] - __bfloat162float(__float2bfloat16(y[k]));
             }
-            const uint32_t at = base + (2 * q + (lane >> 4)) * kOSlab + 8 * (lane & 1);
-            const uint32_t ch = (lane & 15) >> 1;
-            asm volatile("st.shared.v2.b32 [%0], {%1, %2};" ::"r"(at + sw128_offset(i, ch)), "r"(pack_bf16x2(y[0], y[1])),
-                         "r"(pack_bf16x2(y[2], y[3])) : "memory");
-            asm volatile("st.shared.v2.b32 [%0], {%1, %2};" ::"r"(at + sw128_offset(kMRows + i, ch)),
-                         "r"(pack_bf16x2(z[0], z[1])), "r"(pack_bf16x2(z[2], z[3])) : "memory");
+            const uint32_t at = base + (2 * q + (lane >> 4)) * kOSlab + 8 * (lane & 1), ch = (lane & 15) >> 1;
+            st_shared_v2(at + sw128_offset(i, ch), pack_bf16x2(y[0], y[1]), pack_bf16x2(y[2], y[3]));
+            st_shared_v2(at + sw128_offset(kMRows + i, ch), pack_bf16x2(z[0], z[1]), pack_bf16x2(z[2], z[3]));
         }
-    };
-    for (int i = warp / per; i < nb; i += 16 / per) {
-        const int len = s_len[i];
-        M = -INFINITY, Lsum = 0.f;
-#pragma unroll
-        for (int k = 0; k < 16; ++k) o[k] = 0.f;
-        const int chunks = len > 0 ? chunks_of(len) : 0;
-        for (int j = 0; j < chunks; ++j) {
-            const int rows = min(kChunkRows, len - j * kChunkRows);
-            const long long r0 = s_pre[i] + static_cast<long long>(j) * kChunkSpan + kOverUnits,
-                            r1 = r0 + (rows + kRows - 1) / kRows;
-            const int c_first = static_cast<int>(((r0 + 1) * p.G - 1) / total);
-            for (int c0 = c_first + sub; c0 < p.G && share_lo(total, c0, p.G) < r1; c0 += 32 * per) {
-                const int c = c0 + lane * per;
-                const bool has = c < p.G && min(share_lo(total, c + 1, p.G), r1) > max(share_lo(total, c, p.G), r0);
-                const size_t slot = static_cast<size_t>(c + s_chunk[i] + j) * p.H + h;
-                const float m = has ? __ldg(p.ws_m + slot) : -INFINITY;
-                float w = m;
-#pragma unroll
-                for (int q = 16; q >= 1; q >>= 1) w = fmaxf(w, __shfl_xor_sync(0xffffffffu, w, q));
-                const float top = fmaxf(M, w), f = M == -INFINITY ? 0.f : fast_exp2(M - top);
-                w = has ? fast_exp2(m - top) : 0.f;
-                float s = has ? w * __ldg(p.ws_l + slot) : 0.f;
-#pragma unroll
-                for (int q = 16; q >= 1; q >>= 1) s += __shfl_xor_sync(0xffffffffu, s, q);
-                Lsum = Lsum * f + s;
-                M = top;
-#pragma unroll
-                for (int k = 0; k < 16; ++k) o[k] *= f;
-                for (unsigned left = __ballot_sync(0xffffffffu, has); left;) {   // two segments' loads in flight
-                    const int a = __ffs(left) - 1;
-                    left &= left - 1;
-                    const int b = left ? __ffs(left) - 1 : a;
-                    const float wa = __shfl_sync(0xffffffffu, w, a), wb = left ? __shfl_sync(0xffffffffu, w, b) : 0.f;
-                    const float4 *sa = reinterpret_cast<const float4 *>(p.ws_o + __shfl_sync(0xffffffffu, slot, a) * kR) + lane;
-                    const float4 *sb = reinterpret_cast<const float4 *>(p.ws_o + __shfl_sync(0xffffffffu, slot, b) * kR) + lane;
-                    const bool two = left != 0;
-                    left &= left - 1;
-                    float4 va[4], vb[4];
-#pragma unroll
-                    for (int q = 0; q < 4; ++q) {
-                        va[q] = __ldg(sa + 32 * q);
-                        vb[q] = two ? __ldg(sb + 32 * q) : make_float4(0.f, 0.f, 0.f, 0.f);
-                    }
-#pragma unroll
-                    for (int q = 0; q < 4; ++q) {
-                        o[4 * q] += wa * va[q].x + wb * vb[q].x;
-                        o[4 * q + 1] += wa * va[q].y + wb * vb[q].y;
-                        o[4 * q + 2] += wa * va[q].z + wb * vb[q].z;
-                        o[4 * q + 3] += wa * va[q].w + wb * vb[q].w;
-                    }
-                }
-            }
-        }
-        if (per == 1) put(i, o, len > 0 ? 1.f / Lsum : 0.f);
-    }
-    if (per > 1) {   // join the warps of each sequence (here every warp has had at most one)
-        float *part = reinterpret_cast<float *>(smem_raw + (base - raw));
-        float4 *mine = reinterpret_cast<float4 *>(part + warp * kR) + lane;
-#pragma unroll
-        for (int q = 0; q < 4; ++q) mine[32 * q] = make_float4(o[4 * q], o[4 * q + 1], o[4 * q + 2], o[4 * q + 3]);
-        if (lane == 0) s_m[warp] = M, s_l[warp] = Lsum;
-        __syncthreads();
-        const int i = warp / per, first = i * per;
-        if (sub == 0 && i < nb) {
-            M = -INFINITY, Lsum = 0.f;
-            for (int k = 0; k < per; ++k) M = fmaxf(M, s_m[first + k]);
-#pragma unroll
-            for (int k = 0; k < 16; ++k) o[k] = 0.f;
-            for (int k = 0; k < per; ++k) {
-                if (s_m[first + k] == -INFINITY) continue;   // a warp without a segment
-                const float w = fast_exp2(s_m[first + k] - M);
-                Lsum += w * s_l[first + k];
-                const float4 *src = reinterpret_cast<const float4 *>(part + (first + k) * kR) + lane;
-#pragma unroll
-                for (int q = 0; q < 4; ++q) {
-                    const float4 v = src[32 * q];
-                    o[4 * q] += w * v.x, o[4 * q + 1] += w * v.y, o[4 * q + 2] += w * v.z, o[4 * q + 3] += w * v.w;
-                }
-            }
-        }
-        __syncthreads();   // the partial rows are read before the tile is written over them
-        if (sub == 0 && i < nb) put(i, o, s_len[i] > 0 ? 1.f / Lsum : 0.f);
     }
     fence_proxy_async_smem();
     tc_fence_before();
@@ -1056,9 +1128,7 @@ __global__ void __launch_bounds__(kMergeThreads, 2)
         for (int k = 0; k < 16; ++k) {
             if (i0 + k >= nb) break;
             const size_t off = (static_cast<size_t>(b0 + i0 + k) * p.H + h) * kDV + v;
-            float y = hi[k] + lo[k];
-            if (p.gate) y *= __fdividef(1.f, 1.f + fast_exp2(-__bfloat162float(p.gate[off]) * kLog2e));
-            p.out[off] = __float2bfloat16(y);
+            p.out[off] = __float2bfloat16(gated(p.gate, off, hi[k] + lo[k]));
         }
     }
     tc_fence_before();
@@ -1097,11 +1167,12 @@ cudaError_t launch_attention(const CUtensorMap &codes, const Fp4Params &p, cudaS
 }  // namespace
 
 size_t decode_fp4_workspace_bytes(int B, int H, int max_len, int num_sms) {
-    return slot_count(B, max_len, num_sms) * H * (kR + 2) * sizeof(float);
+    return static_cast<size_t>(B) * sizeof(int2) + (num_sms + 1) * sizeof(int) + 8 + slot_count(B, max_len, num_sms) * H * (kR + 2) * sizeof(float);
 }
 
 cudaError_t launch_decode_fp4(const DecodeArgs &a, cudaStream_t s) {
     if (!decode_bf16_supports(a.H, a.d_v, a.r)) return cudaErrorInvalidValue;
+    if (a.num_sms > kMaxShares) return cudaErrorInvalidConfiguration;
     Fp4Params p;
     p.q_abs = static_cast<const __nv_bfloat16 *>(a.q_abs);
     p.c4 = static_cast<const uint8_t *>(a.c_cache);
@@ -1112,10 +1183,13 @@ cudaError_t launch_decode_fp4(const DecodeArgs &a, cudaStream_t s) {
     p.max_len = a.max_len;
     p.G = a.num_sms;
     const size_t slots = slot_count(a.B, a.max_len, p.G);
-    if (slots * a.H * (kR + 2) * sizeof(float) > a.workspace_bytes) return cudaErrorInvalidValue;
+    if (decode_fp4_workspace_bytes(a.B, a.H, a.max_len, a.num_sms) > a.workspace_bytes) return cudaErrorInvalidValue;
     p.ws_o = static_cast<float *>(a.workspace);
     p.ws_m = p.ws_o + slots * a.H * kR;
     p.ws_l = p.ws_m + slots * a.H;
+    p.ws_seq = reinterpret_cast<int2 *>((reinterpret_cast<uintptr_t>(p.ws_l + slots * a.H) + 7) & ~static_cast<uintptr_t>(7));
+    p.ws_share = reinterpret_cast<int *>(p.ws_seq + a.B);
+    p.w_uv = static_cast<const __nv_bfloat16 *>(a.w_uv);
     p.err = a.dev_err;
     p.scale_log2 = a.scale * kLog2e;
     CUtensorMap tm_codes, tm_wuv;
@@ -1138,14 +1212,9 @@ cudaError_t launch_decode_fp4(const DecodeArgs &a, cudaStream_t s) {
                     : a.H <= 64 ? launch_attention<64>(tm_codes, p, s)
                                 : launch_attention<96>(tm_codes, p, s);
     if (e != cudaSuccess) return e;
-    e = cudaFuncSetAttribute(fp4_merge_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(kSmemMerge));
-    if (e != cudaSuccess) return e;
-    const MergeParams mp{a.lens, p.ws_o, p.ws_m, p.ws_l, static_cast<const __nv_bfloat16 *>(a.gate),
+    const MergeParams mp{a.lens, p.ws_seq, p.ws_share, p.ws_o, p.ws_m, p.ws_l, p.w_uv, static_cast<const __nv_bfloat16 *>(a.gate),
                          static_cast<__nv_bfloat16 *>(a.out), a.dev_err, a.B, a.H, a.max_len, p.G};
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(a.H, (a.B + kMRows - 1) / kMRows);
-    cfg.blockDim = dim3(kMergeThreads);
-    cfg.dynamicSmemBytes = kSmemMerge;
     cfg.stream = s;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -1153,6 +1222,22 @@ cudaError_t launch_decode_fp4(const DecodeArgs &a, cudaStream_t s) {
     cfg.attrs = attr;
     cfg.numAttrs = 1;
     note_launch();
+    // up to eight sequences per CTA as long as one wave of CTAs takes them all
+    for (int seqs = 1; seqs <= 8; seqs *= 2)
+        if (static_cast<long long>(a.H) * ((a.B + seqs - 1) / seqs) <= a.num_sms) {
+            cfg.gridDim = dim3(a.H, (a.B + seqs - 1) / seqs);
+            cfg.blockDim = dim3(kDotThreads);
+            return seqs == 1   ? cudaLaunchKernelEx(&cfg, fp4_merge_dot_kernel<1>, mp)
+                   : seqs == 2 ? cudaLaunchKernelEx(&cfg, fp4_merge_dot_kernel<2>, mp)
+                   : seqs == 4 ? cudaLaunchKernelEx(&cfg, fp4_merge_dot_kernel<4>, mp)
+                               : cudaLaunchKernelEx(&cfg, fp4_merge_dot_kernel<8>, mp);
+        }
+    if ((e = cudaFuncSetAttribute(fp4_merge_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                  static_cast<int>(kSmemMerge))) != cudaSuccess)
+        return e;
+    cfg.gridDim = dim3(a.H, (a.B + kMRows - 1) / kMRows);
+    cfg.blockDim = dim3(kMergeThreads);
+    cfg.dynamicSmemBytes = kSmemMerge;
     return cudaLaunchKernelEx(&cfg, fp4_merge_kernel, tm_wuv, mp);
 }
 
