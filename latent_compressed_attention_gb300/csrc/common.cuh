@@ -153,6 +153,13 @@ __device__ __forceinline__ void bulk_prefetch_l2(const void *ptr, uint32_t bytes
                  : "memory");
 }
 
+// Untiled copy of `bytes` (a multiple of 16) of global memory to shared memory, both 16-byte aligned.
+__device__ __forceinline__ void bulk_load(uint32_t dst, const void *src, uint32_t bytes, uint32_t bar) {
+    asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst),
+                 "l"(reinterpret_cast<uint64_t>(src)), "r"(bytes), "r"(bar)
+                 : "memory");
+}
+
 // L2 cache policies for the .L2::cache_hint forms: lines filled or touched
 // with evict_first leave L2 before normal lines; evict_last ones stay longer.
 __device__ __forceinline__ uint64_t l2_policy_evict_first() {

@@ -46,25 +46,23 @@ constexpr int kDV = 128;
 constexpr int kRows = 128;                 // cache rows per unit
 constexpr int kChunkUnits = 256;           // units of a sequence that share one running maximum per segment
 constexpr int kChunkRows = kChunkUnits * kRows;
-constexpr int kOverUnits = 2;              // what starting a segment costs, in units (query, first fill, drain)
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kBias = 8.f;               // P = 2^(a - M + kBias)
 constexpr float kHead = 1.f, kSlack = 0.75f;   // a new maximum is set kHead above the row that forced it
 constexpr uint32_t kSlab = 16384;          // [128 rows x 128 latent] e4m3, 128-byte swizzle
 constexpr uint32_t kPicks = 2048;          // [128 rows x 16 groups] table numbers of a unit
 constexpr uint32_t kStage = 8192;          // codes of one slab: [128 rows x 64 bytes]
-constexpr int kPickBufs = 2;
+constexpr int kPickBufs = 4;
 constexpr int kTables = 22;                // exponents -14 (all zero) .. 6 below the row's largest, then NaN
 constexpr int kMaxSoftWarps = 16, kMaxHW = 24;
 
 struct Fp4Shared {
     uint64_t stage_full[4], stage_empty[4];
-    uint64_t pick_full[kPickBufs], pick_empty[kPickBufs];
+    uint64_t scale_full[kPickBufs], pick_full[kPickBufs], pick_empty[kPickBufs];
     uint64_t slab_full[8], slab_free[8];
     uint64_t s_full[2], s_free[2], q_ready;
     uint64_t p_full[2], p_free[2];
     uint32_t tmem_base;
-    int abort;
     uint2 table[kTables];
     int16_t ref[8][kRows];                 // per row of the last eight units: the power of two its tile is divided by
     alignas(16) float mul[96];             // per head: score factor
@@ -111,21 +109,21 @@ struct Fp4Params {
     int *ws_share;               // [G + 1] the shares' first virtual units
     const __nv_bfloat16 *w_uv;   // asked into L2 for the merge
     int *err;
-    int B, H, max_len, G;
+    int B, H, max_len, G, over;
     float scale_log2;
 };
 
 // ------------------------------------------------------------------ the work axis
-// Virtual units: a sequence is a run of chunks of up to kChunkUnits units, each preceded by kOverUnits.  Share c of G
+// Virtual units: a sequence is a run of chunks of up to kChunkUnits units, each preceded by `over` (what starting a segment
+// costs: its queries, the first fill, the drain).  Share c of G
 // owns [share_lo(c), share_lo(c + 1)); its part of chunk number v (over all sequences) is segment slot c + v: both
 // only grow along the axis and one of them does between two segments.
-constexpr int kChunkSpan = kOverUnits + kChunkUnits;
 __host__ __device__ __forceinline__ int chunks_of(int len) {
     return static_cast<int>((static_cast<unsigned>(len) + kChunkRows - 1u) / kChunkRows);
 }
-__device__ __forceinline__ long long units_of(int len) {   // virtual units of a sequence
+__device__ __forceinline__ long long units_of(int len, int over) {   // virtual units of a sequence
     const int full = len / kChunkRows, rest = len - full * kChunkRows;
-    return static_cast<long long>(full) * kChunkSpan + (rest > 0 ? kOverUnits + (rest + kRows - 1) / kRows : 0);
+    return static_cast<long long>(full) * (over + kChunkUnits) + (rest > 0 ? over + (rest + kRows - 1) / kRows : 0);
 }
 __device__ __forceinline__ long long share_lo(long long total, int c, int G) { return total * c / G; }
 __device__ __forceinline__ int read_len(const int *lens, int b, int max_len, int *err) {
@@ -151,21 +149,23 @@ struct Segment {
 // (Positions on the axis fit 32 bits: 2^31 units are 75 TB of cache.)
 struct Walk {
     const int *lens;
-    int B, max_len, c, b, j;     // chunk j of sequence b is next
+    int B, max_len, over, c, b, j;   // chunk j of sequence b is next
     int lo, hi, pre, v;          // its first virtual unit and its number
     // Every lane of a warp calls this; all get the same walk.
     __device__ void start(const Fp4Params &p, int share, int lane, int *err) {
-        lens = p.lens, B = p.B, max_len = p.max_len, c = share;
+        lens = p.lens, B = p.B, max_len = p.max_len, over = p.over, c = share;
         long long total = 0;
-        for (int i = lane; i < B; i += 32) total += units_of(read_len(lens, i, max_len, err));
+#pragma unroll 1
+        for (int i = lane; i < B; i += 32) total += units_of(read_len(lens, i, max_len, err), p.over);
 #pragma unroll
         for (int o = 16; o >= 1; o >>= 1) total += __shfl_xor_sync(0xffffffffu, total, o);
         lo = static_cast<int>(share_lo(total, share, p.G)), hi = static_cast<int>(share_lo(total, share + 1, p.G));
         b = B, j = 0, pre = hi, v = 0;
         int run = 0, chunks = 0;
+#pragma unroll 1
         for (int i0 = 0; i0 < B && lo < hi; i0 += 32) {
             const int len = i0 + lane < B ? read_len(lens, i0 + lane, max_len, nullptr) : 0;
-            const int u = static_cast<int>(units_of(len)), incl = warp_scan(u, lane);
+            const int u = static_cast<int>(units_of(len, p.over)), incl = warp_scan(u, lane);
             const int n = len > 0 ? chunks_of(len) : 0, nincl = warp_scan(n, lane);
             const unsigned past = __ballot_sync(0xffffffffu, run + incl > lo);
             if (past) {
@@ -173,8 +173,8 @@ struct Walk {
                 b = i0 + first;
                 pre = run + __shfl_sync(0xffffffffu, incl - u, first);
                 v = chunks + __shfl_sync(0xffffffffu, nincl - n, first);
-                j = (lo - pre) / kChunkSpan;
-                pre += j * kChunkSpan;
+                j = (lo - pre) / (over + kChunkUnits);
+                pre += j * (over + kChunkUnits);
                 v += j;
                 break;
             }
@@ -183,6 +183,7 @@ struct Walk {
         }
     }
     __device__ bool next(Segment &s) {
+#pragma unroll 1
         while (b < B && pre < hi) {
             const int len = read_len(lens, b, max_len, nullptr);
             if (len <= 0) {
@@ -191,7 +192,7 @@ struct Walk {
             }
             const int left = len - j * kChunkRows;   // > 0: the walk leaves a sequence with its last chunk
             const int units = left >= kChunkRows ? kChunkUnits : (left + kRows - 1) / kRows;
-            const int base = pre + kOverUnits, s0 = max(base, lo), s1 = min(base + units, hi);
+            const int base = pre + over, s0 = max(base, lo), s1 = min(base + units, hi);
             s.seq = b, s.len = len, s.slot = c + v;
             s.row0 = j * kChunkRows + (s0 - base) * kRows;
             s.units = s1 - s0;
@@ -206,14 +207,16 @@ struct Walk {
 // Where each sequence and each share lies on the axis, for the merge.
 __device__ __forceinline__ void write_seq(const Fp4Params &p, int lane) {
     int run = 0, chunks = 0;
+#pragma unroll 1
     for (int i0 = 0; i0 < p.B; i0 += 32) {
         const int len = i0 + lane < p.B ? read_len(p.lens, i0 + lane, p.max_len, nullptr) : 0;
-        const int u = static_cast<int>(units_of(len)), n = len > 0 ? chunks_of(len) : 0;
+        const int u = static_cast<int>(units_of(len, p.over)), n = len > 0 ? chunks_of(len) : 0;
         const int incl = warp_scan(u, lane), nincl = warp_scan(n, lane);
         if (i0 + lane < p.B) p.ws_seq[i0 + lane] = make_int2(run + incl - u, chunks + nincl - n);
         run += __shfl_sync(0xffffffffu, incl, 31);
         chunks += __shfl_sync(0xffffffffu, nincl, 31);
     }
+#pragma unroll 1
     for (int c = lane; c <= p.G; c += 32) p.ws_share[c] = static_cast<int>(share_lo(run, c, p.G));
 }
 
@@ -267,11 +270,9 @@ __device__ __forceinline__ void expand8(uint32_t w, uint2 table, uint32_t &o0, u
     o0 = byte_perm(table.x, table.y, m) | (byte_perm(w, w4, 0x1504) & 0x80808080u);
     o1 = byte_perm(table.x, table.y, m_hi) | (byte_perm(w, w4, 0x3726) & 0x80808080u);
 }
-// 16 bytes that are read once by this SM.
-__device__ __forceinline__ uint4 ld_stream(const uint8_t *p) {
-    uint4 v;
-    asm("ld.global.nc.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "l"(p));
-    return v;
+// A store whose line stays in L2.
+__device__ __forceinline__ void st_keep(float *p, float v, uint64_t policy) {
+    asm volatile("st.global.L2::cache_hint.f32 [%0], %1, %2;" ::"l"(p), "f"(v), "l"(policy) : "memory");
 }
 // A row's 16 scale bytes to the numbers of their tables; returns the largest of them, NaN bytes aside, in the range that
 // the format allows: what becomes e4m3's 2^6.
@@ -375,18 +376,17 @@ __device__ __forceinline__ float store_query(uint32_t q_base, int h, int lane, c
     return top >= 0x7F800000u ? __uint_as_float(0x7FFFFFFFu) : exp2_int(-e);
 }
 
-// mbar_wait that looks at the clock only every 256 tries.
-__device__ __forceinline__ bool wait_bar(uint32_t bar, uint32_t parity, int *err, const volatile int *abort = nullptr) {
+// mbar_wait that looks at the clock only every 256 tries and leaves the error to the caller: there are many of these, and
+// the kernel's loops have to share the instruction cache.
+__device__ __forceinline__ bool wait_bar(uint32_t bar, uint32_t parity) {
     uint64_t t0 = 0;
-    for (uint32_t i = 1; !mbar_try_wait(bar, parity); ++i) {
-        if ((i & 255u) != 0) continue;
-        if (abort && *abort) return false;
+    uint32_t tries = 0;
+#pragma unroll 1
+    while (!mbar_try_wait(bar, parity)) {
+        if ((++tries & 255u) != 0) continue;
         const uint64_t now = globaltimer_ns();
         if (t0 == 0) t0 = now;
-        if (now - t0 > MLA_WAIT_LIMIT_NS) {
-            record_error(err, kDevErrTimeout);
-            return false;
-        }
+        if (now - t0 > MLA_WAIT_LIMIT_NS) return false;
     }
     return true;
 }
@@ -394,7 +394,8 @@ __device__ __forceinline__ bool wait_bar(uint32_t bar, uint32_t parity, int *err
 // ------------------------------------------------------------------ attention
 template <int HP>
 __global__ void __launch_bounds__(Fp4Layout<HP>::kThreads, 1) 
-    fp4_attention_kernel(const __grid_constant__ CUtensorMap tm_codes, const Fp4Params p) {
+    fp4_attention_kernel(const __grid_constant__ CUtensorMap tm_codes, const __grid_constant__ CUtensorMap tm_scales,
+                         const Fp4Params p) {
     using L = Fp4Layout<HP>;
     constexpr bool kJoin = L::kJoin;
     constexpr int HW = L::HW, N = L::N, WC = L::WC, kSlabs = L::kSlabs, kPBufs = L::kPBufs, kSBufs = L::kSBufs, kStages = L::kStages;
@@ -403,18 +404,16 @@ __global__ void __launch_bounds__(Fp4Layout<HP>::kThreads, 1)
     const uint32_t raw = smem_u32(smem_raw), base = (raw + 1023u) & ~1023u;
     uint8_t *const smem = smem_raw + (base - raw);
     Fp4Shared &sh = *reinterpret_cast<Fp4Shared *>(smem + L::END);
-    volatile int *abort_flag = &sh.abort;
     auto bar = [](uint64_t &b) { return smem_u32(&b); };
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
     if (threadIdx.x == 0) {
         for (int i = 0; i < kStages; ++i) mbar_init(bar(sh.stage_full[i]), 1), mbar_init(bar(sh.stage_empty[i]), 4);
-        for (int i = 0; i < kPickBufs; ++i) mbar_init(bar(sh.pick_full[i]), 1), mbar_init(bar(sh.pick_empty[i]), kExpWarps);
+        for (int i = 0; i < kPickBufs; ++i) mbar_init(bar(sh.scale_full[i]), 1), mbar_init(bar(sh.pick_full[i]), 1), mbar_init(bar(sh.pick_empty[i]), kExpWarps);
         for (int i = 0; i < kSlabs; ++i) mbar_init(bar(sh.slab_full[i]), 4), mbar_init(bar(sh.slab_free[i]), 1);
         for (int i = 0; i < kSBufs; ++i) mbar_init(bar(sh.s_full[i]), 1), mbar_init(bar(sh.s_free[i]), kSoftWarps);
         for (int i = 0; i < kPBufs; ++i) mbar_init(bar(sh.p_full[i]), kSoftWarps), mbar_init(bar(sh.p_free[i]), 1);
         mbar_init(bar(sh.q_ready), kSoftWarps);
-        sh.abort = 0;
         fence_mbar_init();
     }
     if (threadIdx.x >= 64 && threadIdx.x < 64 + kTables) {   // magnitudes times 2^k as e4m3 bytes
@@ -443,57 +442,73 @@ __global__ void __launch_bounds__(Fp4Layout<HP>::kThreads, 1)
     if (warp < 4) {
         regs_release<L::kRegsCtl>();
         if (warp == 0) {
-            // ---- scale bytes to table numbers and refs, a unit or two ahead: a lane takes rows lane + 32 i
-            uint4 v[4];
-            Units unit;
+            // ---- a unit's scale bytes to table numbers, in place, and refs; the bytes are asked for three units ahead
+            Walk far = walk;
+            Segment far_seg;
+            Units unit, next;
             unit.start(walk, seg);
-            auto load = [&] {
-                const uint8_t *src = p.c4 + (static_cast<long long>(seg.seq) * p.max_len + unit.row(seg) + lane) * p.ld + kR / 2;
-#pragma unroll
-                for (int i = 0; i < 4; ++i)
-                    v[i] = lane + 32 * i < unit.rows ? ld_stream(src + 32 * i * p.ld) : make_uint4(0, 0, 0, 0);
-            };
-            if (unit.rows > 0) load();
+            next.start(far, far_seg);
             bool ok = true;
+            uint32_t asked = 0;
+            auto ask = [&] {
+                const uint32_t pb = asked % kPickBufs;
+                if (asked >= kPickBufs) ok = ok && wait_bar(bar(sh.pick_empty[pb]), (asked / kPickBufs - 1) & 1);
+                if (lane == 0) {
+                    mbar_arrive_expect_tx(bar(sh.scale_full[pb]), kPicks);
+                    tma_load_3d(base + L::PICK + pb * kPicks, &tm_scales, bar(sh.scale_full[pb]), kR / 2, next.row(far_seg),
+                                far_seg.seq);
+                }
+                ++asked;
+                next.next(far, far_seg);
+            };
+            for (int i = 0; i < kPickBufs - 1 && next.rows > 0; ++i) ask();
             for (uint32_t un = 0; unit.rows > 0; ++un) {
                 const uint32_t pb = un % kPickBufs;
-                // the expansion has begun with the unit two back, so it is done with the one before, for which products at
-                // most five back were done: the softmax has read what the ref slot held eight back
-                if (un >= kPickBufs) ok &= wait_bar(bar(sh.pick_empty[pb]), (un / kPickBufs - 1) & 1, p.err, abort_flag);
-                uint4 *const dst = reinterpret_cast<uint4 *>(smem + L::PICK + pb * kPicks) + lane;
+                ok = ok && wait_bar(bar(sh.scale_full[pb]), (un / kPickBufs) & 1);
+                // (the expansion is done with the unit four back and has begun with the slabs of none that the softmax is not
+                // done with six back: the ref slot, last used eight back, is free)
+                uint4 *const at = reinterpret_cast<uint4 *>(smem + L::PICK + pb * kPicks) + lane;
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    uint32_t w[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
+                for (int i = 0; i < 4; ++i) {   // a lane takes rows lane + 32 i
+                    const uint4 v = at[32 * i];
+                    uint32_t w[4] = {v.x, v.y, v.z, v.w};
                     const int top = row_picks(w);
                     const bool real = lane + 32 * i < unit.rows;   // rows past the end: zeros
-                    dst[32 * i] = real ? make_uint4(w[0], w[1], w[2], w[3]) : make_uint4(0, 0, 0, 0);
+                    at[32 * i] = real ? make_uint4(w[0], w[1], w[2], w[3]) : make_uint4(0, 0, 0, 0);
                     sh.ref[un & 7][lane + 32 * i] = static_cast<int16_t>(top - 127 - 6);
                 }
-                unit.next(walk, seg);
-                if (unit.rows > 0) load();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(bar(sh.pick_full[pb]));
+                unit.next(walk, seg);
+                if (next.rows > 0) ask();
             }
-            if (!ok) *abort_flag = 1;
+            if (!ok) {
+                record_error(p.err, kDevErrTimeout);
+                // no load may still be landing when the CTA exits
+                for (uint32_t k = asked > kPickBufs ? asked - kPickBufs : 0; k < asked; ++k)
+                    wait_bar(bar(sh.scale_full[k % kPickBufs]), (k / kPickBufs) & 1);
+            }
         } else if (warp == 3 && lane == 0) {
             // ---- TMA: a unit's codes, slab by slab
             tma_prefetch_desc(&tm_codes);
+            const uint64_t once = l2_policy_evict_first();
             uint32_t it = 0;
             bool ok = true;
             while (ok && walk.next(seg)) {
                 for (int u = 0; ok && u < seg.units; ++u) {
+#pragma unroll 1
                     for (int k = 0; k < 4; ++k, ++it) {
                         const uint32_t st = it % kStages;
                         if (it >= kStages &&
-                            !(ok = wait_bar(bar(sh.stage_empty[st]), (it / kStages - 1) & 1, p.err, abort_flag)))
+                            !(ok = wait_bar(bar(sh.stage_empty[st]), (it / kStages - 1) & 1)))
                             break;
                         mbar_arrive_expect_tx(bar(sh.stage_full[st]), kStage);
-                        tma_load_3d(base + L::STAGE + st * kStage, &tm_codes, bar(sh.stage_full[st]), k * 64,
-                                    seg.row0 + u * kRows, seg.seq);
+                        tma_load_3d_hint(base + L::STAGE + st * kStage, &tm_codes, bar(sh.stage_full[st]), k * 64,
+                                         seg.row0 + u * kRows, seg.seq, once);
                     }
                 }
             }
-            if (!ok) *abort_flag = 1;
+            if (!ok) record_error(p.err, kDevErrTimeout);
             {   // this CTA's part of W_UV into L2: the cache's rows have pushed it out
                 const long long bytes = static_cast<long long>(p.H) * kDV * kR * 2, from = bytes * blockIdx.x / gridDim.x & ~15ll,
                                 to = bytes * (blockIdx.x + 1) / gridDim.x & ~15ll;
@@ -501,7 +516,7 @@ __global__ void __launch_bounds__(Fp4Layout<HP>::kThreads, 1)
             }
             // no load may still be landing when the CTA exits
             for (uint32_t k = it > kStages ? it - kStages : 0; k < it; ++k)
-                wait_bar(bar(sh.stage_full[k % kStages]), (k / kStages) & 1, p.err);
+                wait_bar(bar(sh.stage_full[k % kStages]), (k / kStages) & 1);
         } else if (warp == 1 && lane == 0) {
             // ---- S^T = c . q^T: four slabs of K = 128
             constexpr uint32_t idesc = make_idesc_e4m3(128, N, 0, 0);
@@ -509,14 +524,15 @@ __global__ void __launch_bounds__(Fp4Layout<HP>::kThreads, 1)
             uint32_t it = 0, un = 0, ns = 0;
             bool ok = true;
             while (ok && walk.next(seg)) {
-                if (!(ok = wait_bar(bar(sh.q_ready), ns++ & 1, p.err, abort_flag))) break;
+                if (!(ok = wait_bar(bar(sh.q_ready), ns++ & 1))) break;
                 for (int u = 0; ok && u < seg.units; ++u, ++un) {
                     const uint32_t sb = un % kSBufs, d = tmem + L::S_COL + sb * N;
-                    if (un >= kSBufs && !(ok = wait_bar(bar(sh.s_free[sb]), (un / kSBufs - 1) & 1, p.err, abort_flag)))
+                    if (un >= kSBufs && !(ok = wait_bar(bar(sh.s_free[sb]), (un / kSBufs - 1) & 1)))
                         break;
+#pragma unroll 1
                     for (int k = 0; k < 4; ++k, ++it) {
                         const uint32_t sl = it % kSlabs;
-                        if (!(ok = wait_bar(bar(sh.slab_full[sl]), (it / kSlabs) & 1, p.err, abort_flag))) break;
+                        if (!(ok = wait_bar(bar(sh.slab_full[sl]), (it / kSlabs) & 1))) break;
                         tc_fence_after();
                         const uint64_t a = desc_add(c0, sl * kSlab), b = desc_add(q0, k * L::kQSlab);
 #pragma unroll
@@ -528,7 +544,7 @@ __global__ void __launch_bounds__(Fp4Layout<HP>::kThreads, 1)
                     if (ok) umma_commit(bar(sh.s_full[sb]));
                 }
             }
-            if (!ok) *abort_flag = 1;
+            if (!ok) record_error(p.err, kDevErrTimeout);
         } else if (warp == 2) {
             if (blockIdx.x == 0) write_seq(p, lane);   // its first product is far off
             if (lane == 0) {
@@ -540,11 +556,12 @@ __global__ void __launch_bounds__(Fp4Layout<HP>::kThreads, 1)
             while (ok && walk.next(seg)) {
                 for (int u = 0; ok && u < seg.units; ++u, ++un) {
                     const uint32_t pb = un % kPBufs;
-                    if (!(ok = wait_bar(bar(sh.p_full[pb]), (un / kPBufs) & 1, p.err, abort_flag))) break;
+                    if (!(ok = wait_bar(bar(sh.p_full[pb]), (un / kPBufs) & 1))) break;
                     tc_fence_after();
+#pragma unroll 1
                     for (int t = 0; t < 4; ++t, ++it) {
                         const uint32_t sl = it % kSlabs, d = tmem + L::O_COL + t * N;
-                        if (!(ok = wait_bar(bar(sh.slab_full[sl]), (it / kSlabs) & 1, p.err, abort_flag))) break;
+                        if (!(ok = wait_bar(bar(sh.slab_full[sl]), (it / kSlabs) & 1))) break;
                         const uint64_t a = desc_add(c0, sl * kSlab), b = desc_add(p0, pb * L::kPBuf);
 #pragma unroll
                         for (int kk = 0; kk < 4; ++kk) {
@@ -556,7 +573,7 @@ __global__ void __launch_bounds__(Fp4Layout<HP>::kThreads, 1)
                     if (ok) umma_commit(bar(sh.p_free[pb]));
                 }
             }
-            if (!ok) *abort_flag = 1;
+            if (!ok) record_error(p.err, kDevErrTimeout);
             }
         }
     } else if (warp < 4 + kSoftWarps) {
@@ -603,7 +620,7 @@ __global__ void __launch_bounds__(Fp4Layout<HP>::kThreads, 1)
                 const uint32_t sb = un % kSBufs, pb = un % kPBufs;
                 float x[HW], s[WC];
                 // one warp asks: tries cost the others their shared-memory accesses
-                if (quad == 0) ok &= wait_bar(bar(sh.s_full[sb]), (un / kSBufs) & 1, p.err, abort_flag);
+                if (quad == 0) ok = ok && wait_bar(bar(sh.s_full[sb]), (un / kSBufs) & 1);
                 named_bar_sync(id, 128);
                 tc_fence_after();
 #pragma unroll
@@ -720,7 +737,7 @@ __global__ void __launch_bounds__(Fp4Layout<HP>::kThreads, 1)
                         w[HW / 4 + h / 4] = byte_perm(y, z, 0x7632);
                     }
                 }
-                if (un >= kPBufs) ok &= wait_bar(bar(sh.p_free[pb]), (un / kPBufs - 1) & 1, p.err, abort_flag);
+                if (un >= kPBufs) ok = ok && wait_bar(bar(sh.p_free[pb]), (un / kPBufs - 1) & 1);
                 const uint32_t prow = base + L::P + pb * L::kPBuf;
                 if constexpr (kJoin) {
 #pragma unroll
@@ -736,7 +753,7 @@ __global__ void __launch_bounds__(Fp4Layout<HP>::kThreads, 1)
                     }
                 }
                 if (moved) {   // once the products of the unit before are complete
-                    ok &= wait_bar(bar(sh.p_free[(un - 1) % kPBufs]), ((un - 1) / kPBufs) & 1, p.err, abort_flag);
+                    ok = ok && wait_bar(bar(sh.p_free[(un - 1) % kPBufs]), ((un - 1) / kPBufs) & 1);
                     __syncwarp();
                     tc_fence_after();
                     for (; moved; moved &= moved - 1) {
@@ -770,10 +787,11 @@ __global__ void __launch_bounds__(Fp4Layout<HP>::kThreads, 1)
                 if (lane == h) part[h] = v;
             }
             const uint32_t last = un - 1;
-            ok &= wait_bar(bar(sh.p_free[last % kPBufs]), (last / kPBufs) & 1, p.err, abort_flag);
+            ok = ok && wait_bar(bar(sh.p_free[last % kPBufs]), (last / kPBufs) & 1);
             named_bar_sync(id, 128);
             tc_fence_after();
             const size_t slot = static_cast<size_t>(seg.slot) * p.H + wg * HW;
+            const uint64_t keep = l2_policy_evict_last();   // the merge reads it soon
             if (t < mine) {   // (mine <= 24: the warpgroup's first warp)
                 p.ws_m[slot + t] = -bias[t];
                 p.ws_l[slot + t] = (all[0][t] + all[1][t]) + (all[2][t] + all[3][t]);
@@ -790,18 +808,20 @@ __global__ void __launch_bounds__(Fp4Layout<HP>::kThreads, 1)
 #pragma unroll
                 for (int k = 0; k < 8; ++k) {
                     const int at = kJoin ? 2 * (k & ~1) + (k & 1) : k;
-                    if (g + k < mine) dst[static_cast<size_t>(k) * kR] = kJoin ? fmaf(o[(at + 2) % 16], kLoPart, o[at]) : o[at];
+                    if (g + k < mine)
+                        st_keep(dst + static_cast<size_t>(k) * kR, kJoin ? fmaf(o[(at + 2) % 16], kLoPart, o[at]) : o[at], keep);
                 }
             }
             tc_fence_before();
             named_bar_sync(id, 128);   // part and mul are read before the next segment sets them
             more = walk.next(seg);
         }
-        if (!ok) *abort_flag = 1;
+        if (!ok) record_error(p.err, kDevErrTimeout);
     } else {
         regs_release<L::kRegsExp>();
         // ---- expansion: a warpgroup takes every other slab, a warp 32 of its rows, a lane the groups (32 codes) `g` of rows
         // r + 8 i
+        constexpr int kBatch = kJoin ? 4 : 2;   // by the registers there are
         const int first = (warp - 4 - kSoftWarps) >> 2, g = lane & 3, r = (warp & 3) * 32 + (lane >> 2);
         const int x = ((2 * g) ^ (lane >> 2)) * 16;   // row & 7 = lane >> 2: the swizzle of the group's first 16 bytes
         const uint32_t slab_at = L::C + sw128_offset(r, 0) - (lane >> 2) * 16, pick_at = L::PICK + r * 16 + g,
@@ -811,31 +831,31 @@ __global__ void __launch_bounds__(Fp4Layout<HP>::kThreads, 1)
         while (walk.next(seg)) {
             for (int u = 0; u < seg.units; ++u, ++un) {
                 const uint32_t pb = un % kPickBufs;
-                ok &= wait_bar(bar(sh.pick_full[pb]), (un / kPickBufs) & 1, p.err, abort_flag);
+                ok = ok && wait_bar(bar(sh.pick_full[pb]), (un / kPickBufs) & 1);
 #pragma unroll 1
                 for (int k = first; k < 4; k += L::kExpGroups) {
                     const uint32_t it = 4 * un + k, sl = it % kSlabs, st = it % kStages;
-                    ok &= wait_bar(bar(sh.stage_full[st]), (it / kStages) & 1, p.err, abort_flag);
-                    if (it >= kSlabs) ok &= wait_bar(bar(sh.slab_free[sl]), (it / kSlabs - 1) & 1, p.err, abort_flag);
+                    ok = ok && wait_bar(bar(sh.stage_full[st]), (it / kStages) & 1);
+                    if (it >= kSlabs) ok = ok && wait_bar(bar(sh.slab_free[sl]), (it / kSlabs - 1) & 1);
                     uint8_t *const slab = smem + slab_at + sl * kSlab;
 #pragma unroll
-                    for (int h = 0; h < 2; ++h) {
-                        uint4 c[2];
-                        uint2 tb[2];   // read before the stores
+                    for (int h = 0; h < 4; h += kBatch) {
+                        uint4 c[kBatch];
+                        uint2 tb[kBatch];   // read before the stores
 #pragma unroll
-                        for (int i = 0; i < 2; ++i) {
-                            c[i] = *reinterpret_cast<const uint4 *>(smem + stage_at + st * kStage + (2 * h + i) * 512);
-                            tb[i] = sh.table[smem[pick_at + pb * kPicks + (2 * h + i) * 128 + k * 4]];
+                        for (int i = 0; i < kBatch; ++i) {
+                            c[i] = *reinterpret_cast<const uint4 *>(smem + stage_at + st * kStage + (h + i) * 512);
+                            tb[i] = sh.table[smem[pick_at + pb * kPicks + (h + i) * 128 + k * 4]];
                         }
 #pragma unroll
-                        for (int i = 0; i < 2; ++i) {
+                        for (int i = 0; i < kBatch; ++i) {
                             uint32_t o[8];
                             expand8(c[i].x, tb[i], o[0], o[1]);
                             expand8(c[i].y, tb[i], o[2], o[3]);
                             expand8(c[i].z, tb[i], o[4], o[5]);
                             expand8(c[i].w, tb[i], o[6], o[7]);
-                            *reinterpret_cast<uint4 *>(slab + (2 * h + i) * 1024 + x) = make_uint4(o[0], o[1], o[2], o[3]);
-                            *reinterpret_cast<uint4 *>(slab + (2 * h + i) * 1024 + (x ^ 16)) = make_uint4(o[4], o[5], o[6], o[7]);
+                            *reinterpret_cast<uint4 *>(slab + (h + i) * 1024 + x) = make_uint4(o[0], o[1], o[2], o[3]);
+                            *reinterpret_cast<uint4 *>(slab + (h + i) * 1024 + (x ^ 16)) = make_uint4(o[4], o[5], o[6], o[7]);
                         }
                     }
                     fence_proxy_async_smem();
@@ -848,7 +868,7 @@ __global__ void __launch_bounds__(Fp4Layout<HP>::kThreads, 1)
                 }
             }
         }
-        if (!ok) *abort_flag = 1;
+        if (!ok) record_error(p.err, kDevErrTimeout);
     }
 
     __syncwarp();
@@ -866,7 +886,7 @@ struct MergeParams {
     const __nv_bfloat16 *w_uv, *gate;
     __nv_bfloat16 *out;
     int *err;
-    int B, H, max_len, G;
+    int B, H, max_len, G, over;
 };
 
 constexpr int kMaxShares = 512;   // share boundaries that the merge keeps in shared memory
@@ -884,7 +904,7 @@ __device__ __forceinline__ void join_segments(const MergeParams &p, const int *s
     int c_first = 0;
     for (int j = 0; j < chunks; ++j) {
         const int rows = min(kChunkRows, len - j * kChunkRows);
-        const int r0 = at.x + j * kChunkSpan + kOverUnits, r1 = r0 + (rows + kRows - 1) / kRows;
+        const int r0 = at.x + j * (p.over + kChunkUnits) + p.over, r1 = r0 + (rows + kRows - 1) / kRows;
         if (j == 0)   // the share that holds r0: from an estimate on, as shares are equal but for a unit
             c_first = min(p.G - 1, static_cast<int>(static_cast<float>(r0) * p.G / shares[p.G]));
         while (c_first > 0 && shares[c_first] > r0) --c_first;
@@ -940,23 +960,30 @@ __device__ __forceinline__ float gated(const __nv_bfloat16 *gate, size_t at, flo
     return gate ? y * __fdividef(1.f, 1.f + fast_exp2(-__bfloat162float(gate[at]) * kLog2e)) : y;
 }
 
-// Few (head, sequence) pairs: a CTA per head and kSeqs sequences, fp32 products.  W_UV[h] is in registers before the
-// attention is done (a warp takes eight of its rows, a lane 16 columns of each); 16 / kSeqs warps join a sequence's
-// segments and one of them their parts.
+// Few (head, sequence) pairs: a CTA per head and kSeqs sequences, fp32 products.  W_UV[h] (128 KB, contiguous) is asked
+// into shared memory before the attention is done; 16 / kSeqs warps join a sequence's segments, then a warp takes eight
+// rows of W_UV, a lane 16 columns of each.
 constexpr int kDotThreads = 512;
+constexpr uint32_t kDotW = kDV * kR * 2, kDotPart = 16 * kR * 4;
+template <int kSeqs>
+constexpr uint32_t kDotSmem = kDotW + kDotPart + kSeqs * kR * 4;
 template <int kSeqs>
 __global__ void __launch_bounds__(kDotThreads, 1) fp4_merge_dot_kernel(const MergeParams p) {
     constexpr int kPer = 16 / kSeqs;
-    __shared__ __align__(16) float s_part[16][kR];
-    __shared__ __align__(16) float s_lat[kSeqs][kR];
+    extern __shared__ __align__(128) uint8_t dot_smem[];
+    float(*const s_part)[kR] = reinterpret_cast<float(*)[kR]>(dot_smem + kDotW);
+    float(*const s_lat)[kR] = reinterpret_cast<float(*)[kR]>(dot_smem + kDotW + kDotPart);
     __shared__ float s_m[16], s_l[16];
     __shared__ int s_shares[kMaxShares + 1];
+    __shared__ uint64_t w_full;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int h = blockIdx.x, b0 = static_cast<int>(blockIdx.y) * kSeqs, nb = min(kSeqs, p.B - b0);
-    uint4 w[8][2];
-    const uint4 *src = reinterpret_cast<const uint4 *>(p.w_uv + (static_cast<size_t>(h) * kDV + warp * 8) * kR) + lane * 2;
-#pragma unroll
-    for (int i = 0; i < 8; ++i) w[i][0] = __ldg(src + i * (kR / 8)), w[i][1] = __ldg(src + i * (kR / 8) + 1);
+    if (threadIdx.x == 0) {
+        mbar_init(smem_u32(&w_full), 1);
+        fence_mbar_init();
+        mbar_arrive_expect_tx(smem_u32(&w_full), kDotW);
+        bulk_load(smem_u32(dot_smem), p.w_uv + static_cast<size_t>(h) * kDV * kR, kDotW, smem_u32(&w_full));
+    }
     const int i = warp / kPer, b = b0 + min(i, nb - 1), len = i < nb ? read_len(p.lens, b, p.max_len, nullptr) : 0;
     grid_dependency_wait();   // the segments are complete and visible after this
     for (int c = threadIdx.x; c <= p.G; c += kDotThreads) s_shares[c] = p.ws_share[c];
@@ -964,59 +991,73 @@ __global__ void __launch_bounds__(kDotThreads, 1) fp4_merge_dot_kernel(const Mer
     __syncthreads();
     {
         float o[16], M, L;
-        join_segments<2>(p, s_shares, at, h, len, warp % kPer, kPer, lane, o, M, L);
+        join_segments<4>(p, s_shares, at, h, len, warp % kPer, kPer, lane, o, M, L);
         float4 *mine = reinterpret_cast<float4 *>(s_part[warp]) + lane;
 #pragma unroll
         for (int q = 0; q < 4; ++q) mine[32 * q] = make_float4(o[4 * q], o[4 * q + 1], o[4 * q + 2], o[4 * q + 3]);
         if (lane == 0) s_m[warp] = M, s_l[warp] = L;
     }
     __syncthreads();
-    for (int k = threadIdx.x; k < nb * kR; k += kDotThreads) {
-        const int s = k / kR, col = k % kR;
+#pragma unroll
+    for (int s = 0; s < kSeqs; ++s) {
         float M = -INFINITY, L = 0.f, x = 0.f;
 #pragma unroll
         for (int q = 0; q < kPer; ++q) M = fmaxf(M, s_m[s * kPer + q]);
+#pragma unroll
         for (int q = 0; q < kPer; ++q) {
-            const float m = s_m[s * kPer + q];
-            if (m == -INFINITY) continue;   // a warp without a segment
-            const float f = fast_exp2(m - M);
+            const float m = s_m[s * kPer + q], f = m == -INFINITY ? 0.f : fast_exp2(m - M);
             L = fmaf(f, s_l[s * kPer + q], L);
-            x = fmaf(f, s_part[s * kPer + q][col], x);
+            x = fmaf(f, s_part[s * kPer + q][threadIdx.x], x);   // (a warp without a segment holds zeros)
         }
-        s_lat[s][col] = M == -INFINITY ? 0.f : x / L;   // (an empty sequence has no segments)
+        s_lat[s][threadIdx.x] = M == -INFINITY ? 0.f : x / L;    // (an empty sequence has none)
     }
+    bool ok = mbar_wait(smem_u32(&w_full), 0, p.err);
     __syncthreads();
-    for (int s = 0; s < nb; ++s) {
-        const float4 *lat = reinterpret_cast<const float4 *>(s_lat[s]) + lane * 4;
-        const float4 a[4] = {lat[0], lat[1], lat[2], lat[3]};
-        float y[8];
+    float y[kSeqs][8];
+    {
+        float2 lat[kSeqs][8];
+#pragma unroll
+        for (int s = 0; s < kSeqs; ++s)
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {   // lane: columns 8 lane .. and 256 + 8 lane ..
+                const float4 v = *reinterpret_cast<const float4 *>(&s_lat[s][(k >> 1) * 256 + lane * 8 + (k & 1) * 4]);
+                lat[s][2 * k] = make_float2(v.x, v.y), lat[s][2 * k + 1] = make_float2(v.z, v.w);
+            }
 #pragma unroll
         for (int v = 0; v < 8; ++v) {
-            const uint32_t x[8] = {w[v][0].x, w[v][0].y, w[v][0].z, w[v][0].w, w[v][1].x, w[v][1].y, w[v][1].z, w[v][1].w};
-            const float c[16] = {a[0].x, a[0].y, a[0].z, a[0].w, a[1].x, a[1].y, a[1].z, a[1].w,
-                                 a[2].x, a[2].y, a[2].z, a[2].w, a[3].x, a[3].y, a[3].z, a[3].w};
-            y[v] = 0.f;
+            const uint4 *row = reinterpret_cast<const uint4 *>(dot_smem) + (warp * 8 + v) * (kR / 8) + lane;
+            const uint4 w0 = row[0], w1 = row[32];
+            const uint32_t w[8] = {w0.x, w0.y, w0.z, w0.w, w1.x, w1.y, w1.z, w1.w};
+            float2 acc[kSeqs];
+#pragma unroll
+            for (int s = 0; s < kSeqs; ++s) acc[s] = make_float2(0.f, 0.f);
 #pragma unroll
             for (int k = 0; k < 8; ++k) {
-                y[v] = fmaf(__uint_as_float(x[k] << 16), c[2 * k], y[v]);
-                y[v] = fmaf(__uint_as_float(x[k] & 0xFFFF0000u), c[2 * k + 1], y[v]);
+                const float2 wk = make_float2(__uint_as_float(w[k] << 16), __uint_as_float(w[k] & 0xFFFF0000u));
+#pragma unroll
+                for (int s = 0; s < kSeqs; ++s) acc[s] = fma2(wk, lat[s][k], acc[s]);
             }
+#pragma unroll
+            for (int s = 0; s < kSeqs; ++s) y[s][v] = acc[s].x + acc[s].y;
         }
+    }
+#pragma unroll
+    for (int s = 0; s < kSeqs; ++s) {
         // eight sums over the warp: halve the number of values held with each of the first three exchanges
 #pragma unroll
         for (int k = 4; k >= 1; k >>= 1) {
             const bool up = lane & k;
 #pragma unroll
             for (int v = 0; v < k; ++v) {
-                const float keep = up ? y[v + k] : y[v], give = up ? y[v] : y[v + k];
-                y[v] = keep + __shfl_xor_sync(0xffffffffu, give, k);
+                const float keep = up ? y[s][v + k] : y[s][v], give = up ? y[s][v] : y[s][v + k];
+                y[s][v] = keep + __shfl_xor_sync(0xffffffffu, give, k);
             }
         }
-        y[0] += __shfl_xor_sync(0xffffffffu, y[0], 8);
-        y[0] += __shfl_xor_sync(0xffffffffu, y[0], 16);
-        if (lane < 8) {   // lane v: output column 8 warp + v
-            const size_t at = (static_cast<size_t>(b0 + s) * p.H + h) * kDV + warp * 8 + lane;
-            p.out[at] = __float2bfloat16(gated(p.gate, at, y[0]));
+        y[s][0] += __shfl_xor_sync(0xffffffffu, y[s][0], 8);
+        y[s][0] += __shfl_xor_sync(0xffffffffu, y[s][0], 16);
+        if (lane < 8 && s < nb && ok) {   // lane v: output column 8 warp + v
+            const size_t to = (static_cast<size_t>(b0 + s) * p.H + h) * kDV + warp * 8 + lane;
+            p.out[to] = __float2bfloat16(gated(p.gate, to, y[s][0]));
         }
     }
 }
@@ -1151,7 +1192,7 @@ size_t slot_count(int B, int max_len, int G) {
 }
 
 template <int HP>
-cudaError_t launch_attention(const CUtensorMap &codes, const Fp4Params &p, cudaStream_t s) {
+cudaError_t launch_attention(const CUtensorMap &codes, const CUtensorMap &scales, const Fp4Params &p, cudaStream_t s) {
     using L = Fp4Layout<HP>;
     cudaError_t e = cudaFuncSetAttribute(fp4_attention_kernel<HP>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                          static_cast<int>(L::kSmem));
@@ -1160,8 +1201,19 @@ cudaError_t launch_attention(const CUtensorMap &codes, const Fp4Params &p, cudaS
     if ((e = cudaFuncGetAttributes(&fa, fp4_attention_kernel<HP>)) != cudaSuccess) return e;
     if (fa.numRegs != static_cast<int>(L::kRegsLaunch)) return cudaErrorInvalidConfiguration;
     note_launch();
-    fp4_attention_kernel<HP><<<p.G, L::kThreads, L::kSmem, s>>>(codes, p);
+    fp4_attention_kernel<HP><<<p.G, L::kThreads, L::kSmem, s>>>(codes, scales, p);
     return cudaGetLastError();
+}
+
+template <int kSeqs>
+cudaError_t launch_dot(const MergeParams &mp, cudaLaunchConfig_t &cfg) {
+    const cudaError_t e = cudaFuncSetAttribute(fp4_merge_dot_kernel<kSeqs>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                               static_cast<int>(kDotSmem<kSeqs>));
+    if (e != cudaSuccess) return e;
+    cfg.gridDim = dim3(mp.H, (mp.B + kSeqs - 1) / kSeqs);
+    cfg.blockDim = dim3(kDotThreads);
+    cfg.dynamicSmemBytes = kDotSmem<kSeqs>;
+    return cudaLaunchKernelEx(&cfg, fp4_merge_dot_kernel<kSeqs>, mp);
 }
 
 }  // namespace
@@ -1182,6 +1234,7 @@ cudaError_t launch_decode_fp4(const DecodeArgs &a, cudaStream_t s) {
     p.H = a.H;
     p.max_len = a.max_len;
     p.G = a.num_sms;
+    p.over = a.H > 48 ? 1 : 3;
     const size_t slots = slot_count(a.B, a.max_len, p.G);
     if (decode_fp4_workspace_bytes(a.B, a.H, a.max_len, a.num_sms) > a.workspace_bytes) return cudaErrorInvalidValue;
     p.ws_o = static_cast<float *>(a.workspace);
@@ -1192,28 +1245,30 @@ cudaError_t launch_decode_fp4(const DecodeArgs &a, cudaStream_t s) {
     p.w_uv = static_cast<const __nv_bfloat16 *>(a.w_uv);
     p.err = a.dev_err;
     p.scale_log2 = a.scale * kLog2e;
-    CUtensorMap tm_codes, tm_wuv;
+    CUtensorMap tm_codes, tm_scales, tm_wuv;
     {
         const cuuint64_t rows = static_cast<cuuint64_t>(a.max_len > 0 ? a.max_len : 1);
-        const cuuint64_t dims[3] = {kR / 2, rows, static_cast<cuuint64_t>(a.B)};
+        const cuuint64_t dims[3] = {kR / 2 + kR / 32, rows, static_cast<cuuint64_t>(a.B)};
         const cuuint64_t strides[2] = {static_cast<cuuint64_t>(a.ld_cache), rows * static_cast<cuuint64_t>(a.ld_cache)};
-        const cuuint32_t box[3] = {64, kRows, 1};
+        const cuuint32_t box[3] = {64, kRows, 1}, sbox[3] = {16, kRows, 1};
         const cuuint64_t wd[2] = {kR, static_cast<cuuint64_t>(a.H) * kDV}, ws[1] = {kR * 2};
         const cuuint32_t wb[2] = {64, kDV};
         if (encode_map(&tm_codes, CU_TENSOR_MAP_DATA_TYPE_UINT8, CU_TENSOR_MAP_SWIZZLE_NONE, a.c_cache, 3, dims, strides,
                        box) != CUDA_SUCCESS ||
+            encode_map(&tm_scales, CU_TENSOR_MAP_DATA_TYPE_UINT8, CU_TENSOR_MAP_SWIZZLE_NONE, a.c_cache, 3, dims, strides,
+                       sbox) != CUDA_SUCCESS ||
             encode_map(&tm_wuv, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, CU_TENSOR_MAP_SWIZZLE_128B, a.w_uv, 2, wd, ws, wb) !=
                 CUDA_SUCCESS)
             return cudaErrorInvalidValue;
     }
-    cudaError_t e = a.H <= 16   ? launch_attention<16>(tm_codes, p, s)
-                    : a.H <= 32 ? launch_attention<32>(tm_codes, p, s)
-                    : a.H <= 48 ? launch_attention<48>(tm_codes, p, s)
-                    : a.H <= 64 ? launch_attention<64>(tm_codes, p, s)
-                                : launch_attention<96>(tm_codes, p, s);
+    cudaError_t e = a.H <= 16   ? launch_attention<16>(tm_codes, tm_scales, p, s)
+                    : a.H <= 32 ? launch_attention<32>(tm_codes, tm_scales, p, s)
+                    : a.H <= 48 ? launch_attention<48>(tm_codes, tm_scales, p, s)
+                    : a.H <= 64 ? launch_attention<64>(tm_codes, tm_scales, p, s)
+                                : launch_attention<96>(tm_codes, tm_scales, p, s);
     if (e != cudaSuccess) return e;
     const MergeParams mp{a.lens, p.ws_seq, p.ws_share, p.ws_o, p.ws_m, p.ws_l, p.w_uv, static_cast<const __nv_bfloat16 *>(a.gate),
-                         static_cast<__nv_bfloat16 *>(a.out), a.dev_err, a.B, a.H, a.max_len, p.G};
+                         static_cast<__nv_bfloat16 *>(a.out), a.dev_err, a.B, a.H, a.max_len, p.G, p.over};
     cudaLaunchConfig_t cfg = {};
     cfg.stream = s;
     cudaLaunchAttribute attr[1];
@@ -1222,16 +1277,11 @@ cudaError_t launch_decode_fp4(const DecodeArgs &a, cudaStream_t s) {
     cfg.attrs = attr;
     cfg.numAttrs = 1;
     note_launch();
-    // up to eight sequences per CTA as long as one wave of CTAs takes them all
-    for (int seqs = 1; seqs <= 8; seqs *= 2)
-        if (static_cast<long long>(a.H) * ((a.B + seqs - 1) / seqs) <= a.num_sms) {
-            cfg.gridDim = dim3(a.H, (a.B + seqs - 1) / seqs);
-            cfg.blockDim = dim3(kDotThreads);
-            return seqs == 1   ? cudaLaunchKernelEx(&cfg, fp4_merge_dot_kernel<1>, mp)
-                   : seqs == 2 ? cudaLaunchKernelEx(&cfg, fp4_merge_dot_kernel<2>, mp)
-                   : seqs == 4 ? cudaLaunchKernelEx(&cfg, fp4_merge_dot_kernel<4>, mp)
-                               : cudaLaunchKernelEx(&cfg, fp4_merge_dot_kernel<8>, mp);
-        }
+    // up to four sequences per CTA, as long as one wave of CTAs (two, of the largest) takes them all
+    const auto ctas = [&](int seqs) { return static_cast<long long>(a.H) * ((a.B + seqs - 1) / seqs); };
+    if (ctas(1) <= a.num_sms) return launch_dot<1>(mp, cfg);
+    if (ctas(2) <= a.num_sms) return launch_dot<2>(mp, cfg);
+    if (ctas(4) <= 2 * a.num_sms) return launch_dot<4>(mp, cfg);
     if ((e = cudaFuncSetAttribute(fp4_merge_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                   static_cast<int>(kSmemMerge))) != cudaSuccess)
         return e;
