@@ -48,7 +48,7 @@ constexpr int kChunkUnits = 256;           // units of a sequence that share one
 constexpr int kChunkRows = kChunkUnits * kRows;
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kBias = 8.f;               // P = 2^(a - M + kBias)
-constexpr float kHead = 1.f, kSlack = 0.75f;   // a new maximum is set kHead above the row that forced it
+constexpr float kSlack = 0.75f;   // a new maximum is set kHead above the row that forced it
 constexpr uint32_t kSlab = 16384;          // [128 rows x 128 latent] e4m3, 128-byte swizzle
 constexpr uint32_t kPicks = 2048;          // [128 rows x 16 groups] table numbers of a unit
 constexpr uint32_t kStage = 8192;          // codes of one slab: [128 rows x 64 bytes]
@@ -81,13 +81,15 @@ struct Fp4Layout {
     static constexpr int kThreads = 128 * kGroups, HW = HP / kSoftGroups, N = kJoin ? 2 * HP : HP;   // N: columns of an MMA
     static constexpr int WC = N / kSoftGroups;                          // columns of a warpgroup
     // expanded tiles in flight (four per unit), and what the rest of shared memory holds of codes
-    static constexpr int kSlabs = HP == 96 ? 4 : (HP == 64 ? 6 : (HP == 48 ? 7 : 8)), kStages = HP == 16 ? 4 : 2;
+    static constexpr int kSlabs = HP == 96 ? 4 : (HP == 64 ? 5 : (HP <= 16 ? 8 : 7)),
+                         kStages = HP >= 48 && HP != 64 ? 2 : 4;
     static constexpr int kPBufs = kJoin ? 2 : 1, kSBufs = 2 * N <= 128 ? 2 : 1;
     static constexpr uint32_t kQPart = HP * 128, kQSlab = 2 * kQPart;   // [hi | lo rows x 128 latent]; kJoin: interleaved
     static constexpr uint32_t kPPart = kRows * 128, kPBuf = kJoin ? kPPart : 2 * kPPart;
     static constexpr uint32_t Q = 0, C = Q + 4 * kQSlab, P = C + kSlabs * kSlab, STAGE = P + kPBufs * kPBuf,
                               PICK = STAGE + kStages * kStage, END = PICK + kPickBufs * kPicks;
     static constexpr uint32_t kSmem = END + sizeof(Fp4Shared) + 1024;   // + alignment slack
+    static constexpr float kHead = kJoin ? 1.f : 3.f;   // a new maximum is set this far above the row that forced it
     static constexpr uint32_t S_COL = 0, O_COL = 128;                   // TMEM columns
     // Register split of the warpgroups: control, softmax, expansion.
     static constexpr uint32_t kRegsLaunch = kJoin ? 96 : 72, kRegsCtl = kJoin ? 80 : 56, kRegsSoft = kJoin ? 104 : 88,
@@ -391,6 +393,13 @@ __device__ __forceinline__ bool wait_bar(uint32_t bar, uint32_t parity) {
     return true;
 }
 
+// True in one lane of a warp that is here together: the issuing warps stay converged around their waits and loops, as
+// code that the compiler knows to be one lane's takes more instructions (319 -> 305 us at 96 heads, 64 x 16384 rows).
+__device__ __forceinline__ bool elect_one() {
+    uint32_t r;
+    asm volatile("{ .reg .pred p; elect.sync _|p, 0xffffffff; selp.u32 %0, 1, 0, p; }" : "=r"(r));
+    return r != 0;
+}
 // ------------------------------------------------------------------ attention
 template <int HP>
 __global__ void __launch_bounds__(Fp4Layout<HP>::kThreads, 1) 
@@ -461,14 +470,16 @@ __global__ void __launch_bounds__(Fp4Layout<HP>::kThreads, 1)
                 ++asked;
                 next.next(far, far_seg);
             };
+#pragma unroll 1
             for (int i = 0; i < kPickBufs - 1 && next.rows > 0; ++i) ask();
+#pragma unroll 1
             for (uint32_t un = 0; unit.rows > 0; ++un) {
                 const uint32_t pb = un % kPickBufs;
                 ok = ok && wait_bar(bar(sh.scale_full[pb]), (un / kPickBufs) & 1);
                 // (the expansion is done with the unit four back and has begun with the slabs of none that the softmax is not
                 // done with six back: the ref slot, last used eight back, is free)
                 uint4 *const at = reinterpret_cast<uint4 *>(smem + L::PICK + pb * kPicks) + lane;
-#pragma unroll
+#pragma unroll 1
                 for (int i = 0; i < 4; ++i) {   // a lane takes rows lane + 32 i
                     const uint4 v = at[32 * i];
                     uint32_t w[4] = {v.x, v.y, v.z, v.w};
@@ -488,13 +499,16 @@ __global__ void __launch_bounds__(Fp4Layout<HP>::kThreads, 1)
                 for (uint32_t k = asked > kPickBufs ? asked - kPickBufs : 0; k < asked; ++k)
                     wait_bar(bar(sh.scale_full[k % kPickBufs]), (k / kPickBufs) & 1);
             }
-        } else if (warp == 3 && lane == 0) {
+        } else if (warp == 3) {
+            const bool lead = elect_one();
             // ---- TMA: a unit's codes, slab by slab
             tma_prefetch_desc(&tm_codes);
             const uint64_t once = l2_policy_evict_first();
             uint32_t it = 0;
             bool ok = true;
+#pragma unroll 1
             while (ok && walk.next(seg)) {
+#pragma unroll 1
                 for (int u = 0; ok && u < seg.units; ++u) {
 #pragma unroll 1
                     for (int k = 0; k < 4; ++k, ++it) {
@@ -502,29 +516,35 @@ __global__ void __launch_bounds__(Fp4Layout<HP>::kThreads, 1)
                         if (it >= kStages &&
                             !(ok = wait_bar(bar(sh.stage_empty[st]), (it / kStages - 1) & 1)))
                             break;
-                        mbar_arrive_expect_tx(bar(sh.stage_full[st]), kStage);
-                        tma_load_3d_hint(base + L::STAGE + st * kStage, &tm_codes, bar(sh.stage_full[st]), k * 64,
-                                         seg.row0 + u * kRows, seg.seq, once);
+                        if (lead) {
+                            mbar_arrive_expect_tx(bar(sh.stage_full[st]), kStage);
+                            tma_load_3d_hint(base + L::STAGE + st * kStage, &tm_codes, bar(sh.stage_full[st]), k * 64,
+                                             seg.row0 + u * kRows, seg.seq, once);
+                        }
                     }
                 }
             }
-            if (!ok) record_error(p.err, kDevErrTimeout);
+            if (!ok && lane == 0) record_error(p.err, kDevErrTimeout);
             {   // this CTA's part of W_UV into L2: the cache's rows have pushed it out
                 const long long bytes = static_cast<long long>(p.H) * kDV * kR * 2, from = bytes * blockIdx.x / gridDim.x & ~15ll,
                                 to = bytes * (blockIdx.x + 1) / gridDim.x & ~15ll;
-                if (to > from) bulk_prefetch_l2(reinterpret_cast<const uint8_t *>(p.w_uv) + from, static_cast<uint32_t>(to - from));
+                if (lead && to > from) bulk_prefetch_l2(reinterpret_cast<const uint8_t *>(p.w_uv) + from, static_cast<uint32_t>(to - from));
             }
             // no load may still be landing when the CTA exits
+#pragma unroll 1
             for (uint32_t k = it > kStages ? it - kStages : 0; k < it; ++k)
                 wait_bar(bar(sh.stage_full[k % kStages]), (k / kStages) & 1);
-        } else if (warp == 1 && lane == 0) {
+        } else if (warp == 1) {
+            const bool lead = elect_one();
             // ---- S^T = c . q^T: four slabs of K = 128
             constexpr uint32_t idesc = make_idesc_e4m3(128, N, 0, 0);
             const uint64_t q0 = make_smem_desc(base + L::Q, 16, 1024), c0 = make_smem_desc(base + L::C, 16, 1024);
             uint32_t it = 0, un = 0, ns = 0;
             bool ok = true;
+#pragma unroll 1
             while (ok && walk.next(seg)) {
                 if (!(ok = wait_bar(bar(sh.q_ready), ns++ & 1))) break;
+#pragma unroll 1
                 for (int u = 0; ok && u < seg.units; ++u, ++un) {
                     const uint32_t sb = un % kSBufs, d = tmem + L::S_COL + sb * N;
                     if (un >= kSBufs && !(ok = wait_bar(bar(sh.s_free[sb]), (un / kSBufs - 1) & 1)))
@@ -535,25 +555,29 @@ __global__ void __launch_bounds__(Fp4Layout<HP>::kThreads, 1)
                         if (!(ok = wait_bar(bar(sh.slab_full[sl]), (it / kSlabs) & 1))) break;
                         tc_fence_after();
                         const uint64_t a = desc_add(c0, sl * kSlab), b = desc_add(q0, k * L::kQSlab);
+                        if (lead)
 #pragma unroll
                         for (int kk = 0; kk < 4; ++kk) {
                             umma_f8(d, desc_add(a, kk * 32), desc_add(b, kk * 32), idesc, (k | kk) != 0);
                             if (!kJoin) umma_f8(d, desc_add(a, kk * 32), desc_add(b, L::kQPart + kk * 32), idesc, 1);
                         }
                     }
-                    if (ok) umma_commit(bar(sh.s_full[sb]));
+                    if (ok && lead) umma_commit(bar(sh.s_full[sb]));
                 }
             }
-            if (!ok) record_error(p.err, kDevErrTimeout);
+            if (!ok && lane == 0) record_error(p.err, kDevErrTimeout);
         } else if (warp == 2) {
             if (blockIdx.x == 0) write_seq(p, lane);   // its first product is far off
-            if (lane == 0) {
+            {
+            const bool lead = elect_one();
             // ---- O^T += c^T . P^T: slab t holds latent columns [128 t, 128 t + 128)
             constexpr uint32_t idesc = make_idesc_e4m3(128, N, 1, 1), idesc_lo = idesc | 1u << 10;   // B: e5m2
             const uint64_t p0 = make_smem_desc(base + L::P, kSlab, 1024), c0 = make_smem_desc(base + L::C, kSlab, 1024);
             uint32_t it = 0, un = 0;
             bool ok = true;
+#pragma unroll 1
             while (ok && walk.next(seg)) {
+#pragma unroll 1
                 for (int u = 0; ok && u < seg.units; ++u, ++un) {
                     const uint32_t pb = un % kPBufs;
                     if (!(ok = wait_bar(bar(sh.p_full[pb]), (un / kPBufs) & 1))) break;
@@ -563,17 +587,19 @@ __global__ void __launch_bounds__(Fp4Layout<HP>::kThreads, 1)
                         const uint32_t sl = it % kSlabs, d = tmem + L::O_COL + t * N;
                         if (!(ok = wait_bar(bar(sh.slab_full[sl]), (it / kSlabs) & 1))) break;
                         const uint64_t a = desc_add(c0, sl * kSlab), b = desc_add(p0, pb * L::kPBuf);
+                        if (lead) {
 #pragma unroll
                         for (int kk = 0; kk < 4; ++kk) {
                             umma_f8(d, desc_add(a, kk * 4096), desc_add(b, kk * 4096), idesc, (u | kk) != 0);
                             if (!kJoin) umma_f8(d, desc_add(a, kk * 4096), desc_add(b, L::kPPart + kk * 4096), idesc_lo, 1);
                         }
                         umma_commit(bar(sh.slab_free[sl]));
+                        }
                     }
-                    if (ok) umma_commit(bar(sh.p_free[pb]));
+                    if (ok && lead) umma_commit(bar(sh.p_free[pb]));
                 }
             }
-            if (!ok) record_error(p.err, kDevErrTimeout);
+            if (!ok && lane == 0) record_error(p.err, kDevErrTimeout);
             }
         }
     } else if (warp < 4 + kSoftWarps) {
@@ -589,8 +615,10 @@ __global__ void __launch_bounds__(Fp4Layout<HP>::kThreads, 1)
         uint32_t un = 0;
         bool ok = true, more = walk.next(seg);
         float l[HW];
+#pragma unroll 1
         while (more) {
             // the segment's queries (S of the last unit before this has been read, so the buffer is free)
+#pragma unroll 1
             for (int i0 = quad; i0 < HW; i0 += 8) {
                 uint4 v[2][2];
 #pragma unroll
@@ -616,6 +644,7 @@ __global__ void __launch_bounds__(Fp4Layout<HP>::kThreads, 1)
 #pragma unroll
             for (int h = 0; h < HW; ++h) l[h] = 0.f;
 
+#pragma unroll 1
             for (int u = 0; u < seg.units; ++u, ++un) {
                 const uint32_t sb = un % kSBufs, pb = un % kPBufs;
                 float x[HW], s[WC];
@@ -656,34 +685,30 @@ __global__ void __launch_bounds__(Fp4Layout<HP>::kThreads, 1)
                 if (u == 0 || named_bar_or(id, 128, top > kBias + kSlack)) {
                     // the maxima over the rows of the heads that a row of this warp pushes past (of all, the first time):
                     // lane h gets head h's, first of its warp, then of all four
+                    // (a short loop that reads S again: this code is seldom in the instruction cache)
                     float most = -INFINITY;
-                    if (u == 0) {
-#pragma unroll
-                        for (int h = 0; h < HW; ++h) {
-                            const float v = warp_max(x[h]);
-                            if (lane == h) most = v;
-                        }
-                    } else {   // a few: a short loop that reads S again, as this code is seldom in the instruction cache
-                        uint32_t past = 0;   // bit HW - 1 - h: head h (the sign of threshold - x)
+                    uint32_t past = u == 0 ? (1u << HW) - 1u : 0u;   // bit HW - 1 - h: head h (the sign of threshold - x)
+                    if (u > 0) {
 #pragma unroll
                         for (int h = 0; h < HW; ++h)
                             past = __funnelshift_l(__float_as_uint(kBias + kSlack - x[h]), past, 1);
-                        for (past = __reduce_or_sync(0xffffffffu, past); past; past &= past - 1) {
-                            const int h = HW - __ffs(past);
-                            float v;
-                            if constexpr (kJoin) {
-                                float lo;
-                                tmem_ld1(lanes + L::S_COL + sb * N + 2 * (h & ~1) + (h & 1), v);
-                                tmem_ld1(lanes + L::S_COL + sb * N + 2 * (h & ~1) + (h & 1) + 2, lo);
-                                tmem_wait_ld();
-                                v = fmaf(lo, kLoPart, v);
-                            } else {
-                                tmem_ld1(lanes + L::S_COL + sb * N + h, v);
-                                tmem_wait_ld();
-                            }
-                            v = warp_max(fmaf(v, mul[h] * row_scale, bias[h] + row_exp));
-                            if (lane == h) most = v;
+                    }
+#pragma unroll 1
+                    for (past = __reduce_or_sync(0xffffffffu, past); past; past &= past - 1) {
+                        const int h = HW - __ffs(past);
+                        float v;
+                        if constexpr (kJoin) {
+                            float lo;
+                            tmem_ld1(lanes + L::S_COL + sb * N + 2 * (h & ~1) + (h & 1), v);
+                            tmem_ld1(lanes + L::S_COL + sb * N + 2 * (h & ~1) + (h & 1) + 2, lo);
+                            tmem_wait_ld();
+                            v = fmaf(lo, kLoPart, v);
+                        } else {
+                            tmem_ld1(lanes + L::S_COL + sb * N + h, v);
+                            tmem_wait_ld();
                         }
+                        v = warp_max(fmaf(v, mul[h] * row_scale, bias[h] + row_exp));
+                        if (lane == h) most = v;
                     }
                     if (lane < HW) part[lane] = most;
                     named_bar_sync(id, 128);
@@ -691,7 +716,7 @@ __global__ void __launch_bounds__(Fp4Layout<HP>::kThreads, 1)
                     if (lane < HW) {
                         most = fmaxf(fmaxf(all[0][lane], all[1][lane]), fmaxf(all[2][lane], all[3][lane]));
                         moves = (most > kBias + kSlack || u == 0) && most > -INFINITY;
-                        const float by = moves ? kBias - kHead - most : 0.f;   // M_old - M_new
+                        const float by = moves ? kBias - L::kHead - most : 0.f;   // M_old - M_new
                         step[lane] = by;
                         fac[lane] = fast_exp2(by);
                         bias[lane] += by;
@@ -756,6 +781,7 @@ __global__ void __launch_bounds__(Fp4Layout<HP>::kThreads, 1)
                     ok = ok && wait_bar(bar(sh.p_free[(un - 1) % kPBufs]), ((un - 1) / kPBufs) & 1);
                     __syncwarp();
                     tc_fence_after();
+#pragma unroll 1
                     for (; moved; moved &= moved - 1) {
                         const int h = __ffs(moved) - 1, j = kJoin ? h & 1 : h & 3, col = kJoin ? 2 * (h & ~1) : h & ~3;
                         const float f = fac[h];
@@ -779,12 +805,24 @@ __global__ void __launch_bounds__(Fp4Layout<HP>::kThreads, 1)
                 if (lane == 0) mbar_arrive(bar(sh.p_full[pb]));
             }
             // ---- drain: l over the 128 rows, then O^T (lane = latent column of its tile)
+            // (every step halves the heads that a lane holds, so that lane h ends with head h's sum over the warp)
+            {
+                constexpr int P = HW <= 8 ? 8 : (HW <= 16 ? 16 : 32);
+                float v[P];
 #pragma unroll
-            for (int h = 0; h < HW; ++h) {
-                float v = l[h];
+                for (int h = 0; h < P; ++h) v[h] = h < HW ? l[h] : 0.f;
 #pragma unroll
-                for (int o = 16; o >= 1; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-                if (lane == h) part[h] = v;
+                for (int o = P / 2; o >= 1; o >>= 1) {
+                    const bool up = lane & o;
+#pragma unroll
+                    for (int i = 0; i < o; ++i) {
+                        const float send = up ? v[i] : v[i + o];
+                        v[i] = (up ? v[i + o] : v[i]) + __shfl_xor_sync(0xffffffffu, send, o);
+                    }
+                }
+#pragma unroll
+                for (int o = 16; o >= P; o >>= 1) v[0] += __shfl_xor_sync(0xffffffffu, v[0], o);
+                if (lane < HW) part[lane] = v[0];
             }
             const uint32_t last = un - 1;
             ok = ok && wait_bar(bar(sh.p_free[last % kPBufs]), (last / kPBufs) & 1);
@@ -816,7 +854,7 @@ __global__ void __launch_bounds__(Fp4Layout<HP>::kThreads, 1)
             named_bar_sync(id, 128);   // part and mul are read before the next segment sets them
             more = walk.next(seg);
         }
-        if (!ok) record_error(p.err, kDevErrTimeout);
+        if (!ok && lane == 0) record_error(p.err, kDevErrTimeout);
     } else {
         regs_release<L::kRegsExp>();
         // ---- expansion: a warpgroup takes every other slab, a warp 32 of its rows, a lane the groups (32 codes) `g` of rows
@@ -828,7 +866,9 @@ __global__ void __launch_bounds__(Fp4Layout<HP>::kThreads, 1)
                        stage_at = L::STAGE + r * 64 + g * 16;
         bool ok = true;
         uint32_t un = 0;
+#pragma unroll 1
         while (walk.next(seg)) {
+#pragma unroll 1
             for (int u = 0; u < seg.units; ++u, ++un) {
                 const uint32_t pb = un % kPickBufs;
                 ok = ok && wait_bar(bar(sh.pick_full[pb]), (un / kPickBufs) & 1);
@@ -868,7 +908,7 @@ __global__ void __launch_bounds__(Fp4Layout<HP>::kThreads, 1)
                 }
             }
         }
-        if (!ok) record_error(p.err, kDevErrTimeout);
+        if (!ok && lane == 0) record_error(p.err, kDevErrTimeout);
     }
 
     __syncwarp();
