@@ -22,6 +22,7 @@ Entry points (same names as the C functions):
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 import threading
@@ -173,6 +174,11 @@ def _stream_ptr(stream, device):
     torch = _torch()
     s = torch.cuda.current_stream(device) if stream is None else stream
     return ctypes.c_void_p(s.cuda_stream)
+
+
+def _raw_stream(stream, device):
+    """_stream_ptr without the stream object, a sixth of a small call's host time."""
+    return _torch()._C._cuda_getCurrentRawStream(device.index) if stream is None else stream.cuda_stream
 
 
 def mla_absorbed_attn_fwd_workspace_size(B: int, T: int, H: int, d_q: int, d_v: int, r: int, dtype) -> int:
@@ -496,28 +502,35 @@ def mla_quantize_latent_fp8(c, cache_scale: float, out=None, stream=None):
 def _on(stream, device):
     """The device, and the stream where one is given, that a call's allocations and launches go to."""
     torch = _torch()
-    return torch.cuda.device(device) if stream is None else torch.cuda.stream(stream)
+    if stream is not None:
+        return torch.cuda.stream(stream)
+    return _HERE if torch.cuda.current_device() == device.index else torch.cuda.device(device)
+
+
+_HERE = contextlib.nullcontext()
 
 
 def mla_latent_fp4_row_bytes(r: int) -> int:
     """Bytes of one row of the fp4 latent cache: r / 2 code bytes and r / 32 scale bytes, rounded up to 16."""
-    n = int(library().mla_latent_fp4_row_bytes(int(r)))
-    if n == 0:
+    r = int(r)
+    if r <= 0 or r > 65536 or r % 32 != 0:
         raise ValueError(f"r = {r}: the fp4 latent cache holds rows of a positive multiple of 32 values, up to 65536")
-    return n
+    return (r // 2 + r // 32 + 15) // 16 * 16
 
 
 def _fp4_cache(c4, B, r):
     """Checks a [B, rows, row_bytes] uint8 cache (rows at one stride); returns (rows, row stride, batch stride)."""
-    torch = _torch()
-    if c4.dtype != torch.uint8 or not c4.is_cuda:
+    if c4.dtype != _torch().uint8 or not c4.is_cuda:
         raise TypeError("the fp4 cache must be a uint8 CUDA tensor")
-    if c4.dim() != 3 or (B is not None and c4.shape[0] != B) or c4.shape[2] != mla_latent_fp4_row_bytes(r) \
-            or c4.stride(2) != 1:
-        raise ValueError(f"the fp4 cache must be [B,max_len,{mla_latent_fp4_row_bytes(r)}] with unit inner stride")
+    n = mla_latent_fp4_row_bytes(r)
+    if c4.dim() != 3 or (B is not None and c4.shape[0] != B) or c4.shape[2] != n or c4.stride(2) != 1:
+        raise ValueError(f"the fp4 cache must be [B,max_len,{n}] with unit inner stride")
+    seqs, rows, _ = c4.shape
+    batch, ld, _ = c4.stride()
     # a dimension of one row or one sequence has no stride of its own to go by
-    ld = c4.stride(1) if c4.shape[1] > 1 else max(c4.stride(1), c4.shape[2])
-    return c4.shape[1], ld, c4.stride(0) if c4.shape[0] > 1 else c4.shape[1] * ld
+    if rows <= 1:
+        ld = max(ld, n)
+    return rows, ld, batch if seqs > 1 else rows * ld
 
 
 def mla_quantize_latent_fp4(c, out=None, stream=None):
@@ -532,7 +545,7 @@ def mla_quantize_latent_fp4(c, out=None, stream=None):
             out = torch.empty(shape, dtype=torch.uint8, device=c.device)
         _check(out, "out", torch.uint8, c.device, shape)
         rc = library().mla_quantize_latent_fp4(c.data_ptr(), r, out.data_ptr(), shape[-1], c.numel() // r, r, code,
-                                               _stream_ptr(stream, c.device))
+                                               _raw_stream(stream, c.device))
     if rc != 0:
         raise MLAError(rc, "mla_quantize_latent_fp4")
     return out
@@ -562,7 +575,7 @@ def mla_append_latent_fp4(c, c4_cache, lens, counts=None, stream=None):
     with _on(stream, dev):
         rc = library().mla_append_latent_fp4(c.data_ptr(), r, c4_cache.data_ptr(), ld, lens.data_ptr(),
                                              None if counts is None else counts.data_ptr(), max_len, B, T, r,
-                                             _dtype_code(c), _stream_ptr(stream, dev))
+                                             _dtype_code(c), _raw_stream(stream, dev))
     if rc != 0:
         raise MLAError(rc, "mla_append_latent_fp4")
     return c4_cache
@@ -592,7 +605,7 @@ def mla_dequantize_latent_fp4(c4, r: int, lens=None, dtype=None, out=None, strea
         _check(out, "out", dtype, dev, (B, rows, r))
         rc = library().mla_dequantize_latent_fp4(c4.data_ptr(), ld, batch, None if lens is None else lens.data_ptr(),
                                                  out.data_ptr(), r, B, rows, r, _dtype_code(out),
-                                                 _stream_ptr(stream, dev))
+                                                 _raw_stream(stream, dev))
     if rc != 0:
         raise MLAError(rc, "mla_dequantize_latent_fp4")
     return out
@@ -636,7 +649,7 @@ def mla_latent_decode_fp4(q_abs, c4_cache, lens, w_uv, gate=None, scale: float =
         ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
         rc = lib.mla_latent_decode_fp4(q_abs.data_ptr(), c4_cache.data_ptr(), ld, lens.data_ptr(), max_len,
                                        w_uv.data_ptr(), None if gate is None else gate.data_ptr(), float(scale),
-                                       out.data_ptr(), B, H, d_v, r, ws_ptr, ws_bytes, _stream_ptr(stream, dev))
+                                       out.data_ptr(), B, H, d_v, r, ws_ptr, ws_bytes, _raw_stream(stream, dev))
     if rc != 0:
         raise MLAError(rc, "mla_latent_decode_fp4")
     return out

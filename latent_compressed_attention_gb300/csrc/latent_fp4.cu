@@ -11,8 +11,11 @@
 //          conversion's rounding is the only one.
 //   read   value = e2m1 * 2^(scale - 127): at most two significant bits, exact in bf16 and fp32.
 //
-// Both directions are a stream bound by HBM: a thread takes 8 elements (16 bytes of bf16 or 32 of fp32 against 4 of
-// codes), four neighbouring lanes a group, so that every access of a warp is contiguous.
+// Both directions are a stream bound by HBM: a thread takes pieces of a few elements, neighbouring lanes a group, so that
+// every access of a warp is contiguous.  A single token's rows want
+// every piece on a thread of its own; a long run wants several pieces' loads in flight per thread (kMany).
+#include <algorithm>
+
 #include "common.cuh"
 #include "internal.h"
 
@@ -20,19 +23,31 @@ namespace mla {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kPiece = 8;      // elements a thread converts at a time
+constexpr int kPiece = 8;      // elements that a thread of the write converts at a time
+constexpr int kMany = 4;       // pieces per thread of a long run
+constexpr long long kLong = 152 * 8;   // blocks of kMany that make a run long: one wave of full SMs
 
-// Rows of one launch: `rows` of them in runs of `run` (a sequence's rows), each cut into r / 8 pieces.
+// The rows of a launch: runs (a sequence's rows) of `run`, each cut into blocks of rows and those into pieces.
 struct Pieces {
-    long long rows, run;
-    int per_row;          // r / 8
+    long long run;
+    int per_row;          // pieces of a row
     unsigned magic;       // ceil(2^32 / per_row): i / per_row = (i * magic) >> 32 for i * per_row < 2^32
     int rows_per_block;
+    unsigned blocks_per_run;
 };
+__device__ __forceinline__ unsigned piece_row(const Pieces &p, unsigned i) { return __umulhi(i, p.magic); }
 
-__device__ __forceinline__ unsigned piece_row(const Pieces &p, unsigned i) {
-    return __umulhi(i, p.magic);
-}
+struct Block {
+    long long seq, row0;   // its run, and its first row there
+    unsigned n;            // its pieces
+    __device__ explicit Block(const Pieces &p) {
+        const unsigned b = blockIdx.x / p.blocks_per_run;
+        seq = b;
+        row0 = static_cast<long long>(blockIdx.x - b * p.blocks_per_run) * p.rows_per_block;
+        n = static_cast<unsigned>(min(static_cast<long long>(p.rows_per_block), p.run - row0)) *
+            static_cast<unsigned>(p.per_row);
+    }
+};
 
 struct WriteParams {
     const void *c;
@@ -45,61 +60,81 @@ struct WriteParams {
     int r;
 };
 
-__device__ __forceinline__ void load_piece(const __nv_bfloat16 *src, float (&x)[8]) {
-    const uint4 v = __ldg(reinterpret_cast<const uint4 *>(src));
-    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+template <typename T>
+struct Raw;
+template <>
+struct Raw<__nv_bfloat16> {
+    uint4 v;
+    __device__ void load(const __nv_bfloat16 *src) { v = __ldcs(reinterpret_cast<const uint4 *>(src)); }
+    __device__ void get(float (&x)[8]) const {
+        const uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
-    for (int k = 0; k < 4; ++k) {
-        x[2 * k] = __uint_as_float(w[k] << 16);
-        x[2 * k + 1] = __uint_as_float(w[k] & 0xFFFF0000u);
-    }
-}
-__device__ __forceinline__ void load_piece(const float *src, float (&x)[8]) {
-    const float4 a = __ldg(reinterpret_cast<const float4 *>(src)), b = __ldg(reinterpret_cast<const float4 *>(src) + 1);
-    x[0] = a.x, x[1] = a.y, x[2] = a.z, x[3] = a.w, x[4] = b.x, x[5] = b.y, x[6] = b.z, x[7] = b.w;
-}
-
-template <typename T, bool kAppend>
-__global__ void __launch_bounds__(kThreads) write_latent_fp4_kernel(const WriteParams p) {
-    const long long row0 = static_cast<long long>(blockIdx.x) * p.pc.rows_per_block;
-    const unsigned n = static_cast<unsigned>(min(static_cast<long long>(p.pc.rows_per_block), p.pc.rows - row0)) *
-                       static_cast<unsigned>(p.pc.per_row);
-    for (unsigned i0 = threadIdx.x; i0 - threadIdx.x < n; i0 += kThreads) {   // whole warps: the shuffles below
-        const unsigned i = min(i0, n - 1);                                    // want every lane
-        const unsigned lr = piece_row(p.pc, i), piece = i - lr * static_cast<unsigned>(p.pc.per_row);
-        const long long row = row0 + lr;
-        float x[kPiece];
-        load_piece(static_cast<const T *>(p.c) + row * p.ld_c + piece * kPiece, x);
-        uint32_t top = 0;   // |x| orders like its bits; infinities and NaN lie above every finite value
-#pragma unroll
-        for (int k = 0; k < kPiece; ++k) top = max(top, __float_as_uint(x[k]) & 0x7FFFFFFFu);
-        top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
-        top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
-        const bool bad = top >= 0x7F800000u;
-        // max|x| = 1.f * 2^E <= 7 * 2^e: e = E - 2 up to 1.75 * 2^E, E - 1 beyond
-        const int e = min(40, max(-40, static_cast<int>(top >> 23) - 129 + ((top & 0x7FFFFFu) > 0x600000u ? 1 : 0)));
-        const float down = exp2_int(-e);
-        uint32_t codes = 0;
-        if (!bad) codes = pack_e2m1x8(x, down);
-        if (i0 >= n) continue;
-        long long to = row;
-        if constexpr (kAppend) {
-            const long long b = row / p.pc.run, t = row - b * p.pc.run;
-            if (p.counts) {
-                const int count = __ldg(p.counts + b);
-                if (count < 0 || count > p.pc.run) record_error(p.err, kDevErrBounds);
-                if (t >= count) continue;
-            }
-            const long long pos = __ldg(p.lens + b) + t;
-            if (pos < 0 || pos >= p.max_len) {
-                record_error(p.err, kDevErrBounds);
-                continue;
-            }
-            to = b * p.max_len + pos;
+        for (int k = 0; k < 4; ++k) {
+            x[2 * k] = __uint_as_float(w[k] << 16);
+            x[2 * k + 1] = __uint_as_float(w[k] & 0xFFFF0000u);
         }
-        uint8_t *dst = p.c4 + to * p.ld_c4;
-        reinterpret_cast<uint32_t *>(dst)[piece] = codes;
-        if ((piece & 3) == 0) dst[p.r / 2 + (piece >> 2)] = static_cast<uint8_t>(bad ? 255 : e + 127);
+    }
+};
+template <>
+struct Raw<float> {
+    float4 a, b;
+    __device__ void load(const float *src) {
+        a = __ldcs(reinterpret_cast<const float4 *>(src)), b = __ldcs(reinterpret_cast<const float4 *>(src) + 1);
+    }
+    __device__ void get(float (&x)[8]) const {
+        x[0] = a.x, x[1] = a.y, x[2] = a.z, x[3] = a.w, x[4] = b.x, x[5] = b.y, x[6] = b.z, x[7] = b.w;
+    }
+};
+
+template <typename T, bool kAppend, int N>
+__global__ void __launch_bounds__(kThreads) write_latent_fp4_kernel(const WriteParams p) {
+    const Block blk(p.pc);
+    const T *const src = static_cast<const T *>(p.c) + (blk.seq * p.pc.run + blk.row0) * p.ld_c;
+    long long row0 = blk.row0;       // of the block's first row, in its sequence's part of c4
+    unsigned first = 0, past = blk.n;   // the block's rows [first, past) are written (append)
+    if constexpr (kAppend) {
+        long long count = p.pc.run;
+        if (p.counts) {
+            count = __ldg(p.counts + blk.seq);
+            if (count < 0 || count > p.pc.run) record_error(p.err, kDevErrBounds);
+        }
+        row0 += __ldg(p.lens + blk.seq);
+        const long long rows = min(static_cast<long long>(p.pc.rows_per_block), min(count, p.pc.run) - blk.row0);
+        const long long lo = min(max(-row0, 0ll), max(rows, 0ll)), hi = max(lo, min(rows, p.max_len - row0));
+        if (rows > 0 && (lo > 0 || hi < rows)) record_error(p.err, kDevErrBounds);
+        first = static_cast<unsigned>(lo), past = static_cast<unsigned>(hi);
+    }
+    uint8_t *const dst = p.c4 + ((kAppend ? blk.seq * p.max_len : blk.seq * p.pc.run) + row0) * p.ld_c4;
+    for (unsigned i0 = 0; i0 < blk.n; i0 += N * blockDim.x) {
+        Raw<T> raw[N];
+        unsigned lr[N], piece[N];
+#pragma unroll
+        for (int j = 0; j < N; ++j) {
+            const unsigned i = min(i0 + j * blockDim.x + threadIdx.x, blk.n - 1);   // whole warps: the shuffles below
+            lr[j] = piece_row(p.pc, i);                                             // want every lane
+            piece[j] = i - lr[j] * static_cast<unsigned>(p.pc.per_row);
+            raw[j].load(src + lr[j] * p.ld_c + piece[j] * kPiece);
+        }
+#pragma unroll
+        for (int j = 0; j < N; ++j) {
+            float x[kPiece];
+            raw[j].get(x);
+            uint32_t top = 0;   // |x| orders like its bits; infinities and NaN lie above every finite value
+#pragma unroll
+            for (int k = 0; k < kPiece; ++k) top = max(top, __float_as_uint(x[k]) & 0x7FFFFFFFu);
+            top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
+            top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
+            const bool bad = top >= 0x7F800000u;
+            // max|x| = 1.f * 2^E <= 7 * 2^e: e = E - 2 up to 1.75 * 2^E, E - 1 beyond
+            const int e = min(40, max(-40, static_cast<int>(top >> 23) - 129 + ((top & 0x7FFFFFu) > 0x600000u ? 1 : 0)));
+            const float down = exp2_int(-e);
+            uint32_t codes = 0;
+            if (!bad) codes = pack_e2m1x8(x, down);
+            if (i0 + j * blockDim.x + threadIdx.x >= blk.n || (kAppend && (lr[j] < first || lr[j] >= past))) continue;
+            uint8_t *to = dst + lr[j] * p.ld_c4;
+            reinterpret_cast<uint32_t *>(to)[piece[j]] = codes;
+            if ((piece[j] & 3) == 0) to[p.r / 2 + (piece[j] >> 2)] = static_cast<uint8_t>(bad ? 255 : e + 127);
+        }
     }
 }
 
@@ -113,49 +148,92 @@ struct ReadParams {
     int r;
 };
 
-__device__ __forceinline__ void store_piece(__nv_bfloat16 *dst, const float (&x)[8]) {
-    *reinterpret_cast<uint4 *>(dst) = make_uint4(pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3]),
-                                                 pack_bf16x2(x[4], x[5]), pack_bf16x2(x[6], x[7]));
+// A piece of the read is 16 bytes of output, so that a warp's stores are contiguous: 8 codes of bf16, 4 of fp32.
+__device__ __forceinline__ uint32_t load_codes(const uint8_t *src, unsigned piece, const __nv_bfloat16 *) {
+    return __ldg(reinterpret_cast<const uint32_t *>(src) + piece);
 }
-__device__ __forceinline__ void store_piece(float *dst, const float (&x)[8]) {
-    reinterpret_cast<float4 *>(dst)[0] = make_float4(x[0], x[1], x[2], x[3]);
-    reinterpret_cast<float4 *>(dst)[1] = make_float4(x[4], x[5], x[6], x[7]);
+__device__ __forceinline__ uint32_t load_codes(const uint8_t *src, unsigned piece, const float *) {
+    return __ldg(reinterpret_cast<const uint16_t *>(src) + piece);
+}
+__device__ __forceinline__ void store_piece(__nv_bfloat16 *dst, uint32_t codes, float by) {
+    float x[8];
+    unpack_e2m1x8(codes, x);
+    *reinterpret_cast<uint4 *>(dst) = make_uint4(pack_bf16x2(x[0] * by, x[1] * by), pack_bf16x2(x[2] * by, x[3] * by),
+                                                 pack_bf16x2(x[4] * by, x[5] * by), pack_bf16x2(x[6] * by, x[7] * by));
+}
+__device__ __forceinline__ void store_piece(float *dst, uint32_t codes, float by) {
+    float x[8];
+    unpack_e2m1x8(codes, x);
+    *reinterpret_cast<float4 *>(dst) = make_float4(x[0] * by, x[1] * by, x[2] * by, x[3] * by);
 }
 
-template <typename T>
+template <typename T, int N>
 __global__ void __launch_bounds__(kThreads) read_latent_fp4_kernel(const ReadParams p) {
-    const long long row0 = static_cast<long long>(blockIdx.x) * p.pc.rows_per_block;
-    const unsigned n = static_cast<unsigned>(min(static_cast<long long>(p.pc.rows_per_block), p.pc.rows - row0)) *
-                       static_cast<unsigned>(p.pc.per_row);
-    for (unsigned i = threadIdx.x; i < n; i += kThreads) {
-        const unsigned lr = piece_row(p.pc, i), piece = i - lr * static_cast<unsigned>(p.pc.per_row);
-        const long long row = row0 + lr;
-        const long long b = p.pc.run == p.pc.rows ? 0 : row / p.pc.run, u = row - b * p.pc.run;
-        if (p.lens) {
-            const int len = __ldg(p.lens + b);
-            if (len < 0) record_error(p.err, kDevErrBounds);
-            if (u >= len) continue;
-        }
-        const uint8_t *src = p.c4 + b * p.batch_c4 + u * p.ld_c4;
-        const uint32_t codes = __ldg(reinterpret_cast<const uint32_t *>(src) + piece);
-        const float scale = fp4_scale(__ldg(src + p.r / 2 + (piece >> 2)));
-        float x[kPiece];
-        unpack_e2m1x8(codes, x);
+    constexpr int kOut = 16 / sizeof(T);
+    const Block blk(p.pc);
+    unsigned n = blk.n;
+    if (p.lens) {
+        const int len = __ldg(p.lens + blk.seq);
+        if (len < 0) record_error(p.err, kDevErrBounds);
+        const long long rows = min(static_cast<long long>(p.pc.rows_per_block), len - blk.row0);
+        n = rows <= 0 ? 0u : min(n, static_cast<unsigned>(rows) * static_cast<unsigned>(p.pc.per_row));
+    }
+    const uint8_t *const src = p.c4 + blk.seq * p.batch_c4 + blk.row0 * p.ld_c4;
+    T *const dst = static_cast<T *>(p.c) + (blk.seq * p.pc.run + blk.row0) * p.ld_c;
+    for (unsigned i0 = 0; i0 < n; i0 += N * blockDim.x) {
+        uint32_t codes[N];
+        uint8_t scale[N];
+        unsigned lr[N], piece[N];
 #pragma unroll
-        for (int k = 0; k < kPiece; ++k) x[k] *= scale;
-        store_piece(static_cast<T *>(p.c) + row * p.ld_c + piece * kPiece, x);
+        for (int j = 0; j < N; ++j) {
+            const unsigned i = min(i0 + j * blockDim.x + threadIdx.x, n - 1);
+            lr[j] = piece_row(p.pc, i);
+            piece[j] = i - lr[j] * static_cast<unsigned>(p.pc.per_row);
+            const uint8_t *row = src + lr[j] * p.ld_c4;
+            codes[j] = load_codes(row, piece[j], static_cast<const T *>(nullptr));
+            scale[j] = __ldg(row + p.r / 2 + piece[j] / (32 / kOut));
+        }
+#pragma unroll
+        for (int j = 0; j < N; ++j)
+            if (i0 + j * blockDim.x + threadIdx.x < n)
+                store_piece(dst + lr[j] * p.ld_c + piece[j] * kOut, codes[j], fp4_scale(scale[j]));
     }
 }
 
-Pieces pieces_of(long long rows, long long run, int r, long long *blocks) {
+// Runs f(pieces, blocks, threads, is_long).
+template <typename F>
+cudaError_t launch_pieces(long long runs, long long run, int per_row, F f) {
+    if (runs <= 0 || run <= 0) return cudaSuccess;
     Pieces pc;
-    pc.rows = rows;
     pc.run = run;
-    pc.per_row = r / kPiece;
-    pc.magic = static_cast<unsigned>((0x100000000ull + pc.per_row - 1) / pc.per_row);
-    pc.rows_per_block = pc.per_row >= kThreads ? 1 : kThreads / pc.per_row;
-    *blocks = (rows + pc.rows_per_block - 1) / pc.rows_per_block;
-    return pc;
+    pc.per_row = per_row;
+    pc.magic = static_cast<unsigned>((0x100000000ull + per_row - 1) / per_row);
+    const auto cut = [&](int pieces) {
+        pc.rows_per_block = std::max(1, pieces * kThreads / per_row);
+        const long long blocks = (run + pc.rows_per_block - 1) / pc.rows_per_block;
+        pc.blocks_per_run = static_cast<unsigned>(std::min(blocks, 0xFFFFFFFFll));
+        return blocks;
+    };
+    const bool is_long = cut(kMany) >= (kLong + runs - 1) / runs && run * per_row >= kMany * kThreads;
+    const long long blocks = is_long ? cut(kMany) : cut(1);
+    if (blocks > 0x7FFFFFFFLL / runs) return cudaErrorInvalidValue;
+    // a short run takes no more warps than it fills
+    const long long pieces = std::min<long long>(run, pc.rows_per_block) * per_row;
+    const unsigned threads = static_cast<unsigned>(std::min<long long>(kThreads, (pieces + 31) / 32 * 32));
+    note_launch();
+    f(pc, static_cast<unsigned>(blocks * runs), threads, is_long);
+    return cudaGetLastError();
+}
+
+template <typename T, bool kAppend>
+void launch_write(const WriteParams &p, unsigned grid, unsigned threads, bool is_long, cudaStream_t s) {
+    is_long ? write_latent_fp4_kernel<T, kAppend, kMany><<<grid, threads, 0, s>>>(p)
+            : write_latent_fp4_kernel<T, kAppend, 1><<<grid, threads, 0, s>>>(p);
+}
+template <typename T>
+void launch_read(const ReadParams &p, unsigned grid, unsigned threads, bool is_long, cudaStream_t s) {
+    is_long ? read_latent_fp4_kernel<T, kMany><<<grid, threads, 0, s>>>(p)
+            : read_latent_fp4_kernel<T, 1><<<grid, threads, 0, s>>>(p);
 }
 
 }  // namespace
@@ -163,33 +241,22 @@ Pieces pieces_of(long long rows, long long run, int r, long long *blocks) {
 cudaError_t launch_write_latent_fp4(const LatentFp4Args &a, cudaStream_t s) {
     WriteParams p{a.c,    static_cast<uint8_t *>(a.c4), a.ld_c, a.ld_c4, a.lens, a.counts, a.max_len,
                   a.dev_err, {},                        a.r};
-    long long blocks = 0;
-    p.pc = pieces_of(a.B * a.rows, a.rows, a.r, &blocks);
-    if (blocks <= 0) return cudaSuccess;
-    if (blocks > 0x7FFFFFFFLL) return cudaErrorInvalidValue;
-    const unsigned grid = static_cast<unsigned>(blocks);
-    note_launch();
-    if (a.lens)
-        a.f32 ? write_latent_fp4_kernel<float, true><<<grid, kThreads, 0, s>>>(p)
-              : write_latent_fp4_kernel<__nv_bfloat16, true><<<grid, kThreads, 0, s>>>(p);
-    else
-        a.f32 ? write_latent_fp4_kernel<float, false><<<grid, kThreads, 0, s>>>(p)
-              : write_latent_fp4_kernel<__nv_bfloat16, false><<<grid, kThreads, 0, s>>>(p);
-    return cudaGetLastError();
+    return launch_pieces(a.B, a.rows, a.r / kPiece, [&](const Pieces &pc, unsigned grid, unsigned threads, bool is_long) {
+        p.pc = pc;
+        if (a.lens)
+            a.f32 ? launch_write<float, true>(p, grid, threads, is_long, s) : launch_write<__nv_bfloat16, true>(p, grid, threads, is_long, s);
+        else
+            a.f32 ? launch_write<float, false>(p, grid, threads, is_long, s) : launch_write<__nv_bfloat16, false>(p, grid, threads, is_long, s);
+    });
 }
 
 cudaError_t launch_read_latent_fp4(const LatentFp4Args &a, cudaStream_t s) {
     ReadParams p{static_cast<const uint8_t *>(a.c4), const_cast<void *>(a.c), a.ld_c4, a.batch_c4, a.ld_c, a.lens,
                  a.dev_err, {}, a.r};
-    long long blocks = 0;
-    p.pc = pieces_of(a.B * a.rows, a.rows, a.r, &blocks);
-    if (blocks <= 0) return cudaSuccess;
-    if (blocks > 0x7FFFFFFFLL) return cudaErrorInvalidValue;
-    const unsigned grid = static_cast<unsigned>(blocks);
-    note_launch();
-    a.f32 ? read_latent_fp4_kernel<float><<<grid, kThreads, 0, s>>>(p)
-          : read_latent_fp4_kernel<__nv_bfloat16><<<grid, kThreads, 0, s>>>(p);
-    return cudaGetLastError();
+    return launch_pieces(a.B, a.rows, a.f32 ? a.r / 4 : a.r / 8, [&](const Pieces &pc, unsigned grid, unsigned threads, bool is_long) {
+        p.pc = pc;
+        a.f32 ? launch_read<float>(p, grid, threads, is_long, s) : launch_read<__nv_bfloat16>(p, grid, threads, is_long, s);
+    });
 }
 
 }  // namespace mla
