@@ -127,7 +127,11 @@ __device__ __forceinline__ long long units_of(int len, int over) {   // virtual 
     const int full = len / kChunkRows, rest = len - full * kChunkRows;
     return static_cast<long long>(full) * (over + kChunkUnits) + (rest > 0 ? over + (rest + kRows - 1) / kRows : 0);
 }
-__device__ __forceinline__ long long share_lo(long long total, int c, int G) { return total * c / G; }
+// floor(total * c / G) without a 64-bit division: total = G a + b, b c < 2^18.
+__device__ __forceinline__ int share_lo(int total, int c, int G) {
+    const int a = total / G, b = total - a * G;
+    return a * c + b * c / G;
+}
 __device__ __forceinline__ int read_len(const int *lens, int b, int max_len, int *err) {
     const int x = __ldg(lens + b);
     if (err && (x < 0 || x > max_len)) record_error(err, kDevErrBounds);
@@ -156,18 +160,19 @@ struct Walk {
     // Every lane of a warp calls this; all get the same walk.
     __device__ void start(const Fp4Params &p, int share, int lane, int *err) {
         lens = p.lens, B = p.B, max_len = p.max_len, over = p.over, c = share;
-        long long total = 0;
+        // (the first 32 sequences are often all there are: loaded once)
+        const int len0 = lane < B ? read_len(lens, lane, max_len, err) : 0;
+        int total = static_cast<int>(units_of(len0, over));
 #pragma unroll 1
-        for (int i = lane; i < B; i += 32) total += units_of(read_len(lens, i, max_len, err), p.over);
-#pragma unroll
-        for (int o = 16; o >= 1; o >>= 1) total += __shfl_xor_sync(0xffffffffu, total, o);
-        lo = static_cast<int>(share_lo(total, share, p.G)), hi = static_cast<int>(share_lo(total, share + 1, p.G));
+        for (int i = lane + 32; i < B; i += 32) total += static_cast<int>(units_of(read_len(lens, i, max_len, err), over));
+        total = __reduce_add_sync(0xffffffffu, total);
+        lo = share_lo(total, share, p.G), hi = share_lo(total, share + 1, p.G);
         b = B, j = 0, pre = hi, v = 0;
         int run = 0, chunks = 0;
 #pragma unroll 1
         for (int i0 = 0; i0 < B && lo < hi; i0 += 32) {
-            const int len = i0 + lane < B ? read_len(lens, i0 + lane, max_len, nullptr) : 0;
-            const int u = static_cast<int>(units_of(len, p.over)), incl = warp_scan(u, lane);
+            const int len = i0 == 0 ? len0 : (i0 + lane < B ? read_len(lens, i0 + lane, max_len, nullptr) : 0);
+            const int u = static_cast<int>(units_of(len, over)), incl = warp_scan(u, lane);
             const int n = len > 0 ? chunks_of(len) : 0, nincl = warp_scan(n, lane);
             const unsigned past = __ballot_sync(0xffffffffu, run + incl > lo);
             if (past) {
@@ -219,7 +224,7 @@ __device__ __forceinline__ void write_seq(const Fp4Params &p, int lane) {
         chunks += __shfl_sync(0xffffffffu, nincl, 31);
     }
 #pragma unroll 1
-    for (int c = lane; c <= p.G; c += 32) p.ws_share[c] = static_cast<int>(share_lo(run, c, p.G));
+    for (int c = lane; c <= p.G; c += 32) p.ws_share[c] = share_lo(run, c, p.G);
 }
 
 // The units of a walk, one after the other; rows = 0 at the end.
@@ -417,6 +422,8 @@ __global__ void __launch_bounds__(Fp4Layout<HP>::kThreads, 1)
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
     if (threadIdx.x == 0) {
+        tma_prefetch_desc(&tm_scales);
+        tma_prefetch_desc(&tm_codes);
         for (int i = 0; i < kStages; ++i) mbar_init(bar(sh.stage_full[i]), 1), mbar_init(bar(sh.stage_empty[i]), 4);
         for (int i = 0; i < kPickBufs; ++i) mbar_init(bar(sh.scale_full[i]), 1), mbar_init(bar(sh.pick_full[i]), 1), mbar_init(bar(sh.pick_empty[i]), kExpWarps);
         for (int i = 0; i < kSlabs; ++i) mbar_init(bar(sh.slab_full[i]), 4), mbar_init(bar(sh.slab_free[i]), 1);
@@ -502,7 +509,6 @@ __global__ void __launch_bounds__(Fp4Layout<HP>::kThreads, 1)
         } else if (warp == 3) {
             const bool lead = elect_one();
             // ---- TMA: a unit's codes, slab by slab
-            tma_prefetch_desc(&tm_codes);
             const uint64_t once = l2_policy_evict_first();
             uint32_t it = 0;
             bool ok = true;
@@ -687,28 +693,45 @@ __global__ void __launch_bounds__(Fp4Layout<HP>::kThreads, 1)
                     // lane h gets head h's, first of its warp, then of all four
                     // (a short loop that reads S again: this code is seldom in the instruction cache)
                     float most = -INFINITY;
-                    uint32_t past = u == 0 ? (1u << HW) - 1u : 0u;   // bit HW - 1 - h: head h (the sign of threshold - x)
-                    if (u > 0) {
+                    if (u == 0) {
+#pragma unroll 1
+                        for (int h0 = 0; h0 < HW; h0 += 8) {
+                            constexpr int W = kJoin ? 16 : 8;
+                            float y[W];
+#pragma unroll
+                            for (int i = 0; i < W; i += 8)
+                                tmem_ld8(lanes + L::S_COL + sb * N + h0 * (W / 8) + i, *reinterpret_cast<float (*)[8]>(y + i));
+                            tmem_wait_ld();
+#pragma unroll
+                            for (int k = 0; k < 8; ++k) {
+                                const int c = kJoin ? 2 * (k & ~1) + (k & 1) : k;
+                                const float sc = kJoin ? fmaf(y[(c + 2) % W], kLoPart, y[c]) : y[c];
+                                const float v = warp_max(fmaf(sc, mul[h0 + k] * row_scale, bias[h0 + k] + row_exp));
+                                if (lane == h0 + k) most = v;
+                            }
+                        }
+                    } else {
+                        uint32_t past = 0;   // bit HW - 1 - h: head h (the sign of threshold - x)
 #pragma unroll
                         for (int h = 0; h < HW; ++h)
                             past = __funnelshift_l(__float_as_uint(kBias + kSlack - x[h]), past, 1);
-                    }
 #pragma unroll 1
-                    for (past = __reduce_or_sync(0xffffffffu, past); past; past &= past - 1) {
-                        const int h = HW - __ffs(past);
-                        float v;
-                        if constexpr (kJoin) {
-                            float lo;
-                            tmem_ld1(lanes + L::S_COL + sb * N + 2 * (h & ~1) + (h & 1), v);
-                            tmem_ld1(lanes + L::S_COL + sb * N + 2 * (h & ~1) + (h & 1) + 2, lo);
-                            tmem_wait_ld();
-                            v = fmaf(lo, kLoPart, v);
-                        } else {
-                            tmem_ld1(lanes + L::S_COL + sb * N + h, v);
-                            tmem_wait_ld();
+                        for (past = __reduce_or_sync(0xffffffffu, past); past; past &= past - 1) {
+                            const int h = HW - __ffs(past);
+                            float v;
+                            if constexpr (kJoin) {
+                                float lo;
+                                tmem_ld1(lanes + L::S_COL + sb * N + 2 * (h & ~1) + (h & 1), v);
+                                tmem_ld1(lanes + L::S_COL + sb * N + 2 * (h & ~1) + (h & 1) + 2, lo);
+                                tmem_wait_ld();
+                                v = fmaf(lo, kLoPart, v);
+                            } else {
+                                tmem_ld1(lanes + L::S_COL + sb * N + h, v);
+                                tmem_wait_ld();
+                            }
+                            v = warp_max(fmaf(v, mul[h] * row_scale, bias[h] + row_exp));
+                            if (lane == h) most = v;
                         }
-                        v = warp_max(fmaf(v, mul[h] * row_scale, bias[h] + row_exp));
-                        if (lane == h) most = v;
                     }
                     if (lane < HW) part[lane] = most;
                     named_bar_sync(id, 128);
