@@ -899,24 +899,29 @@ __global__ void __launch_bounds__(Fp4Layout<HP>::kThreads, 1)
                 for (int k = first; k < 4; k += L::kExpGroups) {
                     const uint32_t it = 4 * un + k, sl = it % kSlabs, st = it % kStages;
                     ok = ok && wait_bar(bar(sh.stage_full[st]), (it / kStages) & 1);
+                    // the codes wait for their slab in registers: the stage can take the next ones meanwhile
+                    uint4 c[4];
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                        c[i] = *reinterpret_cast<const uint4 *>(smem + stage_at + st * kStage + i * 512);
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(bar(sh.stage_empty[st]));
                     if (it >= kSlabs) ok = ok && wait_bar(bar(sh.slab_free[sl]), (it / kSlabs - 1) & 1);
                     uint8_t *const slab = smem + slab_at + sl * kSlab;
 #pragma unroll
                     for (int h = 0; h < 4; h += kBatch) {
-                        uint4 c[kBatch];
                         uint2 tb[kBatch];   // read before the stores
 #pragma unroll
-                        for (int i = 0; i < kBatch; ++i) {
-                            c[i] = *reinterpret_cast<const uint4 *>(smem + stage_at + st * kStage + (h + i) * 512);
+                        for (int i = 0; i < kBatch; ++i)
                             tb[i] = sh.table[smem[pick_at + pb * kPicks + (h + i) * 128 + k * 4]];
-                        }
 #pragma unroll
                         for (int i = 0; i < kBatch; ++i) {
+                            const uint4 w = c[h + i];
                             uint32_t o[8];
-                            expand8(c[i].x, tb[i], o[0], o[1]);
-                            expand8(c[i].y, tb[i], o[2], o[3]);
-                            expand8(c[i].z, tb[i], o[4], o[5]);
-                            expand8(c[i].w, tb[i], o[6], o[7]);
+                            expand8(w.x, tb[i], o[0], o[1]);
+                            expand8(w.y, tb[i], o[2], o[3]);
+                            expand8(w.z, tb[i], o[4], o[5]);
+                            expand8(w.w, tb[i], o[6], o[7]);
                             *reinterpret_cast<uint4 *>(slab + (h + i) * 1024 + x) = make_uint4(o[0], o[1], o[2], o[3]);
                             *reinterpret_cast<uint4 *>(slab + (h + i) * 1024 + (x ^ 16)) = make_uint4(o[4], o[5], o[6], o[7]);
                         }
@@ -925,7 +930,6 @@ __global__ void __launch_bounds__(Fp4Layout<HP>::kThreads, 1)
                     __syncwarp();
                     if (lane == 0) {
                         mbar_arrive(bar(sh.slab_full[sl]));
-                        mbar_arrive(bar(sh.stage_empty[st]));
                         if (k >= 2) mbar_arrive(bar(sh.pick_empty[pb]));
                     }
                 }
@@ -1297,7 +1301,7 @@ cudaError_t launch_decode_fp4(const DecodeArgs &a, cudaStream_t s) {
     p.H = a.H;
     p.max_len = a.max_len;
     p.G = a.num_sms;
-    p.over = a.H > 48 ? 1 : 3;
+    p.over = a.H > 48 ? 2 : 3;
     const size_t slots = slot_count(a.B, a.max_len, p.G);
     if (decode_fp4_workspace_bytes(a.B, a.H, a.max_len, a.num_sms) > a.workspace_bytes) return cudaErrorInvalidValue;
     p.ws_o = static_cast<float *>(a.workspace);
