@@ -655,7 +655,10 @@ __global__ void __launch_bounds__(Fp4Layout<HP>::kThreads, 1)
                 const uint32_t sb = un % kSBufs, pb = un % kPBufs;
                 float x[HW], s[WC];
                 // one warp asks: tries cost the others their shared-memory accesses
-                if (quad == 0) ok = ok && wait_bar(bar(sh.s_full[sb]), (un / kSBufs) & 1);
+                if (quad == 0) {
+                    ok = ok && wait_bar(bar(sh.s_full[sb]), (un / kSBufs) & 1);
+                    if (un >= kPBufs) ok = ok && wait_bar(bar(sh.p_free[pb]), (un / kPBufs - 1) & 1);
+                }
                 named_bar_sync(id, 128);
                 tc_fence_after();
 #pragma unroll
@@ -785,7 +788,6 @@ __global__ void __launch_bounds__(Fp4Layout<HP>::kThreads, 1)
                         w[HW / 4 + h / 4] = byte_perm(y, z, 0x7632);
                     }
                 }
-                if (un >= kPBufs) ok = ok && wait_bar(bar(sh.p_free[pb]), (un / kPBufs - 1) & 1);
                 const uint32_t prow = base + L::P + pb * L::kPBuf;
                 if constexpr (kJoin) {
 #pragma unroll
@@ -1301,7 +1303,7 @@ cudaError_t launch_decode_fp4(const DecodeArgs &a, cudaStream_t s) {
     p.H = a.H;
     p.max_len = a.max_len;
     p.G = a.num_sms;
-    p.over = a.H > 48 ? 2 : 3;
+    p.over = a.H > 48 ? 4 : 3;
     const size_t slots = slot_count(a.B, a.max_len, p.G);
     if (decode_fp4_workspace_bytes(a.B, a.H, a.max_len, a.num_sms) > a.workspace_bytes) return cudaErrorInvalidValue;
     p.ws_o = static_cast<float *>(a.workspace);
