@@ -156,6 +156,9 @@ def _dtype_code(t) -> int:
 
 
 def _check(t, name, dtype, device, shape=None):
+    if t is not None and t.is_cuda and t.dtype == dtype and t.device == device and t.is_contiguous() \
+            and (shape is None or t.shape == shape):
+        return
     if t is None:
         raise ValueError(f"{name} is required")
     if not t.is_cuda:
@@ -539,13 +542,14 @@ def mla_quantize_latent_fp4(c, out=None, stream=None):
     if not c.is_cuda or not c.is_contiguous():
         raise ValueError("c must be a contiguous CUDA tensor")
     code, r = _dtype_code(c), c.shape[-1]
-    shape = (*c.shape[:-1], mla_latent_fp4_row_bytes(r))
-    with _on(stream, c.device):
+    shape, dev = (*c.shape[:-1], mla_latent_fp4_row_bytes(r)), c.device
+    with _on(stream, dev):
         if out is None:
-            out = torch.empty(shape, dtype=torch.uint8, device=c.device)
-        _check(out, "out", torch.uint8, c.device, shape)
+            out = torch.empty(shape, dtype=torch.uint8, device=dev)
+        else:
+            _check(out, "out", torch.uint8, dev, shape)
         rc = library().mla_quantize_latent_fp4(c.data_ptr(), r, out.data_ptr(), shape[-1], c.numel() // r, r, code,
-                                               _raw_stream(stream, c.device))
+                                               _raw_stream(stream, dev))
     if rc != 0:
         raise MLAError(rc, "mla_quantize_latent_fp4")
     return out
@@ -591,18 +595,18 @@ def mla_dequantize_latent_fp4(c4, r: int, lens=None, dtype=None, out=None, strea
     torch = _torch()
     if dtype is None:
         dtype = torch.bfloat16 if out is None else out.dtype
+    shape = (*c4.shape[:-1], r)
     if c4.dim() == 2 and lens is None:
-        got = mla_dequantize_latent_fp4(c4.unsqueeze(0), r, None, dtype, None if out is None else out.unsqueeze(0),
-                                        stream)
-        return got.squeeze(0)
+        c4 = c4.unsqueeze(0)
     rows, ld, batch = _fp4_cache(c4, None, r)
     B, dev = c4.shape[0], c4.device
     if lens is not None:
         _check(lens, "lens", torch.int32, dev, (B,))
     with _on(stream, dev):
         if out is None:
-            out = (torch.empty if lens is None else torch.zeros)((B, rows, r), dtype=dtype, device=dev)
-        _check(out, "out", dtype, dev, (B, rows, r))
+            out = (torch.empty if lens is None else torch.zeros)(shape, dtype=dtype, device=dev)
+        else:
+            _check(out, "out", dtype, dev, shape)
         rc = library().mla_dequantize_latent_fp4(c4.data_ptr(), ld, batch, None if lens is None else lens.data_ptr(),
                                                  out.data_ptr(), r, B, rows, r, _dtype_code(out),
                                                  _raw_stream(stream, dev))
@@ -641,10 +645,11 @@ def mla_latent_decode_fp4(q_abs, c4_cache, lens, w_uv, gate=None, scale: float =
     with _on(stream, dev):
         if out is None:
             out = torch.empty((B, H * d_v), dtype=torch.bfloat16, device=dev)
-        _check(out, "out", torch.bfloat16, dev, (B, H * d_v))
-        need = int(lib.mla_latent_decode_fp4_workspace_size(B, H, r, max_len))
-        if workspace is None and need > 0:
-            workspace = torch.empty(need, dtype=torch.uint8, device=dev)
+        else:
+            _check(out, "out", torch.bfloat16, dev, (B, H * d_v))
+        if workspace is None:
+            need = lib.mla_latent_decode_fp4_workspace_size(B, H, r, max_len)
+            workspace = torch.empty(need, dtype=torch.uint8, device=dev) if need > 0 else None
         ws_ptr = None if workspace is None else workspace.data_ptr()
         ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
         rc = lib.mla_latent_decode_fp4(q_abs.data_ptr(), c4_cache.data_ptr(), ld, lens.data_ptr(), max_len,

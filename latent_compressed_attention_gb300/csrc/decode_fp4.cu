@@ -20,18 +20,33 @@
 //
 // Softmax of one unit: thread = row, so every head's statistics lie across lanes.  With a = score * log2 e + ref,
 //   P = 2^(a - M + 8), l += P * 2^-ref,   M[head] >= running max of a - 0.75
-// M moves only when some row exceeds it by more than 0.75 (P <= 2^8.75 = 430, inside e4m3's 448), then to one above
+// M moves only when some row exceeds it by more than 0.75 (P <= 2^8.75 = 430, inside e4m3's 448), then to kHead above
 // that row: a barrier with an OR tells whether any does, and only then are the maxima taken across lanes and the moved
-// heads' columns of O^T rescaled.  A weight below 2^-22 of the largest is lost; sequences are cut into chunks of 32768
-// rows with maxima of their own, so less than 2^-7 of a chunk's weight can go that way.
+// heads' columns of O^T rescaled.  What two 8-bit parts cannot hold of P is half a step of lo: 2^-14 up to 48 heads
+// (kHead = 1: 2^-21 of the largest weight), 2^-17 above (kHead = 3: 2^-22; there every move stops four warpgroups, and
+// the higher start makes a third of them: 332 -> 321 us at 96 heads when it came).  Sequences are cut into chunks of
+// 32768 rows with maxima of their own, so less than 2^-6 of a chunk's weight can be lost to that, and that only when
+// nearly all of its rows lie 2^-21 below the largest.
 //
-// Warps: 0 turns scale bytes into table numbers, 1 issues S, 2 issues O, 3 loads codes (TMA); two (above 48 heads: four) softmax
-// warpgroups, each with its share of the heads, that never wait for one another (also q_abs, rescale and drain); two
-// (one) warpgroups expand.  The expansion is a byte permute per four codes: the group's exponent selects an 8-byte table
-// of e4m3 magnitudes, the codes' three magnitude bits are the selector.
+// Warps: 0 loads scale bytes (TMA) and turns them into table numbers, 1 issues S, 2 issues O, 3 loads codes (TMA); two
+// (above 48 heads: four) softmax warpgroups, each with its share of the heads, that never wait for one another (also
+// q_abs, rescale and drain); two warpgroups expand, every other slab of 128 latent columns each.  The expansion is a byte
+// permute per four codes: the group's exponent selects an 8-byte table of e4m3 magnitudes, the codes' three magnitude
+// bits are the selector.
 //
-// Merge kernel: a CTA per (head, 32 sequences) joins the segments of a sequence with the log-sum-exp rule, splits
-// o_lat into bf16 hi + lo and multiplies by W_UV^T on the tensor cores (W_UV as the M side), then the gate.
+// What bounds it (64 x 16384 rows, 1.93 GHz): at 96 heads 268 us, 9600 cycles a unit, of which the tensor pipe needs
+// 3600 (64 products of 56 cycles: shared memory feeds it 128 bytes a cycle).  The queries' 96 KB leave room for one unit
+// of expanded slabs, so a unit's expansion, S, softmax and O follow one another, each slab of the next unit expanded as
+// O leaves it.  At 48 heads 168 us (6000 cycles a unit), at 16 heads 107 us (3850; 1650 on the tensor pipe, the
+// expansion's byte permutes and logic about 2000 on the ALUs).  All roles' loops share an instruction cache that they
+// overflow easily: waits that carry their error path and issue loops unrolled fourfold cost 193 us instead of 127 at 16
+// heads, which is why loops here are kept rolled and cold code short.
+//
+// Merge kernels: the segments of a sequence are joined with the log-sum-exp rule and multiplied by W_UV^T, then the gate.
+// Few (head, sequence) pairs: a CTA per head and up to four sequences, the product in fp32 from W_UV[h] in shared memory.
+// Many: a CTA per head and 32 sequences, o_lat as bf16 hi + lo, on the tensor cores (W_UV as the M side).
+#include <atomic>
+
 #include <cuda.h>
 #include <cudaTypedefs.h>
 
@@ -48,7 +63,7 @@ constexpr int kChunkUnits = 256;           // units of a sequence that share one
 constexpr int kChunkRows = kChunkUnits * kRows;
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kBias = 8.f;               // P = 2^(a - M + kBias)
-constexpr float kSlack = 0.75f;   // a new maximum is set kHead above the row that forced it
+constexpr float kSlack = 0.75f;            // how far a row may exceed M before M moves
 constexpr uint32_t kSlab = 16384;          // [128 rows x 128 latent] e4m3, 128-byte swizzle
 constexpr uint32_t kPicks = 2048;          // [128 rows x 16 groups] table numbers of a unit
 constexpr uint32_t kStage = 8192;          // codes of one slab: [128 rows x 64 bytes]
@@ -80,7 +95,8 @@ struct Fp4Layout {
     static constexpr int kSoftGroups = kJoin ? 2 : 4, kExpGroups = 2, kGroups = 1 + kSoftGroups + kExpGroups;
     static constexpr int kThreads = 128 * kGroups, HW = HP / kSoftGroups, N = kJoin ? 2 * HP : HP;   // N: columns of an MMA
     static constexpr int WC = N / kSoftGroups;                          // columns of a warpgroup
-    // expanded tiles in flight (four per unit), and what the rest of shared memory holds of codes
+    // Expanded slabs in flight (four per unit), and stages of codes, which pay more than the eighth slab (32 heads: 176 us
+    // with 8 + 2, 152 with 7 + 4).
     static constexpr int kSlabs = HP == 96 ? 4 : (HP == 64 ? 5 : (HP <= 16 ? 8 : 7)),
                          kStages = HP >= 48 && HP != 64 ? 2 : 4;
     static constexpr int kPBufs = kJoin ? 2 : 1, kSBufs = 2 * N <= 128 ? 2 : 1;
@@ -103,8 +119,6 @@ struct Fp4Layout {
 
 struct Fp4Params {
     const __nv_bfloat16 *q_abs;
-    const uint8_t *c4;
-    long long ld;
     const int *lens;
     float *ws_o, *ws_m, *ws_l;   // [slots][H] (x r): sum of P c, M - kBias, l
     int2 *ws_seq;                // [B] per sequence: its first virtual unit and first chunk number
@@ -407,12 +421,13 @@ __device__ __forceinline__ bool elect_one() {
 }
 // ------------------------------------------------------------------ attention
 template <int HP>
-__global__ void __launch_bounds__(Fp4Layout<HP>::kThreads, 1) 
+__global__ void __launch_bounds__(Fp4Layout<HP>::kThreads, 1)
     fp4_attention_kernel(const __grid_constant__ CUtensorMap tm_codes, const __grid_constant__ CUtensorMap tm_scales,
                          const Fp4Params p) {
     using L = Fp4Layout<HP>;
     constexpr bool kJoin = L::kJoin;
-    constexpr int HW = L::HW, N = L::N, WC = L::WC, kSlabs = L::kSlabs, kPBufs = L::kPBufs, kSBufs = L::kSBufs, kStages = L::kStages;
+    constexpr int HW = L::HW, N = L::N, WC = L::WC, kSlabs = L::kSlabs, kStages = L::kStages, kPBufs = L::kPBufs,
+                  kSBufs = L::kSBufs;
     constexpr int kSoftWarps = 4 * L::kSoftGroups, kExpWarps = 4 * L::kExpGroups;
     extern __shared__ uint8_t smem_raw[];
     const uint32_t raw = smem_u32(smem_raw), base = (raw + 1023u) & ~1023u;
@@ -425,7 +440,11 @@ __global__ void __launch_bounds__(Fp4Layout<HP>::kThreads, 1)
         tma_prefetch_desc(&tm_scales);
         tma_prefetch_desc(&tm_codes);
         for (int i = 0; i < kStages; ++i) mbar_init(bar(sh.stage_full[i]), 1), mbar_init(bar(sh.stage_empty[i]), 4);
-        for (int i = 0; i < kPickBufs; ++i) mbar_init(bar(sh.scale_full[i]), 1), mbar_init(bar(sh.pick_full[i]), 1), mbar_init(bar(sh.pick_empty[i]), kExpWarps);
+        for (int i = 0; i < kPickBufs; ++i) {
+            mbar_init(bar(sh.scale_full[i]), 1);
+            mbar_init(bar(sh.pick_full[i]), 1);
+            mbar_init(bar(sh.pick_empty[i]), kExpWarps);
+        }
         for (int i = 0; i < kSlabs; ++i) mbar_init(bar(sh.slab_full[i]), 4), mbar_init(bar(sh.slab_free[i]), 1);
         for (int i = 0; i < kSBufs; ++i) mbar_init(bar(sh.s_full[i]), 1), mbar_init(bar(sh.s_free[i]), kSoftWarps);
         for (int i = 0; i < kPBufs; ++i) mbar_init(bar(sh.p_full[i]), kSoftWarps), mbar_init(bar(sh.p_free[i]), 1);
@@ -470,6 +489,7 @@ __global__ void __launch_bounds__(Fp4Layout<HP>::kThreads, 1)
                 const uint32_t pb = asked % kPickBufs;
                 if (asked >= kPickBufs) ok = ok && wait_bar(bar(sh.pick_empty[pb]), (asked / kPickBufs - 1) & 1);
                 if (lane == 0) {
+                    fence_proxy_async_smem();   // this warp's table numbers were written through the generic proxy
                     mbar_arrive_expect_tx(bar(sh.scale_full[pb]), kPicks);
                     tma_load_3d(base + L::PICK + pb * kPicks, &tm_scales, bar(sh.scale_full[pb]), kR / 2, next.row(far_seg),
                                 far_seg.seq);
@@ -483,8 +503,8 @@ __global__ void __launch_bounds__(Fp4Layout<HP>::kThreads, 1)
             for (uint32_t un = 0; unit.rows > 0; ++un) {
                 const uint32_t pb = un % kPickBufs;
                 ok = ok && wait_bar(bar(sh.scale_full[pb]), (un / kPickBufs) & 1);
-                // (the expansion is done with the unit four back and has begun with the slabs of none that the softmax is not
-                // done with six back: the ref slot, last used eight back, is free)
+                // (the expansion is done with the unit four back, so O is with the unit six back, and the softmax: the
+                // ref slot, last used eight back, is free)
                 uint4 *const at = reinterpret_cast<uint4 *>(smem + L::PICK + pb * kPicks) + lane;
 #pragma unroll 1
                 for (int i = 0; i < 4; ++i) {   // a lane takes rows lane + 32 i
@@ -532,9 +552,10 @@ __global__ void __launch_bounds__(Fp4Layout<HP>::kThreads, 1)
             }
             if (!ok && lane == 0) record_error(p.err, kDevErrTimeout);
             {   // this CTA's part of W_UV into L2: the cache's rows have pushed it out
-                const long long bytes = static_cast<long long>(p.H) * kDV * kR * 2, from = bytes * blockIdx.x / gridDim.x & ~15ll,
-                                to = bytes * (blockIdx.x + 1) / gridDim.x & ~15ll;
-                if (lead && to > from) bulk_prefetch_l2(reinterpret_cast<const uint8_t *>(p.w_uv) + from, static_cast<uint32_t>(to - from));
+                const uint32_t lines = static_cast<uint32_t>(p.H) * (kDV * kR * 2 / 128);   // of 128 bytes
+                const uint32_t from = lines * blockIdx.x / gridDim.x, to = lines * (blockIdx.x + 1) / gridDim.x;
+                if (lead && to > from)
+                    bulk_prefetch_l2(reinterpret_cast<const uint8_t *>(p.w_uv) + from * 128ull, (to - from) * 128);
             }
             // no load may still be landing when the CTA exits
 #pragma unroll 1
@@ -561,11 +582,12 @@ __global__ void __launch_bounds__(Fp4Layout<HP>::kThreads, 1)
                         if (!(ok = wait_bar(bar(sh.slab_full[sl]), (it / kSlabs) & 1))) break;
                         tc_fence_after();
                         const uint64_t a = desc_add(c0, sl * kSlab), b = desc_add(q0, k * L::kQSlab);
-                        if (lead)
+                        if (lead) {
 #pragma unroll
-                        for (int kk = 0; kk < 4; ++kk) {
-                            umma_f8(d, desc_add(a, kk * 32), desc_add(b, kk * 32), idesc, (k | kk) != 0);
-                            if (!kJoin) umma_f8(d, desc_add(a, kk * 32), desc_add(b, L::kQPart + kk * 32), idesc, 1);
+                            for (int kk = 0; kk < 4; ++kk) {
+                                umma_f8(d, desc_add(a, kk * 32), desc_add(b, kk * 32), idesc, (k | kk) != 0);
+                                if (!kJoin) umma_f8(d, desc_add(a, kk * 32), desc_add(b, L::kQPart + kk * 32), idesc, 1);
+                            }
                         }
                     }
                     if (ok && lead) umma_commit(bar(sh.s_full[sb]));
@@ -574,7 +596,6 @@ __global__ void __launch_bounds__(Fp4Layout<HP>::kThreads, 1)
             if (!ok && lane == 0) record_error(p.err, kDevErrTimeout);
         } else if (warp == 2) {
             if (blockIdx.x == 0) write_seq(p, lane);   // its first product is far off
-            {
             const bool lead = elect_one();
             // ---- O^T += c^T . P^T: slab t holds latent columns [128 t, 128 t + 128)
             constexpr uint32_t idesc = make_idesc_e4m3(128, N, 1, 1), idesc_lo = idesc | 1u << 10;   // B: e5m2
@@ -595,18 +616,18 @@ __global__ void __launch_bounds__(Fp4Layout<HP>::kThreads, 1)
                         const uint64_t a = desc_add(c0, sl * kSlab), b = desc_add(p0, pb * L::kPBuf);
                         if (lead) {
 #pragma unroll
-                        for (int kk = 0; kk < 4; ++kk) {
-                            umma_f8(d, desc_add(a, kk * 4096), desc_add(b, kk * 4096), idesc, (u | kk) != 0);
-                            if (!kJoin) umma_f8(d, desc_add(a, kk * 4096), desc_add(b, L::kPPart + kk * 4096), idesc_lo, 1);
-                        }
-                        umma_commit(bar(sh.slab_free[sl]));
+                            for (int kk = 0; kk < 4; ++kk) {
+                                umma_f8(d, desc_add(a, kk * 4096), desc_add(b, kk * 4096), idesc, (u | kk) != 0);
+                                if (!kJoin)
+                                    umma_f8(d, desc_add(a, kk * 4096), desc_add(b, L::kPPart + kk * 4096), idesc_lo, 1);
+                            }
+                            umma_commit(bar(sh.slab_free[sl]));
                         }
                     }
                     if (ok && lead) umma_commit(bar(sh.p_free[pb]));
                 }
             }
             if (!ok && lane == 0) record_error(p.err, kDevErrTimeout);
-            }
         }
     } else if (warp < 4 + kSoftWarps) {
         regs_acquire<L::kRegsSoft>();
@@ -630,9 +651,8 @@ __global__ void __launch_bounds__(Fp4Layout<HP>::kThreads, 1)
 #pragma unroll
                 for (int i = 0; i < 2; ++i) {
                     const int h = i0 + 4 * i;
-                    const uint4 *src = reinterpret_cast<const uint4 *>(
-                                           p.q_abs + (static_cast<size_t>(seg.seq) * p.H + (h < mine ? wg * HW + h : 0)) * kR) +
-                                       lane * 2;
+                    const size_t row = static_cast<size_t>(seg.seq) * p.H + (h < mine ? wg * HW + h : 0);
+                    const uint4 *src = reinterpret_cast<const uint4 *>(p.q_abs + row * kR) + lane * 2;
                     v[i][0] = h < mine ? __ldg(src) : make_uint4(0, 0, 0, 0);
                     v[i][1] = h < mine ? __ldg(src + 1) : make_uint4(0, 0, 0, 0);
                 }
@@ -662,7 +682,8 @@ __global__ void __launch_bounds__(Fp4Layout<HP>::kThreads, 1)
                 named_bar_sync(id, 128);
                 tc_fence_after();
 #pragma unroll
-                for (int g = 0; g < WC; g += 8) tmem_ld8(lanes + L::S_COL + sb * N + g, *reinterpret_cast<float (*)[8]>(s + g));
+                for (int g = 0; g < WC; g += 8)
+                    tmem_ld8(lanes + L::S_COL + sb * N + g, *reinterpret_cast<float (*)[8]>(s + g));
                 const int ref = sh.ref[un & 7][t];
                 // a row past the end has an all-zero tile row: its exponents are -infinity
                 const float row_scale = exp2_int(ref),
@@ -681,7 +702,8 @@ __global__ void __launch_bounds__(Fp4Layout<HP>::kThreads, 1)
                         float2 sc;
                         if constexpr (kJoin) {
                             const int c = 2 * (h + k);
-                            sc = fma2(make_float2(s[c + 2], s[c + 3]), make_float2(kLoPart, kLoPart), make_float2(s[c], s[c + 1]));
+                            sc = fma2(make_float2(s[c + 2], s[c + 3]), make_float2(kLoPart, kLoPart),
+                                      make_float2(s[c], s[c + 1]));
                         } else {
                             sc = make_float2(s[h + k], s[h + k + 1]);
                         }
@@ -703,7 +725,8 @@ __global__ void __launch_bounds__(Fp4Layout<HP>::kThreads, 1)
                             float y[W];
 #pragma unroll
                             for (int i = 0; i < W; i += 8)
-                                tmem_ld8(lanes + L::S_COL + sb * N + h0 * (W / 8) + i, *reinterpret_cast<float (*)[8]>(y + i));
+                                tmem_ld8(lanes + L::S_COL + sb * N + h0 * (W / 8) + i,
+                                         *reinterpret_cast<float (*)[8]>(y + i));
                             tmem_wait_ld();
 #pragma unroll
                             for (int k = 0; k < 8; ++k) {
@@ -792,7 +815,8 @@ __global__ void __launch_bounds__(Fp4Layout<HP>::kThreads, 1)
                 if constexpr (kJoin) {
 #pragma unroll
                     for (int i = 0; i < HW / 8; ++i)
-                        st_shared_v4(prow + sw128_offset(t, wg * (HW / 8) + i), w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
+                        st_shared_v4(prow + sw128_offset(t, wg * (HW / 8) + i), w[4 * i], w[4 * i + 1], w[4 * i + 2],
+                                     w[4 * i + 3]);
                 } else {
 #pragma unroll
                     for (int i = 0; i < HW / 8; ++i) {   // HW = 24 leaves 8-byte pieces
@@ -872,7 +896,8 @@ __global__ void __launch_bounds__(Fp4Layout<HP>::kThreads, 1)
                 for (int k = 0; k < 8; ++k) {
                     const int at = kJoin ? 2 * (k & ~1) + (k & 1) : k;
                     if (g + k < mine)
-                        st_keep(dst + static_cast<size_t>(k) * kR, kJoin ? fmaf(o[(at + 2) % 16], kLoPart, o[at]) : o[at], keep);
+                        st_keep(dst + static_cast<size_t>(k) * kR, kJoin ? fmaf(o[(at + 2) % 16], kLoPart, o[at]) : o[at],
+                                keep);
                 }
             }
             tc_fence_before();
@@ -882,8 +907,8 @@ __global__ void __launch_bounds__(Fp4Layout<HP>::kThreads, 1)
         if (!ok && lane == 0) record_error(p.err, kDevErrTimeout);
     } else {
         regs_release<L::kRegsExp>();
-        // ---- expansion: a warpgroup takes every other slab, a warp 32 of its rows, a lane the groups (32 codes) `g` of rows
-        // r + 8 i
+        // ---- expansion: a warpgroup takes every other slab, a warp 32 of its rows, a lane the groups (32 codes) `g` of
+        // rows r + 8 i
         constexpr int kBatch = kJoin ? 4 : 2;   // by the registers there are
         const int first = (warp - 4 - kSoftWarps) >> 2, g = lane & 3, r = (warp & 3) * 32 + (lane >> 2);
         const int x = ((2 * g) ^ (lane >> 2)) * 16;   // row & 7 = lane >> 2: the swizzle of the group's first 16 bytes
@@ -924,8 +949,9 @@ __global__ void __launch_bounds__(Fp4Layout<HP>::kThreads, 1)
                             expand8(w.y, tb[i], o[2], o[3]);
                             expand8(w.z, tb[i], o[4], o[5]);
                             expand8(w.w, tb[i], o[6], o[7]);
-                            *reinterpret_cast<uint4 *>(slab + (h + i) * 1024 + x) = make_uint4(o[0], o[1], o[2], o[3]);
-                            *reinterpret_cast<uint4 *>(slab + (h + i) * 1024 + (x ^ 16)) = make_uint4(o[4], o[5], o[6], o[7]);
+                            uint8_t *const to = slab + (h + i) * 1024;
+                            *reinterpret_cast<uint4 *>(to + x) = make_uint4(o[0], o[1], o[2], o[3]);
+                            *reinterpret_cast<uint4 *>(to + (x ^ 16)) = make_uint4(o[4], o[5], o[6], o[7]);
                         }
                     }
                     fence_proxy_async_smem();
@@ -1260,15 +1286,31 @@ size_t slot_count(int B, int max_len, int G) {
     return static_cast<size_t>(G) + static_cast<size_t>(B) * (max_len > 0 ? chunks_of(max_len) : 0);
 }
 
+// Runs f, which sets a kernel's attributes, the first time on each device (a call's host time counts in small decodes).
+template <typename F>
+cudaError_t first_time(std::atomic<unsigned long long> &done, F f) {
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    const unsigned long long bit = dev >= 0 && dev < 64 ? 1ull << dev : 0ull;
+    if (done.load(std::memory_order_relaxed) & bit) return cudaSuccess;
+    if ((e = f()) == cudaSuccess) done.fetch_or(bit, std::memory_order_relaxed);
+    return e;
+}
+
 template <int HP>
 cudaError_t launch_attention(const CUtensorMap &codes, const CUtensorMap &scales, const Fp4Params &p, cudaStream_t s) {
     using L = Fp4Layout<HP>;
-    cudaError_t e = cudaFuncSetAttribute(fp4_attention_kernel<HP>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                         static_cast<int>(L::kSmem));
+    static std::atomic<unsigned long long> done{0};
+    const cudaError_t e = first_time(done, [] {
+        cudaFuncAttributes fa;   // the kernel's register split assumes this launch budget
+        const cudaError_t e = cudaFuncGetAttributes(&fa, fp4_attention_kernel<HP>);
+        if (e != cudaSuccess) return e;
+        if (fa.numRegs != static_cast<int>(L::kRegsLaunch)) return cudaErrorInvalidConfiguration;
+        return cudaFuncSetAttribute(fp4_attention_kernel<HP>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                    static_cast<int>(L::kSmem));
+    });
     if (e != cudaSuccess) return e;
-    cudaFuncAttributes fa;   // the kernel's register split assumes this launch budget
-    if ((e = cudaFuncGetAttributes(&fa, fp4_attention_kernel<HP>)) != cudaSuccess) return e;
-    if (fa.numRegs != static_cast<int>(L::kRegsLaunch)) return cudaErrorInvalidConfiguration;
     note_launch();
     fp4_attention_kernel<HP><<<p.G, L::kThreads, L::kSmem, s>>>(codes, scales, p);
     return cudaGetLastError();
@@ -1276,8 +1318,11 @@ cudaError_t launch_attention(const CUtensorMap &codes, const CUtensorMap &scales
 
 template <int kSeqs>
 cudaError_t launch_dot(const MergeParams &mp, cudaLaunchConfig_t &cfg) {
-    const cudaError_t e = cudaFuncSetAttribute(fp4_merge_dot_kernel<kSeqs>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                               static_cast<int>(kDotSmem<kSeqs>));
+    static std::atomic<unsigned long long> done{0};
+    const cudaError_t e = first_time(done, [] {
+        return cudaFuncSetAttribute(fp4_merge_dot_kernel<kSeqs>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                    static_cast<int>(kDotSmem<kSeqs>));
+    });
     if (e != cudaSuccess) return e;
     cfg.gridDim = dim3(mp.H, (mp.B + kSeqs - 1) / kSeqs);
     cfg.blockDim = dim3(kDotThreads);
@@ -1288,7 +1333,8 @@ cudaError_t launch_dot(const MergeParams &mp, cudaLaunchConfig_t &cfg) {
 }  // namespace
 
 size_t decode_fp4_workspace_bytes(int B, int H, int max_len, int num_sms) {
-    return static_cast<size_t>(B) * sizeof(int2) + (num_sms + 1) * sizeof(int) + 8 + slot_count(B, max_len, num_sms) * H * (kR + 2) * sizeof(float);
+    return static_cast<size_t>(B) * sizeof(int2) + (num_sms + 1) * sizeof(int) + 8 +
+           slot_count(B, max_len, num_sms) * H * (kR + 2) * sizeof(float);
 }
 
 cudaError_t launch_decode_fp4(const DecodeArgs &a, cudaStream_t s) {
@@ -1296,38 +1342,35 @@ cudaError_t launch_decode_fp4(const DecodeArgs &a, cudaStream_t s) {
     if (a.num_sms > kMaxShares) return cudaErrorInvalidConfiguration;
     Fp4Params p;
     p.q_abs = static_cast<const __nv_bfloat16 *>(a.q_abs);
-    p.c4 = static_cast<const uint8_t *>(a.c_cache);
-    p.ld = a.ld_cache;
     p.lens = a.lens;
     p.B = a.B;
     p.H = a.H;
     p.max_len = a.max_len;
     p.G = a.num_sms;
+    // a segment's start and end in units (64 ragged sequences up to 32768 rows at 96 heads: 289 us with 1, 278 with 3,
+    // 275 with 4, 277 with 6; 7 x 5000 rows at 37 heads: 17.2 with 3, 18.6 with 4)
     p.over = a.H > 48 ? 4 : 3;
     const size_t slots = slot_count(a.B, a.max_len, p.G);
     if (decode_fp4_workspace_bytes(a.B, a.H, a.max_len, a.num_sms) > a.workspace_bytes) return cudaErrorInvalidValue;
     p.ws_o = static_cast<float *>(a.workspace);
     p.ws_m = p.ws_o + slots * a.H * kR;
     p.ws_l = p.ws_m + slots * a.H;
-    p.ws_seq = reinterpret_cast<int2 *>((reinterpret_cast<uintptr_t>(p.ws_l + slots * a.H) + 7) & ~static_cast<uintptr_t>(7));
+    const uintptr_t seq = reinterpret_cast<uintptr_t>(p.ws_l + slots * a.H);
+    p.ws_seq = reinterpret_cast<int2 *>((seq + 7) & ~static_cast<uintptr_t>(7));
     p.ws_share = reinterpret_cast<int *>(p.ws_seq + a.B);
     p.w_uv = static_cast<const __nv_bfloat16 *>(a.w_uv);
     p.err = a.dev_err;
     p.scale_log2 = a.scale * kLog2e;
-    CUtensorMap tm_codes, tm_scales, tm_wuv;
+    CUtensorMap tm_codes, tm_scales;
     {
         const cuuint64_t rows = static_cast<cuuint64_t>(a.max_len > 0 ? a.max_len : 1);
         const cuuint64_t dims[3] = {kR / 2 + kR / 32, rows, static_cast<cuuint64_t>(a.B)};
         const cuuint64_t strides[2] = {static_cast<cuuint64_t>(a.ld_cache), rows * static_cast<cuuint64_t>(a.ld_cache)};
         const cuuint32_t box[3] = {64, kRows, 1}, sbox[3] = {16, kRows, 1};
-        const cuuint64_t wd[2] = {kR, static_cast<cuuint64_t>(a.H) * kDV}, ws[1] = {kR * 2};
-        const cuuint32_t wb[2] = {64, kDV};
         if (encode_map(&tm_codes, CU_TENSOR_MAP_DATA_TYPE_UINT8, CU_TENSOR_MAP_SWIZZLE_NONE, a.c_cache, 3, dims, strides,
                        box) != CUDA_SUCCESS ||
             encode_map(&tm_scales, CU_TENSOR_MAP_DATA_TYPE_UINT8, CU_TENSOR_MAP_SWIZZLE_NONE, a.c_cache, 3, dims, strides,
-                       sbox) != CUDA_SUCCESS ||
-            encode_map(&tm_wuv, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, CU_TENSOR_MAP_SWIZZLE_128B, a.w_uv, 2, wd, ws, wb) !=
-                CUDA_SUCCESS)
+                       sbox) != CUDA_SUCCESS)
             return cudaErrorInvalidValue;
     }
     cudaError_t e = a.H <= 16   ? launch_attention<16>(tm_codes, tm_scales, p, s)
@@ -1336,8 +1379,9 @@ cudaError_t launch_decode_fp4(const DecodeArgs &a, cudaStream_t s) {
                     : a.H <= 64 ? launch_attention<64>(tm_codes, tm_scales, p, s)
                                 : launch_attention<96>(tm_codes, tm_scales, p, s);
     if (e != cudaSuccess) return e;
-    const MergeParams mp{a.lens, p.ws_seq, p.ws_share, p.ws_o, p.ws_m, p.ws_l, p.w_uv, static_cast<const __nv_bfloat16 *>(a.gate),
-                         static_cast<__nv_bfloat16 *>(a.out), a.dev_err, a.B, a.H, a.max_len, p.G, p.over};
+    const MergeParams mp{a.lens, p.ws_seq, p.ws_share, p.ws_o, p.ws_m, p.ws_l, p.w_uv,
+                         static_cast<const __nv_bfloat16 *>(a.gate), static_cast<__nv_bfloat16 *>(a.out), a.dev_err, a.B,
+                         a.H, a.max_len, p.G, p.over};
     cudaLaunchConfig_t cfg = {};
     cfg.stream = s;
     cudaLaunchAttribute attr[1];
@@ -1346,14 +1390,26 @@ cudaError_t launch_decode_fp4(const DecodeArgs &a, cudaStream_t s) {
     cfg.attrs = attr;
     cfg.numAttrs = 1;
     note_launch();
-    // up to four sequences per CTA, as long as one wave of CTAs (two, of the largest) takes them all
+    // Up to four sequences per CTA, as long as one wave of CTAs (two, of the largest) takes them all.  Whole decodes of 300
+    // rows: 16 heads x 16 sequences 17.1 / 14.7 / 15.9 / 18.5 us with one, two, four per CTA and the tensor cores, x 64
+    // 37.5 / 30.4 / 25.9 / 27.8, x 96 49.7 / 38.2 / 32.2 / 29.4; 96 heads x 1 20.9 / 21.6 / 23.2 / 24.8 (of 100000 rows
+    // 55 / 57 / 59 / 97: there a pair's segments are spread over sixteen warps), x 64 156 / 109 / 87 / 41.
     const auto ctas = [&](int seqs) { return static_cast<long long>(a.H) * ((a.B + seqs - 1) / seqs); };
     if (ctas(1) <= a.num_sms) return launch_dot<1>(mp, cfg);
     if (ctas(2) <= a.num_sms) return launch_dot<2>(mp, cfg);
     if (ctas(4) <= 2 * a.num_sms) return launch_dot<4>(mp, cfg);
-    if ((e = cudaFuncSetAttribute(fp4_merge_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                  static_cast<int>(kSmemMerge))) != cudaSuccess)
+    static std::atomic<unsigned long long> done{0};
+    if ((e = first_time(done, [] {
+             return cudaFuncSetAttribute(fp4_merge_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                         static_cast<int>(kSmemMerge));
+         })) != cudaSuccess)
         return e;
+    CUtensorMap tm_wuv;
+    const cuuint64_t wd[2] = {kR, static_cast<cuuint64_t>(a.H) * kDV}, ws[1] = {kR * 2};
+    const cuuint32_t wb[2] = {64, kDV};
+    if (encode_map(&tm_wuv, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, CU_TENSOR_MAP_SWIZZLE_128B, a.w_uv, 2, wd, ws, wb) !=
+        CUDA_SUCCESS)
+        return cudaErrorInvalidValue;
     cfg.gridDim = dim3(a.H, (a.B + kMRows - 1) / kMRows);
     cfg.blockDim = dim3(kMergeThreads);
     cfg.dynamicSmemBytes = kSmemMerge;

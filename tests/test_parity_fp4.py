@@ -341,9 +341,10 @@ def test_decode_maxima_that_keep_rising(env, H):
         check(env, d, decode(env, d))
 
 
-def test_decode_nan_row_stays_in_its_sequence(env):
+@pytest.mark.parametrize("H", [40, 96])
+def test_decode_nan_row_stays_in_its_sequence(env, H):
     torch, lca, _ = env
-    d = decode_case(40, [300, 300, 300], 300, seed=9)
+    d = decode_case(H, [300, 300, 300], 300, seed=9)
     clean = decode(env, d)
     d["rows"][1, 222, 256 + 3] = 255
     got = decode(env, d)
