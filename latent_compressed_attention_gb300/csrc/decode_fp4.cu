@@ -67,13 +67,13 @@ constexpr float kSlack = 0.75f;            // how far a row may exceed M before 
 constexpr uint32_t kSlab = 16384;          // [128 rows x 128 latent] e4m3, 128-byte swizzle
 constexpr uint32_t kPicks = 2048;          // [128 rows x 16 groups] table numbers of a unit
 constexpr uint32_t kStage = 8192;          // codes of one slab: [128 rows x 64 bytes]
-constexpr int kPickBufs = 4;
+constexpr int kMaxPickBufs = 4;
 constexpr int kTables = 22;                // exponents -14 (all zero) .. 6 below the row's largest, then NaN
 constexpr int kMaxSoftWarps = 16, kMaxHW = 24;
 
 struct Fp4Shared {
     uint64_t stage_full[4], stage_empty[4];
-    uint64_t scale_full[kPickBufs], pick_full[kPickBufs], pick_empty[kPickBufs];
+    uint64_t scale_full[kMaxPickBufs], pick_full[kMaxPickBufs], pick_empty[kMaxPickBufs];
     uint64_t slab_full[8], slab_free[8];
     uint64_t s_full[2], s_free[2], q_ready;
     uint64_t p_full[2], p_free[2];
@@ -81,9 +81,9 @@ struct Fp4Shared {
     uint2 table[kTables];
     int16_t ref[8][kRows];                 // per row of the last eight units: the power of two its tile is divided by
     alignas(16) float mul[96];             // per head: score factor
-    // per softmax warp and head, the same in a warpgroup's four: kBias - M, and the last change of it with its power of
-    // two (part: the warps' maxima, and their parts of l while a segment is drained)
-    alignas(16) float bias[kMaxSoftWarps][kMaxHW], step[kMaxSoftWarps][kMaxHW], fac[kMaxSoftWarps][kMaxHW];
+    // per softmax warpgroup and head: kBias - M, and the last change of it with its power of two
+    alignas(16) float bias[kMaxSoftWarps / 4][kMaxHW], step[kMaxSoftWarps / 4][kMaxHW], fac[kMaxSoftWarps / 4][kMaxHW];
+    // per softmax warp: maxima, and parts of l while a segment is drained
     float part[kMaxSoftWarps][kMaxHW];
 };
 
@@ -95,10 +95,12 @@ struct Fp4Layout {
     static constexpr int kSoftGroups = kJoin ? 2 : 4, kExpGroups = 2, kGroups = 1 + kSoftGroups + kExpGroups;
     static constexpr int kThreads = 128 * kGroups, HW = HP / kSoftGroups, N = kJoin ? 2 * HP : HP;   // N: columns of an MMA
     static constexpr int WC = N / kSoftGroups;                          // columns of a warpgroup
-    // Expanded slabs in flight (four per unit), and stages of codes, which pay more than the eighth slab (32 heads: 176 us
-    // with 8 + 2, 152 with 7 + 4).
-    static constexpr int kSlabs = HP == 96 ? 4 : (HP == 64 ? 5 : (HP <= 16 ? 8 : 7)),
-                         kStages = HP >= 48 && HP != 64 ? 2 : 4;
+    // Expanded slabs in flight (four per unit), stages of codes and buffers of table numbers, as the queries leave room:
+    // 64 x 16384 rows, us with slabs + stages: 16 heads 111 with 8 + 4, 121 with 7 + 4; 32 heads 136 with 8 + 2, 149 with
+    // 7 + 4; 48 heads 172 with 7 + 2, 217 with 8 + 1; 64 heads 210 with 6 + 2, 221 with 5 + 4, 233 with 7 + 1; 96 heads
+    // 264 with 5 + 1, 268 with 4 + 2.
+    static constexpr int kSlabs = HP == 96 ? 5 : (HP == 64 ? 6 : (HP == 48 ? 7 : 8)),
+                         kStages = HP == 96 ? 1 : (HP == 16 ? 4 : 2), kPickBufs = HP == 96 ? 2 : 4;
     static constexpr int kPBufs = kJoin ? 2 : 1, kSBufs = 2 * N <= 128 ? 2 : 1;
     static constexpr uint32_t kQPart = HP * 128, kQSlab = 2 * kQPart;   // [hi | lo rows x 128 latent]; kJoin: interleaved
     static constexpr uint32_t kPPart = kRows * 128, kPBuf = kJoin ? kPPart : 2 * kPPart;
@@ -113,6 +115,9 @@ struct Fp4Layout {
     static_assert(kRegsCtl + kSoftGroups * kRegsSoft + kExpGroups * kRegsExp <= kGroups * kRegsLaunch,
                   "register split exceeds the launch");
     static_assert(kQPart % 1024 == 0 && O_COL + 4 * N <= 512 && kSBufs * N <= O_COL && N <= 128, "layout");
+    // barriers of full stages: each is waited on by one warpgroup alone, which so sees every one of its phases
+    static constexpr int kFull = kStages == 1 ? 2 : kStages;
+    static_assert(kExpGroups == 2 && kFull % 2 == 0, "layout");
     static_assert(HW % 8 == 0 && HW <= kMaxHW && 4 * kSoftGroups <= kMaxSoftWarps, "layout");
     static_assert(kSlabs <= 8 && kSlabs >= 4 && END % 16 == 0 && kSmem <= 232448, "shared memory");
 };
@@ -412,6 +417,11 @@ __device__ __forceinline__ bool wait_bar(uint32_t bar, uint32_t parity) {
     return true;
 }
 
+// The same for a whole warp, which leaves it together and of one mind (a lane that fell two phases behind the others would
+// mistake the barrier's parity).
+__device__ __forceinline__ bool wait_warp(uint32_t bar, uint32_t parity) {
+    return __all_sync(0xffffffffu, wait_bar(bar, parity));
+}
 // True in one lane of a warp that is here together: the issuing warps stay converged around their waits and loops, as
 // code that the compiler knows to be one lane's takes more instructions (319 -> 305 us at 96 heads, 64 x 16384 rows).
 __device__ __forceinline__ bool elect_one() {
@@ -427,7 +437,7 @@ __global__ void __launch_bounds__(Fp4Layout<HP>::kThreads, 1)
     using L = Fp4Layout<HP>;
     constexpr bool kJoin = L::kJoin;
     constexpr int HW = L::HW, N = L::N, WC = L::WC, kSlabs = L::kSlabs, kStages = L::kStages, kPBufs = L::kPBufs,
-                  kSBufs = L::kSBufs;
+                  kSBufs = L::kSBufs, kPickBufs = L::kPickBufs, kFull = L::kFull;
     constexpr int kSoftWarps = 4 * L::kSoftGroups, kExpWarps = 4 * L::kExpGroups;
     extern __shared__ uint8_t smem_raw[];
     const uint32_t raw = smem_u32(smem_raw), base = (raw + 1023u) & ~1023u;
@@ -439,7 +449,8 @@ __global__ void __launch_bounds__(Fp4Layout<HP>::kThreads, 1)
     if (threadIdx.x == 0) {
         tma_prefetch_desc(&tm_scales);
         tma_prefetch_desc(&tm_codes);
-        for (int i = 0; i < kStages; ++i) mbar_init(bar(sh.stage_full[i]), 1), mbar_init(bar(sh.stage_empty[i]), 4);
+        for (int i = 0; i < kFull; ++i) mbar_init(bar(sh.stage_full[i]), 1);
+        for (int i = 0; i < kStages; ++i) mbar_init(bar(sh.stage_empty[i]), 4);
         for (int i = 0; i < kPickBufs; ++i) {
             mbar_init(bar(sh.scale_full[i]), 1);
             mbar_init(bar(sh.pick_full[i]), 1);
@@ -540,11 +551,12 @@ __global__ void __launch_bounds__(Fp4Layout<HP>::kThreads, 1)
                     for (int k = 0; k < 4; ++k, ++it) {
                         const uint32_t st = it % kStages;
                         if (it >= kStages &&
-                            !(ok = wait_bar(bar(sh.stage_empty[st]), (it / kStages - 1) & 1)))
+                            !(ok = wait_warp(bar(sh.stage_empty[st]), (it / kStages - 1) & 1)))
                             break;
                         if (lead) {
-                            mbar_arrive_expect_tx(bar(sh.stage_full[st]), kStage);
-                            tma_load_3d_hint(base + L::STAGE + st * kStage, &tm_codes, bar(sh.stage_full[st]), k * 64,
+                            const uint32_t full = bar(sh.stage_full[it % kFull]);
+                            mbar_arrive_expect_tx(full, kStage);
+                            tma_load_3d_hint(base + L::STAGE + st * kStage, &tm_codes, full, k * 64,
                                              seg.row0 + u * kRows, seg.seq, once);
                         }
                     }
@@ -560,7 +572,7 @@ __global__ void __launch_bounds__(Fp4Layout<HP>::kThreads, 1)
             // no load may still be landing when the CTA exits
 #pragma unroll 1
             for (uint32_t k = it > kStages ? it - kStages : 0; k < it; ++k)
-                wait_bar(bar(sh.stage_full[k % kStages]), (k / kStages) & 1);
+                wait_bar(bar(sh.stage_full[k % kFull]), (k / kFull) & 1);
         } else if (warp == 1) {
             const bool lead = elect_one();
             // ---- S^T = c . q^T: four slabs of K = 128
@@ -570,16 +582,16 @@ __global__ void __launch_bounds__(Fp4Layout<HP>::kThreads, 1)
             bool ok = true;
 #pragma unroll 1
             while (ok && walk.next(seg)) {
-                if (!(ok = wait_bar(bar(sh.q_ready), ns++ & 1))) break;
+                if (!(ok = wait_warp(bar(sh.q_ready), ns++ & 1))) break;
 #pragma unroll 1
                 for (int u = 0; ok && u < seg.units; ++u, ++un) {
                     const uint32_t sb = un % kSBufs, d = tmem + L::S_COL + sb * N;
-                    if (un >= kSBufs && !(ok = wait_bar(bar(sh.s_free[sb]), (un / kSBufs - 1) & 1)))
+                    if (un >= kSBufs && !(ok = wait_warp(bar(sh.s_free[sb]), (un / kSBufs - 1) & 1)))
                         break;
 #pragma unroll 1
                     for (int k = 0; k < 4; ++k, ++it) {
                         const uint32_t sl = it % kSlabs;
-                        if (!(ok = wait_bar(bar(sh.slab_full[sl]), (it / kSlabs) & 1))) break;
+                        if (!(ok = wait_warp(bar(sh.slab_full[sl]), (it / kSlabs) & 1))) break;
                         tc_fence_after();
                         const uint64_t a = desc_add(c0, sl * kSlab), b = desc_add(q0, k * L::kQSlab);
                         if (lead) {
@@ -607,12 +619,12 @@ __global__ void __launch_bounds__(Fp4Layout<HP>::kThreads, 1)
 #pragma unroll 1
                 for (int u = 0; ok && u < seg.units; ++u, ++un) {
                     const uint32_t pb = un % kPBufs;
-                    if (!(ok = wait_bar(bar(sh.p_full[pb]), (un / kPBufs) & 1))) break;
+                    if (!(ok = wait_warp(bar(sh.p_full[pb]), (un / kPBufs) & 1))) break;
                     tc_fence_after();
 #pragma unroll 1
                     for (int t = 0; t < 4; ++t, ++it) {
                         const uint32_t sl = it % kSlabs, d = tmem + L::O_COL + t * N;
-                        if (!(ok = wait_bar(bar(sh.slab_full[sl]), (it / kSlabs) & 1))) break;
+                        if (!(ok = wait_warp(bar(sh.slab_full[sl]), (it / kSlabs) & 1))) break;
                         const uint64_t a = desc_add(c0, sl * kSlab), b = desc_add(p0, pb * L::kPBuf);
                         if (lead) {
 #pragma unroll
@@ -635,7 +647,7 @@ __global__ void __launch_bounds__(Fp4Layout<HP>::kThreads, 1)
         // failed wait every warp runs its loops to their end, without waiting
         const int sw = warp - 4, wg = sw >> 2, quad = warp & 3, t = quad * 32 + lane, id = 1 + wg;
         const uint32_t lanes = tmem + (static_cast<uint32_t>(quad * 32) << 16) + wg * WC;
-        float *const mul = sh.mul + wg * HW, *const bias = sh.bias[sw], *const step = sh.step[sw], *const fac = sh.fac[sw],
+        float *const mul = sh.mul + wg * HW, *const bias = sh.bias[wg], *const step = sh.step[wg], *const fac = sh.fac[wg],
                      *const part = sh.part[sw];
         const float(*const all)[kMaxHW] = sh.part + 4 * wg;
         const int mine = min(HW, p.H - wg * HW);   // real heads of this warpgroup (may be <= 0)
@@ -663,7 +675,8 @@ __global__ void __launch_bounds__(Fp4Layout<HP>::kThreads, 1)
                     if (lane == 0) mul[h] = h < mine ? undo * p.scale_log2 : 0.f;
                 }
             }
-            if (lane < HW) bias[lane] = lane < mine ? kBias : -INFINITY;   // padding heads: P = 0, never a new maximum
+            if (quad == 0 && lane < HW)
+                bias[lane] = lane < mine ? kBias : -INFINITY;   // padding heads: P = 0, never a new maximum
             fence_proxy_async_smem();
             named_bar_sync(id, 128);
             if (lane == 0) mbar_arrive(bar(sh.q_ready));
@@ -766,12 +779,14 @@ __global__ void __launch_bounds__(Fp4Layout<HP>::kThreads, 1)
                         most = fmaxf(fmaxf(all[0][lane], all[1][lane]), fmaxf(all[2][lane], all[3][lane]));
                         moves = (most > kBias + kSlack || u == 0) && most > -INFINITY;
                         const float by = moves ? kBias - L::kHead - most : 0.f;   // M_old - M_new
-                        step[lane] = by;
-                        fac[lane] = fast_exp2(by);
-                        bias[lane] += by;
+                        if (quad == 0) {
+                            step[lane] = by;
+                            fac[lane] = fast_exp2(by);
+                            bias[lane] += by;
+                        }
                     }
                     moved = u > 0 ? __ballot_sync(0xffffffffu, moves) : 0u;
-                    __syncwarp();
+                    named_bar_sync(id, 128);
 #pragma unroll
                     for (int h = 0; h < HW; h += 4) {
                         const float4 by = lds4(step + h);
@@ -925,12 +940,13 @@ __global__ void __launch_bounds__(Fp4Layout<HP>::kThreads, 1)
 #pragma unroll 1
                 for (int k = first; k < 4; k += L::kExpGroups) {
                     const uint32_t it = 4 * un + k, sl = it % kSlabs, st = it % kStages;
-                    ok = ok && wait_bar(bar(sh.stage_full[st]), (it / kStages) & 1);
+                    ok = ok && wait_bar(bar(sh.stage_full[it % kFull]), (it / kFull) & 1);
                     // the codes wait for their slab in registers: the stage can take the next ones meanwhile
                     uint4 c[4];
 #pragma unroll
                     for (int i = 0; i < 4; ++i)
                         c[i] = *reinterpret_cast<const uint4 *>(smem + stage_at + st * kStage + i * 512);
+                    fence_proxy_async_smem();   // the reads, before TMA writes there again
                     __syncwarp();
                     if (lane == 0) mbar_arrive(bar(sh.stage_empty[st]));
                     if (it >= kSlabs) ok = ok && wait_bar(bar(sh.slab_free[sl]), (it / kSlabs - 1) & 1);
