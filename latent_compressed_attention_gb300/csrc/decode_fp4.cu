@@ -34,13 +34,14 @@
 // permute per four codes: the group's exponent selects an 8-byte table of e4m3 magnitudes, the codes' three magnitude
 // bits are the selector.
 //
-// What bounds it (64 x 16384 rows, 1.93 GHz): at 96 heads 268 us, 9600 cycles a unit, of which the tensor pipe needs
-// 3600 (64 products of 56 cycles: shared memory feeds it 128 bytes a cycle).  The queries' 96 KB leave room for one unit
-// of expanded slabs, so a unit's expansion, S, softmax and O follow one another, each slab of the next unit expanded as
-// O leaves it.  At 48 heads 168 us (6000 cycles a unit), at 16 heads 107 us (3850; 1650 on the tensor pipe, the
-// expansion's byte permutes and logic about 2000 on the ALUs).  All roles' loops share an instruction cache that they
-// overflow easily: waits that carry their error path and issue loops unrolled fourfold cost 193 us instead of 127 at 16
-// heads, which is why loops here are kept rolled and cold code short.
+// What bounds it (64 x 16384 rows with their merge, 1.93 GHz): at 96 heads 264 us, 9450 cycles a unit, of which the
+// tensor pipe is busy 46 % (64 products of 56 cycles: shared memory feeds it 128 bytes a cycle).  The queries' 96 KB leave
+// room for one unit of expanded slabs and one slab more, so a unit's expansion, S, softmax and O mostly follow one
+// another, each slab of the next unit expanded as O leaves one.  At 48 heads 172 us (6200 cycles a unit), at 16 heads
+// 110 us (3940; tensor pipe 47 %, ALUs 55 %: the expansion's byte permutes and logic).  HBM is at 0.16 to 0.38 of its
+// peak.  All roles' loops share an instruction cache that they overflow easily: waits that carry their error path and
+// issue loops unrolled fourfold cost 193 us instead of 127 at 16 heads, which is why loops here are kept rolled, issuing
+// warps converged and cold code short.
 //
 // Merge kernels: the segments of a sequence are joined with the log-sum-exp rule and multiplied by W_UV^T, then the gate.
 // Few (head, sequence) pairs: a CTA per head and up to four sequences, the product in fp32 from W_UV[h] in shared memory.

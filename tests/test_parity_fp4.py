@@ -478,6 +478,26 @@ def test_same_inputs_same_bits(env):
     assert np.array_equal(decode(env, d), decode(env, d))
 
 
+@pytest.mark.parametrize("H", [16, 32, 48, 64, 96])
+def test_same_bits_over_long_shares(env, H):
+    """Many units per CTA, every buffer reused many times: flat softmaxes, so that each row counts."""
+    torch, lca, oracle = env
+    B, n = 16, 12000
+    gen = torch.Generator(device="cuda").manual_seed(H)
+    cache = torch.empty((B, n, ROW), dtype=torch.uint8, device="cuda")
+    for b in range(B):
+        lca.mla_quantize_latent_fp4(torch.randn((n, R), generator=gen, device="cuda"), out=cache[b])
+    q = (torch.randn((B, H, R), generator=gen, device="cuda") * 0.05).bfloat16()
+    w_uv = (torch.randn((H, 128, R), generator=gen, device="cuda") * 0.02).bfloat16()
+    lens = torch.full((B,), n, dtype=torch.int32, device="cuda")
+    runs = [lca.mla_latent_decode_fp4(q, cache, lens, w_uv) for _ in range(4)]
+    torch.cuda.synchronize()
+    assert lca.mla_get_device_error() == 0 and all(torch.equal(runs[0], x) for x in runs[1:])
+    one = dict(q_abs=q[3:4].double().cpu().numpy(), lens=np.array([n], np.int32), gate=None,
+               w_uv=w_uv.double().cpu().numpy(), rows=cache[3:4].cpu().numpy())
+    check(env, one, runs[0][3:4].double().cpu().numpy())
+
+
 def test_decode_length_outside_the_cache_is_clamped_and_reported(env):
     torch, lca, _ = env
     d = decode_case(8, [300, 50], 300, seed=14)
