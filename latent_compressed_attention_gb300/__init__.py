@@ -647,14 +647,20 @@ def mla_latent_decode_fp4(q_abs, c4_cache, lens, w_uv, gate=None, scale: float =
             out = torch.empty((B, H * d_v), dtype=torch.bfloat16, device=dev)
         else:
             _check(out, "out", torch.bfloat16, dev, (B, H * d_v))
-        if workspace is None:
-            need = lib.mla_latent_decode_fp4_workspace_size(B, H, r, max_len)
-            workspace = torch.empty(need, dtype=torch.uint8, device=dev) if need > 0 else None
-        ws_ptr = None if workspace is None else workspace.data_ptr()
-        ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
-        rc = lib.mla_latent_decode_fp4(q_abs.data_ptr(), c4_cache.data_ptr(), ld, lens.data_ptr(), max_len,
-                                       w_uv.data_ptr(), None if gate is None else gate.data_ptr(), float(scale),
-                                       out.data_ptr(), B, H, d_v, r, ws_ptr, ws_bytes, _raw_stream(stream, dev))
+        on, scratch = _raw_stream(stream, dev), None
+        if workspace is not None:
+            ws_ptr, ws_bytes = workspace.data_ptr(), workspace.numel() * workspace.element_size()
+        else:
+            # from the caching allocator without a tensor around it, which small decodes' host time would show
+            ws_bytes = lib.mla_latent_decode_fp4_workspace_size(B, H, r, max_len)
+            ws_ptr = scratch = torch._C._cuda_cudaCachingAllocator_raw_alloc(ws_bytes, on) if ws_bytes > 0 else None
+        try:
+            rc = lib.mla_latent_decode_fp4(q_abs.data_ptr(), c4_cache.data_ptr(), ld, lens.data_ptr(), max_len,
+                                           w_uv.data_ptr(), None if gate is None else gate.data_ptr(), float(scale),
+                                           out.data_ptr(), B, H, d_v, r, ws_ptr, ws_bytes, on)
+        finally:
+            if scratch is not None:   # as a tensor's memory: the next taker on this stream comes after these kernels
+                torch._C._cuda_cudaCachingAllocator_raw_delete(scratch)
     if rc != 0:
         raise MLAError(rc, "mla_latent_decode_fp4")
     return out
