@@ -654,33 +654,64 @@ __global__ void __launch_bounds__(Fp4Layout<HP>::kThreads, 1)
         const int mine = min(HW, p.H - wg * HW);   // real heads of this warpgroup (may be <= 0)
         uint32_t un = 0;
         bool ok = true, more = walk.next(seg);
+        size_t done = 0;   // the slot (first row of this warpgroup's heads) of the segment before, to be drained
         float l[HW];
 #pragma unroll 1
-        while (more) {
-            // the segment's queries (S of the last unit before this has been read, so the buffer is free)
+        for (;;) {
+            if (more) {
+                // the segment's queries: S of the last unit before this has been read, so the buffer is free, and S of the
+                // first one can run while O^T of the segment before is drained
 #pragma unroll 1
-            for (int i0 = quad; i0 < HW; i0 += 8) {
-                uint4 v[2][2];
+                for (int i0 = quad; i0 < HW; i0 += 8) {
+                    uint4 v[2][2];
 #pragma unroll
-                for (int i = 0; i < 2; ++i) {
-                    const int h = i0 + 4 * i;
-                    const size_t row = static_cast<size_t>(seg.seq) * p.H + (h < mine ? wg * HW + h : 0);
-                    const uint4 *src = reinterpret_cast<const uint4 *>(p.q_abs + row * kR) + lane * 2;
-                    v[i][0] = h < mine ? __ldg(src) : make_uint4(0, 0, 0, 0);
-                    v[i][1] = h < mine ? __ldg(src + 1) : make_uint4(0, 0, 0, 0);
-                }
+                    for (int i = 0; i < 2; ++i) {
+                        const int h = i0 + 4 * i;
+                        const size_t row = static_cast<size_t>(seg.seq) * p.H + (h < mine ? wg * HW + h : 0);
+                        const uint4 *src = reinterpret_cast<const uint4 *>(p.q_abs + row * kR) + lane * 2;
+                        v[i][0] = h < mine ? __ldg(src) : make_uint4(0, 0, 0, 0);
+                        v[i][1] = h < mine ? __ldg(src + 1) : make_uint4(0, 0, 0, 0);
+                    }
 #pragma unroll
-                for (int i = 0; i < 2; ++i) {
-                    const int h = i0 + 4 * i;
-                    const float undo = store_query<HP>(base + L::Q, wg * HW + h, lane, v[i]);
-                    if (lane == 0) mul[h] = h < mine ? undo * p.scale_log2 : 0.f;
+                    for (int i = 0; i < 2; ++i) {
+                        const int h = i0 + 4 * i;
+                        const float undo = store_query<HP>(base + L::Q, wg * HW + h, lane, v[i]);
+                        if (lane == 0) mul[h] = h < mine ? undo * p.scale_log2 : 0.f;
+                    }
                 }
+                if (quad == 0 && lane < HW)
+                    bias[lane] = lane < mine ? kBias : -INFINITY;   // padding heads: P = 0, never a new maximum
+                fence_proxy_async_smem();
+                named_bar_sync(id, 128);
+                if (lane == 0) mbar_arrive(bar(sh.q_ready));
             }
-            if (quad == 0 && lane < HW)
-                bias[lane] = lane < mine ? kBias : -INFINITY;   // padding heads: P = 0, never a new maximum
-            fence_proxy_async_smem();
-            named_bar_sync(id, 128);
-            if (lane == 0) mbar_arrive(bar(sh.q_ready));
+            if (un > 0) {
+                // ---- O^T of the segment before (lane = latent column of its tile)
+                const uint32_t last = un - 1;
+                ok = ok && wait_bar(bar(sh.p_free[last % kPBufs]), (last / kPBufs) & 1);
+                __syncwarp();
+                tc_fence_after();
+                const uint64_t keep = l2_policy_evict_last();   // the merge reads it soon
+#pragma unroll 1
+                for (int c = 0; c < 4 * (HW / 8); ++c) {
+                    const int tile = c / (HW / 8), g = c % (HW / 8) * 8;
+                    float *const dst = p.ws_o + (done + g) * kR + tile * 128 + t;
+                    float o[kJoin ? 16 : 8];
+#pragma unroll
+                    for (int i = 0; i < (kJoin ? 16 : 8); i += 8)
+                        tmem_ld8(lanes + L::O_COL + tile * N + (kJoin ? 2 * g : g) + i, *reinterpret_cast<float (*)[8]>(o + i));
+                    tmem_wait_ld();
+#pragma unroll
+                    for (int k = 0; k < 8; ++k) {
+                        const int at = kJoin ? 2 * (k & ~1) + (k & 1) : k;
+                        if (g + k < mine)
+                            st_keep(dst + static_cast<size_t>(k) * kR, kJoin ? fmaf(o[(at + 2) % 16], kLoPart, o[at]) : o[at],
+                                    keep);
+                    }
+                }
+                tc_fence_before();
+            }
+            if (!more) break;
 #pragma unroll
             for (int h = 0; h < HW; ++h) l[h] = 0.f;
 
@@ -869,7 +900,7 @@ __global__ void __launch_bounds__(Fp4Layout<HP>::kThreads, 1)
                 __syncwarp();
                 if (lane == 0) mbar_arrive(bar(sh.p_full[pb]));
             }
-            // ---- drain: l over the 128 rows, then O^T (lane = latent column of its tile)
+            // ---- the segment's maxima, and l over the 128 rows
             // (every step halves the heads that a lane holds, so that lane h ends with head h's sum over the warp)
             {
                 constexpr int P = HW <= 8 ? 8 : (HW <= 16 ? 16 : 32);
@@ -889,35 +920,12 @@ __global__ void __launch_bounds__(Fp4Layout<HP>::kThreads, 1)
                 for (int o = 16; o >= P; o >>= 1) v[0] += __shfl_xor_sync(0xffffffffu, v[0], o);
                 if (lane < HW) part[lane] = v[0];
             }
-            const uint32_t last = un - 1;
-            ok = ok && wait_bar(bar(sh.p_free[last % kPBufs]), (last / kPBufs) & 1);
-            named_bar_sync(id, 128);
-            tc_fence_after();
-            const size_t slot = static_cast<size_t>(seg.slot) * p.H + wg * HW;
-            const uint64_t keep = l2_policy_evict_last();   // the merge reads it soon
+            named_bar_sync(id, 128);   // also: every warp is done with mul and bias
+            done = static_cast<size_t>(seg.slot) * p.H + wg * HW;
             if (t < mine) {   // (mine <= 24: the warpgroup's first warp)
-                p.ws_m[slot + t] = -bias[t];
-                p.ws_l[slot + t] = (all[0][t] + all[1][t]) + (all[2][t] + all[3][t]);
+                p.ws_m[done + t] = -bias[t];
+                p.ws_l[done + t] = (all[0][t] + all[1][t]) + (all[2][t] + all[3][t]);
             }
-#pragma unroll 1
-            for (int c = 0; c < 4 * (HW / 8); ++c) {
-                const int tile = c / (HW / 8), g = c % (HW / 8) * 8;
-                float *const dst = p.ws_o + (slot + g) * kR + tile * 128 + t;
-                float o[kJoin ? 16 : 8];
-#pragma unroll
-                for (int i = 0; i < (kJoin ? 16 : 8); i += 8)
-                    tmem_ld8(lanes + L::O_COL + tile * N + (kJoin ? 2 * g : g) + i, *reinterpret_cast<float (*)[8]>(o + i));
-                tmem_wait_ld();
-#pragma unroll
-                for (int k = 0; k < 8; ++k) {
-                    const int at = kJoin ? 2 * (k & ~1) + (k & 1) : k;
-                    if (g + k < mine)
-                        st_keep(dst + static_cast<size_t>(k) * kR, kJoin ? fmaf(o[(at + 2) % 16], kLoPart, o[at]) : o[at],
-                                keep);
-                }
-            }
-            tc_fence_before();
-            named_bar_sync(id, 128);   // part and mul are read before the next segment sets them
             more = walk.next(seg);
         }
         if (!ok && lane == 0) record_error(p.err, kDevErrTimeout);
