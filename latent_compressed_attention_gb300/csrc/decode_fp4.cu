@@ -34,7 +34,7 @@
 // permute per four codes: the group's exponent selects an 8-byte table of e4m3 magnitudes, the codes' three magnitude
 // bits are the selector.
 //
-// What bounds it (64 x 16384 rows with their merge, 1.93 GHz): at 96 heads 264 us, 9450 cycles a unit, of which the
+// What bounds it (64 x 16384 rows with their merge, 1.93 GHz): at 96 heads 262 us, 9400 cycles a unit, of which the
 // tensor pipe is busy 46 % (64 products of 56 cycles: shared memory feeds it 128 bytes a cycle).  The queries' 96 KB leave
 // room for one unit of expanded slabs and one slab more, so a unit's expansion, S, softmax and O mostly follow one
 // another, each slab of the next unit expanded as O leaves one.  At 48 heads 172 us (6200 cycles a unit), at 16 heads
@@ -45,7 +45,8 @@
 //
 // Merge kernels: the segments of a sequence are joined with the log-sum-exp rule and multiplied by W_UV^T, then the gate.
 // Few (head, sequence) pairs: a CTA per head and up to four sequences, the product in fp32 from W_UV[h] in shared memory.
-// Many: a CTA per head and 32 sequences, o_lat as bf16 hi + lo, on the tensor cores (W_UV as the M side).
+// Many: a CTA per head and 32 sequences, o_lat as bf16 hi + lo (2^-17 of a value off, far below the output's own rounding),
+// on the tensor cores (W_UV as the M side).
 #include <atomic>
 
 #include <cuda.h>
@@ -699,14 +700,15 @@ __global__ void __launch_bounds__(Fp4Layout<HP>::kThreads, 1)
                     float o[kJoin ? 16 : 8];
 #pragma unroll
                     for (int i = 0; i < (kJoin ? 16 : 8); i += 8)
-                        tmem_ld8(lanes + L::O_COL + tile * N + (kJoin ? 2 * g : g) + i, *reinterpret_cast<float (*)[8]>(o + i));
+                        tmem_ld8(lanes + L::O_COL + tile * N + (kJoin ? 2 * g : g) + i,
+                                 *reinterpret_cast<float (*)[8]>(o + i));
                     tmem_wait_ld();
 #pragma unroll
                     for (int k = 0; k < 8; ++k) {
                         const int at = kJoin ? 2 * (k & ~1) + (k & 1) : k;
                         if (g + k < mine)
-                            st_keep(dst + static_cast<size_t>(k) * kR, kJoin ? fmaf(o[(at + 2) % 16], kLoPart, o[at]) : o[at],
-                                    keep);
+                            st_keep(dst + static_cast<size_t>(k) * kR,
+                                    kJoin ? fmaf(o[(at + 2) % 16], kLoPart, o[at]) : o[at], keep);
                     }
                 }
                 tc_fence_before();
