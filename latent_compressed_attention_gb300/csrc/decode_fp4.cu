@@ -1014,7 +1014,8 @@ struct MergeParams {
 constexpr int kMaxShares = 512;   // share boundaries that the merge keeps in shared memory
 
 // Log-sum-exp join of a sequence's segments for one head by one warp, which takes every `per`-th share of the axis from
-// the `sub`-th on: o = sum of 2^(m - M) ws_o in the lane's columns 4 lane + 128 q, L = sum of 2^(m - M) l.
+// the `sub`-th on, all chunks' segments together (one chunk after the other waits once for each: 59 against 53 us for one
+// sequence of 131000 rows): o = sum of 2^(m - M) ws_o in the lane's columns 4 lane + 128 q, L = sum of 2^(m - M) l.
 template <int kFly>   // segments whose rows are in flight at a time
 __device__ __forceinline__ void join_segments(const MergeParams &p, const int *shares, int2 at, int h, int len, int sub,
                                               int per, int lane, float (&o)[16], float &M, float &L) {
@@ -1022,18 +1023,21 @@ __device__ __forceinline__ void join_segments(const MergeParams &p, const int *s
 #pragma unroll
     for (int k = 0; k < 16; ++k) o[k] = 0.f;
     if (len <= 0) return;
-    const int chunks = chunks_of(len);
-    int c_first = 0;
-    for (int j = 0; j < chunks; ++j) {
-        const int rows = min(kChunkRows, len - j * kChunkRows);
-        const int r0 = at.x + j * (p.over + kChunkUnits) + p.over, r1 = r0 + (rows + kRows - 1) / kRows;
-        if (j == 0)   // the share that holds r0: from an estimate on, as shares are equal but for a unit
-            c_first = min(p.G - 1, static_cast<int>(static_cast<float>(r0) * p.G / shares[p.G]));
-        while (c_first > 0 && shares[c_first] > r0) --c_first;
-        while (c_first + 1 < p.G && shares[c_first + 1] <= r0) ++c_first;
-        for (int c0 = c_first + sub; c0 < p.G && shares[c0] < r1; c0 += 32 * per) {
-            const int c = c0 + lane * per;
-            const bool has = c < p.G && min(shares[c + 1], r1) > max(shares[c], r0);
+    const int span = p.over + kChunkUnits, chunks = chunks_of(len), r0 = at.x + p.over;
+    const int end = r0 + (chunks - 1) * span + (len - (chunks - 1) * kChunkRows + kRows - 1) / kRows;
+    // the share that holds the first unit: from an estimate on, as shares are equal but for a unit
+    int c_first = min(p.G - 1, static_cast<int>(static_cast<float>(r0) * p.G / shares[p.G]));
+    while (c_first > 0 && shares[c_first] > r0) --c_first;
+    while (c_first + 1 < p.G && shares[c_first + 1] <= r0) ++c_first;
+    for (int c0 = c_first + sub; c0 < p.G && shares[c0] < end; c0 += 32 * per) {
+        // a lane takes a share, and one after the other the chunks j that it has rows of (mostly one or two)
+        const int c = c0 + lane * per;
+        const bool in = c < p.G && shares[min(c, p.G)] < end;
+        const int lo = in ? max(shares[c], r0) : 0, hi = in ? min(shares[c + 1], end) : 0;
+        const int j0 = (lo - at.x) / span, turns = hi > lo ? (hi - 1 - at.x) / span - j0 + 1 : 0;
+        for (int turn = 0, most = __reduce_max_sync(0xffffffffu, turns); turn < most; ++turn) {
+            const int j = j0 + turn;
+            const bool has = turn < turns && hi > max(lo, r0 + j * span);   // (between two chunks lie the `over` units)
             const size_t slot = static_cast<size_t>(c + at.y + j) * p.H + h;
             const float m = has ? p.ws_m[slot] : -INFINITY, l = has ? p.ws_l[slot] : 0.f;
             float w = 0.f;
@@ -1419,8 +1423,8 @@ cudaError_t launch_decode_fp4(const DecodeArgs &a, cudaStream_t s) {
     note_launch();
     // Up to four sequences per CTA, as long as one wave of CTAs (two, of the largest) takes them all.  Whole decodes of 300
     // rows: 16 heads x 16 sequences 17.1 / 14.7 / 15.9 / 18.5 us with one, two, four per CTA and the tensor cores, x 64
-    // 37.5 / 30.4 / 25.9 / 27.8, x 96 49.7 / 38.2 / 32.2 / 29.4; 96 heads x 1 20.9 / 21.6 / 23.2 / 24.8 (of 100000 rows
-    // 55 / 57 / 59 / 97: there a pair's segments are spread over sixteen warps), x 64 156 / 109 / 87 / 41.
+    // 37.5 / 30.4 / 25.9 / 27.8, x 96 49.7 / 38.2 / 32.2 / 29.4; 96 heads x 1 20.9 / 21.6 / 23.2 / 24.8 (of 100000 rows,
+    // chunk by chunk, 55 / 57 / 59 / 97: there a pair's segments are spread over sixteen warps), x 64 156 / 109 / 87 / 41.
     const auto ctas = [&](int seqs) { return static_cast<long long>(a.H) * ((a.B + seqs - 1) / seqs); };
     if (ctas(1) <= a.num_sms) return launch_dot<1>(mp, cfg);
     if (ctas(2) <= a.num_sms) return launch_dot<2>(mp, cfg);
