@@ -59,6 +59,8 @@ def library_path() -> str:
 def library():
     """The loaded C library (ctypes.CDLL) with argument types declared."""
     global _lib
+    if _lib is not None:
+        return _lib
     with _lock:
         if _lib is None:
             if not os.path.exists(LIB_PATH):
@@ -141,9 +143,15 @@ def mla_kernel_launches() -> int:
 
 
 # ----------------------------------------------------------------------------- torch marshalling
+_torch_module = None
+
+
 def _torch():
-    import torch
-    return torch
+    global _torch_module
+    if _torch_module is None:
+        import torch
+        _torch_module = torch
+    return _torch_module
 
 
 def _dtype_code(t) -> int:
