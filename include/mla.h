@@ -270,6 +270,7 @@ MLA_API int mla_quantize_latent_fp8(const void *c, long long ld_c, void *c8, lon
  *   r / 32 bytes   one scale byte X per 32 consecutive elements: 2^(X - 127), X taken into [87, 167]; 255 is NaN
  *                  (every element of the group is then NaN)
  *   padding        to a multiple of 16 bytes; never read or written
+ * Every pointer of the calls below is 16-byte aligned, lens and counts among them.
  * mla_latent_fp4_row_bytes(r) is that row's size: 272 at r = 512 (1024 in bf16).  Returns 0 for an r that is not a
  * positive multiple of 32 up to 65536.
  */
