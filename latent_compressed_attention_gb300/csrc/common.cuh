@@ -726,4 +726,21 @@ __device__ __forceinline__ void store_row32_bf16(uint32_t tile, uint32_t slab_by
     }
 }
 
+// Launch as a programmatic dependent of whatever precedes it on the stream: the launch and what the kernel does before
+// grid_dependency_wait overlap that work's end.  Every thread of the kernel calls it before it touches global memory.
+template <typename K, typename... A>
+cudaError_t launch_dependent(K kernel, dim3 grid, unsigned threads, size_t smem, cudaStream_t s, const A &...args) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3(threads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = s;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kernel, args...);
+}
+
 }  // namespace mla

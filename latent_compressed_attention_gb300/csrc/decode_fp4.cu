@@ -481,6 +481,7 @@ __global__ void __launch_bounds__(Fp4Layout<HP>::kThreads, 1)
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = sh.tmem_base;
+    grid_dependency_wait();     // launched as a programmatic dependent too: nothing before this reads or writes memory
     grid_launch_dependents();   // the merge takes SMs as CTAs finish; it waits for the whole grid
 
     Walk walk;
@@ -1343,8 +1344,7 @@ cudaError_t launch_attention(const CUtensorMap &codes, const CUtensorMap &scales
     });
     if (e != cudaSuccess) return e;
     note_launch();
-    fp4_attention_kernel<HP><<<p.G, L::kThreads, L::kSmem, s>>>(codes, scales, p);
-    return cudaGetLastError();
+    return launch_dependent(fp4_attention_kernel<HP>, dim3(p.G), L::kThreads, L::kSmem, s, codes, scales, p);
 }
 
 template <int kSeqs>

@@ -88,6 +88,7 @@ struct Raw<float> {
 
 template <typename T, bool kAppend, int N>
 __global__ void __launch_bounds__(kThreads) write_latent_fp4_kernel(const WriteParams p) {
+    grid_dependency_wait();
     const Block blk(p.pc);
     const T *const src = static_cast<const T *>(p.c) + (blk.seq * p.pc.run + blk.row0) * p.ld_c;
     long long row0 = blk.row0;       // of the block's first row, in its sequence's part of c4
@@ -170,6 +171,7 @@ __device__ __forceinline__ void store_piece(float *dst, uint32_t codes, float by
 template <typename T, int N>
 __global__ void __launch_bounds__(kThreads) read_latent_fp4_kernel(const ReadParams p) {
     constexpr int kOut = 16 / sizeof(T);
+    grid_dependency_wait();
     const Block blk(p.pc);
     unsigned n = blk.n;
     if (p.lens) {
@@ -221,19 +223,18 @@ cudaError_t launch_pieces(long long runs, long long run, int per_row, F f) {
     const long long pieces = std::min<long long>(run, pc.rows_per_block) * per_row;
     const unsigned threads = static_cast<unsigned>(std::min<long long>(kThreads, (pieces + 31) / 32 * 32));
     note_launch();
-    f(pc, static_cast<unsigned>(blocks * runs), threads, is_long);
-    return cudaGetLastError();
+    return f(pc, static_cast<unsigned>(blocks * runs), threads, is_long);
 }
 
 template <typename T, bool kAppend>
-void launch_write(const WriteParams &p, unsigned grid, unsigned threads, bool is_long, cudaStream_t s) {
-    is_long ? write_latent_fp4_kernel<T, kAppend, kMany><<<grid, threads, 0, s>>>(p)
-            : write_latent_fp4_kernel<T, kAppend, 1><<<grid, threads, 0, s>>>(p);
+cudaError_t launch_write(const WriteParams &p, unsigned grid, unsigned threads, bool is_long, cudaStream_t s) {
+    return is_long ? launch_dependent(write_latent_fp4_kernel<T, kAppend, kMany>, dim3(grid), threads, 0, s, p)
+                   : launch_dependent(write_latent_fp4_kernel<T, kAppend, 1>, dim3(grid), threads, 0, s, p);
 }
 template <typename T>
-void launch_read(const ReadParams &p, unsigned grid, unsigned threads, bool is_long, cudaStream_t s) {
-    is_long ? read_latent_fp4_kernel<T, kMany><<<grid, threads, 0, s>>>(p)
-            : read_latent_fp4_kernel<T, 1><<<grid, threads, 0, s>>>(p);
+cudaError_t launch_read(const ReadParams &p, unsigned grid, unsigned threads, bool is_long, cudaStream_t s) {
+    return is_long ? launch_dependent(read_latent_fp4_kernel<T, kMany>, dim3(grid), threads, 0, s, p)
+                   : launch_dependent(read_latent_fp4_kernel<T, 1>, dim3(grid), threads, 0, s, p);
 }
 
 }  // namespace
@@ -244,11 +245,10 @@ cudaError_t launch_write_latent_fp4(const LatentFp4Args &a, cudaStream_t s) {
     return launch_pieces(a.B, a.rows, a.r / kPiece, [&](const Pieces &pc, unsigned grid, unsigned threads, bool is_long) {
         p.pc = pc;
         if (a.lens)
-            a.f32 ? launch_write<float, true>(p, grid, threads, is_long, s)
-                  : launch_write<__nv_bfloat16, true>(p, grid, threads, is_long, s);
-        else
-            a.f32 ? launch_write<float, false>(p, grid, threads, is_long, s)
-                  : launch_write<__nv_bfloat16, false>(p, grid, threads, is_long, s);
+            return a.f32 ? launch_write<float, true>(p, grid, threads, is_long, s)
+                         : launch_write<__nv_bfloat16, true>(p, grid, threads, is_long, s);
+        return a.f32 ? launch_write<float, false>(p, grid, threads, is_long, s)
+                     : launch_write<__nv_bfloat16, false>(p, grid, threads, is_long, s);
     });
 }
 
@@ -258,7 +258,8 @@ cudaError_t launch_read_latent_fp4(const LatentFp4Args &a, cudaStream_t s) {
     const int per_row = a.f32 ? a.r / 4 : a.r / 8;
     return launch_pieces(a.B, a.rows, per_row, [&](const Pieces &pc, unsigned grid, unsigned threads, bool is_long) {
         p.pc = pc;
-        a.f32 ? launch_read<float>(p, grid, threads, is_long, s) : launch_read<__nv_bfloat16>(p, grid, threads, is_long, s);
+        return a.f32 ? launch_read<float>(p, grid, threads, is_long, s)
+                     : launch_read<__nv_bfloat16>(p, grid, threads, is_long, s);
     });
 }
 
