@@ -473,6 +473,49 @@ def test_two_graphs_one_workspace_and_two_streams(env):
     assert lca.mla_get_device_error() == 0
 
 
+def test_captured_between_copies_and_branches(env):
+    """A graph in which the calls follow copies, memsets and two joined branches, and other kernels follow them: each
+    launch is a programmatic dependent, whatever kind of node comes before it."""
+    torch, lca, _ = env
+    d = decode_case(33, [300, 129], 400, seed=41)
+    want = decode(env, d)
+    src = [bf(torch, d["q_abs"]), bf(torch, W.decode_fp4(d["rows"], R)), dev(torch, d["lens"])]
+    q, c, lens = (torch.empty_like(x) for x in src)
+    cache = torch.empty((2, 400, ROW), dtype=torch.uint8, device="cuda")
+    w_uv, zeros = bf(torch, d["w_uv"]), torch.zeros(2, dtype=torch.int32, device="cuda")
+    twice, back = torch.empty(want.shape, dtype=torch.bfloat16, device="cuda"), torch.empty_like(c)
+    side, other, graph = torch.cuda.Stream(), torch.cuda.Stream(), torch.cuda.CUDAGraph()
+
+    def work():
+        c.copy_(src[1])
+        cache.zero_()
+        lca.mla_append_latent_fp4(c, cache, zeros)
+        other.wait_stream(side)
+        with torch.cuda.stream(other):
+            q.copy_(src[0])
+            lens.copy_(src[2])
+        lca.mla_dequantize_latent_fp4(cache, R, out=back)
+        side.wait_stream(other)
+        out = lca.mla_latent_decode_fp4(q, cache, lens, w_uv)
+        twice.copy_(out + out)
+        lens.zero_()
+
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        work()
+        side.synchronize()
+        with torch.cuda.graph(graph, stream=side):
+            work()
+        for _ in range(20):
+            for x in (q, c, back, twice):
+                x.fill_(3.0)
+            graph.replay()
+    side.synchronize()
+    assert np.array_equal(twice.double().cpu().numpy(), 2 * want)
+    assert np.array_equal(back.double().cpu().numpy(), W.decode_fp4(d["rows"], R)) and not bool(lens.any())
+    assert lca.mla_get_device_error() == 0
+
+
 def test_same_inputs_same_bits(env):
     d = decode_case(96, [3000, 1, 777], 3000, seed=13)
     assert np.array_equal(decode(env, d), decode(env, d))
