@@ -880,19 +880,24 @@ __global__ void __launch_bounds__(Fp4Layout<HP>::kThreads, 1)
                     ok = ok && wait_bar(bar(sh.p_free[(un - 1) % kPBufs]), ((un - 1) / kPBufs) & 1);
                     __syncwarp();
                     tc_fence_after();
+                    // four columns at a time, of all the heads that they hold (a factor of one for those that did not move):
+                    // a head on its own would load columns that its neighbour's store has not reached yet, as only
+                    // wait::st orders a store before a later load
+                    constexpr int kQuad = kJoin ? 2 : 4;   // heads of four columns
 #pragma unroll 1
-                    for (; moved; moved &= moved - 1) {
-                        const int h = __ffs(moved) - 1, j = kJoin ? h & 1 : h & 3, col = kJoin ? 2 * (h & ~1) : h & ~3;
-                        const float f = fac[h];
-                        float o[4][4];   // the four columns around the head's, of the four latent tiles
+                    while (moved) {
+                        const int h = (__ffs(moved) - 1) & ~(kQuad - 1), col = kJoin ? 2 * h : h;
+                        moved &= ~(((1u << kQuad) - 1u) << h);
+                        float f[kQuad], o[4][4];   // of the four latent tiles
+#pragma unroll
+                        for (int i = 0; i < kQuad; ++i) f[i] = fac[h + i];
 #pragma unroll
                         for (int c = 0; c < 4; ++c) tmem_ld4(lanes + L::O_COL + c * N + col, o[c]);
                         tmem_wait_ld();
 #pragma unroll
                         for (int c = 0; c < 4; ++c) {
 #pragma unroll
-                            for (int i = 0; i < 4; ++i)
-                                if ((kJoin ? i & 1 : i) == j) o[c][i] *= f;
+                            for (int i = 0; i < 4; ++i) o[c][i] *= f[i % kQuad];
                             tmem_st4(lanes + L::O_COL + c * N + col, o[c]);
                         }
                     }
