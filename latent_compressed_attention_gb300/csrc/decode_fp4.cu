@@ -20,13 +20,15 @@
 //
 // Softmax of one unit: thread = row, so every head's statistics lie across lanes.  With a = score * log2 e + ref,
 //   P = 2^(a - M + 8), l += P * 2^-ref,   M[head] >= running max of a - 0.75
-// M moves only when some row exceeds it by more than 0.75 (P <= 2^8.75 = 430, inside e4m3's 448), then to kHead above
-// that row: a barrier with an OR tells whether any does, and only then are the maxima taken across lanes and the moved
-// heads' columns of O^T rescaled.  What two 8-bit parts cannot hold of P is half a step of lo: 2^-14 up to 48 heads
-// (kHead = 1: 2^-21 of the largest weight), 2^-17 above (kHead = 3: 2^-22; there every move stops four warpgroups, and
-// the higher start makes a third of them: 332 -> 321 us at 96 heads when it came).  Sequences are cut into chunks of
-// 32768 rows with maxima of their own, so less than 2^-6 of a chunk's weight can be lost to that, and that only when
-// nearly all of its rows lie 2^-21 below the largest.
+// M moves when some row exceeds it by more than 0.75 (P <= 2^8.75 = 430, inside e4m3's 448), to kHead above that row: a
+// barrier with an OR tells whether any does, and only then are the maxima taken across lanes and the moved heads' columns
+// of O^T rescaled.  Of P two 8-bit parts hold all but 2^-8 of it (above 48 heads 2^-7), and 2^-14 where hi is subnormal
+// (half a step of lo up to 48 heads; above, e5m2's 2^-4 of a rest of 2^-10), while l takes all of it.  2^-14 is 2^-21 of
+// the largest P when M was set; so that thousands of light rows behind one heavy row are not lost, M is set anew, lower
+// or higher, every kWindow units: what the rows of a window lose is at most 4096 * 2^-21 = 2^-9 of their largest P, or
+// 2^-45 each of the segment's, as M goes no lower than kDepth below its highest value (so that O^T and l stay in fp32's
+// range over a segment's 32768 rows).  64 x 16384 rows: up to 48 heads within 1 % of M never lowered; at 96 heads 265 us
+// against 250 with kHead = 3 and M never lowered, 278 with kHead = 3 and windows of 8 units, which lose as much.
 //
 // Warps: 0 loads scale bytes (TMA) and turns them into table numbers, 1 issues S, 2 issues O, 3 loads codes (TMA); two
 // (above 48 heads: four) softmax warpgroups, each with its share of the heads, that never wait for one another (also
@@ -66,6 +68,9 @@ constexpr int kChunkRows = kChunkUnits * kRows;
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kBias = 8.f;               // P = 2^(a - M + kBias)
 constexpr float kSlack = 0.75f;            // how far a row may exceed M before M moves
+constexpr float kHead = 1.f;               // M is set this far above the row that forces it
+constexpr int kWindow = 32;                // units after which M is set anew
+constexpr float kDepth = 24.f;             // how far M may be set below its highest value in a segment
 constexpr uint32_t kSlab = 16384;          // [128 rows x 128 latent] e4m3, 128-byte swizzle
 constexpr uint32_t kPicks = 2048;          // [128 rows x 16 groups] table numbers of a unit
 constexpr uint32_t kStage = 8192;          // codes of one slab: [128 rows x 64 bytes]
@@ -85,6 +90,7 @@ struct Fp4Shared {
     alignas(16) float mul[96];             // per head: score factor
     // per softmax warpgroup and head: kBias - M, and the last change of it with its power of two
     alignas(16) float bias[kMaxSoftWarps / 4][kMaxHW], step[kMaxSoftWarps / 4][kMaxHW], fac[kMaxSoftWarps / 4][kMaxHW];
+    float below[kMaxSoftWarps / 4][kMaxHW];   // M's highest value in the segment - M
     // per softmax warp: maxima, and parts of l while a segment is drained
     float part[kMaxSoftWarps][kMaxHW];
 };
@@ -109,7 +115,6 @@ struct Fp4Layout {
     static constexpr uint32_t Q = 0, C = Q + 4 * kQSlab, P = C + kSlabs * kSlab, STAGE = P + kPBufs * kPBuf,
                               PICK = STAGE + kStages * kStage, END = PICK + kPickBufs * kPicks;
     static constexpr uint32_t kSmem = END + sizeof(Fp4Shared) + 1024;   // + alignment slack
-    static constexpr float kHead = kJoin ? 1.f : 3.f;   // a new maximum is set this far above the row that forced it
     static constexpr uint32_t S_COL = 0, O_COL = 128;                   // TMEM columns
     // Register split of the warpgroups: control, softmax, expansion.
     static constexpr uint32_t kRegsLaunch = kJoin ? 96 : 72, kRegsCtl = kJoin ? 80 : 56, kRegsSoft = kJoin ? 104 : 88,
@@ -761,12 +766,13 @@ __global__ void __launch_bounds__(Fp4Layout<HP>::kThreads, 1)
                     }
                 }
                 uint32_t moved = 0;   // heads whose columns of O^T are to be rescaled
-                if (u == 0 || named_bar_or(id, 128, top > kBias + kSlack)) {
-                    // the maxima over the rows of the heads that a row of this warp pushes past (of all, the first time):
+                const bool fresh = u % kWindow == 0;   // M is set anew, higher or lower
+                if (fresh || named_bar_or(id, 128, top > kBias + kSlack)) {
+                    // the maxima over the rows of the heads that a row of this warp pushes past (of all, in a fresh unit):
                     // lane h gets head h's, first of its warp, then of all four
                     // (a short loop that reads S again: this code is seldom in the instruction cache)
                     float most = -INFINITY;
-                    if (u == 0) {
+                    if (fresh) {
 #pragma unroll 1
                         for (int h0 = 0; h0 < HW; h0 += 8) {
                             constexpr int W = kJoin ? 16 : 8;
@@ -812,9 +818,12 @@ __global__ void __launch_bounds__(Fp4Layout<HP>::kThreads, 1)
                     bool moves = false;
                     if (lane < HW) {
                         most = fmaxf(fmaxf(all[0][lane], all[1][lane]), fmaxf(all[2][lane], all[3][lane]));
-                        moves = (most > kBias + kSlack || u == 0) && most > -INFINITY;
-                        const float by = moves ? kBias - L::kHead - most : 0.f;   // M_old - M_new
+                        moves = (most > kBias + kSlack || fresh) && most > -INFINITY;
                         if (quad == 0) {
+                            float by = moves ? kBias - kHead - most : 0.f;   // M_old - M_new
+                            float &below = sh.below[wg][lane];
+                            if (u > 0) by = fminf(by, kDepth - below);
+                            below = u > 0 ? fmaxf(below + by, 0.f) : 0.f;
                             step[lane] = by;
                             fac[lane] = fast_exp2(by);
                             bias[lane] += by;

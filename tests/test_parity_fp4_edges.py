@@ -10,13 +10,22 @@ from tests.test_parity_fp4 import R, check, decode, decode_case, env, latent  # 
 pytestmark = pytest.mark.gpu
 
 
-def counted_rows(n, seed):
-    """Latent rows that hold their own number u = d0 + 7 d1 + 49 d2 + 343 d3 in columns 32, 64, 96 and 128, as values
-    that e2m1 has: d0 .. d2 less 3, d3 less 1 (n < 343 * 6); columns 32 .. 159 are zero otherwise."""
-    c, u = latent(np.random.default_rng(seed), (n, R)), np.arange(n)
-    c[:, 32:160] = 0.0
-    c[:, 32], c[:, 64], c[:, 96], c[:, 128] = u % 7 - 3.0, u // 7 % 7 - 3.0, u // 49 % 7 - 3.0, u // 343 - 1.0
+def counted_rows(u, seed):
+    """Latent rows that hold a number each, u = sum of 7^k digit_k < 6 * 7^4, its digits in columns 32 (k + 1) as values
+    that e2m1 has: digit - 3, the last one less 1; columns 32 .. 191 are zero otherwise."""
+    c, u = latent(np.random.default_rng(seed), (len(u), R)), np.asarray(u)
+    c[:, 32:192] = 0.0
+    for k in range(5):
+        c[:, 32 * (k + 1)] = u // 7**k % 7 - 3.0 if k < 4 else u // 7**4 - 1.0
     return c
+
+
+def query_of_numbers(H, step):
+    """q_abs [1, H, r] whose scores are step[h] times the rows' numbers (and a constant)."""
+    q = np.zeros((1, H, R))
+    for k in range(5):
+        q[0, :, 32 * (k + 1)] = W.round_bf16(step * 7.0**k)
+    return q
 
 
 @pytest.mark.parametrize("H", [16, 31, 48, 49, 64, 96])
@@ -25,12 +34,82 @@ def test_heads_whose_maxima_move_together(env, H):  # noqa: F811
     columns of the accumulator move in the same unit, each by an amount of its own."""
     n = 2050
     d = decode_case(H, [n], n, seed=51)
-    d["rows"][0] = W.encode_fp4(counted_rows(n, 52))
-    d["q_abs"][:] = 0.0
-    step = 0.01 * (1 + np.arange(H) % 5)
-    for k, at in enumerate((32, 64, 96, 128)):
-        d["q_abs"][0, :, at] = W.round_bf16(step * 7.0**k)
+    d["rows"][0] = W.encode_fp4(counted_rows(np.arange(n), 52))
+    d["q_abs"] = query_of_numbers(H, 0.01 * (1 + np.arange(H) % 5))
     got = decode(env, d)
     check(env, d, got)
     for _ in range(5):
         assert np.array_equal(decode(env, d), got)
+
+
+def many_light_rows(torch, lca, H, light, heavy_at, n, seed):
+    """len(heavy_at) sequences of n rows: n - 1 equal light ones and the heavy one at heavy_at[b].  The heavy row lies in
+    the lower half of the latent and the light ones in the upper; a head's light rows weigh about light[b, h] of its
+    heavy one, and the first half of each head's outputs comes from the upper half alone.  Returns the call's arguments
+    and per (b, h, v): the exact output, the sum of the rows' shares without regard to their signs, that sum over single
+    latent values (A of test_parity_fp4.py), and the share of one light row as heavy as the heavy one."""
+    rng = np.random.default_rng([seed, H])
+    B = len(heavy_at)
+    heavy, dim = np.zeros(R), np.zeros(R)
+    heavy[:256], dim[256:] = 1.0, np.where(np.arange(256) % 2 == 0, 1.0, -1.0)
+    cache = torch.tensor(W.encode_fp4(dim[None]), device="cuda").repeat(B, n, 1)
+    cache[torch.arange(B), torch.tensor(heavy_at)] = torch.tensor(W.encode_fp4(heavy[None]), device="cuda")
+    q = np.zeros((B, H, R))
+    rest = -np.log(light) / 4   # by which the heavy row's score is higher: in three bf16 parts, on four columns each
+    for k in range(3):
+        q[:, :, 4 * k : 4 * k + 4] = W.round_bf16(rest)[..., None]
+        rest = rest - q[:, :, 4 * k]
+    w_uv = W.round_bf16(rng.standard_normal((H, 128, R)) * 0.02)
+    w_uv[:, :64, :256] = 0.0
+    w = np.exp(-(q @ heavy))[..., None]
+    total = 1.0 + (n - 1) * w
+    y = (w_uv @ heavy + (n - 1) * w * (w_uv @ dim)) / total
+    rows = (np.abs(w_uv @ heavy) + (n - 1) * w * np.abs(w_uv @ dim)) / total
+    A = (np.abs(w_uv) @ heavy + (n - 1) * w * (np.abs(w_uv) @ np.abs(dim))) / total
+    args = [torch.tensor(x, dtype=torch.bfloat16, device="cuda") for x in (q, w_uv)]
+    lens = torch.full((B,), n, dtype=torch.int32, device="cuda")
+    return (args[0], cache, lens, args[1]), y, rows, A, np.abs(w_uv @ dim) / total
+
+
+@pytest.mark.parametrize("H", [16, 48, 64, 96])
+def test_light_rows_far_below_a_heavy_one(env, H):  # noqa: F811
+    """32767 equal rows at 2^-8 .. 2^-21 of a heavy one, 2^-16 * 1.125 and both sides of 2^-21 among them: together they
+    count for their weight wherever the heavy row lies.  A row's weight is held within 2^-8 of itself up to 48 heads, 2^-7
+    above, and 2^-21 of the largest weight among the 4096 rows around it, the heavy one for 4096 of them.  The error of a
+    weight is a factor of its whole row, so it counts by |c . W_UV|.  q_abs's smaller parts lie below 2^-9 of its largest
+    (3.7 at most) and are off by at most 2^-17 of it on four columns each: 2^-12 of a weight; 2^-10 covers that and the
+    exponential.  Sums in fp32 and the merge's o_lat (2^-17) are within 2^-15 of A."""
+    torch, lca, _ = env
+    n, B = 32768, 64
+    rng = np.random.default_rng(H)
+    light = np.exp2(-rng.uniform(8, 21, (B, H)))
+    light[:, 0], light[:, 1], light[:, 2] = 1.125 * 2.0**-16, 2.0**-20.99, 2.0**-21.01
+    light[:, 3:6] = 2.0**-17 * np.array([1.125, 1.375, 1.875])
+    heavy_at = rng.integers(0, n, B)
+    heavy_at[:4] = 0, n - 1, 4095, 127
+    args, y, rows, A, one = many_light_rows(torch, lca, H, light, heavy_at, n, 53)
+    got = lca.mla_latent_decode_fp4(*args).double().cpu().numpy().reshape(y.shape)
+    assert lca.mla_get_device_error() == 0
+    weights = 2.0**-8 if H <= 48 else 2.0**-7
+    bound = 2.0**-8 * np.abs(y) + (weights + 2.0**-10) * rows + 4096 * 2.0**-21 * one + 2.0**-15 * A
+    worst = np.unravel_index(np.argmax(np.abs(got - y) / bound), y.shape)
+    assert np.all(np.abs(got - y) <= bound), (worst, light[worst[:2]], got[worst], y[worst], bound[worst])
+
+
+@pytest.mark.parametrize("H", [16, 48, 49, 96])
+def test_maxima_that_fall_and_rise_in_long_runs(env, H):  # noqa: F811
+    """Scores that fall (in other heads rise) over thousands of rows and turn: the maxima are set lower and higher again
+    by anything from a fraction of a binade to far more than the accumulators could follow."""
+    torch, lca, _ = env
+    n, B = 14000, 140
+    u = np.abs(np.arange(n) - 9000) + 100
+    rows = W.encode_fp4(counted_rows(u, 54))
+    q = query_of_numbers(H, 0.02 * (-1.0) ** np.arange(H) * 2.0 ** (-(np.arange(H) // 2 % 6)))
+    w_uv = W.round_bf16(np.random.default_rng(55).standard_normal((H, 128, R)) * 0.02)
+    bf16 = dict(dtype=torch.bfloat16, device="cuda")
+    got = lca.mla_latent_decode_fp4(torch.tensor(q, **bf16).repeat(B, 1, 1), torch.tensor(rows, device="cuda").repeat(B, 1, 1),
+                                    torch.full((B,), n, dtype=torch.int32, device="cuda"), torch.tensor(w_uv, **bf16))
+    assert lca.mla_get_device_error() == 0
+    one = dict(q_abs=q, w_uv=w_uv, gate=None, lens=np.array([n], np.int32), rows=rows[None])
+    for b in (0, 61, B - 1):
+        check(env, one, got[b : b + 1].double().cpu().numpy())
