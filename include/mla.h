@@ -328,7 +328,8 @@ MLA_API int mla_dequantize_latent_fp4(const void *c4, long long ld_c4, long long
  * largest) and the rows' values exactly; the softmax weights are two 8-bit parts: a weight is at most 2^-8 of itself off
  * up to 48 heads, 2^-7 above, and in both cases 2^-21 of the largest among the 4096 rows around it (weights times their
  * rows' largest scales), so that many light rows beside a heavy one lose no more than 2^-9 of its weight together; sums,
- * maxima and the join are fp32.
+ * maxima and the join are fp32.  Rows that hold a group of values more than 2^14 below their largest scale (and the rows
+ * around them) are taken in fp32, one after the other: right, but about fifty times slower.
  * lens[b] outside [0, max_len] is taken into it and reported as MLA_ERR_DEVICE_BOUNDS; lens[b] = 0 gives zeros.
  * Supported: r = 512, d_v = 128, 1 <= H <= 96.
  * Returns MLA_OK or a negative mla_status_t; nothing is launched on error.

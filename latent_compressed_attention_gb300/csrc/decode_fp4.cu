@@ -11,8 +11,10 @@
 //   O^T [128 latent x heads] x 4 += c^T . P^T      A = the same tile, MN-major    (K = rows)
 // so a unit is expanded once, to e4m3 in shared memory, for both, heads are not padded to 128, and O^T (fp32) leaves room
 // in tensor memory for S^T.  An e2m1 value times its group's power of two is exact in e4m3 relative to its row's largest
-// scale (14 binades down; smaller groups are rounded at 2^-18 of the row's largest value), so the tile is the row divided
-// by a power of two, `ref`, that goes into the softmax's exponent.  q_abs and P are split into two 8-bit parts:
+// scale, 14 binades down, so the tile is the row divided by a power of two, `ref`, that goes into the softmax's exponent.
+// Where a group of other values than zeros lies further down, e4m3 would round it or lose it: the expanding warps mark the
+// CTA's share, and the merge does the share's segments again in fp32 from the codes (no real latent does that; 64 x 16384
+// such rows take 6.0 ms at 16 heads).  q_abs and P are split into two 8-bit parts:
 //   up to 48 heads   e4m3 hi and lo = e4m3(16 x rest), side by side as 2 x heads columns of the N side: one pass over the
 //                    tile serves both parts, which the fp32 epilogues join
 //   above            the two parts' products go into the same accumulators, as 2 x heads columns would not fit tensor
@@ -75,7 +77,8 @@ constexpr uint32_t kSlab = 16384;          // [128 rows x 128 latent] e4m3, 128-
 constexpr uint32_t kPicks = 2048;          // [128 rows x 16 groups] table numbers of a unit
 constexpr uint32_t kStage = 8192;          // codes of one slab: [128 rows x 64 bytes]
 constexpr int kMaxPickBufs = 4;
-constexpr int kTables = 22;                // exponents -14 (all zero) .. 6 below the row's largest, then NaN
+// Tables of a group's magnitudes, by its exponent below the row's largest (kTop); below kExact e4m3 rounds some of them.
+constexpr int kTop = 20, kExact = 6, kNanTable = 21, kPastTable = 22, kTables = 23;   // (rows past the end: zeros)
 constexpr int kMaxSoftWarps = 16, kMaxHW = 24;
 
 struct Fp4Shared {
@@ -93,6 +96,7 @@ struct Fp4Shared {
     float below[kMaxSoftWarps / 4][kMaxHW];   // M's highest value in the segment - M
     // per softmax warp: maxima, and parts of l while a segment is drained
     float part[kMaxSoftWarps][kMaxHW];
+    bool low[8];                           // of the last eight units: whether any group takes a table below kExact
 };
 
 // Heads are padded to HP and shared by the softmax warpgroups, HW each.  kJoin: hi and lo parts have columns of their own,
@@ -135,6 +139,7 @@ struct Fp4Params {
     float *ws_o, *ws_m, *ws_l;   // [slots][H] (x r): sum of P c, M - kBias, l
     int2 *ws_seq;                // [B] per sequence: its first virtual unit and first chunk number
     int *ws_share;               // [G + 1] the shares' first virtual units
+    int *ws_far;                 // [G] whether a share has rows that e4m3 cannot hold: the merge does it again
     const __nv_bfloat16 *w_uv;   // asked into L2 for the merge
     int *err;
     int B, H, max_len, G, over;
@@ -308,8 +313,8 @@ __device__ __forceinline__ void st_keep(float *p, float v, uint64_t policy) {
     asm volatile("st.global.L2::cache_hint.f32 [%0], %1, %2;" ::"l"(p), "f"(v), "l"(policy) : "memory");
 }
 // A row's 16 scale bytes to the numbers of their tables; returns the largest of them, NaN bytes aside, in the range that
-// the format allows: what becomes e4m3's 2^6.
-__device__ __forceinline__ int row_picks(uint32_t (&w)[4]) {
+// the format allows: what becomes e4m3's 2^6.  Sets `low` if some table may be one below kExact.
+__device__ __forceinline__ int row_picks(uint32_t (&w)[4], bool &low) {
     uint32_t hi = 0, lo = 0x00FF00FFu;   // two 16-bit maxima and minima
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
@@ -319,9 +324,10 @@ __device__ __forceinline__ int row_picks(uint32_t (&w)[4]) {
     }
     int top = max(hi & 0xFFFFu, hi >> 16);
     const int least = min(lo & 0xFFFFu, lo >> 16);
-    if (top <= kFp4ScaleMax && least >= max(kFp4ScaleMin, top - 20)) {   // every group within the tables
+    low = least < top - (kTop - kExact);
+    if (top <= kFp4ScaleMax && least >= max(kFp4ScaleMin, top - kTop)) {   // every group within the tables
 #pragma unroll
-        for (int i = 0; i < 4; ++i) w[i] -= static_cast<uint32_t>(top - 20) * 0x01010101u;   // no byte borrows
+        for (int i = 0; i < 4; ++i) w[i] -= static_cast<uint32_t>(top - kTop) * 0x01010101u;   // no byte borrows
         return top;
     }
     if (top == kFp4ScaleNan) {
@@ -339,7 +345,7 @@ __device__ __forceinline__ int row_picks(uint32_t (&w)[4]) {
 #pragma unroll 1
         for (int k = 0; k < 32; k += 8) {
             const int X = w[i] >> k & 0xFF, in = min(max(X, kFp4ScaleMin), kFp4ScaleMax);
-            at |= static_cast<uint32_t>(X == kFp4ScaleNan ? kTables - 1 : max(in - top + 20, 0)) << k;
+            at |= static_cast<uint32_t>(X == kFp4ScaleNan ? kNanTable : max(in - top + kTop, 0)) << k;
         }
         w[i] = at;
     }
@@ -471,7 +477,8 @@ __global__ void __launch_bounds__(Fp4Layout<HP>::kThreads, 1)
     }
     if (threadIdx.x >= 64 && threadIdx.x < 64 + kTables) {   // magnitudes times 2^k as e4m3 bytes
         const int i = threadIdx.x - 64;
-        const float f = i == kTables - 1 ? __uint_as_float(0x7FFFFFFFu) : (i == 0 ? 0.f : exp2_int(i - 14));
+        const float f = i == kNanTable ? __uint_as_float(0x7FFFFFFFu)
+                                       : (i == 0 || i == kPastTable ? 0.f : exp2_int(i - kTop + 6));
         uint32_t b[4];
         const float m[8] = {0.f, 0.5f, 1.f, 1.5f, 2.f, 3.f, 4.f, 6.f};
 #pragma unroll
@@ -497,6 +504,7 @@ __global__ void __launch_bounds__(Fp4Layout<HP>::kThreads, 1)
         regs_release<L::kRegsCtl>();
         if (warp == 0) {
             // ---- a unit's scale bytes to table numbers, in place, and refs; the bytes are asked for three units ahead
+            if (lane == 0) p.ws_far[blockIdx.x] = 0;
             Walk far = walk;
             Segment far_seg;
             Units unit, next;
@@ -525,15 +533,21 @@ __global__ void __launch_bounds__(Fp4Layout<HP>::kThreads, 1)
                 // (the expansion is done with the unit four back, so O is with the unit six back, and the softmax: the
                 // ref slot, last used eight back, is free)
                 uint4 *const at = reinterpret_cast<uint4 *>(smem + L::PICK + pb * kPicks) + lane;
+                bool low = false;
 #pragma unroll 1
                 for (int i = 0; i < 4; ++i) {   // a lane takes rows lane + 32 i
                     const uint4 v = at[32 * i];
                     uint32_t w[4] = {v.x, v.y, v.z, v.w};
-                    const int top = row_picks(w);
+                    bool row_low;
+                    const int top = row_picks(w, row_low);
                     const bool real = lane + 32 * i < unit.rows;   // rows past the end: zeros
-                    at[32 * i] = real ? make_uint4(w[0], w[1], w[2], w[3]) : make_uint4(0, 0, 0, 0);
+                    constexpr uint32_t past = kPastTable * 0x01010101u;
+                    at[32 * i] = real ? make_uint4(w[0], w[1], w[2], w[3]) : make_uint4(past, past, past, past);
                     sh.ref[un & 7][lane + 32 * i] = static_cast<int16_t>(top - 127 - 6);
+                    low |= real && row_low;
                 }
+                low = __any_sync(0xffffffffu, low);
+                if (lane == 0) sh.low[un & 7] = low;
                 __syncwarp();
                 if (lane == 0) mbar_arrive(bar(sh.pick_full[pb]));
                 unit.next(walk, seg);
@@ -963,6 +977,7 @@ __global__ void __launch_bounds__(Fp4Layout<HP>::kThreads, 1)
             for (int u = 0; u < seg.units; ++u, ++un) {
                 const uint32_t pb = un % kPickBufs;
                 ok = ok && wait_bar(bar(sh.pick_full[pb]), (un / kPickBufs) & 1);
+                const bool low = sh.low[un & 7];
 #pragma unroll 1
                 for (int k = first; k < 4; k += L::kExpGroups) {
                     const uint32_t it = 4 * un + k, sl = it % kSlabs, st = it % kStages;
@@ -972,6 +987,16 @@ __global__ void __launch_bounds__(Fp4Layout<HP>::kThreads, 1)
 #pragma unroll
                     for (int i = 0; i < 4; ++i)
                         c[i] = *reinterpret_cast<const uint4 *>(smem + stage_at + st * kStage + i * 512);
+                    if (__builtin_expect(low, 0)) {
+                        // groups of zeros may lie anywhere below their row's largest, others make the merge do the share again
+#pragma unroll 1
+                        for (int i = 0; i < 4; ++i) {
+                            const uint4 w = *reinterpret_cast<const uint4 *>(smem + stage_at + st * kStage + i * 512);
+                            if (smem[pick_at + pb * kPicks + i * 128 + k * 4] < kExact &&
+                                ((w.x | w.y | w.z | w.w) & 0x77777777u))
+                                p.ws_far[blockIdx.x] = 1;   // (after warp 0's zero: pick_full lies between)
+                        }
+                    }
                     fence_proxy_async_smem();   // the reads, before TMA writes there again
                     __syncwarp();
                     if (lane == 0) mbar_arrive(bar(sh.stage_empty[st]));
@@ -1018,15 +1043,98 @@ __global__ void __launch_bounds__(Fp4Layout<HP>::kThreads, 1)
 struct MergeParams {
     const int *lens;
     const int2 *ws_seq;
-    const int *ws_share;
-    const float *ws_o, *ws_m, *ws_l;
+    const int *ws_share, *ws_far;
+    float *ws_o, *ws_m, *ws_l;
     const __nv_bfloat16 *w_uv, *gate;
     __nv_bfloat16 *out;
     int *err;
     int B, H, max_len, G, over;
+    const __nv_bfloat16 *q_abs;   // of the segments that are left to the merge
+    const uint8_t *c4_cache;
+    long long ld_cache;
+    float scale_log2;
 };
 
 constexpr int kMaxShares = 512;   // share boundaries that the merge keeps in shared memory
+
+// A segment with rows that e4m3 cannot hold (groups more than 2^14 below their row's largest), for one head by one warp:
+// fp32 from the codes, one row after the other, into ws_o, ws_m and ws_l.
+__device__ __forceinline__ void exact_segment(const __nv_bfloat16 *q, const uint8_t *rows, long long ld, int n,
+                                           float scale_log2, float *to_o, float *to_m, float *to_l) {
+    const int lane = threadIdx.x & 31;   // columns 16 lane .. 16 lane + 15
+    const uint4 *src = reinterpret_cast<const uint4 *>(q) + lane * 2;
+    const uint4 q0 = __ldg(src), q1 = __ldg(src + 1);
+    const uint32_t qw[8] = {q0.x, q0.y, q0.z, q0.w, q1.x, q1.y, q1.z, q1.w};
+    float o[16], m = -INFINITY, l = 0.f;
+#pragma unroll
+    for (int k = 0; k < 16; ++k) o[k] = 0.f;
+    uint2 codes = __ldg(reinterpret_cast<const uint2 *>(rows) + lane);
+    int X = __ldg(rows + kR / 2 + (lane >> 1));
+#pragma unroll 1
+    for (int u = 0; u < n; ++u) {
+        const float by = fp4_scale(X);
+        const uint32_t w[2] = {codes.x, codes.y};
+        if (u + 1 < n) {   // the next row, meanwhile
+            rows += ld;
+            codes = __ldg(reinterpret_cast<const uint2 *>(rows) + lane);
+            X = __ldg(rows + kR / 2 + (lane >> 1));
+        }
+        float c[16], s = 0.f;
+        unpack_e2m1x8(w[0], *reinterpret_cast<float (*)[8]>(c));
+        unpack_e2m1x8(w[1], *reinterpret_cast<float (*)[8]>(c + 8));
+#pragma unroll
+        for (int k = 0; k < 16; ++k) {
+            c[k] *= by;
+            s = fmaf(c[k], __uint_as_float(k & 1 ? qw[k / 2] & 0xFFFF0000u : qw[k / 2] << 16), s);
+        }
+#pragma unroll
+        for (int k = 16; k >= 1; k >>= 1) s += __shfl_xor_sync(0xffffffffu, s, k);
+        s *= scale_log2;
+        const float top = fmaxf(m, s), f = fast_exp2(m - top), p = fast_exp2(s - top);
+        m = top;
+        l = fmaf(l, f, p);
+#pragma unroll
+        for (int k = 0; k < 16; ++k) o[k] = fmaf(o[k], f, p * c[k]);
+    }
+#pragma unroll
+    for (int k = 0; k < 16; k += 4)
+        *reinterpret_cast<float4 *>(to_o + lane * 16 + k) = make_float4(o[k], o[k + 1], o[k + 2], o[k + 3]);
+    if (lane == 0) *to_m = m, *to_l = l;
+    __syncwarp();
+}
+
+// A sequence whose first unit is r0: where its last one ends, and the share that holds the first.
+__device__ __forceinline__ int end_of(const MergeParams &p, int r0, int len) {
+    const int more = chunks_of(len) - 1;
+    return r0 + more * (p.over + kChunkUnits) + (len - more * kChunkRows + kRows - 1) / kRows;
+}
+__device__ __forceinline__ int first_share(const MergeParams &p, const int *shares, int r0) {
+    // from an estimate on, as shares are equal but for a unit
+    int c = min(p.G - 1, static_cast<int>(static_cast<float>(r0) * p.G / shares[p.G]));
+    while (c > 0 && shares[c] > r0) --c;
+    while (c + 1 < p.G && shares[c + 1] <= r0) ++c;
+    return c;
+}
+// A sequence's segments in shares with such rows, for one head by one warp: of the shares that join_segments takes there.
+__device__ __noinline__ void finish_segments(const MergeParams &p, const int *shares, int b, int h, int len, int sub,
+                                             int per) {
+    if (len <= 0) return;
+    const int2 at = p.ws_seq[b];
+    const int span = p.over + kChunkUnits, r0 = at.x + p.over, end = end_of(p, r0, len);
+    for (int c = first_share(p, shares, r0) + sub; c < p.G && shares[c] < end; c += per) {
+        if (p.ws_far[c] == 0) continue;
+        const int lo = max(shares[c], r0), hi = min(shares[c + 1], end);
+        for (int j = (lo - at.x) / span, base; (base = r0 + j * span) < hi; ++j) {   // base: the chunk's first unit
+            const int u0 = max(lo, base) - base, u1 = min(hi - base, kChunkUnits), row0 = j * kChunkRows + u0 * kRows;
+            const size_t slot = static_cast<size_t>(c + at.y + j) * p.H + h;
+            if (u1 <= u0) continue;
+            exact_segment(p.q_abs + (static_cast<size_t>(b) * p.H + h) * kR,
+                          p.c4_cache + (static_cast<long long>(b) * p.max_len + row0) * p.ld_cache, p.ld_cache,
+                          min(len - row0, (u1 - u0) * kRows), p.scale_log2, p.ws_o + slot * kR, p.ws_m + slot,
+                          p.ws_l + slot);
+        }
+    }
+}
 
 // Log-sum-exp join of a sequence's segments for one head by one warp, which takes every `per`-th share of the axis from
 // the `sub`-th on, all chunks' segments together (one chunk after the other waits once for each: 59 against 53 us for one
@@ -1038,12 +1146,7 @@ __device__ __forceinline__ void join_segments(const MergeParams &p, const int *s
 #pragma unroll
     for (int k = 0; k < 16; ++k) o[k] = 0.f;
     if (len <= 0) return;
-    const int span = p.over + kChunkUnits, chunks = chunks_of(len), r0 = at.x + p.over;
-    const int end = r0 + (chunks - 1) * span + (len - (chunks - 1) * kChunkRows + kRows - 1) / kRows;
-    // the share that holds the first unit: from an estimate on, as shares are equal but for a unit
-    int c_first = min(p.G - 1, static_cast<int>(static_cast<float>(r0) * p.G / shares[p.G]));
-    while (c_first > 0 && shares[c_first] > r0) --c_first;
-    while (c_first + 1 < p.G && shares[c_first + 1] <= r0) ++c_first;
+    const int span = p.over + kChunkUnits, r0 = at.x + p.over, end = end_of(p, r0, len), c_first = first_share(p, shares, r0);
     for (int c0 = c_first + sub; c0 < p.G && shares[c0] < end; c0 += 32 * per) {
         // a lane takes a share, and one after the other the chunks j that it has rows of (mostly one or two)
         const int c = c0 + lane * per;
@@ -1109,7 +1212,7 @@ constexpr uint32_t kDotW = kDV * kR * 2, kDotPart = 16 * kR * 4;
 template <int kSeqs>
 constexpr uint32_t kDotSmem = kDotW + kDotPart + kSeqs * kR * 4;
 template <int kSeqs>
-__global__ void __launch_bounds__(kDotThreads, 1) fp4_merge_dot_kernel(const MergeParams p) {
+__global__ void __launch_bounds__(kDotThreads, 1) fp4_merge_dot_kernel(const __grid_constant__ MergeParams p) {
     constexpr int kPer = 16 / kSeqs;
     extern __shared__ __align__(128) uint8_t dot_smem[];
     float(*const s_part)[kR] = reinterpret_cast<float(*)[kR]>(dot_smem + kDotW);
@@ -1127,9 +1230,10 @@ __global__ void __launch_bounds__(kDotThreads, 1) fp4_merge_dot_kernel(const Mer
     }
     const int i = warp / kPer, b = b0 + min(i, nb - 1), len = i < nb ? read_len(p.lens, b, p.max_len, nullptr) : 0;
     grid_dependency_wait();   // the segments are complete and visible after this
-    for (int c = threadIdx.x; c <= p.G; c += kDotThreads) s_shares[c] = p.ws_share[c];
+    bool far = false;
+    for (int c = threadIdx.x; c <= p.G; c += kDotThreads) s_shares[c] = p.ws_share[c], far |= c < p.G && p.ws_far[c];
     const int2 at = p.ws_seq[b];
-    __syncthreads();
+    if (__syncthreads_or(far)) finish_segments(p, s_shares, b, h, len, warp % kPer, kPer);
     {
         float o[16], M, L;
         join_segments<4>(p, s_shares, at, h, len, warp % kPer, kPer, lane, o, M, L);
@@ -1213,7 +1317,7 @@ constexpr uint32_t MW_OFF = 8 * kOSlab, MBAR_OFF = MW_OFF + kWStages * kWSlab;
 constexpr uint32_t kSmemMerge = MBAR_OFF + 128 + 1024;
 
 __global__ void __launch_bounds__(kMergeThreads, 2)
-    fp4_merge_kernel(const __grid_constant__ CUtensorMap tm_wuv, const MergeParams p) {
+    fp4_merge_kernel(const __grid_constant__ CUtensorMap tm_wuv, const __grid_constant__ MergeParams p) {
     extern __shared__ uint8_t smem_raw[];
     const uint32_t raw = smem_u32(smem_raw), base = (raw + 1023u) & ~1023u;
     uint64_t *w_full = reinterpret_cast<uint64_t *>(smem_raw + (base - raw) + MBAR_OFF), *w_empty = w_full + kWStages,
@@ -1248,8 +1352,11 @@ __global__ void __launch_bounds__(kMergeThreads, 2)
     // and visible after this
     grid_dependency_wait();
 
-    for (int c = threadIdx.x; c <= p.G; c += kMergeThreads) s_shares[c] = p.ws_share[c];
-    __syncthreads();
+    bool far = false;
+    for (int c = threadIdx.x; c <= p.G; c += kMergeThreads) s_shares[c] = p.ws_share[c], far |= c < p.G && p.ws_far[c];
+    if (__syncthreads_or(far))
+        for (int i = warp; i < nb; i += kMergeThreads / 32)
+            finish_segments(p, s_shares, b0 + i, h, read_len(p.lens, b0 + i, p.max_len, nullptr), 0, 1);
     for (int i = warp; i < nb; i += kMergeThreads / 32) {
         const int len = read_len(p.lens, b0 + i, p.max_len, nullptr);
         float o[16], M, L;
@@ -1378,7 +1485,7 @@ cudaError_t launch_dot(const MergeParams &mp, cudaLaunchConfig_t &cfg) {
 }  // namespace
 
 size_t decode_fp4_workspace_bytes(int B, int H, int max_len, int num_sms) {
-    return static_cast<size_t>(B) * sizeof(int2) + (num_sms + 1) * sizeof(int) + 8 +
+    return static_cast<size_t>(B) * sizeof(int2) + (2 * num_sms + 1) * sizeof(int) + 8 +
            slot_count(B, max_len, num_sms) * H * (kR + 2) * sizeof(float);
 }
 
@@ -1403,6 +1510,7 @@ cudaError_t launch_decode_fp4(const DecodeArgs &a, cudaStream_t s) {
     const uintptr_t seq = reinterpret_cast<uintptr_t>(p.ws_l + slots * a.H);
     p.ws_seq = reinterpret_cast<int2 *>((seq + 7) & ~static_cast<uintptr_t>(7));
     p.ws_share = reinterpret_cast<int *>(p.ws_seq + a.B);
+    p.ws_far = p.ws_share + p.G + 1;
     p.w_uv = static_cast<const __nv_bfloat16 *>(a.w_uv);
     p.err = a.dev_err;
     p.scale_log2 = a.scale * kLog2e;
@@ -1424,9 +1532,10 @@ cudaError_t launch_decode_fp4(const DecodeArgs &a, cudaStream_t s) {
                     : a.H <= 64 ? launch_attention<64>(tm_codes, tm_scales, p, s)
                                 : launch_attention<96>(tm_codes, tm_scales, p, s);
     if (e != cudaSuccess) return e;
-    const MergeParams mp{a.lens, p.ws_seq, p.ws_share, p.ws_o, p.ws_m, p.ws_l, p.w_uv,
+    const MergeParams mp{a.lens, p.ws_seq, p.ws_share, p.ws_far, p.ws_o, p.ws_m, p.ws_l, p.w_uv,
                          static_cast<const __nv_bfloat16 *>(a.gate), static_cast<__nv_bfloat16 *>(a.out), a.dev_err, a.B,
-                         a.H, a.max_len, p.G, p.over};
+                         a.H, a.max_len, p.G, p.over, p.q_abs, static_cast<const uint8_t *>(a.c_cache), a.ld_cache,
+                         p.scale_log2};
     cudaLaunchConfig_t cfg = {};
     cfg.stream = s;
     cudaLaunchAttribute attr[1];

@@ -113,3 +113,51 @@ def test_maxima_that_fall_and_rise_in_long_runs(env, H):  # noqa: F811
     one = dict(q_abs=q, w_uv=w_uv, gate=None, lens=np.array([n], np.int32), rows=rows[None])
     for b in (0, 61, B - 1):
         check(env, one, got[b : b + 1].double().cpu().numpy())
+
+
+def apart(rng, n, least, most):
+    """Latent rows whose sixteen groups lie 2^least to 2^most below the row's largest, the even ones (group 0 holds the
+    largest) by half of that at most."""
+    far = np.where(np.arange(R // 32) % 2 == 0, rng.integers(0, least // 2 + 1, (n, R // 32)),
+                   rng.integers(least, most + 1, (n, R // 32)))
+    far[:, 0] = 0
+    return latent(rng, (n, R)) * np.exp2(-far.astype(np.float64)).repeat(32, -1)
+
+
+@pytest.mark.parametrize("H,lens,max_len", [(8, [300, 129, 1], 300), (48, [1000], 1024), (60, [257, 0, 640], 640),
+                                            (96, [200] * 5, 256), (96, [40, 300] + [90] * 38, 300), (3, [40000], 40000)])
+def test_groups_far_below_their_row_s_largest(env, H, lens, max_len):  # noqa: F811
+    """Groups 2^15 to 2^70 below their row's largest: scores and half of the outputs that come from such groups alone."""
+    d = decode_case(H, lens, max_len, seed=61)
+    rng = np.random.default_rng(62)
+    odd = (np.arange(R) // 32 % 2 == 1)
+    rows = d["rows"].reshape(-1, d["rows"].shape[-1])
+    for b, (least, most) in zip(range(len(lens)), [(15, 19), (19, 22), (25, 35), (15, 70)] * len(lens)):
+        c = apart(rng, max_len, least, most)
+        if b % 2 == 1:   # only some of the rows, in the middle
+            c[: max_len // 3], c[max_len // 2 :] = latent(rng, (max_len // 3, R)), latent(rng, (max_len - max_len // 2, R))
+        c *= 2.0 ** (least // 2)   # all within the scale bytes' range
+        rows[b * max_len : (b + 1) * max_len] = W.encode_fp4(c)
+        scale = np.abs(c[: max(lens[b], 1), odd]).max()
+        d["q_abs"][b][:, ~odd] = 0.0
+        d["q_abs"][b] = W.round_bf16(d["q_abs"][b] * np.exp2(-np.round(np.log2(scale))))
+    d["w_uv"][:, :64, ~odd] = 0.0
+    check(env, d, decode(env, d))
+
+
+@pytest.mark.parametrize("H", [20, 96])
+def test_scale_bytes_of_groups_of_zeros(env, H):  # noqa: F811
+    """Groups of zeros under any scale byte, the largest and NaN's among them, beside ordinary ones."""
+    d = decode_case(H, [700, 300], 700, seed=63)
+    rng = np.random.default_rng(64)
+    rows = d["rows"]
+    zero = rng.random((2, 700, R // 32)) < 0.3
+    zero[:, :, 0] = False
+    codes = rows[..., : R // 2].reshape(2, 700, R // 32, 16)
+    codes[zero] = rng.choice(np.array([0x00, 0x80, 0x08, 0x88], np.uint8), (zero.sum(), 16))
+    rows[..., R // 2 : 272][zero] = rng.choice([0, 87, 90, 120, 140, 150, 167, 200], zero.sum())
+    got = decode(env, d)
+    check(env, d, got)
+    rows[1, 299, R // 2 + 7], rows[1, 299, R // 2 + 8] = 255, 167
+    again = decode(env, d)
+    assert np.array_equal(again[0], got[0]) and np.all(np.isnan(again[1]))
