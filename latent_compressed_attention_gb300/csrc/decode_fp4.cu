@@ -745,6 +745,7 @@ __global__ void __launch_bounds__(Fp4Layout<HP>::kThreads, 1)
                 if (quad == 0) {
                     ok = ok && wait_bar(bar(sh.s_full[sb]), (un / kSBufs) & 1);
                     if (un >= kPBufs) ok = ok && wait_bar(bar(sh.p_free[pb]), (un / kPBufs - 1) & 1);
+                    __syncwarp();   // its lanes leave the waits one by one; the barrier takes a whole warp
                 }
                 named_bar_sync(id, 128);
                 tc_fence_after();
