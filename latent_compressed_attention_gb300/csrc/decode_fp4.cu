@@ -1326,7 +1326,8 @@ __global__ void __launch_bounds__(kMergeThreads, 2)
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(done + 1);
     __shared__ int s_shares[kMaxShares + 1];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int h = blockIdx.x, b0 = static_cast<int>(blockIdx.y) * kMRows, nb = min(kMRows, p.B - b0);
+    // (sequences along x: the grid's other dimensions end at 65535)
+    const int h = blockIdx.y, b0 = static_cast<int>(blockIdx.x) * kMRows, nb = min(kMRows, p.B - b0);
     if (threadIdx.x == 0) {
         for (int i = 0; i < 2 * kWStages + 1; ++i) mbar_init(smem_u32(w_full + i), 1);
         fence_mbar_init();
@@ -1565,7 +1566,7 @@ cudaError_t launch_decode_fp4(const DecodeArgs &a, cudaStream_t s) {
     if (encode_map(&tm_wuv, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, CU_TENSOR_MAP_SWIZZLE_128B, a.w_uv, 2, wd, ws, wb) !=
         CUDA_SUCCESS)
         return cudaErrorInvalidValue;
-    cfg.gridDim = dim3(a.H, (a.B + kMRows - 1) / kMRows);
+    cfg.gridDim = dim3((a.B + kMRows - 1) / kMRows, a.H);
     cfg.blockDim = dim3(kMergeThreads);
     cfg.dynamicSmemBytes = kSmemMerge;
     return cudaLaunchKernelEx(&cfg, fp4_merge_kernel, tm_wuv, mp);

@@ -161,3 +161,22 @@ def test_scale_bytes_of_groups_of_zeros(env, H):  # noqa: F811
     rows[1, 299, R // 2 + 7], rows[1, 299, R // 2 + 8] = 255, 167
     again = decode(env, d)
     assert np.array_equal(again[0], got[0]) and np.all(np.isnan(again[1]))
+
+
+def test_more_sequences_than_a_grid_has_rows(env):  # noqa: F811
+    """32 * 65535 sequences and one more: each of one row (or none), whose output is its values times W_UV."""
+    torch, lca, _ = env
+    B = 32 * 65535 + 1
+    gen = torch.Generator(device="cuda").manual_seed(71)
+    cache = lca.mla_quantize_latent_fp4(torch.randn((B, R), generator=gen, device="cuda", dtype=torch.bfloat16))
+    q = torch.zeros((B, 1, R), dtype=torch.bfloat16, device="cuda")
+    w_uv = (torch.randn((1, 128, R), generator=gen, device="cuda") * 0.02).bfloat16()
+    lens = torch.ones(B, dtype=torch.int32, device="cuda")
+    lens[5] = lens[B - 2] = 0
+    got = lca.mla_latent_decode_fp4(q, cache.view(B, 1, -1), lens, w_uv)
+    assert lca.mla_get_device_error() == 0
+    for at in (0, 1 << 20, B - 64):
+        c = W.decode_fp4(cache[at : at + 64].cpu().numpy(), R) * lens[at : at + 64].double().cpu().numpy()[:, None]
+        w = w_uv[0].double().cpu().numpy()
+        err, A = np.abs(got[at : at + 64].double().cpu().numpy() - c @ w.T), np.abs(c) @ np.abs(w).T
+        assert np.all(err <= 2.0**-8 * np.abs(c @ w.T) + (2.0**-8 + 2.0**-10) * A)
