@@ -319,7 +319,7 @@ MLA_API int mla_dequantize_latent_fp4(const void *c4, long long ld_c4, long long
  * mla_latent_decode_fp4 - mla_latent_decode over an fp4 latent cache: exactly mla_latent_decode over the rows'
  * values.
  * Arguments as for mla_latent_decode, except:
- *   c4_cache   row u of sequence b at byte (b * max_len + u) * ld_cache
+ *   c4_cache   row u of sequence b at byte (b * max_len + u) * ld_cache; may be NULL when max_len is 0
  *   ld_cache   row stride in bytes (>= 272, a multiple of 16)
  *   q_abs, w_uv, gate, out  bf16 (there is no dtype argument)
  *   workspace  >= mla_latent_decode_fp4_workspace_size(...) bytes, 16-byte aligned, not used by any other call in
@@ -331,6 +331,7 @@ MLA_API int mla_dequantize_latent_fp4(const void *c4, long long ld_c4, long long
  * maxima and the join are fp32.  Rows that hold a group of values more than 2^14 below their largest scale (and the rows
  * around them) are taken in fp32, one after the other: right, but about fifty times slower.
  * lens[b] outside [0, max_len] is taken into it and reported as MLA_ERR_DEVICE_BOUNDS; lens[b] = 0 gives zeros.
+ * B == 0 is a no-op.
  * Supported: r = 512, d_v = 128, 1 <= H <= 96.
  * Returns MLA_OK or a negative mla_status_t; nothing is launched on error.
  */

@@ -541,7 +541,7 @@ def _fp4_cache(c4, B, r):
     # a dimension of one row or one sequence has no stride of its own to go by
     if rows <= 1:
         ld = max(ld, n)
-    return rows, ld, batch if seqs > 1 else rows * ld
+    return rows, ld, batch if seqs > 1 and rows > 0 else rows * ld
 
 
 def mla_quantize_latent_fp4(c, out=None, stream=None):

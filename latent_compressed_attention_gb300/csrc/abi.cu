@@ -411,11 +411,11 @@ MLA_API int mla_latent_decode_fp4(const void *q_abs, const void *c4_cache, long 
     if (!decode_bf16_supports(H, d_v, r)) return MLA_ERR_UNSUPPORTED;
     if (ld_cache < latent_fp4_row_bytes(r) || !mul_fits(static_cast<long long>(B) * max_len, ld_cache, LLONG_MAX / 8))
         return MLA_ERR_SHAPE;
-    if (!q_abs || !c4_cache || !lens || !w_uv || !out) return MLA_ERR_NULL;
+    if (B == 0) return MLA_OK;
+    if (!q_abs || (!c4_cache && max_len > 0) || !lens || !w_uv || !out) return MLA_ERR_NULL;
     if (!aligned16(q_abs) || !aligned16(c4_cache) || !aligned16(w_uv) || !aligned16(out) || !aligned16(lens) ||
         (gate && !aligned16(gate)) || (ld_cache % 16) != 0)
         return MLA_ERR_ALIGN;
-    if (B == 0) return MLA_OK;
     DeviceInfo *dev = nullptr;
     if (device_info(dev) != cudaSuccess) return MLA_ERR_CUDA;
     const size_t need = decode_fp4_workspace_bytes(B, H, max_len, dev->num_sms);

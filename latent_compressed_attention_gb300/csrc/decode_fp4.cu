@@ -1522,9 +1522,10 @@ cudaError_t launch_decode_fp4(const DecodeArgs &a, cudaStream_t s) {
         const cuuint64_t dims[3] = {kR / 2 + kR / 32, rows, static_cast<cuuint64_t>(a.B)};
         const cuuint64_t strides[2] = {static_cast<cuuint64_t>(a.ld_cache), rows * static_cast<cuuint64_t>(a.ld_cache)};
         const cuuint32_t box[3] = {64, kRows, 1}, sbox[3] = {16, kRows, 1};
-        if (encode_map(&tm_codes, CU_TENSOR_MAP_DATA_TYPE_UINT8, CU_TENSOR_MAP_SWIZZLE_NONE, a.c_cache, 3, dims, strides,
+        const void *rows_at = a.c_cache ? a.c_cache : a.q_abs;   // an empty cache: the maps are not used
+        if (encode_map(&tm_codes, CU_TENSOR_MAP_DATA_TYPE_UINT8, CU_TENSOR_MAP_SWIZZLE_NONE, rows_at, 3, dims, strides,
                        box) != CUDA_SUCCESS ||
-            encode_map(&tm_scales, CU_TENSOR_MAP_DATA_TYPE_UINT8, CU_TENSOR_MAP_SWIZZLE_NONE, a.c_cache, 3, dims, strides,
+            encode_map(&tm_scales, CU_TENSOR_MAP_DATA_TYPE_UINT8, CU_TENSOR_MAP_SWIZZLE_NONE, rows_at, 3, dims, strides,
                        sbox) != CUDA_SUCCESS)
             return cudaErrorInvalidValue;
     }

@@ -180,3 +180,21 @@ def test_more_sequences_than_a_grid_has_rows(env):  # noqa: F811
         w = w_uv[0].double().cpu().numpy()
         err, A = np.abs(got[at : at + 64].double().cpu().numpy() - c @ w.T), np.abs(c) @ np.abs(w).T
         assert np.all(err <= 2.0**-8 * np.abs(c @ w.T) + (2.0**-8 + 2.0**-10) * A)
+
+
+@pytest.mark.parametrize("gate", [False, True])
+def test_empty_caches_and_batches(env, gate):  # noqa: F811
+    """Caches without rows give zeros, batches without sequences nothing: as the writers and the reader take them."""
+    torch, lca, _ = env
+    for B in (3, 0):
+        empty = torch.empty((B, 0, 272), dtype=torch.uint8, device="cuda")
+        q = torch.ones((B, 20, R), dtype=torch.bfloat16, device="cuda")
+        w_uv = torch.ones((20, 128, R), dtype=torch.bfloat16, device="cuda")
+        g = torch.ones((B, 20 * 128), dtype=torch.bfloat16, device="cuda") if gate else None
+        lens = torch.zeros(B, dtype=torch.int32, device="cuda")
+        out = torch.full((B, 20 * 128), 7.0, dtype=torch.bfloat16, device="cuda")
+        assert lca.mla_latent_decode_fp4(q, empty, lens, w_uv, g, out=out) is out and not bool(out.any())
+        assert lca.mla_latent_decode_fp4(q, empty, lens, w_uv, g).shape == (B, 20 * 128)
+        assert lca.mla_dequantize_latent_fp4(empty, R).shape == (B, 0, R)
+    assert lca.mla_append_latent_fp4(torch.empty((0, 1, R), device="cuda"), empty, lens) is empty
+    assert lca.mla_get_device_error() == 0
