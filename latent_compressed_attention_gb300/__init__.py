@@ -538,9 +538,9 @@ def _fp4_cache(c4, B, r):
         raise ValueError(f"the fp4 cache must be [B,max_len,{n}] with unit inner stride")
     seqs, rows, _ = c4.shape
     batch, ld, _ = c4.stride()
-    # a dimension of one row or one sequence has no stride of its own to go by
+    # a dimension of one row or one sequence has no stride of its own to go by: a sequence's one row is as long as its batch
     if rows <= 1:
-        ld = max(ld, n)
+        ld = batch if seqs > 1 and batch >= n else max(ld, n)
     return rows, ld, batch if seqs > 1 and rows > 0 else rows * ld
 
 

@@ -198,3 +198,25 @@ def test_empty_caches_and_batches(env, gate):  # noqa: F811
         assert lca.mla_dequantize_latent_fp4(empty, R).shape == (B, 0, R)
     assert lca.mla_append_latent_fp4(torch.empty((0, 1, R), device="cuda"), empty, lens) is empty
     assert lca.mla_get_device_error() == 0
+
+
+@pytest.mark.parametrize("view", ["middle", "unsqueezed"])
+def test_one_row_caches_at_any_stride(env, view):  # noqa: F811
+    """A cache of one row per sequence that lies in a larger one: appended to, read back and attended to in place."""
+    torch, lca, _ = env
+    d = decode_case(9, [1, 1, 0, 1], 1, seed=81, gate=True)
+    c = latent(np.random.default_rng(82), (4, 1, R))
+    d["rows"][..., :272] = W.encode_fp4(c)
+    base = torch.full((4, 9, 320), 7, dtype=torch.uint8, device="cuda")
+    cache = base[:, 5:6, :272] if view == "middle" else base[:, 5, :272].unsqueeze(1)
+    bf16 = lambda x: torch.tensor(x, dtype=torch.bfloat16, device="cuda")  # noqa: E731
+    assert lca.mla_append_latent_fp4(bf16(c), cache, torch.zeros(4, dtype=torch.int32, device="cuda")) is cache
+    want = np.full((4, 9, 320), 7, np.uint8)
+    want[:, 5, :272] = d["rows"][:, 0, :272]
+    assert np.array_equal(base.cpu().numpy(), want)
+    back = lca.mla_dequantize_latent_fp4(cache, R)
+    assert np.array_equal(back.double().cpu().numpy(), W.decode_fp4(want[:, 5:6, :272], R))
+    lens = torch.tensor(d["lens"], device="cuda")
+    got = lca.mla_latent_decode_fp4(bf16(d["q_abs"]), cache, lens, bf16(d["w_uv"]), bf16(d["gate"]))
+    check(env, d, got.double().cpu().numpy())
+    assert lca.mla_get_device_error() == 0
