@@ -633,7 +633,7 @@ def mla_latent_decode_fp4(q_abs, c4_cache, lens, w_uv, gate=None, scale: float =
 
     c4_cache: uint8 [B,max_len,272] (or a row-strided view, row stride a multiple of 16 bytes), e.g. from
     mla_quantize_latent_fp4 and mla_append_latent_fp4; q_abs [B,H,512], w_uv [H,128,512] and gate [B,H*128] (or None)
-    bf16; lens int32 [B].  A workspace is allocated when not given.
+    bf16; lens int32 [B].  A workspace (a contiguous tensor on the query's device) is allocated when not given.
     """
     torch = _torch()
     B, H, r = q_abs.shape
@@ -657,6 +657,7 @@ def mla_latent_decode_fp4(q_abs, c4_cache, lens, w_uv, gate=None, scale: float =
             _check(out, "out", torch.bfloat16, dev, (B, H * d_v))
         on, scratch = _raw_stream(stream, dev), None
         if workspace is not None:
+            _check(workspace, "workspace", workspace.dtype, dev)
             ws_ptr, ws_bytes = workspace.data_ptr(), workspace.numel() * workspace.element_size()
         else:
             # from the caching allocator without a tensor around it, which small decodes' host time would show

@@ -220,3 +220,17 @@ def test_one_row_caches_at_any_stride(env, view):  # noqa: F811
     got = lca.mla_latent_decode_fp4(bf16(d["q_abs"]), cache, lens, bf16(d["w_uv"]), bf16(d["gate"]))
     check(env, d, got.double().cpu().numpy())
     assert lca.mla_get_device_error() == 0
+
+
+def test_workspaces_that_are_none(env):  # noqa: F811
+    """Tensors that do not stand for as much memory of the device as they have elements are refused on the host."""
+    torch, lca, _ = env
+    d = decode_case(8, [30, 5], 30, seed=91)
+    n = lca.mla_latent_decode_fp4_workspace_size(2, 8, R, 30)
+    for workspace in (torch.empty(n, dtype=torch.uint8), torch.empty(1, dtype=torch.uint8, device="cuda").expand(n),
+                      torch.empty((n, 2), dtype=torch.uint8, device="cuda")[:, 0]):
+        with pytest.raises(ValueError, match="workspace"):
+            decode(env, d, workspace=workspace)
+    with pytest.raises(lca.MLAError):
+        decode(env, d, workspace=torch.empty(n - 1, dtype=torch.uint8, device="cuda"))
+    check(env, d, decode(env, d, workspace=torch.empty(n, dtype=torch.uint8, device="cuda")))
