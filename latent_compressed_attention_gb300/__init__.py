@@ -514,6 +514,8 @@ def _on(stream, device):
     """The device, and the stream where one is given, that a call's allocations and launches go to."""
     torch = _torch()
     if stream is not None:
+        if stream.device != device:
+            raise ValueError(f"the stream is on {stream.device}, the tensors on {device}")
         return torch.cuda.stream(stream)
     return _HERE if torch.cuda.current_device() == device.index else torch.cuda.device(device)
 

@@ -1,4 +1,7 @@
-"""What the entry points of the fp4 latent cache refuse or take without a GPU, beside test_fp4_codec.py: empty calls."""
+"""What the entry points of the fp4 latent cache refuse or take without a GPU, beside test_fp4_codec.py: empty calls,
+streams of another device."""
+import pytest
+
 from tests.test_fp4_codec import FAKE, NULL, OK, lib  # noqa: F401 (lib: the fixture)
 
 
@@ -12,3 +15,15 @@ def test_decode_of_nothing(lib):  # noqa: F811
     assert call(0, **args) == OK and call(0, **args, max_len=9) == OK
     assert call(2, **dict.fromkeys(args, FAKE) | {"c4": None}, max_len=9) == NULL
     assert call(2, **dict.fromkeys(args, FAKE) | {"c4": None}) not in (OK, NULL)   # goes on to the workspace
+
+
+def test_stream_of_another_device():
+    import torch
+
+    import latent_compressed_attention_gb300 as lca
+
+    class Stream:
+        device = torch.device("cuda", 1)
+
+    with pytest.raises(ValueError, match="cuda:1"):
+        lca._on(Stream(), torch.device("cuda", 0))

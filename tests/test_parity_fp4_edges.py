@@ -234,3 +234,26 @@ def test_workspaces_that_are_none(env):  # noqa: F811
     with pytest.raises(lca.MLAError):
         decode(env, d, workspace=torch.empty(n - 1, dtype=torch.uint8, device="cuda"))
     check(env, d, decode(env, d, workspace=torch.empty(n, dtype=torch.uint8, device="cuda")))
+
+
+def test_calls_on_a_given_stream(env):  # noqa: F811
+    """The stream argument of every call: the same results as on the current stream, in order on that one."""
+    torch, lca, _ = env
+    d = decode_case(40, [0, 300], 400, seed=92)
+    c = latent(np.random.default_rng(93), (2, 1, R))
+    bf16 = lambda x: torch.tensor(x, dtype=torch.bfloat16, device="cuda")  # noqa: E731
+    q, w_uv, new = bf16(d["q_abs"]), bf16(d["w_uv"]), bf16(c)
+    cache, lens = torch.tensor(d["rows"], device="cuda"), torch.tensor(d["lens"], device="cuda")
+    after, side = lens + 1, torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    lca.mla_append_latent_fp4(new, cache, lens, stream=side)
+    got = lca.mla_latent_decode_fp4(q, cache, after, w_uv, stream=side)
+    back = lca.mla_dequantize_latent_fp4(cache, R, stream=side)
+    rows = lca.mla_quantize_latent_fp4(new, stream=side)
+    side.synchronize()
+    for b, n in enumerate((0, 300)):
+        d["rows"][b, n] = W.encode_fp4(c[b, 0])
+    d["lens"] = d["lens"] + 1
+    check(env, d, got.double().cpu().numpy())
+    assert np.array_equal(back.double().cpu().numpy(), W.decode_fp4(d["rows"], R))
+    assert np.array_equal(rows.cpu().numpy(), W.encode_fp4(c)) and lca.mla_get_device_error() == 0
