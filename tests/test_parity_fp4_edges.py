@@ -270,3 +270,53 @@ def test_without_torch_s_inner_names(env, gone, monkeypatch):  # noqa: F811
     with torch.cuda.stream(torch.cuda.Stream()):
         got = decode(env, d)
     assert np.array_equal(got, want)
+
+
+@pytest.mark.parametrize("B,T,max_len,r,ld", [(1, 1, 1, 512, 272), (5, 1, 300, 512, 320), (3, 700, 900, 512, 272),
+                                              (4, 3, 9, 96, 64), (2, 5000, 5003, 32, 32)])
+@pytest.mark.parametrize("with_counts", [False, True])
+def test_append_of_fp32_rows(env, B, T, max_len, r, ld, with_counts):  # noqa: F811
+    """fp32 rows with more bits than bf16 has: the bytes of the rows from lens[b] on, and no other byte of the cache."""
+    torch, lca, _ = env
+    rng = np.random.default_rng(B * T + r)
+    row, used = W.fp4_row_bytes(r), r // 2 + r // 32
+    c = (latent(rng, (B, T, r), spread=5) * (1 + 2.0**-12 * rng.integers(-8, 9, (B, T, r)))).astype(np.float32)
+    c[0, 0, 3] = np.nan
+    lens = rng.integers(0, max_len - T + 1, B).astype(np.int32)
+    counts = rng.integers(0, T + 1, B).astype(np.int32) if with_counts else np.full(B, T, np.int32)
+    counts[0] = T
+    want = rng.integers(0, 256, (B, max_len, ld)).astype(np.uint8)
+    cache = torch.tensor(want, device="cuda")
+    lca.mla_append_latent_fp4(torch.tensor(c, device="cuda"), cache[:, :, :row], torch.tensor(lens, device="cuda"),
+                              torch.tensor(counts, device="cuda") if with_counts else None)
+    for b in range(B):
+        want[b, lens[b] : lens[b] + counts[b], :used] = W.encode_fp4(c[b, : counts[b]])[:, :used]
+    assert np.array_equal(cache.cpu().numpy(), want) and lca.mla_get_device_error() == 0
+
+
+@pytest.mark.parametrize("H", [16, 48, 64, 96])
+def test_query_elements_far_below_the_largest(env, H):  # noqa: F811
+    """Queries whose larger elements lie on a group of small values and the smaller ones, 2^10 to 2^13 below, on the rest:
+    a smaller element is off by at most 2^-21 of its head's largest (2^-17 above 48 heads), so a score by at most that
+    times the sum of the row's other values, and the weights by twice its exponential's change."""
+    d = decode_case(H, [900, 40], 900, seed=95)
+    rng = np.random.default_rng(96)
+    c = latent(rng, (2, 900, R))
+    c[..., :32] *= 2.0**-9
+    d["rows"][..., :272] = W.encode_fp4(c)
+    q = rng.standard_normal((2, H, R)) * np.exp2(-rng.integers(10, 14, (2, H, R)).astype(float)) * 64
+    q[..., :32] = rng.standard_normal((2, H, 32)) * 64
+    d["q_abs"] = W.round_bf16(q)
+    got = decode(env, d)
+    part = 2.0**-21 if H <= 48 else 2.0**-17
+    for b, n in enumerate(d["lens"]):
+        c = W.decode_fp4(d["rows"][b, :n, :272], R)
+        s = d["q_abs"][b] @ c.T
+        p = np.exp(s - s.max(-1, keepdims=True))
+        p /= p.sum(-1, keepdims=True)
+        y = np.einsum("hr,hvr->hv", p @ c, d["w_uv"]).reshape(-1)
+        A = np.einsum("hr,hvr->hv", p @ np.abs(c), np.abs(d["w_uv"]))
+        off = 2 * np.expm1(part * np.abs(d["q_abs"][b]).max(-1) * np.abs(c[:, 32:]).sum(-1).max())
+        weights = 2.0**-8 if H <= 48 else 2.0**-7
+        bound = 2.0**-8 * np.abs(y) + ((weights + 2.0**-9 + 2.0**-10 + off[:, None]) * A).reshape(-1)
+        assert np.all(np.abs(got[b] - y) <= bound)
