@@ -325,7 +325,7 @@ MLA_API int mla_dequantize_latent_fp4(const void *c4, long long ld_c4, long long
  *   workspace  >= mla_latent_decode_fp4_workspace_size(...) bytes, 16-byte aligned, not used by any other call in
  *              flight
  * Precision: the scores take q_abs as two e4m3 parts (exact for a bf16 query but for elements below 2^-9 of their head's
- * largest) and the rows' values exactly; the softmax weights are two 8-bit parts: a weight is at most 2^-8 of itself off
+ * largest, which are off by at most 2^-21 of it up to 48 heads, 2^-17 above) and the rows' values exactly; the softmax weights are two 8-bit parts: a weight is at most 2^-8 of itself off
  * up to 48 heads, 2^-7 above, and in both cases 2^-21 of the largest among the 4096 rows around it (weights times their
  * rows' largest scales), so that many light rows beside a heavy one lose no more than 2^-9 of its weight together; sums,
  * maxima and the join are fp32.  Rows that hold a group of values more than 2^14 below their largest scale (and the rows
