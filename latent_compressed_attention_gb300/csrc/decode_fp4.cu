@@ -69,6 +69,9 @@ constexpr int kDV = 128;
 constexpr int kRows = 128;                 // cache rows per unit
 constexpr int kChunkUnits = 256;           // units of a sequence that share one running maximum per segment
 constexpr int kChunkRows = kChunkUnits * kRows;
+// A segment's start and end in units: 64 ragged sequences up to 32768 rows at 96 heads 273 / 267 / 269 / 270 / 271 us with
+// 1 / 2 / 3 / 4 / 5, up to 8192 rows at 64 heads 86 / 88 / 88 / 90 / 90, at 48 heads 63 / 63 / 63 / 64 / 65.
+constexpr int kOver = 2;
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kBias = 8.f;               // P = 2^(a - M + kBias)
 constexpr float kSlack = 0.75f;            // how far a row may exceed M before M moves
@@ -144,21 +147,21 @@ struct Fp4Params {
     int *ws_far;                 // [G] whether a share has rows that e4m3 cannot hold: the merge does it again
     const __nv_bfloat16 *w_uv;   // asked into L2 for the merge
     int *err;
-    int B, H, max_len, G, over;
+    int B, H, max_len, G;
     float scale_log2;
 };
 
 // ------------------------------------------------------------------ the work axis
-// Virtual units: a sequence is a run of chunks of up to kChunkUnits units, each preceded by `over` (what starting a segment
+// Virtual units: a sequence is a run of chunks of up to kChunkUnits units, each preceded by kOver (what starting a segment
 // costs: its queries, the first fill, the drain).  Share c of G
 // owns [share_lo(c), share_lo(c + 1)); its part of chunk number v (over all sequences) is segment slot c + v: both
 // only grow along the axis and one of them does between two segments.
 __host__ __device__ __forceinline__ int chunks_of(int len) {
     return static_cast<int>((static_cast<unsigned>(len) + kChunkRows - 1u) / kChunkRows);
 }
-__device__ __forceinline__ long long units_of(int len, int over) {   // virtual units of a sequence
+__device__ __forceinline__ long long units_of(int len) {   // virtual units of a sequence
     const int full = len / kChunkRows, rest = len - full * kChunkRows;
-    return static_cast<long long>(full) * (over + kChunkUnits) + (rest > 0 ? over + (rest + kRows - 1) / kRows : 0);
+    return static_cast<long long>(full) * (kOver + kChunkUnits) + (rest > 0 ? kOver + (rest + kRows - 1) / kRows : 0);
 }
 // floor(total * c / G) without a 64-bit division: total = G a + b, b c < 2^18.
 __device__ __forceinline__ int share_lo(int total, int c, int G) {
@@ -188,16 +191,16 @@ struct Segment {
 // (Positions on the axis fit 32 bits: 2^31 units are 75 TB of cache.)
 struct Walk {
     const int *lens;
-    int B, max_len, over, c, b, j;   // chunk j of sequence b is next
+    int B, max_len, c, b, j;   // chunk j of sequence b is next
     int lo, hi, pre, v;          // its first virtual unit and its number
     // Every lane of a warp calls this; all get the same walk.
     __device__ void start(const Fp4Params &p, int share, int lane, int *err) {
-        lens = p.lens, B = p.B, max_len = p.max_len, over = p.over, c = share;
+        lens = p.lens, B = p.B, max_len = p.max_len, c = share;
         // (the first 32 sequences are often all there are: loaded once)
         const int len0 = lane < B ? read_len(lens, lane, max_len, err) : 0;
-        int total = static_cast<int>(units_of(len0, over));
+        int total = static_cast<int>(units_of(len0));
 #pragma unroll 1
-        for (int i = lane + 32; i < B; i += 32) total += static_cast<int>(units_of(read_len(lens, i, max_len, err), over));
+        for (int i = lane + 32; i < B; i += 32) total += static_cast<int>(units_of(read_len(lens, i, max_len, err)));
         total = __reduce_add_sync(0xffffffffu, total);
         lo = share_lo(total, share, p.G), hi = share_lo(total, share + 1, p.G);
         b = B, j = 0, pre = hi, v = 0;
@@ -205,7 +208,7 @@ struct Walk {
 #pragma unroll 1
         for (int i0 = 0; i0 < B && lo < hi; i0 += 32) {
             const int len = i0 == 0 ? len0 : (i0 + lane < B ? read_len(lens, i0 + lane, max_len, nullptr) : 0);
-            const int u = static_cast<int>(units_of(len, over)), incl = warp_scan(u, lane);
+            const int u = static_cast<int>(units_of(len)), incl = warp_scan(u, lane);
             const int n = len > 0 ? chunks_of(len) : 0, nincl = warp_scan(n, lane);
             const unsigned past = __ballot_sync(0xffffffffu, run + incl > lo);
             if (past) {
@@ -213,8 +216,8 @@ struct Walk {
                 b = i0 + first;
                 pre = run + __shfl_sync(0xffffffffu, incl - u, first);
                 v = chunks + __shfl_sync(0xffffffffu, nincl - n, first);
-                j = (lo - pre) / (over + kChunkUnits);
-                pre += j * (over + kChunkUnits);
+                j = (lo - pre) / (kOver + kChunkUnits);
+                pre += j * (kOver + kChunkUnits);
                 v += j;
                 break;
             }
@@ -232,7 +235,7 @@ struct Walk {
             }
             const int left = len - j * kChunkRows;   // > 0: the walk leaves a sequence with its last chunk
             const int units = left >= kChunkRows ? kChunkUnits : (left + kRows - 1) / kRows;
-            const int base = pre + over, s0 = max(base, lo), s1 = min(base + units, hi);
+            const int base = pre + kOver, s0 = max(base, lo), s1 = min(base + units, hi);
             s.seq = b, s.len = len, s.slot = c + v;
             s.row0 = j * kChunkRows + (s0 - base) * kRows;
             s.units = s1 - s0;
@@ -250,7 +253,7 @@ __device__ __forceinline__ void write_seq(const Fp4Params &p, int lane) {
 #pragma unroll 1
     for (int i0 = 0; i0 < p.B; i0 += 32) {
         const int len = i0 + lane < p.B ? read_len(p.lens, i0 + lane, p.max_len, nullptr) : 0;
-        const int u = static_cast<int>(units_of(len, p.over)), n = len > 0 ? chunks_of(len) : 0;
+        const int u = static_cast<int>(units_of(len)), n = len > 0 ? chunks_of(len) : 0;
         const int incl = warp_scan(u, lane), nincl = warp_scan(n, lane);
         if (i0 + lane < p.B) p.ws_seq[i0 + lane] = make_int2(run + incl - u, chunks + nincl - n);
         run += __shfl_sync(0xffffffffu, incl, 31);
@@ -1051,7 +1054,7 @@ struct MergeParams {
     const __nv_bfloat16 *w_uv, *gate;
     __nv_bfloat16 *out;
     int *err;
-    int B, H, max_len, G, over;
+    int B, H, max_len, G;
     const __nv_bfloat16 *q_abs;   // of the segments that are left to the merge
     const uint8_t *c4_cache;
     long long ld_cache;
@@ -1107,9 +1110,9 @@ __device__ __forceinline__ void exact_segment(const __nv_bfloat16 *q, const uint
 }
 
 // A sequence whose first unit is r0: where its last one ends, and the share that holds the first.
-__device__ __forceinline__ int end_of(const MergeParams &p, int r0, int len) {
+__device__ __forceinline__ int end_of(int r0, int len) {
     const int more = chunks_of(len) - 1;
-    return r0 + more * (p.over + kChunkUnits) + (len - more * kChunkRows + kRows - 1) / kRows;
+    return r0 + more * (kOver + kChunkUnits) + (len - more * kChunkRows + kRows - 1) / kRows;
 }
 __device__ __forceinline__ int first_share(const MergeParams &p, const int *shares, int r0) {
     // from an estimate on, as shares are equal but for a unit
@@ -1123,7 +1126,7 @@ __device__ __noinline__ void finish_segments(const MergeParams &p, const int *sh
                                              int per) {
     if (len <= 0) return;
     const int2 at = p.ws_seq[b];
-    const int span = p.over + kChunkUnits, r0 = at.x + p.over, end = end_of(p, r0, len);
+    const int span = kOver + kChunkUnits, r0 = at.x + kOver, end = end_of(r0, len);
     for (int c = first_share(p, shares, r0) + sub; c < p.G && shares[c] < end; c += per) {
         if (p.ws_far[c] == 0) continue;
         const int lo = max(shares[c], r0), hi = min(shares[c + 1], end);
@@ -1149,7 +1152,7 @@ __device__ __forceinline__ void join_segments(const MergeParams &p, const int *s
 #pragma unroll
     for (int k = 0; k < 16; ++k) o[k] = 0.f;
     if (len <= 0) return;
-    const int span = p.over + kChunkUnits, r0 = at.x + p.over, end = end_of(p, r0, len), c_first = first_share(p, shares, r0);
+    const int span = kOver + kChunkUnits, r0 = at.x + kOver, end = end_of(r0, len), c_first = first_share(p, shares, r0);
     for (int c0 = c_first + sub; c0 < p.G && shares[c0] < end; c0 += 32 * per) {
         // a lane takes a share, and one after the other the chunks j that it has rows of (mostly one or two)
         const int c = c0 + lane * per;
@@ -1158,7 +1161,7 @@ __device__ __forceinline__ void join_segments(const MergeParams &p, const int *s
         const int j0 = (lo - at.x) / span, turns = hi > lo ? (hi - 1 - at.x) / span - j0 + 1 : 0;
         for (int turn = 0, most = __reduce_max_sync(0xffffffffu, turns); turn < most; ++turn) {
             const int j = j0 + turn;
-            const bool has = turn < turns && hi > max(lo, r0 + j * span);   // (between two chunks lie the `over` units)
+            const bool has = turn < turns && hi > max(lo, r0 + j * span);   // (between two chunks lie the kOver units)
             const size_t slot = static_cast<size_t>(c + at.y + j) * p.H + h;
             const float m = has ? p.ws_m[slot] : -INFINITY, l = has ? p.ws_l[slot] : 0.f;
             float w = 0.f;
@@ -1503,9 +1506,6 @@ cudaError_t launch_decode_fp4(const DecodeArgs &a, cudaStream_t s) {
     p.H = a.H;
     p.max_len = a.max_len;
     p.G = a.num_sms;
-    // a segment's start and end in units (64 ragged sequences up to 32768 rows at 96 heads: 289 us with 1, 278 with 3,
-    // 275 with 4, 277 with 6; 7 x 5000 rows at 37 heads: 17.2 with 3, 18.6 with 4)
-    p.over = a.H > 48 ? 4 : 3;
     const size_t slots = slot_count(a.B, a.max_len, p.G);
     if (decode_fp4_workspace_bytes(a.B, a.H, a.max_len, a.num_sms) > a.workspace_bytes) return cudaErrorInvalidValue;
     p.ws_o = static_cast<float *>(a.workspace);
@@ -1539,7 +1539,7 @@ cudaError_t launch_decode_fp4(const DecodeArgs &a, cudaStream_t s) {
     if (e != cudaSuccess) return e;
     const MergeParams mp{a.lens, p.ws_seq, p.ws_share, p.ws_far, p.ws_o, p.ws_m, p.ws_l, p.w_uv,
                          static_cast<const __nv_bfloat16 *>(a.gate), static_cast<__nv_bfloat16 *>(a.out), a.dev_err, a.B,
-                         a.H, a.max_len, p.G, p.over, p.q_abs, static_cast<const uint8_t *>(a.c_cache), a.ld_cache,
+                         a.H, a.max_len, p.G, p.q_abs, static_cast<const uint8_t *>(a.c_cache), a.ld_cache,
                          p.scale_log2};
     cudaLaunchConfig_t cfg = {};
     cfg.stream = s;
