@@ -113,11 +113,11 @@ struct Fp4Layout {
     static constexpr int kThreads = 128 * kGroups, HW = HP / kSoftGroups, N = kJoin ? 2 * HP : HP;   // N: columns of an MMA
     static constexpr int WC = N / kSoftGroups;                          // columns of a warpgroup
     // Expanded slabs in flight (four per unit), stages of codes and buffers of table numbers, as the queries leave room:
-    // 64 x 16384 rows, us with slabs + stages: 16 heads 105 with 7 + 4, 106 with 8 + 4; 32 heads 127 with 7 + 4, 130 with
-    // 8 + 2; 48 heads 145 with 7 + 2, 156 with 6 + 4; 64 heads 218 with 6 + 2, 227 with 5 + 4; 96 heads 263 with 5 + 1,
-    // 272 with 4 + 2.
-    static constexpr int kSlabs = HP == 96 ? 5 : (HP == 64 ? 6 : 7), kStages = HP == 96 ? 1 : (HP <= 32 ? 4 : 2),
-                         kPickBufs = HP == 96 ? 2 : 4;
+    // 64 x 16384 rows, us with slabs + stages: 16 heads 111 with 8 + 4, 121 with 7 + 4; 32 heads 136 with 8 + 2, 149 with
+    // 7 + 4; 48 heads 172 with 7 + 2, 217 with 8 + 1; 64 heads 210 with 6 + 2, 221 with 5 + 4, 233 with 7 + 1; 96 heads
+    // 264 with 5 + 1, 268 with 4 + 2.
+    static constexpr int kSlabs = HP == 96 ? 5 : (HP == 64 ? 6 : (HP == 48 ? 7 : 8)),
+                         kStages = HP == 96 ? 1 : (HP == 16 ? 4 : 2), kPickBufs = HP == 96 ? 2 : 4;
     static constexpr int kPBufs = kJoin ? 2 : 1, kSBufs = 2 * N <= 128 ? 2 : 1;
     static constexpr uint32_t kQPart = HP * 128, kQSlab = 2 * kQPart;   // [hi | lo rows x 128 latent]; kJoin: interleaved
     static constexpr uint32_t kPPart = kRows * 128, kPBuf = kJoin ? kPPart : 2 * kPPart;
