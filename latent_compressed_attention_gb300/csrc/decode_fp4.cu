@@ -113,9 +113,9 @@ struct Fp4Layout {
     static constexpr int kThreads = 128 * kGroups, HW = HP / kSoftGroups, N = kJoin ? 2 * HP : HP;   // N: columns of an MMA
     static constexpr int WC = N / kSoftGroups;                          // columns of a warpgroup
     // Expanded slabs in flight (four per unit), stages of codes and buffers of table numbers, as the queries leave room:
-    // 64 x 16384 rows, us with slabs + stages: 16 heads 111 with 8 + 4, 121 with 7 + 4; 32 heads 136 with 8 + 2, 149 with
-    // 7 + 4; 48 heads 172 with 7 + 2, 217 with 8 + 1; 64 heads 210 with 6 + 2, 221 with 5 + 4, 233 with 7 + 1; 96 heads
-    // 264 with 5 + 1, 268 with 4 + 2.
+    // 64 x 16384 rows, us with slabs + stages and scores of a deviation of 5 / 0.5: 16 heads 106 / 106 with 8 + 4, 117 / 105
+    // with 7 + 4; 32 heads 131 / 128 with 8 + 2, 144 / 125 with 7 + 4; 48 heads 171 / 144 with 7 + 2, 177 / 152 with 6 + 4;
+    // 64 heads 211 / 186 with 6 + 2, 221 / 198 with 5 + 4; 96 heads 258 / 237 with 5 + 1, 265 / 231 with 4 + 2.
     static constexpr int kSlabs = HP == 96 ? 5 : (HP == 64 ? 6 : (HP == 48 ? 7 : 8)),
                          kStages = HP == 96 ? 1 : (HP == 16 ? 4 : 2), kPickBufs = HP == 96 ? 2 : 4;
     static constexpr int kPBufs = kJoin ? 2 : 1, kSBufs = 2 * N <= 128 ? 2 : 1;
