@@ -325,11 +325,12 @@ MLA_API int mla_dequantize_latent_fp4(const void *c4, long long ld_c4, long long
  *   workspace  >= mla_latent_decode_fp4_workspace_size(...) bytes, 16-byte aligned, not used by any other call in
  *              flight
  * Precision: the scores take q_abs as two e4m3 parts (exact for a bf16 query but for elements below 2^-9 of their head's
- * largest, which are off by at most 2^-21 of it up to 48 heads, 2^-17 above) and the rows' values exactly; the softmax weights are two 8-bit parts: a weight is at most 2^-8 of itself off
- * up to 48 heads, 2^-7 above, and in both cases 2^-21 of the largest among the 4096 rows around it (weights times their
- * rows' largest scales), so that many light rows beside a heavy one lose no more than 2^-9 of its weight together; sums,
- * maxima and the join are fp32.  Rows that hold a group of values more than 2^14 below their largest scale (and the rows
- * around them) are taken in fp32, one after the other: right, but about fifty times slower.
+ * largest, which are off by at most 2^-21 of it up to 48 heads, 2^-17 above) and the rows' values exactly.  The softmax
+ * weights are two 8-bit parts: a weight is off by at most 2^-8 of itself up to 48 heads and 2^-7 above, and in both cases
+ * by 2^-21 of the largest among the 4096 rows around it and 2^-24 of the largest of all (weights times their rows' largest
+ * scales); all light rows beside a heavy one together lose at most 1.15 * 2^-9 of its weight.  Sums, maxima and the join
+ * are fp32.  Rows that hold a group of values more than 2^14 below their largest scale (and the rows around them) are taken
+ * in fp32, one after the other: right, but about fifty times slower.
  * lens[b] outside [0, max_len] is taken into it and reported as MLA_ERR_DEVICE_BOUNDS; lens[b] = 0 gives zeros.
  * B == 0 is a no-op.
  * Supported: r = 512, d_v = 128, 1 <= H <= 96.

@@ -28,11 +28,11 @@
 // barrier with an OR tells whether any does, and only then are the maxima taken across lanes and the moved heads' columns
 // of O^T rescaled.  Of P two 8-bit parts hold all but 2^-8 of it (above 48 heads 2^-7), and 2^-14 where hi is subnormal
 // (half a step of lo up to 48 heads; above, e5m2's 2^-4 of a rest of 2^-10), while l takes all of it.  2^-14 is 2^-21 of
-// the largest P when M was set; so that thousands of light rows behind one heavy row are not lost, M is set anew, lower
-// or higher, every kWindow units: what the rows of a window lose is at most 4096 * 2^-21 = 2^-9 of their largest P, or
-// 2^-45 each of the segment's, as M goes no lower than kDepth below its highest value (so that O^T and l stay in fp32's
-// range over a segment's 32768 rows).  64 x 16384 rows: up to 48 heads within 1 % of M never lowered; at 96 heads 265 us
-// against 250 with kHead = 3 and M never lowered, 278 with kHead = 3 and windows of 8 units, which lose as much.
+// the largest P when M was set.  So that thousands of light rows behind one heavy row are not lost, M is set anew, higher
+// or up to kDrop lower, every kWindow units: rows behind the heavy one lose at most 2^-21 of its P each in its window, 2^-24
+// in the next and so on, 4096 * 2^-21 * 8/7 = 1.15 * 2^-9 of it in all (and over a segment's eight windows O^T and l grow by
+// 2^21 at most, well inside fp32).  64 x 16384 rows, scores of a deviation of 5, with M never lowered / a drop of 3 / to
+// any depth: 16 heads 116 / 117 / 119 us (with seven slabs), 48 heads 170 / 172 / 174, 96 heads 256 / 257 / 260.
 //
 // Warps: 0 loads scale bytes (TMA) and turns them into table numbers, 1 issues S, 2 issues O, 3 loads codes (TMA); two
 // (above 48 heads: four) softmax warpgroups, each with its share of the heads, that never wait for one another (also
@@ -77,7 +77,7 @@ constexpr float kBias = 8.f;               // P = 2^(a - M + kBias)
 constexpr float kSlack = 0.75f;            // how far a row may exceed M before M moves
 constexpr float kHead = 1.f;               // M is set this far above the row that forces it
 constexpr int kWindow = 32;                // units after which M is set anew
-constexpr float kDepth = 24.f;             // how far M may be set below its highest value in a segment
+constexpr float kDrop = 3.f;               // how far it may then fall
 constexpr uint32_t kSlab = 16384;          // [128 rows x 128 latent] e4m3, 128-byte swizzle
 constexpr uint32_t kPicks = 2048;          // [128 rows x 16 groups] table numbers of a unit
 constexpr uint32_t kStage = 8192;          // codes of one slab: [128 rows x 64 bytes]
@@ -98,7 +98,6 @@ struct Fp4Shared {
     alignas(16) float mul[96];             // per head: score factor
     // per softmax warpgroup and head: kBias - M, and the last change of it with its power of two
     alignas(16) float bias[kMaxSoftWarps / 4][kMaxHW], step[kMaxSoftWarps / 4][kMaxHW], fac[kMaxSoftWarps / 4][kMaxHW];
-    float below[kMaxSoftWarps / 4][kMaxHW];   // M's highest value in the segment - M
     // per softmax warp: maxima, and parts of l while a segment is drained
     float part[kMaxSoftWarps][kMaxHW];
     bool low[8];                           // of the last eight units: whether any group takes a table below kExact
@@ -841,9 +840,7 @@ __global__ void __launch_bounds__(Fp4Layout<HP>::kThreads, 1)
                         moves = (most > kBias + kSlack || fresh) && most > -INFINITY;
                         if (quad == 0) {
                             float by = moves ? kBias - kHead - most : 0.f;   // M_old - M_new
-                            float &below = sh.below[wg][lane];
-                            if (u > 0) by = fminf(by, kDepth - below);
-                            below = u > 0 ? fmaxf(below + by, 0.f) : 0.f;
+                            if (u > 0) by = fminf(by, kDrop);
                             step[lane] = by;
                             fac[lane] = fast_exp2(by);
                             bias[lane] += by;
