@@ -40,11 +40,12 @@
 // permute per four codes: the group's exponent selects an 8-byte table of e4m3 magnitudes, the codes' three magnitude
 // bits are the selector.
 //
-// What bounds it (64 x 16384 rows with their merge, 1.93 GHz): at 96 heads 262 us, 9400 cycles a unit, of which the
-// tensor pipe is busy 46 % (64 products of 56 cycles: shared memory feeds it 128 bytes a cycle).  The queries' 96 KB leave
-// room for one unit of expanded slabs and one slab more, so a unit's expansion, S, softmax and O mostly follow one
-// another, each slab of the next unit expanded as O leaves one.  At 48 heads 172 us (6200 cycles a unit), at 16 heads
-// 110 us (3940; tensor pipe 47 %, ALUs 55 %: the expansion's byte permutes and logic).  HBM is at 0.16 to 0.38 of its
+// What bounds it (64 x 16384 rows, scores of a deviation of 5, 1.85 GHz): at 96 heads 242 us and 17 of the merge, 8400 cycles
+// a unit, of which the tensor pipe is busy 46 % (64 products of about 56 cycles: shared memory feeds it 128 bytes a cycle).
+// The queries' 96 KB leave room for one unit of expanded slabs and one slab more, so a unit's expansion, S, softmax and O
+// mostly follow one another, each slab of the next unit expanded as O leaves one.  At 48 heads 171 us with the merge (144
+// for scores of a deviation of 0.5, where the maxima seldom move), at 16 heads 106 (3300 cycles a unit; tensor pipe 46 %,
+// ALUs 55 %: the expansion's byte permutes and logic; nothing is full).  HBM is at 0.16 to 0.38 of its
 // peak.  All roles' loops share an instruction cache that they overflow easily: waits that carry their error path and
 // issue loops unrolled fourfold cost 193 us instead of 127 at 16 heads, which is why loops here are kept rolled, issuing
 // warps converged and cold code short.
@@ -69,8 +70,8 @@ constexpr int kDV = 128;
 constexpr int kRows = 128;                 // cache rows per unit
 constexpr int kChunkUnits = 256;           // units of a sequence that share one running maximum per segment
 constexpr int kChunkRows = kChunkUnits * kRows;
-// A segment's start and end in units: 64 ragged sequences up to 32768 rows at 96 heads 273 / 267 / 269 / 270 / 271 us with
-// 1 / 2 / 3 / 4 / 5, up to 8192 rows at 64 heads 86 / 88 / 88 / 90 / 90, at 48 heads 63 / 63 / 63 / 64 / 65.
+// A segment's start and end in units: 64 ragged sequences up to 32768 rows at 96 heads 270 / 266 / 266 / 267 us with 1 / 2 /
+// 3 / 4, up to 8192 rows at 64 heads 86 / 86 / 86 / 89, at 48 heads 73 / 73 / 73 / 75, at 16 heads 46 / 47 / 47 / 48.
 constexpr int kOver = 2;
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kBias = 8.f;               // P = 2^(a - M + kBias)

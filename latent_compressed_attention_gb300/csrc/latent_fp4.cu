@@ -12,9 +12,10 @@
 //   read   value = e2m1 * 2^(scale - 127): at most two significant bits, exact in bf16 and fp32.
 //
 // Both directions are a stream bound by HBM: a thread takes pieces of a few elements, neighbouring lanes a group, so that
-// every access of a warp is contiguous.  A thread has four pieces' loads in flight (131072 rows written in 28 us, 6.0 TB/s,
-// and read back in 27 us, against 40 and 39 with one; 4096 rows 2.8 and 2.5 us against 2.9 and 2.9), or one where a
-// sequence has too few rows for that, as the single tokens of a decode step.
+// every access of a warp is contiguous.  A thread has four pieces' loads in flight (131072 bf16 rows written in 30 us,
+// 5.7 TB/s, and read back in 26, against 42 and 38 with one; 4096 rows 2.1 and 1.8 us against 2.3 and 2.2; 131072 fp32
+// rows 47 us, 6.5 TB/s, and 46, against 46 and 70), or one where a sequence has too few rows for that, as the single
+// tokens of a decode step.
 #include <algorithm>
 
 #include "common.cuh"
