@@ -26,13 +26,13 @@
 //   P = 2^(a - M + 8), l += P * 2^-ref,   M[head] >= running max of a - 0.75
 // M moves when some row exceeds it by more than 0.75 (P <= 2^8.75 = 430, inside e4m3's 448), to kHead above that row: a
 // barrier with an OR tells whether any does, and only then are the maxima taken across lanes and the moved heads' columns
-// of O^T rescaled.  Of P two 8-bit parts hold all but 2^-8 of it (above 48 heads 2^-7), and 2^-14 where hi is subnormal
+// of O^T rescaled.  The two 8-bit parts of P are off by 2^-8 of it (above 48 heads 2^-7), or by 2^-14 where hi is subnormal
 // (half a step of lo up to 48 heads; above, e5m2's 2^-4 of a rest of 2^-10), while l takes all of it.  2^-14 is 2^-21 of
 // the largest P when M was set.  So that thousands of light rows behind one heavy row are not lost, M is set anew, higher
 // or up to kDrop lower, every kWindow units: rows behind the heavy one lose at most 2^-21 of its P each in its window, 2^-24
 // in the next and so on, 4096 * 2^-21 * 8/7 = 1.15 * 2^-9 of it in all (and over a segment's eight windows O^T and l grow by
 // 2^21 at most, well inside fp32).  64 x 16384 rows, scores of a deviation of 5, with M never lowered / a drop of 3 / to
-// any depth: 16 heads 116 / 117 / 119 us (with seven slabs), 48 heads 170 / 172 / 174, 96 heads 256 / 257 / 260.
+// any depth: 48 heads 170 / 172 / 174 us, 96 heads 256 / 257 / 260.
 //
 // Warps: 0 loads scale bytes (TMA) and turns them into table numbers, 1 issues S, 2 issues O, 3 loads codes (TMA); two
 // (above 48 heads: four) softmax warpgroups, each with its share of the heads, that never wait for one another (also
@@ -1053,7 +1053,7 @@ struct MergeParams {
     __nv_bfloat16 *out;
     int *err;
     int B, H, max_len, G;
-    const __nv_bfloat16 *q_abs;   // of the segments that are left to the merge
+    const __nv_bfloat16 *q_abs;   // for the shares that are done again
     const uint8_t *c4_cache;
     long long ld_cache;
     float scale_log2;
@@ -1064,7 +1064,7 @@ constexpr int kMaxShares = 512;   // share boundaries that the merge keeps in sh
 // A segment with rows that e4m3 cannot hold (groups more than 2^14 below their row's largest), for one head by one warp:
 // fp32 from the codes, one row after the other, into ws_o, ws_m and ws_l.
 __device__ __forceinline__ void exact_segment(const __nv_bfloat16 *q, const uint8_t *rows, long long ld, int n,
-                                           float scale_log2, float *to_o, float *to_m, float *to_l) {
+                                              float scale_log2, float *to_o, float *to_m, float *to_l) {
     const int lane = threadIdx.x & 31;   // columns 16 lane .. 16 lane + 15
     const uint4 *src = reinterpret_cast<const uint4 *>(q) + lane * 2;
     const uint4 q0 = __ldg(src), q1 = __ldg(src + 1);
