@@ -342,6 +342,85 @@ MLA_API int mla_latent_decode_fp4(const void *q_abs, const void *c4_cache, long 
                                   int H, int d_v, int r, void *workspace, size_t workspace_bytes, void *stream);
 
 /*
+ * The paged latent cache.  Rows live in a pool of `num_blocks` blocks of `block_size` rows (bf16, row stride ld_pool
+ * elements, block stride block_size * ld_pool); cache row u of sequence b is row u % block_size of block
+ * block_table[b * ld_table + u / block_size].  A serving step of T new tokens per sequence: reserve (blocks for rows
+ * lens[b] .. lens[b] + counts[b] - 1 and their slots), append (their latents), attend, then the caller advances lens by
+ * the tokens it keeps.  Drafts that are dropped need nothing: their rows are written again, their blocks go back at the
+ * next reserve.  num_blocks * block_size and max_blocks * block_size are at most 2^31 - 1.
+ *
+ * mla_reserve_latent_blocks - give each sequence the blocks for lens[b] + counts[b] rows and map its new tokens to
+ * pool rows.  In place, on the device, in a fixed order (the same inputs give the same blocks):
+ *   need_b = ceil((lens[b] + counts[b]) / block_size).  Sequences with held[b] > need_b give up their last blocks;
+ *   numbered in order of sequence and index, these go first to the sequences with held[b] < need_b, in the same order;
+ *   then the top of the free stack is taken; what nobody takes is put on the stack, the first one given up on top.
+ *   A growth followed by the same shrinking leaves the stack as it was.  lens[b] = counts[b] = 0 releases a sequence.
+ *   lens, counts  int32 [B] on the device
+ *   block_table   int32 [B, max_blocks] (row stride ld_table elements); entries from held[b] on are not read, and those
+ *                 past the new held[b] are left as they are
+ *   held          int32 [B]: the blocks in each sequence's row of the table; becomes need_b
+ *   free_blocks   int32 [capacity]: the free blocks are its first free_count[0] entries, the last one on top
+ *   free_count    int32 [1]
+ *   slots         int32 [B, T] (16-byte aligned) or NULL when T is 0: block_table[b][u / block_size] * block_size +
+ *                 u % block_size with u = lens[b] + t for t < counts[b], -1 for the other t
+ * All or nothing: when the free blocks do not suffice, a sequence needs more than max_blocks, a count is above T (with
+ * slots) or a length, count, held or free_count is out of its range, the state stays as it was, every slot is -1 and
+ * MLA_ERR_DEVICE_BOUNDS is reported (mla_get_device_error).  Blocks are numbers from 0 on; one whose rows pass 2^31 - 1
+ * gives slots of -1 and the same report.
+ * Supported: B <= 16384.  Returns MLA_OK or a negative mla_status_t; nothing is launched on error.
+ */
+MLA_API int mla_reserve_latent_blocks(const int *lens, const int *counts, int *block_table, long long ld_table, int *held,
+                                      int *free_blocks, int *free_count, int *slots, int B, int T, int max_blocks,
+                                      int capacity, int block_size, void *stream);
+
+/*
+ * mla_append_latent_paged - pool row slots[i] becomes row i of c, in bf16 (rounded to nearest even from F32), for every
+ * i < rows with a slot; a slot of -1 skips its row, any other outside the pool is skipped and reported as
+ * MLA_ERR_DEVICE_BOUNDS.  A slot that occurs twice holds pieces of either row afterwards (mla_reserve_latent_blocks gives
+ * each row one of its own).  No other row of the pool is touched.
+ *   c      [rows, r] of `dtype`, row stride ld_c elements
+ *   pool   pool row i (row i % block_size of block i / block_size) at element i * ld_pool; pool_rows of them
+ * Rows 16-byte aligned, r a multiple of 8.
+ * Returns MLA_OK or a negative mla_status_t; nothing is launched on error.
+ */
+MLA_API int mla_append_latent_paged(const void *c, long long ld_c, void *pool, long long ld_pool, long long pool_rows,
+                                    const int *slots, long long rows, int r, int dtype, void *stream);
+
+/*
+ * mla_latent_attend_paged - steps 2-4 for counts[b] new tokens of each sequence over the paged cache, in which the new
+ * tokens' own latents are rows lens[b] .. lens[b] + counts[b] - 1 (mla_append_latent_paged):
+ *
+ *   out[b,t,h] = sigmoid(gate[b,t,h]) * W_UV[h] . sum_u a_u c_u,   a = softmax over the visible rows u of
+ *                scale * q_abs[b,t,h] . c_u
+ *
+ * Without parents token t is the t-th of a chunk: its position is lens[b] + t and it sees rows u <= lens[b] + t.  With
+ * parents it is a draft: parents[b][t] < t is the new token it follows, -1 none; its position is lens[b] + the number of
+ * its ancestors among the new tokens, and it sees the rows u < lens[b], its ancestors' and its own.  With window > 0 a row
+ * is seen only if its position is above the token's - window or below sinks (window 1: the token itself; 0: no window).
+ * A row that a token does not see has no effect on it, whatever it holds.
+ *   q_abs        [B, T, H, r] bf16, absorbed queries (unscaled)
+ *   block_table  int32 [B, max_blocks] on the device, row stride ld_table; only entries for visible rows are read
+ *   lens         int32 [B]: rows cached before the new tokens
+ *   counts       int32 [B] or NULL (T each); rows of out for t >= counts[b] are left as they were
+ *   parents      int32 [B, T] or NULL; T <= 64 with it
+ *   w_uv         [H, d_v, r], gate [B, T, H*d_v] or NULL (pre-sigmoid logits), out [B, T, H*d_v], all bf16
+ *   workspace    >= mla_latent_attend_paged_workspace_size(B, T, H, r) bytes, 16-byte aligned, not used by any other call
+ *                in flight
+ * A sequence with a length, count or lens + counts outside [0, T] and [0, max_blocks * block_size] is skipped, rows of a
+ * block outside the pool count as zeros, and a parent outside [-1, t) as -1; each is reported as MLA_ERR_DEVICE_BOUNDS.
+ * Precision: products of bf16 values in fp32; softmax statistics, sums and the join of split rows in fp32; rounded to
+ * bf16 are the softmax weights, the weighted latent before W_UV, and out.
+ * Supported: r = 512, d_v = 128, 1 <= H <= 128, block_size a multiple of 64.
+ * Returns MLA_OK or a negative mla_status_t; nothing is launched on error.
+ */
+MLA_API size_t mla_latent_attend_paged_workspace_size(int B, int T, int H, int r);
+MLA_API int mla_latent_attend_paged(const void *q_abs, const void *pool, long long ld_pool, const int *block_table,
+                                    long long ld_table, const int *lens, const int *counts, const int *parents,
+                                    const void *w_uv, const void *gate, float scale, int window, int sinks, void *out,
+                                    int B, int T, int H, int d_v, int r, int num_blocks, int block_size, int max_blocks,
+                                    void *workspace, size_t workspace_bytes, void *stream);
+
+/*
  * mla_latent_decode_noalloc - mla_latent_decode for callers that cannot
  * allocate device memory.
  *

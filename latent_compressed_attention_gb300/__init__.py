@@ -18,6 +18,10 @@ Entry points (same names as the C functions):
     mla_append_latent_fp4(c, c4_cache, lens, counts=None)
     mla_dequantize_latent_fp4(c4, r, lens=None, dtype=torch.bfloat16, out=None)
     mla_latent_decode_fp4(q_abs, c4_cache, lens, w_uv, gate=None, scale=1.0, out=None, workspace=None)
+    mla_reserve_latent_blocks(lens, counts, T, block_table, held, free_blocks, free_count, block_size, slots=None)
+    mla_append_latent_paged(c, pool, slots)
+    mla_latent_attend_paged(q_abs, pool, block_table, lens, w_uv, counts=None, parents=None, gate=None, scale=1.0,
+                            window=0, sinks=0, out=None, workspace=None)
     mla_get_device_error(stream=None)
 """
 from __future__ import annotations
@@ -34,7 +38,8 @@ __all__ = ["MLAError", "build", "library", "library_path", "mla_absorbed_attn_fw
            "mla_latent_decode_workspace_size", "mla_latent_decode_noalloc", "mla_latent_decode_fp8",
            "mla_quantize_latent_fp8", "mla_latent_fp4_row_bytes", "mla_quantize_latent_fp4",
            "mla_append_latent_fp4", "mla_dequantize_latent_fp4", "mla_latent_decode_fp4",
-           "mla_latent_decode_fp4_workspace_size", "mla_get_device_error",
+           "mla_latent_decode_fp4_workspace_size", "mla_reserve_latent_blocks", "mla_append_latent_paged",
+           "mla_latent_attend_paged", "mla_latent_attend_paged_workspace_size", "mla_get_device_error",
            "mla_status_string", "mla_version", "mla_kernel_launches", "mla_debug_wait_timeout",
            "mla_absorbed_attn_bwd", "mla_gated_layer_fwd", "mla_gated_layer_workspace_size",
            "mla_gated_layer_decode", "layer_workspace_views", "DTYPE_BF16", "DTYPE_F32"]
@@ -96,6 +101,14 @@ def library():
             lib.mla_latent_decode_fp4_workspace_size.restype = sz
             lib.mla_latent_decode_fp4.argtypes = [vp, vp, ll, vp, i, vp, vp, f, vp, i, i, i, i, vp, sz, vp]
             lib.mla_latent_decode_fp4.restype = i
+            lib.mla_reserve_latent_blocks.argtypes = [vp, vp, vp, ll, vp, vp, vp, vp, i, i, i, i, i, vp]
+            lib.mla_reserve_latent_blocks.restype = i
+            lib.mla_append_latent_paged.argtypes = [vp, ll, vp, ll, ll, vp, ll, i, i, vp]
+            lib.mla_append_latent_paged.restype = i
+            lib.mla_latent_attend_paged_workspace_size.argtypes = [i] * 4
+            lib.mla_latent_attend_paged_workspace_size.restype = sz
+            lib.mla_latent_attend_paged.argtypes = [vp, vp, ll, vp, ll, vp, vp, vp, vp, vp, f, i, i, vp] + [i] * 8 + [vp, sz, vp]
+            lib.mla_latent_attend_paged.restype = i
             lib.mla_latent_decode_noalloc.argtypes = [vp, vp, ll, vp, i, vp, vp, f, vp, i, i, i, i, i, vp]
             lib.mla_latent_decode_noalloc.restype = i
             lib.mla_gated_layer_workspace_size.argtypes = [i, i, i, i, i, i, i, i, i]
@@ -686,6 +699,177 @@ def mla_latent_decode_fp4(q_abs, c4_cache, lens, w_uv, gate=None, scale: float =
                 free(scratch)
     if rc != 0:
         raise MLAError(rc, "mla_latent_decode_fp4")
+    return out
+
+
+def _count(value, name):
+    """A size or number that has to fit a C int; negative ones go on to the library, which refuses them."""
+    value = int(value)
+    if not -2**31 <= value < 2**31:
+        raise ValueError(f"{name} = {value} does not fit 32 bits")
+    return value
+
+
+def _paged_pool(pool, device):
+    """Checks a [num_blocks, block_size, r] pool (rows at one stride); returns (num_blocks, block_size, r, row stride)."""
+    if not pool.is_cuda or pool.dtype != _torch().bfloat16:
+        raise TypeError("pool must be a bf16 CUDA tensor")
+    if pool.device != device:
+        raise ValueError(f"pool is on {pool.device}, expected {device}")
+    if pool.dim() != 3:
+        raise ValueError("pool must be [num_blocks,block_size,r]")
+    blocks, bs, r = pool.shape
+    batch, ld, inner = pool.stride()
+    # a dimension of one entry has no stride of its own to go by: blocks of one row each are as long as their stride
+    if bs == 1:
+        ld = batch if blocks > 1 else max(ld, r)
+    if (inner != 1 and r > 1) or (blocks > 1 and batch != bs * ld):
+        raise ValueError("pool must have unit inner stride and block stride block_size*row_stride")
+    return blocks, bs, r, ld
+
+
+def _block_table(table, B, device):
+    """Checks an int32 [B, max_blocks] table; returns (max_blocks, row stride)."""
+    if not table.is_cuda or table.dtype != _torch().int32:
+        raise TypeError("block_table must be an int32 CUDA tensor")
+    if table.device != device:
+        raise ValueError(f"block_table is on {table.device}, expected {device}")
+    if table.dim() != 2 or table.shape[0] != B or (table.shape[1] > 1 and table.stride(1) != 1):
+        raise ValueError(f"block_table must be [{B},max_blocks] with unit inner stride")
+    wide = table.shape[1]
+    ld = table.stride(0) if B > 1 and wide > 0 else wide
+    if ld < wide:
+        raise ValueError("block_table's rows overlap")
+    return wide, ld
+
+
+def mla_reserve_latent_blocks(lens, counts, T: int, block_table, held, free_blocks, free_count, block_size: int,
+                              slots=None, stream=None):
+    """Blocks of a paged cache for lens[b] + counts[b] rows of each sequence, in place; returns the new tokens' pool rows,
+    slots int32 [B,T] (-1 for t >= counts[b]).
+
+    lens, counts, held: int32 [B]; block_table int32 [B,max_blocks] (rows at any stride); free_blocks int32 [capacity]: a
+    stack of free_count[0] (int32 [1]) blocks, its last entry on top.  Sequences that hold more than they need give blocks
+    up, which serve the others before the stack does; held becomes what each one needs.  T is at least the largest count;
+    with T = 0 only the blocks are moved.  If something does not fit or is out of range, nothing changes, every slot is -1
+    and the device error word is set (mla_get_device_error).
+    """
+    torch = _torch()
+    dev, B, T = lens.device, lens.shape[0], _count(T, "T")
+    _check(lens, "lens", torch.int32, dev, (B,))
+    _check(counts, "counts", torch.int32, dev, (B,))
+    _check(held, "held", torch.int32, dev, (B,))
+    wide, ld = _block_table(block_table, B, dev)
+    _check(free_blocks, "free_blocks", torch.int32, dev)
+    _check(free_count, "free_count", torch.int32, dev, (1,))
+    if T < 0 or free_blocks.dim() != 1:
+        raise ValueError("T must not be negative and free_blocks must be [capacity]")
+    with _on(stream, dev):
+        if slots is None:
+            slots = torch.empty((B, T), dtype=torch.int32, device=dev)
+        else:
+            _check(slots, "slots", torch.int32, dev, (B, T))
+        rc = library().mla_reserve_latent_blocks(lens.data_ptr(), counts.data_ptr(), block_table.data_ptr(), ld,
+                                                 held.data_ptr(), free_blocks.data_ptr(), free_count.data_ptr(),
+                                                 slots.data_ptr(), B, T, wide, free_blocks.shape[0],
+                                                 _count(block_size, "block_size"),
+                                                 _raw_stream(stream, dev))
+    if rc != 0:
+        raise MLAError(rc, "mla_reserve_latent_blocks")
+    return slots
+
+
+def mla_append_latent_paged(c, pool, slots, stream=None):
+    """c [...,r] (bf16 or fp32, contiguous) into rows slots [...] (int32, -1: none) of a paged cache, pool
+    [num_blocks,block_size,r] bf16 (or a row-strided view), whose row i is row i % block_size of block i / block_size;
+    returns pool.  A slot outside the pool is skipped and sets the device error word; no slot may occur twice.
+    """
+    torch = _torch()
+    dev = c.device
+    _check(c, "c", c.dtype, dev)
+    blocks, bs, r, ld = _paged_pool(pool, dev)
+    if c.dim() < 1 or c.shape[-1] != r:
+        raise ValueError(f"c must be [...,{r}]")
+    _check(slots, "slots", torch.int32, dev, c.shape[:-1])
+    with _on(stream, dev):
+        rc = library().mla_append_latent_paged(c.data_ptr(), r, pool.data_ptr(), ld, blocks * bs, slots.data_ptr(),
+                                               slots.numel(), r, _dtype_code(c), _raw_stream(stream, dev))
+    if rc != 0:
+        raise MLAError(rc, "mla_append_latent_paged")
+    return pool
+
+
+def mla_latent_attend_paged_workspace_size(B: int, T: int, H: int, r: int) -> int:
+    return int(library().mla_latent_attend_paged_workspace_size(B, T, H, r))
+
+
+def mla_latent_attend_paged(q_abs, pool, block_table, lens, w_uv, counts=None, parents=None, gate=None,
+                            scale: float = 1.0, window: int = 0, sinks: int = 0, out=None, workspace=None, stream=None):
+    """Attention of T new tokens per sequence over a paged latent cache; returns out [B,T,H*128] (bf16).
+
+    q_abs [B,T,H,512], w_uv [H,128,512] and gate [B,T,H*128] (or None) bf16; pool [num_blocks,block_size,512] bf16 (or a
+    row-strided view; block_size a multiple of 64); block_table int32 [B,max_blocks]; lens int32 [B]: the rows cached
+    before the new tokens, whose own latents are rows lens[b] + t already (mla_append_latent_paged).  counts int32 [B] (or
+    None: T each): sequence b has counts[b] new tokens; the other rows of out are left as they were (out, when not given,
+    is then zeroed first).
+
+    Without parents the tokens are a chunk and token t sees rows up to lens[b] + t.  With parents (int32 [B,T], T <= 64)
+    they are drafts: token t follows the new token parents[b,t] < t (-1: the cached ones) and sees the cached rows, its
+    ancestors and itself.  With window > 0 it sees only the last `window` positions up to its own, and positions below
+    `sinks`.  A workspace (a contiguous tensor on the query's device) is allocated when not given.
+    """
+    torch = _torch()
+    if q_abs.dim() != 4:
+        raise ValueError("q_abs must be [B,T,H,r]")
+    B, T, H, r = q_abs.shape
+    dev, bf16, i32 = q_abs.device, torch.bfloat16, torch.int32
+    _check(q_abs, "q_abs", bf16, dev)
+    blocks, bs, width, ld = _paged_pool(pool, dev)
+    if width != r:
+        raise ValueError(f"pool must be [num_blocks,block_size,{r}]")
+    wide, ld_table = _block_table(block_table, B, dev)
+    _check(lens, "lens", i32, dev, (B,))
+    d_v = w_uv.shape[1]
+    _check(w_uv, "w_uv", bf16, dev, (H, d_v, r))
+    if counts is not None:
+        _check(counts, "counts", i32, dev, (B,))
+    if parents is not None:
+        _check(parents, "parents", i32, dev, (B, T))
+    shape = (B, T, H * d_v)
+    if gate is not None:
+        _check(gate, "gate", bf16, dev, shape)
+    lib = library()
+    with _on(stream, dev):
+        if out is None:
+            out = (torch.empty if counts is None else torch.zeros)(shape, dtype=bf16, device=dev)
+        else:
+            _check(out, "out", bf16, dev, shape)
+        on, scratch = _raw_stream(stream, dev), None
+        if workspace is None:
+            # from the caching allocator without a tensor around it, where torch has the names
+            ws_bytes = lib.mla_latent_attend_paged_workspace_size(B, T, H, r)
+            alloc = getattr(torch._C, "_cuda_cudaCachingAllocator_raw_alloc", None)
+            free = getattr(torch._C, "_cuda_cudaCachingAllocator_raw_delete", None)
+            if ws_bytes > 0 and alloc is not None and free is not None:
+                ws_ptr = scratch = alloc(ws_bytes, on)
+            else:
+                workspace = torch.empty(ws_bytes, dtype=torch.uint8, device=dev)
+        else:
+            _check(workspace, "workspace", workspace.dtype, dev)
+        if workspace is not None:
+            ws_ptr, ws_bytes = workspace.data_ptr(), workspace.numel() * workspace.element_size()
+        try:
+            rc = lib.mla_latent_attend_paged(
+                q_abs.data_ptr(), pool.data_ptr(), ld, block_table.data_ptr(), ld_table, lens.data_ptr(),
+                None if counts is None else counts.data_ptr(), None if parents is None else parents.data_ptr(),
+                w_uv.data_ptr(), None if gate is None else gate.data_ptr(), float(scale),
+                _count(window, "window"), _count(sinks, "sinks"), out.data_ptr(), B, T, H, d_v, r, blocks, bs, wide,
+                ws_ptr, ws_bytes, on)
+        finally:
+            if scratch is not None:   # as a tensor's memory: the next taker on this stream comes after these kernels
+                free(scratch)
+    if rc != 0:
+        raise MLAError(rc, "mla_latent_attend_paged")
     return out
 
 

@@ -427,6 +427,84 @@ MLA_API int mla_latent_decode_fp4(const void *q_abs, const void *c4_cache, long 
     return e == cudaSuccess ? MLA_OK : MLA_ERR_CUDA;
 }
 
+namespace {
+bool aligned4(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
+}  // namespace
+
+MLA_API int mla_reserve_latent_blocks(const int *lens, const int *counts, int *block_table, long long ld_table, int *held,
+                                      int *free_blocks, int *free_count, int *slots, int B, int T, int max_blocks,
+                                      int capacity, int block_size, void *stream) {
+    if (B < 0 || T < 0 || max_blocks < 0 || capacity < 0 || block_size <= 0 || ld_table < max_blocks) return MLA_ERR_SHAPE;
+    if (!mul_fits(max_blocks, block_size, INT_MAX) || !mul_fits(B, ld_table, LLONG_MAX / 8)) return MLA_ERR_SHAPE;
+    if (B > kReserveMaxB) return MLA_ERR_UNSUPPORTED;
+    if (B == 0) return MLA_OK;
+    if (!lens || !counts || !held || !free_count || (max_blocks > 0 && !block_table) || (capacity > 0 && !free_blocks) ||
+        (T > 0 && !slots))
+        return MLA_ERR_NULL;
+    if (!aligned4(lens) || !aligned4(counts) || !aligned4(block_table) || !aligned4(held) || !aligned4(free_blocks) ||
+        !aligned4(free_count) || !aligned16(slots))
+        return MLA_ERR_ALIGN;
+    DeviceInfo *dev = nullptr;
+    if (device_info(dev) != cudaSuccess) return MLA_ERR_CUDA;
+    const ReserveArgs a{lens, counts, block_table, held, free_blocks, free_count, slots, ld_table, B, T, max_blocks,
+                        capacity, block_size, dev->err_word};
+    return launch_reserve_latent_blocks(a, static_cast<cudaStream_t>(stream)) == cudaSuccess ? MLA_OK : MLA_ERR_CUDA;
+}
+
+MLA_API int mla_append_latent_paged(const void *c, long long ld_c, void *pool, long long ld_pool, long long pool_rows,
+                                    const int *slots, long long rows, int r, int dtype, void *stream) {
+    if (dtype != MLA_DTYPE_BF16 && dtype != MLA_DTYPE_F32) return MLA_ERR_DTYPE;
+    if (rows < 0 || pool_rows < 0 || pool_rows > INT_MAX || r <= 0 || r % 8 != 0 || ld_c < r || ld_pool < r)
+        return MLA_ERR_SHAPE;
+    if (!mul_fits(rows, ld_c, LLONG_MAX / 8) || !mul_fits(pool_rows, ld_pool, LLONG_MAX / 8)) return MLA_ERR_SHAPE;
+    if (rows == 0) return MLA_OK;
+    if (!c || !slots || (!pool && pool_rows > 0)) return MLA_ERR_NULL;
+    if (!aligned16(c) || !aligned16(pool) || !aligned4(slots) || ld_pool % 8 != 0 ||
+        ld_c % (dtype == MLA_DTYPE_BF16 ? 8 : 4) != 0)
+        return MLA_ERR_ALIGN;
+    DeviceInfo *dev = nullptr;
+    if (device_info(dev) != cudaSuccess) return MLA_ERR_CUDA;
+    const AppendPagedArgs a{c, pool, slots, ld_c, ld_pool, rows, pool_rows, r, dtype == MLA_DTYPE_F32, dev->err_word};
+    return launch_append_latent_paged(a, static_cast<cudaStream_t>(stream)) == cudaSuccess ? MLA_OK : MLA_ERR_CUDA;
+}
+
+MLA_API size_t mla_latent_attend_paged_workspace_size(int B, int T, int H, int r) {
+    if (B <= 0 || T <= 0 || !attend_paged_supports(H, 128, r) || !mul_fits(static_cast<long long>(B) * T, H, INT_MAX))
+        return 0;
+    DeviceInfo *dev = nullptr;
+    if (device_info(dev) != cudaSuccess) return 0;
+    return attend_paged_workspace_bytes(B, T, H, dev->num_sms);
+}
+
+MLA_API int mla_latent_attend_paged(const void *q_abs, const void *pool, long long ld_pool, const int *block_table,
+                                    long long ld_table, const int *lens, const int *counts, const int *parents,
+                                    const void *w_uv, const void *gate, float scale, int window, int sinks, void *out,
+                                    int B, int T, int H, int d_v, int r, int num_blocks, int block_size, int max_blocks,
+                                    void *workspace, size_t workspace_bytes, void *stream) {
+    if (B < 0 || T < 0 || H <= 0 || d_v <= 0 || r <= 0 || num_blocks < 0 || block_size <= 0 || max_blocks < 0 ||
+        window < 0 || sinks < 0 || ld_pool < r || ld_table < max_blocks)
+        return MLA_ERR_SHAPE;
+    if (!attend_paged_supports(H, d_v, r) || block_size % 64 != 0 || (parents && T > 64)) return MLA_ERR_UNSUPPORTED;
+    if (!mul_fits(num_blocks, block_size, INT_MAX) || !mul_fits(max_blocks, block_size, INT_MAX) ||
+        !mul_fits(static_cast<long long>(B) * T, H, INT_MAX) || !mul_fits(B, ld_table, LLONG_MAX / 8) ||
+        !mul_fits(static_cast<long long>(num_blocks) * block_size, ld_pool, LLONG_MAX / 8))
+        return MLA_ERR_SHAPE;
+    if (B == 0 || T == 0) return MLA_OK;
+    if (!q_abs || !lens || !w_uv || !out || (num_blocks > 0 && !pool) || (max_blocks > 0 && !block_table)) return MLA_ERR_NULL;
+    if (!aligned16(q_abs) || !aligned16(pool) || !aligned16(w_uv) || !aligned16(out) || !aligned16(gate) ||
+        !aligned4(block_table) || !aligned4(lens) || !aligned4(counts) || !aligned4(parents) || ld_pool % 8 != 0)
+        return MLA_ERR_ALIGN;
+    DeviceInfo *dev = nullptr;
+    if (device_info(dev) != cudaSuccess) return MLA_ERR_CUDA;
+    const size_t need = attend_paged_workspace_bytes(B, T, H, dev->num_sms);
+    if (!workspace || workspace_bytes < need) return MLA_ERR_WORKSPACE;
+    if (!aligned16(workspace)) return MLA_ERR_ALIGN;
+    const AttendPagedArgs a{q_abs, pool, w_uv, gate, block_table, lens, counts, parents, out, ld_pool, ld_table, B, T, H,
+                            num_blocks, block_size, max_blocks, window, sinks, scale, workspace, workspace_bytes,
+                            dev->err_word, dev->num_sms};
+    return launch_attend_paged(a, static_cast<cudaStream_t>(stream)) == cudaSuccess ? MLA_OK : MLA_ERR_CUDA;
+}
+
 MLA_API int mla_latent_decode_noalloc(const void *q_abs, const void *c_cache, long long ld_cache, const int *lens,
                                       int max_len, const void *w_uv, const void *gate, float scale, void *out,
                                       int B, int H, int d_v, int r, int dtype, void *stream) {

@@ -122,6 +122,44 @@ cudaError_t launch_read_latent_fp4(const LatentFp4Args &a, cudaStream_t s);
 size_t decode_fp4_workspace_bytes(int B, int H, int max_len, int num_sms);
 cudaError_t launch_decode_fp4(const DecodeArgs &a, cudaStream_t s);
 
+// The paged latent cache (paged.cu): block tables and slot maps, rows written through them.
+struct ReserveArgs {
+    const int *lens, *counts;                     // [B]
+    int *table, *held, *free_blocks, *free_count; // [B][ld_table], [B], [capacity], [1]
+    int *slots;                                   // [B][T]
+    long long ld_table;
+    int B, T, max_blocks, capacity, bs;
+    int *dev_err;
+};
+constexpr int kReserveMaxB = 16384;               // two prefix sums over the sequences in shared memory
+cudaError_t launch_reserve_latent_blocks(const ReserveArgs &a, cudaStream_t s);
+struct AppendPagedArgs {
+    const void *c;
+    void *pool;
+    const int *slots;
+    long long ld_c, ld_pool, rows, pool_rows;     // strides in elements
+    int r;
+    bool f32;                                     // c's type (the pool is bf16)
+    int *dev_err;
+};
+cudaError_t launch_append_latent_paged(const AppendPagedArgs &a, cudaStream_t s);
+// A run of tokens per sequence over the paged cache (attend_paged.cu).
+struct AttendPagedArgs {
+    const void *q_abs, *pool, *w_uv, *gate;
+    const int *table, *lens, *counts, *parents;   // counts, parents: or NULL
+    void *out;
+    long long ld_pool, ld_table;
+    int B, T, H, num_blocks, bs, max_blocks, window, sinks;
+    float scale;
+    void *workspace;
+    size_t workspace_bytes;
+    int *dev_err;
+    int num_sms;
+};
+bool attend_paged_supports(int H, int d_v, int r);
+size_t attend_paged_workspace_bytes(long long B, long long T, int H, int num_sms);
+cudaError_t launch_attend_paged(const AttendPagedArgs &a, cudaStream_t s);
+
 // Scratch of the no-alloc decode entry point: capacity in bytes, and its
 // device address on the current device (set up once per device).
 size_t decode_noalloc_scratch_capacity();
