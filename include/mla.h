@@ -347,7 +347,7 @@ MLA_API int mla_latent_decode_fp4(const void *q_abs, const void *c4_cache, long 
  * block_table[b * ld_table + u / block_size].  A serving step of T new tokens per sequence: reserve (blocks for rows
  * lens[b] .. lens[b] + counts[b] - 1 and their slots), append (their latents), attend, then the caller advances lens by
  * the tokens it keeps.  Drafts that are dropped need nothing: their rows are written again, their blocks go back at the
- * next reserve.  num_blocks * block_size and max_blocks * block_size are at most 2^31 - 1.
+ * next reserve.  num_blocks * block_size and max_blocks * block_size are at most 2^31 - 1024.
  *
  * mla_reserve_latent_blocks - give each sequence the blocks for lens[b] + counts[b] rows and map its new tokens to
  * pool rows.  In place, on the device, in a fixed order (the same inputs give the same blocks):

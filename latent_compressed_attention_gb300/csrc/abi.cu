@@ -435,7 +435,7 @@ MLA_API int mla_reserve_latent_blocks(const int *lens, const int *counts, int *b
                                       int *free_blocks, int *free_count, int *slots, int B, int T, int max_blocks,
                                       int capacity, int block_size, void *stream) {
     if (B < 0 || T < 0 || max_blocks < 0 || capacity < 0 || block_size <= 0 || ld_table < max_blocks) return MLA_ERR_SHAPE;
-    if (!mul_fits(max_blocks, block_size, INT_MAX) || !mul_fits(B, ld_table, LLONG_MAX / 8)) return MLA_ERR_SHAPE;
+    if (!mul_fits(max_blocks, block_size, INT_MAX - 1023) || !mul_fits(B, ld_table, LLONG_MAX / 8)) return MLA_ERR_SHAPE;
     if (B > kReserveMaxB) return MLA_ERR_UNSUPPORTED;
     if (B == 0) return MLA_OK;
     if (!lens || !counts || !held || !free_count || (max_blocks > 0 && !block_table) || (capacity > 0 && !free_blocks) ||
@@ -485,7 +485,7 @@ MLA_API int mla_latent_attend_paged(const void *q_abs, const void *pool, long lo
         window < 0 || sinks < 0 || ld_pool < r || ld_table < max_blocks)
         return MLA_ERR_SHAPE;
     if (!attend_paged_supports(H, d_v, r) || block_size % 64 != 0 || (parents && T > 64)) return MLA_ERR_UNSUPPORTED;
-    if (!mul_fits(num_blocks, block_size, INT_MAX) || !mul_fits(max_blocks, block_size, INT_MAX) ||
+    if (!mul_fits(num_blocks, block_size, INT_MAX - 1023) || !mul_fits(max_blocks, block_size, INT_MAX - 1023) ||
         !mul_fits(static_cast<long long>(B) * T, H, INT_MAX) || !mul_fits(B, ld_table, LLONG_MAX / 8) ||
         !mul_fits(static_cast<long long>(num_blocks) * block_size, ld_pool, LLONG_MAX / 8))
         return MLA_ERR_SHAPE;

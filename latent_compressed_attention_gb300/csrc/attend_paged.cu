@@ -1,4 +1,35 @@
-// Attention of each sequence's new tokens over the paged latent cache (r = 512, d_v = 128).
+// Attention of each sequence's new tokens (one, a chunk or a drafted tree) over the paged latent cache on the sm_103a
+// tensor cores: r = 512, d_v = 128, 1 <= H <= 128.
+//
+// Steps 2-4 of section "完整计算流（四步）" on the page "Gated MLA（矩阵吸收版）", over the cache of latents alone (KV-cache
+// table, section "形状与参数对比"): token t's head h scores the visible rows u, a = softmax(scale q_abs . c_u),
+// o_lat = sum a_u c_u, out = sigmoid(gate) * W_UV[h] o_lat.  All heads of all tokens of a sequence read the same rows, so
+// a sequence's (token, head) pairs, in the order of q_abs, are cut into tiles of M = 128 rows of one product.
+//
+// Pair kernel (persistent, one cluster of two CTAs per SM pair).  A tile walks the cache in units of 128 rows that any of
+// its tokens sees: the first few (sinks), then from the window's start to the last token's own row.  All tiles' units, each
+// tile's preceded by the cost of starting it, are cut into one equal share per cluster, so that one long sequence and
+// many ragged ones keep every SM busy.
+//   rank 0, the score CTA: the tile's q_abs sits in TMEM as packed bf16 (columns 0-255) and is the A operand of
+//     S = q_abs . c^T, N = 128 cache rows, into one of two buffers (columns 256-511).  Two warpgroups take the units in
+//     turn (thread = row of the tile) and hand each other the running maximum, so that a unit's product runs while the
+//     one before is exponentiated; P (bf16) with each row's rescaling factor and sum goes to the value CTA by a bulk copy.
+//   rank 1, the value CTA: o_lat += P . c, N = 2 x 256 latent columns, fp32 in all 512 TMEM columns, rescaled lazily when
+//     a row's maximum grew by more than 2^16.
+// Each CTA loads the rows it needs: boxes of 64 (score) or 32 rows, which lie inside one block of the pool.
+//
+// Masks are bit sets of 128 rows per row of the tile, used only in units that some of the tile's tokens do not see whole.
+// There the value CTA's math warps also replace what is not finite in the rows by zeros before the product: 0 * NaN of a
+// row that a token does not see would reach it; a token that does see one gets its NaN through the sum of its weights.
+//
+// A tile that one cluster walked whole leaves o_lat / l as bf16 rows; a tile cut between clusters leaves fp32 sums with
+// their maxima and weights, at most two such parts per cluster.  The second kernel joins those, applies W_UV^T on the
+// tensor cores and the gate.
+#include <cuda.h>
+#include <cudaTypedefs.h>
+
+#include <atomic>
+
 #include "common.cuh"
 #include "internal.h"
 
@@ -6,114 +37,1062 @@ namespace mla {
 namespace {
 
 constexpr int kR = 512, kDV = 128;
+constexpr int kM = 128;         // (token, head) rows of a tile
+constexpr int kUnit = 128;      // cache rows of a unit
+constexpr int kThreads = 384;   // warps 0 and 3 TMA, 1 MMA, 2 relay (value CTA), 4-7 and 8-11: two warpgroups
+constexpr uint32_t kRegsCtl = 80, kRegsMath = 208, kRegsLaunch = 168;
+static_assert(128 * kRegsCtl + 256 * kRegsMath <= kThreads * kRegsLaunch, "register split exceeds the launch");
 constexpr float kLog2e = 1.4426950408889634f;
+// A stale maximum is kept until the new one exceeds it by this (log2 units): p <= 2^16, far inside fp32's range.
+constexpr float kRescaleLog2 = 16.0f;
+// Units that starting a tile counts for in the shares: its queries' load, its accumulator's drain, the pipeline's refill.
+constexpr int kStart = 8;
 
-// Which cache rows a token sees: [0, head) and [lo, hi), and of the rows from `tree` on those whose bit is set.
-struct Sight {
-    int head, lo, hi, tree;
-    unsigned long long bits;
-    __device__ bool sees(int u) const {
-        return u < tree ? (u < head || u >= lo) && u < hi : u - tree < 64 && ((bits >> (u - tree)) & 1);
+constexpr uint32_t kSlab = 16384;                  // [128 rows x 64 columns] bf16, 128-byte swizzle
+constexpr uint32_t kInfo = kM * 8;                 // {rescaling factor, sum} per row of the tile
+constexpr uint32_t kPUnit = 2 * kSlab + kInfo;     // P [128 x 128] and its info
+constexpr uint32_t kStage = 16384;                 // of either ring
+// score CTA: stages of [128 cache rows x 64 latent columns], P staging per warpgroup, running maxima per warpgroup
+constexpr int kSStages = 9;
+constexpr uint32_t S_PST = kSStages * kStage;
+constexpr uint32_t S_MAX = S_PST + 2 * kPUnit;
+constexpr uint32_t S_END = S_MAX + 2 * kM * 4;
+// value CTA: P buffers, stages of [32 cache rows x 256 latent columns] (four slabs of 64 columns)
+constexpr int kPBufs = 3, kVStages = 7, kVRows = 32;
+constexpr uint32_t kVSlab = kVRows * 128;
+constexpr uint32_t V_RING = kPBufs * kPUnit;
+constexpr uint32_t V_END = V_RING + kVStages * kStage;
+constexpr uint32_t BARS = (S_END > V_END ? S_END : V_END);
+constexpr uint32_t kSmemPair = BARS + 768 + 1024;  // + alignment slack
+static_assert(kPUnit % 1024 == 0 && BARS % 16 == 0 && kSmemPair <= 232448, "shared memory");
+constexpr uint64_t kLandNs = 50000000;             // a load that was issued lands long before this
+constexpr uint32_t S_COL = 256;                    // S buffers in the score CTA's TMEM
+
+constexpr uint32_t kIdescS = make_idesc_bf16(128, 128, 0, 0);   // q_abs (TMEM) x c (K-major)
+constexpr uint32_t kIdescO = make_idesc_bf16(128, 256, 0, 1);   // P (K-major) x c (MN-major)
+
+struct PairBars {
+    uint64_t q_ready, s_full[2], s_free[2], m_ready[2];
+    uint64_t sc_full[kSStages], sc_empty[kSStages];
+    uint64_t p_free[kPBufs];                             // arrivals from the value CTA
+    uint64_t v_full[kVStages], v_empty[kVStages], v_clean[kVStages];
+    uint64_t p_full[kPBufs];                             // the score CTA's copies
+    uint64_t pv_done[kPBufs], info_read[kPBufs], rescaled, drained;
+    uint32_t tmem_base;
+    int abort;
+    // where the cluster's share starts on the axis of units
+    long long lo, hi, pre;
+    int b, j;
+    long long warp_sum[kThreads / 32];
+};
+static_assert(sizeof(PairBars) <= 768, "barrier block too large");
+
+struct PairParams {
+    const __nv_bfloat16 *q_abs;
+    const int *table, *lens, *counts, *parents;
+    long long ld_table;
+    __nv_bfloat16 *ws_rows;              // [B * T * H][r]: whole tiles' o_lat / l
+    float *ws_o, *ws_m, *ws_l;           // [2 G][128][r], [2 G][128]: parts' sums, maxima (log2 units), weights
+    int2 *ws_tile;                       // [B * tiles]: first and last cluster of each tile
+    int *err;
+    int B, T, H, tiles, num_blocks, bs, max_blocks, window, sinks;
+    float scale_log2;
+};
+
+// New tokens of sequence b and its cached rows; none when its numbers are out of range.
+template <typename P>
+__device__ __forceinline__ int tokens(const P &p, int b, int &len, bool report) {
+    len = __ldg(p.lens + b);
+    const int count = p.counts ? __ldg(p.counts + b) : p.T;
+    if (len < 0 || count < 0 || count > p.T || static_cast<long long>(len) + count > static_cast<long long>(p.max_blocks) * p.bs) {
+        if (report) record_error(p.err, kDevErrBounds);
+        return 0;
+    }
+    return count;
+}
+
+// Tile j of a sequence: its tokens, and the units of the cache that any of them sees.
+struct Tile {
+    int rows, t0, t1;      // (token, head) rows; first and last token
+    int head, main, n;     // units from the cache's start on, first unit after those, units in all
+    int end;               // cache rows past the last one that is seen
+    __device__ __forceinline__ Tile() {}
+    __device__ __forceinline__ Tile(const PairParams &p, int j, int len, int count) {
+        const int m0 = j * kM;
+        rows = min(count * p.H - m0, kM);
+        t0 = m0 / p.H, t1 = (m0 + rows - 1) / p.H;
+        end = len + t1 + 1;
+        main = head = 0;
+        if (p.window > 0) {   // a draft stands at least at the first new position
+            main = max(len + (p.parents ? 0 : t0) - p.window + 1, 0) / kUnit;
+            head = min((min(p.sinks, end) + kUnit - 1) / kUnit, main);
+        }
+        n = head + (end + kUnit - 1) / kUnit - main;
+    }
+    __device__ __forceinline__ int row0(int i) const { return (i < head ? i : main + i - head) * kUnit; }
+    // Whether some token of the tile does not see all rows of the unit at u0.
+    __device__ __forceinline__ bool mixed(const PairParams &p, int len, int u0) const {
+        const bool low = p.window > 0 && u0 < len + t1 - p.window + 1 && u0 + kUnit > p.sinks;
+        return low || u0 + kUnit > (p.parents ? len : len + t0 + 1);
     }
 };
 
-__device__ Sight sight(const AttendPagedArgs &p, int b, int t, int len) {
-    Sight s;
-    if (p.parents) {
-        const int *const up = p.parents + static_cast<long long>(b) * p.T;
-        int depth = -1;
-        for (int a = t; a >= 0; ++depth) {
-            const int q = up[a];
-            if (q < -1 || q >= a) record_error(p.dev_err, kDevErrBounds);
-            a = q < a ? max(q, -1) : -1;
-        }
-        s.bits = 0;
-        int d = depth;
-        for (int a = t; a >= 0; --d) {
-            if (p.window == 0 || depth - d < p.window || len + d < p.sinks) s.bits |= 1ull << a;
-            const int q = up[a];
-            a = q < a ? max(q, -1) : -1;
-        }
-        s.tree = s.hi = len;
-        s.lo = p.window ? max(len + depth - p.window + 1, 0) : 0;
-    } else {
-        s.bits = 0;
-        s.hi = s.tree = len + t + 1;
-        s.lo = p.window ? max(len + t - p.window + 1, 0) : 0;
+// Every role of both CTAs walks the cluster's share, tile by tile.
+struct Walk {
+    long long lo, hi, pre;   // pre: the axis position of tile j of sequence b
+    int b, j, len, count;
+    int seq, i0, i1;         // the current part: its sequence and units [i0, i1) of the tile
+    int index;               // the tile's number in the sequence
+    Tile t;
+    __device__ __forceinline__ Walk(const PairParams &p, const PairBars *s) {
+        lo = s->lo, hi = s->hi, pre = s->pre, b = s->b, j = s->j;
+        len = count = 0;
+        if (b < p.B) count = tokens(p, b, len, false);
     }
-    s.head = min(p.sinks, s.lo);
-    return s;
+    __device__ __forceinline__ bool next(const PairParams &p) {
+        while (pre < hi) {
+            if (static_cast<long long>(j) * kM >= static_cast<long long>(count) * p.H) {
+                j = 0;
+                if (++b >= p.B) return false;
+                count = tokens(p, b, len, false);
+                continue;
+            }
+            t = Tile(p, j, len, count);
+            const long long base = pre + kStart;
+            const long long s0 = max(base, lo), s1 = min(base + t.n, hi);
+            seq = b, index = j;
+            pre = base + t.n;
+            ++j;
+            if (s1 > s0) {
+                i0 = static_cast<int>(s0 - base), i1 = static_cast<int>(s1 - base);
+                return true;
+            }
+        }
+        return false;
+    }
+    __device__ __forceinline__ int seq_len(const PairParams &p) const { return __ldg(p.lens + seq); }
+    __device__ __forceinline__ bool whole() const { return i0 == 0 && i1 == t.n; }
+    // A cluster has at most one part that starts before it and one that starts in it and ends after it.
+    __device__ __forceinline__ int slot(int cl) const { return 2 * cl + (i0 == 0 ? 1 : 0); }
+};
+
+// The cache rows that a token sees: [0, head), [lo, hi), and of the 64 from `hi` on those whose bit is set.
+struct Sight {
+    int head, lo, hi;
+    unsigned long long bits;
+    __device__ __forceinline__ Sight() {}
+    __device__ __forceinline__ Sight(const PairParams &p, int b, int t, int len) {
+        bits = 0;
+        int position = len + t;
+        hi = position + 1;
+        if (p.parents) {
+            const int *const up = p.parents + static_cast<long long>(b) * p.T;
+            const auto parent = [&](int a) {   // below a, so that every walk ends
+                const int q = __ldg(up + a);
+                if (q < -1 || q >= a) record_error(p.err, kDevErrBounds);
+                return q < -1 || q >= a ? -1 : q;
+            };
+            int depth = 0;
+            for (int a = parent(t); a >= 0; a = parent(a)) ++depth;
+            int d = depth;
+            for (int a = t; a >= 0; a = parent(a), --d)
+                if (p.window == 0 || depth - d < p.window || len + d < p.sinks) bits |= 1ull << a;
+            hi = len, position = len + depth;
+        }
+        lo = p.window > 0 ? max(position - p.window + 1, 0) : 0;
+        head = min(min(p.sinks, lo), hi);
+    }
+    // Rows u0 + 32 w .. + 31 as bits.
+    __device__ __forceinline__ uint32_t word(int u0, int w) const {
+        const int at = u0 + 32 * w;
+        const auto below = [&](int x) { return x <= at ? 0u : x - at >= 32 ? ~0u : (1u << (x - at)) - 1; };
+        uint32_t m = below(head) | (below(hi) & ~below(lo));
+        const int off = at - hi;
+        if (off >= 0) {
+            if (off < 64) m |= static_cast<uint32_t>(bits >> off);
+        } else if (off > -32) {
+            m |= static_cast<uint32_t>(bits << -off);
+        }
+        return m;
+    }
+};
+
+__device__ __forceinline__ void st_shared_f32(uint32_t addr, float v) {
+    asm volatile("st.shared.f32 [%0], %1;" ::"r"(addr), "f"(v) : "memory");
+}
+__device__ __forceinline__ float ld_shared_f32(uint32_t addr) {
+    float v;
+    asm volatile("ld.shared.f32 %0, [%1];" : "=f"(v) : "r"(addr) : "memory");
+    return v;
+}
+__device__ __forceinline__ float2 ld_shared_v2f(uint32_t addr) {
+    float2 v;
+    asm volatile("ld.shared.v2.f32 {%0, %1}, [%2];" : "=f"(v.x), "=f"(v.y) : "r"(addr) : "memory");
+    return v;
+}
+__device__ __forceinline__ void st_shared_v2f(uint32_t addr, float a, float b) {
+    asm volatile("st.shared.v2.f32 [%0], {%1, %2};" ::"r"(addr), "f"(a), "f"(b) : "memory");
 }
 
-__global__ void __launch_bounds__(256) attend_paged_simple_kernel(const AttendPagedArgs p) {
-    const int h = blockIdx.x % p.H, t = blockIdx.x / p.H % p.T, b = blockIdx.x / (p.H * p.T);
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    grid_dependency_wait();
-    const int len = p.lens[b], count = p.counts ? p.counts[b] : p.T;
-    const long long cap = static_cast<long long>(p.max_blocks) * p.bs;
-    if (len < 0 || count < 0 || count > p.T || static_cast<long long>(len) + count > cap) {
-        if (threadIdx.x == 0) record_error(p.dev_err, kDevErrBounds);
-        return;
-    }
-    if (t >= count) return;
-    const Sight s = sight(p, b, t, len);
-    const long long row = (static_cast<long long>(b) * p.T + t) * p.H + h;
-    const auto *q = static_cast<const __nv_bfloat16 *>(p.q_abs) + row * kR;
-    float qv[16], o[16] = {};
-    for (int i = 0; i < 16; ++i) qv[i] = __bfloat162float(q[lane * 16 + i]) * p.scale * kLog2e;
-    float m = -INFINITY, l = 0.f;
-    for (int u = warp; u < len + count; u += 8) {
-        if (!s.sees(u)) continue;
-        const int block = p.table[b * p.ld_table + u / p.bs];
-        float c[16] = {}, dot = 0.f;
-        if (block >= 0 && block < p.num_blocks) {
-            const auto *src = static_cast<const __nv_bfloat16 *>(p.pool) +
-                              (static_cast<long long>(block) * p.bs + u % p.bs) * p.ld_pool + lane * 16;
-            for (int i = 0; i < 16; ++i) c[i] = __bfloat162float(src[i]);
-        } else if (lane == 0) {
-            record_error(p.dev_err, kDevErrBounds);
+// Reductions over 128 values as 8 interleaved chains: short chains without many temporaries.
+template <typename F>
+__device__ __forceinline__ float reduce128(const float (&s)[4][32], F f) {
+    float m[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) m[i] = s[0][i];
+#pragma unroll
+    for (int k = 8; k < 128; ++k) m[k & 7] = f(m[k & 7], s[k >> 5][k & 31]);
+    return f(f(f(m[0], m[1]), f(m[2], m[3])), f(f(m[4], m[5]), f(m[6], m[7])));
+}
+
+// A row's query into TMEM: its packed bf16 pairs are its 32-bit words in memory order.  Warpgroup wg owns latent columns
+// [256 wg, 256 wg + 256), in two halves of 16 x 16 bytes.
+__device__ __forceinline__ void q_issue(const uint4 *src, bool valid, int half, uint4 (&v)[16]) {
+#pragma unroll
+    for (int i = 0; i < 16; ++i) v[i] = valid ? __ldg(src + half * 16 + i) : make_uint4(0, 0, 0, 0);
+}
+__device__ __forceinline__ void q_store(uint32_t taddr, int half, const uint4 (&v)[16]) {
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+        float w[32];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            w[4 * i + 0] = __uint_as_float(v[8 * k + i].x);
+            w[4 * i + 1] = __uint_as_float(v[8 * k + i].y);
+            w[4 * i + 2] = __uint_as_float(v[8 * k + i].z);
+            w[4 * i + 3] = __uint_as_float(v[8 * k + i].w);
         }
-        for (int i = 0; i < 16; ++i) dot = fmaf(qv[i], c[i], dot);
-        for (int off = 16; off; off >>= 1) dot += __shfl_xor_sync(0xffffffffu, dot, off);
-        const float top = fmaxf(m, dot), f = exp2f(m - top), w = exp2f(dot - top);
-        for (int i = 0; i < 16; ++i) o[i] = o[i] * f + w * c[i];
-        l = l * f + w;
-        m = top;
-    }
-    __shared__ float sm[8], sl[8], so[8][kR], lat[kR];
-    if (lane == 0) sm[warp] = m, sl[warp] = l;
-    for (int i = 0; i < 16; ++i) so[warp][lane * 16 + i] = o[i];
-    __syncthreads();
-    float top = -INFINITY, all = 0.f;
-    for (int w = 0; w < 8; ++w) top = fmaxf(top, sm[w]);
-    for (int w = 0; w < 8; ++w) all += sl[w] > 0.f || sl[w] != sl[w] ? sl[w] * exp2f(sm[w] - top) : 0.f;
-    for (int i = threadIdx.x; i < kR; i += 256) {
-        float v = 0.f;
-        for (int w = 0; w < 8; ++w) v += sl[w] > 0.f || sl[w] != sl[w] ? so[w][i] * exp2f(sm[w] - top) : 0.f;
-        lat[i] = v / all;
-    }
-    __syncthreads();
-    for (int v = warp; v < kDV; v += 8) {
-        const auto *w = static_cast<const __nv_bfloat16 *>(p.w_uv) + (static_cast<long long>(h) * kDV + v) * kR;
-        float x = 0.f;
-        for (int i = lane; i < kR; i += 32) x = fmaf(lat[i], __bfloat162float(w[i]), x);
-        for (int off = 16; off; off >>= 1) x += __shfl_xor_sync(0xffffffffu, x, off);
-        if (lane == 0) {
-            if (p.gate) x /= 1.f + __expf(-__bfloat162float(static_cast<const __nv_bfloat16 *>(p.gate)[row * kDV + v]));
-            static_cast<__nv_bfloat16 *>(p.out)[row * kDV + v] = __float2bfloat16(x);
-        }
+        tmem_st32(taddr + (half * 2 + k) * 32, w);
     }
 }
+
+// Not finite bf16 halves of a word to zero.
+__device__ __forceinline__ uint32_t finite_halves(uint32_t w) {
+    if ((w & 0x7F80u) == 0x7F80u) w &= 0xFFFF0000u;
+    if ((w & 0x7F800000u) == 0x7F800000u) w &= 0xFFFFu;
+    return w;
+}
+
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
+    attend_pair_kernel(const __grid_constant__ CUtensorMap tm_s, const __grid_constant__ CUtensorMap tm_v,
+                       const PairParams p) {
+    extern __shared__ uint8_t smem_raw[];
+    const uint32_t raw = smem_u32(smem_raw);
+    const uint32_t base = (raw + 1023u) & ~1023u;
+    PairBars *const bars = reinterpret_cast<PairBars *>(smem_raw + (base - raw) + BARS);
+    volatile int *const abort_flag = &bars->abort;
+    const auto B_ = [](uint64_t &b) { return smem_u32(&b); };
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const uint32_t rank = cluster_ctarank();
+    const int G = static_cast<int>(gridDim.x >> 1), cl = static_cast<int>(blockIdx.x >> 1);
+
+    if (threadIdx.x == 0) {
+        mbar_init(B_(bars->q_ready), 256);
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(B_(bars->s_full[i]), 1);
+            mbar_init(B_(bars->s_free[i]), 128);
+            mbar_init(B_(bars->m_ready[i]), 128);
+        }
+        for (int i = 0; i < kSStages; ++i) {
+            mbar_init(B_(bars->sc_full[i]), 2);
+            mbar_init(B_(bars->sc_empty[i]), 1);
+        }
+        for (int i = 0; i < kPBufs; ++i) {
+            mbar_init(B_(bars->p_free[i]), 1);
+            mbar_init(B_(bars->p_full[i]), 1);
+            mbar_init(B_(bars->pv_done[i]), 1);
+            mbar_init(B_(bars->info_read[i]), 256);
+        }
+        for (int i = 0; i < kVStages; ++i) {
+            mbar_init(B_(bars->v_full[i]), 1);
+            mbar_init(B_(bars->v_empty[i]), 1);
+            mbar_init(B_(bars->v_clean[i]), 256);
+        }
+        mbar_init(B_(bars->rescaled), 256);
+        mbar_init(B_(bars->drained), 1);
+        bars->abort = 0;
+        fence_mbar_init();
+    }
+    if (warp == 1) {
+        tmem_alloc(smem_u32(&bars->tmem_base), 512);
+        tmem_relinquish();
+    }
+    tc_fence_before();
+    cluster_sync_all();   // both CTAs' barriers exist before any remote arrival or copy
+    tc_fence_after();
+    const uint32_t tmem = bars->tmem_base;
+    grid_dependency_wait();
+    grid_launch_dependents();   // the second kernel may take SMs as clusters finish; it waits for the whole grid
+
+    // The axis: thread i adds up its part of the tiles; the one that holds the share's start finds the tile there.
+    {
+        const long long all = static_cast<long long>(p.B) * p.tiles;
+        const long long per = (all + kThreads - 1) / kThreads;
+        const long long g0 = min(threadIdx.x * per, all), g1 = min(g0 + per, all);
+        const auto units = [&](long long g, bool report) {
+            const int b = static_cast<int>(g / p.tiles), j = static_cast<int>(g - static_cast<long long>(b) * p.tiles);
+            int len;
+            const int count = tokens(p, b, len, report);
+            return static_cast<long long>(j) * kM < static_cast<long long>(count) * p.H
+                       ? kStart + Tile(p, j, len, count).n : 0;
+        };
+        long long sum = 0;
+        for (long long g = g0; g < g1; ++g) sum += units(g, cl == 0 && rank == 0);
+        long long incl = sum;
+#pragma unroll
+        for (int off = 1; off < 32; off <<= 1) {
+            const long long v = __shfl_up_sync(0xffffffffu, incl, off);
+            if (lane >= off) incl += v;
+        }
+        if (lane == 31) bars->warp_sum[warp] = incl;
+        __syncthreads();
+        long long before = 0, total = 0;
+        for (int w = 0; w < kThreads / 32; ++w) {
+            if (w < warp) before += bars->warp_sum[w];
+            total += bars->warp_sum[w];
+        }
+        // no share is empty but those of the clusters that are too many: a tile's parts lie in successive clusters
+        const long long n_shares = min(static_cast<long long>(G), total);
+        const long long lo = cl < n_shares ? total * cl / n_shares : 0, hi = cl < n_shares ? total * (cl + 1) / n_shares : 0;
+        long long pre = before + incl - sum;
+        if (threadIdx.x == 0) bars->lo = lo, bars->hi = hi, bars->b = p.B, bars->pre = hi;
+        __syncthreads();
+        if (lo < hi && pre <= lo && lo < pre + sum) {
+            for (long long g = g0; g < g1; ++g) {
+                const long long n = units(g, false);
+                if (lo < pre + n) {
+                    bars->b = static_cast<int>(g / p.tiles);
+                    bars->j = static_cast<int>(g - bars->b * static_cast<long long>(p.tiles));
+                    bars->pre = pre;
+                    break;
+                }
+                pre += n;
+            }
+        }
+        __syncthreads();
+    }
+
+    // The pool row of cache row u (u % 32 == 0) of a sequence, or one past the pool, which reads as zeros.
+    const auto pool_row = [&](int seq, int u) {
+        const int j = u / p.bs, block = __ldg(p.table + seq * p.ld_table + j);
+        if (block < 0 || block >= p.num_blocks) {
+            record_error(p.err, kDevErrBounds);
+            return max(p.num_blocks * p.bs, 1);
+        }
+        return block * p.bs + (u - j * p.bs);
+    };
+
+    if (warp < 4) {
+        regs_release<kRegsCtl>();
+        Walk w(p, bars);
+        if (rank == 0) {
+            // =========================================================== score CTA
+            if ((warp == 0 || warp == 3) && lane == 0) {
+                // ---- TMA producers: rows [64 half, 64 half + 64) of each stage
+                const int half = warp == 0 ? 0 : 1;
+                tma_prefetch_desc(&tm_s);
+                uint32_t it = 0;
+                bool ok = true;
+                while (ok && w.next(p)) {
+                    for (int i = w.i0; ok && i < w.i1; ++i) {
+                        const int u = w.t.row0(i) + half * 64;
+                        const int row = u < w.t.end ? pool_row(w.seq, u) : -1;
+                        for (int kc = 0; kc < 8; ++kc, ++it) {
+                            const int st = it % kSStages;
+                            if (it >= kSStages &&
+                                !(ok = mbar_wait(B_(bars->sc_empty[st]), (it / kSStages - 1) & 1, p.err, abort_flag)))
+                                break;
+                            const uint32_t full = B_(bars->sc_full[st]);
+                            if (row < 0) {   // past the last row that is seen: masked, whatever the stage holds
+                                mbar_arrive(full);
+                                continue;
+                            }
+                            mbar_arrive_expect_tx(full, kStage / 2);
+                            tma_load_2d(base + st * kStage + half * (kStage / 2), &tm_s, full, kc * 64, row);
+                        }
+                    }
+                }
+                if (!ok) *abort_flag = 1;
+                // no load may still be landing when the CTA exits
+                for (uint32_t k = it > kSStages ? it - kSStages : 0; k < it; ++k)
+                    mbar_wait(B_(bars->sc_full[k % kSStages]), (k / kSStages) & 1, p.err, nullptr, kLandNs);
+            } else if (warp == 1 && lane == 0) {
+                // ---- MMA issuer
+                const uint64_t ring = make_smem_desc(base, 16, 1024);
+                uint32_t it = 0, jb = 0, nseg = 0;
+                bool ok = true;
+                while (ok && w.next(p)) {
+                    if (!(ok = mbar_wait(B_(bars->q_ready), nseg & 1, p.err, abort_flag))) break;
+                    ++nseg;
+                    for (int i = w.i0; ok && i < w.i1; ++i, ++jb) {
+                        if (jb >= 2 && !(ok = mbar_wait(B_(bars->s_free[jb & 1]), (jb / 2 - 1) & 1, p.err, abort_flag))) break;
+                        tc_fence_after();
+                        const uint32_t d = tmem + S_COL + (jb & 1) * 128;
+                        for (int kc = 0; kc < 8; ++kc, ++it) {
+                            const int st = it % kSStages;
+                            if (!(ok = mbar_wait(B_(bars->sc_full[st]), (it / kSStages) & 1, p.err, abort_flag))) break;
+                            tc_fence_after();
+                            const uint64_t bd = desc_add(ring, st * kStage);
+#pragma unroll
+                            for (int kk = 0; kk < 4; ++kk)
+                                umma_bf16_tmem_a(d, tmem + (kc * 4 + kk) * 8, desc_add(bd, kk * 32), kIdescS, (kc | kk) != 0);
+                            umma_commit(B_(bars->sc_empty[st]));
+                        }
+                        if (ok) umma_commit(B_(bars->s_full[jb & 1]));
+                    }
+                }
+                if (!ok) *abort_flag = 1;
+            }
+        } else {
+            // =========================================================== value CTA
+            if ((warp == 0 || warp == 3) && lane == 0) {
+                // ---- TMA producers: a unit is 8 stages, latent half i >> 2, row quarter i & 3; each takes one half of
+                // the rows
+                const int half = warp == 0 ? 0 : 1;
+                tma_prefetch_desc(&tm_v);
+                uint32_t it = 0;
+                bool ok = true;
+                while (ok && w.next(p)) {
+                    for (int i = w.i0; ok && i < w.i1; ++i, it += 8) {
+                        const int u = w.t.row0(i) + half * 64;
+                        const int row = u < w.t.end ? pool_row(w.seq, u) : -1;
+                        for (int k = 0; k < 4; ++k) {
+                            const uint32_t s = it + (k >> 1) * 4 + half * 2 + (k & 1);
+                            const int st = s % kVStages;
+                            if (s >= kVStages &&
+                                !(ok = mbar_wait(B_(bars->v_empty[st]), (s / kVStages - 1) & 1, p.err, abort_flag)))
+                                break;
+                            const uint32_t full = B_(bars->v_full[st]);
+                            if (row < 0) {
+                                mbar_arrive(full);
+                                continue;
+                            }
+                            mbar_arrive_expect_tx(full, kStage);
+                            tma_load_3d(base + V_RING + st * kStage, &tm_v, full, 0, row + (k & 1) * kVRows, (k >> 1) * 4);
+                        }
+                    }
+                }
+                if (!ok) *abort_flag = 1;
+                for (uint32_t k = it > kVStages ? it - kVStages : 0; k < it; ++k)
+                    mbar_wait(B_(bars->v_full[k % kVStages]), (k / kVStages) & 1, p.err, nullptr, kLandNs);
+            } else if (warp == 1) {
+                // ---- MMA warp; lane 0 issues
+                const bool leader = lane == 0;
+                const auto wait_all = [&](uint64_t &bar, uint32_t parity, bool cluster) {
+                    return __all_sync(0xffffffffu, cluster ? mbar_wait<true>(B_(bar), parity, p.err, abort_flag)
+                                                           : mbar_wait(B_(bar), parity, p.err, abort_flag));
+                };
+                const uint64_t pdesc = make_smem_desc(base, 16, 1024), ring = make_smem_desc(base + V_RING, kVSlab, 1024);
+                uint32_t it = 0, jj = 0, nfix = 0, nseg = 0, cleaned = 0;   // cleaned: a phase bit per stage
+                bool ok = true;
+                while (ok && w.next(p)) {
+                    const int len = w.seq_len(p);
+                    const uint32_t bytes = 2u * ((w.t.rows + 7) & ~7) * 128u + kInfo;
+                    for (int i = w.i0; ok && i < w.i1; ++i, ++jj) {
+                        const uint32_t pb = jj % kPBufs;
+                        const bool first = i == w.i0, mixed = w.t.mixed(p, len, w.t.row0(i));
+                        if (leader) mbar_arrive_expect_tx(B_(bars->p_full[pb]), bytes);
+                        if (!(ok = wait_all(bars->p_full[pb], (jj / kPBufs) & 1, true))) break;
+                        // the accumulator of the part before has been drained
+                        if (first && nseg > 0 && !(ok = wait_all(bars->drained, (nseg - 1) & 1, false))) break;
+                        // rows whose maximum grew need their accumulator rescaled before this unit's product
+                        const uint32_t info = base + pb * kPUnit + 2 * kSlab;
+                        bool grew = false;
+#pragma unroll
+                        for (int k = 0; k < 4; ++k) grew |= ld_shared_f32(info + (lane + 32 * k) * 8) != 1.f;
+                        if (!first && __any_sync(0xffffffffu, grew)) {
+                            if (!(ok = wait_all(bars->rescaled, nfix & 1, false))) break;
+                            ++nfix;
+                        }
+                        for (int k = 0; ok && k < 8; ++k, ++it) {
+                            const int st = it % kVStages;
+                            if (!(ok = wait_all(bars->v_full[st], (it / kVStages) & 1, false))) break;
+                            if (mixed) {
+                                if (!(ok = wait_all(bars->v_clean[st], (cleaned >> st) & 1, false))) break;
+                                cleaned ^= 1u << st;
+                            }
+                            tc_fence_after();
+                            if (leader) {
+                                const uint64_t a = desc_add(pdesc, pb * kPUnit + ((k >> 1) & 1) * kSlab + (k & 1) * 64);
+                                const uint64_t bd = desc_add(ring, st * kStage);
+                                const uint32_t d = tmem + (k >> 2) * 256;
+                                umma_bf16(d, a, bd, kIdescO, !first || (k & 3) != 0);
+                                umma_bf16(d, desc_add(a, 32), desc_add(bd, 2048), kIdescO, 1);
+                                umma_commit(B_(bars->v_empty[st]));
+                            }
+                            __syncwarp();
+                        }
+                        if (ok && leader) umma_commit(B_(bars->pv_done[pb]));
+                    }
+                    ++nseg;
+                }
+                if (!ok && leader) *abort_flag = 1;
+            } else if (warp == 2 && lane == 0) {
+                // ---- relay: a P buffer is free again once its product completed and its info was read
+                uint32_t jj = 0;
+                bool ok = true;
+                while (ok && w.next(p)) {
+                    for (int i = w.i0; i < w.i1; ++i, ++jj) {
+                        const uint32_t pb = jj % kPBufs;
+                        if (!mbar_wait(B_(bars->pv_done[pb]), (jj / kPBufs) & 1, p.err, abort_flag) ||
+                            !mbar_wait(B_(bars->info_read[pb]), (jj / kPBufs) & 1, p.err, abort_flag)) {
+                            *abort_flag = 1;
+                            ok = false;
+                            break;
+                        }
+                        mbar_arrive_remote(B_(bars->p_free[pb]), 0);
+                    }
+                }
+            }
+        }
+    } else {
+        regs_acquire<kRegsMath>();
+        Walk w(p, bars);
+        const int wg = (warp - 4) >> 2, row = (warp & 3) * 32 + lane;   // row of the tile, TMEM lane
+        const uint32_t trow = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16);
+        const bool first_thread = (threadIdx.x & 127) == 0;
+        if (rank == 0) {
+            // ---- softmax: warpgroup wg takes every other unit
+            const uint32_t ptile = base + S_PST + wg * kPUnit, info = ptile + 2 * kSlab;
+            const auto query = [&](const Walk &v, bool &valid) {
+                valid = row < v.t.rows;
+                const long long r0 = static_cast<long long>(v.seq) * p.T * p.H + static_cast<long long>(v.index) * kM;
+                return reinterpret_cast<const uint4 *>(p.q_abs + (r0 + (valid ? row : 0)) * kR) + wg * 32;
+            };
+            uint32_t jb = 0;
+            bool ok = true;
+            bool more = w.next(p);
+            if (more) {
+                bool valid;
+                const uint4 *const src = query(w, valid);
+                uint4 v[16];
+#pragma unroll 1
+                for (int half = 0; half < 2; ++half) {
+                    q_issue(src, valid, half, v);
+                    q_store(trow + wg * 128, half, v);
+                }
+                tmem_wait_st();
+                tc_fence_before();
+                mbar_arrive(B_(bars->q_ready));
+            }
+            // A failed wait is voted on at the next barrier of the warpgroup, which no warp leaves alone.
+            bool fail = false;
+            const auto wait_warp = [&](uint64_t &bar, uint32_t parity) {
+                return __any_sync(0xffffffffu, fail || !mbar_wait(B_(bar), parity, p.err, abort_flag));
+            };
+            while (ok && more) {
+                const int len = w.seq_len(p);
+                const Sight sight(p, w.seq, min((w.index * kM + row) / p.H, w.t.t1), len);
+                const int i0 = w.i0, i1 = w.i1, slot = w.slot(cl), rows = w.t.rows;
+                const Tile tile = w.t;
+                const bool whole = w.whole();
+                more = w.next(p);   // the next part's query goes into TMEM after this one's last product
+                float m_mine = -INFINITY, l = 0.f;
+                for (int i = i0; ok && i < i1; ++i, ++jb) {
+                    const bool mine = (jb & 1) == static_cast<uint32_t>(wg), last = i == i1 - 1;
+                    if (!mine && !(last && more)) continue;
+                    if (last && more) {
+                        bool valid;
+                        const uint4 *const src = query(w, valid);
+                        uint4 v[16];   // half the query rides across the wait
+                        q_issue(src, valid, 0, v);
+                        fail = wait_warp(bars->s_full[jb & 1], (jb >> 1) & 1);
+                        tc_fence_after();
+                        q_store(trow + wg * 128, 0, v);
+                        q_issue(src, valid, 1, v);
+                        q_store(trow + wg * 128, 1, v);
+                        tmem_wait_st();
+                        tc_fence_before();
+                        mbar_arrive(B_(bars->q_ready));
+                        if (!mine) continue;
+                    } else {
+                        fail = wait_warp(bars->s_full[jb & 1], (jb >> 1) & 1);
+                    }
+                    tc_fence_after();
+                    float s[4][32];
+#pragma unroll
+                    for (int c4 = 0; c4 < 4; ++c4) tmem_ld32(trow + S_COL + (jb & 1) * 128 + c4 * 32, s[c4]);
+                    tmem_wait_ld();
+                    tc_fence_before();
+                    mbar_arrive(B_(bars->s_free[jb & 1]));
+                    // The scale multiplies inside the exponent: the largest of c s is c max(s) for c >= 0, c min(s)
+                    // otherwise.  Masked units multiply first.
+                    float mul = p.scale_log2;
+                    const int u0 = tile.row0(i);
+                    if (tile.mixed(p, len, u0)) {
+                        mul = 1.f;
+#pragma unroll
+                        for (int c4 = 0; c4 < 4; ++c4) {
+                            const uint32_t seen = sight.word(u0, c4);
+#pragma unroll
+                            for (int k = 0; k < 32; ++k) {
+                                // an infinite score's row gives NaN, as its product with the weight 0 would
+                                const float x = fabsf(s[c4][k]) == INFINITY ? NAN : s[c4][k] * p.scale_log2;
+                                s[c4][k] = (seen >> k) & 1 ? x : -INFINITY;
+                            }
+                        }
+                    }
+                    const float mx = mul >= 0.f ? mul * reduce128(s, [](float a, float b) { return fmaxf(a, b); })
+                                                : mul * reduce128(s, [](float a, float b) { return fminf(a, b); });
+                    // the running maximum of the unit before, from the other warpgroup
+                    if (jb > 0) fail = wait_warp(bars->m_ready[wg ^ 1], ((jb - 1) >> 1) & 1);
+                    const float m_old = i == i0 ? -INFINITY : ld_shared_f32(base + S_MAX + (wg ^ 1) * kM * 4 + row * 4);
+                    float m = m_old, factor = 1.f;
+                    if (mx > m_old + kRescaleLog2) {
+                        factor = fast_exp2(m_old - mx);
+                        m = mx;
+                    }
+                    st_shared_f32(base + S_MAX + wg * kM * 4 + row * 4, m);
+                    mbar_arrive(B_(bars->m_ready[wg]));
+                    const float neg_m = m == -INFINITY ? 0.f : -m;
+#pragma unroll
+                    for (int c4 = 0; c4 < 4; ++c4)
+#pragma unroll
+                        for (int k = 0; k < 32; ++k) s[c4][k] = fast_exp2(fmaf(s[c4][k], mul, neg_m));
+                    l = (m == m_mine ? l : l * fast_exp2(m_mine - m)) + reduce128(s, [](float a, float b) { return a + b; });
+                    m_mine = m;
+                    if (last && !whole && row < rows) p.ws_m[static_cast<size_t>(slot) * kM + row] = m;
+
+                    // the staging unit is free once this warpgroup's copy before has read it
+                    if (first_thread) bulk_wait_read_all();
+                    if (named_bar_or(2 + wg, 128, fail)) { ok = false; break; }
+#pragma unroll
+                    for (int c4 = 0; c4 < 4; ++c4)
+#pragma unroll
+                        for (int k = 0; k < 4; ++k) {
+                            const float *v = &s[c4][8 * k];
+                            st_shared_v4(ptile + (c4 >> 1) * kSlab + sw128_offset(row, (c4 & 1) * 4 + k),
+                                         pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]), pack_bf16x2(v[4], v[5]),
+                                         pack_bf16x2(v[6], v[7]));
+                        }
+                    st_shared_v2f(info + row * 8, factor, l);
+                    fence_proxy_async_smem();
+                    named_bar_sync(2 + wg, 128);
+                    if (first_thread) {
+                        const uint32_t pb = jb % kPBufs;
+                        if (jb >= kPBufs)
+                            fail = !mbar_wait<true>(B_(bars->p_free[pb]), (jb / kPBufs - 1) & 1, p.err, abort_flag);
+                        if (!fail) {
+                            const uint32_t bar = mapa_shared(B_(bars->p_full[pb]), 1);
+                            const uint32_t dst = mapa_shared(base + pb * kPUnit, 1);
+                            if (rows == kM) {
+                                bulk_copy_s2cluster(dst, ptile, kPUnit, bar);
+                            } else {   // whole groups of 8 rows: the others' products are not read
+                                const uint32_t n = static_cast<uint32_t>((rows + 7) & ~7) * 128;
+                                bulk_copy_s2cluster(dst, ptile, n, bar);
+                                bulk_copy_s2cluster(dst + kSlab, ptile + kSlab, n, bar);
+                                bulk_copy_s2cluster(dst + 2 * kSlab, info, kInfo, bar);
+                            }
+                            bulk_commit_group();
+                        }
+                    }
+                    __syncwarp();
+                }
+            }
+            if (first_thread) bulk_wait_all();
+            if (!ok || fail) *abort_flag = 1;
+        } else {
+            // ---- rescaling, cleaning and drain: thread = TMEM lane, warpgroup wg has latent columns [256 wg, 256 wg + 256)
+            uint32_t jj = 0, it = 0;
+            bool ok = true, fail;
+            while (ok && w.next(p)) {
+                const int len = w.seq_len(p);
+                float l_old = 0.f, l_new = 0.f;   // the sums of the two warpgroups of the score CTA
+                for (int i = w.i0; i < w.i1; ++i, ++jj, it += 8) {
+                    const uint32_t pb = jj % kPBufs;
+                    fail = !mbar_wait<true>(B_(bars->p_full[pb]), (jj / kPBufs) & 1, p.err, abort_flag);
+                    if (named_bar_or(4, 256, fail)) { ok = false; break; }
+                    const float2 fl = ld_shared_v2f(base + pb * kPUnit + 2 * kSlab + row * 8);
+                    mbar_arrive(B_(bars->info_read[pb]));
+                    l_old = i == w.i0 ? 0.f : l_new * fl.x;
+                    l_new = fl.y;
+                    if (named_bar_or(4, 256, i > w.i0 && fl.x != 1.f)) {
+                        const uint32_t prev = jj - 1;
+                        fail = !mbar_wait(B_(bars->pv_done[prev % kPBufs]), (prev / kPBufs) & 1, p.err, abort_flag);
+                        if (named_bar_or(4, 256, fail)) { ok = false; break; }
+                        tc_fence_after();
+                        if (__any_sync(0xffffffffu, fl.x != 1.f)) {
+#pragma unroll 1
+                            for (int cc = 0; cc < 8; ++cc) {
+                                float v[32];
+                                const uint32_t ta = trow + wg * 256 + cc * 32;
+                                tmem_ld32(ta, v);
+                                tmem_wait_ld();
+#pragma unroll
+                                for (int k = 0; k < 32; ++k) v[k] *= fl.x;
+                                tmem_st32(ta, v);
+                            }
+                            tmem_wait_st();
+                        }
+                        tc_fence_before();
+                        mbar_arrive(B_(bars->rescaled));
+                    }
+                    if (w.t.mixed(p, len, w.t.row0(i))) {
+                        for (int k = 0; k < 8; ++k) {
+                            const uint32_t s = it + k, st = s % kVStages;
+                            fail = !mbar_wait(B_(bars->v_full[st]), (s / kVStages) & 1, p.err, abort_flag);
+                            if (fail) break;
+                            const uint32_t at = base + V_RING + st * kStage + (threadIdx.x - 128) * 16;
+#pragma unroll
+                            for (int q = 0; q < 4; ++q) {
+                                const uint4 v = ld_shared_v4(at + q * 4096);
+                                const uint4 c = make_uint4(finite_halves(v.x), finite_halves(v.y), finite_halves(v.z),
+                                                           finite_halves(v.w));
+                                if (c.x != v.x || c.y != v.y || c.z != v.z || c.w != v.w)
+                                    st_shared_v4(at + q * 4096, c.x, c.y, c.z, c.w);
+                            }
+                            fence_proxy_async_smem();
+                            mbar_arrive(B_(bars->v_clean[st]));
+                        }
+                        if (named_bar_or(4, 256, fail)) { ok = false; break; }
+                    }
+                }
+                if (!ok) break;
+                // the part's end
+                const uint32_t prev = jj - 1;
+                fail = !mbar_wait(B_(bars->pv_done[prev % kPBufs]), (prev / kPBufs) & 1, p.err, abort_flag);
+                if (named_bar_or(4, 256, fail)) { ok = false; break; }
+                tc_fence_after();
+                const bool whole = w.whole(), valid = row < w.t.rows;
+                const float sum = l_old + l_new, inv = 1.f / sum;
+                const long long g = static_cast<long long>(w.seq) * p.T * p.H + static_cast<long long>(w.index) * kM + row;
+                const size_t part = static_cast<size_t>(w.slot(cl)) * kM + row;
+#pragma unroll 1
+                for (int cc = 0; cc < 8; ++cc) {
+                    float v[32];
+                    tmem_ld32(trow + wg * 256 + cc * 32, v);
+                    tmem_wait_ld();
+                    if (!valid) continue;
+                    if (whole) {   // the operand of the product with W_UV: bf16, as in the prefill and the other decodes
+                        uint4 o[4];
+#pragma unroll
+                        for (int q = 0; q < 4; ++q)
+                            o[q] = make_uint4(pack_bf16x2(v[8 * q] * inv, v[8 * q + 1] * inv),
+                                              pack_bf16x2(v[8 * q + 2] * inv, v[8 * q + 3] * inv),
+                                              pack_bf16x2(v[8 * q + 4] * inv, v[8 * q + 5] * inv),
+                                              pack_bf16x2(v[8 * q + 6] * inv, v[8 * q + 7] * inv));
+                        __nv_bfloat16 *const dst = p.ws_rows + g * kR + wg * 256 + cc * 32;
+                        st_global_32B(dst, o[0], o[1]);
+                        st_global_32B(dst + 16, o[2], o[3]);
+                    } else {
+                        float *const dst = p.ws_o + part * kR + wg * 256 + cc * 32;
+#pragma unroll
+                        for (int q = 0; q < 4; ++q) {
+                            const uint32_t *x = reinterpret_cast<const uint32_t *>(&v[8 * q]);
+                            st_global_32B(dst + 8 * q, make_uint4(x[0], x[1], x[2], x[3]), make_uint4(x[4], x[5], x[6], x[7]));
+                        }
+                    }
+                }
+                if (wg == 0 && valid && !whole) p.ws_l[part] = sum;
+                if (threadIdx.x == 128) {
+                    int2 *const tile = p.ws_tile + static_cast<long long>(w.seq) * p.tiles + w.index;
+                    if (w.i0 == 0) tile->x = cl;
+                    if (w.i1 == w.t.n) tile->y = cl;
+                }
+                tc_fence_before();
+                named_bar_sync(4, 256);
+                if (threadIdx.x == 128) mbar_arrive(B_(bars->drained));
+            }
+            if (!ok) *abort_flag = 1;
+        }
+    }
+
+    __syncwarp();
+    tc_fence_before();
+    __syncthreads();
+    if (warp == 1) tmem_dealloc(tmem, 512);
+    cluster_sync_all();   // the partner no longer touches this CTA's shared memory or barriers
+}
+
+// ----------------------------------------------------------------------------- join, W_UV, gate
+// One CTA per (head, kRows new tokens): o_lat rows into a swizzled tile (whole tiles' as they are, parts joined by the
+// log-sum-exp rule), times W_UV[h]^T, streamed in four chunks of 128 latent columns, then the gate.
+constexpr int kUpThreads = 512;
+template <int kRows>
+struct Up {
+    static constexpr uint32_t kASlab = kRows * 128;              // o_lat [kRows x 64 latent columns]
+    static constexpr uint32_t kA = 7 * kASlab + kSlab;           // an M = 128 operand read of the last slab stays inside
+    static constexpr uint32_t kWStage = 2 * kSlab;               // W_UV[h] [128 x 128 latent columns]
+    static constexpr uint32_t kBars = kA + 2 * kWStage;
+    static constexpr uint32_t kSmem = kBars + 64 + 1024;
+};
+
+struct UpParams {
+    const int *lens, *counts;
+    const __nv_bfloat16 *ws_rows;
+    const float *ws_o, *ws_m, *ws_l;
+    const int2 *ws_tile;
+    const __nv_bfloat16 *gate;
+    __nv_bfloat16 *out;
+    int *err;
+    int B, T, H, tiles, bs, max_blocks;
+};
+
+template <int kRows>
+__global__ void __launch_bounds__(kUpThreads, kRows == 32 ? 2 : 1)
+    attend_up_kernel(const __grid_constant__ CUtensorMap tm_w, const UpParams p) {
+    using L = Up<kRows>;
+    extern __shared__ uint8_t smem_raw[];
+    const uint32_t raw = smem_u32(smem_raw);
+    const uint32_t base = (raw + 1023u) & ~1023u;
+    uint64_t *const w_full = reinterpret_cast<uint64_t *>(smem_raw + (base - raw) + L::kBars);   // [2]
+    uint64_t *const w_empty = w_full + 2;                                                         // [2]
+    uint64_t *const mma_done = w_full + 4;
+    uint32_t *const tmem_slot = reinterpret_cast<uint32_t *>(w_full + 5);
+    __shared__ int2 s_tile[kRows];   // first and last cluster of each row's tile; {-1, .}: not a token
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int h = blockIdx.x % p.H;
+    const long long m0 = static_cast<long long>(blockIdx.x / p.H) * kRows;   // first token, counted over [B, T]
+
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < 5; ++i) mbar_init(smem_u32(w_full + i), 1);
+        fence_mbar_init();
+    }
+    if (warp == 0) {
+        tmem_alloc(smem_u32(tmem_slot), 128);
+        tmem_relinquish();
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = *tmem_slot;
+    const auto load_w = [&](int k) {   // latent columns [128 k, 128 k + 128) of W_UV[h] into stage k % 2
+        const uint32_t bar = smem_u32(w_full + (k & 1));
+        mbar_arrive_expect_tx(bar, L::kWStage);
+        for (int sl = 0; sl < 2; ++sl)
+            tma_load_2d(base + L::kA + (k & 1) * L::kWStage + sl * kSlab, &tm_w, bar, k * 128 + sl * 64, h * kDV);
+    };
+    // the pair kernel launches this one after its own wait: what the call was given may be read already
+    if (threadIdx.x == 0) {
+        tma_prefetch_desc(&tm_w);
+        load_w(0);
+        load_w(1);
+    }
+    grid_dependency_wait();
+    if (threadIdx.x < kRows) {
+        const long long m = m0 + threadIdx.x;
+        const int b = static_cast<int>(m / p.T), t = static_cast<int>(m - static_cast<long long>(b) * p.T);
+        int2 tile = make_int2(-1, -1);
+        if (b < p.B) {
+            int len;
+            if (t < tokens(p, b, len, false))
+                tile = p.ws_tile[static_cast<long long>(b) * p.tiles + (static_cast<long long>(t) * p.H + h) / kM];
+        }
+        s_tile[threadIdx.x] = tile;
+    }
+    __syncthreads();
+    for (int i = warp; i < kRows; i += kUpThreads / 32) {   // a warp per row, 16 latent columns per lane
+        const int2 tile = s_tile[i];
+        const long long row = (m0 + i) * p.H + h;
+        uint4 v[2] = {};
+        if (tile.x >= 0 && tile.x == tile.y) {
+            ld_global_32B(p.ws_rows + row * kR + lane * 16, v[0], v[1]);
+        } else if (tile.x >= 0) {
+            const long long m = m0 + i, b = m / p.T;
+            const int r = static_cast<int>(((m - b * p.T) * p.H + h) % kM);   // the tile's row
+            float o[16], M = -INFINITY, sum = 0.f;
+#pragma unroll
+            for (int k = 0; k < 16; ++k) o[k] = 0.f;
+            for (int c = tile.x; c <= tile.y; ++c) {   // the first cluster's part starts the tile, the others go on with it
+                const size_t part = static_cast<size_t>(2 * c + (c == tile.x ? 1 : 0)) * kM + r;
+                const float m_c = p.ws_m[part], l_c = p.ws_l[part];
+                const float top = fmaxf(M, m_c);
+                const float f = M == top ? 1.f : fast_exp2(M - top), g = m_c == top ? 1.f : fast_exp2(m_c - top);
+                M = top;
+                sum = sum * f + l_c * g;
+                const float4 *const src = reinterpret_cast<const float4 *>(p.ws_o + part * kR + lane * 16);
+#pragma unroll
+                for (int q = 0; q < 4; ++q) {
+                    const float4 x = src[q];
+                    o[4 * q] = o[4 * q] * f + x.x * g, o[4 * q + 1] = o[4 * q + 1] * f + x.y * g;
+                    o[4 * q + 2] = o[4 * q + 2] * f + x.z * g, o[4 * q + 3] = o[4 * q + 3] * f + x.w * g;
+                }
+            }
+            const float inv = 1.f / sum;
+            uint32_t x[8];
+#pragma unroll
+            for (int k = 0; k < 8; ++k) x[k] = pack_bf16x2(o[2 * k] * inv, o[2 * k + 1] * inv);
+            v[0] = make_uint4(x[0], x[1], x[2], x[3]), v[1] = make_uint4(x[4], x[5], x[6], x[7]);
+        }
+        const uint32_t slab = base + (lane >> 2) * L::kASlab;
+#pragma unroll
+        for (int k = 0; k < 2; ++k)
+            st_shared_v4(slab + sw128_offset(i, (lane & 3) * 2 + k), v[k].x, v[k].y, v[k].z, v[k].w);
+    }
+    fence_proxy_async_smem();
+    tc_fence_before();
+    __syncthreads();
+    if (threadIdx.x == 0) {
+        const uint32_t idesc = make_idesc_bf16(128, kDV, 0, 0);
+        bool ok = true;
+        int loaded = 2;
+        for (int k = 0; ok && k < 4; ++k) {
+            const int st = k & 1;
+            if (!(ok = mbar_wait(smem_u32(w_full + st), (k >> 1) & 1, p.err))) break;
+            tc_fence_after();
+#pragma unroll
+            for (int kk = 0; kk < 8; ++kk) {
+                const int ks = 8 * k + kk;   // K step of 16 latent columns
+                const uint64_t a = make_smem_desc(base + (ks >> 2) * L::kASlab + (ks & 3) * 32, 16, 1024);
+                const uint64_t bd =
+                    make_smem_desc(base + L::kA + st * L::kWStage + (kk >> 2) * kSlab + (kk & 3) * 32, 16, 1024);
+                umma_bf16(tmem, a, bd, idesc, ks > 0);
+            }
+            umma_commit(smem_u32(w_empty + st));
+            if (k + 2 < 4) {   // the stage is refilled once its products completed
+                if (!(ok = mbar_wait(smem_u32(w_empty + st), 0, p.err))) break;
+                load_w(k + 2);
+                ++loaded;
+            }
+        }
+        if (ok) umma_commit(smem_u32(mma_done));
+        if (!ok)   // no load may still be landing when the CTA exits
+            for (int k = 0; k < loaded; ++k) mbar_wait(smem_u32(w_full + (k & 1)), (k >> 1) & 1, p.err);
+    }
+    __syncwarp();
+    const bool done = mbar_wait(smem_u32(mma_done), 0, p.err);
+    tc_fence_after();
+    if (warp < kRows / 32 && __all_sync(0xffffffffu, done)) {
+        const int i = warp * 32 + lane;
+        const bool token = s_tile[i].x >= 0;
+        const long long off = ((m0 + i) * p.H + h) * kDV;
+        const uint4 *const g4 = p.gate ? reinterpret_cast<const uint4 *>(p.gate + off) : nullptr;
+        uint4 *const o4 = reinterpret_cast<uint4 *>(p.out + off);
+#pragma unroll 1
+        for (int c4 = 0; c4 < kDV / 32; ++c4) {
+            float o[32];
+            tmem_ld32(tmem + (static_cast<uint32_t>(warp * 32) << 16) + c4 * 32, o);
+            tmem_wait_ld();
+            if (!token) continue;
+#pragma unroll
+            for (int v8 = 0; v8 < 4; ++v8) {
+                float y[8];
+#pragma unroll
+                for (int k = 0; k < 8; ++k) y[k] = o[v8 * 8 + k];
+                if (g4) {
+                    const uint4 gv = __ldg(g4 + c4 * 4 + v8);
+                    const uint32_t gw[4] = {gv.x, gv.y, gv.z, gv.w};
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) {
+                        y[2 * k] *= __fdividef(1.f, 1.f + fast_exp2(-__uint_as_float(gw[k] << 16) * kLog2e));
+                        y[2 * k + 1] *= __fdividef(1.f, 1.f + fast_exp2(-__uint_as_float(gw[k] & 0xFFFF0000u) * kLog2e));
+                    }
+                }
+                o4[c4 * 4 + v8] = make_uint4(pack_bf16x2(y[0], y[1]), pack_bf16x2(y[2], y[3]), pack_bf16x2(y[4], y[5]),
+                                             pack_bf16x2(y[6], y[7]));
+            }
+        }
+    }
+    tc_fence_before();
+    __syncthreads();
+    if (warp == 0) tmem_dealloc(tmem, 128);
+}
+
+CUresult encode_map(CUtensorMap *m, const void *ptr, int rank, const cuuint64_t *dims, const cuuint64_t *strides,
+                    const cuuint32_t *box) {
+    auto fn = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(tensor_map_encode_fn());
+    if (!fn) return CUDA_ERROR_NOT_SUPPORTED;
+    cuuint32_t es[5] = {1, 1, 1, 1, 1};
+    return fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, rank, const_cast<void *>(ptr), dims, strides, box, es,
+              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+}
+
+// What is asked of a device once: the kernels' attributes, and how many clusters of the pair kernel run at once.
+cudaError_t prepare(int num_sms, int &clusters) {
+    constexpr int kMaxDev = 64;
+    static std::atomic<int> cached[kMaxDev];
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    if (dev < kMaxDev && (clusters = cached[dev].load()) > 0) return cudaSuccess;
+    const auto smem = [](auto *kernel, uint32_t bytes) {
+        return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(bytes));
+    };
+    if ((e = smem(attend_pair_kernel, kSmemPair)) != cudaSuccess) return e;
+    if ((e = smem(attend_up_kernel<32>, Up<32>::kSmem)) != cudaSuccess) return e;
+    if ((e = smem(attend_up_kernel<128>, Up<128>::kSmem)) != cudaSuccess) return e;
+    cudaFuncAttributes fa;   // the register split assumes this launch budget
+    if ((e = cudaFuncGetAttributes(&fa, attend_pair_kernel)) != cudaSuccess) return e;
+    if (fa.numRegs != static_cast<int>(kRegsLaunch)) return cudaErrorInvalidConfiguration;
+    const int cap = num_sms / 2 > 0 ? num_sms / 2 : 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(2 * cap);
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = kSmemPair;
+    int n = 0;
+    if (cudaOccupancyMaxActiveClusters(&n, attend_pair_kernel, &cfg) != cudaSuccess || n < 1) {
+        (void)cudaGetLastError();
+        n = cap;
+    }
+    clusters = n < cap ? n : cap;
+    if (dev < kMaxDev) cached[dev].store(clusters);
+    return cudaSuccess;
+}
+
+// The workspace: whole tiles' rows, parts, tiles' clusters.
+struct Space {
+    size_t o, m, l, tile, end;
+    int tiles;
+    Space(long long B, long long T, int H, int num_sms) {
+        const size_t parts = static_cast<size_t>(num_sms / 2 > 0 ? num_sms / 2 : 1) * 2 * kM;
+        tiles = static_cast<int>((T * H + kM - 1) / kM);
+        o = static_cast<size_t>(B) * T * H * kR * 2;
+        m = o + parts * kR * 4;
+        l = m + parts * 4;
+        tile = l + parts * 4;
+        end = tile + static_cast<size_t>(B) * tiles * sizeof(int2);
+    }
+};
 
 }  // namespace
 
 bool attend_paged_supports(int H, int d_v, int r) { return r == kR && d_v == kDV && H >= 1 && H <= 128; }
 
-size_t attend_paged_workspace_bytes(long long, long long, int, int) { return 256; }
+size_t attend_paged_workspace_bytes(long long B, long long T, int H, int num_sms) { return Space(B, T, H, num_sms).end; }
 
 cudaError_t launch_attend_paged(const AttendPagedArgs &a, cudaStream_t s) {
+    const Space sp(a.B, a.T, a.H, a.num_sms);
+    if (sp.end > a.workspace_bytes) return cudaErrorInvalidValue;
+    int G = 0;
+    cudaError_t e = prepare(a.num_sms, G);
+    if (e != cudaSuccess) return e;
+    CUtensorMap tm_s, tm_v, tm_w;
+    {
+        const long long rows = static_cast<long long>(a.num_blocks) * a.bs;
+        const void *const pool = rows > 0 ? a.pool : a.q_abs;   // no row of an empty pool is inside its map
+        const cuuint64_t n = static_cast<cuuint64_t>(rows > 0 ? rows : 1), ld = static_cast<cuuint64_t>(a.ld_pool) * 2;
+        const cuuint64_t dims_s[2] = {kR, n}, dims_v[3] = {64, n, kR / 64};
+        const cuuint64_t strides_s[1] = {ld}, strides_v[2] = {ld, 128};
+        const cuuint32_t box_s[2] = {64, 64}, box_v[3] = {64, kVRows, 4};
+        const cuuint64_t dims_w[2] = {kR, static_cast<cuuint64_t>(a.H) * kDV}, strides_w[1] = {kR * 2};
+        const cuuint32_t box_w[2] = {64, kDV};
+        if (encode_map(&tm_s, pool, 2, dims_s, strides_s, box_s) != CUDA_SUCCESS ||
+            encode_map(&tm_v, pool, 3, dims_v, strides_v, box_v) != CUDA_SUCCESS ||
+            encode_map(&tm_w, a.w_uv, 2, dims_w, strides_w, box_w) != CUDA_SUCCESS)
+            return cudaErrorInvalidValue;
+    }
+    char *const ws = static_cast<char *>(a.workspace);
+    auto *const ws_rows = reinterpret_cast<__nv_bfloat16 *>(ws);
+    float *const ws_o = reinterpret_cast<float *>(ws + sp.o), *const ws_m = reinterpret_cast<float *>(ws + sp.m),
+                *const ws_l = reinterpret_cast<float *>(ws + sp.l);
+    int2 *const ws_tile = reinterpret_cast<int2 *>(ws + sp.tile);
+    const PairParams pp{static_cast<const __nv_bfloat16 *>(a.q_abs), a.table, a.lens, a.counts, a.parents, a.ld_table,
+                        ws_rows, ws_o, ws_m, ws_l, ws_tile, a.dev_err, a.B, a.T, a.H, sp.tiles, a.num_blocks, a.bs,
+                        a.max_blocks, a.window, a.sinks, a.scale * kLog2e};
     note_launch();
-    return launch_dependent(attend_paged_simple_kernel, dim3(static_cast<unsigned>(a.B) * a.T * a.H), 256, 0, s, a);
+    e = launch_dependent(attend_pair_kernel, dim3(2 * G), kThreads, kSmemPair, s, tm_s, tm_v, pp);
+    if (e != cudaSuccess) return e;
+    const UpParams up{a.lens, a.counts, ws_rows, ws_o, ws_m, ws_l, ws_tile, static_cast<const __nv_bfloat16 *>(a.gate),
+                      static_cast<__nv_bfloat16 *>(a.out), a.dev_err, a.B, a.T, a.H, sp.tiles, a.bs, a.max_blocks};
+    const long long m = static_cast<long long>(a.B) * a.T;
+    note_launch();
+    if (m > 1024) {
+        return launch_dependent(attend_up_kernel<128>, dim3(static_cast<unsigned>((m + 127) / 128 * a.H)), kUpThreads,
+                                Up<128>::kSmem, s, tm_w, up);
+    }
+    return launch_dependent(attend_up_kernel<32>, dim3(static_cast<unsigned>((m + 31) / 32 * a.H)), kUpThreads,
+                            Up<32>::kSmem, s, tm_w, up);
 }
 
 }  // namespace mla
