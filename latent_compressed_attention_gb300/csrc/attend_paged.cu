@@ -273,6 +273,22 @@ __device__ __forceinline__ uint32_t finite_halves(uint32_t w) {
     return w;
 }
 
+// A place in a ring of barriers and stages.
+template <int N>
+struct Ring {
+    uint32_t st = 0, phase = 0;
+    __device__ __forceinline__ void next() {
+        if (++st == N) st = 0, phase ^= 1;
+    }
+};
+
+// True in one lane of a warp that is here together.
+__device__ __forceinline__ bool elect_one() {
+    uint32_t r;
+    asm volatile("{ .reg .pred p; elect.sync _|p, 0xffffffff; selp.u32 %0, 1, 0, p; }" : "=r"(r));
+    return r != 0;
+}
+
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     attend_pair_kernel(const __grid_constant__ CUtensorMap tm_s, const __grid_constant__ CUtensorMap tm_v,
                        const PairParams p) {
@@ -282,7 +298,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     PairBars *const bars = reinterpret_cast<PairBars *>(smem_raw + (base - raw) + BARS);
     volatile int *const abort_flag = &bars->abort;
     const auto B_ = [](uint64_t &b) { return smem_u32(&b); };
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;   // known to be one per warp
     const uint32_t rank = cluster_ctarank();
     const int G = static_cast<int>(gridDim.x >> 1), cl = static_cast<int>(blockIdx.x >> 1);
 
@@ -320,7 +336,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     tc_fence_before();
     cluster_sync_all();   // both CTAs' barriers exist before any remote arrival or copy
     tc_fence_after();
-    const uint32_t tmem = bars->tmem_base;
+    const uint32_t tmem = __shfl_sync(0xffffffffu, bars->tmem_base, 0);
     grid_dependency_wait();
     grid_launch_dependents();   // the second kernel may take SMs as clusters finish; it waits for the whole grid
 
@@ -385,30 +401,37 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     if (warp < 4) {
         regs_release<kRegsCtl>();
         Walk w(p, bars);
+        const bool lead = elect_one();
+        // a whole warp leaves a wait together and of one mind
+        const auto wait = [&](uint32_t bar, uint32_t parity) {
+            return __all_sync(0xffffffffu, mbar_wait(bar, parity, p.err, abort_flag));
+        };
         if (rank == 0) {
             // =========================================================== score CTA
-            if ((warp == 0 || warp == 3) && lane == 0) {
+            if (warp == 0 || warp == 3) {
                 // ---- TMA producers: rows [64 half, 64 half + 64) of each stage
                 const int half = warp == 0 ? 0 : 1;
                 tma_prefetch_desc(&tm_s);
+                const uint32_t full0 = B_(bars->sc_full[0]), empty0 = B_(bars->sc_empty[0]);
+                Ring<kSStages> at;
                 uint32_t it = 0;
                 bool ok = true;
                 while (ok && w.next(p)) {
                     for (int i = w.i0; ok && i < w.i1; ++i) {
                         const int u = w.t.row0(i) + half * 64;
                         const int row = u < w.t.end ? pool_row(w.seq, u) : -1;
-                        for (int kc = 0; kc < 8; ++kc, ++it) {
-                            const int st = it % kSStages;
-                            if (it >= kSStages &&
-                                !(ok = mbar_wait(B_(bars->sc_empty[st]), (it / kSStages - 1) & 1, p.err, abort_flag)))
-                                break;
-                            const uint32_t full = B_(bars->sc_full[st]);
+#pragma unroll 1
+                        for (int kc = 0; kc < 8; ++kc, ++it, at.next()) {
+                            // a barrier that no one has arrived at counts as past phase 1
+                            if (!(ok = wait(empty0 + at.st * 8, at.phase ^ 1))) break;
+                            if (!lead) continue;
+                            const uint32_t full = full0 + at.st * 8;
                             if (row < 0) {   // past the last row that is seen: masked, whatever the stage holds
                                 mbar_arrive(full);
-                                continue;
+                            } else {
+                                mbar_arrive_expect_tx(full, kStage / 2);
+                                tma_load_2d(base + at.st * kStage + half * (kStage / 2), &tm_s, full, kc * 64, row);
                             }
-                            mbar_arrive_expect_tx(full, kStage / 2);
-                            tma_load_2d(base + st * kStage + half * (kStage / 2), &tm_s, full, kc * 64, row);
                         }
                     }
                 }
@@ -416,59 +439,67 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                 // no load may still be landing when the CTA exits
                 for (uint32_t k = it > kSStages ? it - kSStages : 0; k < it; ++k)
                     mbar_wait(B_(bars->sc_full[k % kSStages]), (k / kSStages) & 1, p.err, nullptr, kLandNs);
-            } else if (warp == 1 && lane == 0) {
+            } else if (warp == 1) {
                 // ---- MMA issuer
                 const uint64_t ring = make_smem_desc(base, 16, 1024);
-                uint32_t it = 0, jb = 0, nseg = 0;
+                const uint32_t full0 = B_(bars->sc_full[0]), empty0 = B_(bars->sc_empty[0]), s_full0 = B_(bars->s_full[0]),
+                               s_free0 = B_(bars->s_free[0]), q_ready = B_(bars->q_ready);
+                Ring<kSStages> at;
+                Ring<2> sb;
+                uint32_t q_phase = 0;
                 bool ok = true;
                 while (ok && w.next(p)) {
-                    if (!(ok = mbar_wait(B_(bars->q_ready), nseg & 1, p.err, abort_flag))) break;
-                    ++nseg;
-                    for (int i = w.i0; ok && i < w.i1; ++i, ++jb) {
-                        if (jb >= 2 && !(ok = mbar_wait(B_(bars->s_free[jb & 1]), (jb / 2 - 1) & 1, p.err, abort_flag))) break;
-                        tc_fence_after();
-                        const uint32_t d = tmem + S_COL + (jb & 1) * 128;
-                        for (int kc = 0; kc < 8; ++kc, ++it) {
-                            const int st = it % kSStages;
-                            if (!(ok = mbar_wait(B_(bars->sc_full[st]), (it / kSStages) & 1, p.err, abort_flag))) break;
+                    if (!(ok = wait(q_ready, q_phase))) break;
+                    q_phase ^= 1;
+#pragma unroll 1
+                    for (int i = w.i0; ok && i < w.i1; ++i, sb.next()) {
+                        if (!(ok = wait(s_free0 + sb.st * 8, sb.phase ^ 1))) break;
+                        const uint32_t d = tmem + S_COL + sb.st * 128;
+#pragma unroll 1
+                        for (int kc = 0; kc < 8; ++kc, at.next()) {
+                            if (!(ok = wait(full0 + at.st * 8, at.phase))) break;
                             tc_fence_after();
-                            const uint64_t bd = desc_add(ring, st * kStage);
+                            if (lead) {
+                                const uint64_t b = desc_add(ring, at.st * kStage);
 #pragma unroll
-                            for (int kk = 0; kk < 4; ++kk)
-                                umma_bf16_tmem_a(d, tmem + (kc * 4 + kk) * 8, desc_add(bd, kk * 32), kIdescS, (kc | kk) != 0);
-                            umma_commit(B_(bars->sc_empty[st]));
+                                for (int kk = 0; kk < 4; ++kk)
+                                    umma_bf16_tmem_a(d, tmem + kc * 32 + kk * 8, desc_add(b, kk * 32), kIdescS, (kc | kk) != 0);
+                                umma_commit(empty0 + at.st * 8);
+                            }
                         }
-                        if (ok) umma_commit(B_(bars->s_full[jb & 1]));
+                        if (ok && lead) umma_commit(s_full0 + sb.st * 8);
                     }
                 }
                 if (!ok) *abort_flag = 1;
             }
         } else {
             // =========================================================== value CTA
-            if ((warp == 0 || warp == 3) && lane == 0) {
+            if (warp == 0 || warp == 3) {
                 // ---- TMA producers: a unit is 8 stages, latent half i >> 2, row quarter i & 3; each takes one half of
                 // the rows
                 const int half = warp == 0 ? 0 : 1;
                 tma_prefetch_desc(&tm_v);
+                const uint32_t full0 = B_(bars->v_full[0]), empty0 = B_(bars->v_empty[0]);
+                Ring<kVStages> at;
                 uint32_t it = 0;
                 bool ok = true;
                 while (ok && w.next(p)) {
                     for (int i = w.i0; ok && i < w.i1; ++i, it += 8) {
                         const int u = w.t.row0(i) + half * 64;
                         const int row = u < w.t.end ? pool_row(w.seq, u) : -1;
-                        for (int k = 0; k < 4; ++k) {
-                            const uint32_t s = it + (k >> 1) * 4 + half * 2 + (k & 1);
-                            const int st = s % kVStages;
-                            if (s >= kVStages &&
-                                !(ok = mbar_wait(B_(bars->v_empty[st]), (s / kVStages - 1) & 1, p.err, abort_flag)))
-                                break;
-                            const uint32_t full = B_(bars->v_full[st]);
+#pragma unroll 1
+                        for (int k = 0; ok && k < 8; ++k, at.next()) {
+                            if (((k >> 1) & 1) != half) continue;
+                            if (!(ok = wait(empty0 + at.st * 8, at.phase ^ 1))) break;
+                            if (!lead) continue;
+                            const uint32_t full = full0 + at.st * 8;
                             if (row < 0) {
                                 mbar_arrive(full);
-                                continue;
+                            } else {
+                                mbar_arrive_expect_tx(full, kStage);
+                                tma_load_3d(base + V_RING + at.st * kStage, &tm_v, full, 0, row + (k & 1) * kVRows,
+                                            (k >> 2) * 4);
                             }
-                            mbar_arrive_expect_tx(full, kStage);
-                            tma_load_3d(base + V_RING + st * kStage, &tm_v, full, 0, row + (k & 1) * kVRows, (k >> 1) * 4);
                         }
                     }
                 }
@@ -476,57 +507,58 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                 for (uint32_t k = it > kVStages ? it - kVStages : 0; k < it; ++k)
                     mbar_wait(B_(bars->v_full[k % kVStages]), (k / kVStages) & 1, p.err, nullptr, kLandNs);
             } else if (warp == 1) {
-                // ---- MMA warp; lane 0 issues
-                const bool leader = lane == 0;
-                const auto wait_all = [&](uint64_t &bar, uint32_t parity, bool cluster) {
-                    return __all_sync(0xffffffffu, cluster ? mbar_wait<true>(B_(bar), parity, p.err, abort_flag)
-                                                           : mbar_wait(B_(bar), parity, p.err, abort_flag));
-                };
+                // ---- MMA issuer
                 const uint64_t pdesc = make_smem_desc(base, 16, 1024), ring = make_smem_desc(base + V_RING, kVSlab, 1024);
-                uint32_t it = 0, jj = 0, nfix = 0, nseg = 0, cleaned = 0;   // cleaned: a phase bit per stage
+                const uint32_t full0 = B_(bars->v_full[0]), empty0 = B_(bars->v_empty[0]), clean0 = B_(bars->v_clean[0]),
+                               p_full0 = B_(bars->p_full[0]), pv_done0 = B_(bars->pv_done[0]);
+                Ring<kVStages> at;
+                Ring<kPBufs> pb;
+                uint32_t fix_phase = 0, drain_phase = 1, cleaned = 0;   // cleaned: a phase bit per stage
                 bool ok = true;
                 while (ok && w.next(p)) {
                     const int len = w.seq_len(p);
                     const uint32_t bytes = 2u * ((w.t.rows + 7) & ~7) * 128u + kInfo;
-                    for (int i = w.i0; ok && i < w.i1; ++i, ++jj) {
-                        const uint32_t pb = jj % kPBufs;
+#pragma unroll 1
+                    for (int i = w.i0; ok && i < w.i1; ++i, pb.next()) {
                         const bool first = i == w.i0, mixed = w.t.mixed(p, len, w.t.row0(i));
-                        if (leader) mbar_arrive_expect_tx(B_(bars->p_full[pb]), bytes);
-                        if (!(ok = wait_all(bars->p_full[pb], (jj / kPBufs) & 1, true))) break;
-                        // the accumulator of the part before has been drained
-                        if (first && nseg > 0 && !(ok = wait_all(bars->drained, (nseg - 1) & 1, false))) break;
-                        // rows whose maximum grew need their accumulator rescaled before this unit's product
-                        const uint32_t info = base + pb * kPUnit + 2 * kSlab;
-                        bool grew = false;
+                        const uint32_t p_full = p_full0 + pb.st * 8;
+                        if (lead) mbar_arrive_expect_tx(p_full, bytes);
+                        if (!(ok = __all_sync(0xffffffffu, mbar_wait<true>(p_full, pb.phase, p.err, abort_flag)))) break;
+                        if (first) {   // the accumulator of the part before has been drained
+                            if (!(ok = wait(B_(bars->drained), drain_phase))) break;
+                            drain_phase ^= 1;
+                        } else {   // rows whose maximum grew need their accumulator rescaled before this unit's product
+                            const uint32_t info = base + pb.st * kPUnit + 2 * kSlab;
+                            bool grew = false;
 #pragma unroll
-                        for (int k = 0; k < 4; ++k) grew |= ld_shared_f32(info + (lane + 32 * k) * 8) != 1.f;
-                        if (!first && __any_sync(0xffffffffu, grew)) {
-                            if (!(ok = wait_all(bars->rescaled, nfix & 1, false))) break;
-                            ++nfix;
+                            for (int k = 0; k < 4; ++k) grew |= ld_shared_f32(info + (lane + 32 * k) * 8) != 1.f;
+                            if (__any_sync(0xffffffffu, grew)) {
+                                if (!(ok = wait(B_(bars->rescaled), fix_phase))) break;
+                                fix_phase ^= 1;
+                            }
                         }
-                        for (int k = 0; ok && k < 8; ++k, ++it) {
-                            const int st = it % kVStages;
-                            if (!(ok = wait_all(bars->v_full[st], (it / kVStages) & 1, false))) break;
+                        uint64_t a = desc_add(pdesc, pb.st * kPUnit);
+#pragma unroll 1
+                        for (int k = 0; k < 8; ++k, at.next()) {   // latent half k >> 2, row quarter k & 3
+                            if (!(ok = wait(full0 + at.st * 8, at.phase))) break;
                             if (mixed) {
-                                if (!(ok = wait_all(bars->v_clean[st], (cleaned >> st) & 1, false))) break;
-                                cleaned ^= 1u << st;
+                                if (!(ok = wait(clean0 + at.st * 8, (cleaned >> at.st) & 1))) break;
+                                cleaned ^= 1u << at.st;
                             }
                             tc_fence_after();
-                            if (leader) {
-                                const uint64_t a = desc_add(pdesc, pb * kPUnit + ((k >> 1) & 1) * kSlab + (k & 1) * 64);
-                                const uint64_t bd = desc_add(ring, st * kStage);
+                            if (lead) {
+                                const uint64_t b = desc_add(ring, at.st * kStage);
+                                const uint64_t ak = desc_add(a, ((k >> 1) & 1) * kSlab + (k & 1) * 64);
                                 const uint32_t d = tmem + (k >> 2) * 256;
-                                umma_bf16(d, a, bd, kIdescO, !first || (k & 3) != 0);
-                                umma_bf16(d, desc_add(a, 32), desc_add(bd, 2048), kIdescO, 1);
-                                umma_commit(B_(bars->v_empty[st]));
+                                umma_bf16(d, ak, b, kIdescO, !first || (k & 3) != 0);
+                                umma_bf16(d, desc_add(ak, 32), desc_add(b, 2048), kIdescO, 1);
+                                umma_commit(empty0 + at.st * 8);
                             }
-                            __syncwarp();
                         }
-                        if (ok && leader) umma_commit(B_(bars->pv_done[pb]));
+                        if (ok && lead) umma_commit(pv_done0 + pb.st * 8);
                     }
-                    ++nseg;
                 }
-                if (!ok && leader) *abort_flag = 1;
+                if (!ok && lead) *abort_flag = 1;
             } else if (warp == 2 && lane == 0) {
                 // ---- relay: a P buffer is free again once its product completed and its info was read
                 uint32_t jj = 0;
