@@ -22,9 +22,10 @@
 // There the value CTA's math warps also replace what is not finite in the rows by zeros before the product: 0 * NaN of a
 // row that a token does not see would reach it; a token that does see one gets its NaN through the sum of its weights.
 //
-// A tile that one cluster walked whole leaves o_lat / l as bf16 rows; a tile cut between clusters leaves fp32 sums with
-// their maxima and weights, at most two such parts per cluster.  The second kernel joins those, applies W_UV^T on the
-// tensor cores and the gate.
+// A tile that one cluster walked whole leaves o_lat / l as rows of two bf16 parts (16 bits of each value: their product
+// with W_UV is as good as fp32's); a tile cut between clusters leaves fp32 sums with their maxima and weights, at most two
+// such parts per cluster.  Up to 64 tokens one kernel joins those, applies W_UV^T on the tensor cores and the gate; above,
+// a kernel joins them into rows and a plain product per head follows, its operands by TMA.
 #include <cuda.h>
 #include <cudaTypedefs.h>
 
@@ -91,9 +92,11 @@ struct PairParams {
     const __nv_bfloat16 *q_abs;
     const int *table, *lens, *counts, *parents;
     long long ld_table;
-    __nv_bfloat16 *ws_rows;              // [B * T * H][r]: whole tiles' o_lat / l
+    __nv_bfloat16 *ws_rows;              // two planes of [B * T * H][r]: o_lat / l, rounded, and what that leaves
     float *ws_o, *ws_m, *ws_l;           // [2 G][128][r], [2 G][128]: parts' sums, maxima (log2 units), weights
     int2 *ws_tile;                       // [B * tiles]: first and last cluster of each tile
+    int2 *ws_cut;                        // [G]: sequence and tile that a cluster starts and leaves unfinished; {-1, .}: none
+    size_t plane;                        // elements of a plane of ws_rows
     int *err;
     int B, T, H, tiles, num_blocks, bs, max_blocks, window, sinks;
     float scale_log2;
@@ -266,6 +269,13 @@ __device__ __forceinline__ void q_store(uint32_t taddr, int half, const uint4 (&
     }
 }
 
+// Two values as bf16 and what the rounding leaves, as bf16 again.
+__device__ __forceinline__ uint32_t split_bf16x2(float a, float b, uint32_t &lo) {
+    const uint32_t hi = pack_bf16x2(a, b);
+    lo = pack_bf16x2(a - __uint_as_float(hi << 16), b - __uint_as_float(hi & 0xFFFF0000u));
+    return hi;
+}
+
 // Not finite bf16 halves of a word to zero.
 __device__ __forceinline__ uint32_t finite_halves(uint32_t w) {
     if ((w & 0x7F80u) == 0x7F80u) w &= 0xFFFF0000u;
@@ -281,6 +291,9 @@ struct Ring {
         if (++st == N) st = 0, phase ^= 1;
     }
 };
+
+// What kernels before this one wrote becomes visible to this thread's TMA loads.
+__device__ __forceinline__ void fence_proxy_async_all() { asm volatile("fence.proxy.async;" ::: "memory"); }
 
 // True in one lane of a warp that is here together.
 __device__ __forceinline__ bool elect_one() {
@@ -412,6 +425,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                 // ---- TMA producers: rows [64 half, 64 half + 64) of each stage
                 const int half = warp == 0 ? 0 : 1;
                 tma_prefetch_desc(&tm_s);
+                fence_proxy_async_all();
                 const uint32_t full0 = B_(bars->sc_full[0]), empty0 = B_(bars->sc_empty[0]);
                 Ring<kSStages> at;
                 uint32_t it = 0;
@@ -479,6 +493,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                 // the rows
                 const int half = warp == 0 ? 0 : 1;
                 tma_prefetch_desc(&tm_v);
+                fence_proxy_async_all();
                 const uint32_t full0 = B_(bars->v_full[0]), empty0 = B_(bars->v_empty[0]);
                 Ring<kVStages> at;
                 uint32_t it = 0;
@@ -726,6 +741,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         } else {
             // ---- rescaling, cleaning and drain: thread = TMEM lane, warpgroup wg has latent columns [256 wg, 256 wg + 256)
             uint32_t jj = 0, it = 0;
+            int2 cut = make_int2(-1, 0);
             bool ok = true, fail;
             while (ok && w.next(p)) {
                 const int len = w.seq_len(p);
@@ -795,17 +811,19 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                     tmem_ld32(trow + wg * 256 + cc * 32, v);
                     tmem_wait_ld();
                     if (!valid) continue;
-                    if (whole) {   // the operand of the product with W_UV: bf16, as in the prefill and the other decodes
-                        uint4 o[4];
+                    if (whole) {
+                        uint32_t hi[16], lo[16];
 #pragma unroll
-                        for (int q = 0; q < 4; ++q)
-                            o[q] = make_uint4(pack_bf16x2(v[8 * q] * inv, v[8 * q + 1] * inv),
-                                              pack_bf16x2(v[8 * q + 2] * inv, v[8 * q + 3] * inv),
-                                              pack_bf16x2(v[8 * q + 4] * inv, v[8 * q + 5] * inv),
-                                              pack_bf16x2(v[8 * q + 6] * inv, v[8 * q + 7] * inv));
+                        for (int k = 0; k < 16; ++k) hi[k] = split_bf16x2(v[2 * k] * inv, v[2 * k + 1] * inv, lo[k]);
                         __nv_bfloat16 *const dst = p.ws_rows + g * kR + wg * 256 + cc * 32;
-                        st_global_32B(dst, o[0], o[1]);
-                        st_global_32B(dst + 16, o[2], o[3]);
+#pragma unroll
+                        for (int k = 0; k < 2; ++k) {
+                            st_global_32B(dst + 16 * k, make_uint4(hi[8 * k], hi[8 * k + 1], hi[8 * k + 2], hi[8 * k + 3]),
+                                          make_uint4(hi[8 * k + 4], hi[8 * k + 5], hi[8 * k + 6], hi[8 * k + 7]));
+                            st_global_32B(dst + p.plane + 16 * k,
+                                          make_uint4(lo[8 * k], lo[8 * k + 1], lo[8 * k + 2], lo[8 * k + 3]),
+                                          make_uint4(lo[8 * k + 4], lo[8 * k + 5], lo[8 * k + 6], lo[8 * k + 7]));
+                        }
                     } else {
                         float *const dst = p.ws_o + part * kR + wg * 256 + cc * 32;
 #pragma unroll
@@ -820,11 +838,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                     int2 *const tile = p.ws_tile + static_cast<long long>(w.seq) * p.tiles + w.index;
                     if (w.i0 == 0) tile->x = cl;
                     if (w.i1 == w.t.n) tile->y = cl;
+                    if (w.i0 == 0 && w.i1 < w.t.n) cut = make_int2(w.seq, w.index);
                 }
                 tc_fence_before();
                 named_bar_sync(4, 256);
                 if (threadIdx.x == 128) mbar_arrive(B_(bars->drained));
             }
+            if (threadIdx.x == 128) p.ws_cut[cl] = cut;
             if (!ok) *abort_flag = 1;
         }
     }
@@ -837,44 +857,139 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 }
 
 // ----------------------------------------------------------------------------- join, W_UV, gate
-// One CTA per (head, kRows new tokens): o_lat rows into a swizzled tile (whole tiles' as they are, parts joined by the
-// log-sum-exp rule), times W_UV[h]^T, streamed in four chunks of 128 latent columns, then the gate.
-constexpr int kUpThreads = 512;
-template <int kRows>
-struct Up {
-    static constexpr uint32_t kASlab = kRows * 128;              // o_lat [kRows x 64 latent columns]
-    static constexpr uint32_t kA = 7 * kASlab + kSlab;           // an M = 128 operand read of the last slab stays inside
-    static constexpr uint32_t kWStage = 2 * kSlab;               // W_UV[h] [128 x 128 latent columns]
-    static constexpr uint32_t kBars = kA + 2 * kWStage;
-    static constexpr uint32_t kSmem = kBars + 64 + 1024;
-};
-
 struct UpParams {
     const int *lens, *counts;
-    const __nv_bfloat16 *ws_rows;
+    __nv_bfloat16 *ws_rows;
     const float *ws_o, *ws_m, *ws_l;
-    const int2 *ws_tile;
+    const int2 *ws_tile, *ws_cut;
+    size_t plane;
     const __nv_bfloat16 *gate;
     __nv_bfloat16 *out;
     int *err;
     int B, T, H, tiles, bs, max_blocks;
 };
 
-template <int kRows>
-__global__ void __launch_bounds__(kUpThreads, kRows == 32 ? 2 : 1)
-    attend_up_kernel(const __grid_constant__ CUtensorMap tm_w, const UpParams p) {
-    using L = Up<kRows>;
+// Parts c0, c0 + step, ... of a tile's row r by one warp: the running maximum M (log2 units), the sum of the weights and,
+// 16 latent columns per lane, the weighted sum.  Cluster `first` started the tile; those up to `last` went on with it.
+__device__ __forceinline__ void join_parts(const UpParams &p, int first, int last, int r, int c0, int step, int lane,
+                                           float (&o)[16], float &M, float &sum) {
+#pragma unroll
+    for (int k = 0; k < 16; ++k) o[k] = 0.f;
+    M = -INFINITY, sum = 0.f;
+    const auto part = [&](int c) { return static_cast<size_t>(2 * c + (c == first ? 1 : 0)) * kM + r; };
+    for (int c = first + c0; c <= last; c += 32 * step) {   // a lane per part: maxima and weights, 32 at a time
+        const int mine = c + lane * step;
+        const bool has = mine <= last;
+        const float m = has ? __ldg(p.ws_m + part(mine)) : -INFINITY, l = has ? __ldg(p.ws_l + part(mine)) : 0.f;
+        float top = m;
+#pragma unroll
+        for (int off = 16; off >= 1; off >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, off));
+        top = fmaxf(top, M);
+        const float f = M == top ? 1.f : fast_exp2(M - top), g = !has ? 0.f : m == top ? 1.f : fast_exp2(m - top);
+        float lw = has ? g * l : 0.f;
+#pragma unroll
+        for (int off = 16; off >= 1; off >>= 1) lw += __shfl_xor_sync(0xffffffffu, lw, off);
+        M = top;
+        sum = sum * f + lw;
+#pragma unroll
+        for (int k = 0; k < 16; ++k) o[k] *= f;
+        const int n = min(32, (last - c) / step + 1);
+        for (int i = 0; i < n; i += 4) {   // four parts' loads in flight
+            uint4 x[4][4];
+            float w[4];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                w[k] = __shfl_sync(0xffffffffu, g, min(i + k, 31));
+                if (i + k < n) {
+                    const float *const src = p.ws_o + part(c + (i + k) * step) * kR + lane * 16;
+                    ld_global_32B(src, x[k][0], x[k][1]);
+                    ld_global_32B(src + 8, x[k][2], x[k][3]);
+                }
+            }
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+                if (i + k < n)
+#pragma unroll
+                    for (int q = 0; q < 4; ++q) {
+                        o[4 * q] = fmaf(__uint_as_float(x[k][q].x), w[k], o[4 * q]);
+                        o[4 * q + 1] = fmaf(__uint_as_float(x[k][q].y), w[k], o[4 * q + 1]);
+                        o[4 * q + 2] = fmaf(__uint_as_float(x[k][q].z), w[k], o[4 * q + 2]);
+                        o[4 * q + 3] = fmaf(__uint_as_float(x[k][q].w), w[k], o[4 * q + 3]);
+                    }
+        }
+    }
+}
+
+// o / sum in its two parts.
+__device__ __forceinline__ void split_row(const float (&o)[16], float sum, uint4 (&hi)[2], uint4 (&lo)[2]) {
+    const float inv = 1.f / sum;
+    uint32_t h[8], l[8];
+#pragma unroll
+    for (int k = 0; k < 8; ++k) h[k] = split_bf16x2(o[2 * k] * inv, o[2 * k + 1] * inv, l[k]);
+    hi[0] = make_uint4(h[0], h[1], h[2], h[3]), hi[1] = make_uint4(h[4], h[5], h[6], h[7]);
+    lo[0] = make_uint4(l[0], l[1], l[2], l[3]), lo[1] = make_uint4(l[4], l[5], l[6], l[7]);
+}
+
+// 32 output columns of a token's head from TMEM, with the gate.
+__device__ __forceinline__ void store_out(uint32_t taddr, const __nv_bfloat16 *gate, __nv_bfloat16 *out, bool token) {
+    float o[32];
+    tmem_ld32(taddr, o);
+    tmem_wait_ld();
+    if (!token) return;
+    if (gate) {
+#pragma unroll
+        for (int q = 0; q < 2; ++q) {
+            uint4 g[2];
+            ld_global_32B(gate + 16 * q, g[0], g[1]);
+            const uint32_t gw[8] = {g[0].x, g[0].y, g[0].z, g[0].w, g[1].x, g[1].y, g[1].z, g[1].w};
+#pragma unroll
+            for (int k = 0; k < 8; ++k) {
+                o[16 * q + 2 * k] *= __fdividef(1.f, 1.f + fast_exp2(-__uint_as_float(gw[k] << 16) * kLog2e));
+                o[16 * q + 2 * k + 1] *= __fdividef(1.f, 1.f + fast_exp2(-__uint_as_float(gw[k] & 0xFFFF0000u) * kLog2e));
+            }
+        }
+    }
+#pragma unroll
+    for (int q = 0; q < 2; ++q) {
+        uint32_t x[8];
+#pragma unroll
+        for (int k = 0; k < 8; ++k) x[k] = pack_bf16x2(o[16 * q + 2 * k], o[16 * q + 2 * k + 1]);
+        st_global_32B(out + 16 * q, make_uint4(x[0], x[1], x[2], x[3]), make_uint4(x[4], x[5], x[6], x[7]));
+    }
+}
+
+// The token of [B, T] numbered m: whether it is one of its sequence's new ones.
+__device__ __forceinline__ bool is_token(const UpParams &p, long long m, int &b, int &t) {
+    b = static_cast<int>(m / p.T), t = static_cast<int>(m - static_cast<long long>(b) * p.T);
+    int len;
+    return b < p.B && t < tokens(p, b, len, false);
+}
+
+// Few tokens: one CTA per (head, 32 tokens).  Rows into two swizzled tiles (one of each part), from ws_rows or joined from
+// parts, as many warps to a row as there are; times W_UV[h]^T, streamed in eight chunks of 64 latent columns; the gate.
+constexpr int kFewRows = 32, kFewThreads = 256, kFewWarps = kFewThreads / 32;
+constexpr uint32_t kFewSlab = kFewRows * 128;             // [32 rows x 64 latent columns]
+constexpr uint32_t kFewW = 2 * 8 * kFewSlab;              // an M = 128 read of the last slab ends inside the W_UV stages
+constexpr uint32_t kFewBars = kFewW + 2 * kSlab;
+constexpr uint32_t kFewSmem = kFewBars + 64 + 1024;       // two CTAs per SM
+static_assert(kFewWarps * kR * 4 <= 16 * kFewSlab, "the warps' sums fit where the tiles go");
+
+__global__ void __launch_bounds__(kFewThreads, 2)
+    attend_few_kernel(const __grid_constant__ CUtensorMap tm_w, const UpParams p) {
     extern __shared__ uint8_t smem_raw[];
     const uint32_t raw = smem_u32(smem_raw);
     const uint32_t base = (raw + 1023u) & ~1023u;
-    uint64_t *const w_full = reinterpret_cast<uint64_t *>(smem_raw + (base - raw) + L::kBars);   // [2]
+    uint64_t *const w_full = reinterpret_cast<uint64_t *>(smem_raw + (base - raw) + kFewBars);   // [2]
     uint64_t *const w_empty = w_full + 2;                                                         // [2]
-    uint64_t *const mma_done = w_full + 4;
+    uint64_t *const done = w_full + 4;
     uint32_t *const tmem_slot = reinterpret_cast<uint32_t *>(w_full + 5);
-    __shared__ int2 s_tile[kRows];   // first and last cluster of each row's tile; {-1, .}: not a token
+    __shared__ int2 s_tile[kFewRows];   // first and last cluster of each row's tile; {-1, .}: not a token
+    __shared__ int s_row[kFewRows];     // the row's place in its tile
+    __shared__ float s_m[kFewWarps], s_sum[kFewWarps];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int h = blockIdx.x % p.H;
-    const long long m0 = static_cast<long long>(blockIdx.x / p.H) * kRows;   // first token, counted over [B, T]
+    const long long m0 = static_cast<long long>(blockIdx.x / p.H) * kFewRows;
+    const int rows = static_cast<int>(min(static_cast<long long>(kFewRows), static_cast<long long>(p.B) * p.T - m0));
 
     if (threadIdx.x == 0) {
         for (int i = 0; i < 5; ++i) mbar_init(smem_u32(w_full + i), 1);
@@ -888,136 +1003,250 @@ __global__ void __launch_bounds__(kUpThreads, kRows == 32 ? 2 : 1)
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = *tmem_slot;
-    const auto load_w = [&](int k) {   // latent columns [128 k, 128 k + 128) of W_UV[h] into stage k % 2
+    const auto load_w = [&](int k) {   // latent columns [64 k, 64 k + 64) of W_UV[h] into stage k % 2
         const uint32_t bar = smem_u32(w_full + (k & 1));
-        mbar_arrive_expect_tx(bar, L::kWStage);
-        for (int sl = 0; sl < 2; ++sl)
-            tma_load_2d(base + L::kA + (k & 1) * L::kWStage + sl * kSlab, &tm_w, bar, k * 128 + sl * 64, h * kDV);
+        mbar_arrive_expect_tx(bar, kSlab);
+        tma_load_2d(base + kFewW + (k & 1) * kSlab, &tm_w, bar, k * 64, h * kDV);
     };
     // the pair kernel launches this one after its own wait: what the call was given may be read already
     if (threadIdx.x == 0) {
         tma_prefetch_desc(&tm_w);
         load_w(0);
         load_w(1);
+        for (int k = 2; k < 8; ++k) tma_prefetch_l2_2d(&tm_w, k * 64, h * kDV);
     }
+    int b = 0, t = 0;
+    const bool token = threadIdx.x < rows && is_token(p, m0 + threadIdx.x, b, t);
     grid_dependency_wait();
-    if (threadIdx.x < kRows) {
-        const long long m = m0 + threadIdx.x;
-        const int b = static_cast<int>(m / p.T), t = static_cast<int>(m - static_cast<long long>(b) * p.T);
-        int2 tile = make_int2(-1, -1);
-        if (b < p.B) {
-            int len;
-            if (t < tokens(p, b, len, false))
-                tile = p.ws_tile[static_cast<long long>(b) * p.tiles + (static_cast<long long>(t) * p.H + h) / kM];
-        }
-        s_tile[threadIdx.x] = tile;
+    if (threadIdx.x < kFewRows) {
+        const long long r = static_cast<long long>(t) * p.H + h;
+        s_tile[threadIdx.x] = token ? p.ws_tile[static_cast<long long>(b) * p.tiles + r / kM] : make_int2(-1, -1);
+        s_row[threadIdx.x] = static_cast<int>(r % kM);
     }
     __syncthreads();
-    for (int i = warp; i < kRows; i += kUpThreads / 32) {   // a warp per row, 16 latent columns per lane
-        const int2 tile = s_tile[i];
-        const long long row = (m0 + i) * p.H + h;
-        uint4 v[2] = {};
-        if (tile.x >= 0 && tile.x == tile.y) {
-            ld_global_32B(p.ws_rows + row * kR + lane * 16, v[0], v[1]);
-        } else if (tile.x >= 0) {
-            const long long m = m0 + i, b = m / p.T;
-            const int r = static_cast<int>(((m - b * p.T) * p.H + h) % kM);   // the tile's row
-            float o[16], M = -INFINITY, sum = 0.f;
+    int per_row = 1;   // warps
+    while (rows * per_row * 2 <= kFewWarps) per_row *= 2;
+    const auto store_row = [&](int i, const uint4 (&hi)[2], const uint4 (&lo)[2]) {
+        const uint32_t slab = base + (lane >> 2) * kFewSlab;
 #pragma unroll
-            for (int k = 0; k < 16; ++k) o[k] = 0.f;
-            for (int c = tile.x; c <= tile.y; ++c) {   // the first cluster's part starts the tile, the others go on with it
-                const size_t part = static_cast<size_t>(2 * c + (c == tile.x ? 1 : 0)) * kM + r;
-                const float m_c = p.ws_m[part], l_c = p.ws_l[part];
-                const float top = fmaxf(M, m_c);
-                const float f = M == top ? 1.f : fast_exp2(M - top), g = m_c == top ? 1.f : fast_exp2(m_c - top);
-                M = top;
-                sum = sum * f + l_c * g;
-                const float4 *const src = reinterpret_cast<const float4 *>(p.ws_o + part * kR + lane * 16);
+        for (int k = 0; k < 2; ++k) {
+            const uint32_t at = slab + sw128_offset(i, (lane & 3) * 2 + k);
+            st_shared_v4(at, hi[k].x, hi[k].y, hi[k].z, hi[k].w);
+            st_shared_v4(at + 8 * kFewSlab, lo[k].x, lo[k].y, lo[k].z, lo[k].w);
+        }
+    };
+    if (per_row == 1) {
+        for (int i = warp; i < rows; i += kFewWarps) {
+            const int2 tile = s_tile[i];
+            uint4 hi[2] = {}, lo[2] = {};
+            if (tile.x >= 0 && tile.x == tile.y) {
+                const __nv_bfloat16 *const src = p.ws_rows + ((m0 + i) * p.H + h) * kR + lane * 16;
+                ld_global_32B(src, hi[0], hi[1]);
+                ld_global_32B(src + p.plane, lo[0], lo[1]);
+            } else if (tile.x >= 0) {
+                float o[16], M, sum;
+                join_parts(p, tile.x, tile.y, s_row[i], 0, 1, lane, o, M, sum);
+                split_row(o, sum, hi, lo);
+            }
+            store_row(i, hi, lo);
+        }
+    } else {
+        const int i = warp / per_row, c0 = warp % per_row;
+        const bool mine = i < rows;
+        const int2 tile = mine ? s_tile[i] : make_int2(-1, -1);
+        const bool cut = tile.x >= 0 && tile.x != tile.y;
+        float o[16], M = -INFINITY, sum = 0.f;
+        if (cut) {
+            join_parts(p, tile.x, tile.y, s_row[i], c0, per_row, lane, o, M, sum);
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+                st_shared_v4(base + warp * (kR * 4) + k * 512 + lane * 16, __float_as_uint(o[4 * k]),
+                             __float_as_uint(o[4 * k + 1]), __float_as_uint(o[4 * k + 2]), __float_as_uint(o[4 * k + 3]));
+            if (lane == 0) s_m[warp] = M, s_sum[warp] = sum;
+        }
+        __syncthreads();
+        uint4 hi[2] = {}, lo[2] = {};
+        if (cut && c0 == 0) {   // the row's first warp adds up the others' sums, in their order
+            float top = M;
+            for (int k = 1; k < per_row; ++k) top = fmaxf(top, s_m[warp + k]);
+            const float f = M == top ? 1.f : fast_exp2(M - top);
+            sum *= f;
+#pragma unroll
+            for (int k = 0; k < 16; ++k) o[k] *= f;
+            for (int k = 1; k < per_row; ++k) {
+                const float g = s_m[warp + k] == top ? 1.f : fast_exp2(s_m[warp + k] - top);
+                if (s_m[warp + k] == -INFINITY && top != -INFINITY) continue;   // no part, or one of weight 0
+                sum = fmaf(s_sum[warp + k], g, sum);
 #pragma unroll
                 for (int q = 0; q < 4; ++q) {
-                    const float4 x = src[q];
-                    o[4 * q] = o[4 * q] * f + x.x * g, o[4 * q + 1] = o[4 * q + 1] * f + x.y * g;
-                    o[4 * q + 2] = o[4 * q + 2] * f + x.z * g, o[4 * q + 3] = o[4 * q + 3] * f + x.w * g;
+                    const uint4 x = ld_shared_v4(base + (warp + k) * (kR * 4) + q * 512 + lane * 16);
+                    o[4 * q] = fmaf(__uint_as_float(x.x), g, o[4 * q]);
+                    o[4 * q + 1] = fmaf(__uint_as_float(x.y), g, o[4 * q + 1]);
+                    o[4 * q + 2] = fmaf(__uint_as_float(x.z), g, o[4 * q + 2]);
+                    o[4 * q + 3] = fmaf(__uint_as_float(x.w), g, o[4 * q + 3]);
                 }
             }
-            const float inv = 1.f / sum;
-            uint32_t x[8];
-#pragma unroll
-            for (int k = 0; k < 8; ++k) x[k] = pack_bf16x2(o[2 * k] * inv, o[2 * k + 1] * inv);
-            v[0] = make_uint4(x[0], x[1], x[2], x[3]), v[1] = make_uint4(x[4], x[5], x[6], x[7]);
+            split_row(o, sum, hi, lo);
+        } else if (tile.x >= 0 && !cut && c0 == 0) {
+            const __nv_bfloat16 *const src = p.ws_rows + ((m0 + i) * p.H + h) * kR + lane * 16;
+            ld_global_32B(src, hi[0], hi[1]);
+            ld_global_32B(src + p.plane, lo[0], lo[1]);
         }
-        const uint32_t slab = base + (lane >> 2) * L::kASlab;
-#pragma unroll
-        for (int k = 0; k < 2; ++k)
-            st_shared_v4(slab + sw128_offset(i, (lane & 3) * 2 + k), v[k].x, v[k].y, v[k].z, v[k].w);
+        __syncthreads();
+        if (mine && c0 == 0) store_row(i, hi, lo);
     }
     fence_proxy_async_smem();
     tc_fence_before();
     __syncthreads();
     if (threadIdx.x == 0) {
         const uint32_t idesc = make_idesc_bf16(128, kDV, 0, 0);
+        const uint64_t a0 = make_smem_desc(base, 16, 1024), b0 = make_smem_desc(base + kFewW, 16, 1024);
         bool ok = true;
         int loaded = 2;
-        for (int k = 0; ok && k < 4; ++k) {
+        for (int k = 0; ok && k < 8; ++k) {
             const int st = k & 1;
             if (!(ok = mbar_wait(smem_u32(w_full + st), (k >> 1) & 1, p.err))) break;
             tc_fence_after();
 #pragma unroll
-            for (int kk = 0; kk < 8; ++kk) {
-                const int ks = 8 * k + kk;   // K step of 16 latent columns
-                const uint64_t a = make_smem_desc(base + (ks >> 2) * L::kASlab + (ks & 3) * 32, 16, 1024);
-                const uint64_t bd =
-                    make_smem_desc(base + L::kA + st * L::kWStage + (kk >> 2) * kSlab + (kk & 3) * 32, 16, 1024);
-                umma_bf16(tmem, a, bd, idesc, ks > 0);
+            for (int kk = 0; kk < 4; ++kk) {
+                const uint64_t a = desc_add(a0, k * kFewSlab + kk * 32), bd = desc_add(b0, st * kSlab + kk * 32);
+                umma_bf16(tmem, a, bd, idesc, (k | kk) != 0);
+                umma_bf16(tmem, desc_add(a, 8 * kFewSlab), bd, idesc, 1);
             }
             umma_commit(smem_u32(w_empty + st));
-            if (k + 2 < 4) {   // the stage is refilled once its products completed
-                if (!(ok = mbar_wait(smem_u32(w_empty + st), 0, p.err))) break;
+            if (k + 2 < 8) {   // the stage is refilled once its products completed
+                if (!(ok = mbar_wait(smem_u32(w_empty + st), (k >> 1) & 1, p.err))) break;
                 load_w(k + 2);
                 ++loaded;
             }
         }
-        if (ok) umma_commit(smem_u32(mma_done));
+        if (ok) umma_commit(smem_u32(done));
         if (!ok)   // no load may still be landing when the CTA exits
-            for (int k = 0; k < loaded; ++k) mbar_wait(smem_u32(w_full + (k & 1)), (k >> 1) & 1, p.err);
+            for (int k = max(loaded - 2, 0); k < loaded; ++k)
+                mbar_wait(smem_u32(w_full + (k & 1)), (k >> 1) & 1, p.err, nullptr, kLandNs);
     }
     __syncwarp();
-    const bool done = mbar_wait(smem_u32(mma_done), 0, p.err);
+    const bool good = mbar_wait(smem_u32(done), 0, p.err);
     tc_fence_after();
-    if (warp < kRows / 32 && __all_sync(0xffffffffu, done)) {
-        const int i = warp * 32 + lane;
-        const bool token = s_tile[i].x >= 0;
-        const long long off = ((m0 + i) * p.H + h) * kDV;
-        const uint4 *const g4 = p.gate ? reinterpret_cast<const uint4 *>(p.gate + off) : nullptr;
-        uint4 *const o4 = reinterpret_cast<uint4 *>(p.out + off);
+    if (warp == 0 && __all_sync(0xffffffffu, good)) {
+        const bool valid = s_tile[lane].x >= 0;
+        const long long off = ((m0 + lane) * p.H + h) * kDV;
 #pragma unroll 1
-        for (int c4 = 0; c4 < kDV / 32; ++c4) {
-            float o[32];
-            tmem_ld32(tmem + (static_cast<uint32_t>(warp * 32) << 16) + c4 * 32, o);
-            tmem_wait_ld();
-            if (!token) continue;
-#pragma unroll
-            for (int v8 = 0; v8 < 4; ++v8) {
-                float y[8];
-#pragma unroll
-                for (int k = 0; k < 8; ++k) y[k] = o[v8 * 8 + k];
-                if (g4) {
-                    const uint4 gv = __ldg(g4 + c4 * 4 + v8);
-                    const uint32_t gw[4] = {gv.x, gv.y, gv.z, gv.w};
-#pragma unroll
-                    for (int k = 0; k < 4; ++k) {
-                        y[2 * k] *= __fdividef(1.f, 1.f + fast_exp2(-__uint_as_float(gw[k] << 16) * kLog2e));
-                        y[2 * k + 1] *= __fdividef(1.f, 1.f + fast_exp2(-__uint_as_float(gw[k] & 0xFFFF0000u) * kLog2e));
-                    }
-                }
-                o4[c4 * 4 + v8] = make_uint4(pack_bf16x2(y[0], y[1]), pack_bf16x2(y[2], y[3]), pack_bf16x2(y[4], y[5]),
-                                             pack_bf16x2(y[6], y[7]));
-            }
-        }
+        for (int c = 0; c < kDV; c += 32) store_out(tmem + c, p.gate ? p.gate + off + c : nullptr, p.out + off + c, valid);
     }
     tc_fence_before();
     __syncthreads();
     if (warp == 0) tmem_dealloc(tmem, 128);
+}
+
+// Many tokens, first: the cut tiles' parts into rows.  Eight CTAs per cluster that left a tile unfinished, a warp per row.
+constexpr int kJoinThreads = 512;
+__global__ void __launch_bounds__(kJoinThreads) attend_join_kernel(const UpParams p) {
+    grid_dependency_wait();
+    grid_launch_dependents();
+    const int2 cut = p.ws_cut[blockIdx.x >> 3];
+    if (cut.x < 0) return;
+    const int lane = threadIdx.x & 31, r = (blockIdx.x & 7) * 16 + (threadIdx.x >> 5);
+    int len;
+    if (static_cast<long long>(cut.y) * kM + r >= static_cast<long long>(tokens(p, cut.x, len, false)) * p.H) return;
+    const int2 tile = p.ws_tile[static_cast<long long>(cut.x) * p.tiles + cut.y];
+    float o[16], M, sum;
+    join_parts(p, tile.x, tile.y, r, 0, 1, lane, o, M, sum);
+    uint4 hi[2], lo[2];
+    split_row(o, sum, hi, lo);
+    __nv_bfloat16 *const dst =
+        p.ws_rows + (static_cast<long long>(cut.x) * p.T * p.H + static_cast<long long>(cut.y) * kM + r) * kR + lane * 16;
+    st_global_32B(dst, hi[0], hi[1]);
+    st_global_32B(dst + p.plane, lo[0], lo[1]);
+}
+
+// Many tokens, then: one CTA per (head, 128 tokens), out = gate * (hi + lo) . W_UV[h]^T over eight slabs of 64 latent
+// columns.  A slab's three operands are a stage of 48 KB; two stages per CTA and two CTAs per SM.
+constexpr int kUpThreads = 192;   // warps 0 TMA, 1 MMA, 2-5 epilogue
+constexpr uint32_t kUpStage = 3 * kSlab;
+constexpr uint32_t kUpBars = 2 * kUpStage;
+constexpr uint32_t kUpSmem = kUpBars + 64 + 1024;
+
+__global__ void __launch_bounds__(kUpThreads, 2)
+    attend_up_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ CUtensorMap tm_w, const UpParams p) {
+    extern __shared__ uint8_t smem_raw[];
+    const uint32_t raw = smem_u32(smem_raw);
+    const uint32_t base = (raw + 1023u) & ~1023u;
+    uint64_t *const full = reinterpret_cast<uint64_t *>(smem_raw + (base - raw) + kUpBars);   // [2]
+    uint64_t *const empty = full + 2;                                                          // [2]
+    uint64_t *const done = full + 4;
+    uint32_t *const tmem_slot = reinterpret_cast<uint32_t *>(full + 5);
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int h = blockIdx.x % p.H;
+    const long long m0 = static_cast<long long>(blockIdx.x / p.H) * kM;
+
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < 5; ++i) mbar_init(smem_u32(full + i), 1);
+        fence_mbar_init();
+    }
+    if (warp == 1) {
+        tmem_alloc(smem_u32(tmem_slot), 128);
+        tmem_relinquish();
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = *tmem_slot;
+    grid_dependency_wait();
+    if (warp == 0) {
+        if (lane == 0) {
+            fence_proxy_async_all();
+            bool ok = true;
+            int k = 0;
+            for (; k < 8; ++k) {
+                const int st = k & 1;
+                if (k >= 2 && !(ok = mbar_wait(smem_u32(empty + st), ((k >> 1) - 1) & 1, p.err))) break;
+                const uint32_t bar = smem_u32(full + st), dst = base + st * kUpStage;
+                mbar_arrive_expect_tx(bar, kUpStage);
+                tma_load_4d(dst, &tm_a, bar, k * 64, h, static_cast<int>(m0), 0);
+                tma_load_2d(dst + 2 * kSlab, &tm_w, bar, k * 64, h * kDV);
+            }
+            if (!ok)   // no load may still be landing when the CTA exits
+                for (int i = max(k - 2, 0); i < k; ++i)
+                    mbar_wait(smem_u32(full + (i & 1)), (i >> 1) & 1, p.err, nullptr, kLandNs);
+        }
+    } else if (warp == 1) {
+        const bool lead = elect_one();
+        const uint32_t idesc = make_idesc_bf16(128, kDV, 0, 0);
+        const uint64_t d0 = make_smem_desc(base, 16, 1024);
+        bool ok = true;
+#pragma unroll 1
+        for (int k = 0; k < 8; ++k) {
+            const int st = k & 1;
+            if (!(ok = __all_sync(0xffffffffu, mbar_wait(smem_u32(full + st), (k >> 1) & 1, p.err)))) break;
+            tc_fence_after();
+            if (lead) {
+                const uint64_t a = desc_add(d0, st * kUpStage);
+#pragma unroll
+                for (int kk = 0; kk < 4; ++kk) {
+                    umma_bf16(tmem, desc_add(a, kk * 32), desc_add(a, 2 * kSlab + kk * 32), idesc, (k | kk) != 0);
+                    umma_bf16(tmem, desc_add(a, kSlab + kk * 32), desc_add(a, 2 * kSlab + kk * 32), idesc, 1);
+                }
+                umma_commit(smem_u32(empty + st));
+            }
+        }
+        if (ok && lead) umma_commit(smem_u32(done));
+    } else {
+        const int i = (warp & 3) * 32 + lane;
+        int b, t;
+        const bool token = is_token(p, m0 + i, b, t);
+        const bool good = mbar_wait(smem_u32(done), 0, p.err);
+        tc_fence_after();
+        if (__all_sync(0xffffffffu, good)) {
+            const long long off = ((m0 + i) * p.H + h) * kDV;
+            const uint32_t row = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16);
+#pragma unroll 1
+            for (int c = 0; c < kDV; c += 32) store_out(row + c, p.gate ? p.gate + off + c : nullptr, p.out + off + c, token);
+        }
+    }
+    tc_fence_before();
+    __syncthreads();
+    if (warp == 1) tmem_dealloc(tmem, 128);
 }
 
 CUresult encode_map(CUtensorMap *m, const void *ptr, int rank, const cuuint64_t *dims, const cuuint64_t *strides,
@@ -1029,6 +1258,9 @@ CUresult encode_map(CUtensorMap *m, const void *ptr, int rank, const cuuint64_t 
               CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
 }
+
+// Up to so many tokens the join, W_UV and the gate are one kernel of short CTAs.
+constexpr long long kFewTokens = 64;
 
 // What is asked of a device once: the kernels' attributes, and how many clusters of the pair kernel run at once.
 cudaError_t prepare(int num_sms, int &clusters) {
@@ -1042,8 +1274,8 @@ cudaError_t prepare(int num_sms, int &clusters) {
         return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(bytes));
     };
     if ((e = smem(attend_pair_kernel, kSmemPair)) != cudaSuccess) return e;
-    if ((e = smem(attend_up_kernel<32>, Up<32>::kSmem)) != cudaSuccess) return e;
-    if ((e = smem(attend_up_kernel<128>, Up<128>::kSmem)) != cudaSuccess) return e;
+    if ((e = smem(attend_few_kernel, kFewSmem)) != cudaSuccess) return e;
+    if ((e = smem(attend_up_kernel, kUpSmem)) != cudaSuccess) return e;
     cudaFuncAttributes fa;   // the register split assumes this launch budget
     if ((e = cudaFuncGetAttributes(&fa, attend_pair_kernel)) != cudaSuccess) return e;
     if (fa.numRegs != static_cast<int>(kRegsLaunch)) return cudaErrorInvalidConfiguration;
@@ -1062,18 +1294,19 @@ cudaError_t prepare(int num_sms, int &clusters) {
     return cudaSuccess;
 }
 
-// The workspace: whole tiles' rows, parts, tiles' clusters.
+// The workspace: rows, parts, tiles' clusters, clusters' unfinished tiles.
 struct Space {
-    size_t o, m, l, tile, end;
+    size_t o, m, l, tile, cut, end;
     int tiles;
     Space(long long B, long long T, int H, int num_sms) {
-        const size_t parts = static_cast<size_t>(num_sms / 2 > 0 ? num_sms / 2 : 1) * 2 * kM;
+        const size_t clusters = num_sms / 2 > 0 ? num_sms / 2 : 1, parts = clusters * 2 * kM;
         tiles = static_cast<int>((T * H + kM - 1) / kM);
-        o = static_cast<size_t>(B) * T * H * kR * 2;
+        o = static_cast<size_t>(B) * T * H * kR * 2 * 2;
         m = o + parts * kR * 4;
         l = m + parts * 4;
         tile = l + parts * 4;
-        end = tile + static_cast<size_t>(B) * tiles * sizeof(int2);
+        cut = tile + static_cast<size_t>(B) * tiles * sizeof(int2);
+        end = cut + clusters * sizeof(int2);
     }
 };
 
@@ -1108,23 +1341,36 @@ cudaError_t launch_attend_paged(const AttendPagedArgs &a, cudaStream_t s) {
     auto *const ws_rows = reinterpret_cast<__nv_bfloat16 *>(ws);
     float *const ws_o = reinterpret_cast<float *>(ws + sp.o), *const ws_m = reinterpret_cast<float *>(ws + sp.m),
                 *const ws_l = reinterpret_cast<float *>(ws + sp.l);
-    int2 *const ws_tile = reinterpret_cast<int2 *>(ws + sp.tile);
+    int2 *const ws_tile = reinterpret_cast<int2 *>(ws + sp.tile), *const ws_cut = reinterpret_cast<int2 *>(ws + sp.cut);
+    const long long m = static_cast<long long>(a.B) * a.T;
+    const size_t plane = static_cast<size_t>(m) * a.H * kR;
     const PairParams pp{static_cast<const __nv_bfloat16 *>(a.q_abs), a.table, a.lens, a.counts, a.parents, a.ld_table,
-                        ws_rows, ws_o, ws_m, ws_l, ws_tile, a.dev_err, a.B, a.T, a.H, sp.tiles, a.num_blocks, a.bs,
-                        a.max_blocks, a.window, a.sinks, a.scale * kLog2e};
+                        ws_rows, ws_o, ws_m, ws_l, ws_tile, ws_cut, plane, a.dev_err, a.B, a.T, a.H, sp.tiles,
+                        a.num_blocks, a.bs, a.max_blocks, a.window, a.sinks, a.scale * kLog2e};
     note_launch();
     e = launch_dependent(attend_pair_kernel, dim3(2 * G), kThreads, kSmemPair, s, tm_s, tm_v, pp);
     if (e != cudaSuccess) return e;
-    const UpParams up{a.lens, a.counts, ws_rows, ws_o, ws_m, ws_l, ws_tile, static_cast<const __nv_bfloat16 *>(a.gate),
-                      static_cast<__nv_bfloat16 *>(a.out), a.dev_err, a.B, a.T, a.H, sp.tiles, a.bs, a.max_blocks};
-    const long long m = static_cast<long long>(a.B) * a.T;
-    note_launch();
-    if (m > 1024) {
-        return launch_dependent(attend_up_kernel<128>, dim3(static_cast<unsigned>((m + 127) / 128 * a.H)), kUpThreads,
-                                Up<128>::kSmem, s, tm_w, up);
+    const UpParams up{a.lens, a.counts, ws_rows, ws_o, ws_m, ws_l, ws_tile, ws_cut, plane,
+                      static_cast<const __nv_bfloat16 *>(a.gate), static_cast<__nv_bfloat16 *>(a.out), a.dev_err, a.B, a.T,
+                      a.H, sp.tiles, a.bs, a.max_blocks};
+    if (m <= kFewTokens) {
+        note_launch();
+        return launch_dependent(attend_few_kernel, dim3(static_cast<unsigned>((m + kFewRows - 1) / kFewRows * a.H)),
+                                kFewThreads, kFewSmem, s, tm_w, up);
     }
-    return launch_dependent(attend_up_kernel<32>, dim3(static_cast<unsigned>((m + 31) / 32 * a.H)), kUpThreads,
-                            Up<32>::kSmem, s, tm_w, up);
+    CUtensorMap tm_a;
+    {
+        const cuuint64_t row = kR * 2, dims[4] = {kR, static_cast<cuuint64_t>(a.H), static_cast<cuuint64_t>(m), 2};
+        const cuuint64_t strides[3] = {row, row * a.H, row * a.H * m};
+        const cuuint32_t box[4] = {64, 1, kM, 2};
+        if (encode_map(&tm_a, ws_rows, 4, dims, strides, box) != CUDA_SUCCESS) return cudaErrorInvalidValue;
+    }
+    note_launch();
+    e = launch_dependent(attend_join_kernel, dim3(8 * G), kJoinThreads, 0, s, up);
+    if (e != cudaSuccess) return e;
+    note_launch();
+    return launch_dependent(attend_up_kernel, dim3(static_cast<unsigned>((m + kM - 1) / kM * a.H)), kUpThreads, kUpSmem, s,
+                            tm_a, tm_w, up);
 }
 
 }  // namespace mla
