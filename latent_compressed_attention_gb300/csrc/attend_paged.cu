@@ -83,13 +83,12 @@ struct PairBars {
     int abort;
     // where the cluster's share starts on the axis of units
     long long lo, hi, pre;
-    int b, j;
+    int b, j, len, count;
     long long warp_sum[kThreads / 32];
 };
 static_assert(sizeof(PairBars) <= 768, "barrier block too large");
 
 struct PairParams {
-    const __nv_bfloat16 *q_abs;
     const int *table, *lens, *counts, *parents;
     long long ld_table;
     __nv_bfloat16 *ws_rows;              // two planes of [B * T * H][r]: o_lat / l, rounded, and what that leaves
@@ -148,9 +147,7 @@ struct Walk {
     int index;               // the tile's number in the sequence
     Tile t;
     __device__ __forceinline__ Walk(const PairParams &p, const PairBars *s) {
-        lo = s->lo, hi = s->hi, pre = s->pre, b = s->b, j = s->j;
-        len = count = 0;
-        if (b < p.B) count = tokens(p, b, len, false);
+        lo = s->lo, hi = s->hi, pre = s->pre, b = s->b, j = s->j, len = s->len, count = s->count;
     }
     __device__ __forceinline__ bool next(const PairParams &p) {
         while (pre < hi) {
@@ -184,23 +181,52 @@ struct Sight {
     int head, lo, hi;
     unsigned long long bits;
     __device__ __forceinline__ Sight() {}
-    __device__ __forceinline__ Sight(const PairParams &p, int b, int t, int len) {
+    // Of token t; a whole warp calls it.  Drafts: lane i holds what is known of drafts i and i + 32, the set of their next
+    // 2^k ancestors and the one after those, and doubles it.
+    __device__ __forceinline__ Sight(const PairParams &p, int b, int t, int len, int count, int lane) {
         bits = 0;
         int position = len + t;
         hi = position + 1;
         if (p.parents) {
             const int *const up = p.parents + static_cast<long long>(b) * p.T;
-            const auto parent = [&](int a) {   // below a, so that every walk ends
-                const int q = __ldg(up + a);
-                if (q < -1 || q >= a) record_error(p.err, kDevErrBounds);
-                return q < -1 || q >= a ? -1 : q;
-            };
-            int depth = 0;
-            for (int a = parent(t); a >= 0; a = parent(a)) ++depth;
-            int d = depth;
-            for (int a = t; a >= 0; a = parent(a), --d)
-                if (p.window == 0 || depth - d < p.window || len + d < p.sinks) bits |= 1ull << a;
+            unsigned long long set[2];
+            int next[2];
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                const int a = lane + 32 * i, q = a < count ? __ldg(up + a) : -1;
+                const bool good = q >= -1 && q < a;
+                if (a < count && !good) record_error(p.err, kDevErrBounds);
+                next[i] = good ? q : -1;   // below a, so that every line ends
+                set[i] = 1ull << a;
+            }
+            for (int k = 0; k < 6; ++k) {
+                unsigned long long more[2];
+                int far[2];
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    const int at = next[i] & 31;
+                    const unsigned long long s0 = __shfl_sync(0xffffffffu, set[0], at), s1 = __shfl_sync(0xffffffffu, set[1], at);
+                    const int n0 = __shfl_sync(0xffffffffu, next[0], at), n1 = __shfl_sync(0xffffffffu, next[1], at);
+                    more[i] = next[i] < 0 ? 0 : next[i] < 32 ? s0 : s1;
+                    far[i] = next[i] < 0 ? -1 : next[i] < 32 ? n0 : n1;
+                }
+#pragma unroll
+                for (int i = 0; i < 2; ++i) set[i] |= more[i], next[i] = far[i];
+            }
+            const unsigned long long s0 = __shfl_sync(0xffffffffu, set[0], t & 31), s1 = __shfl_sync(0xffffffffu, set[1], t & 31);
+            bits = t < 32 ? s0 : s1;
+            const int depth = __popcll(bits) - 1;
             hi = len, position = len + depth;
+            if (p.window > 0) {
+                // ancestors come in the order of their depths: those before the window and past the sinks go
+                unsigned long long rest = bits, sinks = 0;
+                for (int d = 0; d <= depth - p.window; ++d) {
+                    const unsigned long long first = rest & (0 - rest);
+                    rest ^= first;
+                    if (len + d < p.sinks) sinks |= first;
+                }
+                bits = rest | sinks;
+            }
         }
         lo = p.window > 0 ? max(position - p.window + 1, 0) : 0;
         head = min(min(p.sinks, lo), hi);
@@ -248,27 +274,6 @@ __device__ __forceinline__ float reduce128(const float (&s)[4][32], F f) {
     return f(f(f(m[0], m[1]), f(m[2], m[3])), f(f(m[4], m[5]), f(m[6], m[7])));
 }
 
-// A row's query into TMEM: its packed bf16 pairs are its 32-bit words in memory order.  Warpgroup wg owns latent columns
-// [256 wg, 256 wg + 256), in two halves of 16 x 16 bytes.
-__device__ __forceinline__ void q_issue(const uint4 *src, bool valid, int half, uint4 (&v)[16]) {
-#pragma unroll
-    for (int i = 0; i < 16; ++i) v[i] = valid ? __ldg(src + half * 16 + i) : make_uint4(0, 0, 0, 0);
-}
-__device__ __forceinline__ void q_store(uint32_t taddr, int half, const uint4 (&v)[16]) {
-#pragma unroll
-    for (int k = 0; k < 2; ++k) {
-        float w[32];
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            w[4 * i + 0] = __uint_as_float(v[8 * k + i].x);
-            w[4 * i + 1] = __uint_as_float(v[8 * k + i].y);
-            w[4 * i + 2] = __uint_as_float(v[8 * k + i].z);
-            w[4 * i + 3] = __uint_as_float(v[8 * k + i].w);
-        }
-        tmem_st32(taddr + (half * 2 + k) * 32, w);
-    }
-}
-
 // Two values as bf16 and what the rounding leaves, as bf16 again.
 __device__ __forceinline__ uint32_t split_bf16x2(float a, float b, uint32_t &lo) {
     const uint32_t hi = pack_bf16x2(a, b);
@@ -303,8 +308,8 @@ __device__ __forceinline__ bool elect_one() {
 }
 
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
-    attend_pair_kernel(const __grid_constant__ CUtensorMap tm_s, const __grid_constant__ CUtensorMap tm_v,
-                       const PairParams p) {
+    attend_pair_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_s,
+                       const __grid_constant__ CUtensorMap tm_v, const PairParams p) {
     extern __shared__ uint8_t smem_raw[];
     const uint32_t raw = smem_u32(smem_raw);
     const uint32_t base = (raw + 1023u) & ~1023u;
@@ -355,18 +360,17 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 
     // The axis: thread i adds up its part of the tiles; the one that holds the share's start finds the tile there.
     {
-        const long long all = static_cast<long long>(p.B) * p.tiles;
-        const long long per = (all + kThreads - 1) / kThreads;
-        const long long g0 = min(threadIdx.x * per, all), g1 = min(g0 + per, all);
-        const auto units = [&](long long g, bool report) {
-            const int b = static_cast<int>(g / p.tiles), j = static_cast<int>(g - static_cast<long long>(b) * p.tiles);
-            int len;
-            const int count = tokens(p, b, len, report);
+        const int all = p.B * p.tiles, per = (all + kThreads - 1) / kThreads;
+        const int g0 = min(static_cast<int>(threadIdx.x) * per, all), g1 = min(g0 + per, all);
+        int len = 0, count = 0;
+        const auto units = [&](int g, bool report) {
+            const int b = g / p.tiles, j = g - b * p.tiles;
+            count = tokens(p, b, len, report);
             return static_cast<long long>(j) * kM < static_cast<long long>(count) * p.H
                        ? kStart + Tile(p, j, len, count).n : 0;
         };
         long long sum = 0;
-        for (long long g = g0; g < g1; ++g) sum += units(g, cl == 0 && rank == 0);
+        for (int g = g0; g < g1; ++g) sum += units(g, cl == 0 && rank == 0);
         long long incl = sum;
 #pragma unroll
         for (int off = 1; off < 32; off <<= 1) {
@@ -375,27 +379,33 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         }
         if (lane == 31) bars->warp_sum[warp] = incl;
         __syncthreads();
-        long long before = 0, total = 0;
+        long long pre = incl - sum, total = 0;
+#pragma unroll
         for (int w = 0; w < kThreads / 32; ++w) {
-            if (w < warp) before += bars->warp_sum[w];
-            total += bars->warp_sum[w];
+            const long long v = bars->warp_sum[w];
+            if (w < warp) pre += v;
+            total += v;
         }
         // no share is empty but those of the clusters that are too many: a tile's parts lie in successive clusters
-        const long long n_shares = min(static_cast<long long>(G), total);
-        const long long lo = cl < n_shares ? total * cl / n_shares : 0, hi = cl < n_shares ? total * (cl + 1) / n_shares : 0;
-        long long pre = before + incl - sum;
-        if (threadIdx.x == 0) bars->lo = lo, bars->hi = hi, bars->b = p.B, bars->pre = hi;
-        __syncthreads();
+        const int n = total < G ? static_cast<int>(total) : G;
+        const auto start = [&](int c) {   // 64-bit divisions take a few hundred cycles
+            if (c >= n) return c == n ? total : 0;
+            return total < (1 << 24) ? static_cast<long long>(static_cast<unsigned>(total) * static_cast<unsigned>(c) /
+                                                              static_cast<unsigned>(n))
+                                     : total * c / n;
+        };
+        const long long lo = cl < n ? start(cl) : 0, hi = cl < n ? start(cl + 1) : 0;
+        if (threadIdx.x == 0 && lo == hi) bars->b = p.B, bars->lo = bars->hi = bars->pre = 0;
         if (lo < hi && pre <= lo && lo < pre + sum) {
-            for (long long g = g0; g < g1; ++g) {
-                const long long n = units(g, false);
-                if (lo < pre + n) {
-                    bars->b = static_cast<int>(g / p.tiles);
-                    bars->j = static_cast<int>(g - bars->b * static_cast<long long>(p.tiles));
-                    bars->pre = pre;
+            for (int g = g0; g < g1; ++g) {
+                const long long k = per == 1 ? sum : units(g, false);
+                if (lo < pre + k) {
+                    bars->b = g / p.tiles, bars->j = g - bars->b * p.tiles;
+                    bars->len = len, bars->count = count;
+                    bars->lo = lo, bars->hi = hi, bars->pre = pre;
                     break;
                 }
-                pre += n;
+                pre += k;
             }
         }
         __syncthreads();
@@ -422,8 +432,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         if (rank == 0) {
             // =========================================================== score CTA
             if (warp == 0 || warp == 3) {
-                // ---- TMA producers: rows [64 half, 64 half + 64) of each stage
+                // ---- TMA producers: rows [64 half, 64 half + 64) of each stage; a part's queries, then its units
                 const int half = warp == 0 ? 0 : 1;
+                tma_prefetch_desc(&tm_q);
                 tma_prefetch_desc(&tm_s);
                 fence_proxy_async_all();
                 const uint32_t full0 = B_(bars->sc_full[0]), empty0 = B_(bars->sc_empty[0]);
@@ -431,9 +442,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                 uint32_t it = 0;
                 bool ok = true;
                 while (ok && w.next(p)) {
-                    for (int i = w.i0; ok && i < w.i1; ++i) {
-                        const int u = w.t.row0(i) + half * 64;
-                        const int row = u < w.t.end ? pool_row(w.seq, u) : -1;
+                    for (int i = w.i0 - 1; ok && i < w.i1; ++i) {
+                        const bool units = i >= w.i0;
+                        const int u = units ? w.t.row0(i) + half * 64 : 0;
+                        // rows past the tile's, of the next one or past the tensor's end (zeros), are not used
+                        const int row = !units ? (half * 64 < w.t.rows ? w.seq * p.T * p.H + w.index * kM + half * 64 : -1)
+                                        : u < w.t.end ? pool_row(w.seq, u) : -1;
 #pragma unroll 1
                         for (int kc = 0; kc < 8; ++kc, ++it, at.next()) {
                             // a barrier that no one has arrived at counts as past phase 1
@@ -444,7 +458,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                                 mbar_arrive(full);
                             } else {
                                 mbar_arrive_expect_tx(full, kStage / 2);
-                                tma_load_2d(base + at.st * kStage + half * (kStage / 2), &tm_s, full, kc * 64, row);
+                                tma_load_2d(base + at.st * kStage + half * (kStage / 2), units ? &tm_s : &tm_q, full,
+                                            kc * 64, row);
                             }
                         }
                     }
@@ -463,6 +478,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                 uint32_t q_phase = 0;
                 bool ok = true;
                 while (ok && w.next(p)) {
+                    for (int k = 0; k < 8; ++k) at.next();   // the queries' stages
                     if (!(ok = wait(q_ready, q_phase))) break;
                     q_phase ^= 1;
 #pragma unroll 1
@@ -581,6 +597,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                 while (ok && w.next(p)) {
                     for (int i = w.i0; i < w.i1; ++i, ++jj) {
                         const uint32_t pb = jj % kPBufs;
+                        if (i == w.i1 - 1) continue;   // the drain goes through a part's last buffer, and frees it
                         if (!mbar_wait(B_(bars->pv_done[pb]), (jj / kPBufs) & 1, p.err, abort_flag) ||
                             !mbar_wait(B_(bars->info_read[pb]), (jj / kPBufs) & 1, p.err, abort_flag)) {
                             *abort_flag = 1;
@@ -601,61 +618,70 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         if (rank == 0) {
             // ---- softmax: warpgroup wg takes every other unit
             const uint32_t ptile = base + S_PST + wg * kPUnit, info = ptile + 2 * kSlab;
-            const auto query = [&](const Walk &v, bool &valid) {
-                valid = row < v.t.rows;
-                const long long r0 = static_cast<long long>(v.seq) * p.T * p.H + static_cast<long long>(v.index) * kM;
-                return reinterpret_cast<const uint4 *>(p.q_abs + (r0 + (valid ? row : 0)) * kR) + wg * 32;
-            };
-            uint32_t jb = 0;
+            uint32_t jb = 0, it = 0;   // units; places in the ring
             bool ok = true;
-            bool more = w.next(p);
-            if (more) {
-                bool valid;
-                const uint4 *const src = query(w, valid);
-                uint4 v[16];
-#pragma unroll 1
-                for (int half = 0; half < 2; ++half) {
-                    q_issue(src, valid, half, v);
-                    q_store(trow + wg * 128, half, v);
-                }
-                tmem_wait_st();
-                tc_fence_before();
-                mbar_arrive(B_(bars->q_ready));
-            }
             // A failed wait is voted on at the next barrier of the warpgroup, which no warp leaves alone.
             bool fail = false;
             const auto wait_warp = [&](uint64_t &bar, uint32_t parity) {
                 return __any_sync(0xffffffffu, fail || !mbar_wait(B_(bar), parity, p.err, abort_flag));
             };
+            // A part's queries into TMEM: a row's packed bf16 pairs are its 32-bit words in memory order.  Warpgroup wg
+            // moves latent columns [256 wg, 256 wg + 256), four stages of 64.
+            const auto load_q = [&](bool active) {
+#pragma unroll 1
+                for (int k = 0; k < 4; ++k) {
+                    const uint32_t at = it + wg * 4 + k, st = at % kSStages;
+                    fail = wait_warp(bars->sc_full[st], (at / kSStages) & 1);
+                    if (active) {
+                        float v[32];
+#pragma unroll
+                        for (int i = 0; i < 8; ++i) {
+                            const uint4 x = ld_shared_v4(base + st * kStage + sw128_offset(row, i));
+                            v[4 * i] = __uint_as_float(x.x), v[4 * i + 1] = __uint_as_float(x.y);
+                            v[4 * i + 2] = __uint_as_float(x.z), v[4 * i + 3] = __uint_as_float(x.w);
+                        }
+                        tmem_st32(trow + (wg * 4 + k) * 32, v);
+                    }
+                }
+                tmem_wait_st();
+                tc_fence_before();
+                mbar_arrive(B_(bars->q_ready));
+                fence_proxy_async_smem();   // TMA writes to these stages again
+                named_bar_sync(2 + wg, 128);
+                if (first_thread)
+                    for (int k = 0; k < 4; ++k) mbar_arrive(B_(bars->sc_empty[(it + wg * 4 + k) % kSStages]));
+            };
+            const auto has_rows = [&](const Walk &v) { return (warp & 3) * 32 < v.t.rows; };
+            bool more = w.next(p);
+            if (more) load_q(has_rows(w));
             while (ok && more) {
                 const int len = w.seq_len(p);
-                const Sight sight(p, w.seq, min((w.index * kM + row) / p.H, w.t.t1), len);
+                const Sight sight(p, w.seq, min((w.index * kM + row) / p.H, w.t.t1), len, w.count, lane);
                 const int i0 = w.i0, i1 = w.i1, slot = w.slot(cl), rows = w.t.rows;
                 const Tile tile = w.t;
-                const bool whole = w.whole();
-                more = w.next(p);   // the next part's query goes into TMEM after this one's last product
+                const bool whole = w.whole(), active = has_rows(w);
+                it += 8 * (1 + i1 - i0);   // where the next part's queries are
+                more = w.next(p);          // they go into TMEM after this one's last product
                 float m_mine = -INFINITY, l = 0.f;
                 for (int i = i0; ok && i < i1; ++i, ++jb) {
                     const bool mine = (jb & 1) == static_cast<uint32_t>(wg), last = i == i1 - 1;
                     if (!mine && !(last && more)) continue;
-                    if (last && more) {
-                        bool valid;
-                        const uint4 *const src = query(w, valid);
-                        uint4 v[16];   // half the query rides across the wait
-                        q_issue(src, valid, 0, v);
-                        fail = wait_warp(bars->s_full[jb & 1], (jb >> 1) & 1);
-                        tc_fence_after();
-                        q_store(trow + wg * 128, 0, v);
-                        q_issue(src, valid, 1, v);
-                        q_store(trow + wg * 128, 1, v);
-                        tmem_wait_st();
-                        tc_fence_before();
-                        mbar_arrive(B_(bars->q_ready));
-                        if (!mine) continue;
-                    } else {
-                        fail = wait_warp(bars->s_full[jb & 1], (jb >> 1) & 1);
-                    }
+                    fail = wait_warp(bars->s_full[jb & 1], (jb >> 1) & 1);
                     tc_fence_after();
+                    if (last && more) {
+                        load_q(has_rows(w));
+                        if (!mine) continue;
+                    }
+                    if (!active) {   // none of the tile's rows are this warp's
+                        mbar_arrive(B_(bars->s_free[jb & 1]));
+                        mbar_arrive(B_(bars->m_ready[wg]));
+                        if (first_thread) bulk_wait_read_all();
+                        if (named_bar_or(2 + wg, 128, fail)) { ok = false; break; }
+                        st_shared_v2f(info + row * 8, 1.f, 0.f);
+                        fence_proxy_async_smem();
+                        named_bar_sync(2 + wg, 128);
+                        continue;
+                    }
                     float s[4][32];
 #pragma unroll
                     for (int c4 = 0; c4 < 4; ++c4) tmem_ld32(trow + S_COL + (jb & 1) * 128 + c4 * 32, s[c4]);
@@ -801,48 +827,69 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                 fail = !mbar_wait(B_(bars->pv_done[prev % kPBufs]), (prev / kPBufs) & 1, p.err, abort_flag);
                 if (named_bar_or(4, 256, fail)) { ok = false; break; }
                 tc_fence_after();
-                const bool whole = w.whole(), valid = row < w.t.rows;
+                const bool whole = w.whole();
                 const float sum = l_old + l_new, inv = 1.f / sum;
-                const long long g = static_cast<long long>(w.seq) * p.T * p.H + static_cast<long long>(w.index) * kM + row;
-                const size_t part = static_cast<size_t>(w.slot(cl)) * kM + row;
+                const int quad = (warp & 3) * 32, rows = min(w.t.rows - quad, 32);   // of the tile's, this warp's
+                const long long g = static_cast<long long>(w.seq) * p.T * p.H + static_cast<long long>(w.index) * kM + quad;
+                const size_t part = static_cast<size_t>(w.slot(cl)) * kM + quad;
+                if (rows > 0) {
+                    // A lane has a row; a warp's 4 KB of the buffer turn 32 columns of 32 rows, so that stores fill whole
+                    // lines (14,500 cycles for a tile's 256 KB with each lane storing its row, 32 bytes at a time)
+                    const uint32_t turn = base + (prev % kPBufs) * kPUnit + (warp - 4) * 4096;
 #pragma unroll 1
-                for (int cc = 0; cc < 8; ++cc) {
-                    float v[32];
-                    tmem_ld32(trow + wg * 256 + cc * 32, v);
-                    tmem_wait_ld();
-                    if (!valid) continue;
-                    if (whole) {
-                        uint32_t hi[16], lo[16];
+                    for (int cc = 0; cc < 8; ++cc) {
+                        float v[32];
+                        tmem_ld32(trow + wg * 256 + cc * 32, v);
+                        tmem_wait_ld();
+                        if (whole) {   // 64 bytes of either bf16 part
 #pragma unroll
-                        for (int k = 0; k < 16; ++k) hi[k] = split_bf16x2(v[2 * k] * inv, v[2 * k + 1] * inv, lo[k]);
-                        __nv_bfloat16 *const dst = p.ws_rows + g * kR + wg * 256 + cc * 32;
+                            for (int k = 0; k < 4; ++k) {
+                                uint32_t hi[4], lo[4];
 #pragma unroll
-                        for (int k = 0; k < 2; ++k) {
-                            st_global_32B(dst + 16 * k, make_uint4(hi[8 * k], hi[8 * k + 1], hi[8 * k + 2], hi[8 * k + 3]),
-                                          make_uint4(hi[8 * k + 4], hi[8 * k + 5], hi[8 * k + 6], hi[8 * k + 7]));
-                            st_global_32B(dst + p.plane + 16 * k,
-                                          make_uint4(lo[8 * k], lo[8 * k + 1], lo[8 * k + 2], lo[8 * k + 3]),
-                                          make_uint4(lo[8 * k + 4], lo[8 * k + 5], lo[8 * k + 6], lo[8 * k + 7]));
+                                for (int q = 0; q < 4; ++q)
+                                    hi[q] = split_bf16x2(v[8 * k + 2 * q] * inv, v[8 * k + 2 * q + 1] * inv, lo[q]);
+                                st_shared_v4(turn + lane * 128 + ((k ^ (lane & 7)) << 4), hi[0], hi[1], hi[2], hi[3]);
+                                st_shared_v4(turn + lane * 128 + (((4 + k) ^ (lane & 7)) << 4), lo[0], lo[1], lo[2], lo[3]);
+                            }
+                        } else {
+#pragma unroll
+                            for (int k = 0; k < 8; ++k)
+                                st_shared_v4(turn + lane * 128 + ((k ^ (lane & 7)) << 4), __float_as_uint(v[4 * k]),
+                                             __float_as_uint(v[4 * k + 1]), __float_as_uint(v[4 * k + 2]),
+                                             __float_as_uint(v[4 * k + 3]));
                         }
-                    } else {
-                        float *const dst = p.ws_o + part * kR + wg * 256 + cc * 32;
+                        __syncwarp();
+                        const int piece = lane & 7;   // 16 bytes of a row; four rows at a time
 #pragma unroll
-                        for (int q = 0; q < 4; ++q) {
-                            const uint32_t *x = reinterpret_cast<const uint32_t *>(&v[8 * q]);
-                            st_global_32B(dst + 8 * q, make_uint4(x[0], x[1], x[2], x[3]), make_uint4(x[4], x[5], x[6], x[7]));
+                        for (int k = 0; k < 8; ++k) {
+                            const int r = k * 4 + (lane >> 3);
+                            const uint4 x = ld_shared_v4(turn + r * 128 + ((piece ^ (r & 7)) << 4));
+                            if (r >= rows) continue;
+                            const int col = wg * 256 + cc * 32;
+                            if (whole) {
+                                __nv_bfloat16 *const dst = p.ws_rows + (piece < 4 ? 0 : p.plane) + (g + r) * kR + col;
+                                reinterpret_cast<uint4 *>(dst)[piece & 3] = x;
+                            } else {
+                                reinterpret_cast<uint4 *>(p.ws_o + (part + r) * kR + col)[piece] = x;
+                            }
                         }
+                        __syncwarp();
                     }
+                    if (wg == 0 && lane < rows && !whole) p.ws_l[part + lane] = sum;
                 }
-                if (wg == 0 && valid && !whole) p.ws_l[part] = sum;
                 if (threadIdx.x == 128) {
                     int2 *const tile = p.ws_tile + static_cast<long long>(w.seq) * p.tiles + w.index;
                     if (w.i0 == 0) tile->x = cl;
                     if (w.i1 == w.t.n) tile->y = cl;
                     if (w.i0 == 0 && w.i1 < w.t.n) cut = make_int2(w.seq, w.index);
                 }
+                fence_proxy_async_smem();   // the next P's copy follows
                 tc_fence_before();
                 named_bar_sync(4, 256);
-                if (threadIdx.x == 128) mbar_arrive(B_(bars->drained));
+                if (threadIdx.x == 128) {
+                    mbar_arrive(B_(bars->drained));
+                    mbar_arrive_remote(B_(bars->p_free[prev % kPBufs]), 0);
+                }
             }
             if (threadIdx.x == 128) p.ws_cut[cl] = cut;
             if (!ok) *abort_flag = 1;
@@ -1018,6 +1065,7 @@ __global__ void __launch_bounds__(kFewThreads, 2)
     int b = 0, t = 0;
     const bool token = threadIdx.x < rows && is_token(p, m0 + threadIdx.x, b, t);
     grid_dependency_wait();
+    grid_launch_dependents();
     if (threadIdx.x < kFewRows) {
         const long long r = static_cast<long long>(t) * p.H + h;
         s_tile[threadIdx.x] = token ? p.ws_tile[static_cast<long long>(b) * p.tiles + r / kM] : make_int2(-1, -1);
@@ -1193,6 +1241,7 @@ __global__ void __launch_bounds__(kUpThreads, 2)
     tc_fence_after();
     const uint32_t tmem = *tmem_slot;
     grid_dependency_wait();
+    grid_launch_dependents();
     if (warp == 0) {
         if (lane == 0) {
             fence_proxy_async_all();
@@ -1322,7 +1371,7 @@ cudaError_t launch_attend_paged(const AttendPagedArgs &a, cudaStream_t s) {
     int G = 0;
     cudaError_t e = prepare(a.num_sms, G);
     if (e != cudaSuccess) return e;
-    CUtensorMap tm_s, tm_v, tm_w;
+    CUtensorMap tm_q, tm_s, tm_v, tm_w;
     {
         const long long rows = static_cast<long long>(a.num_blocks) * a.bs;
         const void *const pool = rows > 0 ? a.pool : a.q_abs;   // no row of an empty pool is inside its map
@@ -1332,7 +1381,9 @@ cudaError_t launch_attend_paged(const AttendPagedArgs &a, cudaStream_t s) {
         const cuuint32_t box_s[2] = {64, 64}, box_v[3] = {64, kVRows, 4};
         const cuuint64_t dims_w[2] = {kR, static_cast<cuuint64_t>(a.H) * kDV}, strides_w[1] = {kR * 2};
         const cuuint32_t box_w[2] = {64, kDV};
-        if (encode_map(&tm_s, pool, 2, dims_s, strides_s, box_s) != CUDA_SUCCESS ||
+        const cuuint64_t dims_q[2] = {kR, static_cast<cuuint64_t>(a.B) * a.T * a.H};
+        if (encode_map(&tm_q, a.q_abs, 2, dims_q, strides_w, box_s) != CUDA_SUCCESS ||
+            encode_map(&tm_s, pool, 2, dims_s, strides_s, box_s) != CUDA_SUCCESS ||
             encode_map(&tm_v, pool, 3, dims_v, strides_v, box_v) != CUDA_SUCCESS ||
             encode_map(&tm_w, a.w_uv, 2, dims_w, strides_w, box_w) != CUDA_SUCCESS)
             return cudaErrorInvalidValue;
@@ -1344,11 +1395,11 @@ cudaError_t launch_attend_paged(const AttendPagedArgs &a, cudaStream_t s) {
     int2 *const ws_tile = reinterpret_cast<int2 *>(ws + sp.tile), *const ws_cut = reinterpret_cast<int2 *>(ws + sp.cut);
     const long long m = static_cast<long long>(a.B) * a.T;
     const size_t plane = static_cast<size_t>(m) * a.H * kR;
-    const PairParams pp{static_cast<const __nv_bfloat16 *>(a.q_abs), a.table, a.lens, a.counts, a.parents, a.ld_table,
+    const PairParams pp{a.table, a.lens, a.counts, a.parents, a.ld_table,
                         ws_rows, ws_o, ws_m, ws_l, ws_tile, ws_cut, plane, a.dev_err, a.B, a.T, a.H, sp.tiles,
                         a.num_blocks, a.bs, a.max_blocks, a.window, a.sinks, a.scale * kLog2e};
     note_launch();
-    e = launch_dependent(attend_pair_kernel, dim3(2 * G), kThreads, kSmemPair, s, tm_s, tm_v, pp);
+    e = launch_dependent(attend_pair_kernel, dim3(2 * G), kThreads, kSmemPair, s, tm_q, tm_s, tm_v, pp);
     if (e != cudaSuccess) return e;
     const UpParams up{a.lens, a.counts, ws_rows, ws_o, ws_m, ws_l, ws_tile, ws_cut, plane,
                       static_cast<const __nv_bfloat16 *>(a.gate), static_cast<__nv_bfloat16 *>(a.out), a.dev_err, a.B, a.T,

@@ -56,6 +56,7 @@ __global__ void __launch_bounds__(kReserveThreads) reserve_latent_blocks_kernel(
     int *const take = pre, *const give = pre + p.B + 1;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     grid_dependency_wait();
+    grid_launch_dependents();
     const int F = *p.free_count;
     const int per = (p.B + kReserveThreads - 1) / kReserveThreads;
     const int b0 = min(tid * per, p.B), b1 = min(b0 + per, p.B);
@@ -174,6 +175,7 @@ struct AppendParams {
 template <typename T, int N>
 __global__ void __launch_bounds__(kAppendThreads) append_latent_paged_kernel(const AppendParams p) {
     grid_dependency_wait();
+    grid_launch_dependents();
     const T *const c = static_cast<const T *>(p.c);
     const long long i0 = static_cast<long long>(blockIdx.x) * (N * kAppendThreads) + threadIdx.x;
     uint4 v[N];
