@@ -19,8 +19,9 @@
 // Each CTA loads the rows it needs: boxes of 64 (score) or 32 rows, which lie inside one block of the pool.
 //
 // Masks are bit sets of 128 rows per row of the tile, used only in units that some of the tile's tokens do not see whole.
-// There the value CTA's math warps also replace what is not finite in the rows by zeros before the product: 0 * NaN of a
-// row that a token does not see would reach it; a token that does see one gets its NaN through the sum of its weights.
+// A NaN or an infinity in a row of such a unit would reach the tokens that do not see it, as 0 * NaN.  It shows in the
+// row's scores with any query: then the value CTA's math warps replace what is not finite in the unit by zeros before the
+// product, and a token that does see it gets its NaN through the sum of its weights.
 //
 // A tile that one cluster walked whole leaves o_lat / l as rows of two bf16 parts (16 bits of each value: their product
 // with W_UV is as good as fp32's); a tile cut between clusters leaves fp32 sums with their maxima and weights, at most two
@@ -50,7 +51,7 @@ constexpr float kRescaleLog2 = 16.0f;
 constexpr int kStart = 8;
 
 constexpr uint32_t kSlab = 16384;                  // [128 rows x 64 columns] bf16, 128-byte swizzle
-constexpr uint32_t kInfo = kM * 8;                 // {rescaling factor, sum} per row of the tile
+constexpr uint32_t kInfo = kM * 8;                 // {rescaling factor, negative to ask for cleaning, sum} per row of the tile
 constexpr uint32_t kPUnit = 2 * kSlab + kInfo;     // P [128 x 128] and its info
 constexpr uint32_t kStage = 16384;                 // of either ring
 // score CTA: stages of [128 cache rows x 64 latent columns], P staging per warpgroup, running maxima per warpgroup
@@ -411,12 +412,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         __syncthreads();
     }
 
-    // The pool row of cache row u (u % 32 == 0) of a sequence, or one past the pool, which reads as zeros.
-    const auto pool_row = [&](int seq, int u) {
+    // The pool row of cache row u (u % 64 == 0) of a sequence, or one past the pool, which reads as zeros.
+    const auto pool_row = [&](int seq, int u, int end) {
+        const int none = max(p.num_blocks * p.bs, 1);
+        if (u >= end) return none;
         const int j = u / p.bs, block = __ldg(p.table + seq * p.ld_table + j);
         if (block < 0 || block >= p.num_blocks) {
             record_error(p.err, kDevErrBounds);
-            return max(p.num_blocks * p.bs, 1);
+            return none;
         }
         return block * p.bs + (u - j * p.bs);
     };
@@ -446,21 +449,16 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                         const bool units = i >= w.i0;
                         const int u = units ? w.t.row0(i) + half * 64 : 0;
                         // rows past the tile's, of the next one or past the tensor's end (zeros), are not used
-                        const int row = !units ? (half * 64 < w.t.rows ? w.seq * p.T * p.H + w.index * kM + half * 64 : -1)
-                                        : u < w.t.end ? pool_row(w.seq, u) : -1;
+                        const int row = units ? pool_row(w.seq, u, w.t.end) : w.seq * p.T * p.H + w.index * kM + half * 64;
 #pragma unroll 1
                         for (int kc = 0; kc < 8; ++kc, ++it, at.next()) {
                             // a barrier that no one has arrived at counts as past phase 1
                             if (!(ok = wait(empty0 + at.st * 8, at.phase ^ 1))) break;
                             if (!lead) continue;
                             const uint32_t full = full0 + at.st * 8;
-                            if (row < 0) {   // past the last row that is seen: masked, whatever the stage holds
-                                mbar_arrive(full);
-                            } else {
-                                mbar_arrive_expect_tx(full, kStage / 2);
-                                tma_load_2d(base + at.st * kStage + half * (kStage / 2), units ? &tm_s : &tm_q, full,
-                                            kc * 64, row);
-                            }
+                            mbar_arrive_expect_tx(full, kStage / 2);
+                            tma_load_2d(base + at.st * kStage + half * (kStage / 2), units ? &tm_s : &tm_q, full, kc * 64,
+                                        row);
                         }
                     }
                 }
@@ -517,20 +515,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                 while (ok && w.next(p)) {
                     for (int i = w.i0; ok && i < w.i1; ++i, it += 8) {
                         const int u = w.t.row0(i) + half * 64;
-                        const int row = u < w.t.end ? pool_row(w.seq, u) : -1;
+                        const int row = pool_row(w.seq, u, w.t.end);
 #pragma unroll 1
                         for (int k = 0; ok && k < 8; ++k, at.next()) {
                             if (((k >> 1) & 1) != half) continue;
                             if (!(ok = wait(empty0 + at.st * 8, at.phase ^ 1))) break;
                             if (!lead) continue;
                             const uint32_t full = full0 + at.st * 8;
-                            if (row < 0) {
-                                mbar_arrive(full);
-                            } else {
-                                mbar_arrive_expect_tx(full, kStage);
-                                tma_load_3d(base + V_RING + at.st * kStage, &tm_v, full, 0, row + (k & 1) * kVRows,
-                                            (k >> 2) * 4);
-                            }
+                            mbar_arrive_expect_tx(full, kStage);
+                            tma_load_3d(base + V_RING + at.st * kStage, &tm_v, full, 0, row + (k & 1) * kVRows, (k >> 2) * 4);
                         }
                     }
                 }
@@ -547,32 +540,34 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                 uint32_t fix_phase = 0, drain_phase = 1, cleaned = 0;   // cleaned: a phase bit per stage
                 bool ok = true;
                 while (ok && w.next(p)) {
-                    const int len = w.seq_len(p);
                     const uint32_t bytes = 2u * ((w.t.rows + 7) & ~7) * 128u + kInfo;
 #pragma unroll 1
                     for (int i = w.i0; ok && i < w.i1; ++i, pb.next()) {
-                        const bool first = i == w.i0, mixed = w.t.mixed(p, len, w.t.row0(i));
+                        const bool first = i == w.i0;
                         const uint32_t p_full = p_full0 + pb.st * 8;
                         if (lead) mbar_arrive_expect_tx(p_full, bytes);
                         if (!(ok = __all_sync(0xffffffffu, mbar_wait<true>(p_full, pb.phase, p.err, abort_flag)))) break;
+                        const uint32_t info = base + pb.st * kPUnit + 2 * kSlab;
+                        bool grew = false, dirty = false;
+#pragma unroll
+                        for (int k = 0; k < 4; ++k) {
+                            const float f = ld_shared_f32(info + (lane + 32 * k) * 8);
+                            grew |= fabsf(f) != 1.f, dirty |= signbit(f);
+                        }
+                        dirty = __any_sync(0xffffffffu, dirty);
                         if (first) {   // the accumulator of the part before has been drained
                             if (!(ok = wait(B_(bars->drained), drain_phase))) break;
                             drain_phase ^= 1;
-                        } else {   // rows whose maximum grew need their accumulator rescaled before this unit's product
-                            const uint32_t info = base + pb.st * kPUnit + 2 * kSlab;
-                            bool grew = false;
-#pragma unroll
-                            for (int k = 0; k < 4; ++k) grew |= ld_shared_f32(info + (lane + 32 * k) * 8) != 1.f;
-                            if (__any_sync(0xffffffffu, grew)) {
-                                if (!(ok = wait(B_(bars->rescaled), fix_phase))) break;
-                                fix_phase ^= 1;
-                            }
+                        } else if (__any_sync(0xffffffffu, grew)) {
+                            // rows whose maximum grew need their accumulator rescaled before this unit's product
+                            if (!(ok = wait(B_(bars->rescaled), fix_phase))) break;
+                            fix_phase ^= 1;
                         }
                         uint64_t a = desc_add(pdesc, pb.st * kPUnit);
 #pragma unroll 1
                         for (int k = 0; k < 8; ++k, at.next()) {   // latent half k >> 2, row quarter k & 3
                             if (!(ok = wait(full0 + at.st * 8, at.phase))) break;
-                            if (mixed) {
+                            if (dirty) {
                                 if (!(ok = wait(clean0 + at.st * 8, (cleaned >> at.st) & 1))) break;
                                 cleaned ^= 1u << at.st;
                             }
@@ -691,6 +686,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                     // The scale multiplies inside the exponent: the largest of c s is c max(s) for c >= 0, c min(s)
                     // otherwise.  Masked units multiply first.
                     float mul = p.scale_log2;
+                    bool dirty = false;
                     const int u0 = tile.row0(i);
                     if (tile.mixed(p, len, u0)) {
                         mul = 1.f;
@@ -700,10 +696,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 #pragma unroll
                             for (int k = 0; k < 32; ++k) {
                                 // an infinite score's row gives NaN, as its product with the weight 0 would
-                                const float x = fabsf(s[c4][k]) == INFINITY ? NAN : s[c4][k] * p.scale_log2;
+                                const bool finite = fabsf(s[c4][k]) < INFINITY;
+                                dirty |= !finite;
+                                const float x = finite ? s[c4][k] * p.scale_log2 : NAN;
                                 s[c4][k] = (seen >> k) & 1 ? x : -INFINITY;
                             }
                         }
+                        dirty = dirty && row < rows;
                     }
                     const float mx = mul >= 0.f ? mul * reduce128(s, [](float a, float b) { return fmaxf(a, b); })
                                                 : mul * reduce128(s, [](float a, float b) { return fminf(a, b); });
@@ -738,7 +737,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                                          pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]), pack_bf16x2(v[4], v[5]),
                                          pack_bf16x2(v[6], v[7]));
                         }
-                    st_shared_v2f(info + row * 8, factor, l);
+                    st_shared_v2f(info + row * 8, dirty ? -factor : factor, l);
                     fence_proxy_async_smem();
                     named_bar_sync(2 + wg, 128);
                     if (first_thread) {
@@ -770,17 +769,20 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             int2 cut = make_int2(-1, 0);
             bool ok = true, fail;
             while (ok && w.next(p)) {
-                const int len = w.seq_len(p);
                 float l_old = 0.f, l_new = 0.f;   // the sums of the two warpgroups of the score CTA
                 for (int i = w.i0; i < w.i1; ++i, ++jj, it += 8) {
                     const uint32_t pb = jj % kPBufs;
                     fail = !mbar_wait<true>(B_(bars->p_full[pb]), (jj / kPBufs) & 1, p.err, abort_flag);
                     if (named_bar_or(4, 256, fail)) { ok = false; break; }
-                    const float2 fl = ld_shared_v2f(base + pb * kPUnit + 2 * kSlab + row * 8);
+                    float2 fl = ld_shared_v2f(base + pb * kPUnit + 2 * kSlab + row * 8);
                     mbar_arrive(B_(bars->info_read[pb]));
+                    const bool dirty = signbit(fl.x);
+                    fl.x = fabsf(fl.x);
                     l_old = i == w.i0 ? 0.f : l_new * fl.x;
                     l_new = fl.y;
-                    if (named_bar_or(4, 256, i > w.i0 && fl.x != 1.f)) {
+                    const bool grew = i > w.i0 && fl.x != 1.f;
+                    const bool any_dirty = named_bar_or(4, 256, dirty), any_grew = named_bar_or(5, 256, grew);
+                    if (any_grew) {
                         const uint32_t prev = jj - 1;
                         fail = !mbar_wait(B_(bars->pv_done[prev % kPBufs]), (prev / kPBufs) & 1, p.err, abort_flag);
                         if (named_bar_or(4, 256, fail)) { ok = false; break; }
@@ -801,7 +803,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                         tc_fence_before();
                         mbar_arrive(B_(bars->rescaled));
                     }
-                    if (w.t.mixed(p, len, w.t.row0(i))) {
+                    if (any_dirty) {
                         for (int k = 0; k < 8; ++k) {
                             const uint32_t s = it + k, st = s % kVStages;
                             fail = !mbar_wait(B_(bars->v_full[st]), (s / kVStages) & 1, p.err, abort_flag);
