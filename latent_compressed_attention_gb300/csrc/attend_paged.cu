@@ -23,10 +23,12 @@
 // row's scores with any query: then the value CTA's math warps replace what is not finite in the unit by zeros before the
 // product, and a token that does see it gets its NaN through the sum of its weights.
 //
-// A tile that one cluster walked whole leaves o_lat / l as rows of two bf16 parts (16 bits of each value: their product
-// with W_UV is as good as fp32's); a tile cut between clusters leaves fp32 sums with their maxima and weights, at most two
-// such parts per cluster.  Up to 64 tokens one kernel joins those, applies W_UV^T on the tensor cores and the gate; above,
-// a kernel joins them into rows and a plain product per head follows, its operands by TMA.
+// A cluster leaves o_lat / l of its part of a tile, with the maxima and the sums of weights where the tile was cut between
+// clusters (at most two such parts per cluster).  The values go as f16 with an exponent for each 32 of a row: off by
+// 2^-12, a sixteenth of what rounding the output costs, in half of fp32's bytes, which is what a part's end takes (an SM
+// stores 27 bytes a cycle: 256 KB of fp32 took as long as four units).  Up to 64 tokens one kernel joins the parts, applies
+// W_UV^T on the tensor cores and the gate; above, a kernel joins them and a product per head follows.  Both take the
+// values to the product as two bf16 parts, which hold them exactly.
 #include <cuda.h>
 #include <cudaTypedefs.h>
 
@@ -92,11 +94,12 @@ static_assert(sizeof(PairBars) <= 768, "barrier block too large");
 struct PairParams {
     const int *table, *lens, *counts, *parents;
     long long ld_table;
-    __nv_bfloat16 *ws_rows;              // two planes of [B * T * H][r]: o_lat / l, rounded, and what that leaves
-    float *ws_o, *ws_m, *ws_l;           // [2 G][128][r], [2 G][128]: parts' sums, maxima (log2 units), weights
+    __half *ws_rows;                     // [B * T * H + 2 G * 128][r]: o_lat / l of (token, head) rows, then of parts' rows
+    uint8_t *ws_exp;                     // [.][16]: their exponents
+    float *ws_m, *ws_l;                  // [2 G][128]: parts' maxima (log2 units) and sums of weights
     int2 *ws_tile;                       // [B * tiles]: first and last cluster of each tile
     int2 *ws_cut;                        // [G]: sequence and tile that a cluster starts and leaves unfinished; {-1, .}: none
-    size_t plane;                        // elements of a plane of ws_rows
+    long long all_rows;                  // B * T * H
     int *err;
     int B, T, H, tiles, num_blocks, bs, max_blocks, window, sinks;
     float scale_log2;
@@ -264,15 +267,16 @@ __device__ __forceinline__ void st_shared_v2f(uint32_t addr, float a, float b) {
     asm volatile("st.shared.v2.f32 [%0], {%1, %2};" ::"r"(addr), "f"(a), "f"(b) : "memory");
 }
 
-// Reductions over 128 values as 8 interleaved chains: short chains without many temporaries.
-template <typename F>
-__device__ __forceinline__ float reduce128(const float (&s)[4][32], F f) {
-    float m[8];
-#pragma unroll
-    for (int i = 0; i < 8; ++i) m[i] = s[0][i];
-#pragma unroll
-    for (int k = 8; k < 128; ++k) m[k & 7] = f(m[k & 7], s[k >> 5][k & 31]);
-    return f(f(f(m[0], m[1]), f(m[2], m[3])), f(f(m[4], m[5]), f(m[6], m[7])));
+// Rows of o_lat: [r] f16, and 16 bytes: the biased exponent E of each 32 values' largest.  A value is f16 * 2^(E - 141), so
+// that the largest is below 2^15 and what is 2^28 times smaller keeps its 11 bits.
+__device__ __forceinline__ int row_exponent(float largest) {
+    return max(static_cast<int>(__float_as_uint(largest) >> 23) & 0xFF, 20);   // below 2^-107: as if it were that
+}
+__device__ __forceinline__ float row_up(int E) { return __uint_as_float(static_cast<uint32_t>(268 - E) << 23); }     // 2^(141 - E)
+__device__ __forceinline__ float row_down(int E) { return __uint_as_float(static_cast<uint32_t>(E - 14) << 23); }   // 2^(E - 141)
+__device__ __forceinline__ float2 row_values(uint32_t w, float down) {
+    const float2 v = __half22float2(*reinterpret_cast<const __half2 *>(&w));
+    return make_float2(v.x * down, v.y * down);
 }
 
 // Two values as bf16 and what the rounding leaves, as bf16 again.
@@ -677,35 +681,46 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                         named_bar_sync(2 + wg, 128);
                         continue;
                     }
-                    float s[4][32];
-#pragma unroll
-                    for (int c4 = 0; c4 < 4; ++c4) tmem_ld32(trow + S_COL + (jb & 1) * 128 + c4 * 32, s[c4]);
-                    tmem_wait_ld();
-                    tc_fence_before();
-                    mbar_arrive(B_(bars->s_free[jb & 1]));
-                    // The scale multiplies inside the exponent: the largest of c s is c max(s) for c >= 0, c min(s)
-                    // otherwise.  Masked units multiply first.
-                    float mul = p.scale_log2;
-                    bool dirty = false;
+                    // Two passes over S, 32 columns at a time in rolled loops: the second one's columns are read again,
+                    // so that the code stays short (it comes from DRAM in a call that follows a sweep of L2).  The scale
+                    // multiplies inside the exponent: the largest of c s is c max(s) for c >= 0, c min(s) otherwise.
+                    // Masked units multiply first.
                     const int u0 = tile.row0(i);
-                    if (tile.mixed(p, len, u0)) {
-                        mul = 1.f;
-#pragma unroll
-                        for (int c4 = 0; c4 < 4; ++c4) {
+                    const bool mixed = tile.mixed(p, len, u0);
+                    const float mul = mixed ? 1.f : p.scale_log2;
+                    const uint32_t scol = trow + S_COL + (jb & 1) * 128;
+                    bool dirty = false;
+                    const auto load = [&](int c4, float (&s)[32]) {
+                        tmem_ld32(scol + c4 * 32, s);
+                        tmem_wait_ld();
+                        if (mixed) {
                             const uint32_t seen = sight.word(u0, c4);
 #pragma unroll
                             for (int k = 0; k < 32; ++k) {
                                 // an infinite score's row gives NaN, as its product with the weight 0 would
-                                const bool finite = fabsf(s[c4][k]) < INFINITY;
+                                const bool finite = fabsf(s[k]) < INFINITY;
                                 dirty |= !finite;
-                                const float x = finite ? s[c4][k] * p.scale_log2 : NAN;
-                                s[c4][k] = (seen >> k) & 1 ? x : -INFINITY;
+                                const float x = finite ? s[k] * p.scale_log2 : NAN;
+                                s[k] = (seen >> k) & 1 ? x : -INFINITY;
                             }
                         }
-                        dirty = dirty && row < rows;
+                    };
+                    float mx = -INFINITY, mn = INFINITY;
+#pragma unroll 1
+                    for (int c4 = 0; c4 < 4; ++c4) {
+                        float s[32];
+                        load(c4, s);
+                        if (mul >= 0.f) {
+                            float t[4] = {mx, s[0], s[1], s[2]};
+#pragma unroll
+                            for (int k = 3; k < 32; ++k) t[k & 3] = fmaxf(t[k & 3], s[k]);
+                            mx = fmaxf(fmaxf(t[0], t[1]), fmaxf(t[2], t[3]));
+                        } else {
+#pragma unroll
+                            for (int k = 0; k < 32; ++k) mn = fminf(mn, s[k]);
+                        }
                     }
-                    const float mx = mul >= 0.f ? mul * reduce128(s, [](float a, float b) { return fmaxf(a, b); })
-                                                : mul * reduce128(s, [](float a, float b) { return fminf(a, b); });
+                    mx = mul * (mul >= 0.f ? mx : mn);
                     // the running maximum of the unit before, from the other warpgroup
                     if (jb > 0) fail = wait_warp(bars->m_ready[wg ^ 1], ((jb - 1) >> 1) & 1);
                     const float m_old = i == i0 ? -INFINITY : ld_shared_f32(base + S_MAX + (wg ^ 1) * kM * 4 + row * 4);
@@ -717,26 +732,35 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                     st_shared_f32(base + S_MAX + wg * kM * 4 + row * 4, m);
                     mbar_arrive(B_(bars->m_ready[wg]));
                     const float neg_m = m == -INFINITY ? 0.f : -m;
-#pragma unroll
-                    for (int c4 = 0; c4 < 4; ++c4)
-#pragma unroll
-                        for (int k = 0; k < 32; ++k) s[c4][k] = fast_exp2(fmaf(s[c4][k], mul, neg_m));
-                    l = (m == m_mine ? l : l * fast_exp2(m_mine - m)) + reduce128(s, [](float a, float b) { return a + b; });
+                    if (m != m_mine) l *= fast_exp2(m_mine - m);
                     m_mine = m;
                     if (last && !whole && row < rows) p.ws_m[static_cast<size_t>(slot) * kM + row] = m;
 
                     // the staging unit is free once this warpgroup's copy before has read it
                     if (first_thread) bulk_wait_read_all();
                     if (named_bar_or(2 + wg, 128, fail)) { ok = false; break; }
-#pragma unroll
-                    for (int c4 = 0; c4 < 4; ++c4)
+#pragma unroll 1
+                    for (int c4 = 0; c4 < 4; ++c4) {
+                        float s[32];
+                        load(c4, s);
+                        float t[4] = {l, 0.f, 0.f, 0.f};
+                        const uint32_t slab = ptile + (c4 >> 1) * kSlab;
 #pragma unroll
                         for (int k = 0; k < 4; ++k) {
-                            const float *v = &s[c4][8 * k];
-                            st_shared_v4(ptile + (c4 >> 1) * kSlab + sw128_offset(row, (c4 & 1) * 4 + k),
-                                         pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]), pack_bf16x2(v[4], v[5]),
-                                         pack_bf16x2(v[6], v[7]));
+                            float *v = &s[8 * k];
+#pragma unroll
+                            for (int q = 0; q < 8; ++q) {
+                                v[q] = fast_exp2(fmaf(v[q], mul, neg_m));
+                                t[q & 3] += v[q];
+                            }
+                            st_shared_v4(slab + sw128_offset(row, (c4 & 1) * 4 + k), pack_bf16x2(v[0], v[1]),
+                                         pack_bf16x2(v[2], v[3]), pack_bf16x2(v[4], v[5]), pack_bf16x2(v[6], v[7]));
                         }
+                        l = (t[0] + t[1]) + (t[2] + t[3]);
+                    }
+                    tc_fence_before();
+                    mbar_arrive(B_(bars->s_free[jb & 1]));
+                    dirty = dirty && row < rows;
                     st_shared_v2f(info + row * 8, dirty ? -factor : factor, l);
                     fence_proxy_async_smem();
                     named_bar_sync(2 + wg, 128);
@@ -832,52 +856,51 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                 const bool whole = w.whole();
                 const float sum = l_old + l_new, inv = 1.f / sum;
                 const int quad = (warp & 3) * 32, rows = min(w.t.rows - quad, 32);   // of the tile's, this warp's
-                const long long g = static_cast<long long>(w.seq) * p.T * p.H + static_cast<long long>(w.index) * kM + quad;
-                const size_t part = static_cast<size_t>(w.slot(cl)) * kM + quad;
+                const long long part = static_cast<long long>(w.slot(cl)) * kM + quad;
+                const long long r0 = whole ? static_cast<long long>(w.seq) * p.T * p.H + static_cast<long long>(w.index) * kM + quad
+                                           : p.all_rows + part;
                 if (rows > 0) {
-                    // A lane has a row; a warp's 4 KB of the buffer turn 32 columns of 32 rows, so that stores fill whole
-                    // lines (14,500 cycles for a tile's 256 KB with each lane storing its row, 32 bytes at a time)
+                    // A lane has a row; a warp's 4 KB of the buffer turn 64 columns of 32 rows, so that stores fill whole
+                    // lines
                     const uint32_t turn = base + (prev % kPBufs) * kPUnit + (warp - 4) * 4096;
+                    const int piece = lane & 7;   // 16 bytes of a row; four rows at a time
+                    uint4 *dst = reinterpret_cast<uint4 *>(p.ws_rows + (r0 + (lane >> 3)) * kR + wg * 256) + piece;
+                    uint32_t exps[2] = {0, 0};
 #pragma unroll 1
-                    for (int cc = 0; cc < 8; ++cc) {
-                        float v[32];
-                        tmem_ld32(trow + wg * 256 + cc * 32, v);
+                    for (int cc = 0; cc < 4; ++cc, dst += 8) {
+                        float v[2][32];
+                        tmem_ld32(trow + wg * 256 + cc * 64, v[0]);
+                        tmem_ld32(trow + wg * 256 + cc * 64 + 32, v[1]);
                         tmem_wait_ld();
-                        if (whole) {   // 64 bytes of either bf16 part
 #pragma unroll
-                            for (int k = 0; k < 4; ++k) {
-                                uint32_t hi[4], lo[4];
+                        for (int g = 0; g < 2; ++g) {
+                            float top = 0.f;
 #pragma unroll
-                                for (int q = 0; q < 4; ++q)
-                                    hi[q] = split_bf16x2(v[8 * k + 2 * q] * inv, v[8 * k + 2 * q + 1] * inv, lo[q]);
-                                st_shared_v4(turn + lane * 128 + ((k ^ (lane & 7)) << 4), hi[0], hi[1], hi[2], hi[3]);
-                                st_shared_v4(turn + lane * 128 + (((4 + k) ^ (lane & 7)) << 4), lo[0], lo[1], lo[2], lo[3]);
-                            }
-                        } else {
+                            for (int k = 0; k < 32; ++k) v[g][k] *= inv, top = fmaxf(top, fabsf(v[g][k]));
+                            const int E = row_exponent(top);
+                            const float up = row_up(E);
+                            exps[1] = __funnelshift_r(exps[1], static_cast<uint32_t>(E), 8);   // bytes enter at the top
 #pragma unroll
-                            for (int k = 0; k < 8; ++k)
-                                st_shared_v4(turn + lane * 128 + ((k ^ (lane & 7)) << 4), __float_as_uint(v[4 * k]),
-                                             __float_as_uint(v[4 * k + 1]), __float_as_uint(v[4 * k + 2]),
-                                             __float_as_uint(v[4 * k + 3]));
+                            for (int k = 0; k < 4; ++k)
+                                st_shared_v4(turn + lane * 128 + (((g * 4 + k) ^ (lane & 7)) << 4),
+                                             pack_f16x2(v[g][8 * k] * up, v[g][8 * k + 1] * up),
+                                             pack_f16x2(v[g][8 * k + 2] * up, v[g][8 * k + 3] * up),
+                                             pack_f16x2(v[g][8 * k + 4] * up, v[g][8 * k + 5] * up),
+                                             pack_f16x2(v[g][8 * k + 6] * up, v[g][8 * k + 7] * up));
                         }
+                        if (cc == 1) exps[0] = exps[1];
                         __syncwarp();
-                        const int piece = lane & 7;   // 16 bytes of a row; four rows at a time
 #pragma unroll
                         for (int k = 0; k < 8; ++k) {
                             const int r = k * 4 + (lane >> 3);
-                            const uint4 x = ld_shared_v4(turn + r * 128 + ((piece ^ (r & 7)) << 4));
-                            if (r >= rows) continue;
-                            const int col = wg * 256 + cc * 32;
-                            if (whole) {
-                                __nv_bfloat16 *const dst = p.ws_rows + (piece < 4 ? 0 : p.plane) + (g + r) * kR + col;
-                                reinterpret_cast<uint4 *>(dst)[piece & 3] = x;
-                            } else {
-                                reinterpret_cast<uint4 *>(p.ws_o + (part + r) * kR + col)[piece] = x;
-                            }
+                            if (r < rows) dst[k * 4 * (kR / 8)] = ld_shared_v4(turn + r * 128 + ((piece ^ (r & 7)) << 4));
                         }
                         __syncwarp();
                     }
-                    if (wg == 0 && lane < rows && !whole) p.ws_l[part + lane] = sum;
+                    if (lane < rows) {
+                        *reinterpret_cast<uint2 *>(p.ws_exp + (r0 + lane) * 16 + wg * 8) = make_uint2(exps[0], exps[1]);
+                        if (wg == 0 && !whole) p.ws_l[part + lane] = sum;
+                    }
                 }
                 if (threadIdx.x == 128) {
                     int2 *const tile = p.ws_tile + static_cast<long long>(w.seq) * p.tiles + w.index;
@@ -908,14 +931,34 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 // ----------------------------------------------------------------------------- join, W_UV, gate
 struct UpParams {
     const int *lens, *counts;
-    __nv_bfloat16 *ws_rows;
-    const float *ws_o, *ws_m, *ws_l;
+    __half *ws_rows;
+    uint8_t *ws_exp;
+    const float *ws_m, *ws_l;
     const int2 *ws_tile, *ws_cut;
-    size_t plane;
+    long long all_rows;
     const __nv_bfloat16 *gate;
     __nv_bfloat16 *out;
     int *err;
     int B, T, H, tiles, bs, max_blocks;
+};
+
+// 16 columns of a row by each lane of a warp, as they are stored: f16 and the exponent of the 32 that they are half of.
+struct RowPiece {
+    uint4 v[2];
+    int E;
+    __device__ __forceinline__ void load(const UpParams &p, long long row, int lane) {
+        ld_global_32B(p.ws_rows + row * kR + lane * 16, v[0], v[1]);
+        E = __ldg(p.ws_exp + row * 16 + (lane >> 1));
+    }
+    __device__ __forceinline__ void get(float (&x)[16]) const {
+        const uint32_t w[8] = {v[0].x, v[0].y, v[0].z, v[0].w, v[1].x, v[1].y, v[1].z, v[1].w};
+        const float down = row_down(E);
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+            const float2 y = row_values(w[k], down);
+            x[2 * k] = y.x, x[2 * k + 1] = y.y;
+        }
+    }
 };
 
 // Parts c0, c0 + step, ... of a tile's row r by one warp: the running maximum M (log2 units), the sum of the weights and,
@@ -925,7 +968,7 @@ __device__ __forceinline__ void join_parts(const UpParams &p, int first, int las
 #pragma unroll
     for (int k = 0; k < 16; ++k) o[k] = 0.f;
     M = -INFINITY, sum = 0.f;
-    const auto part = [&](int c) { return static_cast<size_t>(2 * c + (c == first ? 1 : 0)) * kM + r; };
+    const auto part = [&](int c) { return static_cast<long long>(2 * c + (c == first ? 1 : 0)) * kM + r; };
     for (int c = first + c0; c <= last; c += 32 * step) {   // a lane per part: maxima and weights, 32 at a time
         const int mine = c + lane * step;
         const bool has = mine <= last;
@@ -934,49 +977,35 @@ __device__ __forceinline__ void join_parts(const UpParams &p, int first, int las
 #pragma unroll
         for (int off = 16; off >= 1; off >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, off));
         top = fmaxf(top, M);
-        const float f = M == top ? 1.f : fast_exp2(M - top), g = !has ? 0.f : m == top ? 1.f : fast_exp2(m - top);
-        float lw = has ? g * l : 0.f;
+        // a part that the row sees nothing of has weight 0 and is not read (0 / 0 = NaN)
+        const float f = M == top ? 1.f : fast_exp2(M - top), g = !has || l == 0.f ? 0.f : m == top ? l : fast_exp2(m - top) * l;
+        float w_all = g;
 #pragma unroll
-        for (int off = 16; off >= 1; off >>= 1) lw += __shfl_xor_sync(0xffffffffu, lw, off);
+        for (int off = 16; off >= 1; off >>= 1) w_all += __shfl_xor_sync(0xffffffffu, w_all, off);
         M = top;
-        sum = sum * f + lw;
+        sum = sum * f + w_all;
 #pragma unroll
         for (int k = 0; k < 16; ++k) o[k] *= f;
         const int n = min(32, (last - c) / step + 1);
+#pragma unroll 1
         for (int i = 0; i < n; i += 4) {   // four parts' loads in flight
-            uint4 x[4][4];
+            RowPiece x[4];
             float w[4];
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
-                w[k] = __shfl_sync(0xffffffffu, g, min(i + k, 31));
-                if (i + k < n) {
-                    const float *const src = p.ws_o + part(c + (i + k) * step) * kR + lane * 16;
-                    ld_global_32B(src, x[k][0], x[k][1]);
-                    ld_global_32B(src + 8, x[k][2], x[k][3]);
-                }
+                w[k] = i + k < n ? __shfl_sync(0xffffffffu, g, i + k) : 0.f;
+                if (w[k] != 0.f) x[k].load(p, p.all_rows + part(c + (i + k) * step), lane);
             }
 #pragma unroll
             for (int k = 0; k < 4; ++k)
-                if (i + k < n)
+                if (w[k] != 0.f) {
+                    float y[16];
+                    x[k].get(y);
 #pragma unroll
-                    for (int q = 0; q < 4; ++q) {
-                        o[4 * q] = fmaf(__uint_as_float(x[k][q].x), w[k], o[4 * q]);
-                        o[4 * q + 1] = fmaf(__uint_as_float(x[k][q].y), w[k], o[4 * q + 1]);
-                        o[4 * q + 2] = fmaf(__uint_as_float(x[k][q].z), w[k], o[4 * q + 2]);
-                        o[4 * q + 3] = fmaf(__uint_as_float(x[k][q].w), w[k], o[4 * q + 3]);
-                    }
+                    for (int q = 0; q < 16; ++q) o[q] = fmaf(y[q], w[k], o[q]);
+                }
         }
     }
-}
-
-// o / sum in its two parts.
-__device__ __forceinline__ void split_row(const float (&o)[16], float sum, uint4 (&hi)[2], uint4 (&lo)[2]) {
-    const float inv = 1.f / sum;
-    uint32_t h[8], l[8];
-#pragma unroll
-    for (int k = 0; k < 8; ++k) h[k] = split_bf16x2(o[2 * k] * inv, o[2 * k + 1] * inv, l[k]);
-    hi[0] = make_uint4(h[0], h[1], h[2], h[3]), hi[1] = make_uint4(h[4], h[5], h[6], h[7]);
-    lo[0] = make_uint4(l[0], l[1], l[2], l[3]), lo[1] = make_uint4(l[4], l[5], l[6], l[7]);
 }
 
 // 32 output columns of a token's head from TMEM, with the gate.
@@ -1076,74 +1105,64 @@ __global__ void __launch_bounds__(kFewThreads, 2)
     __syncthreads();
     int per_row = 1;   // warps
     while (rows * per_row * 2 <= kFewWarps) per_row *= 2;
-    const auto store_row = [&](int i, const uint4 (&hi)[2], const uint4 (&lo)[2]) {
+    const auto store_row = [&](int i, const float (&o)[16], float mul) {
         const uint32_t slab = base + (lane >> 2) * kFewSlab;
 #pragma unroll
         for (int k = 0; k < 2; ++k) {
+            uint32_t hi[4], lo[4];
+#pragma unroll
+            for (int q = 0; q < 4; ++q) hi[q] = split_bf16x2(o[8 * k + 2 * q] * mul, o[8 * k + 2 * q + 1] * mul, lo[q]);
             const uint32_t at = slab + sw128_offset(i, (lane & 3) * 2 + k);
-            st_shared_v4(at, hi[k].x, hi[k].y, hi[k].z, hi[k].w);
-            st_shared_v4(at + 8 * kFewSlab, lo[k].x, lo[k].y, lo[k].z, lo[k].w);
+            st_shared_v4(at, hi[0], hi[1], hi[2], hi[3]);
+            st_shared_v4(at + 8 * kFewSlab, lo[0], lo[1], lo[2], lo[3]);
         }
     };
-    if (per_row == 1) {
-        for (int i = warp; i < rows; i += kFewWarps) {
-            const int2 tile = s_tile[i];
-            uint4 hi[2] = {}, lo[2] = {};
-            if (tile.x >= 0 && tile.x == tile.y) {
-                const __nv_bfloat16 *const src = p.ws_rows + ((m0 + i) * p.H + h) * kR + lane * 16;
-                ld_global_32B(src, hi[0], hi[1]);
-                ld_global_32B(src + p.plane, lo[0], lo[1]);
-            } else if (tile.x >= 0) {
-                float o[16], M, sum;
-                join_parts(p, tile.x, tile.y, s_row[i], 0, 1, lane, o, M, sum);
-                split_row(o, sum, hi, lo);
-            }
-            store_row(i, hi, lo);
-        }
-    } else {
-        const int i = warp / per_row, c0 = warp % per_row;
-        const bool mine = i < rows;
-        const int2 tile = mine ? s_tile[i] : make_int2(-1, -1);
+    for (int i0 = 0; i0 < rows; i0 += kFewWarps / per_row) {
+        const int i = i0 + warp / per_row, c0 = warp % per_row;
+        const int2 tile = i < rows ? s_tile[i] : make_int2(-1, -1);
         const bool cut = tile.x >= 0 && tile.x != tile.y;
-        float o[16], M = -INFINITY, sum = 0.f;
+        float o[16], M = -INFINITY, sum = 1.f;
         if (cut) {
             join_parts(p, tile.x, tile.y, s_row[i], c0, per_row, lane, o, M, sum);
-#pragma unroll
-            for (int k = 0; k < 4; ++k)
-                st_shared_v4(base + warp * (kR * 4) + k * 512 + lane * 16, __float_as_uint(o[4 * k]),
-                             __float_as_uint(o[4 * k + 1]), __float_as_uint(o[4 * k + 2]), __float_as_uint(o[4 * k + 3]));
-            if (lane == 0) s_m[warp] = M, s_sum[warp] = sum;
+        } else if (tile.x >= 0 && c0 == 0) {
+            RowPiece x;
+            x.load(p, (m0 + i) * p.H + h, lane);
+            x.get(o);
         }
-        __syncthreads();
-        uint4 hi[2] = {}, lo[2] = {};
-        if (cut && c0 == 0) {   // the row's first warp adds up the others' sums, in their order
-            float top = M;
-            for (int k = 1; k < per_row; ++k) top = fmaxf(top, s_m[warp + k]);
-            const float f = M == top ? 1.f : fast_exp2(M - top);
-            sum *= f;
+        if (per_row > 1) {   // once: the row's first warp adds up the others' sums, in their order
+            if (cut && c0 > 0) {
 #pragma unroll
-            for (int k = 0; k < 16; ++k) o[k] *= f;
-            for (int k = 1; k < per_row; ++k) {
-                const float g = s_m[warp + k] == top ? 1.f : fast_exp2(s_m[warp + k] - top);
-                if (s_m[warp + k] == -INFINITY && top != -INFINITY) continue;   // no part, or one of weight 0
-                sum = fmaf(s_sum[warp + k], g, sum);
+                for (int k = 0; k < 4; ++k)
+                    st_shared_v4(base + warp * (kR * 4) + k * 512 + lane * 16, __float_as_uint(o[4 * k]),
+                                 __float_as_uint(o[4 * k + 1]), __float_as_uint(o[4 * k + 2]), __float_as_uint(o[4 * k + 3]));
+                if (lane == 0) s_m[warp] = M, s_sum[warp] = sum;
+            }
+            __syncthreads();
+            if (cut && c0 == 0) {
+                float top = M;
+                for (int k = 1; k < per_row; ++k) top = fmaxf(top, s_m[warp + k]);
+                const float f = M == top ? 1.f : fast_exp2(M - top);
+                sum *= f;
 #pragma unroll
-                for (int q = 0; q < 4; ++q) {
-                    const uint4 x = ld_shared_v4(base + (warp + k) * (kR * 4) + q * 512 + lane * 16);
-                    o[4 * q] = fmaf(__uint_as_float(x.x), g, o[4 * q]);
-                    o[4 * q + 1] = fmaf(__uint_as_float(x.y), g, o[4 * q + 1]);
-                    o[4 * q + 2] = fmaf(__uint_as_float(x.z), g, o[4 * q + 2]);
-                    o[4 * q + 3] = fmaf(__uint_as_float(x.w), g, o[4 * q + 3]);
+                for (int k = 0; k < 16; ++k) o[k] *= f;
+#pragma unroll 1
+                for (int k = 1; k < per_row; ++k) {
+                    if (s_sum[warp + k] == 0.f) continue;
+                    const float g = s_m[warp + k] == top ? 1.f : fast_exp2(s_m[warp + k] - top);
+                    sum = fmaf(s_sum[warp + k], g, sum);
+#pragma unroll
+                    for (int q = 0; q < 4; ++q) {
+                        const uint4 x = ld_shared_v4(base + (warp + k) * (kR * 4) + q * 512 + lane * 16);
+                        o[4 * q] = fmaf(__uint_as_float(x.x), g, o[4 * q]);
+                        o[4 * q + 1] = fmaf(__uint_as_float(x.y), g, o[4 * q + 1]);
+                        o[4 * q + 2] = fmaf(__uint_as_float(x.z), g, o[4 * q + 2]);
+                        o[4 * q + 3] = fmaf(__uint_as_float(x.w), g, o[4 * q + 3]);
+                    }
                 }
             }
-            split_row(o, sum, hi, lo);
-        } else if (tile.x >= 0 && !cut && c0 == 0) {
-            const __nv_bfloat16 *const src = p.ws_rows + ((m0 + i) * p.H + h) * kR + lane * 16;
-            ld_global_32B(src, hi[0], hi[1]);
-            ld_global_32B(src + p.plane, lo[0], lo[1]);
+            __syncthreads();
         }
-        __syncthreads();
-        if (mine && c0 == 0) store_row(i, hi, lo);
+        if (tile.x >= 0 && c0 == 0) store_row(i, o, 1.f / sum);
     }
     fence_proxy_async_smem();
     tc_fence_before();
@@ -1202,17 +1221,24 @@ __global__ void __launch_bounds__(kJoinThreads) attend_join_kernel(const UpParam
     const int2 tile = p.ws_tile[static_cast<long long>(cut.x) * p.tiles + cut.y];
     float o[16], M, sum;
     join_parts(p, tile.x, tile.y, r, 0, 1, lane, o, M, sum);
-    uint4 hi[2], lo[2];
-    split_row(o, sum, hi, lo);
-    __nv_bfloat16 *const dst =
-        p.ws_rows + (static_cast<long long>(cut.x) * p.T * p.H + static_cast<long long>(cut.y) * kM + r) * kR + lane * 16;
-    st_global_32B(dst, hi[0], hi[1]);
-    st_global_32B(dst + p.plane, lo[0], lo[1]);
+    const float inv = 1.f / sum;
+    float top = 0.f;
+#pragma unroll
+    for (int k = 0; k < 16; ++k) o[k] *= inv, top = fmaxf(top, fabsf(o[k]));
+    const int E = row_exponent(fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1)));   // of 32 columns
+    const float up = row_up(E);
+    uint32_t x[8];
+#pragma unroll
+    for (int k = 0; k < 8; ++k) x[k] = pack_f16x2(o[2 * k] * up, o[2 * k + 1] * up);
+    const long long row = static_cast<long long>(cut.x) * p.T * p.H + static_cast<long long>(cut.y) * kM + r;
+    st_global_32B(p.ws_rows + row * kR + lane * 16, make_uint4(x[0], x[1], x[2], x[3]), make_uint4(x[4], x[5], x[6], x[7]));
+    if ((lane & 1) == 0) p.ws_exp[row * 16 + (lane >> 1)] = static_cast<uint8_t>(E);
 }
 
 // Many tokens, then: one CTA per (head, 128 tokens), out = gate * (hi + lo) . W_UV[h]^T over eight slabs of 64 latent
-// columns.  A slab's three operands are a stage of 48 KB; two stages per CTA and two CTAs per SM.
-constexpr int kUpThreads = 192;   // warps 0 TMA, 1 MMA, 2-5 epilogue
+// columns.  A stage takes a slab of f16 rows, which four warps (thread = row) turn into hi in its place and lo beside it,
+// and W_UV's: 48 KB, two stages per CTA and two CTAs per SM.
+constexpr int kUpThreads = 192;   // warps 0 TMA, 1 MMA, 2-5 rows
 constexpr uint32_t kUpStage = 3 * kSlab;
 constexpr uint32_t kUpBars = 2 * kUpStage;
 constexpr uint32_t kUpSmem = kUpBars + 64 + 1024;
@@ -1223,15 +1249,15 @@ __global__ void __launch_bounds__(kUpThreads, 2)
     const uint32_t raw = smem_u32(smem_raw);
     const uint32_t base = (raw + 1023u) & ~1023u;
     uint64_t *const full = reinterpret_cast<uint64_t *>(smem_raw + (base - raw) + kUpBars);   // [2]
-    uint64_t *const empty = full + 2;                                                          // [2]
-    uint64_t *const done = full + 4;
-    uint32_t *const tmem_slot = reinterpret_cast<uint32_t *>(full + 5);
+    uint64_t *const empty = full + 2, *const split = full + 4;                                 // [2] each
+    uint64_t *const done = full + 6;
+    uint32_t *const tmem_slot = reinterpret_cast<uint32_t *>(full + 7);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int h = blockIdx.x % p.H;
     const long long m0 = static_cast<long long>(blockIdx.x / p.H) * kM;
 
     if (threadIdx.x == 0) {
-        for (int i = 0; i < 5; ++i) mbar_init(smem_u32(full + i), 1);
+        for (int i = 0; i < 7; ++i) mbar_init(smem_u32(full + i), i == 4 || i == 5 ? 128 : 1);
         fence_mbar_init();
     }
     if (warp == 1) {
@@ -1253,8 +1279,8 @@ __global__ void __launch_bounds__(kUpThreads, 2)
                 const int st = k & 1;
                 if (k >= 2 && !(ok = mbar_wait(smem_u32(empty + st), ((k >> 1) - 1) & 1, p.err))) break;
                 const uint32_t bar = smem_u32(full + st), dst = base + st * kUpStage;
-                mbar_arrive_expect_tx(bar, kUpStage);
-                tma_load_4d(dst, &tm_a, bar, k * 64, h, static_cast<int>(m0), 0);
+                mbar_arrive_expect_tx(bar, 2 * kSlab);
+                tma_load_3d(dst, &tm_a, bar, k * 64, h, static_cast<int>(m0));
                 tma_load_2d(dst + 2 * kSlab, &tm_w, bar, k * 64, h * kDV);
             }
             if (!ok)   // no load may still be landing when the CTA exits
@@ -1269,7 +1295,7 @@ __global__ void __launch_bounds__(kUpThreads, 2)
 #pragma unroll 1
         for (int k = 0; k < 8; ++k) {
             const int st = k & 1;
-            if (!(ok = __all_sync(0xffffffffu, mbar_wait(smem_u32(full + st), (k >> 1) & 1, p.err)))) break;
+            if (!(ok = __all_sync(0xffffffffu, mbar_wait(smem_u32(split + st), (k >> 1) & 1, p.err)))) break;
             tc_fence_after();
             if (lead) {
                 const uint64_t a = desc_add(d0, st * kUpStage);
@@ -1286,6 +1312,30 @@ __global__ void __launch_bounds__(kUpThreads, 2)
         const int i = (warp & 3) * 32 + lane;
         int b, t;
         const bool token = is_token(p, m0 + i, b, t);
+        uint4 E = {};
+        if (token) E = __ldg(reinterpret_cast<const uint4 *>(p.ws_exp) + (m0 + i) * p.H + h);
+        const uint32_t ew[4] = {E.x, E.y, E.z, E.w};
+#pragma unroll 1
+        for (int k = 0; k < 8; ++k) {
+            const uint32_t at = base + (k & 1) * kUpStage;
+            mbar_wait(smem_u32(full + (k & 1)), (k >> 1) & 1, p.err);   // a failed one shows in `done`
+            const uint32_t e2 = (k < 4 ? k < 2 ? ew[0] : ew[1] : k < 6 ? ew[2] : ew[3]) >> ((k & 1) * 16);
+#pragma unroll
+            for (int c = 0; c < 8; ++c) {
+                const float down = row_down(max(static_cast<int>(c < 4 ? e2 & 0xFF : (e2 >> 8) & 0xFF), 20));
+                const uint32_t a = at + sw128_offset(i, c);
+                const uint4 v = ld_shared_v4(a);
+                const float2 x0 = row_values(v.x, down), x1 = row_values(v.y, down), x2 = row_values(v.z, down),
+                             x3 = row_values(v.w, down);
+                uint32_t lo[4];
+                const uint32_t h0 = split_bf16x2(x0.x, x0.y, lo[0]), h1 = split_bf16x2(x1.x, x1.y, lo[1]),
+                               h2 = split_bf16x2(x2.x, x2.y, lo[2]), h3 = split_bf16x2(x3.x, x3.y, lo[3]);
+                st_shared_v4(a, h0, h1, h2, h3);
+                st_shared_v4(a + kSlab, lo[0], lo[1], lo[2], lo[3]);
+            }
+            fence_proxy_async_smem();
+            mbar_arrive(smem_u32(split + (k & 1)));
+        }
         const bool good = mbar_wait(smem_u32(done), 0, p.err);
         tc_fence_after();
         if (__all_sync(0xffffffffu, good)) {
@@ -1347,13 +1397,14 @@ cudaError_t prepare(int num_sms, int &clusters) {
 
 // The workspace: rows, parts, tiles' clusters, clusters' unfinished tiles.
 struct Space {
-    size_t o, m, l, tile, cut, end;
+    size_t exp, m, l, tile, cut, end;
     int tiles;
     Space(long long B, long long T, int H, int num_sms) {
         const size_t clusters = num_sms / 2 > 0 ? num_sms / 2 : 1, parts = clusters * 2 * kM;
         tiles = static_cast<int>((T * H + kM - 1) / kM);
-        o = static_cast<size_t>(B) * T * H * kR * 2 * 2;
-        m = o + parts * kR * 4;
+        const size_t rows = static_cast<size_t>(B) * T * H + parts;
+        exp = rows * kR * 2;
+        m = exp + rows * 16;
         l = m + parts * 4;
         tile = l + parts * 4;
         cut = tile + static_cast<size_t>(B) * tiles * sizeof(int2);
@@ -1391,19 +1442,19 @@ cudaError_t launch_attend_paged(const AttendPagedArgs &a, cudaStream_t s) {
             return cudaErrorInvalidValue;
     }
     char *const ws = static_cast<char *>(a.workspace);
-    auto *const ws_rows = reinterpret_cast<__nv_bfloat16 *>(ws);
-    float *const ws_o = reinterpret_cast<float *>(ws + sp.o), *const ws_m = reinterpret_cast<float *>(ws + sp.m),
-                *const ws_l = reinterpret_cast<float *>(ws + sp.l);
+    auto *const ws_rows = reinterpret_cast<__half *>(ws);
+    auto *const ws_exp = reinterpret_cast<uint8_t *>(ws + sp.exp);
+    float *const ws_m = reinterpret_cast<float *>(ws + sp.m), *const ws_l = reinterpret_cast<float *>(ws + sp.l);
     int2 *const ws_tile = reinterpret_cast<int2 *>(ws + sp.tile), *const ws_cut = reinterpret_cast<int2 *>(ws + sp.cut);
     const long long m = static_cast<long long>(a.B) * a.T;
-    const size_t plane = static_cast<size_t>(m) * a.H * kR;
+    const long long all_rows = m * a.H;
     const PairParams pp{a.table, a.lens, a.counts, a.parents, a.ld_table,
-                        ws_rows, ws_o, ws_m, ws_l, ws_tile, ws_cut, plane, a.dev_err, a.B, a.T, a.H, sp.tiles,
+                        ws_rows, ws_exp, ws_m, ws_l, ws_tile, ws_cut, all_rows, a.dev_err, a.B, a.T, a.H, sp.tiles,
                         a.num_blocks, a.bs, a.max_blocks, a.window, a.sinks, a.scale * kLog2e};
     note_launch();
     e = launch_dependent(attend_pair_kernel, dim3(2 * G), kThreads, kSmemPair, s, tm_q, tm_s, tm_v, pp);
     if (e != cudaSuccess) return e;
-    const UpParams up{a.lens, a.counts, ws_rows, ws_o, ws_m, ws_l, ws_tile, ws_cut, plane,
+    const UpParams up{a.lens, a.counts, ws_rows, ws_exp, ws_m, ws_l, ws_tile, ws_cut, all_rows,
                       static_cast<const __nv_bfloat16 *>(a.gate), static_cast<__nv_bfloat16 *>(a.out), a.dev_err, a.B, a.T,
                       a.H, sp.tiles, a.bs, a.max_blocks};
     if (m <= kFewTokens) {
@@ -1413,10 +1464,10 @@ cudaError_t launch_attend_paged(const AttendPagedArgs &a, cudaStream_t s) {
     }
     CUtensorMap tm_a;
     {
-        const cuuint64_t row = kR * 2, dims[4] = {kR, static_cast<cuuint64_t>(a.H), static_cast<cuuint64_t>(m), 2};
-        const cuuint64_t strides[3] = {row, row * a.H, row * a.H * m};
-        const cuuint32_t box[4] = {64, 1, kM, 2};
-        if (encode_map(&tm_a, ws_rows, 4, dims, strides, box) != CUDA_SUCCESS) return cudaErrorInvalidValue;
+        const cuuint64_t row = kR * 2, dims[3] = {kR, static_cast<cuuint64_t>(a.H), static_cast<cuuint64_t>(m)};
+        const cuuint64_t strides[2] = {row, row * a.H};
+        const cuuint32_t box[3] = {64, 1, kM};
+        if (encode_map(&tm_a, ws_rows, 3, dims, strides, box) != CUDA_SUCCESS) return cudaErrorInvalidValue;
     }
     note_launch();
     e = launch_dependent(attend_join_kernel, dim3(8 * G), kJoinThreads, 0, s, up);
