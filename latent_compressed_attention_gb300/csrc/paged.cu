@@ -7,8 +7,8 @@
 //   reserve  need_b = ceil((lens_b + counts_b) / bs) blocks.  Sequences that hold more give the rest up, numbered
 //            k = 0 .. R - 1 in order of (sequence, index); those that need more take, in the same order, number k of what
 //            was given up for k < R and then free[F - 1 - (k - R)], the top of the free stack.  What nobody took goes to
-//            free[F + R - 1 - k], so that number A, the first left over, is not on top of number A + 1 by chance: a
-//            growth and the same shrinking leave the stack as it was.
+//            free[F + R - 1 - k], the first one given up on top, so that a growth and the same shrinking leave the
+//            stack as it was.
 //   append   pool row slots[i] = c[i].
 #include "common.cuh"
 #include "internal.h"
@@ -36,19 +36,36 @@ __device__ __forceinline__ int owner(const int *pre, int B, int k) {
     return lo;
 }
 
-template <bool kCluster>
-__device__ __forceinline__ void sync_all() {
-    if constexpr (kCluster) {
-        __threadfence();
-        cluster_sync_all();
+// The slots of four tokens from t0 on.
+__device__ __forceinline__ void write_slots(const ReserveParams &p, int b, int t0, int len, int count) {
+    const int *const table = p.table + b * p.ld_table;
+    int s[4], j = (len + t0) / p.bs, off = len + t0 - j * p.bs;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+        s[k] = -1;
+        if (t0 + k < count) {
+            const long long row = static_cast<long long>(table[j]) * p.bs + off;
+            if (row >= 0 && row <= 0x7FFFFFFF)
+                s[k] = static_cast<int>(row);
+            else
+                record_error(p.err, kDevErrBounds);
+        }
+        if (++off == p.bs) off = 0, ++j;
+    }
+    int *const dst = p.slots + static_cast<long long>(b) * p.T + t0;
+    if (p.T % 4 == 0) {
+        *reinterpret_cast<int4 *>(dst) = make_int4(s[0], s[1], s[2], s[3]);
     } else {
-        __syncthreads();
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+            if (t0 + k < p.T) dst[k] = s[k];
     }
 }
 
-// Every CTA adds up all sequences' needs (they fit one CTA's threads); after a barrier, when no one reads the old state
-// any more, all of them change it, each thread a block at a time.
-template <bool kCluster>
+// One CTA adds up all sequences' needs and, once no thread reads the old state any more, changes it, each thread a block at
+// a time.  With kAll it maps the slots too; otherwise it maps each sequence's first one (-1 where there is none, or where
+// nothing fits) and map_slots_kernel the others.
+template <bool kAll>
 __global__ void __launch_bounds__(kReserveThreads) reserve_latent_blocks_kernel(const ReserveParams p) {
     extern __shared__ int pre[];   // [B + 1] blocks taken, [B + 1] blocks given up by the sequences before
     __shared__ long long warp_sum[2][32];
@@ -60,14 +77,16 @@ __global__ void __launch_bounds__(kReserveThreads) reserve_latent_blocks_kernel(
     const int F = *p.free_count;
     const int per = (p.B + kReserveThreads - 1) / kReserveThreads;
     const int b0 = min(tid * per, p.B), b1 = min(b0 + per, p.B);
-    auto need = [&](int b) {
-        return static_cast<int>((static_cast<long long>(p.lens[b]) + p.counts[b] + p.bs - 1) / p.bs);
+    const auto blocks = [&](int len, int count) {   // neither below 0
+        const unsigned n = static_cast<unsigned>(len) + static_cast<unsigned>(count), q = n / static_cast<unsigned>(p.bs);
+        return q + (n != q * p.bs ? 1 : 0);
     };
+    const auto need = [&](int b) { return static_cast<int>(blocks(p.lens[b], p.counts[b])); };
     long long sum[2] = {0, 0};
     bool bad = F < 0 || F > p.capacity;
     for (int b = b0; b < b1; ++b) {
         const int len = p.lens[b], count = p.counts[b], h = p.held[b];
-        const long long n = (static_cast<long long>(len) + count + p.bs - 1) / p.bs;
+        const long long n = len < 0 || count < 0 ? 0 : blocks(len, count);
         bad |= len < 0 || count < 0 || (p.slots != nullptr && count > p.T) || n > p.max_blocks || h < 0 || h > p.max_blocks;
         sum[0] += max(n - h, 0ll), sum[1] += max(h - n, 0ll);
     }
@@ -105,15 +124,14 @@ __global__ void __launch_bounds__(kReserveThreads) reserve_latent_blocks_kernel(
         }
         if (tid == 0) take[p.B] = static_cast<int>(A), give[p.B] = static_cast<int>(R);
     }
-    const int step = kCluster ? kReserveThreads * static_cast<int>(gridDim.x) : kReserveThreads;
-    const int me = kCluster ? tid + kReserveThreads * static_cast<int>(blockIdx.x) : tid;
+    const bool slots = p.slots != nullptr;
     if (bad) {
-        if (me == 0) record_error(p.err, kDevErrBounds);
-        if (p.slots != nullptr)
-            for (long long i = me; i < static_cast<long long>(p.B) * p.T; i += step) p.slots[i] = -1;
+        if (tid == 0) record_error(p.err, kDevErrBounds);
+        const long long every = kAll ? 1 : p.T, n = slots ? static_cast<long long>(p.B) * p.T : 0;
+        for (long long i = tid * every; i < n; i += kReserveThreads * every) p.slots[i] = -1;
         return;
     }
-    sync_all<kCluster>();   // the prefix sums are there; held and free_count have been read
+    __syncthreads();   // the prefix sums are there; held and free_count have been read
     const int a_all = static_cast<int>(A), r_all = static_cast<int>(R);
     // Only sequences that keep no more than they need take blocks, and only the others give some up: the entries read
     // here and those written are of different sequences, as are the stack's places below F and from F on.
@@ -121,42 +139,44 @@ __global__ void __launch_bounds__(kReserveThreads) reserve_latent_blocks_kernel(
         const int b = owner(give, p.B, k);
         return p.table[b * p.ld_table + need(b) + (k - give[b])];
     };
-    for (int k = me; k < a_all; k += step) {
+    for (int k = tid; k < a_all; k += kReserveThreads) {
         const int b = owner(take, p.B, k), n = need(b), had = n - (take[b + 1] - take[b]);
         p.table[b * p.ld_table + had + (k - take[b])] = k < r_all ? given(k) : p.free_blocks[F - 1 - (k - r_all)];
     }
-    for (int k = a_all + me; k < r_all; k += step) p.free_blocks[F + r_all - 1 - k] = given(k);
-    for (int b = me; b < p.B; b += step) p.held[b] = need(b);
-    if (me == 0) *p.free_count = F + r_all - a_all;
-    if (p.slots == nullptr) return;
-    sync_all<kCluster>();   // the tables are whole
-    const int quads = (p.T + 3) / 4;
-    const bool wide = p.T % 4 == 0;
-    for (long long i = me; i < static_cast<long long>(p.B) * quads; i += step) {
-        const int b = static_cast<int>(i / quads), t0 = static_cast<int>(i - static_cast<long long>(b) * quads) * 4;
-        const int len = p.lens[b], count = p.counts[b];
-        int s[4];
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-            s[k] = -1;
-            if (t0 + k < count) {
-                const int u = len + t0 + k, j = u / p.bs;
-                const long long row = static_cast<long long>(p.table[b * p.ld_table + j]) * p.bs + (u - j * p.bs);
-                if (row >= 0 && row <= 0x7FFFFFFF)
-                    s[k] = static_cast<int>(row);
-                else
-                    record_error(p.err, kDevErrBounds);
-            }
+    for (int k = a_all + tid; k < r_all; k += kReserveThreads) p.free_blocks[F + r_all - 1 - k] = given(k);
+    for (int b = tid; b < p.B; b += kReserveThreads) p.held[b] = need(b);
+    if (tid == 0) *p.free_count = F + r_all - a_all;
+    if (!slots) return;
+    __syncthreads();   // the tables are whole
+    if constexpr (kAll) {
+        const int quads = (p.T + 3) / 4, n = p.B * quads;
+        for (int i = tid; i < n; i += kReserveThreads) {
+            const int b = i / quads;
+            write_slots(p, b, (i - b * quads) * 4, p.lens[b], p.counts[b]);
         }
-        int *const dst = p.slots + static_cast<long long>(b) * p.T + t0;
-        if (wide) {
-            *reinterpret_cast<int4 *>(dst) = make_int4(s[0], s[1], s[2], s[3]);
-        } else {
-#pragma unroll
-            for (int k = 0; k < 4; ++k)
-                if (t0 + k < p.T) dst[k] = s[k];
+    } else {
+        for (int b = tid; b < p.B; b += kReserveThreads) {
+            const int len = p.lens[b], j = len / p.bs;
+            long long row = -1;
+            if (p.counts[b] > 0) {
+                row = static_cast<long long>(p.table[b * p.ld_table + j]) * p.bs + (len - j * p.bs);
+                if (row < 0 || row > 0x7FFFFFFF) record_error(p.err, kDevErrBounds), row = -1;
+            }
+            p.slots[static_cast<long long>(b) * p.T] = static_cast<int>(row);
         }
     }
+}
+
+// The slots of 1024 tokens of a sequence.  Its first slot is there already: -1 where the sequence has none.
+constexpr int kMapThreads = 256;
+__global__ void __launch_bounds__(kMapThreads) map_slots_kernel(const ReserveParams p, unsigned per_seq) {
+    grid_dependency_wait();
+    grid_launch_dependents();
+    const int b = static_cast<int>(blockIdx.x / per_seq);
+    const int t0 = static_cast<int>((blockIdx.x - b * per_seq) * kMapThreads + threadIdx.x) * 4;
+    if (t0 >= p.T) return;
+    const int first = *static_cast<const volatile int *>(p.slots + static_cast<long long>(b) * p.T);
+    write_slots(p, b, t0, p.lens[b], first < 0 ? 0 : p.counts[b]);
 }
 
 constexpr int kAppendThreads = 256;
@@ -213,28 +233,21 @@ cudaError_t launch_reserve_latent_blocks(const ReserveArgs &a, cudaStream_t s) {
     const ReserveParams p{a.lens, a.counts, a.table, a.held, a.free_blocks, a.free_count, a.T > 0 ? a.slots : nullptr,
                           a.ld_table, a.B, a.T, a.max_blocks, a.capacity, a.bs, a.dev_err};
     const size_t smem = 2 * (static_cast<size_t>(a.B) + 1) * sizeof(int);
-    // one CTA up to 8192 slots; above, a cluster of 8
-    const bool many = static_cast<long long>(a.B) * a.T > 8192;
-    auto *kernel = many ? reserve_latent_blocks_kernel<true> : reserve_latent_blocks_kernel<false>;
+    // the one CTA maps up to 8192 slots itself
+    const bool all = static_cast<long long>(a.B) * a.T <= 8192;
+    auto *const kernel = all ? reserve_latent_blocks_kernel<true> : reserve_latent_blocks_kernel<false>;
     if (smem > 40000) {
         const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
         if (e != cudaSuccess) return e;
     }
     note_launch();
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(many ? 8 : 1);
-    cfg.blockDim = dim3(kReserveThreads);
-    cfg.dynamicSmemBytes = smem;
-    cfg.stream = s;
-    cudaLaunchAttribute attr[2];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    attr[1].id = cudaLaunchAttributeClusterDimension;
-    attr[1].val.clusterDim.x = 8;
-    attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = many ? 2 : 1;
-    return cudaLaunchKernelEx(&cfg, kernel, p);
+    const cudaError_t e = launch_dependent(kernel, dim3(1), kReserveThreads, smem, s, p);
+    if (e != cudaSuccess || all) return e;
+    const unsigned per_seq = (static_cast<unsigned>(a.T) + 4 * kMapThreads - 1) / (4 * kMapThreads);
+    const long long blocks = static_cast<long long>(per_seq) * a.B;
+    if (blocks > 0x7FFFFFFFll) return cudaErrorInvalidValue;
+    note_launch();
+    return launch_dependent(map_slots_kernel, dim3(static_cast<unsigned>(blocks)), kMapThreads, 0, s, p, per_seq);
 }
 
 cudaError_t launch_append_latent_paged(const AppendPagedArgs &a, cudaStream_t s) {
