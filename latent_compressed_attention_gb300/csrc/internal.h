@@ -131,7 +131,7 @@ struct ReserveArgs {
     int B, T, max_blocks, capacity, bs;
     int *dev_err;
 };
-constexpr int kReserveMaxB = 16384;               // two prefix sums over the sequences in shared memory
+constexpr int kReserveMaxB = 16384;               // three numbers for each sequence in shared memory
 cudaError_t launch_reserve_latent_blocks(const ReserveArgs &a, cudaStream_t s);
 struct AppendPagedArgs {
     const void *c;

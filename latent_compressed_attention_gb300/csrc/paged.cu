@@ -26,14 +26,16 @@ struct ReserveParams {
     int *err;
 };
 
-// Number of the sequence whose part of [0, pre[B]) holds k.
-__device__ __forceinline__ int owner(const int *pre, int B, int k) {
-    int lo = 0, hi = B;   // pre[lo] <= k < pre[hi]
-    while (hi - lo > 1) {
-        const int mid = (lo + hi) >> 1;
-        (pre[mid] <= k ? lo : hi) = mid;
-    }
-    return lo;
+constexpr int kBatch = 4;   // blocks that a thread moves at a time, their searches and loads in flight together
+
+// Of each k the sequence whose part of [0, pre[B]) holds it.  `top`: the largest power of two up to B.
+__device__ __forceinline__ void owners(const int *pre, int B, int top, const int (&k)[kBatch], int (&b)[kBatch]) {
+#pragma unroll
+    for (int i = 0; i < kBatch; ++i) b[i] = 0;
+    for (int s = top; s > 0; s >>= 1)
+#pragma unroll
+        for (int i = 0; i < kBatch; ++i)
+            if (b[i] + s < B && pre[b[i] + s] <= k[i]) b[i] += s;
 }
 
 // The slots of four tokens from t0 on.
@@ -67,10 +69,10 @@ __device__ __forceinline__ void write_slots(const ReserveParams &p, int b, int t
 // nothing fits) and map_slots_kernel the others.
 template <bool kAll>
 __global__ void __launch_bounds__(kReserveThreads) reserve_latent_blocks_kernel(const ReserveParams p) {
-    extern __shared__ int pre[];   // [B + 1] blocks taken, [B + 1] blocks given up by the sequences before
+    extern __shared__ int pre[];   // [B + 1] blocks taken, [B + 1] blocks given up by the sequences before; [B] needs
     __shared__ long long warp_sum[2][32];
     __shared__ long long all_sum[2];
-    int *const take = pre, *const give = pre + p.B + 1;
+    int *const take = pre, *const give = pre + p.B + 1, *const need = give + p.B + 1;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     grid_dependency_wait();
     grid_launch_dependents();
@@ -81,7 +83,6 @@ __global__ void __launch_bounds__(kReserveThreads) reserve_latent_blocks_kernel(
         const unsigned n = static_cast<unsigned>(len) + static_cast<unsigned>(count), q = n / static_cast<unsigned>(p.bs);
         return q + (n != q * p.bs ? 1 : 0);
     };
-    const auto need = [&](int b) { return static_cast<int>(blocks(p.lens[b], p.counts[b])); };
     long long sum[2] = {0, 0};
     bool bad = F < 0 || F > p.capacity;
     for (int b = b0; b < b1; ++b) {
@@ -118,8 +119,8 @@ __global__ void __launch_bounds__(kReserveThreads) reserve_latent_blocks_kernel(
     if (!bad) {
         long long t = warp_sum[0][warp] + before[0] - sum[0], g = warp_sum[1][warp] + before[1] - sum[1];
         for (int b = b0; b < b1; ++b) {
-            take[b] = static_cast<int>(t), give[b] = static_cast<int>(g);
-            const int n = need(b), h = p.held[b];
+            const int n = static_cast<int>(blocks(p.lens[b], p.counts[b])), h = p.held[b];
+            take[b] = static_cast<int>(t), give[b] = static_cast<int>(g), need[b] = n;
             t += max(n - h, 0), g += max(h - n, 0);
         }
         if (tid == 0) take[p.B] = static_cast<int>(A), give[p.B] = static_cast<int>(R);
@@ -135,16 +136,31 @@ __global__ void __launch_bounds__(kReserveThreads) reserve_latent_blocks_kernel(
     const int a_all = static_cast<int>(A), r_all = static_cast<int>(R);
     // Only sequences that keep no more than they need take blocks, and only the others give some up: the entries read
     // here and those written are of different sequences, as are the stack's places below F and from F on.
-    auto given = [&](int k) {
-        const int b = owner(give, p.B, k);
-        return p.table[b * p.ld_table + need(b) + (k - give[b])];
-    };
-    for (int k = tid; k < a_all; k += kReserveThreads) {
-        const int b = owner(take, p.B, k), n = need(b), had = n - (take[b + 1] - take[b]);
-        p.table[b * p.ld_table + had + (k - take[b])] = k < r_all ? given(k) : p.free_blocks[F - 1 - (k - r_all)];
+    const int top = p.B > 0 ? 1 << (31 - __clz(p.B)) : 0;
+    for (int k0 = tid; k0 < max(a_all, r_all); k0 += kBatch * kReserveThreads) {
+        int k[kBatch], b[kBatch], block[kBatch];
+#pragma unroll
+        for (int i = 0; i < kBatch; ++i) k[i] = k0 + i * kReserveThreads;
+        if (k0 < r_all) {   // number k of what was given up
+            owners(give, p.B, top, k, b);
+#pragma unroll
+            for (int i = 0; i < kBatch; ++i)
+                if (k[i] < r_all) block[i] = p.table[b[i] * p.ld_table + need[b[i]] + (k[i] - give[b[i]])];
+        }
+#pragma unroll
+        for (int i = 0; i < kBatch; ++i)
+            if (k[i] >= r_all && k[i] < a_all) block[i] = p.free_blocks[F - 1 - (k[i] - r_all)];
+        if (k0 < a_all) {
+            owners(take, p.B, top, k, b);
+#pragma unroll
+            for (int i = 0; i < kBatch; ++i)
+                if (k[i] < a_all) p.table[b[i] * p.ld_table + need[b[i]] + k[i] - take[b[i] + 1]] = block[i];
+        }
+#pragma unroll
+        for (int i = 0; i < kBatch; ++i)
+            if (k[i] >= a_all && k[i] < r_all) p.free_blocks[F + r_all - 1 - k[i]] = block[i];
     }
-    for (int k = a_all + tid; k < r_all; k += kReserveThreads) p.free_blocks[F + r_all - 1 - k] = given(k);
-    for (int b = tid; b < p.B; b += kReserveThreads) p.held[b] = need(b);
+    for (int b = tid; b < p.B; b += kReserveThreads) p.held[b] = need[b];
     if (tid == 0) *p.free_count = F + r_all - a_all;
     if (!slots) return;
     __syncthreads();   // the tables are whole
@@ -232,7 +248,7 @@ __global__ void __launch_bounds__(kAppendThreads) append_latent_paged_kernel(con
 cudaError_t launch_reserve_latent_blocks(const ReserveArgs &a, cudaStream_t s) {
     const ReserveParams p{a.lens, a.counts, a.table, a.held, a.free_blocks, a.free_count, a.T > 0 ? a.slots : nullptr,
                           a.ld_table, a.B, a.T, a.max_blocks, a.capacity, a.bs, a.dev_err};
-    const size_t smem = 2 * (static_cast<size_t>(a.B) + 1) * sizeof(int);
+    const size_t smem = (3 * static_cast<size_t>(a.B) + 2) * sizeof(int);
     // the one CTA maps up to 8192 slots itself
     const bool all = static_cast<long long>(a.B) * a.T <= 8192;
     auto *const kernel = all ? reserve_latent_blocks_kernel<true> : reserve_latent_blocks_kernel<false>;
