@@ -667,11 +667,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                     if (!mine && !(last && more)) continue;
                     fail = wait_warp(bars->s_full[jb & 1], (jb >> 1) & 1);
                     tc_fence_after();
-                    if (last && more) {
-                        load_q(has_rows(w));
-                        if (!mine) continue;
-                    }
-                    if (!active) {   // none of the tile's rows are this warp's
+                    if (mine && !active) {   // none of the tile's rows are this warp's
                         mbar_arrive(B_(bars->s_free[jb & 1]));
                         mbar_arrive(B_(bars->m_ready[wg]));
                         if (first_thread) bulk_wait_read_all();
@@ -679,110 +675,111 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                         st_shared_v2f(info + row * 8, 1.f, 0.f);
                         fence_proxy_async_smem();
                         named_bar_sync(2 + wg, 128);
-                        continue;
-                    }
-                    // Two passes over S, 32 columns at a time in rolled loops: the second one's columns are read again,
-                    // so that the code stays short (it comes from DRAM in a call that follows a sweep of L2).  The scale
-                    // multiplies inside the exponent: the largest of c s is c max(s) for c >= 0, c min(s) otherwise.
-                    // Masked units multiply first.
-                    const int u0 = tile.row0(i);
-                    const bool mixed = tile.mixed(p, len, u0);
-                    const float mul = mixed ? 1.f : p.scale_log2;
-                    const uint32_t scol = trow + S_COL + (jb & 1) * 128;
-                    bool dirty = false;
-                    const auto load = [&](int c4, float (&s)[32]) {
-                        tmem_ld32(scol + c4 * 32, s);
-                        tmem_wait_ld();
-                        if (mixed) {
-                            const uint32_t seen = sight.word(u0, c4);
+                    } else if (mine) {
+                        // Two passes over S, 32 columns at a time in rolled loops: the second one's columns are read again,
+                        // so that the code stays short (it comes from DRAM in a call that follows a sweep of L2).  The scale
+                        // multiplies inside the exponent: the largest of c s is c max(s) for c >= 0, c min(s) otherwise.
+                        // Masked units multiply first.
+                        const int u0 = tile.row0(i);
+                        const bool mixed = tile.mixed(p, len, u0);
+                        const float mul = mixed ? 1.f : p.scale_log2;
+                        const uint32_t scol = trow + S_COL + (jb & 1) * 128;
+                        float zeros[4] = {0.f, 0.f, 0.f, 0.f};   // NaN once a masked unit's score is not finite
+                        const auto load = [&](int c4, float (&s)[32]) {
+                            tmem_ld32(scol + c4 * 32, s);
+                            tmem_wait_ld();
+                            if (mixed) {
+                                const uint32_t seen = sight.word(u0, c4);
 #pragma unroll
-                            for (int k = 0; k < 32; ++k) {
-                                // an infinite score's row gives NaN, as its product with the weight 0 would
-                                const bool finite = fabsf(s[k]) < INFINITY;
-                                dirty |= !finite;
-                                const float x = finite ? s[k] * p.scale_log2 : NAN;
-                                s[k] = (seen >> k) & 1 ? x : -INFINITY;
+                                for (int k = 0; k < 32; ++k) {
+                                    // an infinite score's row gives NaN, as its product with the weight 0 would
+                                    const float zero = s[k] - s[k];
+                                    zeros[k & 3] += zero;
+                                    s[k] = (seen >> k) & 1 ? fmaf(s[k], p.scale_log2, zero) : -INFINITY;
+                                }
+                            }
+                        };
+                        float mx = -INFINITY, mn = INFINITY;
+#pragma unroll 1
+                        for (int c4 = 0; c4 < 4; ++c4) {
+                            float s[32];
+                            load(c4, s);
+                            if (mul >= 0.f) {
+                                float t[4] = {mx, s[0], s[1], s[2]};
+#pragma unroll
+                                for (int k = 3; k < 32; ++k) t[k & 3] = fmaxf(t[k & 3], s[k]);
+                                mx = fmaxf(fmaxf(t[0], t[1]), fmaxf(t[2], t[3]));
+                            } else {
+#pragma unroll
+                                for (int k = 0; k < 32; ++k) mn = fminf(mn, s[k]);
                             }
                         }
-                    };
-                    float mx = -INFINITY, mn = INFINITY;
-#pragma unroll 1
-                    for (int c4 = 0; c4 < 4; ++c4) {
-                        float s[32];
-                        load(c4, s);
-                        if (mul >= 0.f) {
-                            float t[4] = {mx, s[0], s[1], s[2]};
-#pragma unroll
-                            for (int k = 3; k < 32; ++k) t[k & 3] = fmaxf(t[k & 3], s[k]);
-                            mx = fmaxf(fmaxf(t[0], t[1]), fmaxf(t[2], t[3]));
-                        } else {
-#pragma unroll
-                            for (int k = 0; k < 32; ++k) mn = fminf(mn, s[k]);
+                        mx = mul * (mul >= 0.f ? mx : mn);
+                        // the running maximum of the unit before, from the other warpgroup
+                        if (jb > 0) fail = wait_warp(bars->m_ready[wg ^ 1], ((jb - 1) >> 1) & 1);
+                        const float m_old = i == i0 ? -INFINITY : ld_shared_f32(base + S_MAX + (wg ^ 1) * kM * 4 + row * 4);
+                        float m = m_old, factor = 1.f;
+                        if (mx > m_old + kRescaleLog2) {
+                            factor = fast_exp2(m_old - mx);
+                            m = mx;
                         }
-                    }
-                    mx = mul * (mul >= 0.f ? mx : mn);
-                    // the running maximum of the unit before, from the other warpgroup
-                    if (jb > 0) fail = wait_warp(bars->m_ready[wg ^ 1], ((jb - 1) >> 1) & 1);
-                    const float m_old = i == i0 ? -INFINITY : ld_shared_f32(base + S_MAX + (wg ^ 1) * kM * 4 + row * 4);
-                    float m = m_old, factor = 1.f;
-                    if (mx > m_old + kRescaleLog2) {
-                        factor = fast_exp2(m_old - mx);
-                        m = mx;
-                    }
-                    st_shared_f32(base + S_MAX + wg * kM * 4 + row * 4, m);
-                    mbar_arrive(B_(bars->m_ready[wg]));
-                    const float neg_m = m == -INFINITY ? 0.f : -m;
-                    if (m != m_mine) l *= fast_exp2(m_mine - m);
-                    m_mine = m;
-                    if (last && !whole && row < rows) p.ws_m[static_cast<size_t>(slot) * kM + row] = m;
+                        st_shared_f32(base + S_MAX + wg * kM * 4 + row * 4, m);
+                        mbar_arrive(B_(bars->m_ready[wg]));
+                        const float neg_m = m == -INFINITY ? 0.f : -m;
+                        if (m != m_mine) l *= fast_exp2(m_mine - m);
+                        m_mine = m;
+                        if (last && !whole && row < rows) p.ws_m[static_cast<size_t>(slot) * kM + row] = m;
 
-                    // the staging unit is free once this warpgroup's copy before has read it
-                    if (first_thread) bulk_wait_read_all();
-                    if (named_bar_or(2 + wg, 128, fail)) { ok = false; break; }
+                        // the staging unit is free once this warpgroup's copy before has read it
+                        if (first_thread) bulk_wait_read_all();
+                        if (named_bar_or(2 + wg, 128, fail)) { ok = false; break; }
 #pragma unroll 1
-                    for (int c4 = 0; c4 < 4; ++c4) {
-                        float s[32];
-                        load(c4, s);
-                        float t[4] = {l, 0.f, 0.f, 0.f};
-                        const uint32_t slab = ptile + (c4 >> 1) * kSlab;
+                        for (int c4 = 0; c4 < 4; ++c4) {
+                            float s[32];
+                            load(c4, s);
+                            float t[4] = {l, 0.f, 0.f, 0.f};
+                            const uint32_t slab = ptile + (c4 >> 1) * kSlab;
 #pragma unroll
-                        for (int k = 0; k < 4; ++k) {
-                            float *v = &s[8 * k];
+                            for (int k = 0; k < 4; ++k) {
+                                float *v = &s[8 * k];
 #pragma unroll
-                            for (int q = 0; q < 8; ++q) {
-                                v[q] = fast_exp2(fmaf(v[q], mul, neg_m));
-                                t[q & 3] += v[q];
+                                for (int q = 0; q < 8; ++q) {
+                                    v[q] = fast_exp2(fmaf(v[q], mul, neg_m));
+                                    t[q & 3] += v[q];
+                                }
+                                st_shared_v4(slab + sw128_offset(row, (c4 & 1) * 4 + k), pack_bf16x2(v[0], v[1]),
+                                             pack_bf16x2(v[2], v[3]), pack_bf16x2(v[4], v[5]), pack_bf16x2(v[6], v[7]));
                             }
-                            st_shared_v4(slab + sw128_offset(row, (c4 & 1) * 4 + k), pack_bf16x2(v[0], v[1]),
-                                         pack_bf16x2(v[2], v[3]), pack_bf16x2(v[4], v[5]), pack_bf16x2(v[6], v[7]));
+                            l = (t[0] + t[1]) + (t[2] + t[3]);
                         }
-                        l = (t[0] + t[1]) + (t[2] + t[3]);
-                    }
-                    tc_fence_before();
-                    mbar_arrive(B_(bars->s_free[jb & 1]));
-                    dirty = dirty && row < rows;
-                    st_shared_v2f(info + row * 8, dirty ? -factor : factor, l);
-                    fence_proxy_async_smem();
-                    named_bar_sync(2 + wg, 128);
-                    if (first_thread) {
-                        const uint32_t pb = jb % kPBufs;
-                        if (jb >= kPBufs)
-                            fail = !mbar_wait<true>(B_(bars->p_free[pb]), (jb / kPBufs - 1) & 1, p.err, abort_flag);
-                        if (!fail) {
-                            const uint32_t bar = mapa_shared(B_(bars->p_full[pb]), 1);
-                            const uint32_t dst = mapa_shared(base + pb * kPUnit, 1);
-                            if (rows == kM) {
-                                bulk_copy_s2cluster(dst, ptile, kPUnit, bar);
-                            } else {   // whole groups of 8 rows: the others' products are not read
-                                const uint32_t n = static_cast<uint32_t>((rows + 7) & ~7) * 128;
-                                bulk_copy_s2cluster(dst, ptile, n, bar);
-                                bulk_copy_s2cluster(dst + kSlab, ptile + kSlab, n, bar);
-                                bulk_copy_s2cluster(dst + 2 * kSlab, info, kInfo, bar);
+                        tc_fence_before();
+                        mbar_arrive(B_(bars->s_free[jb & 1]));
+                        const float z = (zeros[0] + zeros[1]) + (zeros[2] + zeros[3]);
+                        const bool dirty = z != 0.f && row < rows;
+                        st_shared_v2f(info + row * 8, dirty ? -factor : factor, l);
+                        fence_proxy_async_smem();
+                        named_bar_sync(2 + wg, 128);
+                        if (first_thread) {
+                            const uint32_t pb = jb % kPBufs;
+                            if (jb >= kPBufs)
+                                fail = !mbar_wait<true>(B_(bars->p_free[pb]), (jb / kPBufs - 1) & 1, p.err, abort_flag);
+                            if (!fail) {
+                                const uint32_t bar = mapa_shared(B_(bars->p_full[pb]), 1);
+                                const uint32_t dst = mapa_shared(base + pb * kPUnit, 1);
+                                if (rows == kM) {
+                                    bulk_copy_s2cluster(dst, ptile, kPUnit, bar);
+                                } else {   // whole groups of 8 rows: the others' products are not read
+                                    const uint32_t n = static_cast<uint32_t>((rows + 7) & ~7) * 128;
+                                    bulk_copy_s2cluster(dst, ptile, n, bar);
+                                    bulk_copy_s2cluster(dst + kSlab, ptile + kSlab, n, bar);
+                                    bulk_copy_s2cluster(dst + 2 * kSlab, info, kInfo, bar);
+                                }
+                                bulk_commit_group();
                             }
-                            bulk_commit_group();
                         }
                     }
                     __syncwarp();
+                    if (last && more) load_q(has_rows(w));
                 }
             }
             if (first_thread) bulk_wait_all();
