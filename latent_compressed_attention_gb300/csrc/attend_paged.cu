@@ -1005,31 +1005,40 @@ __device__ __forceinline__ void join_parts(const UpParams &p, int first, int las
     }
 }
 
-// 32 output columns of a token's head from TMEM, with the gate.
-__device__ __forceinline__ void store_out(uint32_t taddr, const __nv_bfloat16 *gate, __nv_bfloat16 *out, bool token) {
-    float o[32];
-    tmem_ld32(taddr, o);
-    tmem_wait_ld();
-    if (!token) return;
-    if (gate) {
+// The gate logits of a token's head, and its 128 output columns from TMEM with them.
+struct Gate {
+    uint4 v[16];
+    __device__ __forceinline__ void load(const __nv_bfloat16 *gate) {
 #pragma unroll
-        for (int q = 0; q < 2; ++q) {
-            uint4 g[2];
-            ld_global_32B(gate + 16 * q, g[0], g[1]);
-            const uint32_t gw[8] = {g[0].x, g[0].y, g[0].z, g[0].w, g[1].x, g[1].y, g[1].z, g[1].w};
+        for (int k = 0; k < 8; ++k) ld_global_32B(gate + 16 * k, v[2 * k], v[2 * k + 1]);
+    }
+};
+__device__ __forceinline__ void store_out(uint32_t taddr, const Gate *gate, __nv_bfloat16 *out, bool token) {
 #pragma unroll
-            for (int k = 0; k < 8; ++k) {
-                o[16 * q + 2 * k] *= __fdividef(1.f, 1.f + fast_exp2(-__uint_as_float(gw[k] << 16) * kLog2e));
-                o[16 * q + 2 * k + 1] *= __fdividef(1.f, 1.f + fast_exp2(-__uint_as_float(gw[k] & 0xFFFF0000u) * kLog2e));
+    for (int c = 0; c < 4; ++c) {
+        float o[32];
+        tmem_ld32(taddr + c * 32, o);
+        tmem_wait_ld();
+        if (!token) continue;
+        if (gate) {
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+                const uint4 g = gate->v[c * 4 + q];
+                const uint32_t gw[4] = {g.x, g.y, g.z, g.w};
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    o[8 * q + 2 * k] *= __fdividef(1.f, 1.f + fast_exp2(-__uint_as_float(gw[k] << 16) * kLog2e));
+                    o[8 * q + 2 * k + 1] *= __fdividef(1.f, 1.f + fast_exp2(-__uint_as_float(gw[k] & 0xFFFF0000u) * kLog2e));
+                }
             }
         }
-    }
 #pragma unroll
-    for (int q = 0; q < 2; ++q) {
-        uint32_t x[8];
+        for (int q = 0; q < 2; ++q) {
+            uint32_t x[8];
 #pragma unroll
-        for (int k = 0; k < 8; ++k) x[k] = pack_bf16x2(o[16 * q + 2 * k], o[16 * q + 2 * k + 1]);
-        st_global_32B(out + 16 * q, make_uint4(x[0], x[1], x[2], x[3]), make_uint4(x[4], x[5], x[6], x[7]));
+            for (int k = 0; k < 8; ++k) x[k] = pack_bf16x2(o[16 * q + 2 * k], o[16 * q + 2 * k + 1]);
+            st_global_32B(out + c * 32 + 16 * q, make_uint4(x[0], x[1], x[2], x[3]), make_uint4(x[4], x[5], x[6], x[7]));
+        }
     }
 }
 
@@ -1192,13 +1201,14 @@ __global__ void __launch_bounds__(kFewThreads, 2)
                 mbar_wait(smem_u32(w_full + (k & 1)), (k >> 1) & 1, p.err, nullptr, kLandNs);
     }
     __syncwarp();
-    const bool good = mbar_wait(smem_u32(done), 0, p.err);
-    tc_fence_after();
-    if (warp == 0 && __all_sync(0xffffffffu, good)) {
+    if (warp == 0) {
         const bool valid = s_tile[lane].x >= 0;
         const long long off = ((m0 + lane) * p.H + h) * kDV;
-#pragma unroll 1
-        for (int c = 0; c < kDV; c += 32) store_out(tmem + c, p.gate ? p.gate + off + c : nullptr, p.out + off + c, valid);
+        Gate gate;
+        if (p.gate && valid) gate.load(p.gate + off);
+        const bool good = mbar_wait(smem_u32(done), 0, p.err);
+        tc_fence_after();
+        if (__all_sync(0xffffffffu, good)) store_out(tmem, p.gate ? &gate : nullptr, p.out + off, valid);
     }
     tc_fence_before();
     __syncthreads();
@@ -1232,119 +1242,191 @@ __global__ void __launch_bounds__(kJoinThreads) attend_join_kernel(const UpParam
     if ((lane & 1) == 0) p.ws_exp[row * 16 + (lane >> 1)] = static_cast<uint8_t>(E);
 }
 
-// Many tokens, then: one CTA per (head, 128 tokens), out = gate * (hi + lo) . W_UV[h]^T over eight slabs of 64 latent
-// columns.  A stage takes a slab of f16 rows, which four warps (thread = row) turn into hi in its place and lo beside it,
-// and W_UV's: 48 KB, two stages per CTA and two CTAs per SM.
-constexpr int kUpThreads = 192;   // warps 0 TMA, 1 MMA, 2-5 rows
-constexpr uint32_t kUpStage = 3 * kSlab;
-constexpr uint32_t kUpBars = 2 * kUpStage;
-constexpr uint32_t kUpSmem = kUpBars + 64 + 1024;
+// Many tokens, then: out = gate * (hi + lo) . W_UV[h]^T, 128 tokens of a head at a time.  Persistent: a CTA takes a run of
+// items, the blocks of one head after the other, with W_UV[h] in shared memory while the head stays.  A stage takes 64
+// latent columns of f16 rows, which eight warps (two threads to a row) turn into hi in its place and lo beside it; two
+// accumulators, so that four more warps store one item while the next one's products run.
+constexpr int kUpThreads = 448;   // warps 0 TMA, 1 MMA, 2-9 split, 10-13 store
+constexpr int kUpStages = 3;
+constexpr uint32_t kUpA = 8 * kSlab, kUpStage = 2 * kSlab;
+constexpr uint32_t kUpBars = kUpA + kUpStages * kUpStage;
+struct UpBars {
+    uint64_t w_full, w_empty, full[kUpStages], split[kUpStages], empty[kUpStages], acc_full[2], acc_empty[2];
+    uint32_t tmem_base;
+};
+constexpr uint32_t kUpSmem = kUpBars + 256 + 1024;
+static_assert(sizeof(UpBars) <= 256 && kUpSmem <= 232448, "shared memory");
 
-__global__ void __launch_bounds__(kUpThreads, 2)
+__global__ void __launch_bounds__(kUpThreads, 1)
     attend_up_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ CUtensorMap tm_w, const UpParams p) {
     extern __shared__ uint8_t smem_raw[];
     const uint32_t raw = smem_u32(smem_raw);
     const uint32_t base = (raw + 1023u) & ~1023u;
-    uint64_t *const full = reinterpret_cast<uint64_t *>(smem_raw + (base - raw) + kUpBars);   // [2]
-    uint64_t *const empty = full + 2, *const split = full + 4;                                 // [2] each
-    uint64_t *const done = full + 6;
-    uint32_t *const tmem_slot = reinterpret_cast<uint32_t *>(full + 7);
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int h = blockIdx.x % p.H;
-    const long long m0 = static_cast<long long>(blockIdx.x / p.H) * kM;
+    UpBars *const bars = reinterpret_cast<UpBars *>(smem_raw + (base - raw) + kUpBars);
+    const auto B_ = [](uint64_t &b) { return smem_u32(&b); };
+    const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
+    const long long m_all = static_cast<long long>(p.B) * p.T;
+    const int blocks = static_cast<int>((m_all + kM - 1) / kM);
+    const long long items = static_cast<long long>(blocks) * p.H;
+    const int i0 = static_cast<int>(items * blockIdx.x / gridDim.x), i1 = static_cast<int>(items * (blockIdx.x + 1) / gridDim.x);
 
     if (threadIdx.x == 0) {
-        for (int i = 0; i < 7; ++i) mbar_init(smem_u32(full + i), i == 4 || i == 5 ? 128 : 1);
+        mbar_init(B_(bars->w_full), 1);
+        mbar_init(B_(bars->w_empty), 1);
+        for (int i = 0; i < kUpStages; ++i) {
+            mbar_init(B_(bars->full[i]), 1);
+            mbar_init(B_(bars->split[i]), 256);
+            mbar_init(B_(bars->empty[i]), 1);
+        }
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(B_(bars->acc_full[i]), 1);
+            mbar_init(B_(bars->acc_empty[i]), 128);
+        }
         fence_mbar_init();
     }
     if (warp == 1) {
-        tmem_alloc(smem_u32(tmem_slot), 128);
+        tmem_alloc(smem_u32(&bars->tmem_base), 256);
         tmem_relinquish();
     }
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    const uint32_t tmem = *tmem_slot;
-    grid_dependency_wait();
-    grid_launch_dependents();
+    const uint32_t tmem = __shfl_sync(0xffffffffu, bars->tmem_base, 0);
+    const auto wait = [&](uint64_t &bar, uint32_t parity) {
+        return __all_sync(0xffffffffu, mbar_wait(B_(bar), parity, p.err));
+    };
     if (warp == 0) {
-        if (lane == 0) {
-            fence_proxy_async_all();
-            bool ok = true;
-            int k = 0;
-            for (; k < 8; ++k) {
-                const int st = k & 1;
-                if (k >= 2 && !(ok = mbar_wait(smem_u32(empty + st), ((k >> 1) - 1) & 1, p.err))) break;
-                const uint32_t bar = smem_u32(full + st), dst = base + st * kUpStage;
-                mbar_arrive_expect_tx(bar, 2 * kSlab);
-                tma_load_3d(dst, &tm_a, bar, k * 64, h, static_cast<int>(m0));
-                tma_load_2d(dst + 2 * kSlab, &tm_w, bar, k * 64, h * kDV);
+        const bool lead = elect_one();
+        Ring<kUpStages> at;
+        uint32_t it = 0, w_phase = 0;
+        int head = -1;
+        bool ok = true;
+        for (int i = i0; ok && i < i1; ++i) {
+            const int h = i / blocks, m0 = (i - h * blocks) * kM;
+            if (h != head) {
+                if (!(ok = wait(bars->w_empty, w_phase ^ 1))) break;
+                w_phase ^= 1;
+                if (lead) {
+                    mbar_arrive_expect_tx(B_(bars->w_full), 8 * kSlab);
+                    for (int k = 0; k < 8; ++k)
+                        tma_load_2d(base + k * kSlab, &tm_w, B_(bars->w_full), k * 64, h * kDV);
+                }
+                if (head < 0) {   // W_UV was there before the kernels that this one waits for
+                    grid_dependency_wait();
+                    fence_proxy_async_all();
+                }
+                head = h;
             }
-            if (!ok)   // no load may still be landing when the CTA exits
-                for (int i = max(k - 2, 0); i < k; ++i)
-                    mbar_wait(smem_u32(full + (i & 1)), (i >> 1) & 1, p.err, nullptr, kLandNs);
+#pragma unroll 1
+            for (int k = 0; k < 8; ++k, ++it, at.next()) {
+                if (!(ok = wait(bars->empty[at.st], at.phase ^ 1))) break;
+                if (lead) {
+                    mbar_arrive_expect_tx(B_(bars->full[at.st]), kSlab);
+                    tma_load_3d(base + kUpA + at.st * kUpStage, &tm_a, B_(bars->full[at.st]), k * 64, h, m0);
+                }
+            }
         }
+        // no load may still be landing when the CTA exits
+        for (uint32_t k = it > kUpStages ? it - kUpStages : 0; k < it; ++k)
+            mbar_wait(B_(bars->full[k % kUpStages]), (k / kUpStages) & 1, p.err, nullptr, kLandNs);
+        if (head >= 0) mbar_wait(B_(bars->w_full), w_phase ^ 1, p.err, nullptr, kLandNs);
     } else if (warp == 1) {
         const bool lead = elect_one();
         const uint32_t idesc = make_idesc_bf16(128, kDV, 0, 0);
-        const uint64_t d0 = make_smem_desc(base, 16, 1024);
+        const uint64_t w0 = make_smem_desc(base, 16, 1024), a0 = make_smem_desc(base + kUpA, 16, 1024);
+        Ring<kUpStages> at;
+        Ring<2> acc;
+        uint32_t w_phase = 0;
+        int head = -1;
         bool ok = true;
+        for (int i = i0; ok && i < i1; ++i, acc.next()) {
+            const int h = i / blocks;
+            if (h != head) {
+                if (!(ok = wait(bars->w_full, w_phase))) break;
+                w_phase ^= 1;
+                head = h;
+            }
+            if (!(ok = wait(bars->acc_empty[acc.st], acc.phase ^ 1))) break;
+            const uint32_t d = tmem + acc.st * 128;
 #pragma unroll 1
-        for (int k = 0; k < 8; ++k) {
-            const int st = k & 1;
-            if (!(ok = __all_sync(0xffffffffu, mbar_wait(smem_u32(split + st), (k >> 1) & 1, p.err)))) break;
-            tc_fence_after();
-            if (lead) {
-                const uint64_t a = desc_add(d0, st * kUpStage);
+            for (int k = 0; k < 8; ++k, at.next()) {
+                if (!(ok = wait(bars->split[at.st], at.phase))) break;
+                tc_fence_after();
+                if (lead) {
+                    const uint64_t a = desc_add(a0, at.st * kUpStage), w = desc_add(w0, k * kSlab);
 #pragma unroll
-                for (int kk = 0; kk < 4; ++kk) {
-                    umma_bf16(tmem, desc_add(a, kk * 32), desc_add(a, 2 * kSlab + kk * 32), idesc, (k | kk) != 0);
-                    umma_bf16(tmem, desc_add(a, kSlab + kk * 32), desc_add(a, 2 * kSlab + kk * 32), idesc, 1);
+                    for (int kk = 0; kk < 4; ++kk) {
+                        umma_bf16(d, desc_add(a, kk * 32), desc_add(w, kk * 32), idesc, (k | kk) != 0);
+                        umma_bf16(d, desc_add(a, kSlab + kk * 32), desc_add(w, kk * 32), idesc, 1);
+                    }
+                    umma_commit(B_(bars->empty[at.st]));
                 }
-                umma_commit(smem_u32(empty + st));
+            }
+            if (ok && lead) {
+                umma_commit(B_(bars->acc_full[acc.st]));
+                if (i + 1 == i1 || (i + 1) / blocks != h) umma_commit(B_(bars->w_empty));
             }
         }
-        if (ok && lead) umma_commit(smem_u32(done));
-    } else {
-        const int i = (warp & 3) * 32 + lane;
-        int b, t;
-        const bool token = is_token(p, m0 + i, b, t);
-        uint4 E = {};
-        if (token) E = __ldg(reinterpret_cast<const uint4 *>(p.ws_exp) + (m0 + i) * p.H + h);
-        const uint32_t ew[4] = {E.x, E.y, E.z, E.w};
+    } else if (warp < 10) {
+        grid_dependency_wait();
+        const int r = ((warp - 2) & 3) * 32 + lane, half = (warp - 2) >> 2;   // of the slab's columns
+        const auto exponents = [&](int i) {
+            const int h = i / blocks;
+            const long long m = static_cast<long long>(i - h * blocks) * kM + r;
+            return i < i1 && m < m_all ? __ldg(reinterpret_cast<const uint4 *>(p.ws_exp) + m * p.H + h) : uint4();
+        };
+        Ring<kUpStages> at;
+        uint4 next = exponents(i0);
+        bool ok = true;
+        for (int i = i0; ok && i < i1; ++i) {
+            const uint4 E = next;
+            next = exponents(i + 1);
 #pragma unroll 1
-        for (int k = 0; k < 8; ++k) {
-            const uint32_t at = base + (k & 1) * kUpStage;
-            mbar_wait(smem_u32(full + (k & 1)), (k >> 1) & 1, p.err);   // a failed one shows in `done`
-            const uint32_t e2 = (k < 4 ? k < 2 ? ew[0] : ew[1] : k < 6 ? ew[2] : ew[3]) >> ((k & 1) * 16);
+            for (int k = 0; k < 8; ++k, at.next()) {
+                if (!(ok = wait(bars->full[at.st], at.phase))) break;
+                const uint32_t slab = base + kUpA + at.st * kUpStage;
+                const uint32_t e = (k < 4 ? k < 2 ? E.x : E.y : k < 6 ? E.z : E.w) >> ((k & 1) * 16 + half * 8);
+                const float down = row_down(max(static_cast<int>(e & 0xFF), 20));   // no token's row may hold anything
 #pragma unroll
-            for (int c = 0; c < 8; ++c) {
-                const float down = row_down(max(static_cast<int>(c < 4 ? e2 & 0xFF : (e2 >> 8) & 0xFF), 20));
-                const uint32_t a = at + sw128_offset(i, c);
-                const uint4 v = ld_shared_v4(a);
-                const float2 x0 = row_values(v.x, down), x1 = row_values(v.y, down), x2 = row_values(v.z, down),
-                             x3 = row_values(v.w, down);
-                uint32_t lo[4];
-                const uint32_t h0 = split_bf16x2(x0.x, x0.y, lo[0]), h1 = split_bf16x2(x1.x, x1.y, lo[1]),
-                               h2 = split_bf16x2(x2.x, x2.y, lo[2]), h3 = split_bf16x2(x3.x, x3.y, lo[3]);
-                st_shared_v4(a, h0, h1, h2, h3);
-                st_shared_v4(a + kSlab, lo[0], lo[1], lo[2], lo[3]);
+                for (int c = 0; c < 4; ++c) {
+                    const uint32_t a = slab + sw128_offset(r, half * 4 + c);
+                    const uint4 v = ld_shared_v4(a);
+                    const float2 x0 = row_values(v.x, down), x1 = row_values(v.y, down), x2 = row_values(v.z, down),
+                                 x3 = row_values(v.w, down);
+                    uint32_t lo[4];
+                    const uint32_t h0 = split_bf16x2(x0.x, x0.y, lo[0]), h1 = split_bf16x2(x1.x, x1.y, lo[1]),
+                                   h2 = split_bf16x2(x2.x, x2.y, lo[2]), h3 = split_bf16x2(x3.x, x3.y, lo[3]);
+                    st_shared_v4(a, h0, h1, h2, h3);
+                    st_shared_v4(a + kSlab, lo[0], lo[1], lo[2], lo[3]);
+                }
+                fence_proxy_async_smem();
+                mbar_arrive(B_(bars->split[at.st]));
             }
-            fence_proxy_async_smem();
-            mbar_arrive(smem_u32(split + (k & 1)));
         }
-        const bool good = mbar_wait(smem_u32(done), 0, p.err);
-        tc_fence_after();
-        if (__all_sync(0xffffffffu, good)) {
-            const long long off = ((m0 + i) * p.H + h) * kDV;
-            const uint32_t row = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16);
-#pragma unroll 1
-            for (int c = 0; c < kDV; c += 32) store_out(row + c, p.gate ? p.gate + off + c : nullptr, p.out + off + c, token);
+    } else {
+        grid_dependency_wait();
+        grid_launch_dependents();
+        const int r = (warp & 3) * 32 + lane;
+        const uint32_t row = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16);
+        Ring<2> acc;
+        bool ok = true;
+        for (int i = i0; ok && i < i1; ++i, acc.next()) {
+            const int h = i / blocks;
+            const long long m = static_cast<long long>(i - h * blocks) * kM + r, off = (m * p.H + h) * kDV;
+            int b, t;
+            const bool token = is_token(p, m, b, t);
+            Gate gate;
+            if (p.gate && token) gate.load(p.gate + off);
+            if (!(ok = wait(bars->acc_full[acc.st], acc.phase))) break;
+            tc_fence_after();
+            store_out(row + acc.st * 128, p.gate ? &gate : nullptr, p.out + off, token);
+            tc_fence_before();
+            mbar_arrive(B_(bars->acc_empty[acc.st]));
         }
     }
     tc_fence_before();
     __syncthreads();
-    if (warp == 1) tmem_dealloc(tmem, 128);
+    if (warp == 1) tmem_dealloc(tmem, 256);
 }
 
 CUresult encode_map(CUtensorMap *m, const void *ptr, int rank, const cuuint64_t *dims, const cuuint64_t *strides,
@@ -1470,8 +1552,9 @@ cudaError_t launch_attend_paged(const AttendPagedArgs &a, cudaStream_t s) {
     e = launch_dependent(attend_join_kernel, dim3(8 * G), kJoinThreads, 0, s, up);
     if (e != cudaSuccess) return e;
     note_launch();
-    return launch_dependent(attend_up_kernel, dim3(static_cast<unsigned>((m + kM - 1) / kM * a.H)), kUpThreads, kUpSmem, s,
-                            tm_a, tm_w, up);
+    const long long items = (m + kM - 1) / kM * a.H;
+    return launch_dependent(attend_up_kernel, dim3(static_cast<unsigned>(items < a.num_sms ? items : a.num_sms)), kUpThreads,
+                            kUpSmem, s, tm_a, tm_w, up);
 }
 
 }  // namespace mla
