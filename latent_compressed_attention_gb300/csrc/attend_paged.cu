@@ -43,14 +43,14 @@ namespace {
 constexpr int kR = 512, kDV = 128;
 constexpr int kM = 128;         // (token, head) rows of a tile
 constexpr int kUnit = 128;      // cache rows of a unit
-constexpr int kThreads = 384;   // warps 0 and 3 TMA, 1 MMA, 2 relay (value CTA), 4-7 and 8-11: two warpgroups
+constexpr int kThreads = 384;   // warps 0 and 3 TMA, 1 MMA, 4-7 and 8-11: two warpgroups
 constexpr uint32_t kRegsCtl = 80, kRegsMath = 208, kRegsLaunch = 168;
 static_assert(128 * kRegsCtl + 256 * kRegsMath <= kThreads * kRegsLaunch, "register split exceeds the launch");
 constexpr float kLog2e = 1.4426950408889634f;
 // A stale maximum is kept until the new one exceeds it by this (log2 units): p <= 2^16, far inside fp32's range.
 constexpr float kRescaleLog2 = 16.0f;
 // Units that starting a tile counts for in the shares: its queries' load, its accumulator's drain, the pipeline's refill.
-constexpr int kStart = 8;
+constexpr int kStart = 3;
 
 constexpr uint32_t kSlab = 16384;                  // [128 rows x 64 columns] bf16, 128-byte swizzle
 constexpr uint32_t kInfo = kM * 8;                 // {rescaling factor, negative to ask for cleaning, sum} per row of the tile
@@ -81,7 +81,7 @@ struct PairBars {
     uint64_t p_free[kPBufs];                             // arrivals from the value CTA
     uint64_t v_full[kVStages], v_empty[kVStages], v_clean[kVStages];
     uint64_t p_full[kPBufs];                             // the score CTA's copies
-    uint64_t pv_done[kPBufs], info_read[kPBufs], rescaled, drained;
+    uint64_t pv_done[kPBufs], rescaled, drained;
     uint32_t tmem_base;
     int abort;
     // where the cluster's share starts on the axis of units
@@ -340,7 +340,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             mbar_init(B_(bars->p_free[i]), 1);
             mbar_init(B_(bars->p_full[i]), 1);
             mbar_init(B_(bars->pv_done[i]), 1);
-            mbar_init(B_(bars->info_read[i]), 256);
         }
         for (int i = 0; i < kVStages; ++i) {
             mbar_init(B_(bars->v_full[i]), 1);
@@ -589,23 +588,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                     }
                 }
                 if (!ok && lead) *abort_flag = 1;
-            } else if (warp == 2 && lane == 0) {
-                // ---- relay: a P buffer is free again once its product completed and its info was read
-                uint32_t jj = 0;
-                bool ok = true;
-                while (ok && w.next(p)) {
-                    for (int i = w.i0; i < w.i1; ++i, ++jj) {
-                        const uint32_t pb = jj % kPBufs;
-                        if (i == w.i1 - 1) continue;   // the drain goes through a part's last buffer, and frees it
-                        if (!mbar_wait(B_(bars->pv_done[pb]), (jj / kPBufs) & 1, p.err, abort_flag) ||
-                            !mbar_wait(B_(bars->info_read[pb]), (jj / kPBufs) & 1, p.err, abort_flag)) {
-                            *abort_flag = 1;
-                            ok = false;
-                            break;
-                        }
-                        mbar_arrive_remote(B_(bars->p_free[pb]), 0);
-                    }
-                }
             }
         }
     } else {
@@ -788,23 +770,22 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             // ---- rescaling, cleaning and drain: thread = TMEM lane, warpgroup wg has latent columns [256 wg, 256 wg + 256)
             uint32_t jj = 0, it = 0;
             int2 cut = make_int2(-1, 0);
-            bool ok = true, fail;
+            bool ok = true, fail = false;
             while (ok && w.next(p)) {
                 float l_old = 0.f, l_new = 0.f;   // the sums of the two warpgroups of the score CTA
                 for (int i = w.i0; i < w.i1; ++i, ++jj, it += 8) {
                     const uint32_t pb = jj % kPBufs;
-                    fail = !mbar_wait<true>(B_(bars->p_full[pb]), (jj / kPBufs) & 1, p.err, abort_flag);
+                    fail = !mbar_wait<true>(B_(bars->p_full[pb]), (jj / kPBufs) & 1, p.err, abort_flag) || fail;
                     if (named_bar_or(4, 256, fail)) { ok = false; break; }
                     float2 fl = ld_shared_v2f(base + pb * kPUnit + 2 * kSlab + row * 8);
-                    mbar_arrive(B_(bars->info_read[pb]));
                     const bool dirty = signbit(fl.x);
                     fl.x = fabsf(fl.x);
                     l_old = i == w.i0 ? 0.f : l_new * fl.x;
                     l_new = fl.y;
                     const bool grew = i > w.i0 && fl.x != 1.f;
                     const bool any_dirty = named_bar_or(4, 256, dirty), any_grew = named_bar_or(5, 256, grew);
+                    const uint32_t prev = jj - 1;
                     if (any_grew) {
-                        const uint32_t prev = jj - 1;
                         fail = !mbar_wait(B_(bars->pv_done[prev % kPBufs]), (prev / kPBufs) & 1, p.err, abort_flag);
                         if (named_bar_or(4, 256, fail)) { ok = false; break; }
                         tc_fence_after();
@@ -825,7 +806,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                         mbar_arrive(B_(bars->rescaled));
                     }
                     if (any_dirty) {
-                        for (int k = 0; k < 8; ++k) {
+                        // the ring has come to this unit once the product of the one before is done
+                        fail = i > w.i0 && !mbar_wait(B_(bars->pv_done[prev % kPBufs]), (prev / kPBufs) & 1, p.err, abort_flag);
+                        for (int k = 0; !fail && k < 8; ++k) {
                             const uint32_t s = it + k, st = s % kVStages;
                             fail = !mbar_wait(B_(bars->v_full[st]), (s / kVStages) & 1, p.err, abort_flag);
                             if (fail) break;
@@ -843,11 +826,18 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                         }
                         if (named_bar_or(4, 256, fail)) { ok = false; break; }
                     }
+                    // All have read the info of the unit before: its P buffer is free once its product is done.  (A part's
+                    // last one is freed by the drain.)
+                    if (threadIdx.x == 128 && i > w.i0) {
+                        fail = !mbar_wait(B_(bars->pv_done[prev % kPBufs]), (prev / kPBufs) & 1, p.err, abort_flag);
+                        if (!fail) mbar_arrive_remote(B_(bars->p_free[prev % kPBufs]), 0);
+                    }
+                    __syncwarp();
                 }
                 if (!ok) break;
                 // the part's end
                 const uint32_t prev = jj - 1;
-                fail = !mbar_wait(B_(bars->pv_done[prev % kPBufs]), (prev / kPBufs) & 1, p.err, abort_flag);
+                fail = !mbar_wait(B_(bars->pv_done[prev % kPBufs]), (prev / kPBufs) & 1, p.err, abort_flag) || fail;
                 if (named_bar_or(4, 256, fail)) { ok = false; break; }
                 tc_fence_after();
                 const bool whole = w.whole();

@@ -193,6 +193,12 @@ def test_many_sequences(env):
     check(env, problem(env, 2, 3, rng.integers(0, 400, 333).tolist(), counts=rng.integers(0, 3, 333).tolist()))
 
 
+@pytest.mark.parametrize("lens", [[0, 0, 0, 700], [0, 300], [0], [130, 0, 0, 0, 0, 1500]])
+def test_short_sequences_before_long_ones(env, lens):
+    """Clusters that take several tiles of one unit of the cache each and then longer ones, in many orders."""
+    check(env, problem(env, 1, 2, (lens * 400)[:400 if len(lens) > 1 else 1000]))
+
+
 def test_rising_scores(env):
     """Each token's scores rise along the cache by far more than a softmax keeps, in a different direction per head."""
     torch, _ = env
