@@ -1040,23 +1040,26 @@ __device__ __forceinline__ bool is_token(const UpParams &p, long long m, int &b,
 }
 
 // Few tokens: one CTA per (head, 32 tokens).  Rows into two swizzled tiles (one of each part), from ws_rows or joined from
-// parts, as many warps to a row as there are; times W_UV[h]^T, streamed in eight chunks of 64 latent columns; the gate.
+// parts, as many warps to a row as there are; times W_UV[h]^T in eight slabs of 64 latent columns; the gate.  All slabs are
+// loaded before the pair kernel ends where every CTA has an SM to itself (kW = 8); otherwise two CTAs share one and two
+// stages take the slabs in turn.
 constexpr int kFewRows = 32, kFewThreads = 256, kFewWarps = kFewThreads / 32;
 constexpr uint32_t kFewSlab = kFewRows * 128;             // [32 rows x 64 latent columns]
 constexpr uint32_t kFewW = 2 * 8 * kFewSlab;              // an M = 128 read of the last slab ends inside the W_UV stages
-constexpr uint32_t kFewBars = kFewW + 2 * kSlab;
-constexpr uint32_t kFewSmem = kFewBars + 64 + 1024;       // two CTAs per SM
+constexpr uint32_t few_bars(int kW) { return kFewW + kW * kSlab; }
+constexpr uint32_t few_smem(int kW) { return few_bars(kW) + 192 + 1024; }
 static_assert(kFewWarps * kR * 4 <= 16 * kFewSlab, "the warps' sums fit where the tiles go");
 
-__global__ void __launch_bounds__(kFewThreads, 2)
+template <int kW>
+__global__ void __launch_bounds__(kFewThreads, kW == 8 ? 1 : 2)
     attend_few_kernel(const __grid_constant__ CUtensorMap tm_w, const UpParams p) {
     extern __shared__ uint8_t smem_raw[];
     const uint32_t raw = smem_u32(smem_raw);
     const uint32_t base = (raw + 1023u) & ~1023u;
-    uint64_t *const w_full = reinterpret_cast<uint64_t *>(smem_raw + (base - raw) + kFewBars);   // [2]
-    uint64_t *const w_empty = w_full + 2;                                                         // [2]
-    uint64_t *const done = w_full + 4;
-    uint32_t *const tmem_slot = reinterpret_cast<uint32_t *>(w_full + 5);
+    uint64_t *const w_full = reinterpret_cast<uint64_t *>(smem_raw + (base - raw) + few_bars(kW));   // [kW]
+    uint64_t *const w_empty = w_full + kW;                                                            // [kW]
+    uint64_t *const done = w_full + 2 * kW;
+    uint32_t *const tmem_slot = reinterpret_cast<uint32_t *>(w_full + 2 * kW + 1);
     __shared__ int2 s_tile[kFewRows];   // first and last cluster of each row's tile; {-1, .}: not a token
     __shared__ int s_row[kFewRows];     // the row's place in its tile
     __shared__ float s_m[kFewWarps], s_sum[kFewWarps];
@@ -1066,7 +1069,7 @@ __global__ void __launch_bounds__(kFewThreads, 2)
     const int rows = static_cast<int>(min(static_cast<long long>(kFewRows), static_cast<long long>(p.B) * p.T - m0));
 
     if (threadIdx.x == 0) {
-        for (int i = 0; i < 5; ++i) mbar_init(smem_u32(w_full + i), 1);
+        for (int i = 0; i < 2 * kW + 1; ++i) mbar_init(smem_u32(w_full + i), 1);
         fence_mbar_init();
     }
     if (warp == 0) {
@@ -1077,17 +1080,17 @@ __global__ void __launch_bounds__(kFewThreads, 2)
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = *tmem_slot;
-    const auto load_w = [&](int k) {   // latent columns [64 k, 64 k + 64) of W_UV[h] into stage k % 2
-        const uint32_t bar = smem_u32(w_full + (k & 1));
+    const auto load_w = [&](int k) {   // latent columns [64 k, 64 k + 64) of W_UV[h] into stage k % kW
+        const uint32_t bar = smem_u32(w_full + k % kW);
         mbar_arrive_expect_tx(bar, kSlab);
-        tma_load_2d(base + kFewW + (k & 1) * kSlab, &tm_w, bar, k * 64, h * kDV);
+        tma_load_2d(base + kFewW + (k % kW) * kSlab, &tm_w, bar, k * 64, h * kDV);
     };
     // the pair kernel launches this one after its own wait: what the call was given may be read already
     if (threadIdx.x == 0) {
         tma_prefetch_desc(&tm_w);
-        load_w(0);
-        load_w(1);
-        for (int k = 2; k < 8; ++k) tma_prefetch_l2_2d(&tm_w, k * 64, h * kDV);
+#pragma unroll 1
+        for (int k = 0; k < kW; ++k) load_w(k);
+        for (int k = kW; k < 8; ++k) tma_prefetch_l2_2d(&tm_w, k * 64, h * kDV);
     }
     int b = 0, t = 0;
     const bool token = threadIdx.x < rows && is_token(p, m0 + threadIdx.x, b, t);
@@ -1167,10 +1170,11 @@ __global__ void __launch_bounds__(kFewThreads, 2)
         const uint32_t idesc = make_idesc_bf16(128, kDV, 0, 0);
         const uint64_t a0 = make_smem_desc(base, 16, 1024), b0 = make_smem_desc(base + kFewW, 16, 1024);
         bool ok = true;
-        int loaded = 2;
+        int loaded = kW;
+#pragma unroll 1
         for (int k = 0; ok && k < 8; ++k) {
-            const int st = k & 1;
-            if (!(ok = mbar_wait(smem_u32(w_full + st), (k >> 1) & 1, p.err))) break;
+            const int st = k % kW;
+            if (!(ok = mbar_wait(smem_u32(w_full + st), (k / kW) & 1, p.err))) break;
             tc_fence_after();
 #pragma unroll
             for (int kk = 0; kk < 4; ++kk) {
@@ -1178,17 +1182,17 @@ __global__ void __launch_bounds__(kFewThreads, 2)
                 umma_bf16(tmem, a, bd, idesc, (k | kk) != 0);
                 umma_bf16(tmem, desc_add(a, 8 * kFewSlab), bd, idesc, 1);
             }
-            umma_commit(smem_u32(w_empty + st));
-            if (k + 2 < 8) {   // the stage is refilled once its products completed
-                if (!(ok = mbar_wait(smem_u32(w_empty + st), (k >> 1) & 1, p.err))) break;
-                load_w(k + 2);
+            if (k + kW < 8) {   // the stage is refilled once its products completed
+                umma_commit(smem_u32(w_empty + st));
+                if (!(ok = mbar_wait(smem_u32(w_empty + st), (k / kW) & 1, p.err))) break;
+                load_w(k + kW);
                 ++loaded;
             }
         }
         if (ok) umma_commit(smem_u32(done));
         if (!ok)   // no load may still be landing when the CTA exits
-            for (int k = max(loaded - 2, 0); k < loaded; ++k)
-                mbar_wait(smem_u32(w_full + (k & 1)), (k >> 1) & 1, p.err, nullptr, kLandNs);
+            for (int k = loaded - kW; k < loaded; ++k)
+                mbar_wait(smem_u32(w_full + k % kW), (k / kW) & 1, p.err, nullptr, kLandNs);
     }
     __syncwarp();
     if (warp == 0) {
@@ -1444,7 +1448,8 @@ cudaError_t prepare(int num_sms, int &clusters) {
         return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(bytes));
     };
     if ((e = smem(attend_pair_kernel, kSmemPair)) != cudaSuccess) return e;
-    if ((e = smem(attend_few_kernel, kFewSmem)) != cudaSuccess) return e;
+    if ((e = smem(attend_few_kernel<2>, few_smem(2))) != cudaSuccess) return e;
+    if ((e = smem(attend_few_kernel<8>, few_smem(8))) != cudaSuccess) return e;
     if ((e = smem(attend_up_kernel, kUpSmem)) != cudaSuccess) return e;
     cudaFuncAttributes fa;   // the register split assumes this launch budget
     if ((e = cudaFuncGetAttributes(&fa, attend_pair_kernel)) != cudaSuccess) return e;
@@ -1527,9 +1532,11 @@ cudaError_t launch_attend_paged(const AttendPagedArgs &a, cudaStream_t s) {
                       static_cast<const __nv_bfloat16 *>(a.gate), static_cast<__nv_bfloat16 *>(a.out), a.dev_err, a.B, a.T,
                       a.H, sp.tiles, a.bs, a.max_blocks};
     if (m <= kFewTokens) {
+        const unsigned ctas = static_cast<unsigned>((m + kFewRows - 1) / kFewRows * a.H);
         note_launch();
-        return launch_dependent(attend_few_kernel, dim3(static_cast<unsigned>((m + kFewRows - 1) / kFewRows * a.H)),
-                                kFewThreads, kFewSmem, s, tm_w, up);
+        return ctas <= static_cast<unsigned>(a.num_sms)
+                   ? launch_dependent(attend_few_kernel<8>, dim3(ctas), kFewThreads, few_smem(8), s, tm_w, up)
+                   : launch_dependent(attend_few_kernel<2>, dim3(ctas), kFewThreads, few_smem(2), s, tm_w, up);
     }
     CUtensorMap tm_a;
     {
