@@ -91,6 +91,23 @@ struct PairBars {
 };
 static_assert(sizeof(PairBars) <= 768, "barrier block too large");
 
+// Division of 0 <= n < 2^31 by a d of the launch: n / d = n * mul >> (31 + s) with 2^(s - 1) < d <= 2^s and mul =
+// floor(2^(31 + s) / d) + 1, as n (mul d - 2^(31 + s)) <= n 2^s < 2^(31 + s).  (Each division takes some forty instructions,
+// and a part's start is a chain of them.)
+struct Divisor {
+    unsigned mul, shift;
+    Divisor() = default;
+    explicit Divisor(int d) {
+        unsigned s = 0;
+        while ((1ull << s) < static_cast<unsigned long long>(d)) ++s;
+        mul = d == 1 ? 0 : static_cast<unsigned>((1ull << (31 + s)) / d + 1);
+        shift = d == 1 ? 0 : s - 1;
+    }
+    __device__ __forceinline__ int operator()(int n) const {
+        return mul ? static_cast<int>(__umulhi(static_cast<unsigned>(n), mul) >> shift) : n;
+    }
+};
+
 struct PairParams {
     const int *table, *lens, *counts, *parents;
     long long ld_table;
@@ -103,6 +120,7 @@ struct PairParams {
     int *err;
     int B, T, H, tiles, num_blocks, bs, max_blocks, window, sinks;
     float scale_log2;
+    Divisor by_H, by_tiles, by_bs;
 };
 
 // New tokens of sequence b and its cached rows; none when its numbers are out of range.
@@ -126,7 +144,7 @@ struct Tile {
     __device__ __forceinline__ Tile(const PairParams &p, int j, int len, int count) {
         const int m0 = j * kM;
         rows = min(count * p.H - m0, kM);
-        t0 = m0 / p.H, t1 = (m0 + rows - 1) / p.H;
+        t0 = p.by_H(m0), t1 = p.by_H(m0 + rows - 1);
         end = len + t1 + 1;
         main = head = 0;
         if (p.window > 0) {   // a draft stands at least at the first new position
@@ -355,11 +373,16 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         tmem_alloc(smem_u32(&bars->tmem_base), 512);
         tmem_relinquish();
     }
+    if (warp == 0 || warp == 3) {   // the producers
+        tma_prefetch_desc(rank == 0 ? &tm_s : &tm_v);
+        if (rank == 0) tma_prefetch_desc(&tm_q);
+    }
     tc_fence_before();
     cluster_sync_all();   // both CTAs' barriers exist before any remote arrival or copy
     tc_fence_after();
     const uint32_t tmem = __shfl_sync(0xffffffffu, bars->tmem_base, 0);
     grid_dependency_wait();
+    if (warp == 0 || warp == 3) fence_proxy_async_all();
     grid_launch_dependents();   // the second kernel may take SMs as clusters finish; it waits for the whole grid
 
     // The axis: thread i adds up its part of the tiles; the one that holds the share's start finds the tile there.
@@ -368,7 +391,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         const int g0 = min(static_cast<int>(threadIdx.x) * per, all), g1 = min(g0 + per, all);
         int len = 0, count = 0;
         const auto units = [&](int g, bool report) {
-            const int b = g / p.tiles, j = g - b * p.tiles;
+            const int b = p.by_tiles(g), j = g - b * p.tiles;
             count = tokens(p, b, len, report);
             return static_cast<long long>(j) * kM < static_cast<long long>(count) * p.H
                        ? kStart + Tile(p, j, len, count).n : 0;
@@ -404,7 +427,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             for (int g = g0; g < g1; ++g) {
                 const long long k = per == 1 ? sum : units(g, false);
                 if (lo < pre + k) {
-                    bars->b = g / p.tiles, bars->j = g - bars->b * p.tiles;
+                    bars->b = p.by_tiles(g), bars->j = g - bars->b * p.tiles;
                     bars->len = len, bars->count = count;
                     bars->lo = lo, bars->hi = hi, bars->pre = pre;
                     break;
@@ -419,7 +442,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     const auto pool_row = [&](int seq, int u, int end) {
         const int none = max(p.num_blocks * p.bs, 1);
         if (u >= end) return none;
-        const int j = u / p.bs, block = __ldg(p.table + seq * p.ld_table + j);
+        const int j = p.by_bs(u), block = __ldg(p.table + seq * p.ld_table + j);
         if (block < 0 || block >= p.num_blocks) {
             record_error(p.err, kDevErrBounds);
             return none;
@@ -440,9 +463,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             if (warp == 0 || warp == 3) {
                 // ---- TMA producers: rows [64 half, 64 half + 64) of each stage; a part's queries, then its units
                 const int half = warp == 0 ? 0 : 1;
-                tma_prefetch_desc(&tm_q);
-                tma_prefetch_desc(&tm_s);
-                fence_proxy_async_all();
                 const uint32_t full0 = B_(bars->sc_full[0]), empty0 = B_(bars->sc_empty[0]);
                 Ring<kSStages> at;
                 uint32_t it = 0;
@@ -509,8 +529,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                 // ---- TMA producers: a unit is 8 stages, latent half i >> 2, row quarter i & 3; each takes one half of
                 // the rows
                 const int half = warp == 0 ? 0 : 1;
-                tma_prefetch_desc(&tm_v);
-                fence_proxy_async_all();
                 const uint32_t full0 = B_(bars->v_full[0]), empty0 = B_(bars->v_empty[0]);
                 Ring<kVStages> at;
                 uint32_t it = 0;
@@ -637,7 +655,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             if (more) load_q(has_rows(w));
             while (ok && more) {
                 const int len = w.seq_len(p);
-                const Sight sight(p, w.seq, min((w.index * kM + row) / p.H, w.t.t1), len, w.count, lane);
+                const Sight sight(p, w.seq, min(p.by_H(w.index * kM + row), w.t.t1), len, w.count, lane);
                 const int i0 = w.i0, i1 = w.i1, slot = w.slot(cl), rows = w.t.rows;
                 const Tile tile = w.t;
                 const bool whole = w.whole(), active = has_rows(w);
@@ -1524,7 +1542,7 @@ cudaError_t launch_attend_paged(const AttendPagedArgs &a, cudaStream_t s) {
     const long long all_rows = m * a.H;
     const PairParams pp{a.table, a.lens, a.counts, a.parents, a.ld_table,
                         ws_rows, ws_exp, ws_m, ws_l, ws_tile, ws_cut, all_rows, a.dev_err, a.B, a.T, a.H, sp.tiles,
-                        a.num_blocks, a.bs, a.max_blocks, a.window, a.sinks, a.scale * kLog2e};
+                        a.num_blocks, a.bs, a.max_blocks, a.window, a.sinks, a.scale * kLog2e, Divisor(a.H), Divisor(sp.tiles), Divisor(a.bs)};
     note_launch();
     e = launch_dependent(attend_pair_kernel, dim3(2 * G), kThreads, kSmemPair, s, tm_q, tm_s, tm_v, pp);
     if (e != cudaSuccess) return e;
