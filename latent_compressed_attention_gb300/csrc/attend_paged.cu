@@ -85,8 +85,8 @@ struct PairBars {
     uint32_t tmem_base;
     int abort;
     // where the cluster's share starts on the axis of units
-    long long lo, hi, pre;
-    int b, j, len, count;
+    long long lo, hi, pre, total;
+    int b, j, len, count, shares;
     long long warp_sum[kThreads / 32];
 };
 static_assert(sizeof(PairBars) <= 768, "barrier block too large");
@@ -115,7 +115,8 @@ struct PairParams {
     uint8_t *ws_exp;                     // [.][16]: their exponents
     float *ws_m, *ws_l;                  // [2 G][128]: parts' maxima (log2 units) and sums of weights
     int2 *ws_tile;                       // [B * tiles]: first and last cluster of each tile
-    int2 *ws_cut;                        // [G]: sequence and tile that a cluster starts and leaves unfinished; {-1, .}: none
+    int4 *ws_cut;                        // [G]: first row, rows and last cluster of the tile that a cluster starts and leaves
+                                         // unfinished; {., 0, ., .}: none
     long long all_rows;                  // B * T * H
     int *err;
     int B, T, H, tiles, num_blocks, bs, max_blocks, window, sinks;
@@ -422,6 +423,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                                      : total * c / n;
         };
         const long long lo = cl < n ? start(cl) : 0, hi = cl < n ? start(cl + 1) : 0;
+        if (threadIdx.x == 0) bars->total = total, bars->shares = n;
         if (threadIdx.x == 0 && lo == hi) bars->b = p.B, bars->lo = bars->hi = bars->pre = 0;
         if (lo < hi && pre <= lo && lo < pre + sum) {
             for (int g = g0; g < g1; ++g) {
@@ -794,7 +796,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         } else {
             // ---- rescaling, cleaning and drain: thread = TMEM lane, warpgroup wg has latent columns [256 wg, 256 wg + 256)
             uint32_t jj = 0, it = 0;
-            int2 cut = make_int2(-1, 0);
+            int4 cut = make_int4(0, 0, 0, 0);
             bool ok = true, fail = false;
             while (ok && w.next(p)) {
                 float l_old = 0.f, l_new = 0.f;   // the sums of the two warpgroups of the score CTA
@@ -918,7 +920,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                     int2 *const tile = p.ws_tile + static_cast<long long>(w.seq) * p.tiles + w.index;
                     if (w.i0 == 0) tile->x = cl;
                     if (w.i1 == w.t.n) tile->y = cl;
-                    if (w.i0 == 0 && w.i1 < w.t.n) cut = make_int2(w.seq, w.index);
+                    if (w.i0 == 0 && w.i1 < w.t.n) {   // the share that holds the tile's last unit: start(c) < w.pre
+                        const int last = static_cast<int>((w.pre * bars->shares - 1) / bars->total);
+                        cut = make_int4(w.seq * p.T * p.H + w.index * kM, w.t.rows, last, 0);
+                    }
                 }
                 fence_proxy_async_smem();   // the next P's copy follows
                 tc_fence_before();
@@ -946,7 +951,8 @@ struct UpParams {
     __half *ws_rows;
     uint8_t *ws_exp;
     const float *ws_m, *ws_l;
-    const int2 *ws_tile, *ws_cut;
+    const int2 *ws_tile;
+    const int4 *ws_cut;
     long long all_rows;
     const __nv_bfloat16 *gate;
     __nv_bfloat16 *out;
@@ -1239,14 +1245,11 @@ constexpr int kJoinThreads = 512;
 __global__ void __launch_bounds__(kJoinThreads) attend_join_kernel(const UpParams p) {
     grid_dependency_wait();
     grid_launch_dependents();
-    const int2 cut = p.ws_cut[blockIdx.x >> 3];
-    if (cut.x < 0) return;
-    const int lane = threadIdx.x & 31, r = (blockIdx.x & 7) * 16 + (threadIdx.x >> 5);
-    int len;
-    if (static_cast<long long>(cut.y) * kM + r >= static_cast<long long>(tokens(p, cut.x, len, false)) * p.H) return;
-    const int2 tile = p.ws_tile[static_cast<long long>(cut.x) * p.tiles + cut.y];
+    const int c = blockIdx.x >> 3, lane = threadIdx.x & 31, r = (blockIdx.x & 7) * 16 + (threadIdx.x >> 5);
+    const int4 cut = p.ws_cut[c];
+    if (r >= cut.y) return;
     float o[16], M, sum;
-    join_parts(p, tile.x, tile.y, r, 0, 1, lane, o, M, sum);
+    join_parts(p, c, cut.z, r, 0, 1, lane, o, M, sum);
     const float inv = 1.f / sum;
     float top = 0.f;
 #pragma unroll
@@ -1256,7 +1259,7 @@ __global__ void __launch_bounds__(kJoinThreads) attend_join_kernel(const UpParam
     uint32_t x[8];
 #pragma unroll
     for (int k = 0; k < 8; ++k) x[k] = pack_f16x2(o[2 * k] * up, o[2 * k + 1] * up);
-    const long long row = static_cast<long long>(cut.x) * p.T * p.H + static_cast<long long>(cut.y) * kM + r;
+    const long long row = cut.x + r;
     st_global_32B(p.ws_rows + row * kR + lane * 16, make_uint4(x[0], x[1], x[2], x[3]), make_uint4(x[4], x[5], x[6], x[7]));
     if ((lane & 1) == 0) p.ws_exp[row * 16 + (lane >> 1)] = static_cast<uint8_t>(E);
 }
@@ -1270,7 +1273,7 @@ constexpr int kUpStages = 3;
 constexpr uint32_t kUpA = 8 * kSlab, kUpStage = 2 * kSlab;
 constexpr uint32_t kUpBars = kUpA + kUpStages * kUpStage;
 struct UpBars {
-    uint64_t w_full, w_empty, full[kUpStages], split[kUpStages], empty[kUpStages], acc_full[2], acc_empty[2];
+    uint64_t w_full[8], w_empty[8], full[kUpStages], split[kUpStages], empty[kUpStages], acc_full[2], acc_empty[2];
     uint32_t tmem_base;
 };
 constexpr uint32_t kUpSmem = kUpBars + 256 + 1024;
@@ -1290,8 +1293,7 @@ __global__ void __launch_bounds__(kUpThreads, 1)
     const int i0 = static_cast<int>(items * blockIdx.x / gridDim.x), i1 = static_cast<int>(items * (blockIdx.x + 1) / gridDim.x);
 
     if (threadIdx.x == 0) {
-        mbar_init(B_(bars->w_full), 1);
-        mbar_init(B_(bars->w_empty), 1);
+        for (int i = 0; i < 8; ++i) mbar_init(B_(bars->w_full[i]), 1), mbar_init(B_(bars->w_empty[i]), 1);
         for (int i = 0; i < kUpStages; ++i) {
             mbar_init(B_(bars->full[i]), 1);
             mbar_init(B_(bars->split[i]), 256);
@@ -1322,54 +1324,52 @@ __global__ void __launch_bounds__(kUpThreads, 1)
         bool ok = true;
         for (int i = i0; ok && i < i1; ++i) {
             const int h = i / blocks, m0 = (i - h * blocks) * kM;
-            if (h != head) {
-                if (!(ok = wait(bars->w_empty, w_phase ^ 1))) break;
-                w_phase ^= 1;
-                if (lead) {
-                    mbar_arrive_expect_tx(B_(bars->w_full), 8 * kSlab);
-                    for (int k = 0; k < 8; ++k)
-                        tma_load_2d(base + k * kSlab, &tm_w, B_(bars->w_full), k * 64, h * kDV);
+            const bool new_head = h != head;
+#pragma unroll 1
+            for (int k = 0; k < 8; ++k, ++it, at.next()) {
+                if (new_head) {   // a slab of the next head's W_UV as soon as this one's last products with it are done
+                    if (!(ok = wait(bars->w_empty[k], w_phase ^ 1))) break;
+                    if (lead) {
+                        mbar_arrive_expect_tx(B_(bars->w_full[k]), kSlab);
+                        tma_load_2d(base + k * kSlab, &tm_w, B_(bars->w_full[k]), k * 64, h * kDV);
+                    }
                 }
-                if (head < 0) {   // W_UV was there before the kernels that this one waits for
+                if (it == 0) {   // W_UV was there before the kernels that this one waits for
                     grid_dependency_wait();
                     fence_proxy_async_all();
                 }
-                head = h;
-            }
-#pragma unroll 1
-            for (int k = 0; k < 8; ++k, ++it, at.next()) {
                 if (!(ok = wait(bars->empty[at.st], at.phase ^ 1))) break;
                 if (lead) {
                     mbar_arrive_expect_tx(B_(bars->full[at.st]), kSlab);
                     tma_load_3d(base + kUpA + at.st * kUpStage, &tm_a, B_(bars->full[at.st]), k * 64, h, m0);
                 }
             }
+            w_phase ^= new_head;
+            head = h;
         }
         // no load may still be landing when the CTA exits
         for (uint32_t k = it > kUpStages ? it - kUpStages : 0; k < it; ++k)
             mbar_wait(B_(bars->full[k % kUpStages]), (k / kUpStages) & 1, p.err, nullptr, kLandNs);
-        if (head >= 0) mbar_wait(B_(bars->w_full), w_phase ^ 1, p.err, nullptr, kLandNs);
+        for (int k = 0; ok && head >= 0 && k < 8; ++k) mbar_wait(B_(bars->w_full[k]), w_phase ^ 1, p.err, nullptr, kLandNs);
     } else if (warp == 1) {
         const bool lead = elect_one();
         const uint32_t idesc = make_idesc_bf16(128, kDV, 0, 0);
         const uint64_t w0 = make_smem_desc(base, 16, 1024), a0 = make_smem_desc(base + kUpA, 16, 1024);
         Ring<kUpStages> at;
         Ring<2> acc;
-        uint32_t w_phase = 0;
+        uint32_t w_phase = 1;   // of the head that is there
         int head = -1;
         bool ok = true;
         for (int i = i0; ok && i < i1; ++i, acc.next()) {
             const int h = i / blocks;
-            if (h != head) {
-                if (!(ok = wait(bars->w_full, w_phase))) break;
-                w_phase ^= 1;
-                head = h;
-            }
+            w_phase ^= h != head;
+            head = h;
+            const bool last = i + 1 == i1 || (i + 1) / blocks != h;   // of the head's items here
             if (!(ok = wait(bars->acc_empty[acc.st], acc.phase ^ 1))) break;
             const uint32_t d = tmem + acc.st * 128;
 #pragma unroll 1
             for (int k = 0; k < 8; ++k, at.next()) {
-                if (!(ok = wait(bars->split[at.st], at.phase))) break;
+                if (!(ok = wait(bars->w_full[k], w_phase)) || !(ok = wait(bars->split[at.st], at.phase))) break;
                 tc_fence_after();
                 if (lead) {
                     const uint64_t a = desc_add(a0, at.st * kUpStage), w = desc_add(w0, k * kSlab);
@@ -1379,12 +1379,10 @@ __global__ void __launch_bounds__(kUpThreads, 1)
                         umma_bf16(d, desc_add(a, kSlab + kk * 32), desc_add(w, kk * 32), idesc, 1);
                     }
                     umma_commit(B_(bars->empty[at.st]));
+                    if (last) umma_commit(B_(bars->w_empty[k]));
                 }
             }
-            if (ok && lead) {
-                umma_commit(B_(bars->acc_full[acc.st]));
-                if (i + 1 == i1 || (i + 1) / blocks != h) umma_commit(B_(bars->w_empty));
-            }
+            if (ok && lead) umma_commit(B_(bars->acc_full[acc.st]));
         }
     } else if (warp < 10) {
         grid_dependency_wait();
@@ -1458,9 +1456,6 @@ CUresult encode_map(CUtensorMap *m, const void *ptr, int rank, const cuuint64_t 
               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
 }
 
-// Up to so many tokens the join, W_UV and the gate are one kernel of short CTAs.
-constexpr long long kFewTokens = 64;
-
 // What is asked of a device once: the kernels' attributes, and how many clusters of the pair kernel run at once.
 cudaError_t prepare(int num_sms, int &clusters) {
     constexpr int kMaxDev = 64;
@@ -1506,8 +1501,8 @@ struct Space {
         m = exp + rows * 16;
         l = m + parts * 4;
         tile = l + parts * 4;
-        cut = tile + static_cast<size_t>(B) * tiles * sizeof(int2);
-        end = cut + clusters * sizeof(int2);
+        cut = (tile + static_cast<size_t>(B) * tiles * sizeof(int2) + 15) / 16 * 16;
+        end = cut + clusters * sizeof(int4);
     }
 };
 
@@ -1544,7 +1539,8 @@ cudaError_t launch_attend_paged(const AttendPagedArgs &a, cudaStream_t s) {
     auto *const ws_rows = reinterpret_cast<__half *>(ws);
     auto *const ws_exp = reinterpret_cast<uint8_t *>(ws + sp.exp);
     float *const ws_m = reinterpret_cast<float *>(ws + sp.m), *const ws_l = reinterpret_cast<float *>(ws + sp.l);
-    int2 *const ws_tile = reinterpret_cast<int2 *>(ws + sp.tile), *const ws_cut = reinterpret_cast<int2 *>(ws + sp.cut);
+    int2 *const ws_tile = reinterpret_cast<int2 *>(ws + sp.tile);
+    int4 *const ws_cut = reinterpret_cast<int4 *>(ws + sp.cut);
     const long long m = static_cast<long long>(a.B) * a.T;
     const long long all_rows = m * a.H;
     const PairParams pp{a.table, a.lens, a.counts, a.parents, a.ld_table,
@@ -1556,12 +1552,15 @@ cudaError_t launch_attend_paged(const AttendPagedArgs &a, cudaStream_t s) {
     const UpParams up{a.lens, a.counts, ws_rows, ws_exp, ws_m, ws_l, ws_tile, ws_cut, all_rows,
                       static_cast<const __nv_bfloat16 *>(a.gate), static_cast<__nv_bfloat16 *>(a.out), a.dev_err, a.B, a.T,
                       a.H, sp.tiles, a.bs, a.max_blocks};
-    if (m <= kFewTokens) {
-        const unsigned ctas = static_cast<unsigned>((m + kFewRows - 1) / kFewRows * a.H);
+    // Up to 32 tokens, and up to 64 of many heads, the join, W_UV and the gate are one kernel of short CTAs (one token of 96
+    // heads over 30000 rows takes 28.7 us with it and 48.7 with the two others, 64 tokens of 96 heads 62.8 and 64.1, of 16
+    // heads 38.9 and 34.8, 128 tokens of 96 heads 87.5 and 75.2).
+    const long long ctas = (m + kFewRows - 1) / kFewRows * a.H;
+    if (m <= kFewRows || (m <= 2 * kFewRows && ctas > a.num_sms / 2)) {
         note_launch();
-        return ctas <= static_cast<unsigned>(a.num_sms)
-                   ? launch_dependent(attend_few_kernel<8>, dim3(ctas), kFewThreads, few_smem(8), s, tm_w, up)
-                   : launch_dependent(attend_few_kernel<2>, dim3(ctas), kFewThreads, few_smem(2), s, tm_w, up);
+        const dim3 grid(static_cast<unsigned>(ctas));
+        return ctas <= a.num_sms ? launch_dependent(attend_few_kernel<8>, grid, kFewThreads, few_smem(8), s, tm_w, up)
+                                 : launch_dependent(attend_few_kernel<2>, grid, kFewThreads, few_smem(2), s, tm_w, up);
     }
     CUtensorMap tm_a;
     {
