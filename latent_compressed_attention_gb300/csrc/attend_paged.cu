@@ -8,8 +8,10 @@
 //
 // Pair kernel (persistent, one cluster of two CTAs per SM pair).  A tile walks the cache in units of 128 rows that any of
 // its tokens sees: the first few (sinks), then from the window's start to the last token's own row.  All tiles' units, each
-// tile's preceded by the cost of starting it, are cut into one equal share per cluster, so that one long sequence and
-// many ragged ones keep every SM busy.
+// tile's preceded by the cost of starting it, are cut into equal shares, so that one long sequence and many ragged ones
+// keep every SM busy: one share per cluster, or a few rounds of one per cluster where a sequence has several tiles and all
+// sequences' rows together do not fit L2: the clusters of a round are at the same sequences, and their tiles read a row
+// from DRAM once.
 //   rank 0, the score CTA: the tile's q_abs sits in TMEM as packed bf16 (columns 0-255) and is the A operand of
 //     S = q_abs . c^T, N = 128 cache rows, into one of two buffers (columns 256-511).  Two warpgroups take the units in
 //     turn (thread = row of the tile) and hand each other the running maximum, so that a unit's product runs while the
@@ -32,6 +34,7 @@
 #include <cuda.h>
 #include <cudaTypedefs.h>
 
+#include <algorithm>
 #include <atomic>
 
 #include "common.cuh"
@@ -51,6 +54,11 @@ constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kRescaleLog2 = 16.0f;
 // Units that starting a tile counts for in the shares: its queries' load, its accumulator's drain, the pipeline's refill.
 constexpr int kStart = 3;
+// Rounds of shares: as many as bring the rows of a round's sequences down to this, but no more than one for every 6 tiles of a
+// sequence, each of them of at least 16 units per cluster.  (16 sequences of 64 drafts of 96 heads over up to 16000 rows, 48
+// tiles each: 1164 us in one round, 1087 in four; 64 sequences of 4, 3 tiles each: 210 and 222.)
+constexpr int kRounds = 4, kRoundTiles = 6, kRoundMin = 16;
+constexpr long long kRoundBytes = 96ll << 20;
 
 constexpr uint32_t kSlab = 16384;                  // [128 rows x 64 columns] bf16, 128-byte swizzle
 constexpr uint32_t kInfo = kM * 8;                 // {rescaling factor, negative to ask for cleaning, sum} per row of the tile
@@ -84,9 +92,13 @@ struct PairBars {
     uint64_t pv_done[kPBufs], rescaled, drained;
     uint32_t tmem_base;
     int abort;
-    // where the cluster's share starts on the axis of units
-    long long lo, hi, pre, total;
-    int b, j, len, count, shares;
+    // the axis of units, and where the cluster's shares start on it
+    long long total;
+    int shares, rounds;
+    struct Start {
+        long long lo, hi, pre;
+        int b, j, len, count;
+    } start[kRounds];
     long long warp_sum[kThreads / 32];
 };
 static_assert(sizeof(PairBars) <= 768, "barrier block too large");
@@ -111,14 +123,15 @@ struct Divisor {
 struct PairParams {
     const int *table, *lens, *counts, *parents;
     long long ld_table;
-    __half *ws_rows;                     // [B * T * H + 2 G * 128][r]: o_lat / l of (token, head) rows, then of parts' rows
+    __half *ws_rows;                     // [B * T * H + 2 shares * 128][r]: o_lat / l of (token, head) rows, then of parts' rows
     uint8_t *ws_exp;                     // [.][16]: their exponents
-    float *ws_m, *ws_l;                  // [2 G][128]: parts' maxima (log2 units) and sums of weights
-    int2 *ws_tile;                       // [B * tiles]: first and last cluster of each tile
-    int4 *ws_cut;                        // [G]: first row, rows and last cluster of the tile that a cluster starts and leaves
-                                         // unfinished; {., 0, ., .}: none
+    float *ws_m, *ws_l;                  // [2 shares][128]: parts' maxima (log2 units) and sums of weights
+    int2 *ws_tile;                       // [B * tiles]: first and last share of each tile
+    int4 *ws_cut;                        // [rounds][G]: first row, rows, first and last share of the tile that a share starts
+                                         // and leaves unfinished; {., 0, ., .}: none
     long long all_rows;                  // B * T * H
     int *err;
+    int max_rounds;
     int B, T, H, tiles, num_blocks, bs, max_blocks, window, sinks;
     float scale_log2;
     Divisor by_H, by_tiles, by_bs;
@@ -162,22 +175,30 @@ struct Tile {
     }
 };
 
-// Every role of both CTAs walks the cluster's share, tile by tile.
+// Every role of both CTAs walks the cluster's shares, tile by tile.
 struct Walk {
     long long lo, hi, pre;   // pre: the axis position of tile j of sequence b
     int b, j, len, count;
-    int seq, i0, i1;         // the current part: its sequence and units [i0, i1) of the tile
+    int round, share;        // of the current part
+    int seq, i0, i1;         // its sequence and units [i0, i1) of the tile
     int index;               // the tile's number in the sequence
     Tile t;
-    __device__ __forceinline__ Walk(const PairParams &p, const PairBars *s) {
-        lo = s->lo, hi = s->hi, pre = s->pre, b = s->b, j = s->j, len = s->len, count = s->count;
+    __device__ __forceinline__ explicit Walk(const PairBars *s) : round(0) { enter(s); }
+    __device__ __forceinline__ void enter(const PairBars *s) {
+        const auto &x = s->start[round];
+        lo = x.lo, hi = x.hi, pre = x.pre, b = x.b, j = x.j, len = x.len, count = x.count;
     }
-    __device__ __forceinline__ bool next(const PairParams &p) {
-        while (pre < hi) {
+    __device__ __forceinline__ bool next(const PairParams &p, const PairBars *s, int cl) {
+        for (;;) {
+            if (pre >= hi || b >= p.B) {
+                if (round + 1 >= s->rounds) return false;
+                ++round;
+                enter(s);
+                continue;
+            }
             if (static_cast<long long>(j) * kM >= static_cast<long long>(count) * p.H) {
                 j = 0;
-                if (++b >= p.B) return false;
-                count = tokens(p, b, len, false);
+                if (++b < p.B) count = tokens(p, b, len, false);
                 continue;
             }
             t = Tile(p, j, len, count);
@@ -188,15 +209,15 @@ struct Walk {
             ++j;
             if (s1 > s0) {
                 i0 = static_cast<int>(s0 - base), i1 = static_cast<int>(s1 - base);
+                share = round * s->shares + cl;
                 return true;
             }
         }
-        return false;
     }
     __device__ __forceinline__ int seq_len(const PairParams &p) const { return __ldg(p.lens + seq); }
     __device__ __forceinline__ bool whole() const { return i0 == 0 && i1 == t.n; }
-    // A cluster has at most one part that starts before it and one that starts in it and ends after it.
-    __device__ __forceinline__ int slot(int cl) const { return 2 * cl + (i0 == 0 ? 1 : 0); }
+    // A share has at most one part that starts before it and one that starts in it and ends after it.
+    __device__ __forceinline__ int slot() const { return 2 * share + (i0 == 0 ? 1 : 0); }
 };
 
 // The cache rows that a token sees: [0, head), [lo, hi), and of the 64 from `hi` on those whose bit is set.
@@ -414,27 +435,34 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             if (w < warp) pre += v;
             total += v;
         }
-        // no share is empty but those of the clusters that are too many: a tile's parts lie in successive clusters
+        // No share is empty but those of the clusters that are too many: a tile's parts lie in successive shares.
         const int n = total < G ? static_cast<int>(total) : G;
+        int rounds = 1;
+        if (p.max_rounds > 1) {
+            const long long bytes = total * (kUnit * kR * 2) / p.tiles, units = total / (n * kRoundMin);
+            rounds = max(1, static_cast<int>(min(min((bytes + kRoundBytes - 1) / kRoundBytes, units),
+                                                 static_cast<long long>(p.max_rounds))));
+        }
+        const int shares = n * rounds;
         const auto start = [&](int c) {   // 64-bit divisions take a few hundred cycles
-            if (c >= n) return c == n ? total : 0;
-            return total < (1 << 24) ? static_cast<long long>(static_cast<unsigned>(total) * static_cast<unsigned>(c) /
-                                                              static_cast<unsigned>(n))
-                                     : total * c / n;
+            return total < (1 << 22) ? static_cast<long long>(static_cast<unsigned>(total) * static_cast<unsigned>(c) /
+                                                              static_cast<unsigned>(shares))
+                                     : total * c / shares;
         };
-        const long long lo = cl < n ? start(cl) : 0, hi = cl < n ? start(cl + 1) : 0;
-        if (threadIdx.x == 0) bars->total = total, bars->shares = n;
-        if (threadIdx.x == 0 && lo == hi) bars->b = p.B, bars->lo = bars->hi = bars->pre = 0;
-        if (lo < hi && pre <= lo && lo < pre + sum) {
+        if (threadIdx.x == 0) bars->total = total, bars->shares = n, bars->rounds = cl < n ? rounds : 0;
+        if (cl >= n && threadIdx.x == 0) bars->start[0] = {0, 0, 0, p.B, 0, 0, 0};
+        for (int r = 0; cl < n && r < rounds; ++r) {
+            const long long lo = start(r * n + cl), hi = start(r * n + cl + 1);
+            if (pre > lo || lo >= pre + sum) continue;
+            long long at = pre;
             for (int g = g0; g < g1; ++g) {
                 const long long k = per == 1 ? sum : units(g, false);
-                if (lo < pre + k) {
-                    bars->b = p.by_tiles(g), bars->j = g - bars->b * p.tiles;
-                    bars->len = len, bars->count = count;
-                    bars->lo = lo, bars->hi = hi, bars->pre = pre;
+                if (lo < at + k) {
+                    const int b = p.by_tiles(g);
+                    bars->start[r] = {lo, hi, at, b, g - b * p.tiles, len, count};
                     break;
                 }
-                pre += k;
+                at += k;
             }
         }
         __syncthreads();
@@ -454,7 +482,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 
     if (warp < 4) {
         regs_release<kRegsCtl>();
-        Walk w(p, bars);
+        Walk w(bars);
         const bool lead = elect_one();
         // a whole warp leaves a wait together and of one mind
         const auto wait = [&](uint32_t bar, uint32_t parity) {
@@ -469,7 +497,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                 Ring<kSStages> at;
                 uint32_t it = 0;
                 bool ok = true;
-                while (ok && w.next(p)) {
+                while (ok && w.next(p, bars, cl)) {
                     for (int i = w.i0 - 1; ok && i < w.i1; ++i) {
                         const bool units = i >= w.i0;
                         const int u = units ? w.t.row0(i) + half * 64 : 0;
@@ -500,7 +528,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                 Ring<2> sb;
                 uint32_t q_phase = 0;
                 bool ok = true;
-                while (ok && w.next(p)) {
+                while (ok && w.next(p, bars, cl)) {
                     for (int k = 0; k < 8; ++k) at.next();   // the queries' stages
                     if (!(ok = wait(q_ready, q_phase))) break;
                     q_phase ^= 1;
@@ -535,7 +563,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                 Ring<kVStages> at;
                 uint32_t it = 0;
                 bool ok = true;
-                while (ok && w.next(p)) {
+                while (ok && w.next(p, bars, cl)) {
                     for (int i = w.i0; ok && i < w.i1; ++i, it += 8) {
                         const int u = w.t.row0(i) + half * 64;
                         const int row = pool_row(w.seq, u, w.t.end);
@@ -562,7 +590,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                 Ring<kPBufs> pb;
                 uint32_t fix_phase = 0, drain_phase = 1, cleaned = 0;   // cleaned: a phase bit per stage
                 bool ok = true;
-                while (ok && w.next(p)) {
+                while (ok && w.next(p, bars, cl)) {
                     const uint32_t bytes = 2u * ((w.t.rows + 7) & ~7) * 128u + kInfo;
 #pragma unroll 1
                     for (int i = w.i0; ok && i < w.i1; ++i, pb.next()) {
@@ -612,7 +640,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         }
     } else {
         regs_acquire<kRegsMath>();
-        Walk w(p, bars);
+        Walk w(bars);
         const int wg = (warp - 4) >> 2, row = (warp & 3) * 32 + lane;   // row of the tile, TMEM lane
         const uint32_t trow = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16);
         const bool first_thread = (threadIdx.x & 127) == 0;
@@ -653,16 +681,16 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                     for (int k = 0; k < 4; ++k) mbar_arrive(B_(bars->sc_empty[(it + wg * 4 + k) % kSStages]));
             };
             const auto has_rows = [&](const Walk &v) { return (warp & 3) * 32 < v.t.rows; };
-            bool more = w.next(p);
+            bool more = w.next(p, bars, cl);
             if (more) load_q(has_rows(w));
             while (ok && more) {
                 const int len = w.seq_len(p);
                 const Sight sight(p, w.seq, min(p.by_H(w.index * kM + row), w.t.t1), len, w.count, lane);
-                const int i0 = w.i0, i1 = w.i1, slot = w.slot(cl), rows = w.t.rows;
+                const int i0 = w.i0, i1 = w.i1, slot = w.slot(), rows = w.t.rows;
                 const Tile tile = w.t;
                 const bool whole = w.whole(), active = has_rows(w);
                 it += 8 * (1 + i1 - i0);   // where the next part's queries are
-                more = w.next(p);          // they go into TMEM after this one's last product
+                more = w.next(p, bars, cl);          // they go into TMEM after this one's last product
                 float m_mine = -INFINITY, l = 0.f;
                 for (int i = i0; ok && i < i1; ++i, ++jb) {
                     const bool mine = (jb & 1) == static_cast<uint32_t>(wg), last = i == i1 - 1;
@@ -796,9 +824,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         } else {
             // ---- rescaling, cleaning and drain: thread = TMEM lane, warpgroup wg has latent columns [256 wg, 256 wg + 256)
             uint32_t jj = 0, it = 0;
-            int4 cut = make_int4(0, 0, 0, 0);
+            uint32_t uncut = (1u << kRounds) - 1;   // rounds whose share leaves no tile unfinished
             bool ok = true, fail = false;
-            while (ok && w.next(p)) {
+            while (ok && w.next(p, bars, cl)) {
                 float l_old = 0.f, l_new = 0.f;   // the sums of the two warpgroups of the score CTA
                 for (int i = w.i0; i < w.i1; ++i, ++jj, it += 8) {
                     const uint32_t pb = jj % kPBufs;
@@ -870,7 +898,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                 const bool whole = w.whole();
                 const float sum = l_old + l_new, inv = 1.f / sum;
                 const int quad = (warp & 3) * 32, rows = min(w.t.rows - quad, 32);   // of the tile's, this warp's
-                const long long part = static_cast<long long>(w.slot(cl)) * kM + quad;
+                const long long part = static_cast<long long>(w.slot()) * kM + quad;
                 const long long r0 = whole ? static_cast<long long>(w.seq) * p.T * p.H + static_cast<long long>(w.index) * kM + quad
                                            : p.all_rows + part;
                 if (rows > 0) {
@@ -918,11 +946,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                 }
                 if (threadIdx.x == 128) {
                     int2 *const tile = p.ws_tile + static_cast<long long>(w.seq) * p.tiles + w.index;
-                    if (w.i0 == 0) tile->x = cl;
-                    if (w.i1 == w.t.n) tile->y = cl;
+                    if (w.i0 == 0) tile->x = w.share;
+                    if (w.i1 == w.t.n) tile->y = w.share;
                     if (w.i0 == 0 && w.i1 < w.t.n) {   // the share that holds the tile's last unit: start(c) < w.pre
-                        const int last = static_cast<int>((w.pre * bars->shares - 1) / bars->total);
-                        cut = make_int4(w.seq * p.T * p.H + w.index * kM, w.t.rows, last, 0);
+                        const int last = static_cast<int>((w.pre * (bars->shares * bars->rounds) - 1) / bars->total);
+                        p.ws_cut[w.round * G + cl] = make_int4(w.seq * p.T * p.H + w.index * kM, w.t.rows, w.share, last);
+                        uncut &= ~(1u << w.round);
                     }
                 }
                 fence_proxy_async_smem();   // the next P's copy follows
@@ -933,7 +962,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                     mbar_arrive_remote(B_(bars->p_free[prev % kPBufs]), 0);
                 }
             }
-            if (threadIdx.x == 128) p.ws_cut[cl] = cut;
+            for (int r = 0; threadIdx.x == 128 && r < p.max_rounds; ++r)
+                if ((uncut >> r) & 1) p.ws_cut[r * G + cl] = make_int4(0, 0, 0, 0);
             if (!ok) *abort_flag = 1;
         }
     }
@@ -957,6 +987,7 @@ struct UpParams {
     const __nv_bfloat16 *gate;
     __nv_bfloat16 *out;
     int *err;
+    int max_rounds, G;
     int B, T, H, tiles, bs, max_blocks;
 };
 
@@ -980,7 +1011,7 @@ struct RowPiece {
 };
 
 // Parts c0, c0 + step, ... of a tile's row r by one warp: the running maximum M (log2 units), the sum of the weights and,
-// 16 latent columns per lane, the weighted sum.  Cluster `first` started the tile; those up to `last` went on with it.
+// 16 latent columns per lane, the weighted sum.  Share `first` started the tile; those up to `last` went on with it.
 __device__ __forceinline__ void join_parts(const UpParams &p, int first, int last, int r, int c0, int step, int lane,
                                            float (&o)[16], float &M, float &sum) {
 #pragma unroll
@@ -1091,7 +1122,7 @@ __global__ void __launch_bounds__(kFewThreads, kW == 8 ? 1 : 2)
     uint64_t *const w_empty = w_full + kW;                                                            // [kW]
     uint64_t *const done = w_full + 2 * kW;
     uint32_t *const tmem_slot = reinterpret_cast<uint32_t *>(w_full + 2 * kW + 1);
-    __shared__ int2 s_tile[kFewRows];   // first and last cluster of each row's tile; {-1, .}: not a token
+    __shared__ int2 s_tile[kFewRows];   // first and last share of each row's tile; {-1, .}: not a token
     __shared__ int s_row[kFewRows];     // the row's place in its tile
     __shared__ float s_m[kFewWarps], s_sum[kFewWarps];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -1240,28 +1271,31 @@ __global__ void __launch_bounds__(kFewThreads, kW == 8 ? 1 : 2)
     if (warp == 0) tmem_dealloc(tmem, 128);
 }
 
-// Many tokens, first: the cut tiles' parts into rows.  Eight CTAs per cluster that left a tile unfinished, a warp per row.
+// Many tokens, first: the cut tiles' parts into rows.  Eight CTAs per cluster, for its shares that left a tile unfinished; a
+// warp per row.
 constexpr int kJoinThreads = 512;
 __global__ void __launch_bounds__(kJoinThreads) attend_join_kernel(const UpParams p) {
     grid_dependency_wait();
     grid_launch_dependents();
-    const int c = blockIdx.x >> 3, lane = threadIdx.x & 31, r = (blockIdx.x & 7) * 16 + (threadIdx.x >> 5);
-    const int4 cut = p.ws_cut[c];
-    if (r >= cut.y) return;
-    float o[16], M, sum;
-    join_parts(p, c, cut.z, r, 0, 1, lane, o, M, sum);
-    const float inv = 1.f / sum;
-    float top = 0.f;
+    const int lane = threadIdx.x & 31, r = (blockIdx.x & 7) * 16 + (threadIdx.x >> 5);
+    for (int round = 0; round < p.max_rounds; ++round) {
+        const int4 cut = p.ws_cut[round * p.G + (blockIdx.x >> 3)];
+        if (r >= cut.y) continue;
+        float o[16], M, sum;
+        join_parts(p, cut.z, cut.w, r, 0, 1, lane, o, M, sum);
+        const float inv = 1.f / sum;
+        float top = 0.f;
 #pragma unroll
-    for (int k = 0; k < 16; ++k) o[k] *= inv, top = fmaxf(top, fabsf(o[k]));
-    const int E = row_exponent(fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1)));   // of 32 columns
-    const float up = row_up(E);
-    uint32_t x[8];
+        for (int k = 0; k < 16; ++k) o[k] *= inv, top = fmaxf(top, fabsf(o[k]));
+        const int E = row_exponent(fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1)));   // of 32 columns
+        const float up = row_up(E);
+        uint32_t x[8];
 #pragma unroll
-    for (int k = 0; k < 8; ++k) x[k] = pack_f16x2(o[2 * k] * up, o[2 * k + 1] * up);
-    const long long row = cut.x + r;
-    st_global_32B(p.ws_rows + row * kR + lane * 16, make_uint4(x[0], x[1], x[2], x[3]), make_uint4(x[4], x[5], x[6], x[7]));
-    if ((lane & 1) == 0) p.ws_exp[row * 16 + (lane >> 1)] = static_cast<uint8_t>(E);
+        for (int k = 0; k < 8; ++k) x[k] = pack_f16x2(o[2 * k] * up, o[2 * k + 1] * up);
+        const long long row = cut.x + r;
+        st_global_32B(p.ws_rows + row * kR + lane * 16, make_uint4(x[0], x[1], x[2], x[3]), make_uint4(x[4], x[5], x[6], x[7]));
+        if ((lane & 1) == 0) p.ws_exp[row * 16 + (lane >> 1)] = static_cast<uint8_t>(E);
+    }
 }
 
 // Many tokens, then: out = gate * (hi + lo) . W_UV[h]^T, 128 tokens of a head at a time.  Persistent: a CTA takes a run of
@@ -1489,20 +1523,21 @@ cudaError_t prepare(int num_sms, int &clusters) {
     return cudaSuccess;
 }
 
-// The workspace: rows, parts, tiles' clusters, clusters' unfinished tiles.
+// The workspace: rows, parts, tiles' shares, shares' unfinished tiles.
 struct Space {
     size_t exp, m, l, tile, cut, end;
-    int tiles;
+    int tiles, rounds;
     Space(long long B, long long T, int H, int num_sms) {
-        const size_t clusters = num_sms / 2 > 0 ? num_sms / 2 : 1, parts = clusters * 2 * kM;
         tiles = static_cast<int>((T * H + kM - 1) / kM);
+        rounds = B > 1 ? std::max(1, std::min(tiles / kRoundTiles, kRounds)) : 1;
+        const size_t shares = static_cast<size_t>(num_sms / 2 > 0 ? num_sms / 2 : 1) * rounds, parts = shares * 2 * kM;
         const size_t rows = static_cast<size_t>(B) * T * H + parts;
         exp = rows * kR * 2;
         m = exp + rows * 16;
         l = m + parts * 4;
         tile = l + parts * 4;
         cut = (tile + static_cast<size_t>(B) * tiles * sizeof(int2) + 15) / 16 * 16;
-        end = cut + clusters * sizeof(int4);
+        end = cut + shares * sizeof(int4);
     }
 };
 
@@ -1544,14 +1579,14 @@ cudaError_t launch_attend_paged(const AttendPagedArgs &a, cudaStream_t s) {
     const long long m = static_cast<long long>(a.B) * a.T;
     const long long all_rows = m * a.H;
     const PairParams pp{a.table, a.lens, a.counts, a.parents, a.ld_table,
-                        ws_rows, ws_exp, ws_m, ws_l, ws_tile, ws_cut, all_rows, a.dev_err, a.B, a.T, a.H, sp.tiles,
+                        ws_rows, ws_exp, ws_m, ws_l, ws_tile, ws_cut, all_rows, a.dev_err, sp.rounds, a.B, a.T, a.H, sp.tiles,
                         a.num_blocks, a.bs, a.max_blocks, a.window, a.sinks, a.scale * kLog2e, Divisor(a.H), Divisor(sp.tiles), Divisor(a.bs)};
     note_launch();
     e = launch_dependent(attend_pair_kernel, dim3(2 * G), kThreads, kSmemPair, s, tm_q, tm_s, tm_v, pp);
     if (e != cudaSuccess) return e;
     const UpParams up{a.lens, a.counts, ws_rows, ws_exp, ws_m, ws_l, ws_tile, ws_cut, all_rows,
-                      static_cast<const __nv_bfloat16 *>(a.gate), static_cast<__nv_bfloat16 *>(a.out), a.dev_err, a.B, a.T,
-                      a.H, sp.tiles, a.bs, a.max_blocks};
+                      static_cast<const __nv_bfloat16 *>(a.gate), static_cast<__nv_bfloat16 *>(a.out), a.dev_err, sp.rounds,
+                      G, a.B, a.T, a.H, sp.tiles, a.bs, a.max_blocks};
     // Up to 32 tokens, and up to 64 of many heads, the join, W_UV and the gate are one kernel of short CTAs (one token of 96
     // heads over 30000 rows takes 28.7 us with it and 48.7 with the two others, 64 tokens of 96 heads 62.8 and 64.1, of 16
     // heads 38.9 and 34.8, 128 tokens of 96 heads 87.5 and 75.2).

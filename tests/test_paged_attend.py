@@ -199,6 +199,20 @@ def test_short_sequences_before_long_ones(env, lens):
     check(env, problem(env, 1, 2, (lens * 400)[:400 if len(lens) > 1 else 1000]))
 
 
+@pytest.mark.parametrize("T,lens", [(24, [20000, 9000, 24000, 6000, 21000, 13000, 700, 12500, 25000]), (40, [9000] * 14)])
+def test_rounds_of_shares(env, T, lens):
+    """Sequences of many tiles whose rows are more than a round's: every cluster has several shares."""
+    d = problem(env, T, 64, lens, gate=False)
+    got = attend(env, d)
+    assert env[1].mla_get_device_error() == 0
+    rng = np.random.default_rng(5)
+    pick = sorted(rng.choice(64, 6, replace=False).tolist())    # heads to compare: the reference takes long
+    some = dict(d, q_abs=d["q_abs"][:, :, pick].contiguous(), w_uv=d["w_uv"][pick].contiguous())
+    for b, c, out, off in reference(env, some):
+        err = (got[b, :c].view(c, 64, D_V)[:, pick].reshape(c, -1).double() - out).abs()
+        assert bool((err <= off).all()), f"sequence {b}: {float((err / off).max()):.3f} of what it may be off by"
+
+
 def test_rising_scores(env):
     """Each token's scores rise along the cache by far more than a softmax keeps, in a different direction per head."""
     torch, _ = env
