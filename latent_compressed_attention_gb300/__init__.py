@@ -729,15 +729,16 @@ def _paged_pool(pool, device):
 
 
 def _block_table(table, B, device):
-    """Checks an int32 [B, max_blocks] table; returns (max_blocks, row stride)."""
-    if not table.is_cuda or table.dtype != _torch().int32:
+    """Checks an int32 [B, max_blocks] table (rows at any stride); returns (max_blocks, row stride)."""
+    if table.dtype != _torch().int32 or not table.is_cuda:
         raise TypeError("block_table must be an int32 CUDA tensor")
     if table.device != device:
         raise ValueError(f"block_table is on {table.device}, expected {device}")
-    if table.dim() != 2 or table.shape[0] != B or (table.shape[1] > 1 and table.stride(1) != 1):
+    shape, stride = table.shape, table.stride()
+    if len(shape) != 2 or shape[0] != B or (shape[1] > 1 and stride[1] != 1):
         raise ValueError(f"block_table must be [{B},max_blocks] with unit inner stride")
-    wide = table.shape[1]
-    ld = table.stride(0) if B > 1 and wide > 0 else wide
+    wide = shape[1]
+    ld = stride[0] if B > 1 and wide > 0 else wide
     if ld < wide:
         raise ValueError("block_table's rows overlap")
     return wide, ld
@@ -751,7 +752,7 @@ def mla_reserve_latent_blocks(lens, counts, T: int, block_table, held, free_bloc
     lens, counts, held: int32 [B]; block_table int32 [B,max_blocks] (rows at any stride); free_blocks int32 [capacity]: a
     stack of free_count[0] (int32 [1]) blocks, its last entry on top.  Sequences that hold more than they need give blocks
     up, which serve the others before the stack does; held becomes what each one needs.  T is at least the largest count;
-    with T = 0 only the blocks are moved.  If something does not fit or is out of range, nothing changes, every slot is -1
+    with T = 0 only the blocks are moved and None is returned.  If something does not fit or is out of range, nothing changes, every slot is -1
     and the device error word is set (mla_get_device_error).
     """
     torch = _torch()
@@ -765,13 +766,13 @@ def mla_reserve_latent_blocks(lens, counts, T: int, block_table, held, free_bloc
     if T < 0 or free_blocks.dim() != 1:
         raise ValueError("T must not be negative and free_blocks must be [capacity]")
     with _on(stream, dev):
-        if slots is None:
-            slots = torch.empty((B, T), dtype=torch.int32, device=dev)
-        else:
+        if slots is not None:
             _check(slots, "slots", torch.int32, dev, (B, T))
+        elif T > 0:
+            slots = torch.empty((B, T), dtype=torch.int32, device=dev)
         rc = library().mla_reserve_latent_blocks(lens.data_ptr(), counts.data_ptr(), block_table.data_ptr(), ld,
                                                  held.data_ptr(), free_blocks.data_ptr(), free_count.data_ptr(),
-                                                 slots.data_ptr(), B, T, wide, free_blocks.shape[0],
+                                                 None if slots is None else slots.data_ptr(), B, T, wide, free_blocks.shape[0],
                                                  _count(block_size, "block_size"),
                                                  _raw_stream(stream, dev))
     if rc != 0:
