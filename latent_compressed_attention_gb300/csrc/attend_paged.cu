@@ -1101,16 +1101,17 @@ __device__ __forceinline__ bool is_token(const UpParams &p, long long m, int &b,
     return b < p.B && t < tokens(p, b, len, false);
 }
 
-// Few tokens: one CTA per (head, 32 tokens).  Rows into two swizzled tiles (one of each part), from ws_rows or joined from
-// parts, as many warps to a row as there are; times W_UV[h]^T in eight slabs of 64 latent columns; the gate.  All slabs are
-// loaded before the pair kernel ends where every CTA has an SM to itself (kW = 8); otherwise two CTAs share one and two
-// stages take the slabs in turn.
+// Few tokens: one CTA per (head, 32 tokens).  Rows into swizzled slabs, hi over lo, from ws_rows or joined from parts, as
+// many warps to a row as there are.  W_UV[h] is the M side and the rows, hi and lo, the N = 64 of one product: 32
+// instructions of 53 cycles where the rows as M = 128 would take 64 of 64, and outputs that lie side by side in a warp.  All
+// of W_UV's eight slabs of 64 latent columns are loaded before the pair kernel ends where every CTA has an SM to itself
+// (kW = 8); otherwise two CTAs share one and two stages take the slabs in turn.
 constexpr int kFewRows = 32, kFewThreads = 256, kFewWarps = kFewThreads / 32;
-constexpr uint32_t kFewSlab = kFewRows * 128;             // [32 rows x 64 latent columns]
-constexpr uint32_t kFewW = 2 * 8 * kFewSlab;              // an M = 128 read of the last slab ends inside the W_UV stages
+constexpr uint32_t kFewSlab = 2 * kFewRows * 128;         // [32 rows x 64 latent columns] hi, then lo
+constexpr uint32_t kFewW = 8 * kFewSlab;
 constexpr uint32_t few_bars(int kW) { return kFewW + kW * kSlab; }
 constexpr uint32_t few_smem(int kW) { return few_bars(kW) + 192 + 1024; }
-static_assert(kFewWarps * kR * 4 <= 16 * kFewSlab, "the warps' sums fit where the tiles go");
+static_assert(kFewWarps * kR * 4 <= 8 * kFewSlab, "the warps' sums fit where the rows go");
 
 template <int kW>
 __global__ void __launch_bounds__(kFewThreads, kW == 8 ? 1 : 2)
@@ -1135,7 +1136,7 @@ __global__ void __launch_bounds__(kFewThreads, kW == 8 ? 1 : 2)
         fence_mbar_init();
     }
     if (warp == 0) {
-        tmem_alloc(smem_u32(tmem_slot), 128);
+        tmem_alloc(smem_u32(tmem_slot), 64);
         tmem_relinquish();
     }
     tc_fence_before();
@@ -1175,7 +1176,7 @@ __global__ void __launch_bounds__(kFewThreads, kW == 8 ? 1 : 2)
             for (int q = 0; q < 4; ++q) hi[q] = split_bf16x2(o[8 * k + 2 * q] * mul, o[8 * k + 2 * q + 1] * mul, lo[q]);
             const uint32_t at = slab + sw128_offset(i, (lane & 3) * 2 + k);
             st_shared_v4(at, hi[0], hi[1], hi[2], hi[3]);
-            st_shared_v4(at + 8 * kFewSlab, lo[0], lo[1], lo[2], lo[3]);
+            st_shared_v4(at + kFewSlab / 2, lo[0], lo[1], lo[2], lo[3]);
         }
     };
     for (int i0 = 0; i0 < rows; i0 += kFewWarps / per_row) {
@@ -1229,8 +1230,8 @@ __global__ void __launch_bounds__(kFewThreads, kW == 8 ? 1 : 2)
     tc_fence_before();
     __syncthreads();
     if (threadIdx.x == 0) {
-        const uint32_t idesc = make_idesc_bf16(128, kDV, 0, 0);
-        const uint64_t a0 = make_smem_desc(base, 16, 1024), b0 = make_smem_desc(base + kFewW, 16, 1024);
+        const uint32_t idesc = make_idesc_bf16(kDV, 2 * kFewRows, 0, 0);
+        const uint64_t rows0 = make_smem_desc(base, 16, 1024), w0 = make_smem_desc(base + kFewW, 16, 1024);
         bool ok = true;
         int loaded = kW;
 #pragma unroll 1
@@ -1239,11 +1240,8 @@ __global__ void __launch_bounds__(kFewThreads, kW == 8 ? 1 : 2)
             if (!(ok = mbar_wait(smem_u32(w_full + st), (k / kW) & 1, p.err))) break;
             tc_fence_after();
 #pragma unroll
-            for (int kk = 0; kk < 4; ++kk) {
-                const uint64_t a = desc_add(a0, k * kFewSlab + kk * 32), bd = desc_add(b0, st * kSlab + kk * 32);
-                umma_bf16(tmem, a, bd, idesc, (k | kk) != 0);
-                umma_bf16(tmem, desc_add(a, 8 * kFewSlab), bd, idesc, 1);
-            }
+            for (int kk = 0; kk < 4; ++kk)
+                umma_bf16(tmem, desc_add(w0, st * kSlab + kk * 32), desc_add(rows0, k * kFewSlab + kk * 32), idesc, (k | kk) != 0);
             if (k + kW < 8) {   // the stage is refilled once its products completed
                 umma_commit(smem_u32(w_empty + st));
                 if (!(ok = mbar_wait(smem_u32(w_empty + st), (k / kW) & 1, p.err))) break;
@@ -1257,18 +1255,31 @@ __global__ void __launch_bounds__(kFewThreads, kW == 8 ? 1 : 2)
                 mbar_wait(smem_u32(w_full + k % kW), (k / kW) & 1, p.err, nullptr, kLandNs);
     }
     __syncwarp();
-    if (warp == 0) {
-        const bool valid = s_tile[lane].x >= 0;
-        const long long off = ((m0 + lane) * p.H + h) * kDV;
-        Gate gate;
-        if (p.gate && valid) gate.load(p.gate + off);
+    if (warp < kDV / 32) {   // thread = output column, TMEM column = token
         const bool good = mbar_wait(smem_u32(done), 0, p.err);
         tc_fence_after();
-        if (__all_sync(0xffffffffu, good)) store_out(tmem, p.gate ? &gate : nullptr, p.out + off, valid);
+        const uint32_t lanes = tmem + (static_cast<uint32_t>(warp * 32) << 16);
+#pragma unroll 1
+        for (int i0 = 0; __all_sync(0xffffffffu, good) && i0 < rows; i0 += 8) {
+            float hi[8], lo[8], g[8];
+            tmem_ld8(lanes + i0, hi);
+            tmem_ld8(lanes + kFewRows + i0, lo);
+            const long long off = ((m0 + i0) * p.H + h) * kDV + threadIdx.x, step = static_cast<long long>(p.H) * kDV;
+#pragma unroll
+            for (int k = 0; k < 8; ++k)
+                g[k] = p.gate && i0 + k < rows && s_tile[i0 + k].x >= 0 ? __bfloat162float(p.gate[off + k * step]) : 0.f;
+            tmem_wait_ld();
+#pragma unroll
+            for (int k = 0; k < 8; ++k) {
+                float y = hi[k] + lo[k];
+                if (p.gate) y *= __fdividef(1.f, 1.f + fast_exp2(-g[k] * kLog2e));
+                if (i0 + k < rows && s_tile[i0 + k].x >= 0) p.out[off + k * step] = __float2bfloat16(y);
+            }
+        }
     }
     tc_fence_before();
     __syncthreads();
-    if (warp == 0) tmem_dealloc(tmem, 128);
+    if (warp == 0) tmem_dealloc(tmem, 64);
 }
 
 // Many tokens, first: the cut tiles' parts into rows.  Eight CTAs per cluster, for its shares that left a tile unfinished; a
