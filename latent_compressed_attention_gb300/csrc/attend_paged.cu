@@ -1062,7 +1062,7 @@ struct Gate {
     uint4 v[16];
     __device__ __forceinline__ void load(const __nv_bfloat16 *gate) {
 #pragma unroll
-        for (int k = 0; k < 8; ++k) ld_global_32B(gate + 16 * k, v[2 * k], v[2 * k + 1]);
+        for (int k = 0; k < 16; ++k) v[k] = __ldg(reinterpret_cast<const uint4 *>(gate) + k);
     }
 };
 __device__ __forceinline__ void store_out(uint32_t taddr, const Gate *gate, __nv_bfloat16 *out, bool token) {
@@ -1085,12 +1085,10 @@ __device__ __forceinline__ void store_out(uint32_t taddr, const Gate *gate, __nv
             }
         }
 #pragma unroll
-        for (int q = 0; q < 2; ++q) {
-            uint32_t x[8];
-#pragma unroll
-            for (int k = 0; k < 8; ++k) x[k] = pack_bf16x2(o[16 * q + 2 * k], o[16 * q + 2 * k + 1]);
-            st_global_32B(out + c * 32 + 16 * q, make_uint4(x[0], x[1], x[2], x[3]), make_uint4(x[4], x[5], x[6], x[7]));
-        }
+        for (int q = 0; q < 4; ++q)
+            reinterpret_cast<uint4 *>(out)[c * 4 + q] =
+                make_uint4(pack_bf16x2(o[8 * q], o[8 * q + 1]), pack_bf16x2(o[8 * q + 2], o[8 * q + 3]),
+                           pack_bf16x2(o[8 * q + 4], o[8 * q + 5]), pack_bf16x2(o[8 * q + 6], o[8 * q + 7]));
     }
 }
 
@@ -1548,7 +1546,7 @@ struct Space {
         l = m + parts * 4;
         tile = l + parts * 4;
         cut = (tile + static_cast<size_t>(B) * tiles * sizeof(int2) + 15) / 16 * 16;
-        end = cut + shares * sizeof(int4);
+        end = cut + shares * sizeof(int4) + 16;   // the base goes up to 32 bytes
     }
 };
 
@@ -1581,7 +1579,7 @@ cudaError_t launch_attend_paged(const AttendPagedArgs &a, cudaStream_t s) {
             encode_map(&tm_w, a.w_uv, 2, dims_w, strides_w, box_w) != CUDA_SUCCESS)
             return cudaErrorInvalidValue;
     }
-    char *const ws = static_cast<char *>(a.workspace);
+    char *const ws = reinterpret_cast<char *>((reinterpret_cast<uintptr_t>(a.workspace) + 31) & ~static_cast<uintptr_t>(31));
     auto *const ws_rows = reinterpret_cast<__half *>(ws);
     auto *const ws_exp = reinterpret_cast<uint8_t *>(ws + sp.exp);
     float *const ws_m = reinterpret_cast<float *>(ws + sp.m), *const ws_l = reinterpret_cast<float *>(ws + sp.l);

@@ -333,6 +333,41 @@ def test_repeatable_and_shared_workspace(env):
     assert lca.mla_get_device_error() == 0
 
 
+@pytest.mark.parametrize("B,T", [(2, 3), (2, 40)])
+def test_least_alignment(env, B, T):
+    """Every tensor at the alignment that the call asks for and no more: 16 bytes, whole numbers 4."""
+    torch, lca = env
+
+    def moved(t, by):
+        if t is None:
+            return None
+        flat = torch.empty(t.numel() + 64, dtype=t.dtype, device="cuda")
+        at = next(i for i in range(64) if (flat.data_ptr() + i * t.element_size()) % 64 == by)
+        return flat[at:at + t.numel()].view(t.shape).copy_(t)
+
+    d = problem(env, T, 16, [100, 300][:B], counts=[T, T - 1], tree="mixed", window=50, sinks=3)
+    want = attend(env, d)
+    for key in d:
+        if isinstance(d[key], torch.Tensor):
+            d[key] = moved(d[key], 16 if d[key].dtype == torch.bfloat16 else 4)
+    ws = torch.empty(lca.mla_latent_attend_paged_workspace_size(B, T, 16, R) + 64, dtype=torch.uint8, device="cuda")
+    out = moved(torch.zeros_like(want), 16)
+    got = attend(env, d, out=out, workspace=ws[next(i for i in range(64) if (ws.data_ptr() + i) % 64 == 16):])
+    assert got.data_ptr() % 32 == 16 and torch.equal(got, want)
+
+
+def test_queries_that_are_no_tokens(env):
+    """Whatever the queries behind a sequence's last token hold, which share its last tile, has no effect."""
+    torch, _ = env
+    d = problem(env, 9, 20, [300, 70, 10], counts=[4, 9, 0], window=90, sinks=2)
+    want = attend(env, d)
+    for bad in (float("nan"), float("inf"), 3e38):
+        for b, c in enumerate((4, 9, 0)):
+            d["q_abs"][b, c:] = bad
+        assert torch.equal(attend(env, d), want)
+    assert env[1].mla_get_device_error() == 0
+
+
 def test_views(env):
     """Tables and pools that are views, a pool of one block, a call without tokens or sequences."""
     torch, lca = env
