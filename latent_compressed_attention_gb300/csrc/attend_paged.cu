@@ -53,7 +53,7 @@ constexpr float kLog2e = 1.4426950408889634f;
 // A stale maximum is kept until the new one exceeds it by this (log2 units): p <= 2^16, far inside fp32's range.
 constexpr float kRescaleLog2 = 16.0f;
 // Units that starting a tile counts for in the shares: its queries' load, its accumulator's drain, the pipeline's refill.
-constexpr int kStart = 3;
+constexpr int kStart = 2;
 // Rounds of shares: as many as bring the rows of a round's sequences down to this, but no more than one for every 6 tiles of a
 // sequence, each of them of at least 16 units per cluster.  (16 sequences of 64 drafts of 96 heads over up to 16000 rows, 48
 // tiles each: 1164 us in one round, 1087 in four; 64 sequences of 4, 3 tiles each: 210 and 222.)
