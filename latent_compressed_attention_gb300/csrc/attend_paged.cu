@@ -25,12 +25,22 @@
 // row's scores with any query: then the value CTA's math warps replace what is not finite in the unit by zeros before the
 // product, and a token that does see it gets its NaN through the sum of its weights.
 //
-// A cluster leaves o_lat / l of its part of a tile, with the maxima and the sums of weights where the tile was cut between
-// clusters (at most two such parts per cluster).  The values go as f16 with an exponent for each 32 of a row: off by
-// 2^-12, a sixteenth of what rounding the output costs, in half of fp32's bytes, which is what a part's end takes (an SM
-// stores 27 bytes a cycle: 256 KB of fp32 took as long as four units).  Up to 64 tokens one kernel joins the parts, applies
-// W_UV^T on the tensor cores and the gate; above, a kernel joins them and a product per head follows.  Both take the
-// values to the product as two bf16 parts, which hold them exactly.
+// A part (what a share has of a tile) leaves o_lat / l, and where the tile was cut between shares its maxima and sums of
+// weights, at most twice per share.  The values go as f16 with an exponent for each 32 of a row: off by 2^-12, a sixteenth
+// of what rounding the output costs, in half of fp32's bytes, which is what a part's end takes (an SM stores 27 bytes a
+// cycle: 256 KB of fp32 took as long as four units).  Up to 32 tokens, and up to 64 of many heads, one kernel joins the
+// parts, applies W_UV^T on the tensor cores and the gate; above, one joins them and a product per head follows.  Both take
+// the values to the product as two bf16 parts, which hold them exactly.  So three roundings to bf16 or f16 are left: the
+// softmax weights' (2^-8 of each, as in the prefill and the other decodes; two parts would double the value CTA's products),
+// this one and the output's.
+//
+// What bounds it.  A unit's products are 2,048 tensor cycles on either CTA.  The score CTA moves 320 KB through shared memory
+// meanwhile (rows written by TMA and read, P written and copied) and the value CTA 350 KB (P read for either latent half):
+// 2,500 to 2,750 cycles at 128 bytes a cycle.  Long calls take 2,520 cycles per unit: 8 chunks of 512 tokens of 96 heads under
+// a window of 4096 take 2.1 ms, 1.5 PFLOP/s.  With one token of 96 heads per sequence HBM is the bound, 1.5 us per unit of all
+// clusters; 64 of them over 1.08 million rows take 215 us, 5.2 TB/s.  Besides, a part costs 1.2 to 3 us (drain, refill), and
+// a call 19 to 31 us before its first unit and after its last one: instructions come from L2 or DRAM then, a cold unit's
+// softmax takes twice as long.
 #include <cuda.h>
 #include <cudaTypedefs.h>
 
@@ -439,7 +449,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         const int n = total < G ? static_cast<int>(total) : G;
         int rounds = 1;
         if (p.max_rounds > 1) {
-            const long long bytes = total * (kUnit * kR * 2) / p.tiles, units = total / (n * kRoundMin);
+            const long long bytes = total * (kUnit * kR * 2) / p.tiles, units = total / (max(n, 1) * kRoundMin);
             rounds = max(1, static_cast<int>(min(min((bytes + kRoundBytes - 1) / kRoundBytes, units),
                                                  static_cast<long long>(p.max_rounds))));
         }
