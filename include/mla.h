@@ -408,9 +408,9 @@ MLA_API int mla_append_latent_paged(const void *c, long long ld_c, void *pool, l
  *                in flight
  * A sequence with a length, count or lens + counts outside [0, T] and [0, max_blocks * block_size] is skipped, rows of a
  * block outside the pool count as zeros, and a parent outside [-1, t) as -1; each is reported as MLA_ERR_DEVICE_BOUNDS.
- * Precision: products of bf16 values in fp32; softmax statistics, sums and the join of split rows in fp32; the weighted
- * latent goes to the product with W_UV as two bf16 parts (2^-16 of each value).  Rounded to bf16 are the softmax weights
- * and out.
+ * Precision: products of bf16 values in fp32; softmax statistics, sums and the join of split rows in fp32.  Rounded to
+ * bf16 are the softmax weights and out.  The weighted latent is kept as f16 with an exponent for each 32 values (2^-11
+ * of each part, once more where split rows are joined) and goes to the product with W_UV as two bf16 parts (2^-16).
  * Supported: r = 512, d_v = 128, 1 <= H <= 128, block_size a multiple of 64.
  * Returns MLA_OK or a negative mla_status_t; nothing is launched on error.
  */

@@ -26,13 +26,13 @@
 // product, and a token that does see it gets its NaN through the sum of its weights.
 //
 // A part (what a share has of a tile) leaves o_lat / l, and where the tile was cut between shares its maxima and sums of
-// weights, at most twice per share.  The values go as f16 with an exponent for each 32 of a row: off by 2^-12, a sixteenth
-// of what rounding the output costs, in half of fp32's bytes, which is what a part's end takes (an SM stores 27 bytes a
-// cycle: 256 KB of fp32 took as long as four units).  Up to 32 tokens, and up to 64 of many heads, one kernel joins the
+// weights, at most twice per share.  The values go as f16 with an exponent for each 32 of a row: off by 2^-11, an eighth of
+// what rounding the output costs, in half of fp32's bytes, which is what a part's end takes (an SM stores 27 bytes a cycle:
+// 256 KB of fp32 took as long as four units).  Up to 32 tokens, and up to 64 of many heads, one kernel joins the
 // parts, applies W_UV^T on the tensor cores and the gate; above, one joins them and a product per head follows.  Both take
-// the values to the product as two bf16 parts, which hold them exactly.  So three roundings to bf16 or f16 are left: the
-// softmax weights' (2^-8 of each, as in the prefill and the other decodes; two parts would double the value CTA's products),
-// this one and the output's.
+// the values to the product as two bf16 parts, off by 2^-16 at most.  So the roundings to 16 bits that count are the softmax
+// weights' (2^-8 of each, as in the prefill and the other decodes; two parts would double the value CTA's products), that of
+// a part (2^-11, and 2^-11 again where joined rows go through memory) and the output's.
 //
 // What bounds it.  A unit's products are 2,048 tensor cycles on either CTA.  The score CTA moves 320 KB through shared memory
 // meanwhile (rows written by TMA and read, P written and copied) and the value CTA 350 KB (P read for either latent half):
