@@ -1067,41 +1067,6 @@ __device__ __forceinline__ void join_parts(const UpParams &p, int first, int las
     }
 }
 
-// The gate logits of a token's head, and its 128 output columns from TMEM with them.
-struct Gate {
-    uint4 v[16];
-    __device__ __forceinline__ void load(const __nv_bfloat16 *gate) {
-#pragma unroll
-        for (int k = 0; k < 16; ++k) v[k] = __ldg(reinterpret_cast<const uint4 *>(gate) + k);
-    }
-};
-__device__ __forceinline__ void store_out(uint32_t taddr, const Gate *gate, __nv_bfloat16 *out, bool token) {
-#pragma unroll
-    for (int c = 0; c < 4; ++c) {
-        float o[32];
-        tmem_ld32(taddr + c * 32, o);
-        tmem_wait_ld();
-        if (!token) continue;
-        if (gate) {
-#pragma unroll
-            for (int q = 0; q < 4; ++q) {
-                const uint4 g = gate->v[c * 4 + q];
-                const uint32_t gw[4] = {g.x, g.y, g.z, g.w};
-#pragma unroll
-                for (int k = 0; k < 4; ++k) {
-                    o[8 * q + 2 * k] *= __fdividef(1.f, 1.f + fast_exp2(-__uint_as_float(gw[k] << 16) * kLog2e));
-                    o[8 * q + 2 * k + 1] *= __fdividef(1.f, 1.f + fast_exp2(-__uint_as_float(gw[k] & 0xFFFF0000u) * kLog2e));
-                }
-            }
-        }
-#pragma unroll
-        for (int q = 0; q < 4; ++q)
-            reinterpret_cast<uint4 *>(out)[c * 4 + q] =
-                make_uint4(pack_bf16x2(o[8 * q], o[8 * q + 1]), pack_bf16x2(o[8 * q + 2], o[8 * q + 3]),
-                           pack_bf16x2(o[8 * q + 4], o[8 * q + 5]), pack_bf16x2(o[8 * q + 6], o[8 * q + 7]));
-    }
-}
-
 // The token of [B, T] numbered m: whether it is one of its sequence's new ones.
 __device__ __forceinline__ bool is_token(const UpParams &p, long long m, int &b, int &t) {
     b = static_cast<int>(m / p.T), t = static_cast<int>(m - static_cast<long long>(b) * p.T);
@@ -1333,18 +1298,23 @@ __global__ void __launch_bounds__(kJoinThreads) attend_join_kernel(const UpParam
 
 // Many tokens, then: out = gate * (hi + lo) . W_UV[h]^T, 128 tokens of a head at a time.  Persistent: a CTA takes a run of
 // items, the blocks of one head after the other, with W_UV[h] in shared memory while the head stays.  A stage takes 64
-// latent columns of f16 rows, which eight warps (two threads to a row) turn into hi in its place and lo beside it; two
-// accumulators, so that four more warps store one item while the next one's products run.
+// latent columns of f16 rows; two warpgroups (thread = row) turn every other one into hi and lo in TMEM, the A operands of
+// the products, so that shared memory has room for four loads in flight.  Two accumulators: four more warps gate and store
+// one item while the next one's products run.
+// 393,216 rows (8 x 512 tokens of 96 heads, 516 MB with W_UV and out) take 110 us, 4.7 TB/s, gated (617 MB) 137; with hi
+// and lo in shared memory, three stages and every lane loading and storing a row of its own 153 and 181.
 constexpr int kUpThreads = 448;   // warps 0 TMA, 1 MMA, 2-9 split, 10-13 store
-constexpr int kUpStages = 3;
-constexpr uint32_t kUpA = 8 * kSlab, kUpStage = 2 * kSlab;
-constexpr uint32_t kUpBars = kUpA + kUpStages * kUpStage;
+constexpr int kUpStages = 4;   // of the loads' ring in shared memory and of the split ones' in TMEM: two turns per item
+constexpr uint32_t kUpA = 8 * kSlab;
+constexpr uint32_t kUpOut = kUpA + kUpStages * kSlab;   // [128 tokens x 128] bf16
+constexpr uint32_t kUpBars = kUpOut + kM * kDV * 2;
 struct UpBars {
-    uint64_t w_full[8], w_empty[8], full[kUpStages], split[kUpStages], empty[kUpStages], acc_full[2], acc_empty[2];
+    uint64_t w_full[8], w_empty[8], full[kUpStages], empty[kUpStages], split[kUpStages], done[kUpStages], acc_full[2], acc_empty[2];
     uint32_t tmem_base;
 };
-constexpr uint32_t kUpSmem = kUpBars + 256 + 1024;
-static_assert(sizeof(UpBars) <= 256 && kUpSmem <= 232448, "shared memory");
+constexpr uint32_t kUpSmem = kUpBars + 384 + 1024;
+static_assert(sizeof(UpBars) <= 384 && kUpSmem <= 232448, "shared memory");
+constexpr uint32_t kUpSplit = 256;   // TMEM: two accumulators of 128 columns, then stages of 32 columns of hi and 32 of lo
 
 __global__ void __launch_bounds__(kUpThreads, 1)
     attend_up_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ CUtensorMap tm_w, const UpParams p) {
@@ -1363,8 +1333,9 @@ __global__ void __launch_bounds__(kUpThreads, 1)
         for (int i = 0; i < 8; ++i) mbar_init(B_(bars->w_full[i]), 1), mbar_init(B_(bars->w_empty[i]), 1);
         for (int i = 0; i < kUpStages; ++i) {
             mbar_init(B_(bars->full[i]), 1);
-            mbar_init(B_(bars->split[i]), 256);
-            mbar_init(B_(bars->empty[i]), 1);
+            mbar_init(B_(bars->empty[i]), 128);
+            mbar_init(B_(bars->split[i]), 128);
+            mbar_init(B_(bars->done[i]), 1);
         }
         for (int i = 0; i < 2; ++i) {
             mbar_init(B_(bars->acc_full[i]), 1);
@@ -1373,7 +1344,7 @@ __global__ void __launch_bounds__(kUpThreads, 1)
         fence_mbar_init();
     }
     if (warp == 1) {
-        tmem_alloc(smem_u32(&bars->tmem_base), 256);
+        tmem_alloc(smem_u32(&bars->tmem_base), 512);
         tmem_relinquish();
     }
     tc_fence_before();
@@ -1408,7 +1379,7 @@ __global__ void __launch_bounds__(kUpThreads, 1)
                 if (!(ok = wait(bars->empty[at.st], at.phase ^ 1))) break;
                 if (lead) {
                     mbar_arrive_expect_tx(B_(bars->full[at.st]), kSlab);
-                    tma_load_3d(base + kUpA + at.st * kUpStage, &tm_a, B_(bars->full[at.st]), k * 64, h, m0);
+                    tma_load_3d(base + kUpA + at.st * kSlab, &tm_a, B_(bars->full[at.st]), k * 64, h, m0);
                 }
             }
             w_phase ^= new_head;
@@ -1421,7 +1392,7 @@ __global__ void __launch_bounds__(kUpThreads, 1)
     } else if (warp == 1) {
         const bool lead = elect_one();
         const uint32_t idesc = make_idesc_bf16(128, kDV, 0, 0);
-        const uint64_t w0 = make_smem_desc(base, 16, 1024), a0 = make_smem_desc(base + kUpA, 16, 1024);
+        const uint64_t w0 = make_smem_desc(base, 16, 1024);
         Ring<kUpStages> at;
         Ring<2> acc;
         uint32_t w_phase = 1;   // of the head that is there
@@ -1439,13 +1410,14 @@ __global__ void __launch_bounds__(kUpThreads, 1)
                 if (!(ok = wait(bars->w_full[k], w_phase)) || !(ok = wait(bars->split[at.st], at.phase))) break;
                 tc_fence_after();
                 if (lead) {
-                    const uint64_t a = desc_add(a0, at.st * kUpStage), w = desc_add(w0, k * kSlab);
+                    const uint32_t a = tmem + kUpSplit + at.st * 64;
+                    const uint64_t w = desc_add(w0, k * kSlab);
 #pragma unroll
                     for (int kk = 0; kk < 4; ++kk) {
-                        umma_bf16(d, desc_add(a, kk * 32), desc_add(w, kk * 32), idesc, (k | kk) != 0);
-                        umma_bf16(d, desc_add(a, kSlab + kk * 32), desc_add(w, kk * 32), idesc, 1);
+                        umma_bf16_tmem_a(d, a + kk * 8, desc_add(w, kk * 32), idesc, (k | kk) != 0);
+                        umma_bf16_tmem_a(d, a + 32 + kk * 8, desc_add(w, kk * 32), idesc, 1);
                     }
-                    umma_commit(B_(bars->empty[at.st]));
+                    umma_commit(B_(bars->done[at.st]));
                     if (last) umma_commit(B_(bars->w_empty[k]));
                 }
             }
@@ -1453,64 +1425,127 @@ __global__ void __launch_bounds__(kUpThreads, 1)
         }
     } else if (warp < 10) {
         grid_dependency_wait();
-        const int r = ((warp - 2) & 3) * 32 + lane, half = (warp - 2) >> 2;   // of the slab's columns
+        const int r = (warp & 3) * 32 + lane, group = (warp - 2) >> 2;   // every other slab
+        const uint32_t to = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16) + kUpSplit;
         const auto exponents = [&](int i) {
             const int h = i / blocks;
             const long long m = static_cast<long long>(i - h * blocks) * kM + r;
             return i < i1 && m < m_all ? __ldg(reinterpret_cast<const uint4 *>(p.ws_exp) + m * p.H + h) : uint4();
         };
-        Ring<kUpStages> at;
         uint4 next = exponents(i0);
         bool ok = true;
         for (int i = i0; ok && i < i1; ++i) {
             const uint4 E = next;
             next = exponents(i + 1);
 #pragma unroll 1
-            for (int k = 0; k < 8; ++k, at.next()) {
-                if (!(ok = wait(bars->full[at.st], at.phase))) break;
-                const uint32_t slab = base + kUpA + at.st * kUpStage;
-                const uint32_t e = (k < 4 ? k < 2 ? E.x : E.y : k < 6 ? E.z : E.w) >> ((k & 1) * 16 + half * 8);
-                const float down = row_down(max(static_cast<int>(e & 0xFF), 20));   // no token's row may hold anything
+            for (int k = group; k < 8; k += 2) {
+                const int st = k & 3, phase = k >> 2;
+                if (!(ok = wait(bars->full[st], phase))) break;
+                const uint32_t slab = base + kUpA + st * kSlab;
+                const uint32_t e = (k < 4 ? k < 2 ? E.x : E.y : k < 6 ? E.z : E.w) >> (group * 16);
+                float hi[32], lo[32];
 #pragma unroll
-                for (int c = 0; c < 4; ++c) {
-                    const uint32_t a = slab + sw128_offset(r, half * 4 + c);
-                    const uint4 v = ld_shared_v4(a);
-                    const float2 x0 = row_values(v.x, down), x1 = row_values(v.y, down), x2 = row_values(v.z, down),
-                                 x3 = row_values(v.w, down);
-                    uint32_t lo[4];
-                    const uint32_t h0 = split_bf16x2(x0.x, x0.y, lo[0]), h1 = split_bf16x2(x1.x, x1.y, lo[1]),
-                                   h2 = split_bf16x2(x2.x, x2.y, lo[2]), h3 = split_bf16x2(x3.x, x3.y, lo[3]);
-                    st_shared_v4(a, h0, h1, h2, h3);
-                    st_shared_v4(a + kSlab, lo[0], lo[1], lo[2], lo[3]);
+                for (int c = 0; c < 8; ++c) {
+                    // (no token's row may hold anything)
+                    const float down = row_down(max(static_cast<int>(e >> (c < 4 ? 0 : 8) & 0xFF), 20));
+                    const uint4 v = ld_shared_v4(slab + sw128_offset(r, c));
+                    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+                    for (int q = 0; q < 4; ++q) {
+                        const float2 x = row_values(w[q], down);
+                        uint32_t rest;
+                        hi[4 * c + q] = __uint_as_float(split_bf16x2(x.x, x.y, rest));
+                        lo[4 * c + q] = __uint_as_float(rest);
+                    }
                 }
-                fence_proxy_async_smem();
-                mbar_arrive(B_(bars->split[at.st]));
+                fence_proxy_async_smem();   // TMA writes there again
+                mbar_arrive(B_(bars->empty[st]));
+                if (!(ok = wait(bars->done[st], phase ^ 1))) break;
+                tc_fence_after();
+                tmem_st32(to + st * 64, hi);
+                tmem_st32(to + st * 64 + 32, lo);
+                tmem_wait_st();
+                tc_fence_before();
+                mbar_arrive(B_(bars->split[st]));
             }
         }
     } else {
         grid_dependency_wait();
         grid_launch_dependents();
-        const int r = (warp & 3) * 32 + lane;
-        const uint32_t row = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16);
+        // A lane has a row of the accumulator, but memory wants a row from 16 lanes: gates come and outputs go through shared
+        // memory, 16 bytes c of row q at c ^ (q & 7), each warp for its own 32 rows.
+        const int w0 = (warp & 3) * 32;
+        const uint32_t row = tmem + (static_cast<uint32_t>(w0) << 16), stage = base + kUpOut + w0 * 256;
+        const auto cell = [&](int q, int c) { return stage + q * 256 + ((c ^ (q & 7)) << 4); };
+        uint4 g[16];
+        uint32_t tokens = 0;
+        // which of the item's 32 tokens there are, and their gates
+        const auto ask = [&](int i) {
+            if (i >= i1) return;
+            const int h = i / blocks;
+            const long long m0 = static_cast<long long>(i - h * blocks) * kM + w0;
+            int b, t;
+            tokens = __ballot_sync(0xffffffffu, is_token(p, m0 + lane, b, t));
+            if (!p.gate) return;
+#pragma unroll
+            for (int k = 0; k < 16; ++k) {
+                const int q = 2 * k + (lane >> 4);
+                if ((tokens >> q) & 1)
+                    g[k] = __ldg(reinterpret_cast<const uint4 *>(p.gate + ((m0 + q) * p.H + h) * kDV) + (lane & 15));
+            }
+        };
+        ask(i0);
         Ring<2> acc;
         bool ok = true;
         for (int i = i0; ok && i < i1; ++i, acc.next()) {
             const int h = i / blocks;
-            const long long m = static_cast<long long>(i - h * blocks) * kM + r, off = (m * p.H + h) * kDV;
-            int b, t;
-            const bool token = is_token(p, m, b, t);
-            Gate gate;
-            if (p.gate && token) gate.load(p.gate + off);
+            const long long m0 = static_cast<long long>(i - h * blocks) * kM + w0;
+            const uint32_t here = tokens;
+            if (p.gate) {
+#pragma unroll
+                for (int k = 0; k < 16; ++k)
+                    st_shared_v4(cell(2 * k + (lane >> 4), lane & 15), g[k].x, g[k].y, g[k].z, g[k].w);
+                __syncwarp();
+            }
+            ask(i + 1);
             if (!(ok = wait(bars->acc_full[acc.st], acc.phase))) break;
             tc_fence_after();
-            store_out(row + acc.st * 128, p.gate ? &gate : nullptr, p.out + off, token);
+#pragma unroll 1
+            for (int c = 0; c < 4; ++c) {
+                float o[32];
+                tmem_ld32(row + acc.st * 128 + c * 32, o);
+                tmem_wait_ld();
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    const uint32_t to = cell(lane, c * 4 + k);
+                    if (p.gate) {
+                        const uint4 g = ld_shared_v4(to);
+                        const uint32_t gw[4] = {g.x, g.y, g.z, g.w};
+#pragma unroll
+                        for (int n = 0; n < 4; ++n) {
+                            o[8 * k + 2 * n] *= __fdividef(1.f, 1.f + fast_exp2(-__uint_as_float(gw[n] << 16) * kLog2e));
+                            o[8 * k + 2 * n + 1] *= __fdividef(1.f, 1.f + fast_exp2(-__uint_as_float(gw[n] & 0xFFFF0000u) * kLog2e));
+                        }
+                    }
+                    st_shared_v4(to, pack_bf16x2(o[8 * k], o[8 * k + 1]), pack_bf16x2(o[8 * k + 2], o[8 * k + 3]),
+                                 pack_bf16x2(o[8 * k + 4], o[8 * k + 5]), pack_bf16x2(o[8 * k + 6], o[8 * k + 7]));
+                }
+            }
             tc_fence_before();
             mbar_arrive(B_(bars->acc_empty[acc.st]));
+            __syncwarp();
+#pragma unroll 4
+            for (int k = 0; k < 16; ++k) {
+                const int q = 2 * k + (lane >> 4);
+                if ((here >> q) & 1)
+                    reinterpret_cast<uint4 *>(p.out + ((m0 + q) * p.H + h) * kDV)[lane & 15] = ld_shared_v4(cell(q, lane & 15));
+            }
+            __syncwarp();
         }
     }
     tc_fence_before();
     __syncthreads();
-    if (warp == 1) tmem_dealloc(tmem, 256);
+    if (warp == 1) tmem_dealloc(tmem, 512);
 }
 
 CUresult encode_map(CUtensorMap *m, const void *ptr, int rank, const cuuint64_t *dims, const cuuint64_t *strides,
