@@ -716,18 +716,19 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                         fence_proxy_async_smem();
                         named_bar_sync(2 + wg, 128);
                     } else if (mine) {
-                        // Two passes over S, 32 columns at a time in rolled loops, and one more before them that masks a mixed
-                        // unit's: short code is faster, in a long call (all roles' loops share the instruction caches:
+                        // Two passes over S, 32 columns at a time in rolled loops, the first one another in a mixed unit, where
+                        // it masks S too: short code is faster, in a long call (all roles' loops share the instruction caches:
                         // 8 chunks of 512 under a window take 2.27 ms with the two loops unrolled, 2.16 so) and at a call's
                         // start, when it comes from L2 or DRAM.  The scale multiplies inside the exponent: the largest of
                         // c s is c max(s) for c >= 0, c min(s) otherwise.  A masked unit's scores are multiplied first.
                         const int u0 = tile.row0(i);
                         const uint32_t scol = trow + S_COL + (jb & 1) * 128;
-                        float mul = p.scale_log2;
+                        float mul = p.scale_log2, mx = -INFINITY;
                         bool dirty = false;
                         if (tile.mixed(p, len, u0)) {
                             mul = 1.f;
                             float zeros[4] = {0.f, 0.f, 0.f, 0.f};   // NaN once a score is not finite
+                            float top[4] = {mx, mx, mx, mx};
 #pragma unroll 1
                             for (int c4 = 0; c4 < 4; ++c4) {
                                 float s[32];
@@ -740,29 +741,32 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                                     const float zero = s[k] - s[k];
                                     zeros[k & 3] += zero;
                                     s[k] = (seen >> k) & 1 ? fmaf(s[k], p.scale_log2, zero) : -INFINITY;
+                                    top[k & 3] = fmaxf(top[k & 3], s[k]);
                                 }
                                 tmem_st32(scol + c4 * 32, s);
                             }
+                            mx = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3]));
                             tmem_wait_st();
                             dirty = (zeros[0] + zeros[1]) + (zeros[2] + zeros[3]) != 0.f && row < rows;
-                        }
-                        float mx = -INFINITY, mn = INFINITY;
+                        } else {
+                            float mn = INFINITY;
 #pragma unroll 1
-                        for (int c4 = 0; c4 < 4; ++c4) {
-                            float s[32];
-                            tmem_ld32(scol + c4 * 32, s);
-                            tmem_wait_ld();
-                            if (mul >= 0.f) {
-                                float t[4] = {mx, s[0], s[1], s[2]};
+                            for (int c4 = 0; c4 < 4; ++c4) {
+                                float s[32];
+                                tmem_ld32(scol + c4 * 32, s);
+                                tmem_wait_ld();
+                                if (mul >= 0.f) {
+                                    float t[4] = {mx, s[0], s[1], s[2]};
 #pragma unroll
-                                for (int k = 3; k < 32; ++k) t[k & 3] = fmaxf(t[k & 3], s[k]);
-                                mx = fmaxf(fmaxf(t[0], t[1]), fmaxf(t[2], t[3]));
-                            } else {
+                                    for (int k = 3; k < 32; ++k) t[k & 3] = fmaxf(t[k & 3], s[k]);
+                                    mx = fmaxf(fmaxf(t[0], t[1]), fmaxf(t[2], t[3]));
+                                } else {
 #pragma unroll
-                                for (int k = 0; k < 32; ++k) mn = fminf(mn, s[k]);
+                                    for (int k = 0; k < 32; ++k) mn = fminf(mn, s[k]);
+                                }
                             }
+                            mx = mul * (mul >= 0.f ? mx : mn);
                         }
-                        mx = mul * (mul >= 0.f ? mx : mn);
                         // the running maximum of the unit before, from the other warpgroup
                         if (jb > 0) fail = wait_warp(bars->m_ready[wg ^ 1], ((jb - 1) >> 1) & 1);
                         const float m_old = i == i0 ? -INFINITY : ld_shared_f32(base + S_MAX + (wg ^ 1) * kM * 4 + row * 4);
@@ -1656,8 +1660,8 @@ cudaError_t launch_attend_paged(const AttendPagedArgs &a, cudaStream_t s) {
                       static_cast<const __nv_bfloat16 *>(a.gate), static_cast<__nv_bfloat16 *>(a.out), a.dev_err, sp.rounds,
                       G, a.B, a.T, a.H, sp.tiles, a.bs, a.max_blocks};
     // Up to 32 tokens, and up to 64 of many heads, the join, W_UV and the gate are one kernel of short CTAs (one token of 96
-    // heads over 30000 rows takes 28.7 us with it and 48.7 with the two others, 64 tokens of 96 heads 62.8 and 64.1, of 16
-    // heads 38.9 and 34.8, 128 tokens of 96 heads 87.5 and 75.2).
+    // heads over 30000 rows takes 28.7 us with it and 48.7 with the two others, 32 tokens of 96 heads 87 and 91, 64 tokens of
+    // 64 heads 84 and 88, of 96 heads 91 either way, of 16 heads 38.9 and 34.8, 128 tokens of 96 heads 87.5 and 75.2).
     const long long ctas = (m + kFewRows - 1) / kFewRows * a.H;
     if (m <= kFewRows || (m <= 2 * kFewRows && ctas > a.num_sms / 2)) {
         note_launch();
