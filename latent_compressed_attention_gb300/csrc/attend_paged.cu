@@ -163,16 +163,17 @@ __device__ __forceinline__ int tokens(const P &p, int b, int &len, bool report) 
 struct Tile {
     int rows, t0, t1;      // (token, head) rows; first and last token
     int head, main, n;     // units from the cache's start on, first unit after those, units in all
-    int end;               // cache rows past the last one that is seen
+    int low, end;          // of the rows behind the sinks [low, end) are seen
     __device__ __forceinline__ Tile() {}
     __device__ __forceinline__ Tile(const PairParams &p, int j, int len, int count) {
         const int m0 = j * kM;
         rows = min(count * p.H - m0, kM);
         t0 = p.by_H(m0), t1 = p.by_H(m0 + rows - 1);
         end = len + t1 + 1;
-        main = head = 0;
+        main = head = low = 0;
         if (p.window > 0) {   // a draft stands at least at the first new position
-            main = max(len + (p.parents ? 0 : t0) - p.window + 1, 0) / kUnit;
+            low = max(len + (p.parents ? 0 : t0) - p.window + 1, 0);
+            main = low / kUnit;
             head = min((min(p.sinks, end) + kUnit - 1) / kUnit, main);
         }
         n = head + (end + kUnit - 1) / kUnit - main;
@@ -478,10 +479,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         __syncthreads();
     }
 
-    // The pool row of cache row u (u % 64 == 0) of a sequence, or one past the pool, which reads as zeros.
-    const auto pool_row = [&](int seq, int u, int end) {
+    // The pool row of cache row u (u % 64 == 0) of a sequence, or one past the pool, which reads as zeros.  Blocks of which
+    // no row is seen may have been given back: their entries are not read.
+    const auto pool_row = [&](int seq, int u, const Tile &t) {
         const int none = max(p.num_blocks * p.bs, 1);
-        if (u >= end) return none;
+        if (u >= t.end || (u + 64 <= t.low && u >= p.sinks)) return none;
         const int j = p.by_bs(u), block = __ldg(p.table + seq * p.ld_table + j);
         if (block < 0 || block >= p.num_blocks) {
             record_error(p.err, kDevErrBounds);
@@ -512,7 +514,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                         const bool units = i >= w.i0;
                         const int u = units ? w.t.row0(i) + half * 64 : 0;
                         // rows past the tile's, of the next one or past the tensor's end (zeros), are not used
-                        const int row = units ? pool_row(w.seq, u, w.t.end) : w.seq * p.T * p.H + w.index * kM + half * 64;
+                        const int row = units ? pool_row(w.seq, u, w.t) : w.seq * p.T * p.H + w.index * kM + half * 64;
 #pragma unroll 1
                         for (int kc = 0; kc < 8; ++kc, ++it, at.next()) {
                             // a barrier that no one has arrived at counts as past phase 1
@@ -576,7 +578,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                 while (ok && w.next(p, bars, cl)) {
                     for (int i = w.i0; ok && i < w.i1; ++i, it += 8) {
                         const int u = w.t.row0(i) + half * 64;
-                        const int row = pool_row(w.seq, u, w.t.end);
+                        const int row = pool_row(w.seq, u, w.t);
 #pragma unroll 1
                         for (int k = 0; ok && k < 8; ++k, at.next()) {
                             if (((k >> 1) & 1) != half) continue;

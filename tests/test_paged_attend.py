@@ -259,6 +259,22 @@ def test_hidden_rows_have_no_effect(env):
     assert env[1].mla_get_device_error() == 0
 
 
+@pytest.mark.parametrize("tree", [None, "mixed"])
+@pytest.mark.parametrize("bs", [64, 192])
+def test_blocks_behind_the_window_may_be_given_back(env, bs, tree):
+    """Table entries of blocks of which no token sees a row are not read, wherever they end in a unit of 128 rows."""
+    for T, lens, window, sinks in ((1, [500, 640, 1000], 70, 3), (5, [700, 449, 66], 129, 65), (7, [2000], 1, 0), (3, [900], 192, 0)):
+        d = problem(env, T, 40, lens, bs=bs, tree=tree, window=window, sinks=sinks, seed=bs)
+        gone = 0
+        for b, n in enumerate(lens):
+            for j in range(-(-n // bs)):
+                if j * bs >= sinks and (j + 1) * bs <= n - window + 1:
+                    d["block_table"][b, j] = -1
+                    gone += 1
+        assert gone
+        check(env, d)
+
+
 def test_nan_in_a_row_that_all_see(env):
     torch, _ = env
     d = problem(env, 2, 96, [700, 700])
