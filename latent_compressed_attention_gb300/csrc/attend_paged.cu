@@ -36,11 +36,11 @@
 //
 // What bounds it.  A unit's products are 2,048 tensor cycles on either CTA.  The score CTA moves 320 KB through shared memory
 // meanwhile (rows written by TMA and read, P written and copied) and the value CTA 350 KB (P read for either latent half):
-// 2,500 to 2,750 cycles at 128 bytes a cycle.  Long calls take 2,520 cycles per unit: 8 chunks of 512 tokens of 96 heads under
-// a window of 4096 take 2.1 ms, 1.5 PFLOP/s.  With one token of 96 heads per sequence HBM is the bound, 1.5 us per unit of all
-// clusters; 64 of them over 1.08 million rows take 215 us, 5.2 TB/s.  Besides, a part costs 1.2 to 3 us (drain, refill), and
-// a call 19 to 31 us before its first unit and after its last one: instructions come from L2 or DRAM then, a cold unit's
-// softmax takes twice as long.
+// 2,500 to 2,750 cycles at 128 bytes a cycle.  Long calls take 2,520 cycles per unit: 8 chunks of 512 tokens of 96 heads
+// under a window of 4096 take 2.1 ms, 1.5 PFLOP/s.  With one token of 96 heads per sequence HBM is the bound, 1.5 to 1.7 us per
+// unit of all clusters; 64 of them over 1.08 million rows take 216 to 221 us, 5.1 TB/s.  Besides, a part costs 1.2 to 3 us
+// (drain, refill), and a call 19 to 31 us before its first unit and after its last one: instructions come from L2 or DRAM
+// then, a cold unit's softmax takes twice as long.
 #include <cuda.h>
 #include <cudaTypedefs.h>
 
