@@ -28,8 +28,8 @@
 // A part (what a share has of a tile) leaves o_lat / l, and where the tile was cut between shares its maxima and sums of
 // weights, at most twice per share.  The values go as f16 with an exponent for each 32 of a row: off by 2^-11, an eighth of
 // what rounding the output costs, in half of fp32's bytes, which is what a part's end takes (an SM stores 27 bytes a cycle:
-// 256 KB of fp32 took as long as four units).  Up to 32 tokens, and up to 64 of many heads, one kernel joins the
-// parts, applies W_UV^T on the tensor cores and the gate; above, one joins them and a product per head follows.  Both take
+// 256 KB of fp32 took as long as four units).  For few tokens and heads one kernel joins the parts, applies W_UV^T on
+// the tensor cores and the gate; otherwise one joins them and a product per head follows.  Both take
 // the values to the product as two bf16 parts, off by 2^-16 at most.  So the roundings to 16 bits that count are the softmax
 // weights' (2^-8 of each, as in the prefill and the other decodes; two parts would double the value CTA's products), that of
 // a part (2^-11, and 2^-11 again where joined rows go through memory) and the output's.
@@ -1080,20 +1080,21 @@ __device__ __forceinline__ bool is_token(const UpParams &p, long long m, int &b,
     return b < p.B && t < tokens(p, b, len, false);
 }
 
-// Few tokens: one CTA per (head, 32 tokens).  Rows into swizzled slabs, hi over lo, from ws_rows or joined from parts, as
+// Few tokens and heads: one CTA per (head, 32 tokens).  Rows into swizzled slabs, hi over lo, from ws_rows or joined from parts, as
 // many warps to a row as there are.  W_UV[h] is the M side and the rows, hi and lo, the N = 64 of one product: 32
 // instructions of 53 cycles where the rows as M = 128 would take 64 of 64, and outputs that lie side by side in a warp.  All
 // of W_UV's eight slabs of 64 latent columns are loaded before the pair kernel ends where every CTA has an SM to itself
 // (kW = 8); otherwise two CTAs share one and two stages take the slabs in turn.
-constexpr int kFewRows = 32, kFewThreads = 256, kFewWarps = kFewThreads / 32;
+constexpr int kFewRows = 32;
+constexpr int few_threads(int kW) { return kW == 8 ? 512 : 256; }   // at most
 constexpr uint32_t kFewSlab = 2 * kFewRows * 128;         // [32 rows x 64 latent columns] hi, then lo
 constexpr uint32_t kFewW = 8 * kFewSlab;
 constexpr uint32_t few_bars(int kW) { return kFewW + kW * kSlab; }
 constexpr uint32_t few_smem(int kW) { return few_bars(kW) + 192 + 1024; }
-static_assert(kFewWarps * kR * 4 <= 8 * kFewSlab, "the warps' sums fit where the rows go");
+static_assert(few_threads(8) / 32 * kR * 4 <= 8 * kFewSlab, "the warps' sums fit where the rows go");
 
 template <int kW>
-__global__ void __launch_bounds__(kFewThreads, kW == 8 ? 1 : 2)
+__global__ void __launch_bounds__(few_threads(kW), kW == 8 ? 1 : 2)
     attend_few_kernel(const __grid_constant__ CUtensorMap tm_w, const UpParams p) {
     extern __shared__ uint8_t smem_raw[];
     const uint32_t raw = smem_u32(smem_raw);
@@ -1104,8 +1105,8 @@ __global__ void __launch_bounds__(kFewThreads, kW == 8 ? 1 : 2)
     uint32_t *const tmem_slot = reinterpret_cast<uint32_t *>(w_full + 2 * kW + 1);
     __shared__ int2 s_tile[kFewRows];   // first and last share of each row's tile; {-1, .}: not a token
     __shared__ int s_row[kFewRows];     // the row's place in its tile
-    __shared__ float s_m[kFewWarps], s_sum[kFewWarps];
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    __shared__ float s_m[few_threads(kW) / 32], s_sum[few_threads(kW) / 32];
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, warps = blockDim.x >> 5;
     const int h = blockIdx.x % p.H;
     const long long m0 = static_cast<long long>(blockIdx.x / p.H) * kFewRows;
     const int rows = static_cast<int>(min(static_cast<long long>(kFewRows), static_cast<long long>(p.B) * p.T - m0));
@@ -1147,7 +1148,7 @@ __global__ void __launch_bounds__(kFewThreads, kW == 8 ? 1 : 2)
     }
     __syncthreads();
     int per_row = 1;   // warps
-    while (rows * per_row * 2 <= kFewWarps) per_row *= 2;
+    while (rows * per_row * 2 <= warps) per_row *= 2;
     const auto store_row = [&](int i, const float (&o)[16], float mul) {
         const uint32_t slab = base + (lane >> 2) * kFewSlab;
 #pragma unroll
@@ -1160,7 +1161,7 @@ __global__ void __launch_bounds__(kFewThreads, kW == 8 ? 1 : 2)
             st_shared_v4(at + kFewSlab / 2, lo[0], lo[1], lo[2], lo[3]);
         }
     };
-    for (int i0 = 0; i0 < rows; i0 += kFewWarps / per_row) {
+    for (int i0 = 0; i0 < rows; i0 += warps / per_row) {
         const int i = i0 + warp / per_row, c0 = warp % per_row;
         const int2 tile = i < rows ? s_tile[i] : make_int2(-1, -1);
         const bool cut = tile.x >= 0 && tile.x != tile.y;
@@ -1661,15 +1662,18 @@ cudaError_t launch_attend_paged(const AttendPagedArgs &a, cudaStream_t s) {
     const UpParams up{a.lens, a.counts, ws_rows, ws_exp, ws_m, ws_l, ws_tile, ws_cut, all_rows,
                       static_cast<const __nv_bfloat16 *>(a.gate), static_cast<__nv_bfloat16 *>(a.out), a.dev_err, sp.rounds,
                       G, a.B, a.T, a.H, sp.tiles, a.bs, a.max_blocks};
-    // Up to 32 tokens, and up to 64 of many heads, the join, W_UV and the gate are one kernel of short CTAs (one token of 96
-    // heads over 30000 rows takes 28.7 us with it and 48.7 with the two others, 32 tokens of 96 heads 87 and 91, 64 tokens of
-    // 64 heads 84 and 88, of 96 heads 91 either way, of 16 heads 38.9 and 34.8, 128 tokens of 96 heads 87.5 and 75.2).
+    // Where all its CTAs run at once (two of kW = 2 to an SM), the join, W_UV and the gate are one kernel of short CTAs; two
+    // kernels otherwise.  One token of 96 heads over 30000 rows takes 26.8 us with the one and 51.1 with the two, 64 tokens of
+    // 64 heads 81 and 88, 512 of 8 heads 40 and 44, 128 of 64 heads 86.8 and 87.2, 128 of 96 heads (384 CTAs) 125 and 113.
     const long long ctas = (m + kFewRows - 1) / kFewRows * a.H;
-    if (m <= kFewRows || (m <= 2 * kFewRows && ctas > a.num_sms / 2)) {
+    if (ctas <= 2 * a.num_sms) {
         note_launch();
         const dim3 grid(static_cast<unsigned>(ctas));
-        return ctas <= a.num_sms ? launch_dependent(attend_few_kernel<8>, grid, kFewThreads, few_smem(8), s, tm_w, up)
-                                 : launch_dependent(attend_few_kernel<2>, grid, kFewThreads, few_smem(2), s, tm_w, up);
+        // Twice the warps for more than 8 rows: 32 tokens of 8 heads 29.5 -> 27.1 us, of 96 heads 89.0 -> 85.7; 4 tokens of 8
+        // heads 17.7 with few and 18.1 with many.
+        const int kW = ctas <= a.num_sms ? 8 : 2, threads = m > 8 ? few_threads(kW) : 256;
+        return kW == 8 ? launch_dependent(attend_few_kernel<8>, grid, threads, few_smem(8), s, tm_w, up)
+                       : launch_dependent(attend_few_kernel<2>, grid, threads, few_smem(2), s, tm_w, up);
     }
     CUtensorMap tm_a;
     {

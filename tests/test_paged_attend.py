@@ -272,6 +272,7 @@ def test_blocks_behind_the_window_may_be_given_back(env, bs, tree):
                     d["block_table"][b, j] = -1
                     gone += 1
         assert gone
+        d["block_table"] = d["block_table"][:, :-1]   # as wide as the longest sequence and no wider
         check(env, d)
 
 
