@@ -253,7 +253,10 @@ cudaError_t launch_reserve_latent_blocks(const ReserveArgs &a, cudaStream_t s) {
     const bool all = static_cast<long long>(a.B) * a.T <= 8192;
     auto *const kernel = all ? reserve_latent_blocks_kernel<true> : reserve_latent_blocks_kernel<false>;
     if (smem > 40000) {
-        const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
+        // The limit is the kernel's, not the call's: always that of the most sequences, so that a call of another thread does
+        // not lower it between here and the launch.
+        constexpr int kMost = (3 * kReserveMaxB + 2) * static_cast<int>(sizeof(int));
+        const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kMost);
         if (e != cudaSuccess) return e;
     }
     note_launch();

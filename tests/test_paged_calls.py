@@ -1,0 +1,48 @@
+"""GPU tests of calls of the paged latent cache as programs make them: from several threads at once, with states at the
+edge of their ranges or outside them."""
+import threading
+
+import pytest
+
+pytestmark = pytest.mark.gpu
+
+BOUNDS = -9
+
+
+@pytest.fixture(scope="module")
+def env():
+    import torch
+
+    import latent_compressed_attention_gb300 as lca
+    lca.build()
+    lca.mla_get_device_error()
+    return torch, lca
+
+
+def test_reserve_from_two_threads(env):
+    """Calls whose numbers of sequences ask for different amounts of shared memory, at the same time."""
+    torch, lca = env
+    lib, status, go = lca.library(), {}, threading.Event()
+
+    def calls(B, n):
+        i32 = dict(dtype=torch.int32, device="cuda")
+        stream = torch.cuda.Stream()
+        with torch.cuda.stream(stream):
+            lens, table, free = torch.full((B,), 70, **i32), torch.zeros(B, 2, **i32), torch.randperm(2 * B, device="cuda").int()
+            held, left, counts = torch.zeros(B, **i32), torch.tensor([2 * B], **i32), torch.zeros(B, **i32)
+        stream.synchronize()
+        args = (lens.data_ptr(), counts.data_ptr(), table.data_ptr(), 2, held.data_ptr(), free.data_ptr(), left.data_ptr(), None,
+                B, 0, 2, 2 * B, 64, stream.cuda_stream)
+        go.wait()
+        status[B] = [lib.mla_reserve_latent_blocks(*args) for _ in range(n)]
+        stream.synchronize()
+        assert int(left) == 0 and held.tolist() == [2] * B
+
+    threads = [threading.Thread(target=calls, args=(B, 3000)) for B in (16384, 3400, 9000)]
+    for t in threads:
+        t.start()
+    go.set()
+    for t in threads:
+        t.join()
+    assert {B: sum(rc != 0 for rc in rcs) for B, rcs in status.items()} == {16384: 0, 3400: 0, 9000: 0}
+    assert lca.mla_get_device_error() == 0
