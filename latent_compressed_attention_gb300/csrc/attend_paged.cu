@@ -47,6 +47,7 @@
 #include <algorithm>
 #include <atomic>
 
+#include "attend_shares.h"
 #include "common.cuh"
 #include "internal.h"
 
@@ -227,8 +228,7 @@ struct Walk {
     }
     __device__ __forceinline__ int seq_len(const PairParams &p) const { return __ldg(p.lens + seq); }
     __device__ __forceinline__ bool whole() const { return i0 == 0 && i1 == t.n; }
-    // A share has at most one part that starts before it and one that starts in it and ends after it.
-    __device__ __forceinline__ int slot() const { return 2 * share + (i0 == 0 ? 1 : 0); }
+    __device__ __forceinline__ int slot() const { return static_cast<int>(part_number(share, i0 == 0)); }
 };
 
 // The cache rows that a token sees: [0, head), [lo, hi), and of the 64 from `hi` on those whose bit is set.
@@ -1033,7 +1033,7 @@ __device__ __forceinline__ void join_parts(const UpParams &p, int first, int las
 #pragma unroll
     for (int k = 0; k < 16; ++k) o[k] = 0.f;
     M = -INFINITY, sum = 0.f;
-    const auto part = [&](int c) { return static_cast<long long>(2 * c + (c == first ? 1 : 0)) * kM + r; };
+    const auto part = [&](int c) { return part_number(c, c == first) * kM + r; };
     for (int c = first + c0; c <= last; c += 32 * step) {   // a lane per part: maxima and weights, 32 at a time
         const int mine = c + lane * step;
         const bool has = mine <= last;
@@ -1103,7 +1103,7 @@ __global__ void __launch_bounds__(few_threads(kW), kW == 8 ? 1 : 2)
     uint64_t *const w_empty = w_full + kW;                                                            // [kW]
     uint64_t *const done = w_full + 2 * kW;
     uint32_t *const tmem_slot = reinterpret_cast<uint32_t *>(w_full + 2 * kW + 1);
-    __shared__ int2 s_tile[kFewRows];   // first and last share of each row's tile; {-1, .}: not a token
+    __shared__ int2 s_tile[kFewRows];   // first and last share of each row's tile; {-1, .}: not a token, or nothing there
     __shared__ int s_row[kFewRows];     // the row's place in its tile
     __shared__ float s_m[few_threads(kW) / 32], s_sum[few_threads(kW) / 32];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, warps = blockDim.x >> 5;
@@ -1143,7 +1143,12 @@ __global__ void __launch_bounds__(few_threads(kW), kW == 8 ? 1 : 2)
     grid_launch_dependents();
     if (threadIdx.x < kFewRows) {
         const long long r = static_cast<long long>(t) * p.H + h;
-        s_tile[threadIdx.x] = token ? p.ws_tile[static_cast<long long>(b) * p.tiles + r / kM] : make_int2(-1, -1);
+        int2 tile = token ? p.ws_tile[static_cast<long long>(b) * p.tiles + r / kM] : make_int2(-1, -1);
+        if (token && !shares_written(tile.x, tile.y, p.max_rounds * p.G)) {   // a wait ran out before the tile was done
+            record_error(p.err, kDevErrTimeout);
+            tile = make_int2(-1, -1);
+        }
+        s_tile[threadIdx.x] = tile;
         s_row[threadIdx.x] = static_cast<int>(r % kM);
     }
     __syncthreads();
