@@ -27,6 +27,7 @@ struct ReserveParams {
 };
 
 constexpr int kBatch = 4;   // blocks that a thread moves at a time, their searches and loads in flight together
+constexpr long long kMostMoved = 0x7FFFFFFFll - kBatch * kReserveThreads;   // their numbers, and a turn of the CTA's more, fit int
 
 // Of each k the sequence whose part of [0, pre[B]) holds it.  `top`: the largest power of two up to B.
 __device__ __forceinline__ void owners(const int *pre, int B, int top, const int (&k)[kBatch], int (&b)[kBatch]) {
@@ -116,6 +117,7 @@ __global__ void __launch_bounds__(kReserveThreads) reserve_latent_blocks_kernel(
     __syncthreads();
     const long long A = all_sum[0], R = all_sum[1];
     bad |= A > F + R || F + R - A > p.capacity;   // what does not fit changes nothing
+    bad |= max(A, R) > kMostMoved;
     if (!bad) {
         long long t = warp_sum[0][warp] + before[0] - sum[0], g = warp_sum[1][warp] + before[1] - sum[1];
         for (int b = b0; b < b1; ++b) {

@@ -46,3 +46,19 @@ def test_reserve_from_two_threads(env):
         t.join()
     assert {B: sum(rc != 0 for rc in rcs) for B, rcs in status.items()} == {16384: 0, 3400: 0, 9000: 0}
     assert lca.mla_get_device_error() == 0
+
+
+def test_more_blocks_than_an_int_counts(env):
+    """Half of the sequences give up all their blocks and the others take as many, 2^31."""
+    torch, lca = env
+    B, wide, i32 = 16384, 2**18, dict(dtype=torch.int32, device="cuda")
+    table = torch.empty((B, wide), **i32)
+    table[:, :2] = 5
+    held = torch.full((B,), wide, **i32)
+    held[1::2] = 0
+    lens = wide - held
+    free, left, none = torch.full((4,), -5, **i32), torch.zeros(1, **i32), torch.zeros(B, **i32)
+    before = [x.clone() for x in (held, free, left, table[:, :2])]
+    lca.mla_reserve_latent_blocks(lens, none, 0, table, held, free, left, 1)
+    assert lca.mla_get_device_error() == BOUNDS
+    assert all(torch.equal(a, b) for a, b in zip(before, (held, free, left, table[:, :2])))
