@@ -364,10 +364,14 @@ MLA_API int mla_latent_decode_fp4(const void *q_abs, const void *c4_cache, long 
  *   slots         int32 [B, T] (16-byte aligned) or NULL when T is 0: block_table[b][u / block_size] * block_size +
  *                 u % block_size with u = lens[b] + t for t < counts[b], -1 for the other t
  * All or nothing: when the free blocks do not suffice, a sequence needs more than max_blocks, a count is above T (with
- * slots), a length, count, held or free_count is out of its range or 2^31 - 4096 blocks or more would be given up or taken,
- * the state stays as it was, every slot is -1 and MLA_ERR_DEVICE_BOUNDS is reported (mla_get_device_error).  Blocks are
- * numbers from 0 on; a new row past pool row 2^31 - 1 is reported the same way and has the slot -1, with more than 8192
- * slots a sequence whose first one is.
+ * slots), a length, count, held or free_count is out of its range, a block that would be given up or taken is below 0 or
+ * 2^31 - 4096 of them or more would be, every sequence and the stack keep their blocks, every slot is -1 and
+ * MLA_ERR_DEVICE_BOUNDS is reported (mla_get_device_error); after a block below 0, entries from held[b] on and the stack's
+ * from free_count on may hold anything.  Blocks are numbers from 0 on; a new row past pool row 2^31 - 1 is reported the
+ * same way and has the slot -1, with more than 8192 slots a sequence whose first one is.
+ * A block is in the first held[b] entries of one sequence or on the stack, never in two places: this is not checked, and a
+ * block in two places serves two sequences.  That goes for blocks behind a window, too: the attention does not read their
+ * entries, but a sequence keeps its blocks until it needs fewer, and gives up its last ones only.
  * Supported: B <= 16384.  Returns MLA_OK or a negative mla_status_t; nothing is launched on error.
  */
 MLA_API int mla_reserve_latent_blocks(const int *lens, const int *counts, int *block_table, long long ld_table, int *held,

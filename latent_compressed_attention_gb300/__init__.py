@@ -752,8 +752,10 @@ def mla_reserve_latent_blocks(lens, counts, T: int, block_table, held, free_bloc
     lens, counts, held: int32 [B]; block_table int32 [B,max_blocks] (rows at any stride); free_blocks int32 [capacity]: a
     stack of free_count[0] (int32 [1]) blocks, its last entry on top.  Sequences that hold more than they need give blocks
     up, which serve the others before the stack does; held becomes what each one needs.  T is at least the largest count;
-    with T = 0 only the blocks are moved and None is returned.  If something does not fit or is out of range, nothing
-    changes, every slot is -1 and the device error word is set (mla_get_device_error).
+    with T = 0 only the blocks are moved and None is returned.  If something does not fit or is out of range, a block to be
+    moved that is below 0 too, nothing changes, every slot is -1 and the device error word is set (mla_get_device_error).
+    A sequence keeps its blocks, those behind a window too, until it needs fewer: a block that a caller puts on the stack
+    while a sequence holds it is handed out twice.
     """
     torch = _torch()
     dev, B, T = lens.device, lens.shape[0], _count(T, "T")

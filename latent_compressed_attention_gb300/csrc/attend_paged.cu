@@ -479,8 +479,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         __syncthreads();
     }
 
-    // The pool row of cache row u (u % 64 == 0) of a sequence, or one past the pool, which reads as zeros.  Blocks of which
-    // no row is seen may have been given back: their entries are not read.
+    // The pool row of cache row u (u % 64 == 0) of a sequence, or one past the pool, which reads as zeros.  Entries of blocks
+    // of which no row is seen are not read and may hold anything.
     const auto pool_row = [&](int seq, int u, const Tile &t) {
         const int none = max(p.num_blocks * p.bs, 1);
         if (u >= t.end || (u + 64 <= t.low && u >= p.sinks)) return none;

@@ -128,12 +128,12 @@ __global__ void __launch_bounds__(kReserveThreads) reserve_latent_blocks_kernel(
         if (tid == 0) take[p.B] = static_cast<int>(A), give[p.B] = static_cast<int>(R);
     }
     const bool slots = p.slots != nullptr;
-    if (bad) {
+    const auto refuse = [&] {
         if (tid == 0) record_error(p.err, kDevErrBounds);
         const long long every = kAll ? 1 : p.T, n = slots ? static_cast<long long>(p.B) * p.T : 0;
         for (long long i = tid * every; i < n; i += kReserveThreads * every) p.slots[i] = -1;
-        return;
-    }
+    };
+    if (bad) return refuse();
     __syncthreads();   // the prefix sums are there; held and free_count have been read
     const int a_all = static_cast<int>(A), r_all = static_cast<int>(R);
     // Only sequences that keep no more than they need take blocks, and only the others give some up: the entries read
@@ -161,7 +161,12 @@ __global__ void __launch_bounds__(kReserveThreads) reserve_latent_blocks_kernel(
 #pragma unroll
         for (int i = 0; i < kBatch; ++i)
             if (k[i] >= a_all && k[i] < r_all) p.free_blocks[F + r_all - 1 - k[i]] = block[i];
+#pragma unroll
+        for (int i = 0; i < kBatch; ++i) bad |= k[i] < max(a_all, r_all) && block[i] < 0;
     }
+    // A number below 0 is no block, and as one would serve another sequence.  What has been written lies behind what each
+    // sequence holds and behind the stack's top: without the new held and free_count nothing has moved.
+    if (__syncthreads_or(bad)) return refuse();
     for (int b = tid; b < p.B; b += kReserveThreads) p.held[b] = need[b];
     if (tid == 0) *p.free_count = F + r_all - a_all;
     if (!slots) return;

@@ -62,3 +62,44 @@ def test_more_blocks_than_an_int_counts(env):
     lca.mla_reserve_latent_blocks(lens, none, 0, table, held, free, left, 1)
     assert lca.mla_get_device_error() == BOUNDS
     assert all(torch.equal(a, b) for a, b in zip(before, (held, free, left, table[:, :2])))
+
+
+@pytest.mark.parametrize("T", [4, 4000])
+@pytest.mark.parametrize("many", [False, True])
+@pytest.mark.parametrize("where", ["given up, to the stack", "given up, taken", "stack"])
+def test_what_is_no_block_is_not_moved(env, where, many, T):
+    """A number below 0 among those given up or taken refuses the call; where it stays it does not count."""
+    torch, lca = env
+    i32 = dict(dtype=torch.int32, device="cuda")
+    wide, bs = (6000, 1) if many else (6, 64)   # up to 12000 blocks moved, more than one each thread's turn, or 12
+    gen = torch.Generator(device="cuda").manual_seed(1)
+    ids = torch.randperm(4 * wide, generator=gen, device="cuda").int()
+    table = torch.full((5, wide), -3, **i32)
+    table[:3] = ids[:3 * wide].view(3, wide)
+    held, left = torch.tensor([wide, wide, wide, 0, 0], **i32), torch.tensor([wide], **i32)
+    free = torch.cat([ids[3 * wide:], torch.full((3 * wide,), -5, **i32)])
+    lens, counts = torch.tensor([wide * bs, 0, 0, 0, 0], **i32), torch.zeros(5, **i32)
+    if where != "given up, to the stack":   # those that two give up go to the others, or some of the stack too
+        lens[3] = lens[4] = wide * bs
+    if where == "stack":
+        lens[2] = wide * bs
+        free[wide // 2] = -1
+    else:
+        table[2 if many else 1, wide // 3] = -1
+    table[0, 1] = -2   # of a sequence that keeps its blocks
+    before = [x.clone() for x in (table[:3], held, free[:wide], left)]
+    slots = lca.mla_reserve_latent_blocks(lens, counts, T, table, held, free, left, bs)
+    assert lca.mla_get_device_error() == BOUNDS and bool((slots == -1).all())
+    assert all(torch.equal(a, b) for a, b in zip(before, (table[:3], held, free[:wide], left)))
+    if where == "stack":
+        free[wide // 2] = 4 * wide
+    else:
+        table[2 if many else 1, wide // 3] = 4 * wide
+    lca.mla_reserve_latent_blocks(lens, counts, T, table, held, free, left, bs)
+    assert lca.mla_get_device_error() == 0
+    assert held.tolist() == [-(-n // bs) for n in lens.tolist()]
+    now = torch.cat([table[b, :n] for b, n in enumerate(held.tolist())] + [free[:int(left)]])
+    then = torch.cat([before[0].flatten(), before[2]])
+    for n in (-1, -2):   # a block each, in one place
+        then, now = then[then != n], now[now != n]
+    assert sorted(now.tolist()) == sorted(then.tolist() + [4 * wide])
