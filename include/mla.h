@@ -346,8 +346,13 @@ MLA_API int mla_latent_decode_fp4(const void *q_abs, const void *c4_cache, long 
  * elements, block stride block_size * ld_pool); cache row u of sequence b is row u % block_size of block
  * block_table[b * ld_table + u / block_size].  A serving step of T new tokens per sequence: reserve (blocks for rows
  * lens[b] .. lens[b] + counts[b] - 1 and their slots), append (their latents), attend, then the caller advances lens by
- * the tokens it keeps.  Drafts that are dropped need nothing: their rows are written again, their blocks go back at the
- * next reserve.  num_blocks * block_size and max_blocks * block_size are at most 2^31 - 1024.
+ * the number of tokens it keeps.
+ * Kept tokens have to stand one after the other.  Tokens 0, 1, .. of a chunk do.  Of a drafted tree, draft t's latent is
+ * row lens[b] + t, but the d-th token of the path that is kept, counted from 0, belongs in row lens[b] + d: unless the path
+ * is drafts 0, 1, 2, .., append its latents again, the d-th to slots[b][d] (all sequences' in one call, with -1 where a
+ * path is shorter), before lens is advanced.  Otherwise later calls take rows of dropped drafts for the past.  Dropped
+ * drafts themselves need nothing: their rows are written again, their blocks go back at the next reserve.
+ * num_blocks * block_size and max_blocks * block_size are at most 2^31 - 1024.
  *
  * mla_reserve_latent_blocks - give each sequence the blocks for lens[b] + counts[b] rows and map its new tokens to
  * pool rows.  In place, on the device, in a fixed order (the same inputs give the same blocks):
@@ -393,7 +398,8 @@ MLA_API int mla_append_latent_paged(const void *c, long long ld_c, void *pool, l
 
 /*
  * mla_latent_attend_paged - steps 2-4 for counts[b] new tokens of each sequence over the paged cache, in which the new
- * tokens' own latents are rows lens[b] .. lens[b] + counts[b] - 1 (mla_append_latent_paged):
+ * tokens' own latents are rows lens[b] .. lens[b] + counts[b] - 1 (mla_append_latent_paged); a tree's kept path is appended
+ * again afterwards, see above:
  *
  *   out[b,t,h] = sigmoid(gate[b,t,h]) * W_UV[h] . sum_u a_u c_u,   a = softmax over the visible rows u of
  *                scale * q_abs[b,t,h] . c_u

@@ -818,8 +818,11 @@ def mla_latent_attend_paged(q_abs, pool, block_table, lens, w_uv, counts=None, p
 
     Without parents the tokens are a chunk and token t sees rows up to lens[b] + t.  With parents (int32 [B,T], T <= 64)
     they are drafts: token t follows the new token parents[b,t] < t (-1: the cached ones) and sees the cached rows, its
-    ancestors and itself.  With window > 0 it sees only the last `window` positions up to its own, and positions below
-    `sinks`.  A workspace (a contiguous tensor on the query's device) is allocated when not given.
+    ancestors and itself.  Drafts stand in the cache by their number, kept tokens one after the other: of the path that is
+    kept the d-th latent, from 0, is appended again to slots[b,d] before lens is advanced (mla_append_latent_paged, one call
+    for all sequences, -1 where a path is shorter), unless the path is drafts 0, 1, 2, ...
+
+    With window > 0 a token sees only the last `window` positions up to its own, and positions below `sinks`.  A workspace (a contiguous tensor on the query's device) is allocated when not given.
     """
     torch = _torch()
     if q_abs.dim() != 4:

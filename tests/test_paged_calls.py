@@ -1,7 +1,8 @@
 """GPU tests of calls of the paged latent cache as programs make them: from several threads at once, with states at the
-edge of their ranges or outside them."""
+edge of their ranges or outside them, step after step."""
 import threading
 
+import numpy as np
 import pytest
 
 pytestmark = pytest.mark.gpu
@@ -103,3 +104,61 @@ def test_what_is_no_block_is_not_moved(env, where, many, T):
     for n in (-1, -2):   # a block each, in one place
         then, now = then[then != n], now[now != n]
     assert sorted(now.tolist()) == sorted(then.tolist() + [4 * wide])
+
+
+def test_kept_paths_of_drafted_trees(env):
+    """Rounds of drafting as the header tells them: of each sequence's tree a path is kept, and all paths' latents are
+    appended again in one call.  Every sequence's rows are its kept tokens, and the attention's outputs those over the same
+    rows in blocks of their own, bit by bit."""
+    torch, lca = env
+    i32, bf16 = dict(dtype=torch.int32, device="cuda"), torch.bfloat16
+    gen = torch.Generator(device="cuda").manual_seed(3)
+    rng = np.random.default_rng(3)
+    B, T, H, bs, wide, r = 5, 9, 16, 64, 4, 512
+    pool = torch.full((B * wide, bs, r), float("nan"), dtype=bf16, device="cuda")
+    table, held = torch.full((B, wide), -1, **i32), torch.zeros(B, **i32)
+    free, left = torch.randperm(B * wide, generator=gen, device="cuda").int(), torch.tensor([B * wide], **i32)
+    w_uv = (torch.randn((H, 128, r), generator=gen, device="cuda") * 0.05).to(bf16)
+    lens, past = torch.tensor([0, 61, 5, 63, 120], **i32), []
+    c = torch.randn((B, 120, r), generator=gen, device="cuda").to(bf16)   # prompts
+    slots = lca.mla_reserve_latent_blocks(torch.zeros_like(lens), lens, 120, table, held, free, left, bs)
+    lca.mla_append_latent_paged(c, pool, slots)
+    past = [c[b, :n] for b, n in enumerate(lens.tolist())]
+
+    def rows(b, n):
+        u = torch.arange(n, device="cuda")
+        return pool[table[b].long()[u // bs], u % bs]
+
+    moved = 0
+    for _ in range(8):
+        counts = torch.full((B,), T, **i32)
+        parents = np.array([[rng.integers(-1, t) if t else -1 for t in range(T)] for _ in range(B)])
+        c = torch.randn((B, T, r), generator=gen, device="cuda")   # fp32, as a norm leaves them
+        slots = lca.mla_reserve_latent_blocks(lens, counts, T, table, held, free, left, bs)
+        lca.mla_append_latent_paged(c, pool, slots)
+        q = torch.randn((B, T, H, r), generator=gen, device="cuda").to(bf16)
+        out = lca.mla_latent_attend_paged(q, pool, table, lens, w_uv, parents=torch.tensor(parents, **i32), scale=0.05)
+        alone = torch.zeros((B, wide * bs, r), dtype=bf16, device="cuda")
+        for b in range(B):
+            alone[b, :len(past[b]) + T] = torch.cat([past[b], c[b].to(bf16)])
+        own = torch.arange(B * wide, **i32).view(B, wide)
+        want = lca.mla_latent_attend_paged(q, alone.view(B * wide, bs, r), own, lens, w_uv,
+                                           parents=torch.tensor(parents, **i32), scale=0.05)
+        assert bool(out.isfinite().all()) and torch.equal(out, want)
+        path = np.full((B, T), -1)
+        for b in range(B):
+            line, a = [], rng.integers(-1, T)   # -1: none is kept
+            while a >= 0:
+                line.insert(0, a)
+                a = parents[b, a]
+            path[b, :len(line)] = line
+            moved += line != list(range(len(line)))
+        path = torch.tensor(path, device="cuda")
+        kept = (path >= 0).sum(1).int()
+        lca.mla_append_latent_paged(c.gather(1, path.clamp(min=0)[:, :, None].expand(B, T, r)), pool,
+                                    torch.where(path >= 0, slots, -1))
+        lens = lens + kept
+        for b in range(B):
+            past[b] = torch.cat([past[b], c[b, path[b, :int(kept[b])]].to(bf16)])
+            assert torch.equal(rows(b, int(lens[b])), past[b])
+    assert moved > B and lca.mla_get_device_error() == 0
