@@ -422,6 +422,7 @@ MLA_API int mla_append_latent_paged(const void *c, long long ld_c, void *pool, l
  * Precision: products of bf16 values in fp32; softmax statistics, sums and the join of split rows in fp32.  Rounded to
  * bf16 are the softmax weights and out.  The weighted latent is kept as f16 with an exponent for each 32 values (2^-11
  * of each part, once more where split rows are joined) and goes to the product with W_UV as two bf16 parts (2^-16).
+ * The same call gives the same bits.  Which rows are split depends on all sequences of a call, and so do last bits.
  * Supported: r = 512, d_v = 128, 1 <= H <= 128, block_size a multiple of 64.
  * Returns MLA_OK or a negative mla_status_t; nothing is launched on error.
  */
