@@ -67,7 +67,10 @@ constexpr float kRescaleLog2 = 16.0f;
 constexpr int kStart = 2;
 // Rounds of shares: as many as bring the rows of a round's sequences down to this, but no more than one for every 6 tiles of a
 // sequence, each of them of at least 16 units per cluster.  (16 sequences of 64 drafts of 96 heads over up to 16000 rows, 48
-// tiles each: 1164 us in one round, 1087 in four; 64 sequences of 4, 3 tiles each: 210 and 222.)
+// tiles each: 1164 us in one round, 1087 in four; 64 sequences of 4, 3 tiles each: 210 and 222.)  Both go by sequences of T
+// tokens each, all with as many tiles: the rows are taken to be the axis' part for one tile, starts included.  Where counts
+// differ they are underestimated, by up to the number of tiles where most sequences have one, and fewer rounds are made than
+// would bring the rows down to this: a matter of time alone.
 constexpr int kRounds = 4, kRoundTiles = 6, kRoundMin = 16;
 constexpr long long kRoundBytes = 96ll << 20;
 
