@@ -464,7 +464,8 @@ MLA_API int mla_append_latent_paged(const void *c, long long ld_c, void *pool, l
         return MLA_ERR_ALIGN;
     DeviceInfo *dev = nullptr;
     if (device_info(dev) != cudaSuccess) return MLA_ERR_CUDA;
-    const AppendPagedArgs a{c, pool, slots, ld_c, ld_pool, rows, pool_rows, r, dtype == MLA_DTYPE_F32, dev->err_word};
+    const AppendPagedArgs a{c, pool, slots, ld_c, ld_pool, rows, pool_rows, r, dtype == MLA_DTYPE_F32, dev->err_word,
+                            dev->num_sms};
     return launch_append_latent_paged(a, static_cast<cudaStream_t>(stream)) == cudaSuccess ? MLA_OK : MLA_ERR_CUDA;
 }
 

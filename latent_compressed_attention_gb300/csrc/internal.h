@@ -141,6 +141,7 @@ struct AppendPagedArgs {
     int r;
     bool f32;                                     // c's type (the pool is bf16)
     int *dev_err;
+    int num_sms;
 };
 cudaError_t launch_append_latent_paged(const AppendPagedArgs &a, cudaStream_t s);
 // A run of tokens per sequence over the paged cache (attend_paged.cu).

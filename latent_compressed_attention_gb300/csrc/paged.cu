@@ -280,7 +280,7 @@ cudaError_t launch_append_latent_paged(const AppendPagedArgs &a, cudaStream_t s)
     AppendParams p{a.c, static_cast<__nv_bfloat16 *>(a.pool), a.slots, a.ld_c, a.ld_pool, a.pool_rows, 0, a.r / 8, a.dev_err};
     p.pieces = a.rows * p.per_row;
     // four pieces per thread from a wave of the GPU's threads on, one below
-    const bool many = p.pieces >= 152ll * 2048;
+    const bool many = p.pieces >= a.num_sms * 2048ll;
     const long long blocks = (p.pieces + kAppendThreads * (many ? kMany : 1) - 1) / (kAppendThreads * (many ? kMany : 1));
     if (blocks > 0x7FFFFFFFll) return cudaErrorInvalidValue;
     const auto go = [&](auto kernel) {

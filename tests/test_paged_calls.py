@@ -162,3 +162,19 @@ def test_kept_paths_of_drafted_trees(env):
             past[b] = torch.cat([past[b], c[b, path[b, :int(kept[b])]].to(bf16)])
             assert torch.equal(rows(b, int(lens[b])), past[b])
     assert moved > B and lca.mla_get_device_error() == 0
+
+
+@pytest.mark.parametrize("dtype", ["bfloat16", "float32"])
+@pytest.mark.parametrize("more", [-1, 0, 1])
+def test_append_at_a_wave_of_threads(env, more, dtype):
+    """Just fewer and just more rows than a thread each of the GPU has a piece of 8 elements for."""
+    torch, lca = env
+    rows = torch.cuda.get_device_properties(0).multi_processor_count * 2048 // 64 + more
+    gen = torch.Generator(device="cuda").manual_seed(rows)
+    c = torch.randn((rows, 512), generator=gen, device="cuda").to(getattr(torch, dtype))
+    pool = torch.zeros((-(-rows // 64) + 1, 64, 512), dtype=torch.bfloat16, device="cuda")
+    slots = torch.randperm(len(pool) * 64, generator=gen, device="cuda")[:rows].int()
+    want = pool.view(-1, 512).clone()
+    want[slots.long()] = c.to(torch.bfloat16)
+    lca.mla_append_latent_paged(c, pool, slots)
+    assert torch.equal(pool.view(-1, 512), want) and lca.mla_get_device_error() == 0
