@@ -32,15 +32,19 @@
 // the tensor cores and the gate; otherwise one joins them and a product per head follows.  Both take
 // the values to the product as two bf16 parts, off by 2^-16 at most.  So the roundings to 16 bits that count are the softmax
 // weights' (2^-8 of each, as in the prefill and the other decodes; two parts would double the value CTA's products), that of
-// a part (2^-11, and 2^-11 again where joined rows go through memory) and the output's.
+// a part (2^-11, and 2^-11 again where joined rows go through memory) and the output's.  Over 9,000 rows in two parts they
+// are 0.0008, 0.0003 and 0.0017 of the outputs' norm.
 //
-// What bounds it.  A unit's products are 2,048 tensor cycles on either CTA.  The score CTA moves 320 KB through shared memory
-// meanwhile (rows written by TMA and read, P written and copied) and the value CTA 350 KB (P read for either latent half):
-// 2,500 to 2,750 cycles at 128 bytes a cycle.  Long calls take 2,520 cycles per unit: 8 chunks of 512 tokens of 96 heads
-// under a window of 4096 take 2.1 ms, 1.5 PFLOP/s.  With one token of 96 heads per sequence HBM is the bound, 1.5 to 1.7 us per
-// unit of all clusters; 64 of them over 1.08 million rows take 216 to 221 us, 5.1 TB/s.  Besides, a part costs 1.2 to 3 us
-// (drain, refill), and a call 19 to 31 us before its first unit and after its last one: instructions come from L2 or DRAM
-// then, a cold unit's softmax takes twice as long.
+// What bounds it.  A unit's products are 2,048 tensor cycles on either CTA, and both work at once.  8 chunks of 512 tokens of 96
+// heads under a window of 4096 take 2.06 to 2.14 ms, 1.5 PFLOP/s: 1,289 units per pair, 1.38 ms of products at 1.92 GHz, 40
+// parts of 1.2 to 3 us (drain, refill), and W_UV's kernel, 0.13 ms.  The rest lies between the products, and no one thing is
+// known to be it.  In copies of the kernel made for timing, cache rows that are loaded once and used again save 0.15 ms,
+// softmaxes that are left out 0.08 ms, both together 0.27 ms.  The counters show the tensor pipe 70 % active, L2's way to the
+// SMs 56 %, shared memory's banks 25 % read and 23 % written; the score CTA moves 320 KB per unit through shared memory (rows
+// written by TMA and read, P written and copied), the value CTA 350 KB (P read for either latent half).
+// With one token of 96 heads per sequence HBM is the bound, 1.5 to 1.7 us per unit of all clusters; 64 of them over 1.08 million
+// rows take 216 to 225 us, 4.9 to 5.1 TB/s, and 166 with rows used again.  Besides, a call takes 19 to 31 us before its first unit
+// and after its last one: instructions come from L2 or DRAM then, a cold unit's softmax takes twice as long.
 #include <cuda.h>
 #include <cudaTypedefs.h>
 
