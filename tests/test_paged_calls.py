@@ -178,3 +178,38 @@ def test_append_at_a_wave_of_threads(env, more, dtype):
     want[slots.long()] = c.to(torch.bfloat16)
     lca.mla_append_latent_paged(c, pool, slots)
     assert torch.equal(pool.view(-1, 512), want) and lca.mla_get_device_error() == 0
+
+
+def test_attention_calls_at_once(env):
+    """Calls of all three endings on four streams at the same time, and a captured one without a workspace of its own between
+    eager calls: each gives the bits that it gives alone."""
+    torch, lca = env
+    from tests.test_paged_attend import attend, problem
+    calls = [problem(env, 1, 8, [300, 1], window=100, sinks=2, seed=1), problem(env, 64, 96, [900, 20], tree="mixed", seed=2),
+             problem(env, 16, 96, [5000, 70, 2000], tree="chain", seed=3), problem(env, 300, 30, [2000], seed=4)]
+    want = [attend(env, d) for d in calls]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in calls]
+    got = [[] for _ in calls]
+    for _ in range(12):
+        for d, s, g in zip(calls, streams, got):
+            with torch.cuda.stream(s):
+                g.append(attend(env, d))
+    torch.cuda.synchronize()
+    for w, g in zip(want, got):
+        assert all(torch.equal(w, x) for x in g)
+    outs, graphs = [torch.zeros_like(w) for w in want], []
+    for d, o in zip(calls, outs):
+        graphs.append(torch.cuda.CUDAGraph())
+        with torch.cuda.graph(graphs[-1]):
+            attend(env, d, out=o)
+            attend(env, d, out=o)
+    for _ in range(3):
+        for graph, d, o, w in zip(graphs, calls[1:] + calls[:1], outs, want):
+            junk = torch.full((2**22,), float("nan"), device="cuda")
+            graph.replay()
+            other = attend(env, d)
+            del junk
+            assert torch.equal(o, w) and bool(other.isfinite().all())
+            o.zero_()
+    assert lca.mla_get_device_error() == 0
