@@ -415,8 +415,8 @@ MLA_API int mla_append_latent_paged(const void *c, long long ld_c, void *pool, l
  *   counts       int32 [B] or NULL (T each); rows of out for t >= counts[b] are left as they were
  *   parents      int32 [B, T] or NULL; T <= 64 with it
  *   w_uv         [H, d_v, r], gate [B, T, H*d_v] or NULL (pre-sigmoid logits), out [B, T, H*d_v], all bf16
- *   workspace    >= mla_latent_attend_paged_workspace_size(B, T, H, r) bytes, 16-byte aligned, not used by any other call
- *                in flight
+ *   workspace    >= mla_latent_attend_paged_workspace_size(B, T, H, r) bytes (1,040 for each of B * T * H, and 20 to 80 MB),
+ *                16-byte aligned, not used by any other call in flight
  * A sequence with a length, count or lens + counts outside [0, T] and [0, max_blocks * block_size] is skipped, rows of a
  * block outside the pool count as zeros, and a parent outside [-1, t) as -1; each is reported as MLA_ERR_DEVICE_BOUNDS.
  * Precision: products of bf16 values in fp32; softmax statistics, sums and the join of split rows in fp32.  Rounded to

@@ -23,7 +23,7 @@ def env():
 def test_reserve_from_two_threads(env):
     """Calls whose numbers of sequences ask for different amounts of shared memory, at the same time."""
     torch, lca = env
-    lib, status, go = lca.library(), {}, threading.Event()
+    lib, status, state, go = lca.library(), {}, {}, threading.Event()
 
     def calls(B, n):
         i32 = dict(dtype=torch.int32, device="cuda")
@@ -37,7 +37,7 @@ def test_reserve_from_two_threads(env):
         go.wait()
         status[B] = [lib.mla_reserve_latent_blocks(*args) for _ in range(n)]
         stream.synchronize()
-        assert int(left) == 0 and held.tolist() == [2] * B
+        state[B] = left, held
 
     threads = [threading.Thread(target=calls, args=(B, 3000)) for B in (16384, 3400, 9000)]
     for t in threads:
@@ -46,6 +46,9 @@ def test_reserve_from_two_threads(env):
     for t in threads:
         t.join()
     assert {B: sum(rc != 0 for rc in rcs) for B, rcs in status.items()} == {16384: 0, 3400: 0, 9000: 0}
+    for left, held in state.values():
+        assert int(left) == 0 and bool((held == 2).all())
+    assert len(state) == 3
     assert lca.mla_get_device_error() == 0
 
 
